@@ -7,7 +7,9 @@ names below resolve to the binding on first use, so importing the package
 """
 __all__ = ["gdn_conv_update", "gdn_decode_step", "gdn_chunk_prefill", "gdn_spec_verify", "gdn_spec_commit",
            "gdn_gated_rmsnorm", "gdn_state_bytes", "gdn_conv_hist_bytes", "gdn_prefill_workspace_bytes",
-           "gdn_read_device_error", "make_dims", "GdnDims", "GdnError"]
+           "gdn_read_device_error", "make_dims", "GdnDims", "GdnError", "gdn_spec_verify_tree", "gdn_qk_norm_rope",
+           "gdn_kv_cache_write", "gdn_kv_cache_read", "gdn_tree_attention", "gdn_tree_attention_workspace_bytes",
+           "make_kv_cache", "GdnKvCache"]
 
 
 def __getattr__(name):

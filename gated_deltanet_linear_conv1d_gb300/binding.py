@@ -21,8 +21,9 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libgdn.so")
 
 GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_CUDA, GDN_ERR_DEVICE_CHECK, GDN_ERR_TIMEOUT = range(6)
-GDN_DEVERR_SLOT, GDN_DEVERR_OFFSETS, GDN_DEVERR_TIMEOUT, GDN_DEVERR_ACCEPTED = 1, 2, 4, 8
+GDN_DEVERR_SLOT, GDN_DEVERR_OFFSETS, GDN_DEVERR_TIMEOUT, GDN_DEVERR_ACCEPTED, GDN_DEVERR_TREE = 1, 2, 4, 8, 16
 GDN_COMMIT_COPY, GDN_COMMIT_REPOINT = 0, 1
+GDN_KV_BF16, GDN_KV_E4M3 = 0, 1
 
 
 class GdnError(RuntimeError):
@@ -41,6 +42,13 @@ class GdnDims(ctypes.Structure):
         return 2 * self.num_k_heads * self.head_k_dim + self.num_v_heads * self.head_v_dim
 
 
+class GdnKvCache(ctypes.Structure):
+    """gdn_kv_cache: one layer's paged key/value cache (make_kv_cache fills it and keeps its tensors alive)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
 def make_dims(geom, num_slots: int) -> GdnDims:
     """gdn_dims from any object with num_k_heads, num_v_heads, head_k_dim, head_v_dim, conv_kernel."""
     return GdnDims(geom.num_k_heads, geom.num_v_heads, geom.head_k_dim, geom.head_v_dim,
@@ -53,8 +61,9 @@ def _load() -> ctypes.CDLL:
                           "`python -m gated_deltanet_linear_conv1d_gb300.build` on a machine with nvcc")
     lib = ctypes.CDLL(LIB_PATH)
     P = ctypes.c_void_p
-    i32, f32, sz = ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+    i32, i64, f32, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
     D = ctypes.POINTER(GdnDims)
+    C = ctypes.POINTER(GdnKvCache)
     sigs = {
         "gdn_conv_update": [D, P, P, P, P, P, P, i32, i32, P, P, P],
         "gdn_decode_step": [D, P, P, P, P, P, P, P, P, P, f32, P, P, i32, P, P],
@@ -63,6 +72,12 @@ def _load() -> ctypes.CDLL:
         "gdn_chunk_prefill_align": [D, P, P, P, P, P, P, P, P, P, P, P, f32, P, P, i32, i32, P, i32, P, i32, P, sz,
                                     P, P],
         "gdn_spec_verify": [D, P, P, P, P, P, P, P, P, P, P, f32, P, P, i32, i32, P, P],
+        "gdn_spec_verify_tree": [D, P, P, P, P, P, P, P, P, P, P, P, f32, P, P, i32, i32, P, P],
+        "gdn_kv_cache_write": [C, P, i64, i64, P, i64, i64, P, i32, P, P],
+        "gdn_kv_cache_read": [C, P, i32, P, i32, i32, P, P, P, P],
+        "gdn_qk_norm_rope": [P, i64, i64, P, i64, i64, P, P, f32, P, P, i32, i32, P, P, P, i64, i64, C, P, i32, i32,
+                             i32, i32, P, P],
+        "gdn_tree_attention": [C, P, P, i32, P, P, P, f32, P, i32, i32, i32, P, sz, P, P],
         "gdn_spec_commit": [D, P, P, P, P, P, i32, i32, i32, P, P],
         "gdn_gated_rmsnorm": [P, P, P, f32, P, i32, i32, i32, P],
         "gdn_out_proj": [P, P, P, P, i32, i32, i32, P, P],
@@ -84,6 +99,8 @@ def _load() -> ctypes.CDLL:
     lib.gdn_prefill_workspace_bytes.restype = sz
     lib.gdn_fp8_linear_workspace_bytes.argtypes = [i32, i32, i32]
     lib.gdn_fp8_linear_workspace_bytes.restype = sz
+    lib.gdn_tree_attention_workspace_bytes.argtypes = [C, i32, i32, i32]
+    lib.gdn_tree_attention_workspace_bytes.restype = sz
     lib.gdn_status_string.argtypes = [ctypes.c_int]
     lib.gdn_status_string.restype = ctypes.c_char_p
     return lib
@@ -109,6 +126,23 @@ def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _rows(t, name: str, shape):
+    """(pointer, token stride, head stride) of a bf16 operand [T, H, D] whose head rows are contiguous;
+    tokens and heads may be strided (a view into a packed projection)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (libgdn has no CPU path)")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must have dtype {torch.bfloat16}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    st, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name}'s head rows must be contiguous")
+    return _ptr(t), st, sh
 
 
 def _need(t, name: str, dtype, shape=None, optional: bool = False):
@@ -373,6 +407,129 @@ def gdn_spec_verify(dims, qkv0, conv_w, conv_hist, state, slot_idx, spec_slot_id
                                 _ptr(slot_idx), _ptr(spec_slot_idx), _ptr(alpha), _ptr(beta), _ptr(z),
                                 _ptr(gamma), float(eps), _ptr(o), _ptr(ogate), N, P, _ptr(dev_err),
                                 _stream(stream)), "gdn_spec_verify")
+
+
+def gdn_spec_verify_tree(dims, qkv0, conv_w, conv_hist, state, slot_idx, spec_slot_idx, parent, alpha, beta, z,
+                         gamma, eps, o=None, ogate=None, dev_err=None, stream=None):
+    """gdn_spec_verify of a draft tree: node p continues from node parent[n, p] (-1: the live slot)."""
+    N, P = spec_slot_idx.shape
+    Hv, dv = dims.num_v_heads, dims.head_v_dim
+    _common(dims, conv_w, conv_hist, state, gamma)
+    _need(qkv0, "qkv0", torch.bfloat16, (N * P, dims.channels))
+    _need(slot_idx, "slot_idx", torch.int32, (N,))
+    _need(spec_slot_idx, "spec_slot_idx", torch.int32, (N, P))
+    _need(parent, "parent", torch.int32, (N, P))
+    _need(alpha, "alpha", torch.float32, (N * P, Hv))
+    _need(beta, "beta", torch.float32, (N * P, Hv))
+    _need(z, "z", torch.bfloat16, (N * P, Hv, dv), optional=ogate is None)
+    _need(o, "o", torch.bfloat16, (N * P, Hv, dv), optional=True)
+    _need(ogate, "ogate", torch.bfloat16, (N * P, Hv * dv), optional=True)
+    _need(dev_err, "dev_err", torch.int32, (1,), optional=True)
+    _check(_lib.gdn_spec_verify_tree(ctypes.byref(dims), _ptr(qkv0), _ptr(conv_w), _ptr(conv_hist), _ptr(state),
+                                     _ptr(slot_idx), _ptr(spec_slot_idx), _ptr(parent), _ptr(alpha), _ptr(beta),
+                                     _ptr(z), _ptr(gamma), float(eps), _ptr(o), _ptr(ogate), N, P, _ptr(dev_err),
+                                     _stream(stream)), "gdn_spec_verify_tree")
+
+
+def make_kv_cache(k, v, k_scale=None, v_scale=None) -> GdnKvCache:
+    """The cache handle of pools k, v [num_pages, num_kv_heads, page_tokens, head_dim]: bf16, or e4m3
+    codes (uint8 storage) with k_scale, v_scale [num_pages, num_kv_heads, page_tokens] fp32."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be a tensor [num_pages, num_kv_heads, page_tokens, head_dim]")
+    e4m3 = k.dtype == torch.uint8
+    dtype = torch.uint8 if e4m3 else torch.bfloat16
+    _need(k, "k", dtype)
+    _need(v, "v", dtype, k.shape)
+    if not e4m3 and (k_scale is not None or v_scale is not None):
+        raise ValueError("a bf16 cache has no scales")
+    _need(k_scale, "k_scale", torch.float32, k.shape[:3], optional=not e4m3)
+    _need(v_scale, "v_scale", torch.float32, k.shape[:3], optional=not e4m3)
+    pages, heads, page, d = k.shape
+    c = GdnKvCache(k.data_ptr(), v.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
+                   None if v_scale is None else v_scale.data_ptr(), pages, page, heads, d,
+                   GDN_KV_E4M3 if e4m3 else GDN_KV_BF16)
+    c.tensors = (k, v, k_scale, v_scale)
+    return c
+
+
+def gdn_kv_cache_write(cache, k, v, kv_slot, dev_err=None, stream=None):
+    """k, v [T, Hkv, D] bf16 (views with contiguous head rows) into slots kv_slot [T] (negative: skipped)."""
+    T = kv_slot.shape[0]
+    shape = (T, cache.num_kv_heads, cache.head_dim)
+    kp, vp = _rows(k, "k", shape), _rows(v, "v", shape)
+    _need(kv_slot, "kv_slot", torch.int32, (T,))
+    _need(dev_err, "dev_err", torch.int32, (1,), optional=True)
+    _check(_lib.gdn_kv_cache_write(ctypes.byref(cache), *kp, *vp, _ptr(kv_slot), T, _ptr(dev_err), _stream(stream)),
+           "gdn_kv_cache_write")
+
+
+def gdn_kv_cache_read(cache, block_table, start, k_out, v_out, dev_err=None, stream=None):
+    """Requests' first start[n+1] - start[n] tokens gathered and dequantised to k_out, v_out [T, Hkv, D] bf16."""
+    N, max_pages = block_table.shape
+    T = k_out.shape[0]
+    shape = (T, cache.num_kv_heads, cache.head_dim)
+    _need(block_table, "block_table", torch.int32)
+    _need(start, "start", torch.int32, (N + 1,))
+    _need(k_out, "k_out", torch.bfloat16, shape)
+    _need(v_out, "v_out", torch.bfloat16, shape)
+    _need(dev_err, "dev_err", torch.int32, (1,), optional=True)
+    _check(_lib.gdn_kv_cache_read(ctypes.byref(cache), _ptr(block_table), max_pages, _ptr(start), N, T, _ptr(k_out),
+                                  _ptr(v_out), _ptr(dev_err), _stream(stream)), "gdn_kv_cache_read")
+
+
+def gdn_qk_norm_rope(q, k, q_gamma, k_gamma, eps, positions, inv_freq, q_out, k_out=None, v=None, cache=None,
+                     kv_slot=None, interleaved: bool = False, dev_err=None, stream=None):
+    """Head norms and rotation of q [T, Hq, D] and k [T, Hkv, D] (views with contiguous head rows) into q_out, k_out;
+    with a cache, k and v also to slots kv_slot. inv_freq [rotary_dim / 2] fp64, or None for no rotation. q and
+    q_out None: the keys alone."""
+    T, Hkv, D = k.shape
+    Hq = Hkv if q is None else q.shape[1]
+    qp = (None, 0, 0) if q is None else _rows(q, "q", (T, Hq, D))
+    kp = _rows(k, "k", (T, Hkv, D))
+    vp = (None, 0, 0) if v is None else _rows(v, "v", (T, Hkv, D))
+    _need(q_gamma, "q_gamma", torch.float32, (D,), optional=q is None)
+    _need(k_gamma, "k_gamma", torch.float32, (D,))
+    rotary = 0 if inv_freq is None else 2 * inv_freq.numel()
+    _need(inv_freq, "inv_freq", torch.float64, (rotary // 2,), optional=True)
+    _need(positions, "positions", torch.int32, (T,), optional=rotary == 0)
+    _need(q_out, "q_out", torch.bfloat16, (T, Hq, D), optional=q is None)
+    _need(k_out, "k_out", torch.bfloat16, (T, Hkv, D), optional=cache is not None)
+    _need(kv_slot, "kv_slot", torch.int32, (T,), optional=cache is None)
+    _need(dev_err, "dev_err", torch.int32, (1,), optional=True)
+    _check(_lib.gdn_qk_norm_rope(*qp, *kp, _ptr(q_gamma), _ptr(k_gamma), float(eps), _ptr(positions), _ptr(inv_freq),
+                                 rotary, int(bool(interleaved)), _ptr(q_out), _ptr(k_out), *vp,
+                                 None if cache is None else ctypes.byref(cache), _ptr(kv_slot), T, Hq, Hkv, D,
+                                 _ptr(dev_err), _stream(stream)), "gdn_qk_norm_rope")
+
+
+def gdn_tree_attention_workspace_bytes(cache, num_seqs: int, num_pos: int, num_q_heads: int) -> int:
+    return int(_lib.gdn_tree_attention_workspace_bytes(ctypes.byref(cache), int(num_seqs), int(num_pos),
+                                                       int(num_q_heads)))
+
+
+def gdn_tree_attention(cache, q, block_table, ctx_len, scale, out, num_pos: int = 1, tree_mask=None, gate=None,
+                       workspace=None, dev_err=None, stream=None):
+    """Attention of num_pos drafted tokens per request (q [N * num_pos, Hq, D]; 1: a decode step) over the cache.
+    tree_mask [N, num_pos] int64, bit i of a node's word: it sees node i; None: a chain. workspace: zero-filled
+    before its first use (each call resets its tickets)."""
+    N, max_pages = block_table.shape
+    shape = (N * num_pos, q.shape[1], cache.head_dim)
+    _need(q, "q", torch.bfloat16, shape)
+    _need(block_table, "block_table", torch.int32)
+    _need(ctx_len, "ctx_len", torch.int32, (N,))
+    _need(tree_mask, "tree_mask", torch.int64, (N, num_pos), optional=True)
+    _need(gate, "gate", torch.bfloat16, shape, optional=True)
+    _need(out, "out", torch.bfloat16, shape)
+    _need(dev_err, "dev_err", torch.int32, (1,), optional=True)
+    if workspace is None:
+        need = gdn_tree_attention_workspace_bytes(cache, N, num_pos, shape[1])
+        workspace = _scratch(need, q.device, stream)
+        with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.current_stream()):
+            workspace.zero_()
+    _check(_lib.gdn_tree_attention(ctypes.byref(cache), _ptr(q), _ptr(block_table), max_pages, _ptr(ctx_len),
+                                   _ptr(tree_mask), _ptr(gate), float(scale), _ptr(out), N, int(num_pos), shape[1],
+                                   _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_err),
+                                   _stream(stream)), "gdn_tree_attention")
 
 
 def gdn_spec_commit(dims, accepted, spec_slot_idx, slot_idx, state=None, conv_hist=None,

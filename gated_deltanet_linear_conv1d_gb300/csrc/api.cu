@@ -95,6 +95,27 @@ int channels(const gdn_dims* d) {
   return 2 * d->num_k_heads * d->head_k_dim + d->num_v_heads * d->head_v_dim;
 }
 
+// Geometry and pointers of a paged key/value cache.
+gdn_status check_cache(const gdn_kv_cache* c, KvArgs* out) {
+  if (!c || !c->k || !c->v || c->num_pages <= 0 || c->page_tokens <= 0 || c->num_kv_heads <= 0 || c->head_dim <= 0)
+    return GDN_ERR_INVALID_ARG;
+  if (c->format != GDN_KV_BF16 && c->format != GDN_KV_E4M3) return GDN_ERR_INVALID_ARG;
+  if ((c->head_dim != 128 && c->head_dim != 256) || c->page_tokens % 16 != 0) return GDN_ERR_UNSUPPORTED;
+  const bool e4m3 = c->format == GDN_KV_E4M3;
+  if (e4m3 ? !c->k_scale || !c->v_scale : c->k_scale || c->v_scale) return GDN_ERR_INVALID_ARG;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))
+    return GDN_ERR_INVALID_ARG;
+  const long long slots = (long long)c->num_pages * c->page_tokens;
+  if (slots > INT32_MAX || slots * c->num_kv_heads > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  *out = KvArgs{c->k, c->v, c->k_scale, c->v_scale, c->num_pages, c->page_tokens, c->num_kv_heads, e4m3, (int)slots};
+  return GDN_OK;
+}
+
+// Rows of a strided operand: 16-byte aligned, strides whole 16-byte pieces.
+bool rows_ok(const uint16_t* p, int64_t stride_t, int64_t stride_h) {
+  return p && aligned(p, 16) && stride_t % 8 == 0 && stride_h % 8 == 0;
+}
+
 bool eps_ok(float eps) { return std::isfinite(eps) && eps >= 0.f; }
 
 gdn_status from_cuda(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
@@ -187,14 +208,17 @@ gdn_status gdn_decode_step(const gdn_dims* d, const uint16_t* qkv0, const float*
   if (!aligned(state, 16) || !aligned(conv_w, 16) || !aligned(qkv0, 16) || !aligned(conv_hist, 16) ||
       (ogate && !aligned(z, 16)))
     return GDN_ERR_INVALID_ARG;
-  StepArgs a{qkv0, conv_w, conv_hist, state, slot_idx, nullptr, alpha, beta, z, gamma, eps, o, ogate, dev_err,
+  StepArgs a{qkv0, conv_w, conv_hist, state, slot_idx, nullptr, nullptr, alpha, beta, z, gamma, eps, o, ogate, dev_err,
              d->num_k_heads, d->num_v_heads, d->num_v_heads / d->num_k_heads, channels(d), d->num_slots,
              num_seqs, 1};
   return from_cuda(launch_stream(a, static_cast<cudaStream_t>(stream)));
 }
 
-gdn_status gdn_spec_verify(const gdn_dims* d, const uint16_t* qkv0, const float* conv_w, uint16_t* conv_hist,
-                           float* state, const int32_t* slot_idx, const int32_t* spec_slot_idx,
+namespace {
+
+// The checks and the launch shared by the verify of a chain (parent NULL) and of a tree.
+gdn_status verify(const gdn_dims* d, const uint16_t* qkv0, const float* conv_w, uint16_t* conv_hist,
+                           float* state, const int32_t* slot_idx, const int32_t* spec_slot_idx, const int32_t* parent,
                            const float* alpha, const float* beta, const uint16_t* z, const float* gamma,
                            float eps, uint16_t* o, uint16_t* ogate, int32_t num_seqs, int32_t num_pos,
                            int32_t* dev_err, void* stream) {
@@ -210,11 +234,32 @@ gdn_status gdn_spec_verify(const gdn_dims* d, const uint16_t* qkv0, const float*
   if (!aligned(state, 16) || !aligned(conv_w, 16) || !aligned(qkv0, 16) || !aligned(conv_hist, 16) ||
       (ogate && !aligned(z, 16)))
     return GDN_ERR_INVALID_ARG;
-  StepArgs a{qkv0, conv_w, conv_hist, state, slot_idx, spec_slot_idx, alpha, beta, z, gamma, eps, o, ogate,
+  StepArgs a{qkv0, conv_w, conv_hist, state, slot_idx, spec_slot_idx, parent, alpha, beta, z, gamma, eps, o, ogate,
              dev_err, d->num_k_heads, d->num_v_heads, d->num_v_heads / d->num_k_heads, channels(d),
              d->num_slots, num_seqs, num_pos};
   if (!stream_supported(a.G, a.P)) return GDN_ERR_UNSUPPORTED;  // never for the supported geometry
   return from_cuda(launch_stream(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+gdn_status gdn_spec_verify(const gdn_dims* d, const uint16_t* qkv0, const float* conv_w, uint16_t* conv_hist,
+                           float* state, const int32_t* slot_idx, const int32_t* spec_slot_idx,
+                           const float* alpha, const float* beta, const uint16_t* z, const float* gamma,
+                           float eps, uint16_t* o, uint16_t* ogate, int32_t num_seqs, int32_t num_pos,
+                           int32_t* dev_err, void* stream) {
+  return verify(d, qkv0, conv_w, conv_hist, state, slot_idx, spec_slot_idx, nullptr, alpha, beta, z, gamma, eps, o,
+                ogate, num_seqs, num_pos, dev_err, stream);
+}
+
+gdn_status gdn_spec_verify_tree(const gdn_dims* d, const uint16_t* qkv0, const float* conv_w, uint16_t* conv_hist,
+                                float* state, const int32_t* slot_idx, const int32_t* spec_slot_idx,
+                                const int32_t* parent, const float* alpha, const float* beta, const uint16_t* z,
+                                const float* gamma, float eps, uint16_t* o, uint16_t* ogate, int32_t num_seqs,
+                                int32_t num_pos, int32_t* dev_err, void* stream) {
+  if (num_seqs > 0 && !parent) return GDN_ERR_INVALID_ARG;
+  return verify(d, qkv0, conv_w, conv_hist, state, slot_idx, spec_slot_idx, parent, alpha, beta, z, gamma, eps, o,
+                ogate, num_seqs, num_pos, dev_err, stream);
 }
 
 gdn_status gdn_spec_commit(const gdn_dims* d, const int32_t* accepted, const int32_t* spec_slot_idx,
@@ -398,6 +443,115 @@ gdn_status gdn_rmsnorm(const uint16_t* x, uint16_t* residual, const float* gamma
     return GDN_ERR_INVALID_ARG;
   RmsArgs a{x, residual, gamma, out, eps, (int)num_tokens, (int)hidden_size};
   return from_cuda(launch_rmsnorm(a, static_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_kv_cache_write(const gdn_kv_cache* cache, const uint16_t* k, int64_t k_stride_t, int64_t k_stride_h,
+                              const uint16_t* v, int64_t v_stride_t, int64_t v_stride_h, const int32_t* kv_slot,
+                              int32_t num_tokens, int32_t* dev_err, void* stream) {
+  KvArgs c{};
+  gdn_status st = check_cache(cache, &c);
+  if (st != GDN_OK) return st;
+  if (num_tokens < 0) return GDN_ERR_INVALID_ARG;
+  if (num_tokens == 0) return GDN_OK;
+  if (!kv_slot || !rows_ok(k, k_stride_t, k_stride_h) || !rows_ok(v, v_stride_t, v_stride_h)) return GDN_ERR_INVALID_ARG;
+  RopeArgs a{};
+  a.k = k;
+  a.v = v;
+  a.k_t = k_stride_t;
+  a.k_h = k_stride_h;
+  a.v_t = v_stride_t;
+  a.v_h = v_stride_h;
+  a.kv_slot = kv_slot;
+  a.T = num_tokens;
+  a.dev_err = dev_err;
+  return from_cuda(launch_rows(a, c, false, cache->head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_kv_cache_read(const gdn_kv_cache* cache, const int32_t* block_table, int32_t max_pages,
+                             const int32_t* start, int32_t num_seqs, int32_t num_tokens, uint16_t* k_out,
+                             uint16_t* v_out, int32_t* dev_err, void* stream) {
+  KvArgs c{};
+  gdn_status st = check_cache(cache, &c);
+  if (st != GDN_OK) return st;
+  if (num_seqs < 0 || num_tokens < 0 || max_pages < 0) return GDN_ERR_INVALID_ARG;
+  if (num_seqs == 0) return num_tokens == 0 ? GDN_OK : GDN_ERR_INVALID_ARG;
+  if (num_tokens == 0) return GDN_OK;
+  if (!block_table || !start || max_pages == 0 || !k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16))
+    return GDN_ERR_INVALID_ARG;
+  ReadArgs a{block_table, start, k_out, v_out, num_seqs, num_tokens, max_pages, dev_err};
+  return from_cuda(launch_kv_read(a, c, cache->head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_qk_norm_rope(const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h, const uint16_t* k,
+                            int64_t k_stride_t, int64_t k_stride_h, const float* q_gamma, const float* k_gamma,
+                            float eps, const int32_t* positions, const double* inv_freq, int32_t rotary_dim,
+                            int32_t interleaved, uint16_t* q_out, uint16_t* k_out, const uint16_t* v,
+                            int64_t v_stride_t, int64_t v_stride_h, const gdn_kv_cache* cache,
+                            const int32_t* kv_slot, int32_t num_tokens, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t* dev_err, void* stream) {
+  KvArgs c{};
+  if (cache) {
+    gdn_status st = check_cache(cache, &c);
+    if (st != GDN_OK) return st;
+    if (cache->num_kv_heads != num_kv_heads || cache->head_dim != head_dim) return GDN_ERR_INVALID_ARG;
+  }
+  if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0) return GDN_ERR_INVALID_ARG;
+  if (head_dim != 128 && head_dim != 256) return GDN_ERR_UNSUPPORTED;
+  // the rows of the eight tokens that a block takes are counted in 32 bits
+  if (num_q_heads > 65535 || num_kv_heads > 65535) return GDN_ERR_UNSUPPORTED;
+  if (rotary_dim < 0 || rotary_dim > head_dim || rotary_dim % 16 != 0) return GDN_ERR_INVALID_ARG;
+  if (!eps_ok(eps)) return GDN_ERR_INVALID_ARG;
+  if (num_tokens == 0) return GDN_OK;
+  if (!q != !q_out || (!cache && !k_out) || !cache != !v || !cache != !kv_slot) return GDN_ERR_INVALID_ARG;
+  if (!rows_ok(k, k_stride_t, k_stride_h) || (q && !rows_ok(q, q_stride_t, q_stride_h)) ||
+      (v && !rows_ok(v, v_stride_t, v_stride_h)))
+    return GDN_ERR_INVALID_ARG;
+  if (!k_gamma || !aligned(k_gamma, 16) || (q && (!q_gamma || !aligned(q_gamma, 16)))) return GDN_ERR_INVALID_ARG;
+  if (rotary_dim > 0 && (!positions || !inv_freq)) return GDN_ERR_INVALID_ARG;
+  if (!aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(inv_freq, 8)) return GDN_ERR_INVALID_ARG;
+  c.Hkv = num_kv_heads;
+  RopeArgs a{q, k, v, q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h, q_gamma, k_gamma, eps,
+             positions, inv_freq, rotary_dim, interleaved != 0, q_out, k_out, kv_slot, num_tokens, num_q_heads, dev_err};
+  return from_cuda(launch_rows(a, c, true, head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+gdn_status check_tree_sizes(const KvArgs& c, int32_t num_seqs, int32_t num_pos, int32_t num_q_heads) {
+  if (num_seqs < 0 || num_seqs > 65535 || num_pos < 1 || num_pos > 64 || num_q_heads <= 0) return GDN_ERR_INVALID_ARG;
+  if (num_q_heads % c.Hkv != 0 || num_q_heads / c.Hkv > 64 || num_q_heads > 65535) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+}  // namespace
+
+size_t gdn_tree_attention_workspace_bytes(const gdn_kv_cache* cache, int32_t num_seqs, int32_t num_pos,
+                                          int32_t num_q_heads) {
+  KvArgs c{};
+  if (check_cache(cache, &c) != GDN_OK || num_seqs <= 0 || check_tree_sizes(c, num_seqs, num_pos, num_q_heads) != GDN_OK)
+    return 0;
+  return tree_attn_workspace_bytes(num_seqs, num_pos, num_q_heads, c.Hkv, cache->head_dim, c.e4m3);
+}
+
+gdn_status gdn_tree_attention(const gdn_kv_cache* cache, const uint16_t* q, const int32_t* block_table,
+                              int32_t max_pages, const int32_t* ctx_len, const uint64_t* tree_mask,
+                              const uint16_t* gate, float scale, uint16_t* out, int32_t num_seqs, int32_t num_pos,
+                              int32_t num_q_heads, void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                              void* stream) {
+  KvArgs c{};
+  gdn_status st = check_cache(cache, &c);
+  if (st != GDN_OK) return st;
+  st = check_tree_sizes(c, num_seqs, num_pos, num_q_heads);
+  if (st != GDN_OK) return st;
+  if (max_pages < 0 || !std::isfinite(scale)) return GDN_ERR_INVALID_ARG;
+  if (num_seqs == 0) return GDN_OK;
+  if (!q || !block_table || !ctx_len || !out || max_pages == 0) return GDN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(gate, 16) || !aligned(tree_mask, 8)) return GDN_ERR_INVALID_ARG;
+  const size_t need = tree_attn_workspace_bytes(num_seqs, num_pos, num_q_heads, c.Hkv, cache->head_dim, c.e4m3);
+  if (workspace_bytes < need || (need > 0 && (!workspace || !aligned(workspace, 256)))) return GDN_ERR_INVALID_ARG;
+  TreeAttnArgs a{q, block_table, ctx_len, tree_mask, gate, out, scale, num_seqs, num_pos, num_q_heads,
+                 num_q_heads / c.Hkv, cache->head_dim, max_pages, workspace, dev_err};
+  return from_cuda(launch_tree_attn(a, c, static_cast<cudaStream_t>(stream)));
 }
 
 gdn_status gdn_fp8_quant_act(const uint16_t* x, uint8_t* x8, float* x_scale, int32_t num_tokens, int32_t k,

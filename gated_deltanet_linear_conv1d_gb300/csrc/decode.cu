@@ -1,7 +1,8 @@
 // decode.cu - the persistent, warp-specialised state-streaming kernel behind
 // gdn_decode_step (one token per request, the state updated in place) and
 // gdn_spec_verify (P positions per request, the state after every position kept
-// in its checkpoint slot).
+// in its checkpoint slot) and gdn_spec_verify_tree (the positions the nodes of a
+// tree, each continuing from its parent's state).
 //
 // Math (page "Qwen3.8-27B: from model structure to vLLM inference data flow",
 // section 01 GDN operator table; section 08: decay first, then predict from the
@@ -65,8 +66,8 @@ constexpr int kIdRing = 4;       // claimed unit ids in flight (two iterations a
 // Dynamic shared-memory layout for group size G and P positions (byte offsets,
 // 16-byte aligned). The stage ring takes what the rest leaves, up to 6 stages.
 struct Layout {
-  int stages, stage, x, hist, z, q, k, v, o, red, ab, bars, total;
-  __host__ __device__ Layout(int G, int P) {
+  int stages, stage, x, hist, z, q, k, v, o, red, ab, tap, bars, total;
+  __host__ __device__ Layout(int G, int P, bool tree) {
     const int nseg = 2 + G;  // q, k, G value heads
     int rest = 0;
     x = rest;        rest += 2 * P * nseg * kHeadDim * 2;   // [2][P][nseg*128] bf16
@@ -78,12 +79,13 @@ struct Layout {
     o = rest;        rest += G * P * kHeadDim * 4;          // [G][P][128] fp32
     red = rest;      rest += (P * 16 + G * P * 4) * 4;      // [P][16] norm and [G*P][4] RMS partial sums
     ab = rest;       rest += kMaxGroup * kMaxPos * 4 * 4 + kMaxPos * 4;  // [G][P][4] alpha, beta; [P] output slots
+    tap = rest;      rest += tree ? kMaxPos * 4 * 4 : 0;    // [P][4] where a node's conv inputs stand, and its parent
     bars = rest;     rest += (2 * kMaxStages + 8) * 8 + 32; // mbarriers + abort flag + claimed unit ids
     stages = (kSmemLimit - rest) / (int)kHalfBytes;
     if (stages > kMaxStages) stages = kMaxStages;
     const int off = stages * (int)kHalfBytes;
     stage = 0;
-    x += off; hist += off; z += off; q += off; k += off; v += off; o += off; red += off; ab += off; bars += off;
+    x += off; hist += off; z += off; q += off; k += off; v += off; o += off; red += off; ab += off; tap += off; bars += off;
     total = off + rest;
   }
 };
@@ -104,8 +106,18 @@ __device__ __forceinline__ void bulk_g2s_nohint(void* smem_dst, const void* gsrc
       : "memory");
 }
 
+// A tree's parents come before their children; -1 is the live slot.
+__device__ __forceinline__ bool unit_parents_ok(const StepArgs& p, int n) {
+  for (int q = 0; q < p.P; ++q) {
+    const int f = p.parent[n * p.P + q];
+    if (f < -1 || f >= q) return false;
+  }
+  return true;
+}
+
 // Slot that receives the state after position p: the live slot (decode) or the
 // position's checkpoint slot (speculative verify). -1 when out of range.
+template <bool kTree>
 __device__ __forceinline__ bool unit_slots_ok(const StepArgs& p, int n) {
   const int slot = p.slot_idx[n];
   if (slot < 0 || slot >= p.Rs) return false;
@@ -114,6 +126,7 @@ __device__ __forceinline__ bool unit_slots_ok(const StepArgs& p, int n) {
       const int s = p.spec_slot[n * p.P + q];
       if (s < 0 || s >= p.Rs) return false;
     }
+  if constexpr (kTree) return unit_parents_ok(p, n);
   return true;
 }
 
@@ -122,11 +135,15 @@ __device__ __forceinline__ bool unit_slots_ok(const StepArgs& p, int n) {
 __device__ int g_unit_counter[kSchedSlots * 2];
 
 // kOne: exactly one position (decode), so the per-position vectors are loaded once per unit.
-template <bool kOne>
+// kTree: position q continues from position parent[q] (-1: the live state). A
+// row's registers hold the last position's state; where the parent is another
+// one, the thread that holds the row loads it again, from the staged live state
+// or from the parent's checkpoint, which the same thread has written.
+template <bool kOne, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const StepArgs p, const int units, const int sched) {
   extern __shared__ __align__(1024) unsigned char smem[];
   const int G = p.G, P = kOne ? 1 : p.P;
-  const Layout L(G, P);
+  const Layout L(G, P, kTree);
   const int S_N = L.stages;
   float* stage = reinterpret_cast<float*>(smem + L.stage);
   uint16_t* xs = reinterpret_cast<uint16_t*>(smem + L.x);
@@ -178,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const StepArgs p, c
       const int u = uid[i % kIdRing];
       if (u < 0) break;
       const int n = u / p.Hk, j = u % p.Hk;
-      if (!unit_slots_ok(p, n)) {  // the consumers skip the same unit: an empty hand-over
+      if (!unit_slots_ok<kTree>(p, n)) {  // the consumers skip the same unit: an empty hand-over
         const int b = kin & 1;
         if (!mbar_wait_bounded(&in_empty[b], ((kin >> 1) & 1) ^ 1)) { *abort_flag = 1; break; }
         mbar_arrive(&in_full[b]);
@@ -236,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const StepArgs p, c
   const uint64_t wpol = l2_policy_evict_first();
   float* rms_part = red + P * 16;  // [G*P][4]
   int* out_slot = reinterpret_cast<int*>(ab + kMaxGroup * kMaxPos * 4);  // [P] slot written after position q
+  int* tap = reinterpret_cast<int*>(smem + L.tap);
   bool dead = false;
   int t = 0, kin = 0;
   // Units are claimed two iterations ahead by consumer thread 0 (uid[i %
@@ -275,13 +293,27 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const StepArgs p, c
     if (u_nx >= 0) prefetch(u_nx);
     claim(i + 2);
     const int b = kin & 1;
-    const bool skip = slot < 0 || slot >= p.Rs || (p.spec_slot && !unit_slots_ok(p, n));
+    const bool skip = slot < 0 || slot >= p.Rs || (p.spec_slot && !unit_slots_ok<kTree>(p, n));
     if (!skip) {
       if (ctid < G * P) {
         ab[ctid * 4 + 0] = a_cur;  // [g][q] with g = ctid / P, q = ctid % P
         ab[ctid * 4 + 1] = b_cur;
       }
       if (ctid < P) out_slot[ctid] = p.spec_slot ? oslot_cur : slot;
+      if constexpr (kTree) {
+        // where the inputs 1, 2 and 3 steps back of position ctid stand: the ancestor's position, or
+        // -1 - e for entry e of the live slot's history; [3]: the parent
+        if (ctid < P) {
+          const int32_t* par = p.parent + n * P;
+          int at = ctid, left = 2;  // the newest history entry not yet used
+          for (int i = 0; i < 3; ++i) {
+            if (at >= 0) at = par[at];
+            tap[ctid * 4 + i] = at >= 0 ? at : -1 - left--;
+          }
+          tap[ctid * 4 + 3] = par[ctid];
+        }
+        consumer_sync();
+      }
     }
     dead = dead || *abort_flag;
     if (!dead && !mbar_wait_bounded(&in_full[b], (kin >> 1) & 1)) {
@@ -290,7 +322,11 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const StepArgs p, c
       report(p.dev_err, GDN_DEVERR_TIMEOUT);
     }
     if (skip) {  // a bad or padding slot: the producer handed over nothing
-      if (ctid == 0 && slot >= 0) report(p.dev_err, GDN_DEVERR_SLOT);
+      if (ctid == 0 && slot >= 0) {
+        bool tree = false;  // the slots are fine, the parents are not
+        if constexpr (kTree) tree = unit_slots_ok<false>(p, n);
+        report(p.dev_err, tree ? GDN_DEVERR_TREE : GDN_DEVERR_SLOT);
+      }
       consumer_sync();
       if (ctid == 0) mbar_arrive(&in_empty[b]);
       ++kin;
@@ -309,6 +345,14 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const StepArgs p, c
       uint16_t h0 = hb[cc * 3], h1 = hb[cc * 3 + 1], h2 = hb[cc * 3 + 2];
       for (int q = 0; q < P; ++q) {
         const uint16_t x0 = xs[(b * P + q) * xrow_len + cc];
+        if constexpr (kTree) {
+          auto input = [&](int at) {
+            return at >= 0 ? xs[(b * P + at) * xrow_len + cc] : hb[cc * 3 + (-1 - at)];
+          };
+          h2 = input(tap[q * 4]);
+          h1 = input(tap[q * 4 + 1]);
+          h0 = input(tap[q * 4 + 2]);
+        }
         float pre = w.x * bf16_to_f32(x0);
         pre = fmaf(w.y, bf16_to_f32(h2), pre);
         pre = fmaf(w.z, bf16_to_f32(h1), pre);
@@ -394,6 +438,19 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const StepArgs p, c
 #pragma unroll
           for (int m = 0; m < 4; ++m) sv[m] = reinterpret_cast<const float4*>(srow)[cl + 8 * m];
           for (int q = 0; q < P; ++q) {
+            if constexpr (kTree) {
+              const int from = tap[q * 4 + 3];
+              if (from != q - 1) {
+                if (from < 0) {
+#pragma unroll
+                  for (int m = 0; m < 4; ++m) sv[m] = reinterpret_cast<const float4*>(srow)[cl + 8 * m];
+                } else {
+                  const float* prow = p.state + (((size_t)out_slot[from] * p.Hv + h) * kHeadDim + ri) * kHeadDim;
+#pragma unroll
+                  for (int m = 0; m < 4; ++m) sv[m] = ld_global_v4(prow + 4 * (cl + 8 * m));
+                }
+              }
+            }
             const float a = ab[(g * P + q) * 4 + 0], bb = ab[(g * P + q) * 4 + 1];
             float kq;
             float4 kk[4], qq[4];
@@ -704,7 +761,7 @@ int sm_count() {
 
 }  // namespace
 
-bool stream_supported(int G, int P) { return P >= 1 && P <= kMaxPos && Layout(G, P).stages >= 2; }
+bool stream_supported(int G, int P) { return P >= 1 && P <= kMaxPos && Layout(G, P, true).stages >= 2; }
 
 // Launch shape of the row-split kernel for nsplit CTAs per unit.
 void split_config(const StepArgs& a, int nsplit, cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr) {
@@ -755,7 +812,7 @@ cudaError_t launch_split(const StepArgs& a, int nsplit, cudaStream_t stream) {
 }
 
 cudaError_t launch_stream(const StepArgs& a, cudaStream_t stream) {
-  const Layout L(a.G, a.P);
+  const Layout L(a.G, a.P, a.parent != nullptr);
   if (L.stages < 2 || a.P > kMaxPos) return cudaErrorInvalidValue;
   {
     const int sms = sm_count();
@@ -763,9 +820,10 @@ cudaError_t launch_stream(const StepArgs& a, cudaStream_t stream) {
     const int nsplit = split_factor(a, sms);
     if (nsplit > 1) return launch_split(a, nsplit, stream);
   }
-  const bool one = a.P == 1 && a.spec_slot == nullptr;
-  const void* fn = one ? reinterpret_cast<const void*>(&stream_kernel<true>)
-                       : reinterpret_cast<const void*>(&stream_kernel<false>);
+  const bool one = a.P == 1 && a.spec_slot == nullptr, tree = a.parent != nullptr;
+  const void* fn = one    ? reinterpret_cast<const void*>(&stream_kernel<true, false>)
+                   : tree ? reinterpret_cast<const void*>(&stream_kernel<false, true>)
+                          : reinterpret_cast<const void*>(&stream_kernel<false, false>);
   cudaError_t err = ensure_dynamic_smem(fn, L.total);
   if (err != cudaSuccess) return err;
   const int units = a.N * a.Hk;
@@ -773,8 +831,9 @@ cudaError_t launch_stream(const StepArgs& a, cudaStream_t stream) {
   if (sms <= 0) return cudaErrorInvalidDevice;
   const int grid = units < sms ? units : sms;
   const int sched = sched_slot(stream);
-  if (one) stream_kernel<true><<<grid, kThreads, L.total, stream>>>(a, units, sched);
-  else stream_kernel<false><<<grid, kThreads, L.total, stream>>>(a, units, sched);
+  if (one) stream_kernel<true, false><<<grid, kThreads, L.total, stream>>>(a, units, sched);
+  else if (tree) stream_kernel<false, true><<<grid, kThreads, L.total, stream>>>(a, units, sched);
+  else stream_kernel<false, false><<<grid, kThreads, L.total, stream>>>(a, units, sched);
   return cudaGetLastError();
 }
 

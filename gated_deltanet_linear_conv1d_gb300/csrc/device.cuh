@@ -181,6 +181,16 @@ __device__ __forceinline__ void st_global_v4_hint(float* gdst, float4 v, uint64_
                : "memory");
 }
 
+// 16-byte global load that stays behind this thread's earlier stores.
+__device__ __forceinline__ float4 ld_global_v4(const float* gsrc) {
+  float4 v;
+  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(gsrc)
+               : "memory");
+  return v;
+}
+
 // ---- warp / block reductions ------------------------------------------------
 
 __device__ __forceinline__ float warp_sum(float v) {

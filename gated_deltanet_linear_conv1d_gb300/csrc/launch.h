@@ -17,6 +17,7 @@ struct StepArgs {
   float* state;               // [Rs][Hv][128][128]
   const int32_t* slot_idx;    // [N]
   const int32_t* spec_slot;   // [N][P] (verify) or nullptr (decode)
+  const int32_t* parent;      // [N][P] (verify of a tree) or nullptr (a chain)
   const float* alpha;         // [N*P][Hv]
   const float* beta;          // [N*P][Hv]
   const uint16_t* z;          // [N*P][Hv][128]
@@ -111,6 +112,56 @@ struct QuantWeightArgs {
   float* scale;       // scale of block (nb, kb) at nb * scale_n + kb * scale_k
   long long scale_n, scale_k;
   int N, K;
+};
+
+// A layer's paged key/value cache (k nullptr: none).
+struct KvArgs {
+  void* k;
+  void* v;         // [pages][Hkv][page][D] bf16 or e4m3
+  float* k_scale;  // [pages][Hkv][page] (e4m3)
+  float* v_scale;
+  int pages, page, Hkv, e4m3;
+  int slots;       // pages * page
+};
+
+struct RopeArgs {
+  const uint16_t* q;  // strides in elements; q may be nullptr
+  const uint16_t* k;
+  const uint16_t* v;  // nullptr: no values
+  int64_t q_t, q_h, k_t, k_h, v_t, v_h;
+  const float* q_gamma;  // [D]
+  const float* k_gamma;
+  float eps;
+  const int32_t* positions;  // [T]
+  const double* inv_freq;    // [rotary / 2]
+  int rotary, interleaved;
+  uint16_t* q_out;  // [T][Hq][D]
+  uint16_t* k_out;  // [T][Hkv][D] or nullptr
+  const int32_t* kv_slot;  // [T] (with a cache)
+  int T, Hq;
+  int32_t* dev_err;
+};
+
+struct ReadArgs {
+  const int32_t* table;  // [N][max_pages]
+  const int32_t* start;  // [N+1]
+  uint16_t* k_out;       // [T][Hkv][D]
+  uint16_t* v_out;
+  int N, T, max_pages;
+  int32_t* dev_err;
+};
+
+struct TreeAttnArgs {
+  const uint16_t* q;       // [N*P][Hq][D]
+  const int32_t* table;    // [N][max_pages]
+  const int32_t* ctx;      // [N]
+  const uint64_t* mask;    // [N][P] or nullptr (chain)
+  const uint16_t* gate;    // [N*P][Hq][D] or nullptr
+  uint16_t* out;           // [N*P][Hq][D]
+  float scale;
+  int N, P, Hq, G, D, max_pages;
+  void* workspace;
+  int32_t* dev_err;
 };
 
 // Block-scaled FP8 GEMM: out[T][N] = dequant(x8) dequant(w8)^T (+ residual).
@@ -208,6 +259,11 @@ struct GemmArgs {
 cudaError_t launch_gemm(const GemmOperands& o, int32_t* dev_err, cudaStream_t stream);
 cudaError_t launch_gated_rmsnorm(const NormArgs& a, cudaStream_t stream);
 cudaError_t launch_rmsnorm(const RmsArgs& a, cudaStream_t stream);
+// The rows of T tokens through the head norm and the rotation (norm) and / or into the cache.
+cudaError_t launch_rows(const RopeArgs& a, const KvArgs& c, bool norm, int D, cudaStream_t stream);
+cudaError_t launch_kv_read(const ReadArgs& a, const KvArgs& c, int D, cudaStream_t stream);
+size_t tree_attn_workspace_bytes(int N, int P, int Hq, int Hkv, int D, bool e4m3);
+cudaError_t launch_tree_attn(const TreeAttnArgs& a, const KvArgs& c, cudaStream_t stream);
 cudaError_t launch_quant_act(const QuantActArgs& a, cudaStream_t stream);
 cudaError_t launch_quant_weight(const QuantWeightArgs& a, cudaStream_t stream);
 // Workspace bytes for the split-K partial tiles of a [T][N] output with K inputs

@@ -53,6 +53,8 @@
  * - Two requests of one call must not name the same slot (undefined result).
  * - Supported geometry: dk = dv = 128, K = 4, Hv a multiple of Hk with
  *   Hv / Hk <= 8. Anything else returns GDN_ERR_UNSUPPORTED.
+ * - The attention layers' entry points (gdn_qk_norm_rope, gdn_kv_cache_*,
+ *   gdn_tree_attention) have a geometry of their own, stated there.
  */
 #ifndef GDN_H
 #define GDN_H
@@ -90,6 +92,7 @@ typedef enum gdn_status {
 #define GDN_DEVERR_OFFSETS 2   /* query_start_loc not monotone or out of range  */
 #define GDN_DEVERR_TIMEOUT 4   /* a bounded wait on an async copy ran out       */
 #define GDN_DEVERR_ACCEPTED 8  /* accepted length outside [0, num_pos)          */
+#define GDN_DEVERR_TREE 16     /* a draft tree's parent outside [-1, its node)  */
 
 /* Commit modes of gdn_spec_commit. */
 #define GDN_COMMIT_COPY 0    /* copy the accepted checkpoint into the live slot */
@@ -411,6 +414,164 @@ gdn_status gdn_fp8_linear(const uint8_t *x8, const float *x_scale, const uint8_t
 gdn_status gdn_out_proj(const uint16_t *ogate, const uint16_t *w, const uint16_t *residual, uint16_t *out,
                         int32_t num_tokens, int32_t in_features, int32_t out_features, int32_t *dev_err,
                         void *stream);
+
+/*
+ * gdn_spec_verify_tree - gdn_spec_verify for a tree of drafts instead of a
+ * chain: node p continues from node parent[n][p] (an earlier node of the same
+ * request), or from the live slot where parent[n][p] is -1, so several
+ * continuations of one token are verified in one forward. The conv taps of a
+ * node read its ancestors' inputs, then the live slot's history. Committing is
+ * unchanged: gdn_spec_commit takes the accepted NODE as accepted[n] (its state
+ * holds its whole path). With parent[n][p] = p - 1 the results are
+ * gdn_spec_verify's, bit for bit. Pages: as gdn_spec_verify (the pages verify a
+ * chain; the tree form is this library's).
+ *
+ *   arguments as gdn_spec_verify, plus
+ *   parent  [N][P] int32, -1 <= parent[n][p] < p (parents before children).
+ *           Anything else sets GDN_DEVERR_TREE and the request writes nothing.
+ */
+gdn_status gdn_spec_verify_tree(const gdn_dims *dims, const uint16_t *qkv0, const float *conv_w,
+                                uint16_t *conv_hist, float *state, const int32_t *slot_idx,
+                                const int32_t *spec_slot_idx, const int32_t *parent, const float *alpha,
+                                const float *beta, const uint16_t *z, const float *gamma, float eps,
+                                uint16_t *o, uint16_t *ogate, int32_t num_seqs, int32_t num_pos,
+                                int32_t *dev_err, void *stream);
+
+/*
+ * The attention layers of the hybrid decoder (every fourth of its layers; page
+ * "Qwen3.8-27B: from model structure to vLLM inference data flow", section 01,
+ * GQA rows: Q [T,24,256], K and V [T,4,256], rotation of 64 of the 256
+ * dimensions, a sigmoid output gate; section 04: an FP8 cache in pages behind a
+ * block table). Geometry of these entry points: head_dim D 128 or 256, Hq a
+ * multiple of Hkv, pages of a multiple of 16 tokens; anything else returns
+ * GDN_ERR_UNSUPPORTED.
+ *
+ * gdn_kv_cache - one layer's paged key/value cache. A page holds page_tokens
+ * tokens of every kv head; token t of a request is row t % page_tokens of page
+ * block_table[t / page_tokens], and "slot" of a token means
+ * page * page_tokens + row. The pools are the caller's; 16-byte aligned, at most
+ * 2^31 - 1 rows (num_pages x num_kv_heads x page_tokens).
+ *   GDN_KV_BF16  bf16 values
+ *   GDN_KV_E4M3  E4M3 codes and one fp32 scale per (token, kv head) and per k
+ *                and v: value = E4M3(code) * scale, scale = max(amax, 1e-12) / 448
+ *                over the head's D values and code = E4M3(x / scale) rounded to
+ *                nearest even with saturation, divisions IEEE fp32 (the rule of
+ *                the FP8 quantisers below). A NaN gives a NaN code and does not
+ *                count in amax; an infinity makes the scale infinite and its
+ *                row's finite codes 0, its own NaN.
+ */
+#define GDN_KV_BF16 0
+#define GDN_KV_E4M3 1
+typedef struct gdn_kv_cache {
+    void *k, *v;             /* [num_pages][num_kv_heads][page_tokens][head_dim] bf16 or e4m3 */
+    float *k_scale, *v_scale; /* [num_pages][num_kv_heads][page_tokens] (e4m3), NULL (bf16)   */
+    int32_t num_pages, page_tokens, num_kv_heads, head_dim;
+    int32_t format;          /* GDN_KV_BF16 or GDN_KV_E4M3                                    */
+} gdn_kv_cache;
+
+/*
+ * gdn_kv_cache_write - k and v of T tokens into their slots, quantised as they
+ * are written where the cache is E4M3.
+ *
+ *   k, v      bf16, head h of token t at k + t * k_stride_t + h * k_stride_h
+ *             (D contiguous values; strides in elements, multiples of 8; 16-byte
+ *             aligned), so they may be views into one projection's output
+ *   kv_slot   [T] int32: a negative slot skips the token (padding, a rejected
+ *             draft); one past the pool sets GDN_DEVERR_SLOT and skips it. Two
+ *             tokens of one call must not name the same slot.
+ */
+gdn_status gdn_kv_cache_write(const gdn_kv_cache *cache, const uint16_t *k, int64_t k_stride_t,
+                              int64_t k_stride_h, const uint16_t *v, int64_t v_stride_t, int64_t v_stride_h,
+                              const int32_t *kv_slot, int32_t num_tokens, int32_t *dev_err, void *stream);
+
+/*
+ * gdn_kv_cache_read - the first tokens of each request gathered from its pages
+ * and dequantised (rounded once to bf16; a bf16 cache is copied).
+ *
+ *   block_table [N][max_pages] int32; a page outside [0, num_pages) sets
+ *               GDN_DEVERR_SLOT and its tokens are left unwritten
+ *   start       [N+1] int32, 0 = start[0] <= ... <= start[N] = T: request n's
+ *               tokens 0 .. start[n+1] - start[n] - 1 go to output rows start[n] ..
+ *               A request that its table cannot hold (more than max_pages pages),
+ *               or offsets that are not monotone within [0, T], set
+ *               GDN_DEVERR_OFFSETS and leave the rows concerned unwritten.
+ *   k_out, v_out [T][Hkv][D] bf16, 16-byte aligned
+ */
+gdn_status gdn_kv_cache_read(const gdn_kv_cache *cache, const int32_t *block_table, int32_t max_pages,
+                             const int32_t *start, int32_t num_seqs, int32_t num_tokens, uint16_t *k_out,
+                             uint16_t *v_out, int32_t *dev_err, void *stream);
+
+/*
+ * gdn_qk_norm_rope - per head: x / sqrt(mean(x^2) + eps) (.) gamma, then the
+ * rotation of the first rotary_dim dimensions by the token's position, in one
+ * pass over the queries and keys of a token; optionally the new keys, with the
+ * values, straight into the cache. Dimensions from rotary_dim on are only
+ * normalised. The pair of frequency i is (i, i + rotary_dim / 2), or with
+ * interleaved != 0 (2i, 2i + 1): (a, b) -> (a cos - b sin, b cos + a sin), angle
+ * position * inv_freq[i]. The angle is taken modulo a turn in 64-bit fixed
+ * point, so its error does not grow with the position.
+ *
+ *   q, k       bf16 with strides as in gdn_kv_cache_write; q may be NULL (then
+ *              q_out too): only the keys, e.g. to write accepted drafts again at
+ *              their final slots, bit for bit
+ *   q_gamma, k_gamma [D] fp32, 16-byte aligned;  eps >= 0 and finite
+ *   positions  [T] int32;  inv_freq [rotary_dim / 2] fp64, radians per position
+ *   rotary_dim a multiple of 16, 0 <= rotary_dim <= D (0: no rotation, positions
+ *              and inv_freq may be NULL)
+ *   q_out      [T][Hq][D] bf16;  k_out [T][Hkv][D] bf16 or NULL: rounded once,
+ *              16-byte aligned. In place (q_out = q, dense) is allowed.
+ *   cache      or NULL (then v and kv_slot too, and k_out is required): the
+ *              rotated key, before its rounding to bf16, and v go to kv_slot[t] as
+ *              gdn_kv_cache_write stores them
+ */
+gdn_status gdn_qk_norm_rope(const uint16_t *q, int64_t q_stride_t, int64_t q_stride_h, const uint16_t *k,
+                            int64_t k_stride_t, int64_t k_stride_h, const float *q_gamma, const float *k_gamma,
+                            float eps, const int32_t *positions, const double *inv_freq, int32_t rotary_dim,
+                            int32_t interleaved, uint16_t *q_out, uint16_t *k_out, const uint16_t *v,
+                            int64_t v_stride_t, int64_t v_stride_h, const gdn_kv_cache *cache,
+                            const int32_t *kv_slot, int32_t num_tokens, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t *dev_err, void *stream);
+
+/*
+ * gdn_tree_attention - attention of P = num_pos drafted tokens per request over
+ * its cached context and over each other, in one forward (P = 1: a decode step).
+ * Node j of request n is token ctx_len[n] + j of the request and its k and v are
+ * already in the cache there. It sees every context token and the nodes i whose
+ * bit is set in tree_mask[n][j] (its ancestors and itself, as a rule):
+ *   out = sum_t p_t v_t,  p = softmax over the seen t of scale * (q . k_t)
+ * and with a gate out <- out (.) sigmoid(gate) before its one rounding. A node
+ * that sees nothing gets zeros. A node that is not seen contributes nothing,
+ * whatever its values. Softmax statistics and sums are fp32.
+ *
+ *   q         [N*P][Hq][D] bf16, request-major (row n*P + j); query head h reads
+ *             kv head h / (Hq / Hkv)
+ *   block_table [N][max_pages] int32;  ctx_len [N] int32: a negative length is a
+ *             padding request (skipped, rows left untouched). ctx_len + P tokens
+ *             that the table cannot hold set GDN_DEVERR_OFFSETS, a page outside
+ *             [0, num_pages) sets GDN_DEVERR_SLOT, and the request writes nothing.
+ *   tree_mask [N][P] uint64 (bits from P on are ignored), or NULL: a chain, node
+ *             j sees nodes 0 .. j
+ *   gate      [N*P][Hq][D] bf16 or NULL
+ *   out       [N*P][Hq][D] bf16; may be q or gate itself
+ *   num_pos   1 <= P <= 64;  Hq / Hkv <= 64;  scale finite
+ *   workspace partial sums of requests that several CTAs share, and their
+ *             tickets: gdn_tree_attention_workspace_bytes(...) bytes, 256-byte
+ *             aligned and ZERO-FILLED before its first use; every call that
+ *             completes leaves the tickets at zero, so it is reusable without
+ *             clearing (after a call that reports GDN_DEVERR_TIMEOUT, clear it
+ *             again). Calls sharing one workspace must not overlap.
+ *   dev_err   GDN_DEVERR_TIMEOUT too, if a bounded wait inside the kernel ran out
+ * Pointers 16-byte aligned.
+ */
+gdn_status gdn_tree_attention(const gdn_kv_cache *cache, const uint16_t *q, const int32_t *block_table,
+                              int32_t max_pages, const int32_t *ctx_len, const uint64_t *tree_mask,
+                              const uint16_t *gate, float scale, uint16_t *out, int32_t num_seqs,
+                              int32_t num_pos, int32_t num_q_heads, void *workspace, size_t workspace_bytes,
+                              int32_t *dev_err, void *stream);
+
+/* Bytes of gdn_tree_attention's workspace for these sizes (whatever the lengths); 0 for invalid ones. */
+size_t gdn_tree_attention_workspace_bytes(const gdn_kv_cache *cache, int32_t num_seqs, int32_t num_pos,
+                                          int32_t num_q_heads);
 
 /* Bytes of one slot of the fp32 state pool: Hv*dv*dk*4 (3 MiB at 48x128x128,
  * the L00 table's "3 MiB per sequence per layer"). 0 for invalid dims. */
