@@ -1,0 +1,1013 @@
+// tree_attn.cuh - the kernel behind gdn_tree_attention: attention of the drafted
+// tokens of a tree over a request's paged cache and over each other, on tcgen05.
+// tree_attn_bf16.cu and tree_attn_e4m3.cu compile it for the two cache formats.
+//
+// Math, per query row (node j, query head h), over the tokens t that it sees:
+//   s_t = scale (q . k_t),  m = max s_t,  l = sum e^(s_t - m),  out = sum e^(s_t - m) v_t / l
+// and with a gate out <- out / (1 + e^-gate).
+//
+// Work. The unit of work is a tile of 128 cached tokens for one (request, kv head,
+// row tile): the query rows of the Hq / Hkv heads of all P nodes, up to kRows of
+// them. The tiles of all requests stand in one line, cut into equal pieces, one
+// per CTA (one CTA per SM): every SM streams the same number of keys and values,
+// whatever the lengths, and a single long request uses the whole GPU. The lengths
+// are read on the device, so a captured graph takes new ones. A (request, head,
+// row tile) that lies in several CTAs' pieces leaves a partial result per CTA in
+// the workspace, and the CTA that arrives last adds them up in a fixed order.
+//
+// Both products take the cache as their first operand, so a tile costs the tensor
+// cores the same 128 lanes for few query rows as for many columns:
+//   S^T [128 tokens x rows] = K Q^T    (K from shared memory as it lies in the cache)
+//   O^T [128 of D x rows]   = V^T P^T  (V the same, read along its other dimension)
+// A bf16 cache runs them in bf16. An E4M3 cache stays E4M3 in shared memory, and
+// the other operand is written as the sum of two E4M3 terms, the value and what
+// its rounding left: 4 + 4 significant bits, as many as bf16 has. For Q (bf16
+// values, scaled by a power of two per row) that is exact down to 2^-17 of the
+// row's largest value; a weight of P is off by at most 2^-8 of itself or 2^-18 of
+// its tile's largest. The two terms are neighbouring columns of one MMA, added up
+// as they are read. The scales stay outside: the key's multiplies the score, the
+// value's its weight (relative to the tile's largest scale).
+//
+// Softmax without a chain between tiles: a tile's weights are taken relative to
+// its own maximum, and the accumulators of the output, in registers, take the
+// tile's product times e^(tile's maximum - running maximum). So the next tile's
+// scores never wait for the last one's.
+//
+// Roles (384 threads): warps 0-3 softmax (a thread per token), warps 4-7 output
+// (a thread per value of D, mod 128), warp 8 copies (TMA, 16 KB blocks of 128
+// tokens x 128 bytes into a ring), warp 9 the MMAs (one thread), warp 10 the
+// query rows, warp 11 the scales. Every wait is bounded: one that runs out sets
+// GDN_DEVERR_TIMEOUT and the CTA leaves.
+//
+// What bounds it: the cache's bytes from HBM while the rows of a tile are few, the
+// MMAs (their operand reads from shared memory, at N < 128) when they are many.
+#pragma once
+
+#include "device.cuh"
+#include "launch.h"
+#include "umma.cuh"
+
+namespace gdn {
+namespace tree_attn {
+
+constexpr int kThreads = 384;
+constexpr int kTile = 128;               // tokens per tile
+constexpr uint32_t kBlock = 128 * 128;   // bytes of one ring block: 128 tokens x 128 bytes
+constexpr int kMaxCtas = 152;
+constexpr int kSmemLimit = 227 * 1024;
+constexpr int kTicketBytes = 1024;
+constexpr int kScSlots = 4;              // tiles of scales in flight
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Args {
+  TreeAttnArgs p;
+  KvArgs c;
+  int rows;       // query rows per row tile (the last one may have fewer)
+  int row_tiles;
+  int box;        // tokens per TMA box: a power of two that divides the page, at most 128
+  int slot_floats;  // workspace floats per partial
+};
+
+template <int D, bool kE4m3, int kRows>
+struct Cfg {
+  static constexpr int kBlk = D * (kE4m3 ? 1 : 2) / 128;  // ring blocks of a tile's K, and of its V
+  static constexpr int kHalves = D / 128;
+  static constexpr int kTerms = kE4m3 ? 2 : 1;
+  static constexpr int kCols = kTerms * kRows;
+  static constexpr int kOBuf = (2 + 2 * kHalves) * kCols <= 512 ? 2 : 1;
+  // two, or the first scores of a segment would wait for the output of the last, which follows them
+  static constexpr int kQBuf = 2;
+  static constexpr int kQBytes = kCols * 128 * kBlk;
+  // shared memory behind the ring, by byte offsets from its end
+  static constexpr int oP = 0;
+  static constexpr int oQ = oP + 2 * (int)kBlock;
+  static constexpr int oSc = oQ + kQBuf * kQBytes;                          // [kScSlots][2][128] fp32
+  static constexpr int oMax = oSc + (kE4m3 ? kScSlots * 2 * kTile * 4 : 0);  // [2][kRows + 1][4]
+  static constexpr int oSum = oMax + 2 * (kRows + 1) * 16;                  // [2][kRows][4]
+  static constexpr int oTile = oSum + 2 * kRows * 16;                       // [2][kRows + 4]: maxima, the V scale
+  static constexpr int oAb = oTile + 2 * (kRows + 4) * 4;                   // [2][kRows] float2
+  static constexpr int oMask = oAb + 2 * kRows * 8;                         // [kQBuf][kRows] uint64
+  static constexpr int oQs = oMask + kQBuf * kRows * 8;                     // [kQBuf][kRows] fp32
+  static constexpr int oFin = oQs + kQBuf * kRows * 4;                      // [2][kRows] fp32
+  static constexpr int oBars = oFin + 2 * kRows * 4;
+  static constexpr int kRest = oBars + 768;
+  static constexpr int kFit = (kSmemLimit - kRest) / (int)kBlock;
+  // an even number of blocks keeps the two bf16 blocks of a 128-wide half of V side by side
+  static constexpr int kStages = kE4m3 ? kFit : kFit / 2 * 2;
+  static constexpr int kSmem = kStages * (int)kBlock + kRest;
+  static_assert(kStages >= kBlk + 2, "a tile's whole V stays until its weights are there");
+  static_assert((2 + kOBuf * kHalves) * kCols <= 512, "tensor memory");
+};
+
+// One CTA's piece of the line of tiles.
+struct Plan {
+  long long total, lo;
+  int count, n, u, t;
+};
+
+struct Bars {
+  uint64_t full[12], empty[12];
+  uint64_t q_full[2], q_empty[2], s_full[2], s_empty[2], p_full[2], p_empty[2], o_full[2], o_empty[2];
+  uint64_t st_full[2], st_empty[2], sc_full[kScSlots], sc_empty[kScSlots], drain;
+  uint32_t tmem;
+  int abort;
+  unsigned long long dirty[2];  // nodes of the tile whose values are no numbers
+  Plan plan;
+  long long warp_total[kThreads / 32];
+};
+static_assert(sizeof(Bars) <= 768, "barrier area");
+
+// The piece's segments: runs of tiles of one (request n, unit u = head x row tiles + row tile).
+struct Seg {
+  int n, u, t0, t1, tiles, len, ctx;
+  long long first;  // the unit's first tile in the line
+};
+
+__device__ __forceinline__ int tiles_of(const Args& a, int ctx, bool* too_long = nullptr) {
+  if (ctx < 0) return 0;
+  const long long len = (long long)ctx + a.p.P;
+  if ((len + a.c.page - 1) / a.c.page > a.p.max_pages || len > INT32_MAX - kTile) {
+    if (too_long) *too_long = true;
+    return 0;
+  }
+  return (int)((len + kTile - 1) / kTile);
+}
+
+struct Walk {
+  int n, u, t, left, units, tiles, ctx;
+  long long at;
+  __device__ __forceinline__ Walk(const Args& a, const Plan& p)
+      : n(p.n), u(p.u), t(p.t), left(p.count), units(a.c.Hkv * a.row_tiles), tiles(0), ctx(0), at(p.lo) {
+    if (left > 0) load(a);
+  }
+  __device__ __forceinline__ void load(const Args& a) {
+    ctx = __ldg(a.p.ctx + n);
+    tiles = tiles_of(a, ctx);
+  }
+  __device__ __forceinline__ bool next(const Args& a, Seg& s) {
+    if (left <= 0) return false;
+    while (tiles == 0) {  // the piece has tiles left, so a request with some follows
+      ++n;
+      load(a);
+    }
+    const int take = min(tiles - t, left);
+    s = Seg{n, u, t, t + take, tiles, ctx + a.p.P, ctx, at - t};
+    left -= take;
+    at += take;
+    t = 0;
+    if (++u == units) {
+      u = 0;
+      ++n;
+      if (left > 0) load(a);
+    }
+    return true;
+  }
+};
+
+// Waits for a phase of the barrier, no longer than the time limit or until another role gave up.
+static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int* abort) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1; it < kWaitMaxIters; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 31u) == 0 && (*(volatile int*)abort || globaltimer_ns() - t0 > kWaitLimitNs)) break;
+  }
+  *(volatile int*)abort = 1;
+  return false;
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort);
+}
+
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The warp's largest value (NaN is passed over).
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
+  float2 r;
+  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(h));
+  return r;
+}
+// Eight values as E4M3 (first) and what their rounding left, again as E4M3 (rest).
+__device__ __forceinline__ void two_terms(const float (&x)[8], uint2& first, uint2& rest) {
+  uint32_t a[4], b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[i] = e4m3x2(x[2 * i], x[2 * i + 1]);
+    const float2 f = from_e4m3x2(a[i]);
+    b[i] = e4m3x2(x[2 * i] - f.x, x[2 * i + 1] - f.y);
+  }
+  first = make_uint2(a[0] | (a[1] << 16), a[2] | (a[3] << 16));
+  rest = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+}
+__device__ __forceinline__ uint4 to_bf16x8(const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = (uint32_t)f32_to_bf16(x[2 * i]) | ((uint32_t)f32_to_bf16(x[2 * i + 1]) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Byte `at` of row `row` in a block of 128-byte rows under the 128-byte swizzle.
+__device__ __forceinline__ uint32_t swz(int row, int at) {
+  return (uint32_t)(row * 128 + ((((at >> 4) ^ (row & 7)) << 4) | (at & 15)));
+}
+
+// Descriptor of 128-byte swizzled rows read along their other dimension: a row is one step of the
+// contraction, its 128 bytes run along M or N; eight-row groups 1024 bytes apart, and the next 128
+// bytes of M one ring block further (used by bf16 alone, where 128 values are two blocks).
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kBlock >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+
+// Eight consecutive columns of this thread's lane, without waiting.
+__device__ __forceinline__ void ld8_nowait(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+
+__device__ __forceinline__ void sync_group(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+// 128 threads of barrier `id`: whether any of them says so.
+__device__ __forceinline__ bool any_in_group(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ int cta_of(long long tile, long long total, int grid) {
+  return (int)(((tile + 1) * grid - 1) / total);
+}
+
+template <int D, bool kE4m3, int kRows>
+__global__ void __launch_bounds__(kThreads, 1) kernel(const Args a, const __grid_constant__ CUtensorMap tmk,
+                                                      const __grid_constant__ CUtensorMap tmv) {
+  using C = Cfg<D, kE4m3, kRows>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  unsigned char* rest = smem + C::kStages * kBlock;
+  Bars* B = reinterpret_cast<Bars*>(rest + C::oBars);
+  const TreeAttnArgs& p = a.p;
+  const KvArgs& c = a.c;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t ring = smem_u32(smem);
+
+  // ---- this CTA's piece: a scan over the requests' tiles
+  {
+    const int per = (p.N + kThreads - 1) / kThreads, n0 = min(p.N, tid * per), n1 = min(p.N, n0 + per);
+    long long mine = 0;
+    bool too_long = false;
+    for (int n = n0; n < n1; ++n) mine += tiles_of(a, p.ctx[n], &too_long);
+    if (too_long && blockIdx.x == 0) report(p.dev_err, GDN_DEVERR_OFFSETS);
+    long long upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += o;
+    }
+    if (lane == 31) B->warp_total[warp] = upto;
+    if (tid == 0) {
+      for (int i = 0; i < C::kStages; ++i) {
+        mbar_init(&B->full[i], 1);
+        mbar_init(&B->empty[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&B->q_full[i], 32);
+        mbar_init(&B->q_empty[i], 9);
+        mbar_init(&B->s_full[i], 1);
+        mbar_init(&B->s_empty[i], 4);
+        mbar_init(&B->p_full[i], 128);
+        mbar_init(&B->p_empty[i], 1);
+        mbar_init(&B->o_full[i], 1);
+        mbar_init(&B->o_empty[i], 4);
+        mbar_init(&B->st_full[i], 128);
+        mbar_init(&B->st_empty[i], 4);
+        B->dirty[i] = 0;
+      }
+      for (int i = 0; i < kScSlots; ++i) {
+        mbar_init(&B->sc_full[i], 32);
+        mbar_init(&B->sc_empty[i], 4);
+      }
+      mbar_init(&B->drain, 1);
+      B->abort = 0;
+      B->plan.count = 0;
+      fence_mbar_init();
+    }
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += B->warp_total[w];
+      total += B->warp_total[w];
+    }
+    before += upto - mine;
+    const int units = c.Hkv * a.row_tiles;
+    total *= units;
+    const long long ctas = min((long long)gridDim.x, total);  // with a piece: none of them empty
+    const long long lo = ctas ? total * blockIdx.x / ctas : 0, hi = ctas ? total * (blockIdx.x + 1) / ctas : 0;
+    if (blockIdx.x < ctas && before * units <= lo && lo < (before + mine) * units) {
+      long long at = before * units;
+      for (int n = n0; n < n1; ++n) {
+        const long long here = (long long)tiles_of(a, p.ctx[n]) * units;
+        if (lo < at + here) {
+          const int tiles = (int)(here / units);
+          B->plan = Plan{total, lo, (int)(hi - lo), n, (int)((lo - at) / tiles), (int)((lo - at) % tiles)};
+          break;
+        }
+        at += here;
+      }
+    }
+    if (warp == 9) umma::tmem_alloc(&B->tmem, 512);
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+  }
+  const Plan plan = B->plan;
+  const uint32_t tmem = B->tmem;
+  int* abort = &B->abort;
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ copies
+    // K of a tile, then V of the tile before it: the order in which the MMAs take them.
+    const int boxes = kTile / a.box, total_rows = c.slots * c.Hkv;
+    int pos = 0;  // blocks issued
+    bool ok = true;
+    auto blocks = [&](const CUtensorMap* map, int row) {
+      for (int b = 0; b < C::kBlk && ok; ++b, ++pos) {
+        const int st = pos % C::kStages;
+        ok = wait(&B->empty[st], ((pos / C::kStages) & 1) ^ 1, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&B->full[st], kBlock);
+        __syncwarp();
+        if (lane < boxes)
+          tma_load_2d(smem + st * kBlock + lane * a.box * 128, map, b * (kE4m3 ? 128 : 64), row, &B->full[st]);
+      }
+    };
+    Walk walk(a, plan);
+    Seg s;
+    int held = -1, row_v = 0;  // the last tile's rows, its V still to come
+    while (ok && walk.next(a, s)) {
+      const int h = s.u / a.row_tiles;
+      const int32_t* table = p.table + (size_t)s.n * p.max_pages;
+      auto row_of = [&](int t) {  // first row of this lane's box; behind the last token: rows that read as zeros
+        const int tok = t * kTile + lane * a.box;
+        if (lane >= boxes || tok >= s.len) return total_rows;
+        const int page = __ldg(table + tok / c.page);
+        if (page < 0 || page >= c.pages) return total_rows;
+        return (page * c.Hkv + h) * c.page + tok % c.page;
+      };
+      int row = row_of(s.t0);
+      for (int t = s.t0; t < s.t1 && ok; ++t) {
+        const int ahead = t + 1 < s.t1 ? row_of(t + 1) : 0;
+        blocks(&tmk, row);
+        if (held >= 0) blocks(&tmv, row_v);
+        held = t;
+        row_v = row;
+        row = ahead;
+      }
+    }
+    if (ok && held >= 0) blocks(&tmv, row_v);
+    if (!ok) {  // copies in flight land before the CTA may leave
+      for (int back = 1; back <= C::kStages && pos - back >= 0; ++back)
+        mbar_wait_bounded(&B->full[(pos - back) % C::kStages], ((pos - back) / C::kStages) & 1);
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMAs
+    if (lane == 0) {
+      const int rp = kE4m3 ? (a.rows + 7) / 8 * 8 : (a.rows + 15) / 16 * 16;  // rows as columns of the MMAs
+      const int N = C::kTerms * rp;
+      constexpr uint32_t kKind = kE4m3 ? umma::kKindF8 : umma::kKindF16, kType = kE4m3 ? umma::kE4M3 : umma::kBF16;
+      const uint32_t id_s = umma::idesc(kType, false, false, kTile, N), id_o = umma::idesc(kType, true, true, kTile, N);
+      const uint32_t sQ = smem_u32(rest + C::oQ), sP = smem_u32(rest + C::oP);
+      int pos = 0, i = 0, seg = 0;
+      bool ok = true;
+      auto block = [&]() {  // the next ring block, once its copy has landed
+        const int st = pos % C::kStages;
+        ok = ok && wait(&B->full[st], (pos / C::kStages) & 1, abort);
+        ++pos;
+        return st;
+      };
+      auto product_o = [&](int j) {
+        const int b = j & 1, ob = j % C::kOBuf;
+        ok = ok && wait(&B->p_full[b], (j >> 1) & 1, abort) &&
+             wait(&B->o_empty[ob], ((j / C::kOBuf) & 1) ^ 1, abort);
+        if (!ok) return;
+        umma::fence_after_sync();
+#pragma unroll
+        for (int h = 0; h < C::kHalves; ++h) {
+          const int st = block(), st2 = kE4m3 ? st : block();
+          if (!ok) return;
+          umma::fence_after_sync();
+          const uint32_t d = tmem + 2 * C::kCols + (ob * C::kHalves + h) * C::kCols;
+          constexpr int kSteps = kE4m3 ? 4 : 8, kStepBytes = kE4m3 ? 4096 : 2048;  // 32 or 16 tokens a step
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k)
+            umma::mma<kKind>(d, desc_mn(ring + st * kBlock + k * kStepBytes), desc_mn(sP + b * kBlock + k * kStepBytes),
+                             id_o, k > 0);
+          umma::commit(&B->empty[st]);
+          if (!kE4m3) umma::commit(&B->empty[st2]);
+        }
+        umma::commit(&B->p_empty[b]);
+        umma::commit(&B->o_full[ob]);
+      };
+      Walk walk(a, plan);
+      Seg s;
+      while (ok && walk.next(a, s)) {
+        const int qb = seg % C::kQBuf;
+        ok = wait(&B->q_full[qb], (seg / C::kQBuf) & 1, abort);
+        for (int t = s.t0; t < s.t1 && ok; ++t, ++i) {
+          const int b = i & 1;
+          ok = wait(&B->s_empty[b], ((i >> 1) & 1) ^ 1, abort);
+          if (!ok) break;
+          umma::fence_after_sync();
+          for (int kb = 0; kb < C::kBlk; ++kb) {
+            const int st = block();
+            if (!ok) break;
+            umma::fence_after_sync();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma::mma<kKind>(tmem + b * C::kCols, umma::smem_desc_sw128(ring + st * kBlock + k * 32),
+                               umma::smem_desc_sw128(sQ + qb * C::kQBytes + kb * (C::kCols * 128) + k * 32), id_s,
+                               kb + k > 0);
+            umma::commit(&B->empty[st]);
+          }
+          if (!ok) break;
+          umma::commit(&B->s_full[b]);
+          if (t + 1 == s.t1) umma::commit(&B->q_empty[qb]);
+          if (i > 0) product_o(i - 1);
+        }
+        ++seg;
+      }
+      if (ok && i > 0) product_o(i - 1);
+      umma::commit(&B->drain);  // nothing of the tensor core's is in flight when the CTA leaves
+      mbar_wait_bounded(&B->drain, 0);
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ query rows
+    Walk walk(a, plan);
+    Seg s;
+    int seg = 0;
+    bool ok = true;
+    const int rp = kE4m3 ? (a.rows + 7) / 8 * 8 : (a.rows + 15) / 16 * 16;
+    const float to_log2 = p.scale * kLog2e;
+    while (ok && walk.next(a, s)) {
+      const int qb = seg % C::kQBuf;
+      ok = wait(&B->q_empty[qb], ((seg / C::kQBuf) & 1) ^ 1, abort);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const int h = s.u / a.row_tiles, r0 = (s.u % a.row_tiles) * a.rows;
+      unsigned char* q_s = rest + C::oQ + qb * C::kQBytes;
+      float* qs_s = reinterpret_cast<float*>(rest + C::oQs) + qb * kRows;
+      uint64_t* mask_s = reinterpret_cast<uint64_t*>(rest + C::oMask) + qb * kRows;
+      for (int r = lane; r < rp; r += 32) {
+        const int j = (r0 + r) / p.G;
+        uint64_t m = 0;
+        if (r < a.rows && j < p.P) m = p.mask ? __ldg(p.mask + (size_t)s.n * p.P + j) : j == 63 ? ~0ull : (2ull << j) - 1;
+        mask_s[r] = m;
+      }
+      constexpr int kBatch = 8;
+      for (int rb = 0; rb < rp; rb += kBatch) {
+        uint4 raw[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = rb + i, j = (r0 + r) / p.G, g = (r0 + r) % p.G;
+          raw[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < a.rows && j < p.P && lane < D / 8)
+            raw[i] = *reinterpret_cast<const uint4*>(p.q + (((size_t)s.n * p.P + j) * p.Hq + h * p.G + g) * D + lane * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = rb + i;
+          if constexpr (!kE4m3) {
+            // eight values are one 16-byte piece of block lane / 8
+            if (lane < D / 8)
+              *reinterpret_cast<uint4*>(q_s + (lane >> 3) * (C::kCols * 128) + swz(r, (lane & 7) * 16)) = raw[i];
+            if (lane == 0) qs_s[r] = to_log2;
+          } else {
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            float x[8], most = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[2 * e] = __uint_as_float(w[e] << 16);
+              x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(x[e]));
+            most = warp_max(most);
+            // a power of two that takes the largest value below 256; a row with an infinity has no scores
+            const int ex = (int)(__float_as_uint(most) >> 23) - 127;
+            const int up = most == 0.f ? 0 : min(7 - ex, 120);
+            const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= f;
+            uint2 first, second;
+            two_terms(x, first, second);
+            if (lane < D / 8) {
+              unsigned char* blk = q_s + (lane >> 4) * (C::kCols * 128);
+              *reinterpret_cast<uint2*>(blk + swz(r, (lane & 15) * 8)) = first;
+              *reinterpret_cast<uint2*>(blk + swz(rp + r, (lane & 15) * 8)) = second;
+            }
+            const float down = __uint_as_float((uint32_t)(127 - up) << 23);
+            if (lane == 0) qs_s[r] = ex == 128 ? __uint_as_float(0x7fffffffu) : to_log2 * down;
+          }
+        }
+      }
+      umma::fence_proxy_async_smem();
+      arrive(&B->q_full[qb]);
+      ++seg;
+    }
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ scales (E4M3)
+    if constexpr (kE4m3) {
+      Walk walk(a, plan);
+      Seg s;
+      int i = 0;
+      bool ok = true;
+      while (ok && walk.next(a, s)) {
+        const int h = s.u / a.row_tiles;
+        const int32_t* table = p.table + (size_t)s.n * p.max_pages;
+        auto row_of = [&](int t) {  // four tokens a lane, all in one page
+          const int tok = t * kTile + lane * 4;
+          if (tok >= s.len) return -1;
+          const int page = __ldg(table + tok / c.page);
+          return page < 0 || page >= c.pages ? -1 : (page * c.Hkv + h) * c.page + tok % c.page;
+        };
+        int row = row_of(s.t0);
+        for (int t = s.t0; t < s.t1; ++t, ++i) {
+          const int slot = i % kScSlots;
+          float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f), v4 = k4;
+          if (row >= 0) {
+            k4 = __ldg(reinterpret_cast<const float4*>(c.k_scale + row));
+            v4 = __ldg(reinterpret_cast<const float4*>(c.v_scale + row));
+          }
+          row = t + 1 < s.t1 ? row_of(t + 1) : -1;
+          ok = wait(&B->sc_empty[slot], ((i / kScSlots) & 1) ^ 1, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          float4* dst = reinterpret_cast<float4*>(rest + C::oSc) + slot * 2 * (kTile / 4);
+          dst[lane] = k4;
+          dst[kTile / 4 + lane] = v4;
+          arrive(&B->sc_full[slot]);
+        }
+      }
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ softmax: thread = token of the tile
+    const int rp = kE4m3 ? (a.rows + 7) / 8 * 8 : (a.rows + 15) / 16 * 16;
+    const int used = (a.rows + 7) / 8;  // groups of eight rows
+    float* sums = reinterpret_cast<float*>(rest + C::oSum);
+    float* maxima = reinterpret_cast<float*>(rest + C::oMax);
+    float* tile_s = reinterpret_cast<float*>(rest + C::oTile);
+    const float* scales = reinterpret_cast<const float*>(rest + C::oSc);
+    Walk walk(a, plan);
+    Seg s;
+    int i = 0, seg = 0;
+    bool ok = true;
+    while (walk.next(a, s)) {
+      const int qb = seg % C::kQBuf;
+      ok = ok && wait(&B->q_full[qb], (seg / C::kQBuf) & 1, abort);
+      ok = __all_sync(0xffffffffu, ok);
+      const float* qs_s = reinterpret_cast<const float*>(rest + C::oQs) + qb * kRows;
+      const uint64_t* mask_s = reinterpret_cast<const uint64_t*>(rest + C::oMask) + qb * kRows;
+      for (int t = s.t0; t < s.t1; ++t, ++i) {
+        const int b = i & 1, ph = (i >> 1) & 1;
+        const int tok = t * kTile + tid;
+        float sk = 1.f, sv = 1.f;
+        if constexpr (kE4m3) {
+          const int slot = i % kScSlots;
+          ok = ok && wait(&B->sc_full[slot], (i / kScSlots) & 1, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          sk = scales[slot * 2 * kTile + tid];
+          sv = scales[slot * 2 * kTile + kTile + tid];
+          __syncwarp();
+          if (lane == 0) arrive(&B->sc_empty[slot]);
+          if (tok >= s.len) sv = 0.f;
+        }
+        ok = ok && wait(&B->s_full[b], ph, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        umma::fence_after_sync();
+        float x[kRows];
+        const uint32_t ts = umma::taddr(tmem, 32 * warp, b * C::kCols);
+#pragma unroll
+        for (int g0 = 0; g0 < kRows / 8; g0 += 4) {  // up to 32 rows at a time
+          uint32_t u[4][8], w[kE4m3 ? 4 : 1][8];
+#pragma unroll
+          for (int g = 0; g < 4 && g0 + g < kRows / 8; ++g)
+            if (g0 + g < used) {
+              ld8_nowait(ts + (g0 + g) * 8, u[g]);
+              if constexpr (kE4m3) ld8_nowait(ts + rp + (g0 + g) * 8, w[g]);
+            }
+          umma::wait_ld();
+#pragma unroll
+          for (int g = 0; g < 4 && g0 + g < kRows / 8; ++g)
+            if (g0 + g < used) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int r = (g0 + g) * 8 + e;
+                float v = __uint_as_float(u[g][e]);
+                if constexpr (kE4m3) v = (v + __uint_as_float(w[g][e])) * sk;
+                x[r] = v * qs_s[r];
+              }
+            }
+        }
+        umma::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive(&B->s_empty[b]);
+        // the statistics of two tiles back have been read
+        ok = ok && wait(&B->st_empty[b], ph ^ 1, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if ((t + 1) * kTile > s.ctx) {  // drafted tokens, or tokens behind the last
+          const int node = tok - s.ctx;
+#pragma unroll
+          for (int g = 0; g < kRows / 8; ++g)
+            if (g < used) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int r = g * 8 + e;
+                const bool seen = node < 0 || (node < p.P && ((mask_s[r] >> (node & 63)) & 1));
+                x[r] = seen ? x[r] : -INFINITY;
+              }
+            }
+          // A weight of zero does not take a NaN or an infinity out of a product. Values behind the last
+          // token become zeros; a drafted token's that are no numbers too, and the output warps add them
+          // to the rows that see the token.
+          if (node >= 0) {
+            const int n_tiles = plan.count;
+            const int first = C::kBlk * min(i + 2, n_tiles) + C::kBlk * i;  // V's place in the order of copies
+            bool odd = false;
+            if (ok) {
+              for (int vb = 0; vb < C::kBlk; ++vb) {
+                const int st = (first + vb) % C::kStages;
+                ok = ok && wait(&B->full[st], ((first + vb) / C::kStages) & 1, abort);
+                if (!ok) break;
+                uint4* row = reinterpret_cast<uint4*>(smem + st * kBlock + tid * 128);
+                for (int k = 0; k < 8; ++k) {
+                  uint4& at = row[k ^ (tid & 7)];  // eight neighbours, eight different banks
+                  uint4 v = at;
+                  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+                  bool fix = false;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    if constexpr (kE4m3) {
+#pragma unroll
+                      for (int y = 0; y < 32; y += 8)
+                        if (((w[e] >> y) & 0x7f) == 0x7f) fix = true, w[e] &= ~(0xffu << y);
+                    } else {
+#pragma unroll
+                      for (int y = 0; y < 32; y += 16)
+                        if (((w[e] >> y) & 0x7f80) == 0x7f80) fix = true, w[e] &= ~(0xffffu << y);
+                    }
+                  }
+                  if (node >= p.P) {
+                    at = make_uint4(0u, 0u, 0u, 0u);
+                  } else if (fix) {
+                    odd = true;
+                    at = v;
+                  }
+                }
+              }
+            }
+            if (node < p.P) {
+              if (kE4m3 && !(fabsf(sv) < INFINITY)) {
+                odd = true;
+                sv = 0.f;
+              }
+              if (odd) atomicOr(&B->dirty[b], 1ull << node);
+            }
+          }
+          ok = __all_sync(0xffffffffu, ok);
+        }
+        // ---- the tile's maximum of each row
+        float keep[kRows / 32 > 0 ? kRows / 32 : 1];
+#pragma unroll
+        for (int g = 0; g < kRows / 8; ++g)
+          if (g < used) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int r = g * 8 + e;
+              const float m = warp_max(x[r]);
+              if (lane == (r & 31)) keep[r >> 5] = m;
+            }
+          }
+        float* max_b = maxima + b * (kRows + 1) * 4;
+#pragma unroll
+        for (int k = 0; k < kRows; k += 32)
+          if (k + lane < used * 8) max_b[(k + lane) * 4 + warp] = keep[k >> 5];
+        if constexpr (kE4m3) {
+          const float m = warp_max(fabsf(sv));
+          if (lane == 0) max_b[kRows * 4 + warp] = m;
+        }
+        sync_group(1);
+        float f = 1.f;  // the weight's factor: the value's scale, the tile's largest at 256
+        if constexpr (kE4m3) {
+          const float4 v4 = *reinterpret_cast<const float4*>(max_b + kRows * 4);
+          const float most = fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w));
+          f = sv == 0.f ? 0.f : 256.f * __fdiv_rn(sv, most);
+          if (tid == 0) tile_s[b * (kRows + 4) + kRows] = most * (1.f / 256.f);
+        }
+        ok = ok && wait(&B->p_empty[b], ph ^ 1, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        unsigned char* prow = rest + C::oP + b * kBlock;
+#pragma unroll
+        for (int g = 0; g < kRows / 8; ++g)
+          if (g < used) {
+            float w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int r = g * 8 + e;
+              const float4 m4 = *reinterpret_cast<const float4*>(max_b + r * 4);
+              float m = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+              if (tid == r) tile_s[b * (kRows + 4) + r] = m;
+              m = m == -INFINITY ? 0.f : m;
+              x[r] = ex2(x[r] - m);
+              w[e] = kE4m3 ? x[r] * f : x[r];
+            }
+            if constexpr (kE4m3) {
+              uint2 first, second;
+              two_terms(w, first, second);
+              *reinterpret_cast<uint2*>(prow + swz(tid, g * 8)) = first;
+              *reinterpret_cast<uint2*>(prow + swz(tid, rp + g * 8)) = second;
+            } else {
+              *reinterpret_cast<uint4*>(prow + swz(tid, g * 16)) = to_bf16x8(w);
+            }
+          }
+        umma::fence_proxy_async_smem();
+        arrive(&B->p_full[b]);
+        // ---- the warp's sums: eight rows at a time, halved over the lanes
+#pragma unroll
+        for (int g = 0; g < kRows / 8; ++g)
+          if (g < used) {
+            float v4[4], v2[2], v1;
+            const bool h16 = lane & 16, h8 = lane & 8, h4 = lane & 4;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float give = h16 ? x[g * 8 + e] : x[g * 8 + e + 4], stay = h16 ? x[g * 8 + e + 4] : x[g * 8 + e];
+              v4[e] = stay + __shfl_xor_sync(0xffffffffu, give, 16);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float give = h8 ? v4[e] : v4[e + 2], stay = h8 ? v4[e + 2] : v4[e];
+              v2[e] = stay + __shfl_xor_sync(0xffffffffu, give, 8);
+            }
+            const float give = h4 ? v2[0] : v2[1], stay = h4 ? v2[1] : v2[0];
+            v1 = stay + __shfl_xor_sync(0xffffffffu, give, 4);
+            v1 += __shfl_xor_sync(0xffffffffu, v1, 2);
+            v1 += __shfl_xor_sync(0xffffffffu, v1, 1);
+            const int r = g * 8 + (h16 ? 4 : 0) + (h8 ? 2 : 0) + (h4 ? 1 : 0);
+            if ((lane & 3) == 0) sums[(b * kRows + r) * 4 + warp] = v1;
+          }
+        arrive(&B->st_full[b]);
+      }
+      __syncwarp();
+      if (lane == 0) arrive(&B->q_empty[qb]);
+      ++seg;
+    }
+  } else {
+    // ------------------------------------------------------------ output: thread = value of D, mod 128
+    const int rp = kE4m3 ? (a.rows + 7) / 8 * 8 : (a.rows + 15) / 16 * 16;
+    const int used = (a.rows + 7) / 8;
+    const int ot = tid - 128;
+    const float* sums = reinterpret_cast<const float*>(rest + C::oSum);
+    const float* tile_s = reinterpret_cast<const float*>(rest + C::oTile);
+    float2* ab = reinterpret_cast<float2*>(rest + C::oAb);
+    float* fin = reinterpret_cast<float*>(rest + C::oFin);
+    float* parts = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kTicketBytes);
+    int* tickets = static_cast<int*>(p.workspace);
+    Walk walk(a, plan);
+    Seg s;
+    int i = 0, seg = 0;
+    bool ok = true;
+    while (walk.next(a, s)) {
+      const int qb = seg % C::kQBuf;
+      const int h = s.u / a.row_tiles, r0 = (s.u % a.row_tiles) * a.rows;
+      const int rows = min(a.rows, p.P * p.G - r0);
+      const int32_t* table = p.table + (size_t)s.n * p.max_pages;
+      const uint64_t* mask_s = reinterpret_cast<const uint64_t*>(rest + C::oMask) + qb * kRows;
+      bool bad = false;  // pages out of the pool among this segment's
+      {
+        const int last = (min(s.len, s.t1 * kTile) - 1) / c.page;
+        for (int k = s.t0 * kTile / c.page + ot; k <= last; k += 128) {
+          const int page = __ldg(table + k);
+          bad |= page < 0 || page >= c.pages;
+        }
+      }
+      ok = ok && wait(&B->q_full[qb], (seg / C::kQBuf) & 1, abort);
+      float acc[C::kHalves][kRows];
+#pragma unroll
+      for (int k = 0; k < C::kHalves; ++k)
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) acc[k][r] = 0.f;
+      float m_run = -INFINITY, l_run = 0.f;  // of row ot
+      for (int t = s.t0; t < s.t1; ++t, ++i) {
+        const int b = i & 1, ph = (i >> 1) & 1, ob = i % C::kOBuf;
+        ok = ok && wait(&B->st_full[b], ph, abort);
+        if (ot < used * 8) {
+          const float mt = tile_s[b * (kRows + 4) + ot];
+          const float4 l4 = *reinterpret_cast<const float4*>(sums + (b * kRows + ot) * 4);
+          const float lt = (l4.x + l4.y) + (l4.z + l4.w);
+          const float mn = fmaxf(m_run, mt);
+          const float keep = m_run == -INFINITY ? 0.f : ex2(m_run - mn), w = mt == -INFINITY ? 0.f : ex2(mt - mn);
+          l_run = l_run * keep + lt * w;
+          m_run = mn;
+          ab[b * kRows + ot] = make_float2(keep, kE4m3 ? w * tile_s[b * (kRows + 4) + kRows] : w);
+        }
+        sync_group(2);
+        ok = ok && wait(&B->o_full[ob], (i / C::kOBuf) & 1, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        umma::fence_after_sync();
+#pragma unroll
+        for (int k = 0; k < C::kHalves; ++k) {
+          const uint32_t to = umma::taddr(tmem, 32 * (warp - 4), 2 * C::kCols + (ob * C::kHalves + k) * C::kCols);
+#pragma unroll
+          for (int g = 0; g < kRows / 8; ++g)
+            if (g < used) {
+              uint32_t u[8], w[8];
+              ld8_nowait(to + g * 8, u);
+              if constexpr (kE4m3) ld8_nowait(to + rp + g * 8, w);
+              umma::wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int r = g * 8 + e;
+                const float2 f = ab[b * kRows + r];
+                float o = __uint_as_float(u[e]);
+                if constexpr (kE4m3) o += __uint_as_float(w[e]);
+                acc[k][r] = fmaf(o, f.y, acc[k][r] * f.x);
+              }
+            }
+        }
+        umma::fence_before_sync();
+        const unsigned long long dirty = ((t + 1) * kTile > s.ctx) ? *(volatile unsigned long long*)&B->dirty[b] : 0ull;
+        if (dirty) {
+          // drafted tokens whose values are no numbers: to the rows that see them
+          for (int node = 0; node < p.P; ++node) {
+            if (!((dirty >> node) & 1)) continue;
+            const int tok = s.ctx + node, page = __ldg(table + tok / c.page);
+            if (page < 0 || page >= c.pages) continue;
+            const size_t row = ((size_t)page * c.Hkv + h) * c.page + tok % c.page;
+#pragma unroll
+            for (int k = 0; k < C::kHalves; ++k) {
+              const size_t at = row * D + k * 128 + ot;
+              float v;
+              if constexpr (kE4m3) v = from_e4m3x2(static_cast<const uint8_t*>(c.v)[at]).x * c.v_scale[row];
+              else v = bf16_to_f32(static_cast<const uint16_t*>(c.v)[at]);
+              if (!(fabsf(v) < INFINITY)) {
+#pragma unroll
+                for (int r = 0; r < kRows; ++r)
+                  if (r < rows && ((mask_s[r] >> node) & 1)) acc[k][r] += v;
+              }
+            }
+          }
+          sync_group(2);
+          if (ot == 0) B->dirty[b] = 0;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          arrive(&B->o_empty[ob]);
+          arrive(&B->st_empty[b]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) arrive(&B->q_empty[qb]);
+      ++seg;
+      // ---- the segment's result: whole, or a partial for the CTA that arrives last
+      bad = any_in_group(2, bad);
+      ok = !any_in_group(2, !ok);
+      if (!ok) continue;
+      if (bad && ot == 0) report(p.dev_err, GDN_DEVERR_SLOT);
+      auto write = [&](int r, int k, float o) {
+        const int rr = r0 + r, j = rr / p.G, g = rr - j * p.G;
+        const size_t at = (((size_t)s.n * p.P + j) * p.Hq + h * p.G + g) * D + k * 128 + ot;
+        if (p.gate) o = __fdividef(o, 1.f + __expf(-bf16_to_f32(p.gate[at])));
+        p.out[at] = f32_to_bf16(o);
+      };
+      if (s.t0 == 0 && s.t1 == s.tiles) {
+        if (bad) continue;
+        if (ot < used * 8) fin[ot] = l_run == 0.f ? 0.f : __fdividef(1.f, l_run);
+        sync_group(2);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+          if (r < rows) {
+#pragma unroll
+            for (int k = 0; k < C::kHalves; ++k) write(r, k, acc[k][r] * fin[r]);
+          }
+        continue;
+      }
+      float* mine = parts + (size_t)(2 * blockIdx.x + (s.t0 == 0 ? 1 : 0)) * a.slot_floats;
+      // [rows] maxima, [rows] sums, the flag, then [rows][D]
+      const int head = (2 * a.rows + 4) / 4 * 4;
+      if (ot < a.rows) {
+        mine[ot] = m_run;
+        mine[a.rows + ot] = l_run;
+      }
+      if (ot == 0) reinterpret_cast<int*>(mine)[2 * a.rows] = bad;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r)
+        if (r < rows) {
+#pragma unroll
+          for (int k = 0; k < C::kHalves; ++k) mine[head + r * D + k * 128 + ot] = acc[k][r];
+        }
+      const int grid = (int)min((long long)gridDim.x, plan.total);
+      const int c0 = cta_of(s.first, plan.total, grid), c1 = cta_of(s.first + s.tiles - 1, plan.total, grid);
+      __threadfence();
+      sync_group(2);
+      bool last = false;
+      if (ot == 0) {
+        last = atomicAdd(tickets + c0, 1) == c1 - c0;
+        if (last) tickets[c0] = 0;
+        __threadfence();
+      }
+      last = any_in_group(2, last);
+      if (!last) continue;
+      __threadfence();
+      auto part = [&](int cta) { return parts + (size_t)(2 * cta + (cta == c0 ? 1 : 0)) * a.slot_floats; };
+      bool any_bad = false;
+      if (ot < a.rows) {
+        float m = -INFINITY, l = 0.f;
+        for (int k = c0; k <= c1; ++k) m = fmaxf(m, __ldcg(part(k) + ot));
+        for (int k = c0; k <= c1; ++k) {
+          const float mk = __ldcg(part(k) + ot), lk = __ldcg(part(k) + a.rows + ot);
+          if (mk != -INFINITY || lk != 0.f) l += lk * ex2(mk - m);
+        }
+        fin[ot] = m;
+        fin[kRows + ot] = l == 0.f ? 0.f : __fdividef(1.f, l);
+      }
+      for (int k = c0 + ot; k <= c1; k += 128) any_bad |= __ldcg(reinterpret_cast<const int*>(part(k)) + 2 * a.rows) != 0;
+      if (any_in_group(2, any_bad)) continue;
+      for (int r = 0; r < rows; ++r) {
+        const float m = fin[r];
+        float o[C::kHalves];
+#pragma unroll
+        for (int k = 0; k < C::kHalves; ++k) o[k] = 0.f;
+#pragma unroll 4
+        for (int k = c0; k <= c1; ++k) {
+          const float* q = part(k);
+          const float mk = __ldcg(q + r), w = mk == -INFINITY ? 0.f : ex2(mk - m);
+#pragma unroll
+          for (int e = 0; e < C::kHalves; ++e) o[e] = fmaf(w, __ldcg(q + head + r * D + e * 128 + ot), o[e]);
+        }
+#pragma unroll
+        for (int k = 0; k < C::kHalves; ++k) write(r, k, o[k] * fin[kRows + r]);
+      }
+      sync_group(2);  // fin is read before the next segment's
+    }
+  }
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  if (warp == 9) umma::tmem_dealloc(tmem, 512);
+  if (tid == 0 && *(volatile int*)abort) report(p.dev_err, GDN_DEVERR_TIMEOUT);
+}
+
+template <int D, bool kE4m3, int kRows>
+cudaError_t launch_rows(const Args& a, const CUtensorMap& tmk, const CUtensorMap& tmv, int grid, cudaStream_t stream) {
+  using C = Cfg<D, kE4m3, kRows>;
+  const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(&kernel<D, kE4m3, kRows>), C::kSmem);
+  if (err != cudaSuccess) return err;
+  kernel<D, kE4m3, kRows><<<grid, kThreads, C::kSmem, stream>>>(a, tmk, tmv);
+  return cudaGetLastError();
+}
+
+template <bool kE4m3>
+cudaError_t launch_format(const Args& a, const CUtensorMap& tmk, const CUtensorMap& tmv, int grid, cudaStream_t stream) {
+  if (a.p.D == 256) {
+    if (a.rows <= 16) return launch_rows<256, kE4m3, 16>(a, tmk, tmv, grid, stream);
+    if (a.rows <= 32) return launch_rows<256, kE4m3, 32>(a, tmk, tmv, grid, stream);
+    return launch_rows<256, kE4m3, 64>(a, tmk, tmv, grid, stream);
+  }
+  if (a.rows <= 16) return launch_rows<128, kE4m3, 16>(a, tmk, tmv, grid, stream);
+  if (a.rows <= 32) return launch_rows<128, kE4m3, 32>(a, tmk, tmv, grid, stream);
+  return launch_rows<128, kE4m3, 64>(a, tmk, tmv, grid, stream);
+}
+
+cudaError_t launch_bf16(const Args& a, const CUtensorMap& tmk, const CUtensorMap& tmv, int grid, cudaStream_t stream);
+cudaError_t launch_e4m3(const Args& a, const CUtensorMap& tmk, const CUtensorMap& tmv, int grid, cudaStream_t stream);
+
+}  // namespace tree_attn
+}  // namespace gdn

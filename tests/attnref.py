@@ -114,6 +114,16 @@ def tree_attention(pool, q, table, ctx, scale, nodes, mask=None, gate=None):
         # a score is a fp32 sum of D products, scaled and taken to base 2; each weight and its sum once more
         ds = (reach.amax(-1) * (D + 8) * 2.0 ** -24 + (c + P + 16) * 2.0 ** -24)[..., None]
         lim = BF16 * o.abs() + (BF16 + 2 * ds) * mass
+        if pool.fmt == "e4m3":
+            # A weight times its value's scale is held as two E4M3 terms, 256 standing for the largest weight times
+            # the largest scale of its tile of 128 tokens: below 2^-6 a term's step is 2^-9, so what is left is off
+            # by up to 2^-10 of 256, 2^-18 of that product, whatever the weight itself.
+            sv = torch.nan_to_num(pool.v_scale[pages].double().transpose(0, 1).reshape(Hkv, -1)[:, :c + P], 0, 0, 0)
+            code = torch.nan_to_num(v / sv[..., None], 0, 0, 0).abs()
+            for t0 in range(0, c + P, 128):
+                t = slice(t0, t0 + 128)
+                top = p[..., t].amax(-1) * sv[:, t].amax(-1)[None, :, None]
+                lim = lim + 2.0 ** -18 * top[..., None] * code[:, t].sum(1)[None, :, None]
         o, lim = o.reshape(P, Hq, D), lim.reshape(P, Hq, D)
         if gate is not None:
             w = torch.sigmoid(gate[rows].double())
