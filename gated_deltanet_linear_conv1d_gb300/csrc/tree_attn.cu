@@ -16,7 +16,9 @@ void row_tiles(int P, int G, int* rows, int* tiles) {
   *tiles = (all + *rows - 1) / *rows;
 }
 
-int slot_floats(int rows, int D) { return ((2 * rows + 4) / 4 * 4 + rows * D + 63) / 64 * 64; }
+// One output group's partial: its rows' maxima and sums, a flag, and rows x 128 values (a group has half
+// of D, or at D = 128 at most half of the kernel's 16, 32 or 64 rows: never more than `rows`).
+int slot_floats(int rows) { return ((2 * rows + 4) / 4 * 4 + rows * 128 + 63) / 64 * 64; }
 
 // Rows of one token and kv head; a box is 128 bytes of `box` tokens, swizzled as the MMAs read it.
 bool encode(CUtensorMap* m, void* base, const KvArgs& c, int D, int box_rows) {
@@ -34,10 +36,10 @@ bool encode(CUtensorMap* m, void* base, const KvArgs& c, int D, int box_rows) {
 
 }  // namespace
 
-size_t tree_attn_workspace_bytes(int P, int G, int D) {
+size_t tree_attn_workspace_bytes(int P, int G) {
   int rows, tiles;
   row_tiles(P, G, &rows, &tiles);
-  return tree_attn::kTicketBytes + (size_t)2 * tree_attn::kMaxCtas * slot_floats(rows, D) * sizeof(float);
+  return tree_attn::kTicketBytes + (size_t)4 * tree_attn::kMaxCtas * slot_floats(rows) * sizeof(float);
 }
 
 cudaError_t launch_tree_attn(const TreeAttnArgs& p, const KvArgs& c, cudaStream_t stream) {
@@ -49,7 +51,7 @@ cudaError_t launch_tree_attn(const TreeAttnArgs& p, const KvArgs& c, cudaStream_
   a.p = p;
   a.c = c;
   row_tiles(p.P, p.G, &a.rows, &a.row_tiles);
-  a.slot_floats = slot_floats(a.rows, p.D);
+  a.slot_floats = slot_floats(a.rows);
   a.box = 16;
   while (a.box < tree_attn::kTile && c.page % (2 * a.box) == 0) a.box *= 2;
   CUtensorMap tmk{}, tmv{};

@@ -33,10 +33,12 @@
 // tile's product times e^(tile's maximum - running maximum). So the next tile's
 // scores never wait for the last one's.
 //
-// Roles (384 threads): warps 0-3 softmax (a thread per token), warps 4-7 output
-// (a thread per value of D, mod 128), warp 8 copies (TMA, 16 KB blocks of 128
-// tokens x 128 bytes into a ring), warp 9 the MMAs (one thread), warp 10 the
-// query rows, warp 11 the scales. Every wait is bounded: one that runs out sets
+// Roles (640 threads): two groups of four warps for the softmax (a thread per
+// token), which take turns at the tiles, or, from 33 rows on, half of a tile's
+// rows each; two groups of four warps for the output (a thread per value of D),
+// each with half of D, or of the rows at D = 128; a warp for the copies (TMA, 16
+// KB blocks of 128 tokens x 128 bytes into a ring), one for the MMAs, one for the
+// query rows, one for the scales. Every wait is bounded: one that runs out sets
 // GDN_DEVERR_TIMEOUT and the CTA leaves.
 //
 // What bounds it: the cache's bytes from HBM while the rows of a tile are few, the
@@ -50,12 +52,13 @@
 namespace gdn {
 namespace tree_attn {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
+constexpr int kOutWarp = 8, kCopyWarp = 16, kMmaWarp = 17, kQueryWarp = 18, kScaleWarp = 19;  // first warps of the roles
 constexpr int kTile = 128;               // tokens per tile
 constexpr uint32_t kBlock = 128 * 128;   // bytes of one ring block: 128 tokens x 128 bytes
 constexpr int kMaxCtas = 152;
 constexpr int kSmemLimit = 227 * 1024;
-constexpr int kTicketBytes = 1024;
+constexpr int kTicketBytes = 2048;
 constexpr int kScSlots = 4;              // tiles of scales in flight
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -65,7 +68,7 @@ struct Args {
   int rows;       // query rows per row tile (the last one may have fewer)
   int row_tiles;
   int box;        // tokens per TMA box: a power of two that divides the page, at most 128
-  int slot_floats;  // workspace floats per partial
+  int slot_floats;  // workspace floats per partial (of one output group)
 };
 
 template <int D, bool kE4m3, int kRows>
@@ -78,18 +81,23 @@ struct Cfg {
   // two, or the first scores of a segment would wait for the output of the last, which follows them
   static constexpr int kQBuf = 2;
   static constexpr int kQBytes = kCols * 128 * kBlk;
+  static constexpr bool kSplit = kRows == 64;               // the softmax groups share each tile's rows
+  static constexpr int kSoftRows = kSplit ? kRows / 2 : kRows;  // rows of a softmax thread
+  static constexpr int kSoftWarps = kSplit ? 8 : 4;         // softmax warps at one tile
+  static constexpr int kOutRows = D == 256 ? kRows : kRows / 2;  // rows of an output thread
   // shared memory behind the ring, by byte offsets from its end
   static constexpr int oP = 0;
   static constexpr int oQ = oP + 2 * (int)kBlock;
   static constexpr int oSc = oQ + kQBuf * kQBytes;                          // [kScSlots][2][128] fp32
-  static constexpr int oMax = oSc + (kE4m3 ? kScSlots * 2 * kTile * 4 : 0);  // [2][kRows + 1][4]
-  static constexpr int oSum = oMax + 2 * (kRows + 1) * 16;                  // [2][kRows][4]
-  static constexpr int oTile = oSum + 2 * kRows * 16;                       // [2][kRows + 4]: maxima, the V scale
-  static constexpr int oAb = oTile + 2 * (kRows + 4) * 4;                   // [2][kRows] float2
-  static constexpr int oMask = oAb + 2 * kRows * 8;                         // [kQBuf][kRows] uint64
+  static constexpr int oMax = oSc + (kE4m3 ? kScSlots * 2 * kTile * 4 : 0);  // [2][kRows + 2][4]
+  static constexpr int oSum = oMax + 2 * (kRows + 2) * 16;                  // [2][kRows][4]
+  static constexpr int oWarp = oSum + 2 * kRows * 16;                       // [8 warps][kSoftRows]
+  static constexpr int oTile = oWarp + 8 * kSoftRows * 4;                   // [2][kRows + 4]: maxima, the V scale
+  static constexpr int oAb = oTile + 2 * (kRows + 4) * 4;                   // [2 groups][2][2][kRows]
+  static constexpr int oMask = oAb + 8 * kRows * 4;                         // [kQBuf][kRows] uint64
   static constexpr int oQs = oMask + kQBuf * kRows * 8;                     // [kQBuf][kRows] fp32
-  static constexpr int oFin = oQs + kQBuf * kRows * 4;                      // [2][kRows] fp32
-  static constexpr int oBars = oFin + 2 * kRows * 4;
+  static constexpr int oFin = oQs + kQBuf * kRows * 4;                      // [2 groups][2][kRows] fp32
+  static constexpr int oBars = oFin + 4 * kRows * 4;
   static constexpr int kRest = oBars + 768;
   static constexpr int kFit = (kSmemLimit - kRest) / (int)kBlock;
   // an even number of blocks keeps the two bf16 blocks of a 128-wide half of V side by side
@@ -182,6 +190,13 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// One thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -216,7 +231,8 @@ __device__ __forceinline__ void two_terms(const float (&x)[8], uint2& first, uin
   for (int i = 0; i < 4; ++i) {
     a[i] = e4m3x2(x[2 * i], x[2 * i + 1]);
     const float2 f = from_e4m3x2(a[i]);
-    b[i] = e4m3x2(x[2 * i] - f.x, x[2 * i + 1] - f.y);
+    const float2 r = __fadd2_rn(make_float2(x[2 * i], x[2 * i + 1]), make_float2(-f.x, -f.y));
+    b[i] = e4m3x2(r.x, r.y);
   }
   first = make_uint2(a[0] | (a[1] << 16), a[2] | (a[3] << 16));
   rest = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
@@ -267,7 +283,7 @@ __device__ __forceinline__ int cta_of(long long tile, long long total, int grid)
 }
 
 template <int D, bool kE4m3, int kRows>
-__global__ void __launch_bounds__(kThreads, 1) kernel(const Args a, const __grid_constant__ CUtensorMap tmk,
+__global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, const __grid_constant__ CUtensorMap tmk,
                                                       const __grid_constant__ CUtensorMap tmv) {
   using C = Cfg<D, kE4m3, kRows>;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -299,20 +315,20 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const Args a, const __grid
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(&B->q_full[i], 32);
-        mbar_init(&B->q_empty[i], 9);
+        mbar_init(&B->q_empty[i], 17);
         mbar_init(&B->s_full[i], 1);
-        mbar_init(&B->s_empty[i], 4);
-        mbar_init(&B->p_full[i], 128);
+        mbar_init(&B->s_empty[i], C::kSoftWarps);
+        mbar_init(&B->p_full[i], C::kSoftWarps * 32);
         mbar_init(&B->p_empty[i], 1);
         mbar_init(&B->o_full[i], 1);
-        mbar_init(&B->o_empty[i], 4);
-        mbar_init(&B->st_full[i], 128);
-        mbar_init(&B->st_empty[i], 4);
+        mbar_init(&B->o_empty[i], 8);
+        mbar_init(&B->st_full[i], C::kSoftWarps * 32);
+        mbar_init(&B->st_empty[i], 8);
         B->dirty[i] = 0;
       }
       for (int i = 0; i < kScSlots; ++i) {
         mbar_init(&B->sc_full[i], 32);
-        mbar_init(&B->sc_empty[i], 4);
+        mbar_init(&B->sc_empty[i], C::kSoftWarps);
       }
       mbar_init(&B->drain, 1);
       B->abort = 0;
@@ -342,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const Args a, const __grid
         at += here;
       }
     }
-    if (warp == 9) umma::tmem_alloc(&B->tmem, 512);
+    if (warp == kMmaWarp) umma::tmem_alloc(&B->tmem, 512);
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
@@ -351,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const Args a, const __grid
   const uint32_t tmem = B->tmem;
   int* abort = &B->abort;
 
-  if (warp == 8) {
+  if (warp == kCopyWarp) {
     // ------------------------------------------------------------ copies
     // K of a tile, then V of the tile before it: the order in which the MMAs take them.
     const int boxes = kTile / a.box, total_rows = c.slots * c.Hkv;
@@ -397,86 +413,95 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const Args a, const __grid
       for (int back = 1; back <= C::kStages && pos - back >= 0; ++back)
         mbar_wait_bounded(&B->full[(pos - back) % C::kStages], ((pos - back) / C::kStages) & 1);
     }
-  } else if (warp == 9) {
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMAs
-    if (lane == 0) {
-      const int rp = kE4m3 ? (a.rows + 7) / 8 * 8 : (a.rows + 15) / 16 * 16;  // rows as columns of the MMAs
-      const int N = C::kTerms * rp;
-      constexpr uint32_t kKind = kE4m3 ? umma::kKindF8 : umma::kKindF16, kType = kE4m3 ? umma::kE4M3 : umma::kBF16;
-      const uint32_t id_s = umma::idesc(kType, false, false, kTile, N), id_o = umma::idesc(kType, true, true, kTile, N);
-      const uint32_t sQ = smem_u32(rest + C::oQ), sP = smem_u32(rest + C::oP);
-      int pos = 0, i = 0, seg = 0;
-      bool ok = true;
-      auto block = [&]() {  // the next ring block, once its copy has landed
-        const int st = pos % C::kStages;
-        ok = ok && wait(&B->full[st], (pos / C::kStages) & 1, abort);
-        ++pos;
-        return st;
-      };
-      auto product_o = [&](int j) {
-        const int b = j & 1, ob = j % C::kOBuf;
-        ok = ok && wait(&B->p_full[b], (j >> 1) & 1, abort) &&
-             wait(&B->o_empty[ob], ((j / C::kOBuf) & 1) ^ 1, abort);
-        if (!ok) return;
-        umma::fence_after_sync();
+    // The whole warp walks and waits, one elected thread issues: with `if (lane == 0)` instead an MMA took
+    // 73 cycles to issue on an idle SM, and about 200 next to the other warps; its work is 41 at 16 columns.
+    const int rp = kE4m3 ? (a.rows + 7) / 8 * 8 : (a.rows + 15) / 16 * 16;  // rows as columns of the MMAs
+    const int N = C::kTerms * rp;
+    constexpr uint32_t kKind = kE4m3 ? umma::kKindF8 : umma::kKindF16, kType = kE4m3 ? umma::kE4M3 : umma::kBF16;
+    const uint32_t id_s = umma::idesc(kType, false, false, kTile, N), id_o = umma::idesc(kType, true, true, kTile, N);
+    const uint32_t sQ = smem_u32(rest + C::oQ), sP = smem_u32(rest + C::oP);
+    int pos = 0, i = 0, seg = 0;
+    bool ok = true;
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+      ok = ok && wait(bar, parity, abort);
+      ok = __all_sync(0xffffffffu, ok);
+      return ok;
+    };
+    auto product_o = [&](int j) {
+      const int b = j & 1, ob = j % C::kOBuf;
+      if (!wait_all(&B->p_full[b], (j >> 1) & 1) || !wait_all(&B->o_empty[ob], ((j / C::kOBuf) & 1) ^ 1)) return;
 #pragma unroll
-        for (int h = 0; h < C::kHalves; ++h) {
-          const int st = block(), st2 = kE4m3 ? st : block();
-          if (!ok) return;
-          umma::fence_after_sync();
+      for (int h = 0; h < C::kHalves; ++h) {
+        const int st = pos % C::kStages, st2 = kE4m3 ? st : st + 1;  // two bf16 blocks are side by side
+        if (!wait_all(&B->full[st], (pos / C::kStages) & 1)) return;
+        if (!kE4m3 && !wait_all(&B->full[st2], (pos / C::kStages) & 1)) return;
+        pos += kE4m3 ? 1 : 2;
+        umma::fence_after_sync();
+        if (elect_one()) {
           const uint32_t d = tmem + 2 * C::kCols + (ob * C::kHalves + h) * C::kCols;
           constexpr int kSteps = kE4m3 ? 4 : 8, kStepBytes = kE4m3 ? 4096 : 2048;  // 32 or 16 tokens a step
+          const uint64_t va = desc_mn(ring + st * kBlock), pa = desc_mn(sP + b * kBlock);
 #pragma unroll
           for (int k = 0; k < kSteps; ++k)
-            umma::mma<kKind>(d, desc_mn(ring + st * kBlock + k * kStepBytes), desc_mn(sP + b * kBlock + k * kStepBytes),
-                             id_o, k > 0);
+            umma::mma<kKind>(d, va + k * (kStepBytes >> 4), pa + k * (kStepBytes >> 4), id_o, k > 0);
           umma::commit(&B->empty[st]);
           if (!kE4m3) umma::commit(&B->empty[st2]);
-        }
-        umma::commit(&B->p_empty[b]);
-        umma::commit(&B->o_full[ob]);
-      };
-      Walk walk(a, plan);
-      Seg s;
-      while (ok && walk.next(a, s)) {
-        const int qb = seg % C::kQBuf;
-        ok = wait(&B->q_full[qb], (seg / C::kQBuf) & 1, abort);
-        for (int t = s.t0; t < s.t1 && ok; ++t, ++i) {
-          const int b = i & 1;
-          ok = wait(&B->s_empty[b], ((i >> 1) & 1) ^ 1, abort);
-          if (!ok) break;
-          umma::fence_after_sync();
-          for (int kb = 0; kb < C::kBlk; ++kb) {
-            const int st = block();
-            if (!ok) break;
-            umma::fence_after_sync();
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma::mma<kKind>(tmem + b * C::kCols, umma::smem_desc_sw128(ring + st * kBlock + k * 32),
-                               umma::smem_desc_sw128(sQ + qb * C::kQBytes + kb * (C::kCols * 128) + k * 32), id_s,
-                               kb + k > 0);
-            umma::commit(&B->empty[st]);
+          if (h == C::kHalves - 1) {
+            umma::commit(&B->p_empty[b]);
+            umma::commit(&B->o_full[ob]);
           }
-          if (!ok) break;
-          umma::commit(&B->s_full[b]);
-          if (t + 1 == s.t1) umma::commit(&B->q_empty[qb]);
-          if (i > 0) product_o(i - 1);
         }
-        ++seg;
+        __syncwarp();
       }
-      if (ok && i > 0) product_o(i - 1);
-      umma::commit(&B->drain);  // nothing of the tensor core's is in flight when the CTA leaves
+    };
+    Walk walk(a, plan);
+    Seg s;
+    while (ok && walk.next(a, s)) {
+      const int qb = seg % C::kQBuf;
+      if (!wait_all(&B->q_full[qb], (seg / C::kQBuf) & 1)) break;
+      for (int t = s.t0; t < s.t1 && ok; ++t, ++i) {
+        const int b = i & 1;
+        if (!wait_all(&B->s_empty[b], ((i >> 1) & 1) ^ 1)) break;
+        for (int kb = 0; kb < C::kBlk; ++kb) {
+          const int st = pos % C::kStages;
+          if (!wait_all(&B->full[st], (pos / C::kStages) & 1)) break;
+          ++pos;
+          umma::fence_after_sync();
+          if (elect_one()) {
+            const uint64_t ka = umma::smem_desc_sw128(ring + st * kBlock);
+            const uint64_t qa = umma::smem_desc_sw128(sQ + qb * C::kQBytes + kb * (C::kCols * 128));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) umma::mma<kKind>(tmem + b * C::kCols, ka + 2 * k, qa + 2 * k, id_s, kb + k > 0);
+            umma::commit(&B->empty[st]);
+            if (kb == C::kBlk - 1) {
+              umma::commit(&B->s_full[b]);
+              if (t + 1 == s.t1) umma::commit(&B->q_empty[qb]);
+            }
+          }
+          __syncwarp();
+        }
+        if (ok && i > 0) product_o(i - 1);
+      }
+      ++seg;
+    }
+    if (ok && i > 0) product_o(i - 1);
+    if (elect_one()) {  // nothing of the tensor core's is in flight when the CTA leaves
+      umma::commit(&B->drain);
       mbar_wait_bounded(&B->drain, 0);
     }
     __syncwarp();
-  } else if (warp == 10) {
+  } else if (warp == kQueryWarp) {
     // ------------------------------------------------------------ query rows
     Walk walk(a, plan);
     Seg s;
     int seg = 0;
     bool ok = true;
     const int rp = kE4m3 ? (a.rows + 7) / 8 * 8 : (a.rows + 15) / 16 * 16;
-    const float to_log2 = p.scale * kLog2e;
+    // scores are maxima before they are scaled: a negative scale turns the query's sign, none leaves zeros
+    const uint32_t sign = p.scale < 0.f ? 0x80008000u : 0u, mask_q = p.scale == 0.f ? 0u : ~0u;
+    const float to_log2 = p.scale == 0.f ? 1.f : fabsf(p.scale) * kLog2e;
     while (ok && walk.next(a, s)) {
       const int qb = seg % C::kQBuf;
       ok = wait(&B->q_empty[qb], ((seg / C::kQBuf) & 1) ^ 1, abort);
@@ -501,6 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const Args a, const __grid
           raw[i] = make_uint4(0u, 0u, 0u, 0u);
           if (r < a.rows && j < p.P && lane < D / 8)
             raw[i] = *reinterpret_cast<const uint4*>(p.q + (((size_t)s.n * p.P + j) * p.Hq + h * p.G + g) * D + lane * 8);
+          raw[i] = make_uint4((raw[i].x ^ sign) & mask_q, (raw[i].y ^ sign) & mask_q, (raw[i].z ^ sign) & mask_q,
+                              (raw[i].w ^ sign) & mask_q);
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
@@ -509,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const Args a, const __grid
             // eight values are one 16-byte piece of block lane / 8
             if (lane < D / 8)
               *reinterpret_cast<uint4*>(q_s + (lane >> 3) * (C::kCols * 128) + swz(r, (lane & 7) * 16)) = raw[i];
-            if (lane == 0) qs_s[r] = to_log2;
+            if (lane == 0) qs_s[r] = fmaxf(to_log2, 1e-37f);
           } else {
             const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
             float x[8], most = 0.f;
@@ -535,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const Args a, const __grid
               *reinterpret_cast<uint2*>(blk + swz(rp + r, (lane & 15) * 8)) = second;
             }
             const float down = __uint_as_float((uint32_t)(127 - up) << 23);
-            if (lane == 0) qs_s[r] = ex == 128 ? __uint_as_float(0x7fffffffu) : to_log2 * down;
+            if (lane == 0) qs_s[r] = ex == 128 ? __uint_as_float(0x7fffffffu) : fmaxf(to_log2 * down, 1e-37f);
           }
         }
       }
@@ -543,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const Args a, const __grid
       arrive(&B->q_full[qb]);
       ++seg;
     }
-  } else if (warp == 11) {
+  } else if (warp == kScaleWarp) {
     // ------------------------------------------------------------ scales (E4M3)
     if constexpr (kE4m3) {
       Walk walk(a, plan);
@@ -578,13 +605,17 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const Args a, const __grid
         }
       }
     }
-  } else if (warp < 4) {
+  } else if (warp < kOutWarp) {
     // ------------------------------------------------------------ softmax: thread = token of the tile
+    const int wg = warp >> 2, w4 = warp & 3, tt = tid & 127;
     const int rp = kE4m3 ? (a.rows + 7) / 8 * 8 : (a.rows + 15) / 16 * 16;
-    const int used = (a.rows + 7) / 8;  // groups of eight rows
+    constexpr int kR = C::kSoftRows;
+    const int roff = C::kSplit ? wg * kR : 0;                            // this thread's first row
+    const int used = min(kR / 8, max(0, (a.rows - roff + 7) / 8));       // its groups of eight rows
     float* sums = reinterpret_cast<float*>(rest + C::oSum);
     float* maxima = reinterpret_cast<float*>(rest + C::oMax);
     float* tile_s = reinterpret_cast<float*>(rest + C::oTile);
+    float* warp_s = reinterpret_cast<float*>(rest + C::oWarp) + warp * kR;
     const float* scales = reinterpret_cast<const float*>(rest + C::oSc);
     Walk walk(a, plan);
     Seg s;
@@ -594,18 +625,19 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const Args a, const __grid
       const int qb = seg % C::kQBuf;
       ok = ok && wait(&B->q_full[qb], (seg / C::kQBuf) & 1, abort);
       ok = __all_sync(0xffffffffu, ok);
-      const float* qs_s = reinterpret_cast<const float*>(rest + C::oQs) + qb * kRows;
-      const uint64_t* mask_s = reinterpret_cast<const uint64_t*>(rest + C::oMask) + qb * kRows;
+      const float* qs_s = reinterpret_cast<const float*>(rest + C::oQs) + qb * kRows + roff;
+      const uint64_t* mask_s = reinterpret_cast<const uint64_t*>(rest + C::oMask) + qb * kRows + roff;
       for (int t = s.t0; t < s.t1; ++t, ++i) {
         const int b = i & 1, ph = (i >> 1) & 1;
-        const int tok = t * kTile + tid;
+        if (!C::kSplit && b != wg) continue;
+        const int tok = t * kTile + tt;
         float sk = 1.f, sv = 1.f;
         if constexpr (kE4m3) {
           const int slot = i % kScSlots;
           ok = ok && wait(&B->sc_full[slot], (i / kScSlots) & 1, abort);
           ok = __all_sync(0xffffffffu, ok);
-          sk = scales[slot * 2 * kTile + tid];
-          sv = scales[slot * 2 * kTile + kTile + tid];
+          sk = scales[slot * 2 * kTile + tt];
+          sv = scales[slot * 2 * kTile + kTile + tt];
           __syncwarp();
           if (lane == 0) arrive(&B->sc_empty[slot]);
           if (tok >= s.len) sv = 0.f;
@@ -613,27 +645,29 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const Args a, const __grid
         ok = ok && wait(&B->s_full[b], ph, abort);
         ok = __all_sync(0xffffffffu, ok);
         umma::fence_after_sync();
-        float x[kRows];
-        const uint32_t ts = umma::taddr(tmem, 32 * warp, b * C::kCols);
+        float2 x[kR / 2];  // scores, not yet taken times the row's scale
+        const uint32_t ts = umma::taddr(tmem, 32 * w4, b * C::kCols + roff);
 #pragma unroll
-        for (int g0 = 0; g0 < kRows / 8; g0 += 4) {  // up to 32 rows at a time
-          uint32_t u[4][8], w[kE4m3 ? 4 : 1][8];
+        for (int g0 = 0; g0 < kR / 8; g0 += 2) {  // sixteen rows at a time
+          uint32_t u[2][8], w[kE4m3 ? 2 : 1][8];
 #pragma unroll
-          for (int g = 0; g < 4 && g0 + g < kRows / 8; ++g)
+          for (int g = 0; g < 2; ++g)
             if (g0 + g < used) {
               ld8_nowait(ts + (g0 + g) * 8, u[g]);
               if constexpr (kE4m3) ld8_nowait(ts + rp + (g0 + g) * 8, w[g]);
             }
           umma::wait_ld();
 #pragma unroll
-          for (int g = 0; g < 4 && g0 + g < kRows / 8; ++g)
+          for (int g = 0; g < 2; ++g)
             if (g0 + g < used) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int r = (g0 + g) * 8 + e;
-                float v = __uint_as_float(u[g][e]);
-                if constexpr (kE4m3) v = (v + __uint_as_float(w[g][e])) * sk;
-                x[r] = v * qs_s[r];
+              for (int e = 0; e < 4; ++e) {
+                float2 v = make_float2(__uint_as_float(u[g][2 * e]), __uint_as_float(u[g][2 * e + 1]));
+                if constexpr (kE4m3) {
+                  v = __fadd2_rn(v, make_float2(__uint_as_float(w[g][2 * e]), __uint_as_float(w[g][2 * e + 1])));
+                  v = __fmul2_rn(v, make_float2(sk, sk));
+                }
+                x[(g0 + g) * 4 + e] = v;
               }
             }
         }
@@ -645,31 +679,42 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const Args a, const __grid
         ok = __all_sync(0xffffffffu, ok);
         if ((t + 1) * kTile > s.ctx) {  // drafted tokens, or tokens behind the last
           const int node = tok - s.ctx;
+          const bool cleans = !C::kSplit || wg == 0;
+          if (cleans) {
+            if (tt == 0) B->dirty[b] = 0;
+            sync_group(1 + wg);
+          }
 #pragma unroll
-          for (int g = 0; g < kRows / 8; ++g)
+          for (int g = 0; g < kR / 8; ++g)
             if (g < used) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int r = g * 8 + e;
-                const bool seen = node < 0 || (node < p.P && ((mask_s[r] >> (node & 63)) & 1));
-                x[r] = seen ? x[r] : -INFINITY;
+              for (int e = 0; e < 4; ++e) {
+                const int r = g * 8 + 2 * e;
+                const bool in = node < p.P;
+                float2& v = x[g * 4 + e];
+                v.x = node < 0 || (in && ((mask_s[r] >> (node & 63)) & 1)) ? v.x : -INFINITY;
+                v.y = node < 0 || (in && ((mask_s[r + 1] >> (node & 63)) & 1)) ? v.y : -INFINITY;
               }
             }
           // A weight of zero does not take a NaN or an infinity out of a product. Values behind the last
           // token become zeros; a drafted token's that are no numbers too, and the output warps add them
           // to the rows that see the token.
           if (node >= 0) {
-            const int n_tiles = plan.count;
-            const int first = C::kBlk * min(i + 2, n_tiles) + C::kBlk * i;  // V's place in the order of copies
+            const int first = C::kBlk * min(i + 2, plan.count) + C::kBlk * i;  // V's place in the order of copies
             bool odd = false;
-            if (ok) {
-              for (int vb = 0; vb < C::kBlk; ++vb) {
+            if (ok && cleans) {
+              // What stood in V's ring blocks before has been used (a barrier's parity tells a phase from
+              // the next, not from the one after): the products up to the next tile's scores are done, or
+              // without a next tile those up to the last tile's output.
+              if (i + 1 < plan.count) ok = wait(&B->s_full[b ^ 1], ((i + 1) >> 1) & 1, abort);
+              else if (i > 0) ok = wait(&B->p_empty[b ^ 1], ((i - 1) >> 1) & 1, abort);
+              for (int vb = 0; vb < C::kBlk && ok; ++vb) {
                 const int st = (first + vb) % C::kStages;
                 ok = ok && wait(&B->full[st], ((first + vb) / C::kStages) & 1, abort);
                 if (!ok) break;
-                uint4* row = reinterpret_cast<uint4*>(smem + st * kBlock + tid * 128);
+                uint4* row = reinterpret_cast<uint4*>(smem + st * kBlock + tt * 128);
                 for (int k = 0; k < 8; ++k) {
-                  uint4& at = row[k ^ (tid & 7)];  // eight neighbours, eight different banks
+                  uint4& at = row[k ^ (tt & 7)];  // eight neighbours, eight different banks
                   uint4 v = at;
                   uint32_t* w = reinterpret_cast<uint32_t*>(&v);
                   bool fix = false;
@@ -699,76 +744,92 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const Args a, const __grid
                 odd = true;
                 sv = 0.f;
               }
-              if (odd) atomicOr(&B->dirty[b], 1ull << node);
+              if (odd && cleans) atomicOr(&B->dirty[b], 1ull << node);
             }
           }
           ok = __all_sync(0xffffffffu, ok);
         }
-        // ---- the tile's maximum of each row
-        float keep[kRows / 32 > 0 ? kRows / 32 : 1];
+        // ---- the tile's maximum of each row: of the warp first (row r's in lane r), then of the four warps
+        float keep = -INFINITY;
 #pragma unroll
-        for (int g = 0; g < kRows / 8; ++g)
+        for (int g = 0; g < kR / 8; ++g)
           if (g < used) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const int r = g * 8 + e;
-              const float m = warp_max(x[r]);
-              if (lane == (r & 31)) keep[r >> 5] = m;
+              const float m = warp_max(e & 1 ? x[r / 2].y : x[r / 2].x);
+              if (lane == r) keep = m;
             }
           }
-        float* max_b = maxima + b * (kRows + 1) * 4;
-#pragma unroll
-        for (int k = 0; k < kRows; k += 32)
-          if (k + lane < used * 8) max_b[(k + lane) * 4 + warp] = keep[k >> 5];
+        float* max_b = maxima + (b * (kRows + 2) + roff) * 4;
+        float* max_v = maxima + (b * (kRows + 2) + kRows + wg) * 4;
+        if (lane < used * 8) max_b[lane * 4 + w4] = keep;
         if constexpr (kE4m3) {
           const float m = warp_max(fabsf(sv));
-          if (lane == 0) max_b[kRows * 4 + warp] = m;
+          if (lane == 0) max_v[w4] = m;
         }
-        sync_group(1);
+        sync_group(1 + wg);
+        if (lane < used * 8) {
+          const float4 m4 = *reinterpret_cast<const float4*>(max_b + lane * 4);
+          const float m = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+          const float scaled = m == -INFINITY ? m : m * qs_s[lane];
+          warp_s[lane] = m == -INFINITY ? 0.f : -scaled;
+          if (w4 == 0) tile_s[b * (kRows + 4) + roff + lane] = scaled;
+        }
         float f = 1.f;  // the weight's factor: the value's scale, the tile's largest at 256
         if constexpr (kE4m3) {
-          const float4 v4 = *reinterpret_cast<const float4*>(max_b + kRows * 4);
+          const float4 v4 = *reinterpret_cast<const float4*>(max_v);
           const float most = fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w));
           f = sv == 0.f ? 0.f : 256.f * __fdiv_rn(sv, most);
-          if (tid == 0) tile_s[b * (kRows + 4) + kRows] = most * (1.f / 256.f);
+          if (tt == 0 && roff == 0) tile_s[b * (kRows + 4) + kRows] = most * (1.f / 256.f);
         }
+        __syncwarp();
         ok = ok && wait(&B->p_empty[b], ph ^ 1, abort);
         ok = __all_sync(0xffffffffu, ok);
         unsigned char* prow = rest + C::oP + b * kBlock;
 #pragma unroll
-        for (int g = 0; g < kRows / 8; ++g)
+        for (int g = 0; g < kR / 8; ++g)
           if (g < used) {
             float w[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int r = g * 8 + e;
-              const float4 m4 = *reinterpret_cast<const float4*>(max_b + r * 4);
-              float m = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
-              if (tid == r) tile_s[b * (kRows + 4) + r] = m;
-              m = m == -INFINITY ? 0.f : m;
-              x[r] = ex2(x[r] - m);
-              w[e] = kE4m3 ? x[r] * f : x[r];
+            for (int e = 0; e < 8; e += 4) {
+              const float4 q4 = *reinterpret_cast<const float4*>(qs_s + g * 8 + e);
+              const float4 m4 = *reinterpret_cast<const float4*>(warp_s + g * 8 + e);
+              float2& lo = x[g * 4 + e / 2];
+              float2& hi = x[g * 4 + e / 2 + 1];
+              lo = __ffma2_rn(lo, make_float2(q4.x, q4.y), make_float2(m4.x, m4.y));
+              hi = __ffma2_rn(hi, make_float2(q4.z, q4.w), make_float2(m4.z, m4.w));
+              lo = make_float2(ex2(lo.x), ex2(lo.y));
+              hi = make_float2(ex2(hi.x), ex2(hi.y));
+              float2 wl = lo, wh = hi;
+              if constexpr (kE4m3) {
+                wl = __fmul2_rn(lo, make_float2(f, f));
+                wh = __fmul2_rn(hi, make_float2(f, f));
+              }
+              w[e] = wl.x; w[e + 1] = wl.y; w[e + 2] = wh.x; w[e + 3] = wh.y;
             }
             if constexpr (kE4m3) {
               uint2 first, second;
               two_terms(w, first, second);
-              *reinterpret_cast<uint2*>(prow + swz(tid, g * 8)) = first;
-              *reinterpret_cast<uint2*>(prow + swz(tid, rp + g * 8)) = second;
+              *reinterpret_cast<uint2*>(prow + swz(tt, roff + g * 8)) = first;
+              *reinterpret_cast<uint2*>(prow + swz(tt, rp + roff + g * 8)) = second;
             } else {
-              *reinterpret_cast<uint4*>(prow + swz(tid, g * 16)) = to_bf16x8(w);
+              *reinterpret_cast<uint4*>(prow + swz(tt, (roff + g * 8) * 2)) = to_bf16x8(w);
             }
           }
         umma::fence_proxy_async_smem();
         arrive(&B->p_full[b]);
         // ---- the warp's sums: eight rows at a time, halved over the lanes
 #pragma unroll
-        for (int g = 0; g < kRows / 8; ++g)
+        for (int g = 0; g < kR / 8; ++g)
           if (g < used) {
+            const float v8[8] = {x[g * 4].x, x[g * 4].y, x[g * 4 + 1].x, x[g * 4 + 1].y,
+                                 x[g * 4 + 2].x, x[g * 4 + 2].y, x[g * 4 + 3].x, x[g * 4 + 3].y};
             float v4[4], v2[2], v1;
             const bool h16 = lane & 16, h8 = lane & 8, h4 = lane & 4;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float give = h16 ? x[g * 8 + e] : x[g * 8 + e + 4], stay = h16 ? x[g * 8 + e + 4] : x[g * 8 + e];
+              const float give = h16 ? v8[e] : v8[e + 4], stay = h16 ? v8[e + 4] : v8[e];
               v4[e] = stay + __shfl_xor_sync(0xffffffffu, give, 16);
             }
 #pragma unroll
@@ -781,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const Args a, const __grid
             v1 += __shfl_xor_sync(0xffffffffu, v1, 2);
             v1 += __shfl_xor_sync(0xffffffffu, v1, 1);
             const int r = g * 8 + (h16 ? 4 : 0) + (h8 ? 2 : 0) + (h4 ? 1 : 0);
-            if ((lane & 3) == 0) sums[(b * kRows + r) * 4 + warp] = v1;
+            if ((lane & 3) == 0) sums[(b * kRows + roff + r) * 4 + w4] = v1;
           }
         arrive(&B->st_full[b]);
       }
@@ -790,26 +851,29 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const Args a, const __grid
       ++seg;
     }
   } else {
-    // ------------------------------------------------------------ output: thread = value of D, mod 128
+    // ------------------------------------------------------------ output: thread = value of D
+    const int og = (warp - kOutWarp) >> 2, ot = tid & 127, bar = 3 + og;
     const int rp = kE4m3 ? (a.rows + 7) / 8 * 8 : (a.rows + 15) / 16 * 16;
-    const int used = (a.rows + 7) / 8;
-    const int ot = tid - 128;
+    constexpr int kR = C::kOutRows;
+    const int half = D == 256 ? og : 0, dim = half * 128 + ot;           // this thread's value
+    const int roff = D == 256 ? 0 : og * kR;                             // its first row
+    const int used = min(kR / 8, max(0, (a.rows - roff + 7) / 8));       // its groups of eight rows
     const float* sums = reinterpret_cast<const float*>(rest + C::oSum);
     const float* tile_s = reinterpret_cast<const float*>(rest + C::oTile);
-    float2* ab = reinterpret_cast<float2*>(rest + C::oAb);
-    float* fin = reinterpret_cast<float*>(rest + C::oFin);
+    float* ab = reinterpret_cast<float*>(rest + C::oAb) + og * 4 * kRows;
+    float* fin = reinterpret_cast<float*>(rest + C::oFin) + og * 2 * kRows;
     float* parts = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kTicketBytes);
-    int* tickets = static_cast<int*>(p.workspace);
+    int* tickets = static_cast<int*>(p.workspace) + og * kMaxCtas;
     Walk walk(a, plan);
     Seg s;
     int i = 0, seg = 0;
     bool ok = true;
     while (walk.next(a, s)) {
       const int qb = seg % C::kQBuf;
-      const int h = s.u / a.row_tiles, r0 = (s.u % a.row_tiles) * a.rows;
-      const int rows = min(a.rows, p.P * p.G - r0);
+      const int h = s.u / a.row_tiles, r0 = (s.u % a.row_tiles) * a.rows + roff;
+      const int rows = max(0, min(min(kR, a.rows - roff), p.P * p.G - r0));  // of this thread, in this row tile
       const int32_t* table = p.table + (size_t)s.n * p.max_pages;
-      const uint64_t* mask_s = reinterpret_cast<const uint64_t*>(rest + C::oMask) + qb * kRows;
+      const uint64_t* mask_s = reinterpret_cast<const uint64_t*>(rest + C::oMask) + qb * kRows + roff;
       bool bad = false;  // pages out of the pool among this segment's
       {
         const int last = (min(s.len, s.t1 * kTile) - 1) / c.page;
@@ -819,46 +883,63 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const Args a, const __grid
         }
       }
       ok = ok && wait(&B->q_full[qb], (seg / C::kQBuf) & 1, abort);
-      float acc[C::kHalves][kRows];
+      float2 acc[kR / 2];
 #pragma unroll
-      for (int k = 0; k < C::kHalves; ++k)
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) acc[k][r] = 0.f;
-      float m_run = -INFINITY, l_run = 0.f;  // of row ot
+      for (int r = 0; r < kR / 2; ++r) acc[r] = make_float2(0.f, 0.f);
+      float m_run = -INFINITY, l_run = 0.f;  // of row ot of the row tile
       for (int t = s.t0; t < s.t1; ++t, ++i) {
         const int b = i & 1, ph = (i >> 1) & 1, ob = i % C::kOBuf;
         ok = ok && wait(&B->st_full[b], ph, abort);
-        if (ot < used * 8) {
+        float* keep_s = ab + b * 2 * kRows;
+        float* w_s = keep_s + kRows;
+        bool moved = false;  // a running maximum has changed
+        if (ot < a.rows) {
           const float mt = tile_s[b * (kRows + 4) + ot];
           const float4 l4 = *reinterpret_cast<const float4*>(sums + (b * kRows + ot) * 4);
           const float lt = (l4.x + l4.y) + (l4.z + l4.w);
           const float mn = fmaxf(m_run, mt);
           const float keep = m_run == -INFINITY ? 0.f : ex2(m_run - mn), w = mt == -INFINITY ? 0.f : ex2(mt - mn);
+          moved = keep != 1.f;
           l_run = l_run * keep + lt * w;
           m_run = mn;
-          ab[b * kRows + ot] = make_float2(keep, kE4m3 ? w * tile_s[b * (kRows + 4) + kRows] : w);
+          keep_s[ot] = keep;
+          w_s[ot] = kE4m3 ? w * tile_s[b * (kRows + 4) + kRows] : w;
         }
-        sync_group(2);
+        moved = any_in_group(bar, moved);
         ok = ok && wait(&B->o_full[ob], (i / C::kOBuf) & 1, abort);
         ok = __all_sync(0xffffffffu, ok);
         umma::fence_after_sync();
+        const uint32_t to = umma::taddr(tmem, 32 * (warp & 3), 2 * C::kCols + (ob * C::kHalves + half) * C::kCols + roff);
 #pragma unroll
-        for (int k = 0; k < C::kHalves; ++k) {
-          const uint32_t to = umma::taddr(tmem, 32 * (warp - 4), 2 * C::kCols + (ob * C::kHalves + k) * C::kCols);
+        for (int g0 = 0; g0 < kR / 8; g0 += 2) {  // sixteen rows at a time
+          uint32_t u[2][8], v[kE4m3 ? 2 : 1][8];
 #pragma unroll
-          for (int g = 0; g < kRows / 8; ++g)
-            if (g < used) {
-              uint32_t u[8], w[8];
-              ld8_nowait(to + g * 8, u);
-              if constexpr (kE4m3) ld8_nowait(to + rp + g * 8, w);
-              umma::wait_ld();
+          for (int g = 0; g < 2 && g0 + g < kR / 8; ++g)
+            if (g0 + g < used) {
+              ld8_nowait(to + (g0 + g) * 8, u[g]);
+              if constexpr (kE4m3) ld8_nowait(to + rp + (g0 + g) * 8, v[g]);
+            }
+          umma::wait_ld();
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int r = g * 8 + e;
-                const float2 f = ab[b * kRows + r];
-                float o = __uint_as_float(u[e]);
-                if constexpr (kE4m3) o += __uint_as_float(w[e]);
-                acc[k][r] = fmaf(o, f.y, acc[k][r] * f.x);
+          for (int g = 0; g < 2 && g0 + g < kR / 8; ++g)
+            if (g0 + g < used) {
+#pragma unroll
+              for (int e = 0; e < 8; e += 4) {
+                const int r = (g0 + g) * 8 + e;
+                const float4 w4 = *reinterpret_cast<const float4*>(w_s + roff + r);
+                float2 lo = make_float2(__uint_as_float(u[g][e]), __uint_as_float(u[g][e + 1]));
+                float2 hi = make_float2(__uint_as_float(u[g][e + 2]), __uint_as_float(u[g][e + 3]));
+                if constexpr (kE4m3) {
+                  lo = __fadd2_rn(lo, make_float2(__uint_as_float(v[g][e]), __uint_as_float(v[g][e + 1])));
+                  hi = __fadd2_rn(hi, make_float2(__uint_as_float(v[g][e + 2]), __uint_as_float(v[g][e + 3])));
+                }
+                if (moved) {
+                  const float4 k4 = *reinterpret_cast<const float4*>(keep_s + roff + r);
+                  acc[r / 2] = __fmul2_rn(acc[r / 2], make_float2(k4.x, k4.y));
+                  acc[r / 2 + 1] = __fmul2_rn(acc[r / 2 + 1], make_float2(k4.z, k4.w));
+                }
+                acc[r / 2] = __ffma2_rn(lo, make_float2(w4.x, w4.y), acc[r / 2]);
+                acc[r / 2 + 1] = __ffma2_rn(hi, make_float2(w4.z, w4.w), acc[r / 2 + 1]);
               }
             }
         }
@@ -871,21 +952,15 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const Args a, const __grid
             const int tok = s.ctx + node, page = __ldg(table + tok / c.page);
             if (page < 0 || page >= c.pages) continue;
             const size_t row = ((size_t)page * c.Hkv + h) * c.page + tok % c.page;
+            float v;
+            if constexpr (kE4m3) v = from_e4m3x2(static_cast<const uint8_t*>(c.v)[row * D + dim]).x * c.v_scale[row];
+            else v = bf16_to_f32(static_cast<const uint16_t*>(c.v)[row * D + dim]);
+            if (!(fabsf(v) < INFINITY)) {
 #pragma unroll
-            for (int k = 0; k < C::kHalves; ++k) {
-              const size_t at = row * D + k * 128 + ot;
-              float v;
-              if constexpr (kE4m3) v = from_e4m3x2(static_cast<const uint8_t*>(c.v)[at]).x * c.v_scale[row];
-              else v = bf16_to_f32(static_cast<const uint16_t*>(c.v)[at]);
-              if (!(fabsf(v) < INFINITY)) {
-#pragma unroll
-                for (int r = 0; r < kRows; ++r)
-                  if (r < rows && ((mask_s[r] >> node) & 1)) acc[k][r] += v;
-              }
+              for (int r = 0; r < kR; ++r)
+                if (r < rows && ((mask_s[r] >> node) & 1)) (r & 1 ? acc[r / 2].y : acc[r / 2].x) += v;
             }
           }
-          sync_group(2);
-          if (ot == 0) B->dirty[b] = 0;
         }
         __syncwarp();
         if (lane == 0) {
@@ -897,30 +972,28 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const Args a, const __grid
       if (lane == 0) arrive(&B->q_empty[qb]);
       ++seg;
       // ---- the segment's result: whole, or a partial for the CTA that arrives last
-      bad = any_in_group(2, bad);
-      ok = !any_in_group(2, !ok);
+      bad = any_in_group(bar, bad);
+      ok = !any_in_group(bar, !ok);
       if (!ok) continue;
       if (bad && ot == 0) report(p.dev_err, GDN_DEVERR_SLOT);
-      auto write = [&](int r, int k, float o) {
+      auto write = [&](int r, float o) {
         const int rr = r0 + r, j = rr / p.G, g = rr - j * p.G;
-        const size_t at = (((size_t)s.n * p.P + j) * p.Hq + h * p.G + g) * D + k * 128 + ot;
+        const size_t at = (((size_t)s.n * p.P + j) * p.Hq + h * p.G + g) * D + dim;
         if (p.gate) o = __fdividef(o, 1.f + __expf(-bf16_to_f32(p.gate[at])));
         p.out[at] = f32_to_bf16(o);
       };
       if (s.t0 == 0 && s.t1 == s.tiles) {
         if (bad) continue;
-        if (ot < used * 8) fin[ot] = l_run == 0.f ? 0.f : __fdividef(1.f, l_run);
-        sync_group(2);
+        if (ot < a.rows) fin[ot] = l_run == 0.f ? 0.f : __fdividef(1.f, l_run);
+        sync_group(bar);
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
-          if (r < rows) {
-#pragma unroll
-            for (int k = 0; k < C::kHalves; ++k) write(r, k, acc[k][r] * fin[r]);
-          }
+        for (int r = 0; r < kR; ++r)
+          if (r < rows) write(r, (r & 1 ? acc[r / 2].y : acc[r / 2].x) * fin[roff + r]);
         continue;
       }
-      float* mine = parts + (size_t)(2 * blockIdx.x + (s.t0 == 0 ? 1 : 0)) * a.slot_floats;
-      // [rows] maxima, [rows] sums, the flag, then [rows][D]
+      // a partial: [rows] maxima, [rows] sums, the flag, then this group's [rows][128] sums
+      auto part = [&](int cta, int first) { return parts + (size_t)((2 * cta + first) * 2 + og) * a.slot_floats; };
+      float* mine = part(blockIdx.x, s.t0 == 0);
       const int head = (2 * a.rows + 4) / 4 * 4;
       if (ot < a.rows) {
         mine[ot] = m_run;
@@ -928,69 +1001,62 @@ __global__ void __launch_bounds__(kThreads, 1) kernel(const Args a, const __grid
       }
       if (ot == 0) reinterpret_cast<int*>(mine)[2 * a.rows] = bad;
 #pragma unroll
-      for (int r = 0; r < kRows; ++r)
-        if (r < rows) {
-#pragma unroll
-          for (int k = 0; k < C::kHalves; ++k) mine[head + r * D + k * 128 + ot] = acc[k][r];
-        }
+      for (int r = 0; r < kR; ++r)
+        if (r < rows) mine[head + r * 128 + ot] = r & 1 ? acc[r / 2].y : acc[r / 2].x;
       const int grid = (int)min((long long)gridDim.x, plan.total);
       const int c0 = cta_of(s.first, plan.total, grid), c1 = cta_of(s.first + s.tiles - 1, plan.total, grid);
       __threadfence();
-      sync_group(2);
+      sync_group(bar);
       bool last = false;
       if (ot == 0) {
         last = atomicAdd(tickets + c0, 1) == c1 - c0;
         if (last) tickets[c0] = 0;
         __threadfence();
       }
-      last = any_in_group(2, last);
+      last = any_in_group(bar, last);
       if (!last) continue;
       __threadfence();
-      auto part = [&](int cta) { return parts + (size_t)(2 * cta + (cta == c0 ? 1 : 0)) * a.slot_floats; };
       bool any_bad = false;
       if (ot < a.rows) {
         float m = -INFINITY, l = 0.f;
-        for (int k = c0; k <= c1; ++k) m = fmaxf(m, __ldcg(part(k) + ot));
+        for (int k = c0; k <= c1; ++k) m = fmaxf(m, __ldcg(part(k, k == c0) + ot));
         for (int k = c0; k <= c1; ++k) {
-          const float mk = __ldcg(part(k) + ot), lk = __ldcg(part(k) + a.rows + ot);
+          const float mk = __ldcg(part(k, k == c0) + ot), lk = __ldcg(part(k, k == c0) + a.rows + ot);
           if (mk != -INFINITY || lk != 0.f) l += lk * ex2(mk - m);
         }
         fin[ot] = m;
         fin[kRows + ot] = l == 0.f ? 0.f : __fdividef(1.f, l);
       }
-      for (int k = c0 + ot; k <= c1; k += 128) any_bad |= __ldcg(reinterpret_cast<const int*>(part(k)) + 2 * a.rows) != 0;
-      if (any_in_group(2, any_bad)) continue;
+      for (int k = c0 + ot; k <= c1; k += 128)
+        any_bad |= __ldcg(reinterpret_cast<const int*>(part(k, k == c0)) + 2 * a.rows) != 0;
+      if (any_in_group(bar, any_bad)) continue;
       for (int r = 0; r < rows; ++r) {
-        const float m = fin[r];
-        float o[C::kHalves];
-#pragma unroll
-        for (int k = 0; k < C::kHalves; ++k) o[k] = 0.f;
+        const float m = fin[roff + r];
+        float o = 0.f;
 #pragma unroll 4
         for (int k = c0; k <= c1; ++k) {
-          const float* q = part(k);
-          const float mk = __ldcg(q + r), w = mk == -INFINITY ? 0.f : ex2(mk - m);
-#pragma unroll
-          for (int e = 0; e < C::kHalves; ++e) o[e] = fmaf(w, __ldcg(q + head + r * D + e * 128 + ot), o[e]);
+          const float* q = part(k, k == c0);
+          const float mk = __ldcg(q + roff + r), w = mk == -INFINITY ? 0.f : ex2(mk - m);
+          o = fmaf(w, __ldcg(q + head + r * 128 + ot), o);
         }
-#pragma unroll
-        for (int k = 0; k < C::kHalves; ++k) write(r, k, o[k] * fin[kRows + r]);
+        write(r, o * fin[kRows + roff + r]);
       }
-      sync_group(2);  // fin is read before the next segment's
+      sync_group(bar);  // fin is read before the next segment's
     }
   }
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
-  if (warp == 9) umma::tmem_dealloc(tmem, 512);
+  if (warp == kMmaWarp) umma::tmem_dealloc(tmem, 512);
   if (tid == 0 && *(volatile int*)abort) report(p.dev_err, GDN_DEVERR_TIMEOUT);
 }
 
 template <int D, bool kE4m3, int kRows>
 cudaError_t launch_rows(const Args& a, const CUtensorMap& tmk, const CUtensorMap& tmv, int grid, cudaStream_t stream) {
   using C = Cfg<D, kE4m3, kRows>;
-  const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(&kernel<D, kE4m3, kRows>), C::kSmem);
+  const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(&tree_attn_kernel<D, kE4m3, kRows>), C::kSmem);
   if (err != cudaSuccess) return err;
-  kernel<D, kE4m3, kRows><<<grid, kThreads, C::kSmem, stream>>>(a, tmk, tmv);
+  tree_attn_kernel<D, kE4m3, kRows><<<grid, kThreads, C::kSmem, stream>>>(a, tmk, tmv);
   return cudaGetLastError();
 }
 
