@@ -16,9 +16,9 @@ void row_tiles(int P, int G, int* rows, int* tiles) {
   *tiles = (all + *rows - 1) / *rows;
 }
 
-// One output group's partial: its rows' maxima and sums, a flag, and rows x 128 values (a group has half
-// of D, or at D = 128 at most half of the kernel's 16, 32 or 64 rows: never more than `rows`).
-int slot_floats(int rows) { return ((2 * rows + 4) / 4 * 4 + rows * 128 + 63) / 64 * 64; }
+// An output group's partial: its rows' maxima and sums, a flag, and rows x 128 values, or rows x 256 where
+// one group has both halves of D = 256 (up to 16 rows).
+int slot_floats(int rows) { return ((2 * rows + 4) / 4 * 4 + rows * (rows <= 16 ? 256 : 128) + 63) / 64 * 64; }
 
 // Rows of one token and kv head; a box is 128 bytes of `box` tokens, swizzled as the MMAs read it.
 bool encode(CUtensorMap* m, void* base, const KvArgs& c, int D, int box_rows) {

@@ -33,12 +33,12 @@
 // tile's product times e^(tile's maximum - running maximum). So the next tile's
 // scores never wait for the last one's.
 //
-// Roles (640 threads): two groups of four warps for the softmax (a thread per
-// token), which take turns at the tiles, or, from 33 rows on, half of a tile's
-// rows each; two groups of four warps for the output (a thread per value of D),
-// each with half of D, or of the rows at D = 128; a warp for the copies (TMA, 16
-// KB blocks of 128 tokens x 128 bytes into a ring), one for the MMAs, one for the
-// query rows, one for the scales. Every wait is bounded: one that runs out sets
+// Roles: two groups of four warps for the softmax (a thread per token), which
+// take turns at the tiles, or, from 33 rows on, half of a tile's rows each; one
+// group of four warps for the output (a thread per value of D, mod 128), from 17
+// rows on two with half of D each, or half of the rows at D = 128; a warp for the
+// copies (TMA, 16 KB blocks of 128 tokens x 128 bytes into a ring), one for the
+// MMAs, one for the query rows. Every wait is bounded: one that runs out sets
 // GDN_DEVERR_TIMEOUT and the CTA leaves.
 //
 // What bounds it: the cache's bytes from HBM while the rows of a tile are few, the
@@ -52,8 +52,6 @@
 namespace gdn {
 namespace tree_attn {
 
-constexpr int kThreads = 640;
-constexpr int kOutWarp = 8, kCopyWarp = 16, kMmaWarp = 17, kQueryWarp = 18, kScaleWarp = 19;  // first warps of the roles
 constexpr int kTile = 128;               // tokens per tile
 constexpr uint32_t kBlock = 128 * 128;   // bytes of one ring block: 128 tokens x 128 bytes
 constexpr int kMaxCtas = 152;
@@ -78,13 +76,20 @@ struct Cfg {
   static constexpr int kTerms = kE4m3 ? 2 : 1;
   static constexpr int kCols = kTerms * kRows;
   static constexpr int kOBuf = (2 + 2 * kHalves) * kCols <= 512 ? 2 : 1;
-  // two, or the first scores of a segment would wait for the output of the last, which follows them
-  static constexpr int kQBuf = 2;
   static constexpr int kQBytes = kCols * 128 * kBlk;
   static constexpr bool kSplit = kRows == 64;               // the softmax groups share each tile's rows
+  // Tiles whose scores are ahead of the output: when a softmax group ends a tile, its next one's scores are there.
+  static constexpr int kAhead = kSplit ? 1 : 2;
+  // query buffers: a tile's scores wait for no output that follows them, though every segment have one tile
+  static constexpr int kQBuf = kAhead + 1;
+  static constexpr int kOutGroups = kRows == 16 ? 1 : 2;    // at few rows a group's fixed work outweighs the rows'
+  static constexpr int kOutWarp = 8, kCopyWarp = kOutWarp + 4 * kOutGroups;  // first warps of the roles
+  static constexpr int kMmaWarp = kCopyWarp + 1, kQueryWarp = kCopyWarp + 2;
+  static constexpr int kThreads = 32 * (kCopyWarp + 3);
   static constexpr int kSoftRows = kSplit ? kRows / 2 : kRows;  // rows of a softmax thread
   static constexpr int kSoftWarps = kSplit ? 8 : 4;         // softmax warps at one tile
-  static constexpr int kOutRows = D == 256 ? kRows : kRows / 2;  // rows of an output thread
+  static constexpr int kOutHalves = kHalves / kOutGroups > 0 ? kHalves / kOutGroups : 1;  // values of an output thread
+  static constexpr int kOutRows = kHalves >= kOutGroups ? kRows : kRows / 2;               // and its rows
   // shared memory behind the ring, by byte offsets from its end
   static constexpr int oP = 0;
   static constexpr int oQ = oP + 2 * (int)kBlock;
@@ -115,13 +120,13 @@ struct Plan {
 
 struct Bars {
   uint64_t full[12], empty[12];
-  uint64_t q_full[2], q_empty[2], s_full[2], s_empty[2], p_full[2], p_empty[2], o_full[2], o_empty[2];
+  uint64_t q_full[3], q_empty[3], s_full[2], s_empty[2], p_full[2], p_empty[2], o_full[2], o_empty[2];
   uint64_t st_full[2], st_empty[2], sc_full[kScSlots], sc_empty[kScSlots], drain;
   uint32_t tmem;
   int abort;
   unsigned long long dirty[2];  // nodes of the tile whose values are no numbers
   Plan plan;
-  long long warp_total[kThreads / 32];
+  long long warp_total[20];
 };
 static_assert(sizeof(Bars) <= 768, "barrier area");
 
@@ -172,18 +177,27 @@ struct Walk {
   }
 };
 
-// Waits for a phase of the barrier, no longer than the time limit or until another role gave up.
+// Waits for a phase of the barrier, no longer than the time limit or until another role gave up. Whoever
+// gives up sets the flag, and all later waits of the CTA end at once: the softmax and output warps run
+// through their tiles without effect (a result is written only while the flag is clear), the copies and
+// the MMAs stop.
 static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int* abort) {
   const uint64_t t0 = globaltimer_ns();
-  for (uint32_t it = 1; it < kWaitMaxIters; ++it) {
+  for (uint32_t it = 0; it < kWaitMaxIters; ++it) {
+    if (*(volatile int*)abort) return false;
     if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 31u) == 0 && (*(volatile int*)abort || globaltimer_ns() - t0 > kWaitLimitNs)) break;
+    if ((it & 31u) == 31u && globaltimer_ns() - t0 > kWaitLimitNs) break;
   }
   *(volatile int*)abort = 1;
   return false;
 }
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort) {
   return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort);
+}
+// The same for a converged warp.
+__device__ __forceinline__ void wait_warp(uint64_t* bar, uint32_t parity, int* abort) {
+  wait(bar, parity, abort);
+  __syncwarp();
 }
 
 __device__ __forceinline__ void arrive(uint64_t* bar) {
@@ -283,9 +297,10 @@ __device__ __forceinline__ int cta_of(long long tile, long long total, int grid)
 }
 
 template <int D, bool kE4m3, int kRows>
-__global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, const __grid_constant__ CUtensorMap tmk,
+__global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_kernel(const Args a, const __grid_constant__ CUtensorMap tmk,
                                                       const __grid_constant__ CUtensorMap tmv) {
   using C = Cfg<D, kE4m3, kRows>;
+  constexpr int kThreads = C::kThreads;
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* rest = smem + C::kStages * kBlock;
   Bars* B = reinterpret_cast<Bars*>(rest + C::oBars);
@@ -313,21 +328,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
         mbar_init(&B->full[i], 1);
         mbar_init(&B->empty[i], 1);
       }
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < C::kQBuf; ++i) {
         mbar_init(&B->q_full[i], 32);
-        mbar_init(&B->q_empty[i], 17);
+        mbar_init(&B->q_empty[i], 1 + 8 + 4 * C::kOutGroups);
+      }
+      for (int i = 0; i < 2; ++i) {
         mbar_init(&B->s_full[i], 1);
         mbar_init(&B->s_empty[i], C::kSoftWarps);
         mbar_init(&B->p_full[i], C::kSoftWarps * 32);
         mbar_init(&B->p_empty[i], 1);
         mbar_init(&B->o_full[i], 1);
-        mbar_init(&B->o_empty[i], 8);
+        mbar_init(&B->o_empty[i], 4 * C::kOutGroups);
         mbar_init(&B->st_full[i], C::kSoftWarps * 32);
-        mbar_init(&B->st_empty[i], 8);
+        mbar_init(&B->st_empty[i], 4 * C::kOutGroups);
         B->dirty[i] = 0;
       }
       for (int i = 0; i < kScSlots; ++i) {
-        mbar_init(&B->sc_full[i], 32);
+        mbar_init(&B->sc_full[i], 1);
         mbar_init(&B->sc_empty[i], C::kSoftWarps);
       }
       mbar_init(&B->drain, 1);
@@ -358,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
         at += here;
       }
     }
-    if (warp == kMmaWarp) umma::tmem_alloc(&B->tmem, 512);
+    if (warp == C::kMmaWarp) umma::tmem_alloc(&B->tmem, 512);
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
@@ -367,27 +384,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
   const uint32_t tmem = B->tmem;
   int* abort = &B->abort;
 
-  if (warp == kCopyWarp) {
+  if (warp == C::kCopyWarp) {
     // ------------------------------------------------------------ copies
-    // K of a tile, then V of the tile before it: the order in which the MMAs take them.
+    // K of a tile (with the tile's scales), then V of the tile kAhead before it: the order in which the
+    // MMAs take them.
     const int boxes = kTile / a.box, total_rows = c.slots * c.Hkv;
-    int pos = 0;  // blocks issued
+    int st = 0, phase = 1, filled = 0, i = 0;
     bool ok = true;
     auto blocks = [&](const CUtensorMap* map, int row) {
-      for (int b = 0; b < C::kBlk && ok; ++b, ++pos) {
-        const int st = pos % C::kStages;
-        ok = wait(&B->empty[st], ((pos / C::kStages) & 1) ^ 1, abort);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+      for (int b = 0; b < C::kBlk; ++b) {
+        ok = __all_sync(0xffffffffu, ok && wait(&B->empty[st], phase, abort));
+        if (!ok) return;
         if (lane == 0) mbar_arrive_expect_tx(&B->full[st], kBlock);
         __syncwarp();
         if (lane < boxes)
           tma_load_2d(smem + st * kBlock + lane * a.box * 128, map, b * (kE4m3 ? 128 : 64), row, &B->full[st]);
+        if (++st == C::kStages) st = 0, phase ^= 1;
+        filled = min(filled + 1, C::kStages);
       }
     };
     Walk walk(a, plan);
     Seg s;
-    int held = -1, row_v = 0;  // the last tile's rows, its V still to come
+    int held[C::kAhead];  // rows of the last tiles, their V still to come
     while (ok && walk.next(a, s)) {
       const int h = s.u / a.row_tiles;
       const int32_t* table = p.table + (size_t)s.n * p.max_pages;
@@ -399,21 +417,42 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
         return (page * c.Hkv + h) * c.page + tok % c.page;
       };
       int row = row_of(s.t0);
-      for (int t = s.t0; t < s.t1 && ok; ++t) {
-        const int ahead = t + 1 < s.t1 ? row_of(t + 1) : 0;
+      for (int t = s.t0; t < s.t1 && ok; ++t, ++i) {
+        const int next = t + 1 < s.t1 ? row_of(t + 1) : 0;
+        if constexpr (kE4m3) {
+          const int slot = i % kScSlots;
+          ok = __all_sync(0xffffffffu, ok && wait(&B->sc_empty[slot], ((i / kScSlots) & 1) ^ 1, abort));
+          if (!ok) break;
+          const bool in = row < total_rows;
+          const uint32_t bytes = a.box * 4, all = 2 * bytes * __popc(__ballot_sync(0xffffffffu, in));
+          if (lane == 0) mbar_arrive_expect_tx(&B->sc_full[slot], all);
+          __syncwarp();
+          if (in) {
+            unsigned char* dst = rest + C::oSc + slot * 2 * kTile * 4 + lane * bytes;
+            bulk_g2s_plain(dst, c.k_scale + row, bytes, &B->sc_full[slot]);
+            bulk_g2s_plain(dst + kTile * 4, c.v_scale + row, bytes, &B->sc_full[slot]);
+          }
+        }
         blocks(&tmk, row);
-        if (held >= 0) blocks(&tmv, row_v);
-        held = t;
-        row_v = row;
-        row = ahead;
+        if (ok && i >= C::kAhead) blocks(&tmv, held[0]);
+        if constexpr (C::kAhead == 2) held[0] = held[1];
+        held[C::kAhead - 1] = row;
+        row = next;
       }
     }
-    if (ok && held >= 0) blocks(&tmv, row_v);
+    if constexpr (C::kAhead == 2)
+      if (ok && i > 1) blocks(&tmv, held[0]);
+    if (ok && i > 0) blocks(&tmv, held[C::kAhead - 1]);
     if (!ok) {  // copies in flight land before the CTA may leave
-      for (int back = 1; back <= C::kStages && pos - back >= 0; ++back)
-        mbar_wait_bounded(&B->full[(pos - back) % C::kStages], ((pos - back) / C::kStages) & 1);
+      for (int k = 0; k < filled; ++k) {
+        if (st == 0) phase ^= 1;
+        st = st == 0 ? C::kStages - 1 : st - 1;
+        mbar_wait_bounded(&B->full[st], phase ^ 1);
+      }
+      if constexpr (kE4m3)
+        for (int k = i < kScSlots ? 0 : i - kScSlots; k < i; ++k) mbar_wait_bounded(&B->sc_full[k % kScSlots], (k / kScSlots) & 1);
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == C::kMmaWarp) {
     // ------------------------------------------------------------ MMAs
     // The whole warp walks and waits, one elected thread issues: with `if (lane == 0)` instead an MMA took
     // 73 cycles to issue on an idle SM, and about 200 next to the other warps; its work is 41 at 16 columns.
@@ -422,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
     constexpr uint32_t kKind = kE4m3 ? umma::kKindF8 : umma::kKindF16, kType = kE4m3 ? umma::kE4M3 : umma::kBF16;
     const uint32_t id_s = umma::idesc(kType, false, false, kTile, N), id_o = umma::idesc(kType, true, true, kTile, N);
     const uint32_t sQ = smem_u32(rest + C::oQ), sP = smem_u32(rest + C::oP);
-    int pos = 0, i = 0, seg = 0;
+    int st = 0, phase = 0, i = 0, seg = 0;
     bool ok = true;
     auto wait_all = [&](uint64_t* bar, uint32_t parity) {
       ok = ok && wait(bar, parity, abort);
@@ -434,10 +473,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
       if (!wait_all(&B->p_full[b], (j >> 1) & 1) || !wait_all(&B->o_empty[ob], ((j / C::kOBuf) & 1) ^ 1)) return;
 #pragma unroll
       for (int h = 0; h < C::kHalves; ++h) {
-        const int st = pos % C::kStages, st2 = kE4m3 ? st : st + 1;  // two bf16 blocks are side by side
-        if (!wait_all(&B->full[st], (pos / C::kStages) & 1)) return;
-        if (!kE4m3 && !wait_all(&B->full[st2], (pos / C::kStages) & 1)) return;
-        pos += kE4m3 ? 1 : 2;
+        const int st2 = kE4m3 ? st : st + 1;  // two bf16 blocks are side by side
+        if (!wait_all(&B->full[st], phase)) return;
+        if (!kE4m3 && !wait_all(&B->full[st2], phase)) return;
         umma::fence_after_sync();
         if (elect_one()) {
           const uint32_t d = tmem + 2 * C::kCols + (ob * C::kHalves + h) * C::kCols;
@@ -454,6 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
           }
         }
         __syncwarp();
+        st = st2 + 1;
+        if (st == C::kStages) st = 0, phase ^= 1;
       }
     };
     Walk walk(a, plan);
@@ -465,9 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
         const int b = i & 1;
         if (!wait_all(&B->s_empty[b], ((i >> 1) & 1) ^ 1)) break;
         for (int kb = 0; kb < C::kBlk; ++kb) {
-          const int st = pos % C::kStages;
-          if (!wait_all(&B->full[st], (pos / C::kStages) & 1)) break;
-          ++pos;
+          if (!wait_all(&B->full[st], phase)) break;
           umma::fence_after_sync();
           if (elect_one()) {
             const uint64_t ka = umma::smem_desc_sw128(ring + st * kBlock);
@@ -481,18 +519,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
             }
           }
           __syncwarp();
+          if (++st == C::kStages) st = 0, phase ^= 1;
         }
-        if (ok && i > 0) product_o(i - 1);
+        if (ok && i >= C::kAhead) product_o(i - C::kAhead);
       }
       ++seg;
     }
-    if (ok && i > 0) product_o(i - 1);
+    for (int j = max(0, i - C::kAhead); j < i && ok; ++j) product_o(j);
     if (elect_one()) {  // nothing of the tensor core's is in flight when the CTA leaves
       umma::commit(&B->drain);
       mbar_wait_bounded(&B->drain, 0);
     }
     __syncwarp();
-  } else if (warp == kQueryWarp) {
+  } else if (warp == C::kQueryWarp) {
     // ------------------------------------------------------------ query rows
     Walk walk(a, plan);
     Seg s;
@@ -570,42 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
       arrive(&B->q_full[qb]);
       ++seg;
     }
-  } else if (warp == kScaleWarp) {
-    // ------------------------------------------------------------ scales (E4M3)
-    if constexpr (kE4m3) {
-      Walk walk(a, plan);
-      Seg s;
-      int i = 0;
-      bool ok = true;
-      while (ok && walk.next(a, s)) {
-        const int h = s.u / a.row_tiles;
-        const int32_t* table = p.table + (size_t)s.n * p.max_pages;
-        auto row_of = [&](int t) {  // four tokens a lane, all in one page
-          const int tok = t * kTile + lane * 4;
-          if (tok >= s.len) return -1;
-          const int page = __ldg(table + tok / c.page);
-          return page < 0 || page >= c.pages ? -1 : (page * c.Hkv + h) * c.page + tok % c.page;
-        };
-        int row = row_of(s.t0);
-        for (int t = s.t0; t < s.t1; ++t, ++i) {
-          const int slot = i % kScSlots;
-          float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f), v4 = k4;
-          if (row >= 0) {
-            k4 = __ldg(reinterpret_cast<const float4*>(c.k_scale + row));
-            v4 = __ldg(reinterpret_cast<const float4*>(c.v_scale + row));
-          }
-          row = t + 1 < s.t1 ? row_of(t + 1) : -1;
-          ok = wait(&B->sc_empty[slot], ((i / kScSlots) & 1) ^ 1, abort);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          float4* dst = reinterpret_cast<float4*>(rest + C::oSc) + slot * 2 * (kTile / 4);
-          dst[lane] = k4;
-          dst[kTile / 4 + lane] = v4;
-          arrive(&B->sc_full[slot]);
-        }
-      }
-    }
-  } else if (warp < kOutWarp) {
+  } else if (warp < C::kOutWarp) {
     // ------------------------------------------------------------ softmax: thread = token of the tile
     const int wg = warp >> 2, w4 = warp & 3, tt = tid & 127;
     const int rp = kE4m3 ? (a.rows + 7) / 8 * 8 : (a.rows + 15) / 16 * 16;
@@ -620,11 +624,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
     Walk walk(a, plan);
     Seg s;
     int i = 0, seg = 0;
-    bool ok = true;
     while (walk.next(a, s)) {
       const int qb = seg % C::kQBuf;
-      ok = ok && wait(&B->q_full[qb], (seg / C::kQBuf) & 1, abort);
-      ok = __all_sync(0xffffffffu, ok);
+      wait_warp(&B->q_full[qb], (seg / C::kQBuf) & 1, abort);
       const float* qs_s = reinterpret_cast<const float*>(rest + C::oQs) + qb * kRows + roff;
       const uint64_t* mask_s = reinterpret_cast<const uint64_t*>(rest + C::oMask) + qb * kRows + roff;
       for (int t = s.t0; t < s.t1; ++t, ++i) {
@@ -634,16 +636,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
         float sk = 1.f, sv = 1.f;
         if constexpr (kE4m3) {
           const int slot = i % kScSlots;
-          ok = ok && wait(&B->sc_full[slot], (i / kScSlots) & 1, abort);
-          ok = __all_sync(0xffffffffu, ok);
+          wait_warp(&B->sc_full[slot], (i / kScSlots) & 1, abort);
           sk = scales[slot * 2 * kTile + tt];
           sv = scales[slot * 2 * kTile + kTile + tt];
           __syncwarp();
           if (lane == 0) arrive(&B->sc_empty[slot]);
           if (tok >= s.len) sv = 0.f;
         }
-        ok = ok && wait(&B->s_full[b], ph, abort);
-        ok = __all_sync(0xffffffffu, ok);
+        wait_warp(&B->s_full[b], ph, abort);
         umma::fence_after_sync();
         float2 x[kR / 2];  // scores, not yet taken times the row's scale
         const uint32_t ts = umma::taddr(tmem, 32 * w4, b * C::kCols + roff);
@@ -675,8 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
         __syncwarp();
         if (lane == 0) arrive(&B->s_empty[b]);
         // the statistics of two tiles back have been read
-        ok = ok && wait(&B->st_empty[b], ph ^ 1, abort);
-        ok = __all_sync(0xffffffffu, ok);
+        wait_warp(C::kOBuf == 2 ? &B->o_empty[b] : &B->st_empty[b], ph ^ 1, abort);
         if ((t + 1) * kTile > s.ctx) {  // drafted tokens, or tokens behind the last
           const int node = tok - s.ctx;
           const bool cleans = !C::kSplit || wg == 0;
@@ -700,18 +699,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
           // token become zeros; a drafted token's that are no numbers too, and the output warps add them
           // to the rows that see the token.
           if (node >= 0) {
-            const int first = C::kBlk * min(i + 2, plan.count) + C::kBlk * i;  // V's place in the order of copies
+            // V's place in the order of copies
+            const int first = C::kBlk * min(i + 1 + C::kAhead, plan.count) + C::kBlk * i;
             bool odd = false;
-            if (ok && cleans) {
+            if (cleans) {
               // What stood in V's ring blocks before has been used (a barrier's parity tells a phase from
-              // the next, not from the one after): the products up to the next tile's scores are done, or
-              // without a next tile those up to the last tile's output.
-              if (i + 1 < plan.count) ok = wait(&B->s_full[b ^ 1], ((i + 1) >> 1) & 1, abort);
+              // the next, not from the one after): the products up to the scores kAhead tiles on are done,
+              // or without such a tile those up to the last tile's output.
+              const int on = i + C::kAhead;
+              bool ok = true;
+              if (on < plan.count) ok = wait(&B->s_full[on & 1], (on >> 1) & 1, abort);
               else if (i > 0) ok = wait(&B->p_empty[b ^ 1], ((i - 1) >> 1) & 1, abort);
               for (int vb = 0; vb < C::kBlk && ok; ++vb) {
                 const int st = (first + vb) % C::kStages;
-                ok = ok && wait(&B->full[st], ((first + vb) / C::kStages) & 1, abort);
-                if (!ok) break;
+                if (!wait(&B->full[st], ((first + vb) / C::kStages) & 1, abort)) break;
                 uint4* row = reinterpret_cast<uint4*>(smem + st * kBlock + tt * 128);
                 for (int k = 0; k < 8; ++k) {
                   uint4& at = row[k ^ (tt & 7)];  // eight neighbours, eight different banks
@@ -747,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
               if (odd && cleans) atomicOr(&B->dirty[b], 1ull << node);
             }
           }
-          ok = __all_sync(0xffffffffu, ok);
+          __syncwarp();
         }
         // ---- the tile's maximum of each row: of the warp first (row r's in lane r), then of the four warps
         float keep = -INFINITY;
@@ -784,8 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
           if (tt == 0 && roff == 0) tile_s[b * (kRows + 4) + kRows] = most * (1.f / 256.f);
         }
         __syncwarp();
-        ok = ok && wait(&B->p_empty[b], ph ^ 1, abort);
-        ok = __all_sync(0xffffffffu, ok);
+        wait_warp(&B->p_empty[b], ph ^ 1, abort);
         unsigned char* prow = rest + C::oP + b * kBlock;
 #pragma unroll
         for (int g = 0; g < kR / 8; ++g)
@@ -852,11 +852,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
     }
   } else {
     // ------------------------------------------------------------ output: thread = value of D
-    const int og = (warp - kOutWarp) >> 2, ot = tid & 127, bar = 3 + og;
+    const int og = (warp - C::kOutWarp) >> 2, ot = tid & 127, bar = 3 + og;
     const int rp = kE4m3 ? (a.rows + 7) / 8 * 8 : (a.rows + 15) / 16 * 16;
     constexpr int kR = C::kOutRows;
-    const int half = D == 256 ? og : 0, dim = half * 128 + ot;           // this thread's value
-    const int roff = D == 256 ? 0 : og * kR;                             // its first row
+    constexpr int kH = C::kOutHalves;
+    const int half = C::kHalves > kH ? og : 0, dim = half * 128 + ot;    // this thread's first value
+    const int roff = kR < kRows ? og * kR : 0;                           // its first row
     const int used = min(kR / 8, max(0, (a.rows - roff + 7) / 8));       // its groups of eight rows
     const float* sums = reinterpret_cast<const float*>(rest + C::oSum);
     const float* tile_s = reinterpret_cast<const float*>(rest + C::oTile);
@@ -867,7 +868,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
     Walk walk(a, plan);
     Seg s;
     int i = 0, seg = 0;
-    bool ok = true;
     while (walk.next(a, s)) {
       const int qb = seg % C::kQBuf;
       const int h = s.u / a.row_tiles, r0 = (s.u % a.row_tiles) * a.rows + roff;
@@ -882,14 +882,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
           bad |= page < 0 || page >= c.pages;
         }
       }
-      ok = ok && wait(&B->q_full[qb], (seg / C::kQBuf) & 1, abort);
-      float2 acc[kR / 2];
+      wait_warp(&B->q_full[qb], (seg / C::kQBuf) & 1, abort);
+      float2 acc[kH][kR / 2];
 #pragma unroll
-      for (int r = 0; r < kR / 2; ++r) acc[r] = make_float2(0.f, 0.f);
+      for (int k = 0; k < kH; ++k)
+#pragma unroll
+        for (int r = 0; r < kR / 2; ++r) acc[k][r] = make_float2(0.f, 0.f);
       float m_run = -INFINITY, l_run = 0.f;  // of row ot of the row tile
       for (int t = s.t0; t < s.t1; ++t, ++i) {
         const int b = i & 1, ph = (i >> 1) & 1, ob = i % C::kOBuf;
-        ok = ok && wait(&B->st_full[b], ph, abort);
+        wait_warp(&B->st_full[b], ph, abort);
         float* keep_s = ab + b * 2 * kRows;
         float* w_s = keep_s + kRows;
         bool moved = false;  // a running maximum has changed
@@ -906,40 +908,46 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
           w_s[ot] = kE4m3 ? w * tile_s[b * (kRows + 4) + kRows] : w;
         }
         moved = any_in_group(bar, moved);
-        ok = ok && wait(&B->o_full[ob], (i / C::kOBuf) & 1, abort);
-        ok = __all_sync(0xffffffffu, ok);
+        wait_warp(&B->o_full[ob], (i / C::kOBuf) & 1, abort);
         umma::fence_after_sync();
         const uint32_t to = umma::taddr(tmem, 32 * (warp & 3), 2 * C::kCols + (ob * C::kHalves + half) * C::kCols + roff);
+        // sixteen rows of one value at a time, or eight of both
+        constexpr int kStep = kH == 1 && kR >= 16 ? 2 : 1;
 #pragma unroll
-        for (int g0 = 0; g0 < kR / 8; g0 += 2) {  // sixteen rows at a time
-          uint32_t u[2][8], v[kE4m3 ? 2 : 1][8];
+        for (int g0 = 0; g0 < kR / 8; g0 += kStep) {
+          uint32_t u_all[kH][kStep][8], v_all[kH][kE4m3 ? kStep : 1][8];
 #pragma unroll
-          for (int g = 0; g < 2 && g0 + g < kR / 8; ++g)
+          for (int k = 0; k < kH; ++k)
+#pragma unroll
+          for (int g = 0; g < kStep; ++g)
             if (g0 + g < used) {
-              ld8_nowait(to + (g0 + g) * 8, u[g]);
-              if constexpr (kE4m3) ld8_nowait(to + rp + (g0 + g) * 8, v[g]);
+              ld8_nowait(to + k * C::kCols + (g0 + g) * 8, u_all[k][g]);
+              if constexpr (kE4m3) ld8_nowait(to + k * C::kCols + rp + (g0 + g) * 8, v_all[k][g]);
             }
           umma::wait_ld();
 #pragma unroll
-          for (int g = 0; g < 2 && g0 + g < kR / 8; ++g)
+          for (int k = 0; k < kH; ++k)
+#pragma unroll
+          for (int g = 0; g < kStep; ++g)
             if (g0 + g < used) {
+              const uint32_t(&u)[8] = u_all[k][g];
 #pragma unroll
               for (int e = 0; e < 8; e += 4) {
                 const int r = (g0 + g) * 8 + e;
                 const float4 w4 = *reinterpret_cast<const float4*>(w_s + roff + r);
-                float2 lo = make_float2(__uint_as_float(u[g][e]), __uint_as_float(u[g][e + 1]));
-                float2 hi = make_float2(__uint_as_float(u[g][e + 2]), __uint_as_float(u[g][e + 3]));
+                float2 lo = make_float2(__uint_as_float(u[e]), __uint_as_float(u[e + 1]));
+                float2 hi = make_float2(__uint_as_float(u[e + 2]), __uint_as_float(u[e + 3]));
                 if constexpr (kE4m3) {
-                  lo = __fadd2_rn(lo, make_float2(__uint_as_float(v[g][e]), __uint_as_float(v[g][e + 1])));
-                  hi = __fadd2_rn(hi, make_float2(__uint_as_float(v[g][e + 2]), __uint_as_float(v[g][e + 3])));
+                  lo = __fadd2_rn(lo, make_float2(__uint_as_float(v_all[k][g][e]), __uint_as_float(v_all[k][g][e + 1])));
+                  hi = __fadd2_rn(hi, make_float2(__uint_as_float(v_all[k][g][e + 2]), __uint_as_float(v_all[k][g][e + 3])));
                 }
                 if (moved) {
                   const float4 k4 = *reinterpret_cast<const float4*>(keep_s + roff + r);
-                  acc[r / 2] = __fmul2_rn(acc[r / 2], make_float2(k4.x, k4.y));
-                  acc[r / 2 + 1] = __fmul2_rn(acc[r / 2 + 1], make_float2(k4.z, k4.w));
+                  acc[k][r / 2] = __fmul2_rn(acc[k][r / 2], make_float2(k4.x, k4.y));
+                  acc[k][r / 2 + 1] = __fmul2_rn(acc[k][r / 2 + 1], make_float2(k4.z, k4.w));
                 }
-                acc[r / 2] = __ffma2_rn(lo, make_float2(w4.x, w4.y), acc[r / 2]);
-                acc[r / 2 + 1] = __ffma2_rn(hi, make_float2(w4.z, w4.w), acc[r / 2 + 1]);
+                acc[k][r / 2] = __ffma2_rn(lo, make_float2(w4.x, w4.y), acc[k][r / 2]);
+                acc[k][r / 2 + 1] = __ffma2_rn(hi, make_float2(w4.z, w4.w), acc[k][r / 2 + 1]);
               }
             }
         }
@@ -952,20 +960,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
             const int tok = s.ctx + node, page = __ldg(table + tok / c.page);
             if (page < 0 || page >= c.pages) continue;
             const size_t row = ((size_t)page * c.Hkv + h) * c.page + tok % c.page;
-            float v;
-            if constexpr (kE4m3) v = from_e4m3x2(static_cast<const uint8_t*>(c.v)[row * D + dim]).x * c.v_scale[row];
-            else v = bf16_to_f32(static_cast<const uint16_t*>(c.v)[row * D + dim]);
-            if (!(fabsf(v) < INFINITY)) {
 #pragma unroll
-              for (int r = 0; r < kR; ++r)
-                if (r < rows && ((mask_s[r] >> node) & 1)) (r & 1 ? acc[r / 2].y : acc[r / 2].x) += v;
+            for (int k = 0; k < kH; ++k) {
+              const size_t at = row * D + k * 128 + dim;
+              float v;
+              if constexpr (kE4m3) v = from_e4m3x2(static_cast<const uint8_t*>(c.v)[at]).x * c.v_scale[row];
+              else v = bf16_to_f32(static_cast<const uint16_t*>(c.v)[at]);
+              if (!(fabsf(v) < INFINITY)) {
+#pragma unroll
+                for (int r = 0; r < kR; ++r)
+                  if (r < rows && ((mask_s[r] >> node) & 1)) (r & 1 ? acc[k][r / 2].y : acc[k][r / 2].x) += v;
+              }
             }
           }
         }
         __syncwarp();
         if (lane == 0) {
           arrive(&B->o_empty[ob]);
-          arrive(&B->st_empty[b]);
+          if (C::kOBuf == 1) arrive(&B->st_empty[b]);
         }
       }
       __syncwarp();
@@ -973,12 +985,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
       ++seg;
       // ---- the segment's result: whole, or a partial for the CTA that arrives last
       bad = any_in_group(bar, bad);
-      ok = !any_in_group(bar, !ok);
-      if (!ok) continue;
+      if (any_in_group(bar, *(volatile int*)abort)) continue;
       if (bad && ot == 0) report(p.dev_err, GDN_DEVERR_SLOT);
-      auto write = [&](int r, float o) {
+      auto write = [&](int r, int k, float o) {
         const int rr = r0 + r, j = rr / p.G, g = rr - j * p.G;
-        const size_t at = (((size_t)s.n * p.P + j) * p.Hq + h * p.G + g) * D + dim;
+        const size_t at = (((size_t)s.n * p.P + j) * p.Hq + h * p.G + g) * D + k * 128 + dim;
         if (p.gate) o = __fdividef(o, 1.f + __expf(-bf16_to_f32(p.gate[at])));
         p.out[at] = f32_to_bf16(o);
       };
@@ -988,11 +999,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
         sync_group(bar);
 #pragma unroll
         for (int r = 0; r < kR; ++r)
-          if (r < rows) write(r, (r & 1 ? acc[r / 2].y : acc[r / 2].x) * fin[roff + r]);
+          if (r < rows) {
+#pragma unroll
+            for (int k = 0; k < kH; ++k) write(r, k, (r & 1 ? acc[k][r / 2].y : acc[k][r / 2].x) * fin[roff + r]);
+          }
         continue;
       }
-      // a partial: [rows] maxima, [rows] sums, the flag, then this group's [rows][128] sums
-      auto part = [&](int cta, int first) { return parts + (size_t)((2 * cta + first) * 2 + og) * a.slot_floats; };
+      // a partial: [rows] maxima, [rows] sums, the flag, then this group's [rows][kH][128] sums
+      auto part = [&](int cta, int first) { return parts + (size_t)((2 * cta + first) * C::kOutGroups + og) * a.slot_floats; };
       float* mine = part(blockIdx.x, s.t0 == 0);
       const int head = (2 * a.rows + 4) / 4 * 4;
       if (ot < a.rows) {
@@ -1002,7 +1016,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
       if (ot == 0) reinterpret_cast<int*>(mine)[2 * a.rows] = bad;
 #pragma unroll
       for (int r = 0; r < kR; ++r)
-        if (r < rows) mine[head + r * 128 + ot] = r & 1 ? acc[r / 2].y : acc[r / 2].x;
+        if (r < rows) {
+#pragma unroll
+          for (int k = 0; k < kH; ++k) mine[head + (r * kH + k) * 128 + ot] = r & 1 ? acc[k][r / 2].y : acc[k][r / 2].x;
+        }
       const int grid = (int)min((long long)gridDim.x, plan.total);
       const int c0 = cta_of(s.first, plan.total, grid), c1 = cta_of(s.first + s.tiles - 1, plan.total, grid);
       __threadfence();
@@ -1032,14 +1049,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
       if (any_in_group(bar, any_bad)) continue;
       for (int r = 0; r < rows; ++r) {
         const float m = fin[roff + r];
-        float o = 0.f;
+        float o[kH];
+#pragma unroll
+        for (int e = 0; e < kH; ++e) o[e] = 0.f;
 #pragma unroll 4
         for (int k = c0; k <= c1; ++k) {
           const float* q = part(k, k == c0);
           const float mk = __ldcg(q + roff + r), w = mk == -INFINITY ? 0.f : ex2(mk - m);
-          o = fmaf(w, __ldcg(q + head + r * 128 + ot), o);
+#pragma unroll
+          for (int e = 0; e < kH; ++e) o[e] = fmaf(w, __ldcg(q + head + (r * kH + e) * 128 + ot), o[e]);
         }
-        write(r, o * fin[kRows + roff + r]);
+#pragma unroll
+        for (int e = 0; e < kH; ++e) write(r, e, o[e] * fin[kRows + roff + r]);
       }
       sync_group(bar);  // fin is read before the next segment's
     }
@@ -1047,7 +1068,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const Args a, co
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
-  if (warp == kMmaWarp) umma::tmem_dealloc(tmem, 512);
+  if (warp == C::kMmaWarp) umma::tmem_dealloc(tmem, 512);
   if (tid == 0 && *(volatile int*)abort) report(p.dev_err, GDN_DEVERR_TIMEOUT);
 }
 
@@ -1056,7 +1077,7 @@ cudaError_t launch_rows(const Args& a, const CUtensorMap& tmk, const CUtensorMap
   using C = Cfg<D, kE4m3, kRows>;
   const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(&tree_attn_kernel<D, kE4m3, kRows>), C::kSmem);
   if (err != cudaSuccess) return err;
-  tree_attn_kernel<D, kE4m3, kRows><<<grid, kThreads, C::kSmem, stream>>>(a, tmk, tmv);
+  tree_attn_kernel<D, kE4m3, kRows><<<grid, C::kThreads, C::kSmem, stream>>>(a, tmk, tmv);
   return cudaGetLastError();
 }
 
