@@ -648,35 +648,39 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         float2 x[kR / 2];  // scores, not yet taken times the row's scale
         const uint32_t ts = umma::taddr(tmem, 32 * w4, b * C::kCols + roff);
 #pragma unroll
-        for (int g0 = 0; g0 < kR / 8; g0 += 2) {  // sixteen rows at a time
-          uint32_t u[2][8], w[kE4m3 ? 2 : 1][8];
+        for (int g = 0; g < kR / 8; ++g)
+          if (g < used) {
+            uint32_t u[8], w[8];
+            ld8_nowait(ts + g * 8, u);
+            if constexpr (kE4m3) ld8_nowait(ts + rp + g * 8, w);
+            umma::wait_ld();
 #pragma unroll
-          for (int g = 0; g < 2; ++g)
-            if (g0 + g < used) {
-              ld8_nowait(ts + (g0 + g) * 8, u[g]);
-              if constexpr (kE4m3) ld8_nowait(ts + rp + (g0 + g) * 8, w[g]);
-            }
-          umma::wait_ld();
-#pragma unroll
-          for (int g = 0; g < 2; ++g)
-            if (g0 + g < used) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float2 v = make_float2(__uint_as_float(u[g][2 * e]), __uint_as_float(u[g][2 * e + 1]));
-                if constexpr (kE4m3) {
-                  v = __fadd2_rn(v, make_float2(__uint_as_float(w[g][2 * e]), __uint_as_float(w[g][2 * e + 1])));
-                  v = __fmul2_rn(v, make_float2(sk, sk));
-                }
-                x[(g0 + g) * 4 + e] = v;
+            for (int e = 0; e < 4; ++e) {
+              float2 v = make_float2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]));
+              if constexpr (kE4m3) {
+                v = __fadd2_rn(v, make_float2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1])));
+                v = __fmul2_rn(v, make_float2(sk, sk));
               }
+              x[g * 4 + e] = v;
             }
-        }
+          }
         umma::fence_before_sync();
         __syncwarp();
         if (lane == 0) arrive(&B->s_empty[b]);
         // the statistics of two tiles back have been read
         wait_warp(C::kOBuf == 2 ? &B->o_empty[b] : &B->st_empty[b], ph ^ 1, abort);
         if ((t + 1) * kTile > s.ctx) {  // drafted tokens, or tokens behind the last
+          // four E4M3 or two bf16 values: those that are no numbers become zeros
+          auto mend = [](uint32_t& w) {
+            uint32_t odd = 0;
+#pragma unroll
+            for (int y = 0; y < 32; y += kE4m3 ? 8 : 16) {
+              const uint32_t m = (kE4m3 ? 0x7fu : 0x7f80u) << y, all = (kE4m3 ? 0xffu : 0xffffu) << y;
+              if ((w & m) == m) odd |= all;
+            }
+            w &= ~odd;
+            return odd != 0;
+          };
           const int node = tok - s.ctx;
           const bool cleans = !C::kSplit || wg == 0;
           if (cleans) {
@@ -696,57 +700,40 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
               }
             }
           // A weight of zero does not take a NaN or an infinity out of a product. Values behind the last
-          // token become zeros; a drafted token's that are no numbers too, and the output warps add them
-          // to the rows that see the token.
-          if (node >= 0) {
+          // token become zeros (as far as its box goes: behind it they are zeros already); a drafted token's
+          // that are no numbers too, and the output warps add them to the rows that see the token.
+          if (cleans) {
+            // What stood in V's ring blocks before has been used (a barrier's parity tells a phase from
+            // the next, not from the one after): the products up to the scores kAhead tiles on are done,
+            // or without such a tile those up to the last tile's output.
+            const int on = i + C::kAhead;
+            if (on < plan.count) wait(&B->s_full[on & 1], (on >> 1) & 1, abort);
+            else if (i > 0) wait(&B->p_empty[b ^ 1], ((i - 1) >> 1) & 1, abort);
             // V's place in the order of copies
             const int first = C::kBlk * min(i + 1 + C::kAhead, plan.count) + C::kBlk * i;
-            bool odd = false;
-            if (cleans) {
-              // What stood in V's ring blocks before has been used (a barrier's parity tells a phase from
-              // the next, not from the one after): the products up to the scores kAhead tiles on are done,
-              // or without such a tile those up to the last tile's output.
-              const int on = i + C::kAhead;
-              bool ok = true;
-              if (on < plan.count) ok = wait(&B->s_full[on & 1], (on >> 1) & 1, abort);
-              else if (i > 0) ok = wait(&B->p_empty[b ^ 1], ((i - 1) >> 1) & 1, abort);
-              for (int vb = 0; vb < C::kBlk && ok; ++vb) {
-                const int st = (first + vb) % C::kStages;
-                if (!wait(&B->full[st], ((first + vb) / C::kStages) & 1, abort)) break;
-                uint4* row = reinterpret_cast<uint4*>(smem + st * kBlock + tt * 128);
-                for (int k = 0; k < 8; ++k) {
-                  uint4& at = row[k ^ (tt & 7)];  // eight neighbours, eight different banks
-                  uint4 v = at;
-                  uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-                  bool fix = false;
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    if constexpr (kE4m3) {
-#pragma unroll
-                      for (int y = 0; y < 32; y += 8)
-                        if (((w[e] >> y) & 0x7f) == 0x7f) fix = true, w[e] &= ~(0xffu << y);
-                    } else {
-#pragma unroll
-                      for (int y = 0; y < 32; y += 16)
-                        if (((w[e] >> y) & 0x7f80) == 0x7f80) fix = true, w[e] &= ~(0xffffu << y);
-                    }
-                  }
-                  if (node >= p.P) {
-                    at = make_uint4(0u, 0u, 0u, 0u);
-                  } else if (fix) {
-                    odd = true;
-                    at = v;
-                  }
-                }
+            for (int vb = 0; vb < C::kBlk; ++vb)
+              wait(&B->full[(first + vb) % C::kStages], ((first + vb) / C::kStages) & 1, abort);
+            const int row0 = max(0, s.ctx - t * kTile), end = min(kTile, s.len - t * kTile);
+            const int row1 = (end + a.box - 1) / a.box * a.box;
+#pragma unroll 1
+            for (int k = row0 * (8 * C::kBlk) + tt; k < row1 * (8 * C::kBlk); k += 128) {
+              const int row = k / (8 * C::kBlk), piece = k % (8 * C::kBlk);
+              uint4* at = reinterpret_cast<uint4*>(smem + (first + (piece >> 3)) % C::kStages * kBlock + row * 128) + (piece & 7);
+              if (row >= end) {
+                *at = make_uint4(0u, 0u, 0u, 0u);
+                continue;
+              }
+              uint4 v = *at;
+              const bool fix = mend(v.x) | mend(v.y) | mend(v.z) | mend(v.w);
+              if (fix) {
+                *at = v;
+                atomicOr(&B->dirty[b], 1ull << (t * kTile + row - s.ctx));
               }
             }
-            if (node < p.P) {
-              if (kE4m3 && !(fabsf(sv) < INFINITY)) {
-                odd = true;
-                sv = 0.f;
-              }
-              if (odd && cleans) atomicOr(&B->dirty[b], 1ull << node);
-            }
+          }
+          if (kE4m3 && node >= 0 && node < p.P && !(fabsf(sv) < INFINITY)) {
+            sv = 0.f;
+            if (cleans) atomicOr(&B->dirty[b], 1ull << node);
           }
           __syncwarp();
         }
@@ -911,35 +898,28 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         wait_warp(&B->o_full[ob], (i / C::kOBuf) & 1, abort);
         umma::fence_after_sync();
         const uint32_t to = umma::taddr(tmem, 32 * (warp & 3), 2 * C::kCols + (ob * C::kHalves + half) * C::kCols + roff);
-        // sixteen rows of one value at a time, or eight of both
-        constexpr int kStep = kH == 1 && kR >= 16 ? 2 : 1;
 #pragma unroll
-        for (int g0 = 0; g0 < kR / 8; g0 += kStep) {
-          uint32_t u_all[kH][kStep][8], v_all[kH][kE4m3 ? kStep : 1][8];
+        for (int g = 0; g < kR / 8; ++g)
+          if (g < used) {
+            uint32_t u_all[kH][8], v_all[kH][8];
 #pragma unroll
-          for (int k = 0; k < kH; ++k)
-#pragma unroll
-          for (int g = 0; g < kStep; ++g)
-            if (g0 + g < used) {
-              ld8_nowait(to + k * C::kCols + (g0 + g) * 8, u_all[k][g]);
-              if constexpr (kE4m3) ld8_nowait(to + k * C::kCols + rp + (g0 + g) * 8, v_all[k][g]);
+            for (int k = 0; k < kH; ++k) {
+              ld8_nowait(to + k * C::kCols + g * 8, u_all[k]);
+              if constexpr (kE4m3) ld8_nowait(to + k * C::kCols + rp + g * 8, v_all[k]);
             }
-          umma::wait_ld();
+            umma::wait_ld();
 #pragma unroll
-          for (int k = 0; k < kH; ++k)
-#pragma unroll
-          for (int g = 0; g < kStep; ++g)
-            if (g0 + g < used) {
-              const uint32_t(&u)[8] = u_all[k][g];
+            for (int k = 0; k < kH; ++k) {
+              const uint32_t(&u)[8] = u_all[k];
 #pragma unroll
               for (int e = 0; e < 8; e += 4) {
-                const int r = (g0 + g) * 8 + e;
+                const int r = g * 8 + e;
                 const float4 w4 = *reinterpret_cast<const float4*>(w_s + roff + r);
                 float2 lo = make_float2(__uint_as_float(u[e]), __uint_as_float(u[e + 1]));
                 float2 hi = make_float2(__uint_as_float(u[e + 2]), __uint_as_float(u[e + 3]));
                 if constexpr (kE4m3) {
-                  lo = __fadd2_rn(lo, make_float2(__uint_as_float(v_all[k][g][e]), __uint_as_float(v_all[k][g][e + 1])));
-                  hi = __fadd2_rn(hi, make_float2(__uint_as_float(v_all[k][g][e + 2]), __uint_as_float(v_all[k][g][e + 3])));
+                  lo = __fadd2_rn(lo, make_float2(__uint_as_float(v_all[k][e]), __uint_as_float(v_all[k][e + 1])));
+                  hi = __fadd2_rn(hi, make_float2(__uint_as_float(v_all[k][e + 2]), __uint_as_float(v_all[k][e + 3])));
                 }
                 if (moved) {
                   const float4 k4 = *reinterpret_cast<const float4*>(keep_s + roff + r);
@@ -987,21 +967,27 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
       bad = any_in_group(bar, bad);
       if (any_in_group(bar, *(volatile int*)abort)) continue;
       if (bad && ot == 0) report(p.dev_err, GDN_DEVERR_SLOT);
-      auto write = [&](int r, int k, float o) {
-        const int rr = r0 + r, j = rr / p.G, g = rr - j * p.G;
-        const size_t at = (((size_t)s.n * p.P + j) * p.Hq + h * p.G + g) * D + k * 128 + dim;
+      // where a row's values go, row after row
+      const int j0 = r0 / p.G, g0 = r0 - j0 * p.G;
+      const size_t at0 = (((size_t)s.n * p.P + j0) * p.Hq + h * p.G + g0) * D + dim, wrap = (size_t)(p.Hq - p.G) * D;
+      auto finish = [&](float o, size_t at) {
         if (p.gate) o = __fdividef(o, 1.f + __expf(-bf16_to_f32(p.gate[at])));
-        p.out[at] = f32_to_bf16(o);
+        return o;
       };
       if (s.t0 == 0 && s.t1 == s.tiles) {
         if (bad) continue;
         if (ot < a.rows) fin[ot] = l_run == 0.f ? 0.f : __fdividef(1.f, l_run);
         sync_group(bar);
+        size_t at = at0;
+        int g = g0;
 #pragma unroll
         for (int r = 0; r < kR; ++r)
           if (r < rows) {
 #pragma unroll
-            for (int k = 0; k < kH; ++k) write(r, k, (r & 1 ? acc[k][r / 2].y : acc[k][r / 2].x) * fin[roff + r]);
+            for (int k = 0; k < kH; ++k)
+              p.out[at + k * 128] = f32_to_bf16(finish((r & 1 ? acc[k][r / 2].y : acc[k][r / 2].x) * fin[roff + r], at + k * 128));
+            at += D;
+            if (++g == p.G) g = 0, at += wrap;
           }
         continue;
       }
@@ -1047,20 +1033,60 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
       for (int k = c0 + ot; k <= c1; k += 128)
         any_bad |= __ldcg(reinterpret_cast<const int*>(part(k, k == c0)) + 2 * a.rows) != 0;
       if (any_in_group(bar, any_bad)) continue;
-      for (int r = 0; r < rows; ++r) {
-        const float m = fin[roff + r];
-        float o[kH];
+      // Eight lanes take 32 of the warp's values, four a lane, and every fourth partial: few round trips to L2.
+      const int piece = lane >> 3, col = (warp & 3) * 32 + (lane & 7) * 4;
+      const size_t at1 = at0 - ot + col;
+      constexpr int kTake = 4 / kH;  // rows at a time
+#pragma unroll 1
+      for (int r = 0; r < rows; r += kTake) {
+        float o[kTake][kH][4];
 #pragma unroll
-        for (int e = 0; e < kH; ++e) o[e] = 0.f;
-#pragma unroll 4
-        for (int k = c0; k <= c1; ++k) {
+        for (int y = 0; y < kTake; ++y)
+#pragma unroll
+          for (int e = 0; e < kH * 4; ++e) o[y][e / 4][e % 4] = 0.f;
+#pragma unroll 2
+        for (int k = c0 + piece; k <= c1; k += 4) {
           const float* q = part(k, k == c0);
-          const float mk = __ldcg(q + roff + r), w = mk == -INFINITY ? 0.f : ex2(mk - m);
 #pragma unroll
-          for (int e = 0; e < kH; ++e) o[e] = fmaf(w, __ldcg(q + head + (r * kH + e) * 128 + ot), o[e]);
+          for (int y = 0; y < kTake; ++y) {
+            const int ry = min(r + y, rows - 1);
+            const float mk = __ldcg(q + roff + ry);
+#pragma unroll
+            for (int e = 0; e < kH; ++e) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(q + head + (ry * kH + e) * 128 + col));
+              const float w = mk == -INFINITY ? 0.f : ex2(mk - fin[roff + ry]);
+              o[y][e][0] = fmaf(w, v.x, o[y][e][0]);
+              o[y][e][1] = fmaf(w, v.y, o[y][e][1]);
+              o[y][e][2] = fmaf(w, v.z, o[y][e][2]);
+              o[y][e][3] = fmaf(w, v.w, o[y][e][3]);
+            }
+          }
         }
+        __syncwarp();
 #pragma unroll
-        for (int e = 0; e < kH; ++e) write(r, e, o[e] * fin[kRows + roff + r]);
+        for (int y = 0; y < kTake; ++y) {
+          const int ry = r + y, step = g0 + ry, j = step / p.G;
+          const size_t at = at1 + (size_t)ry * D + (size_t)j * wrap;
+#pragma unroll
+          for (int e = 0; e < kH; ++e) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              o[y][e][x] += __shfl_xor_sync(0xffffffffu, o[y][e][x], 8);
+              o[y][e][x] += __shfl_xor_sync(0xffffffffu, o[y][e][x], 16);
+            }
+            if (piece == (y * kH + e) % 4 && ry < rows) {
+              const float f = fin[kRows + roff + ry];
+              uint32_t w[2];
+#pragma unroll
+              for (int x = 0; x < 4; x += 2) {
+                const size_t to = at + e * 128 + x;
+                w[x / 2] = (uint32_t)f32_to_bf16(finish(o[y][e][x] * f, to)) |
+                           ((uint32_t)f32_to_bf16(finish(o[y][e][x + 1] * f, to + 1)) << 16);
+              }
+              *reinterpret_cast<uint2*>(p.out + at + e * 128) = make_uint2(w[0], w[1]);
+            }
+          }
+        }
       }
       sync_group(bar);  // fin is read before the next segment's
     }
