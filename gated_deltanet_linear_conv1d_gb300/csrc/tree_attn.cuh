@@ -38,7 +38,8 @@
 // group of four warps for the output (a thread per value of D, mod 128), from 17
 // rows on two with half of D each, or half of the rows at D = 128; a warp for the
 // copies (TMA, 16 KB blocks of 128 tokens x 128 bytes into a ring), one for the
-// MMAs, one for the query rows. Every wait is bounded: one that runs out sets
+// MMAs, one for the query rows, one that checks pages and clears values behind the
+// last token. Every wait is bounded: one that runs out sets
 // GDN_DEVERR_TIMEOUT and the CTA leaves.
 //
 // What bounds it: the cache's bytes from HBM while the rows of a tile are few, the
@@ -58,6 +59,9 @@ constexpr int kMaxCtas = 152;
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kTicketBytes = 2048;
 constexpr int kScSlots = 4;              // tiles of scales in flight
+// A barrier's parity tells a phase from the next one only. So there are more of them than their writer can be
+// ahead of their reader: the ring (at most 11 blocks) holds K or V of fewer than 8 tiles.
+constexpr int kSlots = 8, kMarks = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Args {
@@ -84,8 +88,8 @@ struct Cfg {
   static constexpr int kQBuf = kAhead + 1;
   static constexpr int kOutGroups = kRows == 16 ? 1 : 2;    // at few rows a group's fixed work outweighs the rows'
   static constexpr int kOutWarp = 8, kCopyWarp = kOutWarp + 4 * kOutGroups;  // first warps of the roles
-  static constexpr int kMmaWarp = kCopyWarp + 1, kQueryWarp = kCopyWarp + 2;
-  static constexpr int kThreads = 32 * (kCopyWarp + 3);
+  static constexpr int kMmaWarp = kCopyWarp + 1, kQueryWarp = kCopyWarp + 2, kCheckWarp = kCopyWarp + 3;
+  static constexpr int kThreads = 32 * (kCopyWarp + 4);
   static constexpr int kSoftRows = kSplit ? kRows / 2 : kRows;  // rows of a softmax thread
   static constexpr int kSoftWarps = kSplit ? 8 : 4;         // softmax warps at one tile
   static constexpr int kOutHalves = kHalves / kOutGroups > 0 ? kHalves / kOutGroups : 1;  // values of an output thread
@@ -103,7 +107,7 @@ struct Cfg {
   static constexpr int oQs = oMask + kQBuf * kRows * 8;                     // [kQBuf][kRows] fp32
   static constexpr int oFin = oQs + kQBuf * kRows * 4;                      // [2 groups][2][kRows] fp32
   static constexpr int oBars = oFin + 4 * kRows * 4;
-  static constexpr int kRest = oBars + 768;
+  static constexpr int kRest = oBars + 1408;
   static constexpr int kFit = (kSmemLimit - kRest) / (int)kBlock;
   // an even number of blocks keeps the two bf16 blocks of a 128-wide half of V side by side
   static constexpr int kStages = kE4m3 ? kFit : kFit / 2 * 2;
@@ -119,16 +123,21 @@ struct Plan {
 };
 
 struct Bars {
-  uint64_t full[12], empty[12];
+  uint64_t empty[12];                     // by ring block
+  uint64_t k_full[kSlots], v_full[kSlots];  // by tile
+  uint64_t v_issued[kMarks];              // by last tile (one with drafted tokens) of the piece: V's copies run
+  uint64_t v_clean[kMarks];               // and V is ready for the MMAs
+  uint64_t checked[kMarks];               // by segment
   uint64_t q_full[3], q_empty[3], s_full[2], s_empty[2], p_full[2], p_empty[2], o_full[2], o_empty[2];
   uint64_t st_full[2], st_empty[2], sc_full[kScSlots], sc_empty[kScSlots], drain;
   uint32_t tmem;
   int abort;
-  unsigned long long dirty[2];  // nodes of the tile whose values are no numbers
+  int bad[kMarks];                        // the segment has a page out of the pool
+  unsigned long long dirty[kMarks];       // nodes whose values in the last tile are no numbers
   Plan plan;
   long long warp_total[20];
 };
-static_assert(sizeof(Bars) <= 768, "barrier area");
+static_assert(sizeof(Bars) <= 1408, "barrier area");
 
 // The piece's segments: runs of tiles of one (request n, unit u = head x row tiles + row tile).
 struct Seg {
@@ -324,9 +333,15 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
     }
     if (lane == 31) B->warp_total[warp] = upto;
     if (tid == 0) {
-      for (int i = 0; i < C::kStages; ++i) {
-        mbar_init(&B->full[i], 1);
-        mbar_init(&B->empty[i], 1);
+      for (int i = 0; i < C::kStages; ++i) mbar_init(&B->empty[i], 1);
+      for (int i = 0; i < kSlots; ++i) {
+        mbar_init(&B->k_full[i], 1);
+        mbar_init(&B->v_full[i], 1);
+      }
+      for (int i = 0; i < kMarks; ++i) {
+        mbar_init(&B->v_issued[i], 1);
+        mbar_init(&B->v_clean[i], 32);
+        mbar_init(&B->checked[i], 1);
       }
       for (int i = 0; i < C::kQBuf; ++i) {
         mbar_init(&B->q_full[i], 32);
@@ -341,7 +356,6 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         mbar_init(&B->o_empty[i], 4 * C::kOutGroups);
         mbar_init(&B->st_full[i], C::kSoftWarps * 32);
         mbar_init(&B->st_empty[i], 4 * C::kOutGroups);
-        B->dirty[i] = 0;
       }
       for (int i = 0; i < kScSlots; ++i) {
         mbar_init(&B->sc_full[i], 1);
@@ -389,23 +403,30 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
     // K of a tile (with the tile's scales), then V of the tile kAhead before it: the order in which the
     // MMAs take them.
     const int boxes = kTile / a.box, total_rows = c.slots * c.Hkv;
-    int st = 0, phase = 1, filled = 0, i = 0;
+    int st = 0, phase = 1, i = 0;
     bool ok = true;
-    auto blocks = [&](const CUtensorMap* map, int row) {
+    auto blocks = [&](const CUtensorMap* map, int row, uint64_t* full) {
+      if (lane == 0) mbar_arrive_expect_tx(full, C::kBlk * kBlock);
+      __syncwarp();
       for (int b = 0; b < C::kBlk; ++b) {
         ok = __all_sync(0xffffffffu, ok && wait(&B->empty[st], phase, abort));
-        if (!ok) return;
-        if (lane == 0) mbar_arrive_expect_tx(&B->full[st], kBlock);
-        __syncwarp();
-        if (lane < boxes)
-          tma_load_2d(smem + st * kBlock + lane * a.box * 128, map, b * (kE4m3 ? 128 : 64), row, &B->full[st]);
+        if (ok && lane < boxes)
+          tma_load_2d(smem + st * kBlock + lane * a.box * 128, map, b * (kE4m3 ? 128 : 64), row, full);
         if (++st == C::kStages) st = 0, phase ^= 1;
-        filled = min(filled + 1, C::kStages);
       }
     };
     Walk walk(a, plan);
     Seg s;
     int held[C::kAhead];  // rows of the last tiles, their V still to come
+    int marks = 0;
+    uint32_t last_tiles = 0;  // bit i % 32: tile i has drafted tokens
+    auto value_blocks = [&](int j, int row) {
+      blocks(&tmv, row, &B->v_full[j % kSlots]);
+      if ((last_tiles >> (j & 31)) & 1) {
+        if (lane == 0) arrive(&B->v_issued[marks % kMarks]);
+        ++marks;
+      }
+    };
     while (ok && walk.next(a, s)) {
       const int h = s.u / a.row_tiles;
       const int32_t* table = p.table + (size_t)s.n * p.max_pages;
@@ -433,24 +454,26 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
             bulk_g2s_plain(dst + kTile * 4, c.v_scale + row, bytes, &B->sc_full[slot]);
           }
         }
-        blocks(&tmk, row);
-        if (ok && i >= C::kAhead) blocks(&tmv, held[0]);
+        blocks(&tmk, row, &B->k_full[i % kSlots]);
+        if (ok && i >= C::kAhead) value_blocks(i - C::kAhead, held[0]);
         if constexpr (C::kAhead == 2) held[0] = held[1];
         held[C::kAhead - 1] = row;
+        last_tiles = (last_tiles & ~(1u << (i & 31))) | (((t + 1) * kTile > s.ctx ? 1u : 0u) << (i & 31));
         row = next;
       }
     }
     if constexpr (C::kAhead == 2)
-      if (ok && i > 1) blocks(&tmv, held[0]);
-    if (ok && i > 0) blocks(&tmv, held[C::kAhead - 1]);
-    if (!ok) {  // copies in flight land before the CTA may leave
-      for (int k = 0; k < filled; ++k) {
-        if (st == 0) phase ^= 1;
-        st = st == 0 ? C::kStages - 1 : st - 1;
-        mbar_wait_bounded(&B->full[st], phase ^ 1);
+      if (ok && i > 1) value_blocks(i - 2, held[0]);
+    if (ok && i > 0) value_blocks(i - 1, held[C::kAhead - 1]);
+    if (!ok) {
+      // copies in flight land before the CTA may leave (bounded: a barrier whose copies were not all issued
+      // runs into the limit)
+      for (int k = max(0, i - kSlots); k <= i; ++k) {
+        if (!mbar_wait_bounded(&B->k_full[k % kSlots], (k / kSlots) & 1)) break;
+        if (k > C::kAhead && !mbar_wait_bounded(&B->v_full[(k - C::kAhead) % kSlots], ((k - C::kAhead) / kSlots) & 1)) break;
       }
       if constexpr (kE4m3)
-        for (int k = i < kScSlots ? 0 : i - kScSlots; k < i; ++k) mbar_wait_bounded(&B->sc_full[k % kScSlots], (k / kScSlots) & 1);
+        for (int k = max(0, i - kScSlots); k < i; ++k) mbar_wait_bounded(&B->sc_full[k % kScSlots], (k / kScSlots) & 1);
     }
   } else if (warp == C::kMmaWarp) {
     // ------------------------------------------------------------ MMAs
@@ -461,7 +484,8 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
     constexpr uint32_t kKind = kE4m3 ? umma::kKindF8 : umma::kKindF16, kType = kE4m3 ? umma::kE4M3 : umma::kBF16;
     const uint32_t id_s = umma::idesc(kType, false, false, kTile, N), id_o = umma::idesc(kType, true, true, kTile, N);
     const uint32_t sQ = smem_u32(rest + C::oQ), sP = smem_u32(rest + C::oP);
-    int st = 0, phase = 0, i = 0, seg = 0;
+    int st = 0, i = 0, seg = 0, marks = 0;
+    uint32_t last_tiles = 0;  // bit i % 32: tile i has drafted tokens, the check warp cleans its V
     bool ok = true;
     auto wait_all = [&](uint64_t* bar, uint32_t parity) {
       ok = ok && wait(bar, parity, abort);
@@ -470,12 +494,16 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
     };
     auto product_o = [&](int j) {
       const int b = j & 1, ob = j % C::kOBuf;
-      if (!wait_all(&B->p_full[b], (j >> 1) & 1) || !wait_all(&B->o_empty[ob], ((j / C::kOBuf) & 1) ^ 1)) return;
+      if (!wait_all(&B->p_full[b], (j >> 1) & 1) || !wait_all(&B->o_empty[ob], ((j / C::kOBuf) & 1) ^ 1) ||
+          !wait_all(&B->v_full[j % kSlots], (j / kSlots) & 1))
+        return;
+      if ((last_tiles >> (j & 31)) & 1) {
+        if (!wait_all(&B->v_clean[marks % kMarks], (marks / kMarks) & 1)) return;
+        ++marks;
+      }
 #pragma unroll
       for (int h = 0; h < C::kHalves; ++h) {
         const int st2 = kE4m3 ? st : st + 1;  // two bf16 blocks are side by side
-        if (!wait_all(&B->full[st], phase)) return;
-        if (!kE4m3 && !wait_all(&B->full[st2], phase)) return;
         umma::fence_after_sync();
         if (elect_one()) {
           const uint32_t d = tmem + 2 * C::kCols + (ob * C::kHalves + h) * C::kCols;
@@ -492,8 +520,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
           }
         }
         __syncwarp();
-        st = st2 + 1;
-        if (st == C::kStages) st = 0, phase ^= 1;
+        st = st2 + 1 == C::kStages ? 0 : st2 + 1;
       }
     };
     Walk walk(a, plan);
@@ -503,9 +530,10 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
       if (!wait_all(&B->q_full[qb], (seg / C::kQBuf) & 1)) break;
       for (int t = s.t0; t < s.t1 && ok; ++t, ++i) {
         const int b = i & 1;
-        if (!wait_all(&B->s_empty[b], ((i >> 1) & 1) ^ 1)) break;
+        if (!wait_all(&B->s_empty[b], ((i >> 1) & 1) ^ 1) || !wait_all(&B->k_full[i % kSlots], (i / kSlots) & 1)) break;
+        const bool last = (t + 1) * kTile > s.ctx;
+        last_tiles = (last_tiles & ~(1u << (i & 31))) | ((last ? 1u : 0u) << (i & 31));
         for (int kb = 0; kb < C::kBlk; ++kb) {
-          if (!wait_all(&B->full[st], phase)) break;
           umma::fence_after_sync();
           if (elect_one()) {
             const uint64_t ka = umma::smem_desc_sw128(ring + st * kBlock);
@@ -519,7 +547,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
             }
           }
           __syncwarp();
-          if (++st == C::kStages) st = 0, phase ^= 1;
+          if (++st == C::kStages) st = 0;
         }
         if (ok && i >= C::kAhead) product_o(i - C::kAhead);
       }
@@ -609,6 +637,84 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
       arrive(&B->q_full[qb]);
       ++seg;
     }
+  } else if (warp == C::kCheckWarp) {
+    // ------------------------------------------------------------ pages, and V of the tiles with drafted tokens
+    // A weight of zero does not take a NaN or an infinity out of a product. Values behind the last token
+    // become zeros (as far as its box goes: behind it they are zeros already); a drafted token's that are no
+    // numbers too, and the output warps add them to the rows that see the token.
+    Walk walk(a, plan);
+    Seg s;
+    int seg = 0, marks = 0, i0 = 0;
+    bool ok = true;
+    while (ok && walk.next(a, s)) {
+      const int h = s.u / a.row_tiles;
+      const int32_t* table = p.table + (size_t)s.n * p.max_pages;
+      bool bad = false;
+      const int last_page = (min(s.len, s.t1 * kTile) - 1) / c.page;
+      for (int k = s.t0 * kTile / c.page + lane; k <= last_page; k += 32) {
+        const int page = __ldg(table + k);
+        bad |= page < 0 || page >= c.pages;
+      }
+      bad = __any_sync(0xffffffffu, bad);
+      if (lane == 0) {
+        B->bad[seg % kMarks] = bad;
+        arrive(&B->checked[seg % kMarks]);
+      }
+      for (int t = max(s.t0, s.ctx / kTile); t < s.t1; ++t, ++marks) {
+        const int i = i0 + t - s.t0, row0 = max(0, s.ctx - t * kTile), end = min(kTile, s.len - t * kTile);
+        const int row1 = (end + a.box - 1) / a.box * a.box;
+        uint32_t odd[2] = {0u, 0u};  // nodes with values that are no numbers
+        if constexpr (kE4m3)
+          for (int row = row0 + lane; row < end; row += 32) {
+            const int tok = t * kTile + row, page = __ldg(table + tok / c.page), node = tok - s.ctx;
+            if (page < 0 || page >= c.pages) continue;
+            const float sv = c.v_scale[((size_t)page * c.Hkv + h) * c.page + tok % c.page];
+            if (!(fabsf(sv) < INFINITY)) odd[node >> 5] |= 1u << (node & 31);
+          }
+        // the copies' warp says when this tile's phase of the barrier has begun: it may be many phases off
+        ok = wait(&B->v_issued[marks % kMarks], (marks / kMarks) & 1, abort) &&
+             wait(&B->v_full[i % kSlots], (i / kSlots) & 1, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        // V's place in the order of copies
+        const int first = C::kBlk * min(i + 1 + C::kAhead, plan.count) + C::kBlk * i;
+        auto piece = [&](int k) {
+          const int row = row0 + k / (8 * C::kBlk), x = k % (8 * C::kBlk);
+          return reinterpret_cast<uint4*>(smem + (first + (x >> 3)) % C::kStages * kBlock + row * 128) + (x & 7);
+        };
+        const int kept = (end - row0) * (8 * C::kBlk), all = (row1 - row0) * (8 * C::kBlk);
+#pragma unroll 1
+        for (int k = lane; k < kept; k += 32) {
+          uint4 v = *piece(k);
+          uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+          uint32_t any = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t o = 0;
+#pragma unroll
+            for (int y = 0; y < 32; y += kE4m3 ? 8 : 16) {
+              const uint32_t m = (kE4m3 ? 0x7fu : 0x7f80u) << y;
+              if ((w[e] & m) == m) o |= (kE4m3 ? 0xffu : 0xffffu) << y;
+            }
+            w[e] &= ~o;
+            any |= o;
+          }
+          if (any) {
+            const int node = t * kTile + row0 + k / (8 * C::kBlk) - s.ctx;
+            *piece(k) = v;
+            odd[node >> 5] |= 1u << (node & 31);
+          }
+        }
+#pragma unroll 4
+        for (int k = kept + lane; k < all; k += 32) *piece(k) = make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t lo = __reduce_or_sync(0xffffffffu, odd[0]), hi = __reduce_or_sync(0xffffffffu, odd[1]);
+        if (lane == 0) B->dirty[marks % kMarks] = lo | ((unsigned long long)hi << 32);
+        umma::fence_proxy_async_smem();
+        arrive(&B->v_clean[marks % kMarks]);
+      }
+      i0 += s.t1 - s.t0;
+      ++seg;
+    }
   } else if (warp < C::kOutWarp) {
     // ------------------------------------------------------------ softmax: thread = token of the tile
     const int wg = warp >> 2, w4 = warp & 3, tt = tid & 127;
@@ -670,23 +776,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         // the statistics of two tiles back have been read
         wait_warp(C::kOBuf == 2 ? &B->o_empty[b] : &B->st_empty[b], ph ^ 1, abort);
         if ((t + 1) * kTile > s.ctx) {  // drafted tokens, or tokens behind the last
-          // four E4M3 or two bf16 values: those that are no numbers become zeros
-          auto mend = [](uint32_t& w) {
-            uint32_t odd = 0;
-#pragma unroll
-            for (int y = 0; y < 32; y += kE4m3 ? 8 : 16) {
-              const uint32_t m = (kE4m3 ? 0x7fu : 0x7f80u) << y, all = (kE4m3 ? 0xffu : 0xffffu) << y;
-              if ((w & m) == m) odd |= all;
-            }
-            w &= ~odd;
-            return odd != 0;
-          };
           const int node = tok - s.ctx;
-          const bool cleans = !C::kSplit || wg == 0;
-          if (cleans) {
-            if (tt == 0) B->dirty[b] = 0;
-            sync_group(1 + wg);
-          }
 #pragma unroll
           for (int g = 0; g < kR / 8; ++g)
             if (g < used) {
@@ -699,43 +789,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
                 v.y = node < 0 || (in && ((mask_s[r + 1] >> (node & 63)) & 1)) ? v.y : -INFINITY;
               }
             }
-          // A weight of zero does not take a NaN or an infinity out of a product. Values behind the last
-          // token become zeros (as far as its box goes: behind it they are zeros already); a drafted token's
-          // that are no numbers too, and the output warps add them to the rows that see the token.
-          if (cleans) {
-            // What stood in V's ring blocks before has been used (a barrier's parity tells a phase from
-            // the next, not from the one after): the products up to the scores kAhead tiles on are done,
-            // or without such a tile those up to the last tile's output.
-            const int on = i + C::kAhead;
-            if (on < plan.count) wait(&B->s_full[on & 1], (on >> 1) & 1, abort);
-            else if (i > 0) wait(&B->p_empty[b ^ 1], ((i - 1) >> 1) & 1, abort);
-            // V's place in the order of copies
-            const int first = C::kBlk * min(i + 1 + C::kAhead, plan.count) + C::kBlk * i;
-            for (int vb = 0; vb < C::kBlk; ++vb)
-              wait(&B->full[(first + vb) % C::kStages], ((first + vb) / C::kStages) & 1, abort);
-            const int row0 = max(0, s.ctx - t * kTile), end = min(kTile, s.len - t * kTile);
-            const int row1 = (end + a.box - 1) / a.box * a.box;
-#pragma unroll 1
-            for (int k = row0 * (8 * C::kBlk) + tt; k < row1 * (8 * C::kBlk); k += 128) {
-              const int row = k / (8 * C::kBlk), piece = k % (8 * C::kBlk);
-              uint4* at = reinterpret_cast<uint4*>(smem + (first + (piece >> 3)) % C::kStages * kBlock + row * 128) + (piece & 7);
-              if (row >= end) {
-                *at = make_uint4(0u, 0u, 0u, 0u);
-                continue;
-              }
-              uint4 v = *at;
-              const bool fix = mend(v.x) | mend(v.y) | mend(v.z) | mend(v.w);
-              if (fix) {
-                *at = v;
-                atomicOr(&B->dirty[b], 1ull << (t * kTile + row - s.ctx));
-              }
-            }
-          }
-          if (kE4m3 && node >= 0 && node < p.P && !(fabsf(sv) < INFINITY)) {
-            sv = 0.f;
-            if (cleans) atomicOr(&B->dirty[b], 1ull << node);
-          }
-          __syncwarp();
+          if (kE4m3 && node >= 0 && !(fabsf(sv) < INFINITY)) sv = 0.f;  // its values are zeros, see the check warp
         }
         // ---- the tile's maximum of each row: of the warp first (row r's in lane r), then of the four warps
         float keep = -INFINITY;
@@ -851,6 +905,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
     float* ab = reinterpret_cast<float*>(rest + C::oAb) + og * 4 * kRows;
     float* fin = reinterpret_cast<float*>(rest + C::oFin) + og * 2 * kRows;
     float* parts = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kTicketBytes);
+    int marks = 0;
     int* tickets = static_cast<int*>(p.workspace) + og * kMaxCtas;
     Walk walk(a, plan);
     Seg s;
@@ -861,14 +916,6 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
       const int rows = max(0, min(min(kR, a.rows - roff), p.P * p.G - r0));  // of this thread, in this row tile
       const int32_t* table = p.table + (size_t)s.n * p.max_pages;
       const uint64_t* mask_s = reinterpret_cast<const uint64_t*>(rest + C::oMask) + qb * kRows + roff;
-      bool bad = false;  // pages out of the pool among this segment's
-      {
-        const int last = (min(s.len, s.t1 * kTile) - 1) / c.page;
-        for (int k = s.t0 * kTile / c.page + ot; k <= last; k += 128) {
-          const int page = __ldg(table + k);
-          bad |= page < 0 || page >= c.pages;
-        }
-      }
       wait_warp(&B->q_full[qb], (seg / C::kQBuf) & 1, abort);
       float2 acc[kH][kR / 2];
 #pragma unroll
@@ -932,7 +979,12 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
             }
         }
         umma::fence_before_sync();
-        const unsigned long long dirty = ((t + 1) * kTile > s.ctx) ? *(volatile unsigned long long*)&B->dirty[b] : 0ull;
+        unsigned long long dirty = 0;
+        if ((t + 1) * kTile > s.ctx) {
+          wait_warp(&B->v_clean[marks % kMarks], (marks / kMarks) & 1, abort);
+          dirty = *(volatile unsigned long long*)&B->dirty[marks % kMarks];
+          ++marks;
+        }
         if (dirty) {
           // drafted tokens whose values are no numbers: to the rows that see them
           for (int node = 0; node < p.P; ++node) {
@@ -960,20 +1012,18 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
           if (C::kOBuf == 1) arrive(&B->st_empty[b]);
         }
       }
-      __syncwarp();
+      wait_warp(&B->checked[seg % kMarks], (seg / kMarks) & 1, abort);
+      const bool bad = *(volatile int*)&B->bad[seg % kMarks] != 0;
       if (lane == 0) arrive(&B->q_empty[qb]);
       ++seg;
       // ---- the segment's result: whole, or a partial for the CTA that arrives last
-      bad = any_in_group(bar, bad);
       if (any_in_group(bar, *(volatile int*)abort)) continue;
       if (bad && ot == 0) report(p.dev_err, GDN_DEVERR_SLOT);
       // where a row's values go, row after row
       const int j0 = r0 / p.G, g0 = r0 - j0 * p.G;
       const size_t at0 = (((size_t)s.n * p.P + j0) * p.Hq + h * p.G + g0) * D + dim, wrap = (size_t)(p.Hq - p.G) * D;
-      auto finish = [&](float o, size_t at) {
-        if (p.gate) o = __fdividef(o, 1.f + __expf(-bf16_to_f32(p.gate[at])));
-        return o;
-      };
+      // o / (1 + e^-gate), as bf16
+      auto gated = [](float o, uint32_t g) { return f32_to_bf16(__fdividef(o, 1.f + __expf(-bf16_to_f32((uint16_t)g)))); };
       if (s.t0 == 0 && s.t1 == s.tiles) {
         if (bad) continue;
         if (ot < a.rows) fin[ot] = l_run == 0.f ? 0.f : __fdividef(1.f, l_run);
@@ -981,13 +1031,30 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         size_t at = at0;
         int g = g0;
 #pragma unroll
-        for (int r = 0; r < kR; ++r)
-          if (r < rows) {
+        for (int r8 = 0; r8 < kR; r8 += 8)
+          if (r8 < rows) {
+            size_t to[8];
+            uint16_t gate[8][kH];
 #pragma unroll
-            for (int k = 0; k < kH; ++k)
-              p.out[at + k * 128] = f32_to_bf16(finish((r & 1 ? acc[k][r / 2].y : acc[k][r / 2].x) * fin[roff + r], at + k * 128));
-            at += D;
-            if (++g == p.G) g = 0, at += wrap;
+            for (int e = 0; e < 8; ++e) {
+              to[e] = at;
+              if (p.gate && r8 + e < rows) {
+#pragma unroll
+                for (int k = 0; k < kH; ++k) gate[e][k] = p.gate[at + k * 128];
+              }
+              at += D;
+              if (++g == p.G) g = 0, at += wrap;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (r8 + e < rows) {
+                const float f = fin[roff + r8 + e];
+#pragma unroll
+                for (int k = 0; k < kH; ++k) {
+                  const float o = (e & 1 ? acc[k][(r8 + e) / 2].y : acc[k][(r8 + e) / 2].x) * f;
+                  p.out[to[e] + k * 128] = p.gate ? gated(o, gate[e][k]) : f32_to_bf16(o);
+                }
+              }
           }
         continue;
       }
@@ -1008,17 +1075,17 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         }
       const int grid = (int)min((long long)gridDim.x, plan.total);
       const int c0 = cta_of(s.first, plan.total, grid), c1 = cta_of(s.first + s.tiles - 1, plan.total, grid);
-      __threadfence();
       sync_group(bar);
       bool last = false;
       if (ot == 0) {
-        last = atomicAdd(tickets + c0, 1) == c1 - c0;
+        // releases the group's partial (the barrier before it) and acquires those of the CTAs that came first
+        int before;
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(tickets + c0) : "memory");
+        last = before == c1 - c0;
         if (last) tickets[c0] = 0;
-        __threadfence();
       }
       last = any_in_group(bar, last);
       if (!last) continue;
-      __threadfence();
       bool any_bad = false;
       if (ot < a.rows) {
         float m = -INFINITY, l = 0.f;
@@ -1039,52 +1106,77 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
       constexpr int kTake = 4 / kH;  // rows at a time
 #pragma unroll 1
       for (int r = 0; r < rows; r += kTake) {
-        float o[kTake][kH][4];
+        float o[kTake * kH][4];
+        uint2 gate[kTake * kH];
 #pragma unroll
-        for (int y = 0; y < kTake; ++y)
+        for (int y = 0; y < kTake * kH; ++y) {
+          gate[y] = make_uint2(0u, 0u);
 #pragma unroll
-          for (int e = 0; e < kH * 4; ++e) o[y][e / 4][e % 4] = 0.f;
-#pragma unroll 2
-        for (int k = c0 + piece; k <= c1; k += 4) {
-          const float* q = part(k, k == c0);
+          for (int x = 0; x < 4; ++x) o[y][x] = 0.f;
+        }
+        size_t at[kTake];
+#pragma unroll
+        for (int y = 0; y < kTake; ++y) {
+          const int ry = min(r + y, rows - 1);
+          at[y] = at1 + (size_t)ry * D + (size_t)((g0 + ry) / p.G) * wrap;
+          if (p.gate) {
+#pragma unroll
+            for (int e = 0; e < kH; ++e) gate[y * kH + e] = *reinterpret_cast<const uint2*>(p.gate + at[y] + e * 128);
+          }
+        }
+        for (int k = c0 + piece; k <= c1; k += 8) {
+          // two partials' values on their way before the first is used; the second may be none
+          const bool two = k + 4 <= c1;
+          const float *q0 = part(k, k == c0), *q1 = two ? part(k + 4, false) : q0;
+          float m[2][kTake];
+          float4 v[2][kTake * kH];
 #pragma unroll
           for (int y = 0; y < kTake; ++y) {
             const int ry = min(r + y, rows - 1);
-            const float mk = __ldcg(q + roff + ry);
+            m[0][y] = __ldcg(q0 + roff + ry);
+            m[1][y] = __ldcg(q1 + roff + ry);
 #pragma unroll
             for (int e = 0; e < kH; ++e) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(q + head + (ry * kH + e) * 128 + col));
-              const float w = mk == -INFINITY ? 0.f : ex2(mk - fin[roff + ry]);
-              o[y][e][0] = fmaf(w, v.x, o[y][e][0]);
-              o[y][e][1] = fmaf(w, v.y, o[y][e][1]);
-              o[y][e][2] = fmaf(w, v.z, o[y][e][2]);
-              o[y][e][3] = fmaf(w, v.w, o[y][e][3]);
+              v[0][y * kH + e] = __ldcg(reinterpret_cast<const float4*>(q0 + head + (ry * kH + e) * 128 + col));
+              v[1][y * kH + e] = __ldcg(reinterpret_cast<const float4*>(q1 + head + (ry * kH + e) * 128 + col));
             }
           }
+#pragma unroll
+          for (int z = 0; z < 2; ++z)
+#pragma unroll
+            for (int y = 0; y < kTake; ++y) {
+              const float w = m[z][y] == -INFINITY || (z && !two) ? 0.f : ex2(m[z][y] - fin[roff + min(r + y, rows - 1)]);
+#pragma unroll
+              for (int e = 0; e < kH; ++e) {
+                float* t = o[y * kH + e];
+                const float4 u = v[z][y * kH + e];
+                if (z == 0 || two) {
+                  t[0] = fmaf(w, u.x, t[0]);
+                  t[1] = fmaf(w, u.y, t[1]);
+                  t[2] = fmaf(w, u.z, t[2]);
+                  t[3] = fmaf(w, u.w, t[3]);
+                }
+              }
+            }
         }
         __syncwarp();
 #pragma unroll
-        for (int y = 0; y < kTake; ++y) {
-          const int ry = r + y, step = g0 + ry, j = step / p.G;
-          const size_t at = at1 + (size_t)ry * D + (size_t)j * wrap;
+        for (int y = 0; y < kTake * kH; ++y) {
 #pragma unroll
-          for (int e = 0; e < kH; ++e) {
+          for (int x = 0; x < 4; ++x) {
+            o[y][x] += __shfl_xor_sync(0xffffffffu, o[y][x], 8);
+            o[y][x] += __shfl_xor_sync(0xffffffffu, o[y][x], 16);
+          }
+          const int ry = r + y / kH;
+          if (piece == y && ry < rows) {
+            const float f = fin[kRows + roff + ry];
+            uint32_t w[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              o[y][e][x] += __shfl_xor_sync(0xffffffffu, o[y][e][x], 8);
-              o[y][e][x] += __shfl_xor_sync(0xffffffffu, o[y][e][x], 16);
+              const uint32_t gx = x & 1 ? (x < 2 ? gate[y].x : gate[y].y) >> 16 : (x < 2 ? gate[y].x : gate[y].y) & 0xffff;
+              w[x] = p.gate ? gated(o[y][x] * f, gx) : f32_to_bf16(o[y][x] * f);
             }
-            if (piece == (y * kH + e) % 4 && ry < rows) {
-              const float f = fin[kRows + roff + ry];
-              uint32_t w[2];
-#pragma unroll
-              for (int x = 0; x < 4; x += 2) {
-                const size_t to = at + e * 128 + x;
-                w[x / 2] = (uint32_t)f32_to_bf16(finish(o[y][e][x] * f, to)) |
-                           ((uint32_t)f32_to_bf16(finish(o[y][e][x + 1] * f, to + 1)) << 16);
-              }
-              *reinterpret_cast<uint2*>(p.out + at + e * 128) = make_uint2(w[0], w[1]);
-            }
+            *reinterpret_cast<uint2*>(p.out + at[y / kH] + (y % kH) * 128) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
           }
         }
       }
