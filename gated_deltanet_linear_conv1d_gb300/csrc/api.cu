@@ -530,7 +530,7 @@ size_t gdn_tree_attention_workspace_bytes(const gdn_kv_cache* cache, int32_t num
   KvArgs c{};
   if (check_cache(cache, &c) != GDN_OK || num_seqs <= 0 || check_tree_sizes(c, num_seqs, num_pos, num_q_heads) != GDN_OK)
     return 0;
-  return tree_attn_workspace_bytes(num_pos, num_q_heads / c.Hkv);
+  return tree_attn_workspace_bytes(num_pos, num_q_heads / c.Hkv, cache->head_dim);
 }
 
 gdn_status gdn_tree_attention(const gdn_kv_cache* cache, const uint16_t* q, const int32_t* block_table,
@@ -547,7 +547,7 @@ gdn_status gdn_tree_attention(const gdn_kv_cache* cache, const uint16_t* q, cons
   if (num_seqs == 0) return GDN_OK;
   if (!q || !block_table || !ctx_len || !out || max_pages == 0) return GDN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(gate, 16) || !aligned(tree_mask, 8)) return GDN_ERR_INVALID_ARG;
-  const size_t need = tree_attn_workspace_bytes(num_pos, num_q_heads / c.Hkv);
+  const size_t need = tree_attn_workspace_bytes(num_pos, num_q_heads / c.Hkv, cache->head_dim);
   if (workspace_bytes < need || (need > 0 && (!workspace || !aligned(workspace, 256)))) return GDN_ERR_INVALID_ARG;
   TreeAttnArgs a{q, block_table, ctx_len, tree_mask, gate, out, scale, num_seqs, num_pos, num_q_heads,
                  num_q_heads / c.Hkv, cache->head_dim, max_pages, workspace, dev_err};

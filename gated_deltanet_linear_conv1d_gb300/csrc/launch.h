@@ -262,7 +262,7 @@ cudaError_t launch_rmsnorm(const RmsArgs& a, cudaStream_t stream);
 // The rows of T tokens through the head norm and the rotation (norm) and / or into the cache.
 cudaError_t launch_rows(const RopeArgs& a, const KvArgs& c, bool norm, int D, cudaStream_t stream);
 cudaError_t launch_kv_read(const ReadArgs& a, const KvArgs& c, int D, cudaStream_t stream);
-size_t tree_attn_workspace_bytes(int P, int G);
+size_t tree_attn_workspace_bytes(int P, int G, int D);
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, const KvArgs& c, cudaStream_t stream);
 cudaError_t launch_quant_act(const QuantActArgs& a, cudaStream_t stream);
 cudaError_t launch_quant_weight(const QuantWeightArgs& a, cudaStream_t stream);

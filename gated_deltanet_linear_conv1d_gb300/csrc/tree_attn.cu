@@ -16,9 +16,59 @@ void row_tiles(int P, int G, int* rows, int* tiles) {
   *tiles = (all + *rows - 1) / *rows;
 }
 
-// An output group's partial: its rows' maxima and sums, a flag, and rows x 128 values, or rows x 256 where
-// one group has both halves of D = 256 (up to 16 rows).
-int slot_floats(int rows) { return ((2 * rows + 4) / 4 * 4 + rows * (rows <= 16 ? 256 : 128) + 63) / 64 * 64; }
+int slot_floats(int rows, int D) { return (tree_attn::head_floats(rows) + rows * D + 63) / 64 * 64; }
+
+// The partial results of the units that several CTAs share, one after the other in the order of their tiles:
+// blockIdx.x is the CTA with a unit's first tile, blockIdx.y 1024 / D of its rows, a thread has four values.
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(const tree_attn::Args a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const TreeAttnArgs& p = a.p;
+  const tree_attn::Desc d = static_cast<const tree_attn::Desc*>(p.workspace)[blockIdx.x];
+  if (!d.valid) return;
+  constexpr int kPer = D / 4;
+  const int row = blockIdx.y * (256 / kPer) + threadIdx.x / kPer, col = threadIdx.x % kPer * 4;
+  const int r = d.u % a.row_tiles * a.rows + row, j = r / p.G;
+  if (row >= a.rows || j >= p.P) return;
+  const int head = tree_attn::head_floats(a.rows);
+  const size_t at = (((size_t)d.n * p.P + j) * p.Hq + d.u / a.row_tiles * p.G + r % p.G) * D + col;
+  uint2 gate = make_uint2(0u, 0u);
+  if (p.gate) gate = *reinterpret_cast<const uint2*>(p.gate + at);
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  bool bad = false;
+  constexpr int kAtOnce = 4;
+  for (int k0 = blockIdx.x; k0 <= d.last; k0 += kAtOnce) {
+    float mk[kAtOnce], lk[kAtOnce];
+    float4 v[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int k = min(k0 + i, d.last);
+      const float* q = tree_attn::partial(a, k, k == blockIdx.x);
+      mk[i] = q[row];
+      lk[i] = q[a.rows + row];
+      bad |= reinterpret_cast<const int*>(q)[2 * a.rows] != 0 || reinterpret_cast<const int*>(q)[2 * a.rows + 1] != 0;
+      v[i] = *reinterpret_cast<const float4*>(q + head + (size_t)row * D + col);
+      if (k0 + i > d.last) mk[i] = -INFINITY, lk[i] = 0.f, v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float mn = m;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) mn = fmaxf(mn, mk[i]);
+    const float keep = m == -INFINITY ? 0.f : tree_attn::ex2(m - mn);
+    l *= keep;
+    o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const float w = mk[i] == -INFINITY ? 0.f : tree_attn::ex2(mk[i] - mn);
+      l += mk[i] == -INFINITY ? lk[i] : lk[i] * w;  // a NaN of a row without a maximum stays one
+      o = make_float4(fmaf(v[i].x, w, o.x), fmaf(v[i].y, w, o.y), fmaf(v[i].z, w, o.z), fmaf(v[i].w, w, o.w));
+    }
+    m = mn;
+  }
+  if (bad) return;
+  const float f = l == 0.f ? 0.f : __fdividef(1.f, l);
+  *reinterpret_cast<uint2*>(p.out + at) = tree_attn::to_out(make_float4(o.x * f, o.y * f, o.z * f, o.w * f), p.gate, gate);
+}
 
 // Rows of one token and kv head; a box is 128 bytes of `box` tokens, swizzled as the MMAs read it.
 bool encode(CUtensorMap* m, void* base, const KvArgs& c, int D, int box_rows) {
@@ -36,10 +86,10 @@ bool encode(CUtensorMap* m, void* base, const KvArgs& c, int D, int box_rows) {
 
 }  // namespace
 
-size_t tree_attn_workspace_bytes(int P, int G) {
+size_t tree_attn_workspace_bytes(int P, int G, int D) {
   int rows, tiles;
   row_tiles(P, G, &rows, &tiles);
-  return tree_attn::kTicketBytes + (size_t)4 * tree_attn::kMaxCtas * slot_floats(rows) * sizeof(float);
+  return tree_attn::kDescBytes + (size_t)2 * tree_attn::kMaxCtas * slot_floats(rows, D) * sizeof(float);
 }
 
 cudaError_t launch_tree_attn(const TreeAttnArgs& p, const KvArgs& c, cudaStream_t stream) {
@@ -51,13 +101,24 @@ cudaError_t launch_tree_attn(const TreeAttnArgs& p, const KvArgs& c, cudaStream_
   a.p = p;
   a.c = c;
   row_tiles(p.P, p.G, &a.rows, &a.row_tiles);
-  a.slot_floats = slot_floats(a.rows);
+  a.slot_floats = slot_floats(a.rows, p.D);
   a.box = 16;
   while (a.box < tree_attn::kTile && c.page % (2 * a.box) == 0) a.box *= 2;
   CUtensorMap tmk{}, tmv{};
   if (!encode(&tmk, c.k, c, p.D, a.box) || !encode(&tmv, c.v, c, p.D, a.box)) return cudaErrorInvalidValue;
   const int grid = sms < tree_attn::kMaxCtas ? sms : tree_attn::kMaxCtas;
-  return c.e4m3 ? tree_attn::launch_e4m3(a, tmk, tmv, grid, stream) : tree_attn::launch_bf16(a, tmk, tmv, grid, stream);
+  err = c.e4m3 ? tree_attn::launch_e4m3(a, tmk, tmv, grid, stream) : tree_attn::launch_bf16(a, tmk, tmv, grid, stream);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)((a.rows * p.D + 1023) / 1024), 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return p.D == 256 ? cudaLaunchKernelEx(&cfg, join_kernel<256>, a) : cudaLaunchKernelEx(&cfg, join_kernel<128>, a);
 }
 
 }  // namespace gdn

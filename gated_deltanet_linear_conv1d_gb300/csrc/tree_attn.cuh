@@ -13,7 +13,9 @@
 // whatever the lengths, and a single long request uses the whole GPU. The lengths
 // are read on the device, so a captured graph takes new ones. A (request, head,
 // row tile) that lies in several CTAs' pieces leaves a partial result per CTA in
-// the workspace, and the CTA that arrives last adds them up in a fixed order.
+// the workspace, and a second kernel adds them up in the order of the tiles. (With
+// the CTA that arrived last doing it, two tickets and a chain of trips to L2 took
+// up to 45 us for 64 rows.)
 //
 // Both products take the cache as their first operand, so a tile costs the tensor
 // cores the same 128 lanes for few query rows as for many columns:
@@ -57,7 +59,7 @@ constexpr int kTile = 128;               // tokens per tile
 constexpr uint32_t kBlock = 128 * 128;   // bytes of one ring block: 128 tokens x 128 bytes
 constexpr int kMaxCtas = 152;
 constexpr int kSmemLimit = 227 * 1024;
-constexpr int kTicketBytes = 2048;
+constexpr int kDescBytes = 4096;          // of the workspace: a Desc per CTA
 constexpr int kScSlots = 4;              // tiles of scales in flight
 // A barrier's parity tells a phase from the next one only. So there are more of them than their writer can be
 // ahead of their reader: the ring (at most 11 blocks) holds K or V of fewer than 8 tiles.
@@ -70,8 +72,22 @@ struct Args {
   int rows;       // query rows per row tile (the last one may have fewer)
   int row_tiles;
   int box;        // tokens per TMA box: a power of two that divides the page, at most 128
-  int slot_floats;  // workspace floats per partial (of one output group)
+  int slot_floats;  // workspace floats per partial
 };
+
+// A unit (request x head x row tile) that lies in several CTAs' pieces, noted by the CTA that has its first tile.
+struct Desc {
+  int valid, n, u, last;  // `last`: the CTA that has its last tile
+};
+
+// A partial result: the rows' maxima and sums, two words that are 0 once an output group has written its part
+// and no page was out of the pool, then [rows][D] fp32. A CTA has two: of the unit that ends in its piece (or
+// runs through it) and of the one that begins there.
+__host__ __device__ __forceinline__ int head_floats(int rows) { return (2 * rows + 2 + 3) / 4 * 4; }
+__device__ __forceinline__ float* partial(const Args& a, int cta, bool begins) {
+  return reinterpret_cast<float*>(static_cast<unsigned char*>(a.p.workspace) + kDescBytes) +
+         (size_t)(2 * cta + (begins ? 1 : 0)) * a.slot_floats;
+}
 
 template <int D, bool kE4m3, int kRows>
 struct Cfg {
@@ -106,7 +122,8 @@ struct Cfg {
   static constexpr int oMask = oAb + 8 * kRows * 4;                         // [kQBuf][kRows] uint64
   static constexpr int oQs = oMask + kQBuf * kRows * 8;                     // [kQBuf][kRows] fp32
   static constexpr int oFin = oQs + kQBuf * kRows * 4;                      // [2 groups][2][kRows] fp32
-  static constexpr int oBars = oFin + 4 * kRows * 4;
+  static constexpr int oStage = oFin + 4 * kRows * 4;                       // [kOutGroups][4 rows][kOutHalves * 128] fp32
+  static constexpr int oBars = oStage + kOutGroups * 4 * kOutHalves * 512;
   static constexpr int kRest = oBars + 1408;
   static constexpr int kFit = (kSmemLimit - kRest) / (int)kBlock;
   // an even number of blocks keeps the two bf16 blocks of a 128-wide half of V side by side
@@ -267,6 +284,18 @@ __device__ __forceinline__ uint4 to_bf16x8(const float (&x)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Four values as bf16, with a gate taken times 1 / (1 + e^-gate) first.
+__device__ __forceinline__ uint2 to_out(float4 o, bool gated, uint2 gate) {
+  if (gated) {
+    o.x = __fdividef(o.x, 1.f + __expf(-bf16_to_f32((uint16_t)(gate.x & 0xffff))));
+    o.y = __fdividef(o.y, 1.f + __expf(-bf16_to_f32((uint16_t)(gate.x >> 16))));
+    o.z = __fdividef(o.z, 1.f + __expf(-bf16_to_f32((uint16_t)(gate.y & 0xffff))));
+    o.w = __fdividef(o.w, 1.f + __expf(-bf16_to_f32((uint16_t)(gate.y >> 16))));
+  }
+  return make_uint2((uint32_t)f32_to_bf16(o.x) | ((uint32_t)f32_to_bf16(o.y) << 16),
+                    (uint32_t)f32_to_bf16(o.z) | ((uint32_t)f32_to_bf16(o.w) << 16));
+}
+
 // Byte `at` of row `row` in a block of 128-byte rows under the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swz(int row, int at) {
   return (uint32_t)(row * 128 + ((((at >> 4) ^ (row & 7)) << 4) | (at & 15)));
@@ -303,6 +332,79 @@ __device__ __forceinline__ bool any_in_group(int id, bool x) {
 
 __device__ __forceinline__ int cta_of(long long tile, long long total, int grid) {
   return (int)(((tile + 1) * grid - 1) / total);
+}
+
+// The query rows of a segment into query buffer qb, as rows of the MMAs' second operand, with their masks and
+// factors. `share` of `shares` warps take eight rows at a time.
+template <int D, bool kE4m3, int kRows>
+__device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned char* rest, int qb, int share, int shares) {
+  using C = Cfg<D, kE4m3, kRows>;
+  const TreeAttnArgs& p = a.p;
+  const int lane = threadIdx.x & 31;
+  const int rp = kE4m3 ? (a.rows + 7) / 8 * 8 : (a.rows + 15) / 16 * 16;
+  // scores are maxima before they are scaled: a negative scale turns the query's sign, none leaves zeros
+  const uint32_t sign = p.scale < 0.f ? 0x80008000u : 0u, mask_q = p.scale == 0.f ? 0u : ~0u;
+  const float to_log2 = p.scale == 0.f ? 1.f : fabsf(p.scale) * kLog2e;
+  const int h = s.u / a.row_tiles, r0 = (s.u % a.row_tiles) * a.rows;
+  unsigned char* q_s = rest + C::oQ + qb * C::kQBytes;
+  float* qs_s = reinterpret_cast<float*>(rest + C::oQs) + qb * kRows;
+  uint64_t* mask_s = reinterpret_cast<uint64_t*>(rest + C::oMask) + qb * kRows;
+  if (share == 0)
+          for (int r = lane; r < rp; r += 32) {
+          const int j = (r0 + r) / p.G;
+          uint64_t m = 0;
+          if (r < a.rows && j < p.P) m = p.mask ? __ldg(p.mask + (size_t)s.n * p.P + j) : j == 63 ? ~0ull : (2ull << j) - 1;
+          mask_s[r] = m;
+        }
+        constexpr int kBatch = 8;
+        for (int rb = share * kBatch; rb < rp; rb += shares * kBatch) {
+          uint4 raw[kBatch];
+  #pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int r = rb + i, j = (r0 + r) / p.G, g = (r0 + r) % p.G;
+            raw[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < a.rows && j < p.P && lane < D / 8)
+              raw[i] = *reinterpret_cast<const uint4*>(p.q + (((size_t)s.n * p.P + j) * p.Hq + h * p.G + g) * D + lane * 8);
+            raw[i] = make_uint4((raw[i].x ^ sign) & mask_q, (raw[i].y ^ sign) & mask_q, (raw[i].z ^ sign) & mask_q,
+                                (raw[i].w ^ sign) & mask_q);
+          }
+  #pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int r = rb + i;
+            if constexpr (!kE4m3) {
+              // eight values are one 16-byte piece of block lane / 8
+              if (lane < D / 8)
+                *reinterpret_cast<uint4*>(q_s + (lane >> 3) * (C::kCols * 128) + swz(r, (lane & 7) * 16)) = raw[i];
+              if (lane == 0) qs_s[r] = fmaxf(to_log2, 1e-37f);
+            } else {
+              const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+              float x[8], most = 0.f;
+  #pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                x[2 * e] = __uint_as_float(w[e] << 16);
+                x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+              }
+  #pragma unroll
+              for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(x[e]));
+              most = warp_max(most);
+              // a power of two that takes the largest value below 256; a row with an infinity has no scores
+              const int ex = (int)(__float_as_uint(most) >> 23) - 127;
+              const int up = most == 0.f ? 0 : min(7 - ex, 120);
+              const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+  #pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] *= f;
+              uint2 first, second;
+              two_terms(x, first, second);
+              if (lane < D / 8) {
+                unsigned char* blk = q_s + (lane >> 4) * (C::kCols * 128);
+                *reinterpret_cast<uint2*>(blk + swz(r, (lane & 15) * 8)) = first;
+                *reinterpret_cast<uint2*>(blk + swz(rp + r, (lane & 15) * 8)) = second;
+              }
+              const float down = __uint_as_float((uint32_t)(127 - up) << 23);
+              if (lane == 0) qs_s[r] = ex == 128 ? __uint_as_float(0x7fffffffu) : fmaxf(to_log2 * down, 1e-37f);
+            }
+          }
+        }
 }
 
 template <int D, bool kE4m3, int kRows>
@@ -395,6 +497,25 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
     umma::fence_after_sync();
   }
   const Plan plan = B->plan;
+  asm volatile("griddepcontrol.launch_dependents;");  // the join may be set up; it waits for this grid's end
+  if (tid == 0) {
+    static_cast<Desc*>(p.workspace)[blockIdx.x].valid = 0;
+    for (int k = 0; k < 2; ++k) {
+      int* written = reinterpret_cast<int*>(partial(a, blockIdx.x, k)) + 2 * a.rows;
+      written[0] = written[1] = 1;
+    }
+  }
+  // All warps but the copies' load the first query rows: no tile can be scored before.
+  if (warp != C::kCopyWarp) {
+    if (plan.count > 0) {
+      Walk walk(a, plan);
+      Seg s;
+      walk.next(a, s);
+      load_queries<D, kE4m3, kRows>(a, s, rest, 0, warp < C::kCopyWarp ? warp : warp - 1, kThreads / 32 - 1);
+      umma::fence_proxy_async_smem();
+    }
+    asm volatile("bar.sync 5, %0;" ::"n"(C::kThreads - 32) : "memory");
+  }
   const uint32_t tmem = B->tmem;
   int* abort = &B->abort;
 
@@ -560,80 +681,19 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
     }
     __syncwarp();
   } else if (warp == C::kQueryWarp) {
-    // ------------------------------------------------------------ query rows
+    // ------------------------------------------------------------ query rows (the first segment's are there)
     Walk walk(a, plan);
     Seg s;
     int seg = 0;
     bool ok = true;
-    const int rp = kE4m3 ? (a.rows + 7) / 8 * 8 : (a.rows + 15) / 16 * 16;
-    // scores are maxima before they are scaled: a negative scale turns the query's sign, none leaves zeros
-    const uint32_t sign = p.scale < 0.f ? 0x80008000u : 0u, mask_q = p.scale == 0.f ? 0u : ~0u;
-    const float to_log2 = p.scale == 0.f ? 1.f : fabsf(p.scale) * kLog2e;
     while (ok && walk.next(a, s)) {
       const int qb = seg % C::kQBuf;
-      ok = wait(&B->q_empty[qb], ((seg / C::kQBuf) & 1) ^ 1, abort);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const int h = s.u / a.row_tiles, r0 = (s.u % a.row_tiles) * a.rows;
-      unsigned char* q_s = rest + C::oQ + qb * C::kQBytes;
-      float* qs_s = reinterpret_cast<float*>(rest + C::oQs) + qb * kRows;
-      uint64_t* mask_s = reinterpret_cast<uint64_t*>(rest + C::oMask) + qb * kRows;
-      for (int r = lane; r < rp; r += 32) {
-        const int j = (r0 + r) / p.G;
-        uint64_t m = 0;
-        if (r < a.rows && j < p.P) m = p.mask ? __ldg(p.mask + (size_t)s.n * p.P + j) : j == 63 ? ~0ull : (2ull << j) - 1;
-        mask_s[r] = m;
+      if (seg > 0) {
+        ok = __all_sync(0xffffffffu, wait(&B->q_empty[qb], ((seg / C::kQBuf) & 1) ^ 1, abort));
+        if (!ok) break;
+        load_queries<D, kE4m3, kRows>(a, s, rest, qb, 0, 1);
+        umma::fence_proxy_async_smem();
       }
-      constexpr int kBatch = 8;
-      for (int rb = 0; rb < rp; rb += kBatch) {
-        uint4 raw[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int r = rb + i, j = (r0 + r) / p.G, g = (r0 + r) % p.G;
-          raw[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < a.rows && j < p.P && lane < D / 8)
-            raw[i] = *reinterpret_cast<const uint4*>(p.q + (((size_t)s.n * p.P + j) * p.Hq + h * p.G + g) * D + lane * 8);
-          raw[i] = make_uint4((raw[i].x ^ sign) & mask_q, (raw[i].y ^ sign) & mask_q, (raw[i].z ^ sign) & mask_q,
-                              (raw[i].w ^ sign) & mask_q);
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int r = rb + i;
-          if constexpr (!kE4m3) {
-            // eight values are one 16-byte piece of block lane / 8
-            if (lane < D / 8)
-              *reinterpret_cast<uint4*>(q_s + (lane >> 3) * (C::kCols * 128) + swz(r, (lane & 7) * 16)) = raw[i];
-            if (lane == 0) qs_s[r] = fmaxf(to_log2, 1e-37f);
-          } else {
-            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-            float x[8], most = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              x[2 * e] = __uint_as_float(w[e] << 16);
-              x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(x[e]));
-            most = warp_max(most);
-            // a power of two that takes the largest value below 256; a row with an infinity has no scores
-            const int ex = (int)(__float_as_uint(most) >> 23) - 127;
-            const int up = most == 0.f ? 0 : min(7 - ex, 120);
-            const float f = __uint_as_float((uint32_t)(up + 127) << 23);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= f;
-            uint2 first, second;
-            two_terms(x, first, second);
-            if (lane < D / 8) {
-              unsigned char* blk = q_s + (lane >> 4) * (C::kCols * 128);
-              *reinterpret_cast<uint2*>(blk + swz(r, (lane & 15) * 8)) = first;
-              *reinterpret_cast<uint2*>(blk + swz(rp + r, (lane & 15) * 8)) = second;
-            }
-            const float down = __uint_as_float((uint32_t)(127 - up) << 23);
-            if (lane == 0) qs_s[r] = ex == 128 ? __uint_as_float(0x7fffffffu) : fmaxf(to_log2 * down, 1e-37f);
-          }
-        }
-      }
-      umma::fence_proxy_async_smem();
       arrive(&B->q_full[qb]);
       ++seg;
     }
@@ -904,9 +964,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
     const float* tile_s = reinterpret_cast<const float*>(rest + C::oTile);
     float* ab = reinterpret_cast<float*>(rest + C::oAb) + og * 4 * kRows;
     float* fin = reinterpret_cast<float*>(rest + C::oFin) + og * 2 * kRows;
-    float* parts = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kTicketBytes);
     int marks = 0;
-    int* tickets = static_cast<int*>(p.workspace) + og * kMaxCtas;
     Walk walk(a, plan);
     Seg s;
     int i = 0, seg = 0;
@@ -1019,168 +1077,64 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
       // ---- the segment's result: whole, or a partial for the CTA that arrives last
       if (any_in_group(bar, *(volatile int*)abort)) continue;
       if (bad && ot == 0) report(p.dev_err, GDN_DEVERR_SLOT);
-      // where a row's values go, row after row
-      const int j0 = r0 / p.G, g0 = r0 - j0 * p.G;
-      const size_t at0 = (((size_t)s.n * p.P + j0) * p.Hq + h * p.G + g0) * D + dim, wrap = (size_t)(p.Hq - p.G) * D;
-      // o / (1 + e^-gate), as bf16
-      auto gated = [](float o, uint32_t g) { return f32_to_bf16(__fdividef(o, 1.f + __expf(-bf16_to_f32((uint16_t)g)))); };
       if (s.t0 == 0 && s.t1 == s.tiles) {
         if (bad) continue;
         if (ot < a.rows) fin[ot] = l_run == 0.f ? 0.f : __fdividef(1.f, l_run);
-        sync_group(bar);
-        size_t at = at0;
-        int g = g0;
+        // Four rows at a time through shared memory, a thread then has neighbouring values of one row. The loop
+        // is not unrolled (the registers' choice is): code that runs once per segment costs its fetches.
+        float* stage = reinterpret_cast<float*>(rest + C::oStage) + og * (4 * kH * 128);
+        const int mine = ot >> 5, col = (ot & 31) * (4 * kH);  // row of the four, first value
+#pragma unroll 1
+        for (int r4 = 0; r4 < rows; r4 += 4) {
+          const int r = r4 + mine, rr = r0 + r, j = rr / p.G, g = rr - j * p.G;
+          const size_t at = (((size_t)s.n * p.P + j) * p.Hq + h * p.G + g) * D + half * 128 + col;
+          uint2 gate[kH];
+          if (p.gate && r < rows) {
 #pragma unroll
-        for (int r8 = 0; r8 < kR; r8 += 8)
-          if (r8 < rows) {
-            size_t to[8];
-            uint16_t gate[8][kH];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              to[e] = at;
-              if (p.gate && r8 + e < rows) {
-#pragma unroll
-                for (int k = 0; k < kH; ++k) gate[e][k] = p.gate[at + k * 128];
-              }
-              at += D;
-              if (++g == p.G) g = 0, at += wrap;
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (r8 + e < rows) {
-                const float f = fin[roff + r8 + e];
-#pragma unroll
-                for (int k = 0; k < kH; ++k) {
-                  const float o = (e & 1 ? acc[k][(r8 + e) / 2].y : acc[k][(r8 + e) / 2].x) * f;
-                  p.out[to[e] + k * 128] = p.gate ? gated(o, gate[e][k]) : f32_to_bf16(o);
-                }
-              }
+            for (int e = 0; e < kH; ++e) gate[e] = *reinterpret_cast<const uint2*>(p.gate + at + 4 * e);
           }
+          sync_group(bar);
+#pragma unroll
+          for (int c4 = 0; c4 < kR; c4 += 4)
+            if (c4 == r4) {
+#pragma unroll
+              for (int k = 0; k < kH; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  stage[e * (kH * 128) + k * 128 + ot] = e & 1 ? acc[k][(c4 + e) / 2].y : acc[k][(c4 + e) / 2].x;
+            }
+          sync_group(bar);
+          if (r < rows) {
+            const float f = fin[roff + r];
+#pragma unroll
+            for (int e = 0; e < kH; ++e) {
+              const float4 o = *reinterpret_cast<const float4*>(stage + mine * (kH * 128) + col + 4 * e);
+              *reinterpret_cast<uint2*>(p.out + at + 4 * e) = to_out(make_float4(o.x * f, o.y * f, o.z * f, o.w * f), p.gate, gate[e]);
+            }
+          }
+        }
         continue;
       }
-      // a partial: [rows] maxima, [rows] sums, the flag, then this group's [rows][kH][128] sums
-      auto part = [&](int cta, int first) { return parts + (size_t)((2 * cta + first) * C::kOutGroups + og) * a.slot_floats; };
-      float* mine = part(blockIdx.x, s.t0 == 0);
-      const int head = (2 * a.rows + 4) / 4 * 4;
-      if (ot < a.rows) {
+      float* mine = partial(a, blockIdx.x, s.t0 == 0);
+      if (ot < a.rows && og == 0) {
         mine[ot] = m_run;
         mine[a.rows + ot] = l_run;
       }
-      if (ot == 0) reinterpret_cast<int*>(mine)[2 * a.rows] = bad;
+      float* rows_at = mine + head_floats(a.rows) + roff * D + dim;
 #pragma unroll
       for (int r = 0; r < kR; ++r)
         if (r < rows) {
 #pragma unroll
-          for (int k = 0; k < kH; ++k) mine[head + (r * kH + k) * 128 + ot] = r & 1 ? acc[k][r / 2].y : acc[k][r / 2].x;
+          for (int k = 0; k < kH; ++k) rows_at[r * D + k * 128] = r & 1 ? acc[k][r / 2].y : acc[k][r / 2].x;
         }
-      const int grid = (int)min((long long)gridDim.x, plan.total);
-      const int c0 = cta_of(s.first, plan.total, grid), c1 = cta_of(s.first + s.tiles - 1, plan.total, grid);
-      sync_group(bar);
-      bool last = false;
       if (ot == 0) {
-        // releases the group's partial (the barrier before it) and acquires those of the CTAs that came first
-        int before;
-        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(tickets + c0) : "memory");
-        last = before == c1 - c0;
-        if (last) tickets[c0] = 0;
-      }
-      last = any_in_group(bar, last);
-      if (!last) continue;
-      bool any_bad = false;
-      if (ot < a.rows) {
-        float m = -INFINITY, l = 0.f;
-        for (int k = c0; k <= c1; ++k) m = fmaxf(m, __ldcg(part(k, k == c0) + ot));
-        for (int k = c0; k <= c1; ++k) {
-          const float mk = __ldcg(part(k, k == c0) + ot), lk = __ldcg(part(k, k == c0) + a.rows + ot);
-          if (mk != -INFINITY || lk != 0.f) l += lk * ex2(mk - m);
-        }
-        fin[ot] = m;
-        fin[kRows + ot] = l == 0.f ? 0.f : __fdividef(1.f, l);
-      }
-      for (int k = c0 + ot; k <= c1; k += 128)
-        any_bad |= __ldcg(reinterpret_cast<const int*>(part(k, k == c0)) + 2 * a.rows) != 0;
-      if (any_in_group(bar, any_bad)) continue;
-      // Eight lanes take 32 of the warp's values, four a lane, and every fourth partial: few round trips to L2.
-      const int piece = lane >> 3, col = (warp & 3) * 32 + (lane & 7) * 4;
-      const size_t at1 = at0 - ot + col;
-      constexpr int kTake = 4 / kH;  // rows at a time
-#pragma unroll 1
-      for (int r = 0; r < rows; r += kTake) {
-        float o[kTake * kH][4];
-        uint2 gate[kTake * kH];
-#pragma unroll
-        for (int y = 0; y < kTake * kH; ++y) {
-          gate[y] = make_uint2(0u, 0u);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) o[y][x] = 0.f;
-        }
-        size_t at[kTake];
-#pragma unroll
-        for (int y = 0; y < kTake; ++y) {
-          const int ry = min(r + y, rows - 1);
-          at[y] = at1 + (size_t)ry * D + (size_t)((g0 + ry) / p.G) * wrap;
-          if (p.gate) {
-#pragma unroll
-            for (int e = 0; e < kH; ++e) gate[y * kH + e] = *reinterpret_cast<const uint2*>(p.gate + at[y] + e * 128);
-          }
-        }
-        for (int k = c0 + piece; k <= c1; k += 8) {
-          // two partials' values on their way before the first is used; the second may be none
-          const bool two = k + 4 <= c1;
-          const float *q0 = part(k, k == c0), *q1 = two ? part(k + 4, false) : q0;
-          float m[2][kTake];
-          float4 v[2][kTake * kH];
-#pragma unroll
-          for (int y = 0; y < kTake; ++y) {
-            const int ry = min(r + y, rows - 1);
-            m[0][y] = __ldcg(q0 + roff + ry);
-            m[1][y] = __ldcg(q1 + roff + ry);
-#pragma unroll
-            for (int e = 0; e < kH; ++e) {
-              v[0][y * kH + e] = __ldcg(reinterpret_cast<const float4*>(q0 + head + (ry * kH + e) * 128 + col));
-              v[1][y * kH + e] = __ldcg(reinterpret_cast<const float4*>(q1 + head + (ry * kH + e) * 128 + col));
-            }
-          }
-#pragma unroll
-          for (int z = 0; z < 2; ++z)
-#pragma unroll
-            for (int y = 0; y < kTake; ++y) {
-              const float w = m[z][y] == -INFINITY || (z && !two) ? 0.f : ex2(m[z][y] - fin[roff + min(r + y, rows - 1)]);
-#pragma unroll
-              for (int e = 0; e < kH; ++e) {
-                float* t = o[y * kH + e];
-                const float4 u = v[z][y * kH + e];
-                if (z == 0 || two) {
-                  t[0] = fmaf(w, u.x, t[0]);
-                  t[1] = fmaf(w, u.y, t[1]);
-                  t[2] = fmaf(w, u.z, t[2]);
-                  t[3] = fmaf(w, u.w, t[3]);
-                }
-              }
-            }
-        }
-        __syncwarp();
-#pragma unroll
-        for (int y = 0; y < kTake * kH; ++y) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            o[y][x] += __shfl_xor_sync(0xffffffffu, o[y][x], 8);
-            o[y][x] += __shfl_xor_sync(0xffffffffu, o[y][x], 16);
-          }
-          const int ry = r + y / kH;
-          if (piece == y && ry < rows) {
-            const float f = fin[kRows + roff + ry];
-            uint32_t w[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const uint32_t gx = x & 1 ? (x < 2 ? gate[y].x : gate[y].y) >> 16 : (x < 2 ? gate[y].x : gate[y].y) & 0xffff;
-              w[x] = p.gate ? gated(o[y][x] * f, gx) : f32_to_bf16(o[y][x] * f);
-            }
-            *reinterpret_cast<uint2*>(p.out + at[y / kH] + (y % kH) * 128) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-          }
+        reinterpret_cast<int*>(mine)[2 * a.rows + og] = bad;
+        if (C::kOutGroups == 1) reinterpret_cast<int*>(mine)[2 * a.rows + 1] = 0;
+        if (s.t0 == 0 && og == 0) {
+          const int ctas = (int)min((long long)gridDim.x, plan.total);
+          static_cast<Desc*>(p.workspace)[blockIdx.x] = Desc{1, s.n, s.u, cta_of(s.first + s.tiles - 1, plan.total, ctas)};
         }
       }
-      sync_group(bar);  // fin is read before the next segment's
     }
   }
   umma::fence_before_sync();
