@@ -118,14 +118,23 @@ def header_symbols() -> list[str]:
 
 # ---------------------------------------------------------------- marshalling helpers
 
+# A call's host time is mostly these checks (a decode-sized kernel runs for a few microseconds), so the common
+# case of each is one expression; addresses go to ctypes as integers.
+
 def _ptr(t: torch.Tensor | None):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+# the current stream's handle without building a torch.cuda.Stream around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _rows(t, name: str, shape):
@@ -135,17 +144,20 @@ def _rows(t, name: str, shape):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (libgdn has no CPU path)")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must have dtype {torch.bfloat16}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     st, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name}'s head rows must be contiguous")
-    return _ptr(t), st, sh
+    return t.data_ptr(), st, sh
 
 
 def _need(t, name: str, dtype, shape=None, optional: bool = False):
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and (
+            shape is None or t.shape == shape):
+        return
     if t is None:
         if optional:
             return
@@ -510,8 +522,7 @@ def gdn_tree_attention_workspace_bytes(cache, num_seqs: int, num_pos: int, num_q
 def gdn_tree_attention(cache, q, block_table, ctx_len, scale, out, num_pos: int = 1, tree_mask=None, gate=None,
                        workspace=None, dev_err=None, stream=None):
     """Attention of num_pos drafted tokens per request (q [N * num_pos, Hq, D]; 1: a decode step) over the cache.
-    tree_mask [N, num_pos] int64, bit i of a node's word: it sees node i; None: a chain. workspace: zero-filled
-    before its first use (each call resets its tickets)."""
+    tree_mask [N, num_pos] int64, bit i of a node's word: it sees node i; None: a chain."""
     N, max_pages = block_table.shape
     shape = (N * num_pos, q.shape[1], cache.head_dim)
     _need(q, "q", torch.bfloat16, shape)
@@ -524,8 +535,6 @@ def gdn_tree_attention(cache, q, block_table, ctx_len, scale, out, num_pos: int 
     if workspace is None:
         need = gdn_tree_attention_workspace_bytes(cache, N, num_pos, shape[1])
         workspace = _scratch(need, q.device, stream)
-        with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.current_stream()):
-            workspace.zero_()
     _check(_lib.gdn_tree_attention(ctypes.byref(cache), _ptr(q), _ptr(block_table), max_pages, _ptr(ctx_len),
                                    _ptr(tree_mask), _ptr(gate), float(scale), _ptr(out), N, int(num_pos), shape[1],
                                    _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_err),

@@ -554,12 +554,10 @@ gdn_status gdn_qk_norm_rope(const uint16_t *q, int64_t q_stride_t, int64_t q_str
  *   gate      [N*P][Hq][D] bf16 or NULL
  *   out       [N*P][Hq][D] bf16; may be q or gate itself
  *   num_pos   1 <= P <= 64;  Hq / Hkv <= 64;  scale finite
- *   workspace partial sums of requests that several CTAs share, and their
- *             tickets: gdn_tree_attention_workspace_bytes(...) bytes, 256-byte
- *             aligned and ZERO-FILLED before its first use; every call that
- *             completes leaves the tickets at zero, so it is reusable without
- *             clearing (after a call that reports GDN_DEVERR_TIMEOUT, clear it
- *             again). Calls sharing one workspace must not overlap.
+ *   workspace partial sums of requests that several CTAs share:
+ *             gdn_tree_attention_workspace_bytes(...) bytes, 256-byte aligned.
+ *             Contents need not be zeroed and are clobbered. Calls sharing one
+ *             workspace must not overlap.
  *   dev_err   GDN_DEVERR_TIMEOUT too, if a bounded wait inside the kernel ran out
  * Pointers 16-byte aligned.
  */

@@ -206,6 +206,24 @@ def test_cache_write_codes_of_special_rows(b):
     assert torch.equal(pool.v[0, 0, :5].cpu(), k)
 
 
+def test_cache_write_codes_are_those_of_the_division(b):
+    """Every pair of bf16 significands (value, row's largest) at sixteen distances of their exponents: the codes of the
+    quotients rounded to fp32, ties among them."""
+    top, j = torch.arange(128, device="cuda"), torch.arange(128, device="cuda")
+    row = torch.cat([torch.stack([(1 + j / 128) * 2.0 ** -off * (-1) ** (j + m) for m in range(128)]) for off in
+                     range(1, 17)])
+    x = torch.zeros(16 * 128, 1, 256, device="cuda")
+    x[:, 0, :128] = row
+    x[:, 0, 200] = (1 + top / 128).repeat(16)
+    x = x.to(torch.bfloat16)
+    pool = R.Pool(x.shape[0] // 16, 1, 16, 256, "e4m3", seed=1)
+    b.gdn_kv_cache_write(pool.handle(b), x, x, torch.arange(x.shape[0], dtype=torch.int32, device="cuda"))
+    codes, scale = R.quantise(x.float())
+    got = pool.k.reshape(-1, 1, 256).cpu()
+    assert torch.equal(pool.k_scale.reshape(-1, 1).cpu(), scale)
+    assert torch.equal(got, codes), torch.nonzero(got != codes)[:5].tolist()
+
+
 def test_cache_flags_bad_slots_pages_and_offsets(b, err):
     pool = R.Pool(4, 2, 16, 128, "e4m3", seed=1)
     c = pool.handle(b)
