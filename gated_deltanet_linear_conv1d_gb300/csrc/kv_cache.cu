@@ -20,11 +20,17 @@ constexpr float kE4m3Max = 448.f;
 constexpr float kMinAmax = 1e-12f;
 constexpr int kMaxTokens = 16;  // tokens per block
 
+__device__ __forceinline__ uint32_t bf16x2(float2 x) {  // x.x in the low half
+  const __nv_bfloat162 v = __floats2bfloat162_rn(x.x, x.y);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 __device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
-  uint32_t w[4];
+  return make_uint4(bf16x2(x[0]), bf16x2(x[1]), bf16x2(x[2]), bf16x2(x[3]));
+}
+__device__ __forceinline__ void unpack8(const uint2 (&u)[2], float2 (&x)[4]) {
+  const uint32_t w[4] = {u[0].x, u[0].y, u[1].x, u[1].y};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = (uint32_t)f32_to_bf16(x[i].x) | ((uint32_t)f32_to_bf16(x[i].y) << 16);
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  for (int e = 0; e < 4; ++e) x[e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
 }
 
 // Two fp32 values to two E4M3 codes (round to nearest even, saturate); lo lands in the low byte.
@@ -80,62 +86,212 @@ __device__ __forceinline__ uint2 codes(const float2 (&x)[4], float s) {
 
 enum { kNoCache = 0, kBf16Cache = 1, kE4m3Cache = 2 };
 
-// The rows of a block's tokens, query heads, key heads and value heads of a token one after the other: a row group
-// of D / 8 lanes takes kRows rows at a time, every kGroups-th of one token's, or, where a token has no more than
-// kGroups of them, its one of kRows tokens. The next rows are on their way while these are worked on: with one batch
-// in flight the loads, the arithmetic and the stores took turns (192 us for 16,384 tokens of 24 + 4 heads of 256).
-// kNorm: the head norm, the rotation and the dense outputs; without it the rows go to the cache as they are.
-// The angles of a token are the same for all its heads: a thread per (token, frequency) puts their cosine and sine
-// into shared memory first. A position times a frequency is taken in turns, in 64-bit fixed point (one turn = 2^64),
-// where the whole turns fall away by themselves: the error is the frequency's rounding to 2^-64 turns times the
-// position, 2^-33 turns at the largest one.
-template <int D, bool kNorm, int kCache>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const RopeArgs p, const KvArgs c, int tokens_per_block) {
+enum { kPartial = 0, kWhole = 1, kInterleaved = 2 };  // up to D / 2 rotated dimensions, all D, neighbours as pairs
+
+// The query rows (kQuery) or the key and value rows of a block's T tokens, H of them a token. D / 8 lanes hold a row:
+// lane l has four values from 4 l on, and four from D / 2 + 4 l on. A row group keeps its head over the tokens, so that
+// what goes by the head (addresses, gains) is found once. A batch is four rows, loaded before the first is worked on:
+// every kGroups-th head of one token (kMany), or, where a token has no more rows than there are groups, one head of
+// four tokens.
+// A rotated value is inv (x A + x' B): x' the other value of its pair, inv the row's 1 / sqrt(mean + eps), A the cosine
+// times x's gain, B the signed sine times the gain of x'. Up to D / 2 rotated dimensions are in the first four values of
+// the first lanes, and pairs half a rotation apart are in lanes l and l ^ (half / 4); with all D rotated they are a lane's
+// first and second four.
+template <int D, bool kNorm, int kCache, bool kQuery, bool kMany, int kRot>
+__device__ __forceinline__ void rows_pass(const RopeArgs& p, const KvArgs& c, const float2* turn, int t0, int T, int H) {
   constexpr int kLanes = D / 8, kGroups = kThreads / kLanes, kRows = 4;
+  const int tid = threadIdx.x, l = tid % kLanes, group = tid / kLanes;
+  const int half = p.rotary / 2;
+  const bool turns = kNorm && l * 4 < (kRot == kWhole ? D / 2 : p.rotary);
+  const bool low = kRot == kWhole || (l * 4 & half) == 0;  // the lane's first four are their pairs' first values
+
+  for (int h0 = 0; h0 < H; h0 += kGroups * (kMany ? kRows : 1)) {
+    const int h = h0 + group;
+    const bool value = !kQuery && h >= c.Hkv, live = h < H;
+    const int hh = value ? h - c.Hkv : h;
+    const int64_t st = kQuery ? p.q_t : value ? p.v_t : p.k_t;
+    // row i of a batch: i steps on from the first
+    const uint16_t* src = (kQuery ? p.q + hh * p.q_h : value ? p.v + hh * p.v_h : p.k + hh * p.k_h) + t0 * st + l * 4;
+    const int64_t step = kMany ? kGroups * p.q_h : st;
+    uint16_t* dst = kQuery ? p.q_out : value ? nullptr : p.k_out;  // dense output, or none
+    const int64_t out_t = (int64_t)(kQuery ? p.Hq : c.Hkv) * D, out_step = kMany ? kGroups * D : out_t;
+    if (dst) dst += t0 * out_t + hh * D + l * 4;
+    float2 gain[4], other_gain[2];
+    if constexpr (kNorm) {
+      const float* gamma = kQuery ? p.q_gamma : p.k_gamma;
+      const float4 g0 = __ldg(reinterpret_cast<const float4*>(gamma + l * 4));
+      const float4 g1 = __ldg(reinterpret_cast<const float4*>(gamma + D / 2 + l * 4));
+      const float4 o = __ldg(reinterpret_cast<const float4*>(gamma + (kRot == kPartial && turns ? (l * 4) ^ half : l * 4)));
+      gain[0] = make_float2(g0.x, g0.y);
+      gain[1] = make_float2(g0.z, g0.w);
+      gain[2] = make_float2(g1.x, g1.y);
+      gain[3] = make_float2(g1.z, g1.w);
+      other_gain[0] = make_float2(o.x, o.y);
+      other_gain[1] = make_float2(o.z, o.w);
+    }
+    for (int tl = 0; tl < T; tl += kMany ? 1 : kRows) {
+      uint2 raw[kRows][2];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        raw[i][0] = raw[i][1] = make_uint2(0u, 0u);
+        if (kMany ? h + i * kGroups < H : live && tl + i < T) {
+          raw[i][0] = *reinterpret_cast<const uint2*>(src + i * step);
+          raw[i][1] = *reinterpret_cast<const uint2*>(src + i * step + D / 2);
+        }
+      }
+      src += kMany ? st : kRows * st;
+      float inv[kRows];
+      if constexpr (kNorm) {
+        // the sums of the rows' squares, each lane's part in `inv` first
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          float2 x[4], ss = make_float2(0.f, 0.f);
+          unpack8(raw[i], x);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ss = __ffma2_rn(x[e], x[e], ss);
+          inv[i] = ss.x + ss.y;
+        }
+        // four rows in one butterfly: after two steps a lane has one row's sum, after the rest its whole
+        const bool b1 = l & (kLanes / 2), b2 = l & (kLanes / 4);
+        float a0 = b1 ? inv[2] : inv[0], a1 = b1 ? inv[3] : inv[1];
+        a0 += __shfl_xor_sync(0xffffffffu, b1 ? inv[0] : inv[2], kLanes / 2);
+        a1 += __shfl_xor_sync(0xffffffffu, b1 ? inv[1] : inv[3], kLanes / 2);
+        float a = b2 ? a1 : a0;
+        a += __shfl_xor_sync(0xffffffffu, b2 ? a0 : a1, kLanes / 4);
+#pragma unroll
+        for (int m = kLanes / 8; m > 0; m >>= 1) a += __shfl_xor_sync(0xffffffffu, a, m);
+        a = rsqrtf(a * (1.f / D) + p.eps);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)  // row i's is in the lanes with bits i / 2 and i % 2
+          inv[i] = __shfl_sync(0xffffffffu, a, (tid & 31) - l + (i >> 1) * (kLanes / 2) + (i & 1) * (kLanes / 4));
+      }
+      float2 A[4], B[4];
+      auto coefficients = [&](int ti) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) A[e] = gain[e], B[e] = make_float2(0.f, 0.f);
+        if (!turns) return;
+        if constexpr (kRot == kInterleaved) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (e < 2 || p.rotary == D) {
+              const float2 w = turn[ti * half + (e < 2 ? 0 : D / 4) + l * 2 + (e & 1)];
+              B[e] = make_float2(-w.y * gain[e].y, w.y * gain[e].x);
+              A[e] = make_float2(w.x * gain[e].x, w.x * gain[e].y);
+            }
+        } else {
+          const float4* w = reinterpret_cast<const float4*>(turn + ti * half + (l * 4 & (half - 1)));
+          const float sign = low ? -1.f : 1.f;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float4 v = w[e];
+            const float2 co = make_float2(v.x, v.z), si = make_float2(v.y, v.w);
+            A[e] = __fmul2_rn(gain[e], co);
+            B[e] = __fmul2_rn(kRot == kWhole ? gain[2 + e] : other_gain[e], make_float2(sign * si.x, sign * si.y));
+            if (kRot == kWhole) {
+              A[2 + e] = __fmul2_rn(gain[2 + e], co);
+              B[2 + e] = __fmul2_rn(gain[e], si);
+            }
+          }
+        }
+      };
+      if (kNorm && kMany) coefficients(tl);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int ti = tl + (kMany ? 0 : i), hi = h + (kMany ? i * kGroups : 0);
+        // nothing left for any group: the shuffles take whole warps
+        if (ti >= T || hi - group >= H) break;
+        float2 x[4];
+        unpack8(raw[i], x);
+        if constexpr (kNorm) {
+          uint2 o = raw[i][0];
+          if (kRot == kPartial && half > 0) {
+            const int from = (tid & 31) ^ (turns ? half / 4 : 0);
+            o.x = __shfl_sync(0xffffffffu, o.x, from);
+            o.y = __shfl_sync(0xffffffffu, o.y, from);
+          }
+          if (!value) {
+            if (!kMany) coefficients(ti);
+            float2 y[4];
+            if constexpr (kRot == kInterleaved) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[e] = make_float2(x[e].y, x[e].x);
+            } else if constexpr (kRot == kWhole) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[e] = x[e ^ 2];
+            } else {
+              const uint2 both[2] = {o, o};
+              unpack8(both, y);
+            }
+            const float2 f = make_float2(inv[i], inv[i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[e] = __fmul2_rn(x[e], A[e]);
+              if (e < 2 || kRot != kPartial) x[e] = turns ? __ffma2_rn(y[e], B[e], x[e]) : x[e];
+              x[e] = __fmul2_rn(x[e], f);
+            }
+            if (dst && (kMany ? hi < H : live)) {
+              uint16_t* to = dst + i * out_step;
+              *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2(x[0]), bf16x2(x[1]));
+              *reinterpret_cast<uint2*>(to + D / 2) = make_uint2(bf16x2(x[2]), bf16x2(x[3]));
+            }
+          }
+        }
+        if constexpr (kCache != kNoCache && !kQuery) {
+          const int to = live ? __ldg(p.kv_slot + t0 + ti) : -1;
+          const bool store = to >= 0 && to < c.slots;
+          if (to >= c.slots && l == 0) report(p.dev_err, GDN_DEVERR_SLOT);
+          if (!__any_sync(0xffffffffu, store)) continue;
+          const int page = store ? to / c.page : 0, row = store ? to - page * c.page : 0;
+          const size_t at = ((size_t)page * c.Hkv + hh) * c.page + row;
+          if constexpr (kCache == kE4m3Cache) {
+            // a / 448, rounded once, as in codes()
+            constexpr float kInv = 1.f / kE4m3Max;
+            const float a = fmaxf(row_amax<kLanes>(x), kMinAmax), s0 = a * kInv;
+            const float s = a < INFINITY ? fmaf(fmaf(-s0, kE4m3Max, a), kInv, s0) : a;
+            if (store) {
+              const uint2 w = codes(x, s);
+              uint8_t* pool = static_cast<uint8_t*>(value ? c.v : c.k) + at * D + l * 4;
+              *reinterpret_cast<uint32_t*>(pool) = w.x;
+              *reinterpret_cast<uint32_t*>(pool + D / 2) = w.y;
+              if (l == 0) (value ? c.v_scale : c.k_scale)[at] = s;
+            }
+          } else if (store) {
+            uint16_t* pool = static_cast<uint16_t*>(value ? c.v : c.k) + at * D + l * 4;
+            *reinterpret_cast<uint2*>(pool) = make_uint2(bf16x2(x[0]), bf16x2(x[1]));
+            *reinterpret_cast<uint2*>(pool + D / 2) = make_uint2(bf16x2(x[2]), bf16x2(x[3]));
+          }
+        }
+      }
+      if (dst) dst += kMany ? out_t : kRows * out_t;
+    }
+  }
+}
+
+// blockIdx.y 0: the key and value rows of the block's tokens, 1: their query rows.
+// kNorm: the head norm, the rotation and the dense outputs; without it the rows go to the cache as they are.
+// The angles: a thread per (token, frequency) puts their cosine and sine into shared memory first. A position times a
+// frequency is taken in turns, in 64-bit fixed point (one turn = 2^64), where the whole turns fall away by themselves:
+// the error is the frequency's rounding to 2^-64 turns times the position, 2^-33 turns at the largest one.
+// What bounds it: the issue of instructions, close to HBM's bytes, at many tokens; the launch and the angles' chain at
+// few. 16,384 tokens of 24 + 4 heads of 256 into a bf16 cache, 571 MB: 116 us with 80 registers a thread (three blocks
+// an SM; 133 us with two and 124 us with four), 192 us when addresses and gains were found row by row, with the
+// compiler's division, 220 instructions a row. Holding a second batch in registers costs more blocks than it hides.
+template <int D, bool kNorm, int kCache, int kRot>
+__global__ void __launch_bounds__(kThreads, 3) rows_kernel(const RopeArgs p, const KvArgs c, int tokens_per_block) {
   __shared__ uint64_t freq[kNorm ? D / 2 : 1];
   extern __shared__ float2 turn[];  // [tokens][half]
-  const int tid = threadIdx.x, l = tid % kLanes, group = tid / kLanes;
+  constexpr int kGroups = kThreads / (D / 8);
   const int t0 = blockIdx.x * tokens_per_block;
   const int T = min(tokens_per_block, p.T - t0);
-  const int half = p.rotary / 2;
-  const bool rotate = kNorm && half > 0;
-  // the lane's eight dimensions: rotated or not, and where the other dimensions of their pairs are
-  const bool turns = rotate && l * 8 < p.rotary;
-  const bool low = l < half / 8;
-  const int partner = (tid & 31) + (!turns || p.interleaved ? 0 : low ? half / 8 : -(half / 8));
-  const int Hq = kNorm && p.q ? p.Hq : 0, Hk = Hq + c.Hkv;
-  const int per_token = Hk + (p.v ? c.Hkv : 0);
-  const bool many = per_token > kGroups;              // rows of one token in a batch, else of kRows tokens
-  const int step_h = many ? kGroups : 0, step_t = many ? 0 : 1;
-
-  // row i of the batch at (tl, h0): token tl + i * step_t, head h0 + i * step_h + group
-  auto fetch = [&](int tl, int h0, uint4 (&raw)[kRows], int (&slot)[kRows]) {
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int ti = tl + i * step_t, h = h0 + i * step_h + group;
-      raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      slot[i] = -1;
-      if (ti < T && h < per_token) {
-        const int64_t t = t0 + ti;
-        const uint16_t* src = h < Hq   ? p.q + t * p.q_t + h * p.q_h
-                              : h < Hk ? p.k + t * p.k_t + (h - Hq) * p.k_h
-                                       : p.v + t * p.v_t + (h - Hk) * p.v_h;
-        raw[i] = *reinterpret_cast<const uint4*>(src + l * 8);
-        if (kCache != kNoCache && h >= Hq) slot[i] = p.kv_slot[t];
-      }
-    }
-  };
-  uint4 raw[kRows];
-  int slot[kRows];
-  fetch(0, 0, raw, slot);
   if constexpr (kNorm) {
-    if (rotate) {
-      for (int i = tid; i < half; i += kThreads) {
+    const int half = p.rotary / 2;
+    if (half > 0) {
+      for (int i = threadIdx.x; i < half; i += kThreads) {
         const double f = p.inv_freq[i] * 0.15915494309189535;  // 1 / (2 pi): turns per position
         freq[i] = __double2ull_rn((f - floor(f)) * 18446744073709551616.0);
       }
       __syncthreads();
-      for (int i = tid; i < T * half; i += kThreads) {
+      for (int i = threadIdx.x; i < T * half; i += kThreads) {
         const int64_t pos = p.positions[t0 + i / half];
         // the upper 32 bits as a signed number: half turns in [-1, 1)
         const int32_t top = (int32_t)(((uint64_t)pos * freq[i % half]) >> 32);
@@ -145,129 +301,13 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RopeArgs p, const 
       }
       __syncthreads();
     }
-  }
-  for (int tl = 0, h0 = 0; tl < T;) {
-    const int tl_now = tl, h0_now = h0;
-    if (many) {
-      h0 += kGroups * kRows;
-      if (h0 >= per_token) h0 = 0, ++tl;
-    } else {
-      tl += kRows;
-    }
-    uint4 next[kRows];
-    int next_slot[kRows];
-    if (tl < T) fetch(tl, h0, next, next_slot);
-    float inv[kRows];
-    if constexpr (kNorm) {
-      // the sums of the rows' squares, each lane's part in `inv` first
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-        float2 ss = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 x = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
-          ss = __ffma2_rn(x, x, ss);
-        }
-        inv[i] = ss.x + ss.y;
-      }
-      // four rows in one butterfly: after two steps a lane has one row's sum, after the rest its whole
-      const bool b1 = l & (kLanes / 2), b2 = l & (kLanes / 4);
-      float a0 = b1 ? inv[2] : inv[0], a1 = b1 ? inv[3] : inv[1];
-      a0 += __shfl_xor_sync(0xffffffffu, b1 ? inv[0] : inv[2], kLanes / 2);
-      a1 += __shfl_xor_sync(0xffffffffu, b1 ? inv[1] : inv[3], kLanes / 2);
-      float a = b2 ? a1 : a0;
-      a += __shfl_xor_sync(0xffffffffu, b2 ? a0 : a1, kLanes / 4);
-#pragma unroll
-      for (int m = kLanes / 8; m > 0; m >>= 1) a += __shfl_xor_sync(0xffffffffu, a, m);
-      a = rsqrtf(a * (1.f / D) + p.eps);
-#pragma unroll
-      for (int i = 0; i < kRows; ++i)  // row i's is in the lanes with bits i / 2 and i % 2
-        inv[i] = __shfl_sync(0xffffffffu, a, (tid & 31) - l + (i >> 1) * (kLanes / 2) + (i & 1) * (kLanes / 4));
-    }
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int ti = tl_now + i * step_t, h = h0_now + i * step_h + group;
-      // nothing left for any group: the shuffles take whole warps
-      if (ti >= T || h - group >= per_token) break;
-      const int64_t t = t0 + ti;
-      const bool live = h < per_token, is_q = h < Hq, is_v = h >= Hk;
-      const int hk = is_q ? 0 : is_v ? h - Hk : h - Hq;
-      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-      float2 x[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
-      if constexpr (kNorm) {
-        uint32_t o[4];
-        if (rotate && !p.interleaved) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = __shfl_sync(0xffffffffu, w[e], partner);
-        }
-        if (live && !is_v) {
-          const float* gamma = is_q ? p.q_gamma : p.k_gamma;
-          const float4 g0 = __ldg(reinterpret_cast<const float4*>(gamma) + 2 * l);
-          const float4 g1 = __ldg(reinterpret_cast<const float4*>(gamma) + 2 * l + 1);
-          const float2 f = make_float2(inv[i], inv[i]);
-          x[0] = __fmul2_rn(__fmul2_rn(x[0], f), make_float2(g0.x, g0.y));
-          x[1] = __fmul2_rn(__fmul2_rn(x[1], f), make_float2(g0.z, g0.w));
-          x[2] = __fmul2_rn(__fmul2_rn(x[2], f), make_float2(g1.x, g1.y));
-          x[3] = __fmul2_rn(__fmul2_rn(x[3], f), make_float2(g1.z, g1.w));
-          if (turns) {
-            if (p.interleaved) {
-              const float4* cs = reinterpret_cast<const float4*>(turn + ti * half + l * 4);
-#pragma unroll
-              for (int e = 0; e < 4; e += 2) {
-                const float4 w2 = cs[e / 2];  // two pairs' cosine and sine
-                const float2 u = x[e], v = x[e + 1];
-                x[e] = make_float2(u.x * w2.x - u.y * w2.y, u.y * w2.x + u.x * w2.y);
-                x[e + 1] = make_float2(v.x * w2.z - v.y * w2.w, v.y * w2.z + v.x * w2.w);
-              }
-            } else {
-              const float4* pg = reinterpret_cast<const float4*>(gamma) + 2 * (low ? l + half / 8 : l - half / 8);
-              const float4 p0 = __ldg(pg), p1 = __ldg(pg + 1);
-              const float2 g[4] = {make_float2(p0.x, p0.y), make_float2(p0.z, p0.w), make_float2(p1.x, p1.y),
-                                   make_float2(p1.z, p1.w)};
-              const float4* cs = reinterpret_cast<const float4*>(turn + ti * half + (low ? l : l - half / 8) * 8);
-              const float sign = low ? -1.f : 1.f;  // a' = a cos - b sin, b' = b cos + a sin
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float4 w2 = cs[e];
-                const float2 other = __fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(o[e] << 16),
-                                                                       __uint_as_float(o[e] & 0xffff0000u)), f), g[e]);
-                x[e] = __ffma2_rn(x[e], make_float2(w2.x, w2.z),
-                                  __fmul2_rn(other, make_float2(sign * w2.y, sign * w2.w)));
-              }
-            }
-          }
-          if (is_q)
-            *reinterpret_cast<uint4*>(p.q_out + ((size_t)t * p.Hq + h) * D + l * 8) = pack8(x);
-          else if (p.k_out)
-            *reinterpret_cast<uint4*>(p.k_out + ((size_t)t * c.Hkv + hk) * D + l * 8) = pack8(x);
-        }
-      }
-      if constexpr (kCache != kNoCache) {
-        const bool store = live && !is_q && slot[i] >= 0 && slot[i] < c.slots;
-        if (slot[i] >= c.slots && l == 0) report(p.dev_err, GDN_DEVERR_SLOT);
-        if (!__any_sync(0xffffffffu, store)) continue;
-        const int page = store ? slot[i] / c.page : 0, row = store ? slot[i] - page * c.page : 0;
-        const size_t at = ((size_t)page * c.Hkv + hk) * c.page + row;
-        if constexpr (kCache == kE4m3Cache) {
-          const float s = __fdiv_rn(fmaxf(row_amax<kLanes>(x), kMinAmax), kE4m3Max);
-          if (store) {
-            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? c.v : c.k) + at * D + l * 8) = codes(x, s);
-            if (l == 0) (is_v ? c.v_scale : c.k_scale)[at] = s;
-          }
-        } else if (store) {
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? c.v : c.k) + at * D + l * 8) = pack8(x);
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      raw[i] = next[i];
-      slot[i] = next_slot[i];
+    if (blockIdx.y == 1) {
+      if (p.Hq > kGroups) rows_pass<D, true, kNoCache, true, true, kRot>(p, c, turn, t0, T, p.Hq);
+      else rows_pass<D, true, kNoCache, true, false, kRot>(p, c, turn, t0, T, p.Hq);
+      return;
     }
   }
+  rows_pass<D, kNorm, kCache, false, false, kRot>(p, c, turn, t0, T, c.Hkv + (p.v ? c.Hkv : 0));
 }
 
 // Cached rows back to bf16: a block takes kReadTokens output tokens, a thread 16
@@ -343,17 +383,24 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs p, const 
 
 namespace {
 
+template <int D, int kRot>
+void run_norm(const RopeArgs& a, const KvArgs& c, dim3 grid, int per, cudaStream_t stream) {
+  const size_t smem = (size_t)per * (a.rotary / 2) * sizeof(float2);
+  if (!c.k) rows_kernel<D, true, kNoCache, kRot><<<grid, kThreads, smem, stream>>>(a, c, per);
+  else if (c.e4m3) rows_kernel<D, true, kE4m3Cache, kRot><<<grid, kThreads, smem, stream>>>(a, c, per);
+  else rows_kernel<D, true, kBf16Cache, kRot><<<grid, kThreads, smem, stream>>>(a, c, per);
+}
+
 template <int D>
-void run_rows(const RopeArgs& a, const KvArgs& c, bool norm, unsigned grid, int per, cudaStream_t stream) {
-  const int cache = !c.k ? kNoCache : c.e4m3 ? kE4m3Cache : kBf16Cache;
-  const size_t smem = norm ? (size_t)per * (a.rotary / 2) * sizeof(float2) : 0;
+void run_rows(const RopeArgs& a, const KvArgs& c, bool norm, dim3 grid, int per, cudaStream_t stream) {
   if (norm) {
-    if (cache == kNoCache) rows_kernel<D, true, kNoCache><<<grid, kThreads, smem, stream>>>(a, c, per);
-    else if (cache == kBf16Cache) rows_kernel<D, true, kBf16Cache><<<grid, kThreads, smem, stream>>>(a, c, per);
-    else rows_kernel<D, true, kE4m3Cache><<<grid, kThreads, smem, stream>>>(a, c, per);
+    if (a.interleaved) run_norm<D, kInterleaved>(a, c, grid, per, stream);
+    else if (a.rotary == D) run_norm<D, kWhole>(a, c, grid, per, stream);
+    else run_norm<D, kPartial>(a, c, grid, per, stream);
+  } else if (c.e4m3) {
+    rows_kernel<D, false, kE4m3Cache, kPartial><<<grid, kThreads, 0, stream>>>(a, c, per);
   } else {
-    if (cache == kBf16Cache) rows_kernel<D, false, kBf16Cache><<<grid, kThreads, smem, stream>>>(a, c, per);
-    else rows_kernel<D, false, kE4m3Cache><<<grid, kThreads, smem, stream>>>(a, c, per);
+    rows_kernel<D, false, kBf16Cache, kPartial><<<grid, kThreads, 0, stream>>>(a, c, per);
   }
 }
 
@@ -363,7 +410,7 @@ cudaError_t launch_rows(const RopeArgs& a, const KvArgs& c, bool norm, int D, cu
   // enough blocks for every SM before a block takes several tokens
   int per = 1;
   while (per < kMaxTokens && a.T / (2 * per) >= 4 * 152) per *= 2;
-  const unsigned grid = (unsigned)((a.T + per - 1) / per);
+  const dim3 grid((unsigned)((a.T + per - 1) / per), norm && a.q ? 2 : 1, 1);
   if (D == 256) run_rows<256>(a, c, norm, grid, per, stream);
   else run_rows<128>(a, c, norm, grid, per, stream);
   return cudaGetLastError();

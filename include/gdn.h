@@ -516,8 +516,8 @@ gdn_status gdn_kv_cache_read(const gdn_kv_cache *cache, const int32_t *block_tab
  *              their final slots, bit for bit
  *   q_gamma, k_gamma [D] fp32, 16-byte aligned;  eps >= 0 and finite
  *   positions  [T] int32;  inv_freq [rotary_dim / 2] fp64, radians per position
- *   rotary_dim a multiple of 16, 0 <= rotary_dim <= D (0: no rotation, positions
- *              and inv_freq may be NULL)
+ *   rotary_dim a power of two, 16 <= rotary_dim <= D, or 0 (no rotation,
+ *              positions and inv_freq may be NULL)
  *   q_out      [T][Hq][D] bf16;  k_out [T][Hkv][D] bf16 or NULL: rounded once,
  *              16-byte aligned. In place (q_out = q, dense) is allowed.
  *   cache      or NULL (then v and kv_slot too, and k_out is required): the

@@ -89,6 +89,7 @@ def test_norm_rope_arguments(b):
                dict(cc=ref, v=P, slot=P, d=128, rot=64), dict(cc=ref, v=ODD, slot=P)):
         assert rope(**kw) == b.GDN_ERR_INVALID_ARG, kw
     assert rope(d=64) == b.GDN_ERR_UNSUPPORTED
+    assert rope(rot=96) == b.GDN_ERR_UNSUPPORTED  # no power of two
     assert rope(T=0) == b.GDN_OK
 
 
