@@ -138,7 +138,8 @@ __device__ int g_unit_counter[kSchedSlots * 2];
 // kTree: position q continues from position parent[q] (-1: the live state). A
 // row's registers hold the last position's state; where the parent is another
 // one, the thread that holds the row loads it again, from the staged live state
-// or from the parent's checkpoint, which the same thread has written.
+// or from the parent's checkpoint, which the same thread has written (one node
+// ahead: a trip to L2 next to the stream takes as long as a node).
 template <bool kOne, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const StepArgs p, const int units, const int sched) {
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -434,21 +435,23 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const StepArgs p, c
           const int lr = warp * kRowsPerWarp + sub;
           const int ri = hh * kHalfRows + lr;  // row of the head's state
           const float* srow = stage + s * kHalfFloats + lr * kHeadDim;
-          float4 sv[4];
+          float4 sv[4], again[4];
 #pragma unroll
           for (int m = 0; m < 4; ++m) sv[m] = reinterpret_cast<const float4*>(srow)[cl + 8 * m];
           for (int q = 0; q < P; ++q) {
             if constexpr (kTree) {
               const int from = tap[q * 4 + 3];
               if (from != q - 1) {
-                if (from < 0) {
 #pragma unroll
-                  for (int m = 0; m < 4; ++m) sv[m] = reinterpret_cast<const float4*>(srow)[cl + 8 * m];
-                } else {
-                  const float* prow = p.state + (((size_t)out_slot[from] * p.Hv + h) * kHeadDim + ri) * kHeadDim;
+                for (int m = 0; m < 4; ++m)
+                  sv[m] = from < 0 ? reinterpret_cast<const float4*>(srow)[cl + 8 * m] : again[m];
+              }
+              // the next node's parent, where it is an older node: on its way while this one is worked on
+              const int then = q + 1 < P ? tap[q * 4 + 7] : -1;
+              if (then >= 0 && then != q) {
+                const float* prow = p.state + (((size_t)out_slot[then] * p.Hv + h) * kHeadDim + ri) * kHeadDim;
 #pragma unroll
-                  for (int m = 0; m < 4; ++m) sv[m] = ld_global_v4(prow + 4 * (cl + 8 * m));
-                }
+                for (int m = 0; m < 4; ++m) again[m] = ld_global_v4(prow + 4 * (cl + 8 * m));
               }
             }
             const float a = ab[(g * P + q) * 4 + 0], bb = ab[(g * P + q) * 4 + 1];
@@ -722,6 +725,183 @@ __global__ void __launch_bounds__(1024) split_kernel(const StepArgs p, const int
   cluster_sync_all();  // no CTA leaves while a peer may still read its partial sums
 }
 
+// The same split for the verify of a tree of P nodes in small batches: with a
+// persistent CTA per (request, key head) a single request at 4/12 heads left 148
+// SMs idle. A thread keeps its eighth of a state row in registers from node to
+// node, or loads the parent's again (the live slot's, or a checkpoint that it has
+// written); the nodes' conv inputs stand in shared memory. The live slot is only
+// read, so no CTA waits for another before it writes.
+// grid: units x nsplit CTAs, clusters of nsplit along x; blockDim >= 256 and >= 8 x G x (128 / nsplit)
+__global__ void __launch_bounds__(1024) split_tree_kernel(const StepArgs p, const int nsplit) {
+  constexpr int kRowsMax = kHeadDim;                          // rows of a CTA: G x 128 / nsplit <= 128
+  __shared__ uint16_t xs[kMaxPos][2 * kHeadDim + kRowsMax];   // the nodes' inputs: q, k channels, the rows' v channels
+  __shared__ float qs[kMaxPos][kHeadDim], ks[kMaxPos][kHeadDim];
+  __shared__ float vs[kMaxPos][kRowsMax], os[kMaxPos][kRowsMax];
+  __shared__ float red[kMaxPos][12];                          // |q|^2, |k|^2, k.q: partials of 4 warps
+  __shared__ float rms[kMaxGroup * kMaxPos];                  // this CTA's sum of o^2 per (head, node)
+  __shared__ int tap[kMaxPos][4], to_slot[kMaxPos];
+  const int G = p.G, P = p.P;
+  const int unit = blockIdx.x / nsplit, part = (int)cluster_ctarank();
+  const int n = unit / p.Hk, j = unit % p.Hk;
+  const int rph = kHeadDim / nsplit, r0 = part * rph, nrows = G * rph;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the same for every CTA of the cluster: all of them leave here, or none
+  const int slot = p.slot_idx[n];
+  if (slot < 0) return;  // padding
+  if (!unit_slots_ok<true>(p, n)) {
+    if (part == 0 && tid == 0) report(p.dev_err, unit_slots_ok<false>(p, n) ? GDN_DEVERR_TREE : GDN_DEVERR_SLOT);
+    return;
+  }
+  const uint64_t wpol = l2_policy_evict_first();
+  // ---- this thread's state row (8 lanes per row), loaded first so the loads fly during the conv
+  const bool has_row = tid < nrows * 8;
+  const int rl = tid >> 3, c8 = tid & 7;
+  const int g_row = rl / rph, ri = r0 + rl % rph, h_row = G * j + g_row;
+  auto row_of = [&](int s) { return p.state + (((size_t)s * p.Hv + h_row) * kHeadDim + ri) * kHeadDim; };
+  float4 sv[4], again[4];
+  if (has_row) {
+    const float* live = row_of(slot);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) sv[m] = *reinterpret_cast<const float4*>(live + 4 * (c8 + 8 * m));
+  }
+  if (tid < P) {
+    to_slot[tid] = p.spec_slot[n * P + tid];
+    const int32_t* par = p.parent + n * P;
+    int at = tid, left = 2;  // the newest history entry not yet used
+    for (int i = 0; i < 3; ++i) {
+      if (at >= 0) at = par[at];
+      tap[tid][i] = at >= 0 ? at : -1 - left--;
+    }
+    tap[tid][3] = par[tid];
+  }
+  // channel of a place in xs: q, k, then the rows' value channels
+  auto channel = [&](int k) {
+    return k < kHeadDim       ? j * kHeadDim + k
+           : k < 2 * kHeadDim ? (p.Hk + j) * kHeadDim + k - kHeadDim
+                              : (2 * p.Hk + G * j + (k - 2 * kHeadDim) / rph) * kHeadDim + r0 + (k - 2 * kHeadDim) % rph;
+  };
+  const int places = 2 * kHeadDim + nrows;
+  for (int k = tid; k < places; k += blockDim.x) {
+    const uint16_t* x = p.qkv0 + (size_t)n * P * p.CH + channel(k);
+    for (int q = 0; q < P; ++q) xs[q][k] = x[(size_t)q * p.CH];
+  }
+  __syncthreads();
+  // ---- conv + SiLU; every node's history to its checkpoint (the q, k channels' by the cluster's first CTA)
+  for (int k = tid; k < places; k += blockDim.x) {
+    const int ch = channel(k);
+    const float4 w = __ldg(reinterpret_cast<const float4*>(p.conv_w) + ch);
+    const uint16_t* hl = p.conv_hist + ((size_t)slot * p.CH + ch) * 3;
+    const uint16_t live[3] = {hl[0], hl[1], hl[2]};
+    for (int q = 0; q < P; ++q) {
+      auto input = [&](int at) { return at >= 0 ? xs[at][k] : at == -3 ? live[2] : at == -2 ? live[1] : live[0]; };
+      const uint16_t x0 = xs[q][k], h2 = input(tap[q][0]), h1 = input(tap[q][1]), h0 = input(tap[q][2]);
+      float pre = w.x * bf16_to_f32(x0);
+      pre = fmaf(w.y, bf16_to_f32(h2), pre);
+      pre = fmaf(w.z, bf16_to_f32(h1), pre);
+      pre = fmaf(w.w, bf16_to_f32(h0), pre);
+      const float y = silu(pre);
+      if (k < kHeadDim) qs[q][k] = y;
+      else if (k < 2 * kHeadDim) ks[q][k - kHeadDim] = y;
+      else vs[q][k - 2 * kHeadDim] = y;
+      if (part == 0 || k >= 2 * kHeadDim) {
+        uint16_t* hp = p.conv_hist + ((size_t)to_slot[q] * p.CH + ch) * 3;
+        hp[0] = h1;
+        hp[1] = h2;
+        hp[2] = x0;
+      }
+    }
+  }
+  __syncthreads();
+  for (int k = warp; k < 4 * P; k += blockDim.x >> 5) {
+    const int q = k >> 2, w4 = k & 3;
+    const float xq = qs[q][w4 * 32 + lane], xk = ks[q][w4 * 32 + lane];
+    const float sq = warp_sum(xq * xq), sk = warp_sum(xk * xk), skq = warp_sum(xk * xq);
+    if (lane == 0) {
+      red[q][w4] = sq;
+      red[q][4 + w4] = sk;
+      red[q][8 + w4] = skq;
+    }
+  }
+  __syncthreads();
+  // ---- the nodes' row updates (the same arithmetic as the streaming kernel)
+  for (int q = 0; q < P; ++q) {
+    if (has_row) {
+      const int from = tap[q][3];
+      if (from != q - 1) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) sv[m] = again[m];
+      }
+      const int then = q + 1 < P ? tap[q + 1][3] : q;
+      if (then != q) {
+        const float* prow = row_of(then < 0 ? slot : to_slot[then]);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) again[m] = ld_global_v4(prow + 4 * (c8 + 8 * m));
+      }
+      const float* r = red[q];
+      const float iq = rsqrtf(((r[0] + r[1]) + (r[2] + r[3])) + 1e-12f);
+      const float ik = rsqrtf(((r[4] + r[5]) + (r[6] + r[7])) + 1e-12f);
+      const float kq = ((r[8] + r[9]) + (r[10] + r[11])) * iq * ik;
+      const size_t ai = ((size_t)n * P + q) * p.Hv + h_row;
+      const float a = p.alpha[ai], bb = p.beta[ai];
+      float pk = 0.f, pq = 0.f;
+      float4 kk[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const float4 kr = reinterpret_cast<const float4*>(ks[q])[c8 + 8 * m];
+        const float4 qr = reinterpret_cast<const float4*>(qs[q])[c8 + 8 * m];
+        kk[m] = make_float4(kr.x * ik, kr.y * ik, kr.z * ik, kr.w * ik);
+        const float4 qq = make_float4(qr.x * iq, qr.y * iq, qr.z * iq, qr.w * iq);
+        pk = fmaf(sv[m].x, kk[m].x, pk);
+        pk = fmaf(sv[m].y, kk[m].y, pk);
+        pk = fmaf(sv[m].z, kk[m].z, pk);
+        pk = fmaf(sv[m].w, kk[m].w, pk);
+        pq = fmaf(sv[m].x, qq.x, pq);
+        pq = fmaf(sv[m].y, qq.y, pq);
+        pq = fmaf(sv[m].z, qq.z, pq);
+        pq = fmaf(sv[m].w, qq.w, pq);
+      }
+      // nrows x 8 threads are whole warps (rph >= 16)
+#pragma unroll
+      for (int x = 1; x < 8; x <<= 1) {
+        pk += __shfl_xor_sync(0xffffffffu, pk, x);
+        pq += __shfl_xor_sync(0xffffffffu, pq, x);
+      }
+      const float e = vs[q][rl] - a * pk;
+      const float be = bb * e;
+      float* grow = row_of(to_slot[q]);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        sv[m].x = fmaf(be, kk[m].x, a * sv[m].x);
+        sv[m].y = fmaf(be, kk[m].y, a * sv[m].y);
+        sv[m].z = fmaf(be, kk[m].z, a * sv[m].z);
+        sv[m].w = fmaf(be, kk[m].w, a * sv[m].w);
+        st_global_v4_hint(grow + 4 * (c8 + 8 * m), sv[m], wpol);
+      }
+      if (c8 == 0) os[q][rl] = fmaf(be, kq, a * pq) * kInvSqrtDk;
+    }
+  }
+  __syncthreads();
+  for (int k = warp; k < G * P; k += blockDim.x >> 5) {  // this CTA's part of each (head, node)'s sum of squares
+    const int g = k / P, q = k % P;
+    float ss = 0.f;
+    for (int r = lane; r < rph; r += 32) ss = fmaf(os[q][g * rph + r], os[q][g * rph + r], ss);
+    ss = warp_sum(ss);
+    if (lane == 0) rms[k] = ss;
+  }
+  cluster_sync_all();  // partial sums published
+  for (int k = tid; k < nrows * P; k += blockDim.x) {
+    const int q = k / nrows, r = k % nrows, g = r / rph, i = r0 + r % rph, h = G * j + g;
+    float ss = 0.f;
+    for (int c = 0; c < nsplit; ++c) ss += ld_cluster_f32(&rms[g * P + q], (uint32_t)c);
+    const float rinv = rsqrtf(ss * (1.0f / kHeadDim) + p.eps);
+    const float oi = os[q][r];
+    const size_t orow = (((size_t)n * P + q) * p.Hv + h) * kHeadDim + i;
+    if (p.o) p.o[orow] = f32_to_bf16(oi);
+    if (p.ogate) p.ogate[orow] = f32_to_bf16(oi * rinv * p.gamma[i] * silu(bf16_to_f32(p.z[orow])));
+  }
+  cluster_sync_all();  // no CTA leaves while a peer may still read its partial sums
+}
+
 // Counter slot of a stream: streams get slots in order of first use (wrapping
 // after kSchedSlots streams), so launches on one stream share a slot (they run
 // one after the other) and launches on different streams use different slots.
@@ -784,12 +964,12 @@ int split_clusters_resident(const StepArgs& a, int nsplit) {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
   split_config(a, nsplit, &cfg, &attr);
-  return resident_clusters(reinterpret_cast<const void*>(split_kernel), (int)cfg.blockDim.x, cfg.dynamicSmemBytes,
-                           nsplit);
+  const void* fn = a.parent ? reinterpret_cast<const void*>(split_tree_kernel) : reinterpret_cast<const void*>(split_kernel);
+  return resident_clusters(fn, (int)cfg.blockDim.x, cfg.dynamicSmemBytes, nsplit);
 }
 
 // Rows of a unit split over nsplit CTAs when the units alone would leave SMs
-// idle (decode only): the smallest power of two that covers the SMs, at least
+// idle (decode, and the verify of a tree): the smallest power of two that covers the SMs, at least
 // G (so a CTA holds at most 128 state rows, 8 lanes each), at most 8. The split
 // is taken only when all the clusters fit on the GPU at once (one wave); with
 // more than that, the persistent kernel streams the units faster (measured: 8
@@ -797,7 +977,7 @@ int split_clusters_resident(const StepArgs& a, int nsplit) {
 // us persistent). 1: no split.
 int split_factor(const StepArgs& a, int sms) {
   const int units = a.N * a.Hk;
-  if (a.P != 1 || a.spec_slot != nullptr || units >= sms) return 1;
+  if ((a.spec_slot != nullptr && !a.parent) || units >= sms) return 1;
   int s = 2;
   while (s < kMaxSplit && (s < a.G || units * s < sms)) s *= 2;
   return units <= split_clusters_resident(a, s) ? s : 1;
@@ -808,7 +988,7 @@ cudaError_t launch_split(const StepArgs& a, int nsplit, cudaStream_t stream) {
   cudaLaunchAttribute attr;
   split_config(a, nsplit, &cfg, &attr);
   cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, split_kernel, a, nsplit);
+  return cudaLaunchKernelEx(&cfg, a.parent ? split_tree_kernel : split_kernel, a, nsplit);
 }
 
 cudaError_t launch_stream(const StepArgs& a, cudaStream_t stream) {
