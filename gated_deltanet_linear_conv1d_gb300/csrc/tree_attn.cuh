@@ -114,8 +114,8 @@ struct Cfg {
   static constexpr int oP = 0;
   static constexpr int oQ = oP + 2 * (int)kBlock;
   static constexpr int oSc = oQ + kQBuf * kQBytes;                          // [kScSlots][2][128] fp32
-  static constexpr int oMax = oSc + (kE4m3 ? kScSlots * 2 * kTile * 4 : 0);  // [2][kRows + 2][4]
-  static constexpr int oSum = oMax + 2 * (kRows + 2) * 16;                  // [2][kRows][4]
+  static constexpr int oMax = oSc + (kE4m3 ? kScSlots * 2 * kTile * 4 : 0);  // [2][4 warps][kRows + 4]
+  static constexpr int oSum = oMax + 2 * (kRows + 4) * 16;                  // [2][4 warps][kRows]
   static constexpr int oWarp = oSum + 2 * kRows * 16;                       // [8 warps][kSoftRows]
   static constexpr int oTile = oWarp + 8 * kSoftRows * 4;                   // [2][kRows + 4]: maxima, the V scale
   static constexpr int oAb = oTile + 2 * (kRows + 4) * 4;                   // [2 groups][2][2][kRows]
@@ -250,6 +250,67 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
+// A warp's 32 tokens (lanes of tensor memory) by eight columns: this thread has tokens lane / 4 + 8 i, i = 0..3, and
+// columns 2 (lane % 4) and the next of each. `lanes16`: the address of the upper sixteen lanes. Without waiting.
+__device__ __forceinline__ void ld_tile8(uint32_t taddr, uint32_t lanes16, uint32_t (&r)[4][2]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0][0]), "=r"(r[0][1]), "=r"(r[1][0]), "=r"(r[1][1])
+               : "r"(taddr)
+               : "memory");
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[2][0]), "=r"(r[2][1]), "=r"(r[3][0]), "=r"(r[3][1])
+               : "r"(lanes16)
+               : "memory");
+}
+
+// The same distribution of 16-bit pairs back to shared memory: register i holds the pair of token lane / 4 + 8 i, and
+// each lane names the 16-byte row of token `lane`.
+__device__ __forceinline__ void st_tile8(uint32_t row, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(row), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3])
+               : "memory");
+}
+
+// Of 2 kC values a lane, kC pairs of columns, the reduction over the eight lanes with the same lane % 4, the values
+// shared out on the way. Afterwards the lane has the result of pair `pair`, value `second` of it.
+template <int kC, typename Op>
+__device__ __forceinline__ float reduce_pairs(const float2 (&v)[kC], int lane, Op op) {
+  const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
+  float a;
+  if constexpr (kC == 1) {
+    a = op(b4 ? v[0].y : v[0].x, __shfl_xor_sync(0xffffffffu, b4 ? v[0].x : v[0].y, 16));
+    a = op(a, __shfl_xor_sync(0xffffffffu, a, 8));
+    a = op(a, __shfl_xor_sync(0xffffffffu, a, 4));
+  } else {
+    constexpr int kN = kC / 2;
+    float2 h[kN];  // the upper or the lower pairs
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const float2 stay = b4 ? v[kN + i] : v[i], give = b4 ? v[i] : v[kN + i];
+      h[i].x = op(stay.x, __shfl_xor_sync(0xffffffffu, give.x, 16));
+      h[i].y = op(stay.y, __shfl_xor_sync(0xffffffffu, give.y, 16));
+    }
+    float2 t = h[0];
+    if constexpr (kN == 2) {
+      const float2 stay = b3 ? h[1] : h[0], give = b3 ? h[0] : h[1];
+      t.x = op(stay.x, __shfl_xor_sync(0xffffffffu, give.x, 8));
+      t.y = op(stay.y, __shfl_xor_sync(0xffffffffu, give.y, 8));
+      a = op(b2 ? t.y : t.x, __shfl_xor_sync(0xffffffffu, b2 ? t.x : t.y, 4));
+    } else {
+      a = op(b3 ? t.y : t.x, __shfl_xor_sync(0xffffffffu, b3 ? t.x : t.y, 8));
+      a = op(a, __shfl_xor_sync(0xffffffffu, a, 4));
+    }
+  }
+  return a;
+}
+// The column (of 8 kC) whose result reduce_pairs leaves in this lane.
+template <int kC>
+__device__ __forceinline__ int reduced_column(int lane) {
+  const int b4 = lane >> 4 & 1, b3 = lane >> 3 & 1, b2 = lane >> 2 & 1;
+  const int pair = kC == 1 ? 0 : kC == 2 ? b4 : b4 * 2 + b3, second = kC == 1 ? b4 : kC == 2 ? b3 : b2;
+  return pair * 8 + (lane & 3) * 2 + second;
+}
+
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
@@ -263,6 +324,18 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
       : "=f"(r.x), "=f"(r.y)
       : "r"(h));
   return r;
+}
+// Two values as E4M3 (lower half) and what their rounding left, again as E4M3 (upper half). By way of fp16, whose 11
+// bits hold the two terms' 4 + 4 and what is lost to it (2^-12) is far below what is lost to them.
+__device__ __forceinline__ uint32_t two_terms(float2 x) {
+  uint32_t h, back;
+  uint16_t first, rest;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(x.y), "f"(x.x));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(first) : "r"(h));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(first));
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(h) : "r"(back));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(rest) : "r"(h));
+  return (uint32_t)first | ((uint32_t)rest << 16);
 }
 // Eight values as E4M3 (first) and what their rounding left, again as E4M3 (rest).
 __device__ __forceinline__ void two_terms(const float (&x)[8], uint2& first, uint2& rest) {
@@ -776,12 +849,18 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
       ++seg;
     }
   } else if (warp < C::kOutWarp) {
-    // ------------------------------------------------------------ softmax: thread = token of the tile
-    const int wg = warp >> 2, w4 = warp & 3, tt = tid & 127;
+    // ------------------------------------------------------------ softmax
+    // A warp has 32 of the tile's tokens; a thread four of them (lane / 4 + 8 i) with a quarter of the rows (2 (lane % 4)
+    // and the next of every eight): the reductions over the tokens are three quarters done before the first exchange
+    // between lanes. (A token a thread, with all its rows, took 36 exchanges for 32 rows instead of 7, and a reduction
+    // instruction for each row's maximum twice as long.)
+    const int wg = warp >> 2, w4 = warp & 3, a4 = lane & 3;
+    constexpr int kR = C::kSoftRows, kC = kR / 8;
     const int rp = kE4m3 ? (a.rows + 7) / 8 * 8 : (a.rows + 15) / 16 * 16;
-    constexpr int kR = C::kSoftRows;
-    const int roff = C::kSplit ? wg * kR : 0;                            // this thread's first row
-    const int used = min(kR / 8, max(0, (a.rows - roff + 7) / 8));       // its groups of eight rows
+    const int roff = C::kSplit ? wg * kR : 0;                            // this group's first row
+    const int used = min(kC, max(0, (a.rows - roff + 7) / 8));           // its groups of eight rows
+    const int mine = reduced_column<kC>(lane);                           // the row whose statistics end in this lane
+    const int tt = 32 * w4 + (lane >> 2);                                // the first of this thread's tokens
     float* sums = reinterpret_cast<float*>(rest + C::oSum);
     float* maxima = reinterpret_cast<float*>(rest + C::oMax);
     float* tile_s = reinterpret_cast<float*>(rest + C::oTile);
@@ -798,37 +877,41 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
       for (int t = s.t0; t < s.t1; ++t, ++i) {
         const int b = i & 1, ph = (i >> 1) & 1;
         if (!C::kSplit && b != wg) continue;
-        const int tok = t * kTile + tt;
-        float sk = 1.f, sv = 1.f;
+        float sk[4], sv[4];
         if constexpr (kE4m3) {
           const int slot = i % kScSlots;
           wait_warp(&B->sc_full[slot], (i / kScSlots) & 1, abort);
-          sk = scales[slot * 2 * kTile + tt];
-          sv = scales[slot * 2 * kTile + kTile + tt];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            sk[k] = scales[slot * 2 * kTile + tt + 8 * k];
+            sv[k] = t * kTile + tt + 8 * k < s.len ? scales[slot * 2 * kTile + kTile + tt + 8 * k] : 0.f;
+          }
           __syncwarp();
           if (lane == 0) arrive(&B->sc_empty[slot]);
-          if (tok >= s.len) sv = 0.f;
         }
         wait_warp(&B->s_full[b], ph, abort);
         umma::fence_after_sync();
-        float2 x[kR / 2];  // scores, not yet taken times the row's scale
+        float2 x[kC][4];  // scores, not yet taken times the row's factor
         const uint32_t ts = umma::taddr(tmem, 32 * w4, b * C::kCols + roff);
 #pragma unroll
-        for (int g = 0; g < kR / 8; ++g)
+        for (int g = 0; g < kC; ++g)
           if (g < used) {
-            uint32_t u[8], w[8];
-            ld8_nowait(ts + g * 8, u);
-            if constexpr (kE4m3) ld8_nowait(ts + rp + g * 8, w);
+            uint32_t u[4][2], w[4][2];
+            ld_tile8(ts + g * 8, ts + (16u << 16) + g * 8, u);
+            if constexpr (kE4m3) ld_tile8(ts + rp + g * 8, ts + (16u << 16) + rp + g * 8, w);
             umma::wait_ld();
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float2 v = make_float2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]));
+            for (int k = 0; k < 4; ++k) {
+              float2 v = make_float2(__uint_as_float(u[k][0]), __uint_as_float(u[k][1]));
               if constexpr (kE4m3) {
-                v = __fadd2_rn(v, make_float2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1])));
-                v = __fmul2_rn(v, make_float2(sk, sk));
+                v = __fadd2_rn(v, make_float2(__uint_as_float(w[k][0]), __uint_as_float(w[k][1])));
+                v = __fmul2_rn(v, make_float2(sk[k], sk[k]));
               }
-              x[g * 4 + e] = v;
+              x[g][k] = v;
             }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[g][k] = make_float2(0.f, 0.f);
           }
         umma::fence_before_sync();
         __syncwarp();
@@ -836,115 +919,85 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         // the statistics of two tiles back have been read
         wait_warp(C::kOBuf == 2 ? &B->o_empty[b] : &B->st_empty[b], ph ^ 1, abort);
         if ((t + 1) * kTile > s.ctx) {  // drafted tokens, or tokens behind the last
-          const int node = tok - s.ctx;
 #pragma unroll
-          for (int g = 0; g < kR / 8; ++g)
-            if (g < used) {
+          for (int k = 0; k < 4; ++k) {
+            const int node = t * kTile + tt + 8 * k - s.ctx;
+            if (node < 0) continue;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int r = g * 8 + 2 * e;
+            for (int g = 0; g < kC; ++g)
+              if (g < used) {
                 const bool in = node < p.P;
-                float2& v = x[g * 4 + e];
-                v.x = node < 0 || (in && ((mask_s[r] >> (node & 63)) & 1)) ? v.x : -INFINITY;
-                v.y = node < 0 || (in && ((mask_s[r + 1] >> (node & 63)) & 1)) ? v.y : -INFINITY;
+                if (!in || !((mask_s[g * 8 + a4 * 2] >> (node & 63)) & 1)) x[g][k].x = -INFINITY;
+                if (!in || !((mask_s[g * 8 + a4 * 2 + 1] >> (node & 63)) & 1)) x[g][k].y = -INFINITY;
               }
-            }
-          if (kE4m3 && node >= 0 && !(fabsf(sv) < INFINITY)) sv = 0.f;  // its values are zeros, see the check warp
-        }
-        // ---- the tile's maximum of each row: of the warp first (row r's in lane r), then of the four warps
-        float keep = -INFINITY;
-#pragma unroll
-        for (int g = 0; g < kR / 8; ++g)
-          if (g < used) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int r = g * 8 + e;
-              const float m = warp_max(e & 1 ? x[r / 2].y : x[r / 2].x);
-              if (lane == r) keep = m;
-            }
+            if (kE4m3 && !(fabsf(sv[k]) < INFINITY)) sv[k] = 0.f;  // its values are zeros, see the check warp
           }
-        float* max_b = maxima + (b * (kRows + 2) + roff) * 4;
-        float* max_v = maxima + (b * (kRows + 2) + kRows + wg) * 4;
-        if (lane < used * 8) max_b[lane * 4 + w4] = keep;
+        }
+        // ---- the tile's maximum of each row: of the warp first, then of the four warps
+        float* max_b = maxima + b * 4 * (kRows + 4);
+        {
+          float2 m[kC];
+#pragma unroll
+          for (int g = 0; g < kC; ++g)
+            m[g] = make_float2(fmaxf(fmaxf(x[g][0].x, x[g][1].x), fmaxf(x[g][2].x, x[g][3].x)),
+                               fmaxf(fmaxf(x[g][0].y, x[g][1].y), fmaxf(x[g][2].y, x[g][3].y)));
+          max_b[w4 * (kRows + 4) + roff + mine] = reduce_pairs<kC>(m, lane, [](float u, float v) { return fmaxf(u, v); });
+        }
         if constexpr (kE4m3) {
-          const float m = warp_max(fabsf(sv));
-          if (lane == 0) max_v[w4] = m;
+          float m = fmaxf(fmaxf(fabsf(sv[0]), fabsf(sv[1])), fmaxf(fabsf(sv[2]), fabsf(sv[3])));
+          m = warp_max(m);
+          if (lane == 0) max_b[w4 * (kRows + 4) + kRows + wg] = m;
         }
         sync_group(1 + wg);
-        if (lane < used * 8) {
-          const float4 m4 = *reinterpret_cast<const float4*>(max_b + lane * 4);
-          const float m = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+        if (lane < kR) {
+          const float* at = max_b + roff + lane;
+          const float m = fmaxf(fmaxf(at[0], at[kRows + 4]), fmaxf(at[2 * (kRows + 4)], at[3 * (kRows + 4)]));
           const float scaled = m == -INFINITY ? m : m * qs_s[lane];
           warp_s[lane] = m == -INFINITY ? 0.f : -scaled;
           if (w4 == 0) tile_s[b * (kRows + 4) + roff + lane] = scaled;
         }
-        float f = 1.f;  // the weight's factor: the value's scale, the tile's largest at 256
+        float f[4] = {1.f, 1.f, 1.f, 1.f};  // the weights' factors: the value's scale, the tile's largest at 256
         if constexpr (kE4m3) {
-          const float4 v4 = *reinterpret_cast<const float4*>(max_v);
-          const float most = fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w));
-          f = sv == 0.f ? 0.f : 256.f * __fdiv_rn(sv, most);
-          if (tt == 0 && roff == 0) tile_s[b * (kRows + 4) + kRows] = most * (1.f / 256.f);
+          const float* at = max_b + kRows + wg;
+          const float most = fmaxf(fmaxf(at[0], at[kRows + 4]), fmaxf(at[2 * (kRows + 4)], at[3 * (kRows + 4)]));
+          const float r = __fdividef(256.f, most);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) f[k] = sv[k] == 0.f ? 0.f : most < 1e-30f ? 256.f * (sv[k] / most) : sv[k] * r;
+          if ((tid & 127) == 0 && roff == 0) tile_s[b * (kRows + 4) + kRows] = most * (1.f / 256.f);
         }
         __syncwarp();
         wait_warp(&B->p_empty[b], ph ^ 1, abort);
-        unsigned char* prow = rest + C::oP + b * kBlock;
+        const uint32_t prow = smem_u32(rest + C::oP + b * kBlock) + (32 * w4 + lane) * 128;
 #pragma unroll
-        for (int g = 0; g < kR / 8; ++g)
+        for (int g = 0; g < kC; ++g)
           if (g < used) {
-            float w[8];
+            const float2 q2 = *reinterpret_cast<const float2*>(qs_s + g * 8 + a4 * 2);
+            const float2 m2 = *reinterpret_cast<const float2*>(warp_s + g * 8 + a4 * 2);
+            uint32_t r[4];
 #pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-              const float4 q4 = *reinterpret_cast<const float4*>(qs_s + g * 8 + e);
-              const float4 m4 = *reinterpret_cast<const float4*>(warp_s + g * 8 + e);
-              float2& lo = x[g * 4 + e / 2];
-              float2& hi = x[g * 4 + e / 2 + 1];
-              lo = __ffma2_rn(lo, make_float2(q4.x, q4.y), make_float2(m4.x, m4.y));
-              hi = __ffma2_rn(hi, make_float2(q4.z, q4.w), make_float2(m4.z, m4.w));
-              lo = make_float2(ex2(lo.x), ex2(lo.y));
-              hi = make_float2(ex2(hi.x), ex2(hi.y));
-              float2 wl = lo, wh = hi;
+            for (int k = 0; k < 4; ++k) {
+              const float2 v = __ffma2_rn(x[g][k], q2, m2);
+              x[g][k] = make_float2(ex2(v.x), ex2(v.y));
               if constexpr (kE4m3) {
-                wl = __fmul2_rn(lo, make_float2(f, f));
-                wh = __fmul2_rn(hi, make_float2(f, f));
+                r[k] = two_terms(__fmul2_rn(x[g][k], make_float2(f[k], f[k])));
+              } else {
+                const __nv_bfloat162 w = __floats2bfloat162_rn(x[g][k].x, x[g][k].y);
+                r[k] = *reinterpret_cast<const uint32_t*>(&w);
               }
-              w[e] = wl.x; w[e + 1] = wl.y; w[e + 2] = wh.x; w[e + 3] = wh.y;
             }
-            if constexpr (kE4m3) {
-              uint2 first, second;
-              two_terms(w, first, second);
-              *reinterpret_cast<uint2*>(prow + swz(tt, roff + g * 8)) = first;
-              *reinterpret_cast<uint2*>(prow + swz(tt, rp + roff + g * 8)) = second;
-            } else {
-              *reinterpret_cast<uint4*>(prow + swz(tt, (roff + g * 8) * 2)) = to_bf16x8(w);
-            }
+            // eight rows are 16 bytes of a token's row of P, in E4M3 too: two rows' first terms, then their second
+            st_tile8(prow + (((roff / 8 + g) ^ (lane & 7)) << 4), r);
           }
         umma::fence_proxy_async_smem();
         arrive(&B->p_full[b]);
-        // ---- the warp's sums: eight rows at a time, halved over the lanes
+        // ---- the warp's sums
+        {
+          float2 v[kC];
 #pragma unroll
-        for (int g = 0; g < kR / 8; ++g)
-          if (g < used) {
-            const float v8[8] = {x[g * 4].x, x[g * 4].y, x[g * 4 + 1].x, x[g * 4 + 1].y,
-                                 x[g * 4 + 2].x, x[g * 4 + 2].y, x[g * 4 + 3].x, x[g * 4 + 3].y};
-            float v4[4], v2[2], v1;
-            const bool h16 = lane & 16, h8 = lane & 8, h4 = lane & 4;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float give = h16 ? v8[e] : v8[e + 4], stay = h16 ? v8[e + 4] : v8[e];
-              v4[e] = stay + __shfl_xor_sync(0xffffffffu, give, 16);
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float give = h8 ? v4[e] : v4[e + 2], stay = h8 ? v4[e + 2] : v4[e];
-              v2[e] = stay + __shfl_xor_sync(0xffffffffu, give, 8);
-            }
-            const float give = h4 ? v2[0] : v2[1], stay = h4 ? v2[1] : v2[0];
-            v1 = stay + __shfl_xor_sync(0xffffffffu, give, 4);
-            v1 += __shfl_xor_sync(0xffffffffu, v1, 2);
-            v1 += __shfl_xor_sync(0xffffffffu, v1, 1);
-            const int r = g * 8 + (h16 ? 4 : 0) + (h8 ? 2 : 0) + (h4 ? 1 : 0);
-            if ((lane & 3) == 0) sums[(b * kRows + roff + r) * 4 + w4] = v1;
-          }
+          for (int g = 0; g < kC; ++g)
+            v[g] = __fadd2_rn(__fadd2_rn(x[g][0], x[g][1]), __fadd2_rn(x[g][2], x[g][3]));
+          sums[(b * 4 + w4) * kRows + roff + mine] = reduce_pairs<kC>(v, lane, [](float u, float w) { return u + w; });
+        }
         arrive(&B->st_full[b]);
       }
       __syncwarp();
@@ -954,7 +1007,6 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
   } else {
     // ------------------------------------------------------------ output: thread = value of D
     const int og = (warp - C::kOutWarp) >> 2, ot = tid & 127, bar = 3 + og;
-    const int rp = kE4m3 ? (a.rows + 7) / 8 * 8 : (a.rows + 15) / 16 * 16;
     constexpr int kR = C::kOutRows;
     constexpr int kH = C::kOutHalves;
     const int half = C::kHalves > kH ? og : 0, dim = half * 128 + ot;    // this thread's first value
@@ -989,8 +1041,8 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         bool moved = false;  // a running maximum has changed
         if (ot < a.rows) {
           const float mt = tile_s[b * (kRows + 4) + ot];
-          const float4 l4 = *reinterpret_cast<const float4*>(sums + (b * kRows + ot) * 4);
-          const float lt = (l4.x + l4.y) + (l4.z + l4.w);
+          const float* l4 = sums + b * 4 * kRows + ot;
+          const float lt = (l4[0] + l4[kRows]) + (l4[2 * kRows] + l4[3 * kRows]);
           const float mn = fmaxf(m_run, mt);
           const float keep = m_run == -INFINITY ? 0.f : ex2(m_run - mn), w = mt == -INFINITY ? 0.f : ex2(mt - mn);
           moved = keep != 1.f;
@@ -1002,40 +1054,43 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         moved = any_in_group(bar, moved);
         wait_warp(&B->o_full[ob], (i / C::kOBuf) & 1, abort);
         umma::fence_after_sync();
-        const uint32_t to = umma::taddr(tmem, 32 * (warp & 3), 2 * C::kCols + (ob * C::kHalves + half) * C::kCols + roff);
+        const uint32_t to = umma::taddr(tmem, 32 * (warp & 3), 2 * C::kCols + (ob * C::kHalves + half) * C::kCols + roff * C::kTerms);
 #pragma unroll
         for (int g = 0; g < kR / 8; ++g)
           if (g < used) {
-            uint32_t u_all[kH][8], v_all[kH][8];
+            constexpr int kN = 8 * C::kTerms;  // columns of eight rows
+            uint32_t u[kH][kN];
 #pragma unroll
             for (int k = 0; k < kH; ++k) {
-              ld8_nowait(to + k * C::kCols + g * 8, u_all[k]);
-              if constexpr (kE4m3) ld8_nowait(to + k * C::kCols + rp + g * 8, v_all[k]);
+              if constexpr (kE4m3) umma::ld16_nowait(to + k * C::kCols + g * kN, u[k]);
+              else ld8_nowait(to + k * C::kCols + g * kN, u[k]);
             }
             umma::wait_ld();
 #pragma unroll
-            for (int k = 0; k < kH; ++k) {
-              const uint32_t(&u)[8] = u_all[k];
+            for (int e = 0; e < 8; e += 4) {
+              const int r = g * 8 + e;
+              const float4 w4 = *reinterpret_cast<const float4*>(w_s + roff + r);
+              float4 k4 = make_float4(1.f, 1.f, 1.f, 1.f);
+              if (moved) k4 = *reinterpret_cast<const float4*>(keep_s + roff + r);
 #pragma unroll
-              for (int e = 0; e < 8; e += 4) {
-                const int r = g * 8 + e;
-                const float4 w4 = *reinterpret_cast<const float4*>(w_s + roff + r);
-                float2 lo = make_float2(__uint_as_float(u[e]), __uint_as_float(u[e + 1]));
-                float2 hi = make_float2(__uint_as_float(u[e + 2]), __uint_as_float(u[e + 3]));
-                if constexpr (kE4m3) {
-                  lo = __fadd2_rn(lo, make_float2(__uint_as_float(v_all[k][e]), __uint_as_float(v_all[k][e + 1])));
-                  hi = __fadd2_rn(hi, make_float2(__uint_as_float(v_all[k][e + 2]), __uint_as_float(v_all[k][e + 3])));
+              for (int k = 0; k < kH; ++k) {
+                float2 o[2];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const uint32_t* c4 = u[k] + (kE4m3 ? 2 * e + 4 * y : e + 2 * y);
+                  o[y] = make_float2(__uint_as_float(c4[0]), __uint_as_float(c4[1]));
+                  if constexpr (kE4m3) o[y] = __fadd2_rn(o[y], make_float2(__uint_as_float(c4[2]), __uint_as_float(c4[3])));
                 }
+                float2 &lo = acc[k][r / 2], &hi = acc[k][r / 2 + 1];
                 if (moved) {
-                  const float4 k4 = *reinterpret_cast<const float4*>(keep_s + roff + r);
-                  acc[k][r / 2] = __fmul2_rn(acc[k][r / 2], make_float2(k4.x, k4.y));
-                  acc[k][r / 2 + 1] = __fmul2_rn(acc[k][r / 2 + 1], make_float2(k4.z, k4.w));
+                  lo = __fmul2_rn(lo, make_float2(k4.x, k4.y));
+                  hi = __fmul2_rn(hi, make_float2(k4.z, k4.w));
                 }
-                acc[k][r / 2] = __ffma2_rn(lo, make_float2(w4.x, w4.y), acc[k][r / 2]);
-                acc[k][r / 2 + 1] = __ffma2_rn(hi, make_float2(w4.z, w4.w), acc[k][r / 2 + 1]);
+                lo = __ffma2_rn(o[0], make_float2(w4.x, w4.y), lo);
+                hi = __ffma2_rn(o[1], make_float2(w4.z, w4.w), hi);
               }
             }
-        }
+          }
         umma::fence_before_sync();
         unsigned long long dirty = 0;
         if ((t + 1) * kTile > s.ctx) {
