@@ -94,8 +94,14 @@ struct Cfg {
   static constexpr int kBlk = D * (kE4m3 ? 1 : 2) / 128;  // ring blocks of a tile's K, and of its V
   static constexpr int kHalves = D / 128;
   static constexpr int kTerms = kE4m3 ? 2 : 1;
-  static constexpr int kCols = kTerms * kRows;
-  static constexpr int kOBuf = (2 + 2 * kHalves) * kCols <= 512 ? 2 : 1;
+  static constexpr int kCols = kTerms * kRows;                // of the scores
+  // The two terms of P are neighbouring columns of one product, added as the output is read; with 64 rows two
+  // products add them up in tensor memory instead (a third more time for the MMAs, which have it, half the columns
+  // to read, and room for two outputs).
+  static constexpr bool kSumTerms = kE4m3 && kRows == 64;
+  static constexpr int kOTerms = kSumTerms ? 1 : kTerms;
+  static constexpr int kOCols = kOTerms * kRows;              // of the output
+  static constexpr int kOBuf = 2;
   static constexpr int kQBytes = kCols * 128 * kBlk;
   static constexpr bool kSplit = kRows == 64;               // the softmax groups share each tile's rows
   // Tiles whose scores are ahead of the output: when a softmax group ends a tile, its next one's scores are there.
@@ -122,15 +128,16 @@ struct Cfg {
   static constexpr int oMask = oAb + 8 * kRows * 4;                         // [kQBuf][kRows] uint64
   static constexpr int oQs = oMask + kQBuf * kRows * 8;                     // [kQBuf][kRows] fp32
   static constexpr int oFin = oQs + kQBuf * kRows * 4;                      // [2 groups][2][kRows] fp32
-  static constexpr int oStage = oFin + 4 * kRows * 4;                       // [kOutGroups][4 rows][kOutHalves * 128] fp32
-  static constexpr int oBars = oStage + kOutGroups * 4 * kOutHalves * 512;
+  static constexpr int kStageRows = kOutHalves == 2 ? 4 : 8;                // rows of a result on their way out at a time
+  static constexpr int oStage = oFin + 4 * kRows * 4;                       // [kOutGroups][kStageRows][kOutHalves * 128] fp32
+  static constexpr int oBars = oStage + kOutGroups * kStageRows * kOutHalves * 512;
   static constexpr int kRest = oBars + 1408;
   static constexpr int kFit = (kSmemLimit - kRest) / (int)kBlock;
   // an even number of blocks keeps the two bf16 blocks of a 128-wide half of V side by side
   static constexpr int kStages = kE4m3 ? kFit : kFit / 2 * 2;
   static constexpr int kSmem = kStages * (int)kBlock + kRest;
   static_assert(kStages >= kBlk + 2, "a tile's whole V stays until its weights are there");
-  static_assert((2 + kOBuf * kHalves) * kCols <= 512, "tensor memory");
+  static_assert(2 * kCols + kOBuf * kHalves * kOCols <= 512, "tensor memory");
 };
 
 // One CTA's piece of the line of tiles.
@@ -146,7 +153,7 @@ struct Bars {
   uint64_t v_clean[kMarks];               // and V is ready for the MMAs
   uint64_t checked[kMarks];               // by segment
   uint64_t q_full[3], q_empty[3], s_full[2], s_empty[2], p_full[2], p_empty[2], o_full[2], o_empty[2];
-  uint64_t st_full[2], st_empty[2], sc_full[kScSlots], sc_empty[kScSlots], drain;
+  uint64_t st_full[2], sc_full[kScSlots], sc_empty[kScSlots], drain;
   uint32_t tmem;
   int abort;
   int bad[kMarks];                        // the segment has a page out of the pool
@@ -429,7 +436,9 @@ __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned 
           if (r < a.rows && j < p.P) m = p.mask ? __ldg(p.mask + (size_t)s.n * p.P + j) : j == 63 ? ~0ull : (2ull << j) - 1;
           mask_s[r] = m;
         }
-        constexpr int kBatch = 8;
+        // rows on their way at once: more hide their loads at the start of a short segment, fewer leave the instruction
+  // cache to the loops (256 x 1k..8k tokens with 6 rows: 288 us with four, 294 with eight; 32 trees of 48 rows: 196 and 177)
+  constexpr int kBatch = kRows == 16 ? 4 : 8;
         for (int rb = share * kBatch; rb < rp; rb += shares * kBatch) {
           uint4 raw[kBatch];
   #pragma unroll
@@ -530,7 +539,6 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         mbar_init(&B->o_full[i], 1);
         mbar_init(&B->o_empty[i], 4 * C::kOutGroups);
         mbar_init(&B->st_full[i], C::kSoftWarps * 32);
-        mbar_init(&B->st_empty[i], 4 * C::kOutGroups);
       }
       for (int i = 0; i < kScSlots; ++i) {
         mbar_init(&B->sc_full[i], 1);
@@ -674,9 +682,10 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
     // The whole warp walks and waits, one elected thread issues: with `if (lane == 0)` instead an MMA took
     // 73 cycles to issue on an idle SM, and about 200 next to the other warps; its work is 41 at 16 columns.
     const int rp = kE4m3 ? (a.rows + 7) / 8 * 8 : (a.rows + 15) / 16 * 16;  // rows as columns of the MMAs
-    const int N = C::kTerms * rp;
+    // (an MMA of 128 lanes takes columns by sixteens)
+    const int N = C::kTerms * rp, NO = C::kSumTerms ? (rp + 15) / 16 * 16 : C::kOTerms * rp;
     constexpr uint32_t kKind = kE4m3 ? umma::kKindF8 : umma::kKindF16, kType = kE4m3 ? umma::kE4M3 : umma::kBF16;
-    const uint32_t id_s = umma::idesc(kType, false, false, kTile, N), id_o = umma::idesc(kType, true, true, kTile, N);
+    const uint32_t id_s = umma::idesc(kType, false, false, kTile, N), id_o = umma::idesc(kType, true, true, kTile, NO);
     const uint32_t sQ = smem_u32(rest + C::oQ), sP = smem_u32(rest + C::oP);
     int st = 0, i = 0, seg = 0, marks = 0;
     uint32_t last_tiles = 0;  // bit i % 32: tile i has drafted tokens, the check warp cleans its V
@@ -700,12 +709,17 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         const int st2 = kE4m3 ? st : st + 1;  // two bf16 blocks are side by side
         umma::fence_after_sync();
         if (elect_one()) {
-          const uint32_t d = tmem + 2 * C::kCols + (ob * C::kHalves + h) * C::kCols;
+          const uint32_t d = tmem + 2 * C::kCols + (ob * C::kHalves + h) * C::kOCols;
           constexpr int kSteps = kE4m3 ? 4 : 8, kStepBytes = kE4m3 ? 4096 : 2048;  // 32 or 16 tokens a step
           const uint64_t va = desc_mn(ring + st * kBlock), pa = desc_mn(sP + b * kBlock);
 #pragma unroll
           for (int k = 0; k < kSteps; ++k)
             umma::mma<kKind>(d, va + k * (kStepBytes >> 4), pa + k * (kStepBytes >> 4), id_o, k > 0);
+          if constexpr (C::kSumTerms) {  // the second terms, 64 bytes on
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)
+              umma::mma<kKind>(d, va + k * (kStepBytes >> 4), pa + 4 + k * (kStepBytes >> 4), id_o, 1);
+          }
           umma::commit(&B->empty[st]);
           if (!kE4m3) umma::commit(&B->empty[st2]);
           if (h == C::kHalves - 1) {
@@ -917,7 +931,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         __syncwarp();
         if (lane == 0) arrive(&B->s_empty[b]);
         // the statistics of two tiles back have been read
-        wait_warp(C::kOBuf == 2 ? &B->o_empty[b] : &B->st_empty[b], ph ^ 1, abort);
+        wait_warp(&B->o_empty[b], ph ^ 1, abort);
         if ((t + 1) * kTile > s.ctx) {  // drafted tokens, or tokens behind the last
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -968,6 +982,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         __syncwarp();
         wait_warp(&B->p_empty[b], ph ^ 1, abort);
         const uint32_t prow = smem_u32(rest + C::oP + b * kBlock) + (32 * w4 + lane) * 128;
+        uint32_t even[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
         for (int g = 0; g < kC; ++g)
           if (g < used) {
@@ -985,8 +1000,28 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
                 r[k] = *reinterpret_cast<const uint32_t*>(&w);
               }
             }
-            // eight rows are 16 bytes of a token's row of P, in E4M3 too: two rows' first terms, then their second
-            st_tile8(prow + (((roff / 8 + g) ^ (lane & 7)) << 4), r);
+            if constexpr (C::kSumTerms) {
+              // sixteen rows' first terms are 16 bytes of a token's row of P, two of the one group and two of the
+              // other in turn; their second terms 64 bytes on
+              if (g % 2 == 0) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) even[k] = r[k];
+              }
+              if (g % 2 == 1 || g + 1 >= used) {
+                uint32_t first[4], second[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t odd = g % 2 ? r[k] : 0u;
+                  first[k] = __byte_perm(even[k], odd, 0x5410);
+                  second[k] = __byte_perm(even[k], odd, 0x7632);
+                }
+                st_tile8(prow + (((roff / 16 + g / 2) ^ (lane & 7)) << 4), first);
+                st_tile8(prow + (((4 + roff / 16 + g / 2) ^ (lane & 7)) << 4), second);
+              }
+            } else {
+              // eight rows are 16 bytes of a token's row of P, in E4M3 too: two rows' first terms, then their second
+              st_tile8(prow + (((roff / 8 + g) ^ (lane & 7)) << 4), r);
+            }
           }
         umma::fence_proxy_async_smem();
         arrive(&B->p_full[b]);
@@ -1054,20 +1089,22 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         moved = any_in_group(bar, moved);
         wait_warp(&B->o_full[ob], (i / C::kOBuf) & 1, abort);
         umma::fence_after_sync();
-        const uint32_t to = umma::taddr(tmem, 32 * (warp & 3), 2 * C::kCols + (ob * C::kHalves + half) * C::kCols + roff * C::kTerms);
+        const uint32_t to = umma::taddr(tmem, 32 * (warp & 3), 2 * C::kCols + (ob * C::kHalves + half) * C::kOCols + roff * C::kOTerms);
+        // rows e .. e + 3 of eight, from g * kN on: their pairs' columns, see where P is stored
+        constexpr int kN = 8 * C::kOTerms;  // columns of eight rows
+        constexpr int kGo = C::kSumTerms ? 2 : 1;  // eights at a time
 #pragma unroll
-        for (int g = 0; g < kR / 8; ++g)
+        for (int g = 0; g < kR / 8; g += kGo)
           if (g < used) {
-            constexpr int kN = 8 * C::kTerms;  // columns of eight rows
-            uint32_t u[kH][kN];
+            uint32_t u[kH][kGo * kN];
 #pragma unroll
             for (int k = 0; k < kH; ++k) {
-              if constexpr (kE4m3) umma::ld16_nowait(to + k * C::kCols + g * kN, u[k]);
-              else ld8_nowait(to + k * C::kCols + g * kN, u[k]);
+              if constexpr (kE4m3) umma::ld16_nowait(to + k * C::kOCols + g * kN, u[k]);
+              else ld8_nowait(to + k * C::kOCols + g * kN, u[k]);
             }
             umma::wait_ld();
 #pragma unroll
-            for (int e = 0; e < 8; e += 4) {
+            for (int e = 0; e < 8 * kGo; e += 4) {
               const int r = g * 8 + e;
               const float4 w4 = *reinterpret_cast<const float4*>(w_s + roff + r);
               float4 k4 = make_float4(1.f, 1.f, 1.f, 1.f);
@@ -1077,9 +1114,10 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
                 float2 o[2];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                  const uint32_t* c4 = u[k] + (kE4m3 ? 2 * e + 4 * y : e + 2 * y);
-                  o[y] = make_float2(__uint_as_float(c4[0]), __uint_as_float(c4[1]));
-                  if constexpr (kE4m3) o[y] = __fadd2_rn(o[y], make_float2(__uint_as_float(c4[2]), __uint_as_float(c4[3])));
+                  const int at = C::kSumTerms ? 2 * (e & 7) + 4 * y + 2 * (e >> 3) : kE4m3 ? 2 * e + 4 * y : e + 2 * y;
+                  o[y] = make_float2(__uint_as_float(u[k][at]), __uint_as_float(u[k][at + 1]));
+                  if constexpr (C::kOTerms == 2)
+                    o[y] = __fadd2_rn(o[y], make_float2(__uint_as_float(u[k][at + 2]), __uint_as_float(u[k][at + 3])));
                 }
                 float2 &lo = acc[k][r / 2], &hi = acc[k][r / 2 + 1];
                 if (moved) {
@@ -1122,7 +1160,6 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         __syncwarp();
         if (lane == 0) {
           arrive(&B->o_empty[ob]);
-          if (C::kOBuf == 1) arrive(&B->st_empty[b]);
         }
       }
       wait_warp(&B->checked[seg % kMarks], (seg / kMarks) & 1, abort);
@@ -1135,36 +1172,45 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
       if (s.t0 == 0 && s.t1 == s.tiles) {
         if (bad) continue;
         if (ot < a.rows) fin[ot] = l_run == 0.f ? 0.f : __fdividef(1.f, l_run);
-        // Four rows at a time through shared memory, a thread then has neighbouring values of one row. The loop
-        // is not unrolled (the registers' choice is): code that runs once per segment costs its fetches.
-        float* stage = reinterpret_cast<float*>(rest + C::oStage) + og * (4 * kH * 128);
-        const int mine = ot >> 5, col = (ot & 31) * (4 * kH);  // row of the four, first value
+        // A few rows at a time through shared memory, a thread then has neighbouring values of one or two rows. The
+        // loop is not unrolled (the registers' choice is): code that runs once per segment costs its fetches.
+        constexpr int kS = C::kStageRows, kY = kS / 4;
+        float* stage = reinterpret_cast<float*>(rest + C::oStage) + og * (kS * kH * 128);
+        const int mine = ot >> 5, col = (ot & 31) * (4 * kH);  // rows `mine` and `mine` + 4 of the eight, first value
 #pragma unroll 1
-        for (int r4 = 0; r4 < rows; r4 += 4) {
-          const int r = r4 + mine, rr = r0 + r, j = rr / p.G, g = rr - j * p.G;
-          const size_t at = (((size_t)s.n * p.P + j) * p.Hq + h * p.G + g) * D + half * 128 + col;
-          uint2 gate[kH];
-          if (p.gate && r < rows) {
+        for (int rs = 0; rs < rows; rs += kS) {
+          size_t at[kY];
+          uint2 gate[kY][kH];
 #pragma unroll
-            for (int e = 0; e < kH; ++e) gate[e] = *reinterpret_cast<const uint2*>(p.gate + at + 4 * e);
+          for (int y = 0; y < kY; ++y) {
+            const int r = rs + mine + 4 * y, rr = r0 + r, j = rr / p.G, g = rr - j * p.G;
+            at[y] = (((size_t)s.n * p.P + j) * p.Hq + h * p.G + g) * D + half * 128 + col;
+            if (p.gate && r < rows) {
+#pragma unroll
+              for (int e = 0; e < kH; ++e) gate[y][e] = *reinterpret_cast<const uint2*>(p.gate + at[y] + 4 * e);
+            }
           }
           sync_group(bar);
 #pragma unroll
-          for (int c4 = 0; c4 < kR; c4 += 4)
-            if (c4 == r4) {
+          for (int c = 0; c < kR; c += kS)
+            if (c == rs) {
 #pragma unroll
               for (int k = 0; k < kH; ++k)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  stage[e * (kH * 128) + k * 128 + ot] = e & 1 ? acc[k][(c4 + e) / 2].y : acc[k][(c4 + e) / 2].x;
+                for (int e = 0; e < kS; ++e)
+                  stage[e * (kH * 128) + k * 128 + ot] = e & 1 ? acc[k][(c + e) / 2].y : acc[k][(c + e) / 2].x;
             }
           sync_group(bar);
-          if (r < rows) {
+#pragma unroll
+          for (int y = 0; y < kY; ++y) {
+            const int r = rs + mine + 4 * y;
+            if (r >= rows) continue;
             const float f = fin[roff + r];
 #pragma unroll
             for (int e = 0; e < kH; ++e) {
-              const float4 o = *reinterpret_cast<const float4*>(stage + mine * (kH * 128) + col + 4 * e);
-              *reinterpret_cast<uint2*>(p.out + at + 4 * e) = to_out(make_float4(o.x * f, o.y * f, o.z * f, o.w * f), p.gate, gate[e]);
+              const float4 o = *reinterpret_cast<const float4*>(stage + (mine + 4 * y) * (kH * 128) + col + 4 * e);
+              *reinterpret_cast<uint2*>(p.out + at[y] + 4 * e) =
+                  to_out(make_float4(o.x * f, o.y * f, o.z * f, o.w * f), p.gate, gate[y][e]);
             }
           }
         }
