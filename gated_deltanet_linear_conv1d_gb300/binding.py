@@ -121,6 +121,10 @@ def header_symbols() -> list[str]:
 # A call's host time is mostly these checks (a decode-sized kernel runs for a few microseconds), so the common
 # case of each is one expression; addresses go to ctypes as integers.
 
+_Tensor, _byref = torch.Tensor, ctypes.byref
+_bf16, _f32, _f64, _i32, _i64 = torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.int64
+
+
 def _ptr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
@@ -140,18 +144,21 @@ def _stream(stream) -> int:
 def _rows(t, name: str, shape):
     """(pointer, token stride, head stride) of a bf16 operand [T, H, D] whose head rows are contiguous;
     tokens and heads may be strided (a view into a packed projection)."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (libgdn has no CPU path)")
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must have dtype {torch.bfloat16}, got {t.dtype}")
+    if t.dtype is not _bf16:
+        raise TypeError(f"{name} must have dtype {_bf16}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     st, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name}'s head rows must be contiguous")
     return t.data_ptr(), st, sh
+
+
+_NO_ROWS = (None, 0, 0)
 
 
 def _need(t, name: str, dtype, shape=None, optional: bool = False):
@@ -173,6 +180,16 @@ def _need(t, name: str, dtype, shape=None, optional: bool = False):
         raise ValueError(f"{name} must be contiguous")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _arg(t, name: str, dtype, shape=None, optional: bool = False):
+    """The address of a tensor that _need accepts (None where an optional one is left out)."""
+    if t is None and optional:
+        return None
+    if type(t) is not _Tensor or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or (
+            shape is not None and t.shape != shape):
+        _need(t, name, dtype, shape)
+    return t.data_ptr()
 
 
 def _scratch(nbytes: int, device, stream) -> torch.Tensor:
@@ -468,10 +485,9 @@ def gdn_kv_cache_write(cache, k, v, kv_slot, dev_err=None, stream=None):
     """k, v [T, Hkv, D] bf16 (views with contiguous head rows) into slots kv_slot [T] (negative: skipped)."""
     T = kv_slot.shape[0]
     shape = (T, cache.num_kv_heads, cache.head_dim)
-    kp, vp = _rows(k, "k", shape), _rows(v, "v", shape)
-    _need(kv_slot, "kv_slot", torch.int32, (T,))
-    _need(dev_err, "dev_err", torch.int32, (1,), optional=True)
-    _check(_lib.gdn_kv_cache_write(ctypes.byref(cache), *kp, *vp, _ptr(kv_slot), T, _ptr(dev_err), _stream(stream)),
+    _check(_lib.gdn_kv_cache_write(_byref(cache), *_rows(k, "k", shape), *_rows(v, "v", shape),
+                                   _arg(kv_slot, "kv_slot", _i32, (T,)), T,
+                                   _arg(dev_err, "dev_err", _i32, (1,), True), _stream(stream)),
            "gdn_kv_cache_write")
 
 
@@ -480,13 +496,10 @@ def gdn_kv_cache_read(cache, block_table, start, k_out, v_out, dev_err=None, str
     N, max_pages = block_table.shape
     T = k_out.shape[0]
     shape = (T, cache.num_kv_heads, cache.head_dim)
-    _need(block_table, "block_table", torch.int32)
-    _need(start, "start", torch.int32, (N + 1,))
-    _need(k_out, "k_out", torch.bfloat16, shape)
-    _need(v_out, "v_out", torch.bfloat16, shape)
-    _need(dev_err, "dev_err", torch.int32, (1,), optional=True)
-    _check(_lib.gdn_kv_cache_read(ctypes.byref(cache), _ptr(block_table), max_pages, _ptr(start), N, T, _ptr(k_out),
-                                  _ptr(v_out), _ptr(dev_err), _stream(stream)), "gdn_kv_cache_read")
+    _check(_lib.gdn_kv_cache_read(_byref(cache), _arg(block_table, "block_table", _i32), max_pages,
+                                  _arg(start, "start", _i32, (N + 1,)), N, T, _arg(k_out, "k_out", _bf16, shape),
+                                  _arg(v_out, "v_out", _bf16, shape), _arg(dev_err, "dev_err", _i32, (1,), True),
+                                  _stream(stream)), "gdn_kv_cache_read")
 
 
 def gdn_qk_norm_rope(q, k, q_gamma, k_gamma, eps, positions, inv_freq, q_out, k_out=None, v=None, cache=None,
@@ -494,29 +507,24 @@ def gdn_qk_norm_rope(q, k, q_gamma, k_gamma, eps, positions, inv_freq, q_out, k_
     """Head norms and rotation of q [T, Hq, D] and k [T, Hkv, D] (views with contiguous head rows) into q_out, k_out;
     with a cache, k and v also to slots kv_slot. inv_freq [rotary_dim / 2] fp64, or None for no rotation. q and
     q_out None: the keys alone."""
-    T, Hkv, D = k.shape
+    T, Hkv, D = kv = k.shape
     Hq = Hkv if q is None else q.shape[1]
-    qp = (None, 0, 0) if q is None else _rows(q, "q", (T, Hq, D))
-    kp = _rows(k, "k", (T, Hkv, D))
-    vp = (None, 0, 0) if v is None else _rows(v, "v", (T, Hkv, D))
-    _need(q_gamma, "q_gamma", torch.float32, (D,), optional=q is None)
-    _need(k_gamma, "k_gamma", torch.float32, (D,))
+    qs = (T, Hq, D)
     rotary = 0 if inv_freq is None else 2 * inv_freq.numel()
-    _need(inv_freq, "inv_freq", torch.float64, (rotary // 2,), optional=True)
-    _need(positions, "positions", torch.int32, (T,), optional=rotary == 0)
-    _need(q_out, "q_out", torch.bfloat16, (T, Hq, D), optional=q is None)
-    _need(k_out, "k_out", torch.bfloat16, (T, Hkv, D), optional=cache is not None)
-    _need(kv_slot, "kv_slot", torch.int32, (T,), optional=cache is None)
-    _need(dev_err, "dev_err", torch.int32, (1,), optional=True)
-    _check(_lib.gdn_qk_norm_rope(*qp, *kp, _ptr(q_gamma), _ptr(k_gamma), float(eps), _ptr(positions), _ptr(inv_freq),
-                                 rotary, int(bool(interleaved)), _ptr(q_out), _ptr(k_out), *vp,
-                                 None if cache is None else ctypes.byref(cache), _ptr(kv_slot), T, Hq, Hkv, D,
-                                 _ptr(dev_err), _stream(stream)), "gdn_qk_norm_rope")
+    _check(_lib.gdn_qk_norm_rope(*(_NO_ROWS if q is None else _rows(q, "q", qs)), *_rows(k, "k", kv),
+                                 _arg(q_gamma, "q_gamma", _f32, (D,), q is None), _arg(k_gamma, "k_gamma", _f32, (D,)),
+                                 float(eps), _arg(positions, "positions", _i32, (T,), rotary == 0),
+                                 _arg(inv_freq, "inv_freq", _f64, (rotary // 2,), True), rotary,
+                                 1 if interleaved else 0, _arg(q_out, "q_out", _bf16, qs, q is None),
+                                 _arg(k_out, "k_out", _bf16, kv, cache is not None),
+                                 *(_NO_ROWS if v is None else _rows(v, "v", kv)),
+                                 None if cache is None else _byref(cache),
+                                 _arg(kv_slot, "kv_slot", _i32, (T,), cache is None), T, Hq, Hkv, D,
+                                 _arg(dev_err, "dev_err", _i32, (1,), True), _stream(stream)), "gdn_qk_norm_rope")
 
 
 def gdn_tree_attention_workspace_bytes(cache, num_seqs: int, num_pos: int, num_q_heads: int) -> int:
-    return int(_lib.gdn_tree_attention_workspace_bytes(ctypes.byref(cache), int(num_seqs), int(num_pos),
-                                                       int(num_q_heads)))
+    return int(_lib.gdn_tree_attention_workspace_bytes(_byref(cache), int(num_seqs), int(num_pos), int(num_q_heads)))
 
 
 def gdn_tree_attention(cache, q, block_table, ctx_len, scale, out, num_pos: int = 1, tree_mask=None, gate=None,
@@ -525,20 +533,16 @@ def gdn_tree_attention(cache, q, block_table, ctx_len, scale, out, num_pos: int 
     tree_mask [N, num_pos] int64, bit i of a node's word: it sees node i; None: a chain."""
     N, max_pages = block_table.shape
     shape = (N * num_pos, q.shape[1], cache.head_dim)
-    _need(q, "q", torch.bfloat16, shape)
-    _need(block_table, "block_table", torch.int32)
-    _need(ctx_len, "ctx_len", torch.int32, (N,))
-    _need(tree_mask, "tree_mask", torch.int64, (N, num_pos), optional=True)
-    _need(gate, "gate", torch.bfloat16, shape, optional=True)
-    _need(out, "out", torch.bfloat16, shape)
-    _need(dev_err, "dev_err", torch.int32, (1,), optional=True)
     if workspace is None:
         need = gdn_tree_attention_workspace_bytes(cache, N, num_pos, shape[1])
         workspace = _scratch(need, q.device, stream)
-    _check(_lib.gdn_tree_attention(ctypes.byref(cache), _ptr(q), _ptr(block_table), max_pages, _ptr(ctx_len),
-                                   _ptr(tree_mask), _ptr(gate), float(scale), _ptr(out), N, int(num_pos), shape[1],
-                                   _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_err),
-                                   _stream(stream)), "gdn_tree_attention")
+    _check(_lib.gdn_tree_attention(_byref(cache), _arg(q, "q", _bf16, shape), _arg(block_table, "block_table", _i32),
+                                   max_pages, _arg(ctx_len, "ctx_len", _i32, (N,)),
+                                   _arg(tree_mask, "tree_mask", _i64, (N, num_pos), True),
+                                   _arg(gate, "gate", _bf16, shape, True), float(scale), _arg(out, "out", _bf16, shape),
+                                   N, int(num_pos), shape[1], _arg(workspace, "workspace", workspace.dtype),
+                                   workspace.nbytes,
+                                   _arg(dev_err, "dev_err", _i32, (1,), True), _stream(stream)), "gdn_tree_attention")
 
 
 def gdn_spec_commit(dims, accepted, spec_slot_idx, slot_idx, state=None, conv_hist=None,

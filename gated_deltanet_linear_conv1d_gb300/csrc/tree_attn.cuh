@@ -108,6 +108,7 @@ struct Cfg {
   static constexpr int kAhead = kSplit ? 1 : 2;
   // query buffers: a tile's scores wait for no output that follows them, though every segment have one tile
   static constexpr int kQBuf = kAhead + 1;
+  static constexpr int kSegCost = kRows == 16 ? (kE4m3 ? 4 : 2) : kE4m3 ? 7 : 5;
   static constexpr int kOutGroups = kRows == 16 ? 1 : 2;    // at few rows a group's fixed work outweighs the rows'
   static constexpr int kOutWarp = 8, kCopyWarp = kOutWarp + 4 * kOutGroups;  // first warps of the roles
   static constexpr int kMmaWarp = kCopyWarp + 1, kQueryWarp = kCopyWarp + 2, kCheckWarp = kCopyWarp + 3;
@@ -140,7 +141,7 @@ struct Cfg {
   static_assert(2 * kCols + kOBuf * kHalves * kOCols <= 512, "tensor memory");
 };
 
-// One CTA's piece of the line of tiles.
+// One CTA's piece of the line. `t`: where it begins in the unit, whose first kSegCost places hold no tile.
 struct Plan {
   long long total, lo;
   int count, n, u, t;
@@ -166,7 +167,7 @@ static_assert(sizeof(Bars) <= 1408, "barrier area");
 // The piece's segments: runs of tiles of one (request n, unit u = head x row tiles + row tile).
 struct Seg {
   int n, u, t0, t1, tiles, len, ctx;
-  long long first;  // the unit's first tile in the line
+  long long first;  // the unit's first place in the line
 };
 
 __device__ __forceinline__ int tiles_of(const Args& a, int ctx, bool* too_long = nullptr) {
@@ -179,6 +180,7 @@ __device__ __forceinline__ int tiles_of(const Args& a, int ctx, bool* too_long =
   return (int)((len + kTile - 1) / kTile);
 }
 
+template <int kSegCost>
 struct Walk {
   int n, u, t, left, units, tiles, ctx;
   long long at;
@@ -191,22 +193,24 @@ struct Walk {
     tiles = tiles_of(a, ctx);
   }
   __device__ __forceinline__ bool next(const Args& a, Seg& s) {
-    if (left <= 0) return false;
-    while (tiles == 0) {  // the piece has tiles left, so a request with some follows
-      ++n;
-      load(a);
+    while (left > 0) {
+      while (tiles == 0) {  // the piece has places left, so a request with some follows
+        ++n;
+        load(a);
+      }
+      const int take = min(tiles + kSegCost - t, left);
+      s = Seg{n, u, max(t - kSegCost, 0), t + take - kSegCost, tiles, ctx + a.p.P, ctx, at - t};
+      left -= take;
+      at += take;
+      t = 0;
+      if (++u == units) {
+        u = 0;
+        ++n;
+        if (left > 0) load(a);
+      }
+      if (s.t1 > 0) return true;
     }
-    const int take = min(tiles - t, left);
-    s = Seg{n, u, t, t + take, tiles, ctx + a.p.P, ctx, at - t};
-    left -= take;
-    at += take;
-    t = 0;
-    if (++u == units) {
-      u = 0;
-      ++n;
-      if (left > 0) load(a);
-    }
-    return true;
+    return false;
   }
 };
 
@@ -507,7 +511,10 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
     const int per = (p.N + kThreads - 1) / kThreads, n0 = min(p.N, tid * per), n1 = min(p.N, n0 + per);
     long long mine = 0;
     bool too_long = false;
-    for (int n = n0; n < n1; ++n) mine += tiles_of(a, p.ctx[n], &too_long);
+    for (int n = n0; n < n1; ++n) {
+      const int tiles = tiles_of(a, p.ctx[n], &too_long);
+      mine += tiles + (tiles > 0 ? C::kSegCost : 0);
+    }
     if (too_long && blockIdx.x == 0) report(p.dev_err, GDN_DEVERR_OFFSETS);
     long long upto = mine;
 #pragma unroll
@@ -563,10 +570,10 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
     if (blockIdx.x < ctas && before * units <= lo && lo < (before + mine) * units) {
       long long at = before * units;
       for (int n = n0; n < n1; ++n) {
-        const long long here = (long long)tiles_of(a, p.ctx[n]) * units;
+        const int tiles = tiles_of(a, p.ctx[n]), places = tiles + (tiles > 0 ? C::kSegCost : 0);
+        const long long here = (long long)places * units;
         if (lo < at + here) {
-          const int tiles = (int)(here / units);
-          B->plan = Plan{total, lo, (int)(hi - lo), n, (int)((lo - at) / tiles), (int)((lo - at) % tiles)};
+          B->plan = Plan{total, lo, (int)(hi - lo), n, (int)((lo - at) / places), (int)((lo - at) % places)};
           break;
         }
         at += here;
@@ -588,10 +595,9 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
   }
   // All warps but the copies' load the first query rows: no tile can be scored before.
   if (warp != C::kCopyWarp) {
-    if (plan.count > 0) {
-      Walk walk(a, plan);
-      Seg s;
-      walk.next(a, s);
+    Walk<C::kSegCost> walk(a, plan);
+    Seg s;
+    if (walk.next(a, s)) {
       load_queries<D, kE4m3, kRows>(a, s, rest, 0, warp < C::kCopyWarp ? warp : warp - 1, kThreads / 32 - 1);
       umma::fence_proxy_async_smem();
     }
@@ -617,7 +623,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         if (++st == C::kStages) st = 0, phase ^= 1;
       }
     };
-    Walk walk(a, plan);
+    Walk<C::kSegCost> walk(a, plan);
     Seg s;
     int held[C::kAhead];  // rows of the last tiles, their V still to come
     int marks = 0;
@@ -731,7 +737,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         st = st2 + 1 == C::kStages ? 0 : st2 + 1;
       }
     };
-    Walk walk(a, plan);
+    Walk<C::kSegCost> walk(a, plan);
     Seg s;
     while (ok && walk.next(a, s)) {
       const int qb = seg % C::kQBuf;
@@ -769,7 +775,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
     __syncwarp();
   } else if (warp == C::kQueryWarp) {
     // ------------------------------------------------------------ query rows (the first segment's are there)
-    Walk walk(a, plan);
+    Walk<C::kSegCost> walk(a, plan);
     Seg s;
     int seg = 0;
     bool ok = true;
@@ -789,9 +795,10 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
     // A weight of zero does not take a NaN or an infinity out of a product. Values behind the last token
     // become zeros (as far as its box goes: behind it they are zeros already); a drafted token's that are no
     // numbers too, and the output warps add them to the rows that see the token.
-    Walk walk(a, plan);
+    Walk<C::kSegCost> walk(a, plan);
     Seg s;
-    int seg = 0, marks = 0, i0 = 0;
+    int seg = 0, marks = 0, i0 = 0, tiles = 0;  // `tiles`: of the piece
+    for (Walk<C::kSegCost> all(a, plan); all.next(a, s);) tiles += s.t1 - s.t0;
     bool ok = true;
     while (ok && walk.next(a, s)) {
       const int h = s.u / a.row_tiles;
@@ -824,7 +831,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         // V's place in the order of copies
-        const int first = C::kBlk * min(i + 1 + C::kAhead, plan.count) + C::kBlk * i;
+        const int first = C::kBlk * min(i + 1 + C::kAhead, tiles) + C::kBlk * i;
         auto piece = [&](int k) {
           const int row = row0 + k / (8 * C::kBlk), x = k % (8 * C::kBlk);
           return reinterpret_cast<uint4*>(smem + (first + (x >> 3)) % C::kStages * kBlock + row * 128) + (x & 7);
@@ -880,7 +887,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
     float* tile_s = reinterpret_cast<float*>(rest + C::oTile);
     float* warp_s = reinterpret_cast<float*>(rest + C::oWarp) + warp * kR;
     const float* scales = reinterpret_cast<const float*>(rest + C::oSc);
-    Walk walk(a, plan);
+    Walk<C::kSegCost> walk(a, plan);
     Seg s;
     int i = 0, seg = 0;
     while (walk.next(a, s)) {
@@ -1052,7 +1059,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
     float* ab = reinterpret_cast<float*>(rest + C::oAb) + og * 4 * kRows;
     float* fin = reinterpret_cast<float*>(rest + C::oFin) + og * 2 * kRows;
     int marks = 0;
-    Walk walk(a, plan);
+    Walk<C::kSegCost> walk(a, plan);
     Seg s;
     int i = 0, seg = 0;
     while (walk.next(a, s)) {
@@ -1233,7 +1240,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         if (C::kOutGroups == 1) reinterpret_cast<int*>(mine)[2 * a.rows + 1] = 0;
         if (s.t0 == 0 && og == 0) {
           const int ctas = (int)min((long long)gridDim.x, plan.total);
-          static_cast<Desc*>(p.workspace)[blockIdx.x] = Desc{1, s.n, s.u, cta_of(s.first + s.tiles - 1, plan.total, ctas)};
+          static_cast<Desc*>(p.workspace)[blockIdx.x] = Desc{1, s.n, s.u, cta_of(s.first + C::kSegCost + s.tiles - 1, plan.total, ctas)};
         }
       }
     }
