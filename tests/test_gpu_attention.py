@@ -515,6 +515,82 @@ def test_a_pool_beyond_32_bit_offsets(b, err, fmt):
     assert bool((pool.v[-1, :, -1] != small["v"][-1, :, -1]).any())
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("scale", [0.0, -0.0625, 2.0 ** -30, 1.0])
+def test_scales_of_any_sign_and_size(b, err, fmt, scale):
+    pool, table, ctx, q, _ = case("24x4x256", fmt, 64, [400, 0, 129], 7)
+    mask = R.tree(3, 7)[1].cuda()
+    out = attend(b, pool, q, table, ctx, scale, 7, mask, dev_err=err)
+    ref, bound, _ = R.tree_attention(pool, q, table, ctx, scale, 7, mask)
+    inside(out, ref, bound, "out")
+    assert b.gdn_read_device_error(err) == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_requests_that_share_pages(b, err, fmt):
+    """A common prefix, and one request's whole table twice."""
+    pool, table, ctx, q, scale = case("24x4x256", fmt, 16, [600, 640, 600], 3)
+    table[1, :30] = table[0, :30]
+    table[2] = table[0]
+    out = attend(b, pool, q, table, ctx, scale, 3, dev_err=err)
+    ref, bound, _ = R.tree_attention(pool, q, table, ctx, scale, 3)
+    inside(out, ref, bound, "out")
+    assert b.gdn_read_device_error(err) == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,nodes", [("24x4x256", 1), ("24x4x256", 5), ("24x4x256", 9), ("5x5x128", 2)])
+def test_many_short_requests(b, err, fmt, heads, nodes):
+    """Pieces of many units: more segments than barriers and buffers, requests without tiles between them."""
+    rng = np.random.default_rng(nodes)
+    lens = [int(x) for x in rng.choice([-1, 0, 1, 100, 127, 128, 129, 300], 500)]
+    pool, table, ctx, q, scale = case(heads, fmt, 16, lens, nodes)
+    out = torch.full_like(q, 7.0)
+    attend(b, pool, q, table, ctx, scale, nodes, out=out, dev_err=err)
+    ref, bound, live = R.tree_attention(pool, q, table, ctx, scale, nodes)
+    inside(out[live], ref[live], bound[live], "out")
+    assert bool((out[~live] == 7.0).all()) and b.gdn_read_device_error(err) == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_most_rows_and_most_requests(b, err, fmt):
+    pool, table, ctx, q, scale = case((64, 1, 128), fmt, 64, [1000], 64)  # 4096 rows of one kv head
+    out = attend(b, pool, q, table, ctx, scale, 64, dev_err=err)
+    ref, bound, _ = R.tree_attention(pool, q, table, ctx, scale, 64)
+    inside(out, ref, bound, "rows")
+    some, n = {0: 5, 40000: 300, 65534: 17}, 65535
+    pool, few, _, _, scale = case((1, 1, 128), fmt, 16, list(some.values()), 1)
+    table = torch.full((n, few.shape[1]), -1, dtype=torch.int32, device="cuda")
+    ctx = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    at = torch.tensor(list(some), device="cuda")
+    table[at], ctx[at] = few, torch.tensor(list(some.values()), dtype=torch.int32, device="cuda")
+    q = randn(n, 1, 128, seed=1).to(torch.bfloat16)
+    out = torch.full_like(q, 7.0)
+    attend(b, pool, q, table, ctx, scale, 1, out=out, dev_err=err)
+    ref, bound, _ = R.tree_attention(pool, q[at], few, ctx[at], scale, 1)
+    inside(out[at], ref, bound, "requests")
+    out[at] = 7.0
+    assert bool((out == 7.0).all()) and b.gdn_read_device_error(err) == 0
+
+
+def test_rows_in_place_and_rows_of_stride_zero(b, err):
+    T = 300
+    one, f = torch.ones(256, device="cuda"), torch.rand(32, dtype=torch.float64, device="cuda")
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    q, k = randn(T, 24, 256).to(torch.bfloat16), randn(T, 4, 256, seed=1).to(torch.bfloat16)
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    b.gdn_qk_norm_rope(q, k, one, one, 1e-6, pos, f, qo, ko, dev_err=err)
+    b.gdn_qk_norm_rope(q, k, one, one, 1e-6, pos, f, q, ko, dev_err=err)
+    assert torch.equal(bits(q), bits(qo))
+    pools = [R.Pool(5, 4, 64, 256, "e4m3") for _ in range(2)]
+    slots = torch.randperm(320, device="cuda")[:T].to(torch.int32)
+    b.gdn_kv_cache_write(pools[0].handle(b), k[:1].expand(T, -1, -1), k[:, :1].expand(-1, 4, -1), slots, dev_err=err)
+    b.gdn_kv_cache_write(pools[1].handle(b), k[:1].repeat(T, 1, 1), k[:, :1].repeat(1, 4, 1), slots, dev_err=err)
+    for name in ("k", "v", "k_scale", "v_scale"):
+        assert torch.equal(bits(getattr(pools[0], name)), bits(getattr(pools[1], name))), name
+    assert b.gdn_read_device_error(err) == 0
+
+
 def test_guard_bands(b, err):
     """Outputs, pools and workspace between bands that every call must leave alone."""
     from tests.test_gpu_guards import Guarded
