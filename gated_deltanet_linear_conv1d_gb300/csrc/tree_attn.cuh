@@ -94,21 +94,22 @@ struct Cfg {
   static constexpr int kBlk = D * (kE4m3 ? 1 : 2) / 128;  // ring blocks of a tile's K, and of its V
   static constexpr int kHalves = D / 128;
   static constexpr int kTerms = kE4m3 ? 2 : 1;
-  static constexpr int kCols = kTerms * kRows;                // of the scores
-  // The two terms of P are neighbouring columns of one product, added as the output is read; with 64 rows two
-  // products add them up in tensor memory instead (a third more time for the MMAs, which have it, half the columns
-  // to read, and room for two outputs).
+  // The two terms of P are neighbouring columns of one product, those of Q rp columns apart, added as the result is
+  // read; with 64 rows two products add them up in tensor memory instead (the MMAs have the time, the threads half the
+  // columns to read).
   static constexpr bool kSumTerms = kE4m3 && kRows == 64;
   static constexpr int kOTerms = kSumTerms ? 1 : kTerms;
+  static constexpr int kQCols = kTerms * kRows;               // rows of Q's operand
+  static constexpr int kCols = kOTerms * kRows;               // of the scores
   static constexpr int kOCols = kOTerms * kRows;              // of the output
-  static constexpr int kOBuf = 2;
-  static constexpr int kQBytes = kCols * 128 * kBlk;
+  static constexpr int kOBuf = 2;                            // outputs, as many as tiles of weights: see o_empty
+  static constexpr int kQBytes = kQCols * 128 * kBlk;
   static constexpr bool kSplit = kRows == 64;               // the softmax groups share each tile's rows
   // Tiles whose scores are ahead of the output: when a softmax group ends a tile, its next one's scores are there.
   static constexpr int kAhead = kSplit ? 1 : 2;
   // query buffers: a tile's scores wait for no output that follows them, though every segment have one tile
   static constexpr int kQBuf = kAhead + 1;
-  static constexpr int kSegCost = kRows == 16 ? (kE4m3 ? 4 : 2) : kE4m3 ? 7 : 5;
+  static constexpr int kSegCost = kRows == 16 ? (kE4m3 ? 4 : 2) : kE4m3 ? 9 : 5;
   static constexpr int kOutGroups = kRows == 16 ? 1 : 2;    // at few rows a group's fixed work outweighs the rows'
   static constexpr int kOutWarp = 8, kCopyWarp = kOutWarp + 4 * kOutGroups;  // first warps of the roles
   static constexpr int kMmaWarp = kCopyWarp + 1, kQueryWarp = kCopyWarp + 2, kCheckWarp = kCopyWarp + 3;
@@ -153,7 +154,7 @@ struct Bars {
   uint64_t v_issued[kMarks];              // by last tile (one with drafted tokens) of the piece: V's copies run
   uint64_t v_clean[kMarks];               // and V is ready for the MMAs
   uint64_t checked[kMarks];               // by segment
-  uint64_t q_full[3], q_empty[3], s_full[2], s_empty[2], p_full[2], p_empty[2], o_full[2], o_empty[2];
+  uint64_t q_full[3], q_empty[3], s_full[2], s_empty[2], p_full[2], o_full[2], o_empty[2];
   uint64_t st_full[2], sc_full[kScSlots], sc_empty[kScSlots], drain;
   uint32_t tmem;
   int abort;
@@ -434,63 +435,63 @@ __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned 
   float* qs_s = reinterpret_cast<float*>(rest + C::oQs) + qb * kRows;
   uint64_t* mask_s = reinterpret_cast<uint64_t*>(rest + C::oMask) + qb * kRows;
   if (share == 0)
-          for (int r = lane; r < rp; r += 32) {
-          const int j = (r0 + r) / p.G;
-          uint64_t m = 0;
-          if (r < a.rows && j < p.P) m = p.mask ? __ldg(p.mask + (size_t)s.n * p.P + j) : j == 63 ? ~0ull : (2ull << j) - 1;
-          mask_s[r] = m;
-        }
-        // rows on their way at once: more hide their loads at the start of a short segment, fewer leave the instruction
+    for (int r = lane; r < rp; r += 32) {
+      const int j = (r0 + r) / p.G;
+      uint64_t m = 0;
+      if (r < a.rows && j < p.P) m = p.mask ? __ldg(p.mask + (size_t)s.n * p.P + j) : j == 63 ? ~0ull : (2ull << j) - 1;
+      mask_s[r] = m;
+    }
+  // rows on their way at once: more hide their loads at the start of a short segment, fewer leave the instruction
   // cache to the loops (256 x 1k..8k tokens with 6 rows: 288 us with four, 294 with eight; 32 trees of 48 rows: 196 and 177)
   constexpr int kBatch = kRows == 16 ? 4 : 8;
-        for (int rb = share * kBatch; rb < rp; rb += shares * kBatch) {
-          uint4 raw[kBatch];
-  #pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int r = rb + i, j = (r0 + r) / p.G, g = (r0 + r) % p.G;
-            raw[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < a.rows && j < p.P && lane < D / 8)
-              raw[i] = *reinterpret_cast<const uint4*>(p.q + (((size_t)s.n * p.P + j) * p.Hq + h * p.G + g) * D + lane * 8);
-            raw[i] = make_uint4((raw[i].x ^ sign) & mask_q, (raw[i].y ^ sign) & mask_q, (raw[i].z ^ sign) & mask_q,
-                                (raw[i].w ^ sign) & mask_q);
-          }
-  #pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int r = rb + i;
-            if constexpr (!kE4m3) {
-              // eight values are one 16-byte piece of block lane / 8
-              if (lane < D / 8)
-                *reinterpret_cast<uint4*>(q_s + (lane >> 3) * (C::kCols * 128) + swz(r, (lane & 7) * 16)) = raw[i];
-              if (lane == 0) qs_s[r] = fmaxf(to_log2, 1e-37f);
-            } else {
-              const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-              float x[8], most = 0.f;
-  #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                x[2 * e] = __uint_as_float(w[e] << 16);
-                x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-              }
-  #pragma unroll
-              for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(x[e]));
-              most = warp_max(most);
-              // a power of two that takes the largest value below 256; a row with an infinity has no scores
-              const int ex = (int)(__float_as_uint(most) >> 23) - 127;
-              const int up = most == 0.f ? 0 : min(7 - ex, 120);
-              const float f = __uint_as_float((uint32_t)(up + 127) << 23);
-  #pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] *= f;
-              uint2 first, second;
-              two_terms(x, first, second);
-              if (lane < D / 8) {
-                unsigned char* blk = q_s + (lane >> 4) * (C::kCols * 128);
-                *reinterpret_cast<uint2*>(blk + swz(r, (lane & 15) * 8)) = first;
-                *reinterpret_cast<uint2*>(blk + swz(rp + r, (lane & 15) * 8)) = second;
-              }
-              const float down = __uint_as_float((uint32_t)(127 - up) << 23);
-              if (lane == 0) qs_s[r] = ex == 128 ? __uint_as_float(0x7fffffffu) : fmaxf(to_log2 * down, 1e-37f);
-            }
-          }
+  for (int rb = share * kBatch; rb < rp; rb += shares * kBatch) {
+    uint4 raw[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = rb + i, j = (r0 + r) / p.G, g = (r0 + r) % p.G;
+      raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < a.rows && j < p.P && lane < D / 8)
+        raw[i] = *reinterpret_cast<const uint4*>(p.q + (((size_t)s.n * p.P + j) * p.Hq + h * p.G + g) * D + lane * 8);
+      raw[i] = make_uint4((raw[i].x ^ sign) & mask_q, (raw[i].y ^ sign) & mask_q, (raw[i].z ^ sign) & mask_q,
+                          (raw[i].w ^ sign) & mask_q);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = rb + i;
+      if constexpr (!kE4m3) {
+        // eight values are one 16-byte piece of block lane / 8
+        if (lane < D / 8)
+          *reinterpret_cast<uint4*>(q_s + (lane >> 3) * (C::kQCols * 128) + swz(r, (lane & 7) * 16)) = raw[i];
+        if (lane == 0) qs_s[r] = fmaxf(to_log2, 1e-37f);
+      } else {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        float x[8], most = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[2 * e] = __uint_as_float(w[e] << 16);
+          x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(x[e]));
+        most = warp_max(most);
+        // a power of two that takes the largest value below 256; a row with an infinity has no scores
+        const int ex = (int)(__float_as_uint(most) >> 23) - 127;
+        const int up = most == 0.f ? 0 : min(7 - ex, 120);
+        const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= f;
+        uint2 first, second;
+        two_terms(x, first, second);
+        if (lane < D / 8) {
+          unsigned char* blk = q_s + (lane >> 4) * (C::kQCols * 128);
+          *reinterpret_cast<uint2*>(blk + swz(r, (lane & 15) * 8)) = first;
+          *reinterpret_cast<uint2*>(blk + swz(rp + r, (lane & 15) * 8)) = second;
+        }
+        const float down = __uint_as_float((uint32_t)(127 - up) << 23);
+        if (lane == 0) qs_s[r] = ex == 128 ? __uint_as_float(0x7fffffffu) : fmaxf(to_log2 * down, 1e-37f);
+      }
+    }
+  }
 }
 
 template <int D, bool kE4m3, int kRows>
@@ -542,7 +543,6 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         mbar_init(&B->s_full[i], 1);
         mbar_init(&B->s_empty[i], C::kSoftWarps);
         mbar_init(&B->p_full[i], C::kSoftWarps * 32);
-        mbar_init(&B->p_empty[i], 1);
         mbar_init(&B->o_full[i], 1);
         mbar_init(&B->o_empty[i], 4 * C::kOutGroups);
         mbar_init(&B->st_full[i], C::kSoftWarps * 32);
@@ -689,9 +689,9 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
     // 73 cycles to issue on an idle SM, and about 200 next to the other warps; its work is 41 at 16 columns.
     const int rp = kE4m3 ? (a.rows + 7) / 8 * 8 : (a.rows + 15) / 16 * 16;  // rows as columns of the MMAs
     // (an MMA of 128 lanes takes columns by sixteens)
-    const int N = C::kTerms * rp, NO = C::kSumTerms ? (rp + 15) / 16 * 16 : C::kOTerms * rp;
+    const int N = C::kSumTerms ? (rp + 15) / 16 * 16 : C::kTerms * rp;
     constexpr uint32_t kKind = kE4m3 ? umma::kKindF8 : umma::kKindF16, kType = kE4m3 ? umma::kE4M3 : umma::kBF16;
-    const uint32_t id_s = umma::idesc(kType, false, false, kTile, N), id_o = umma::idesc(kType, true, true, kTile, NO);
+    const uint32_t id_s = umma::idesc(kType, false, false, kTile, N), id_o = umma::idesc(kType, true, true, kTile, N);
     const uint32_t sQ = smem_u32(rest + C::oQ), sP = smem_u32(rest + C::oP);
     int st = 0, i = 0, seg = 0, marks = 0;
     uint32_t last_tiles = 0;  // bit i % 32: tile i has drafted tokens, the check warp cleans its V
@@ -701,11 +701,17 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
       ok = __all_sync(0xffffffffu, ok);
       return ok;
     };
+    // two at once: a wait whose phase is over costs 130 cycles of this warp, the tightest of all at few rows
+    auto wait_both = [&](uint64_t* x, uint32_t px, uint64_t* y, uint32_t py) {
+      const bool x_done = mbar_try_wait(x, px), y_done = mbar_try_wait(y, py);
+      if (!x_done || !y_done) ok = ok && wait(x, px, abort) && wait(y, py, abort);
+      ok = __all_sync(0xffffffffu, ok);
+      return ok;
+    };
     auto product_o = [&](int j) {
       const int b = j & 1, ob = j % C::kOBuf;
-      if (!wait_all(&B->p_full[b], (j >> 1) & 1) || !wait_all(&B->o_empty[ob], ((j / C::kOBuf) & 1) ^ 1) ||
-          !wait_all(&B->v_full[j % kSlots], (j / kSlots) & 1))
-        return;
+      // (the softmax waited for the output of two tiles back: its place in tensor memory is free)
+      if (!wait_both(&B->p_full[b], (j >> 1) & 1, &B->v_full[j % kSlots], (j / kSlots) & 1)) return;
       if ((last_tiles >> (j & 31)) & 1) {
         if (!wait_all(&B->v_clean[marks % kMarks], (marks / kMarks) & 1)) return;
         ++marks;
@@ -729,7 +735,6 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
           umma::commit(&B->empty[st]);
           if (!kE4m3) umma::commit(&B->empty[st2]);
           if (h == C::kHalves - 1) {
-            umma::commit(&B->p_empty[b]);
             umma::commit(&B->o_full[ob]);
           }
         }
@@ -744,16 +749,21 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
       if (!wait_all(&B->q_full[qb], (seg / C::kQBuf) & 1)) break;
       for (int t = s.t0; t < s.t1 && ok; ++t, ++i) {
         const int b = i & 1;
-        if (!wait_all(&B->s_empty[b], ((i >> 1) & 1) ^ 1) || !wait_all(&B->k_full[i % kSlots], (i / kSlots) & 1)) break;
+        if (!wait_both(&B->s_empty[b], ((i >> 1) & 1) ^ 1, &B->k_full[i % kSlots], (i / kSlots) & 1)) break;
         const bool last = (t + 1) * kTile > s.ctx;
         last_tiles = (last_tiles & ~(1u << (i & 31))) | ((last ? 1u : 0u) << (i & 31));
         for (int kb = 0; kb < C::kBlk; ++kb) {
           umma::fence_after_sync();
           if (elect_one()) {
             const uint64_t ka = umma::smem_desc_sw128(ring + st * kBlock);
-            const uint64_t qa = umma::smem_desc_sw128(sQ + qb * C::kQBytes + kb * (C::kCols * 128));
+            const uint64_t qa = umma::smem_desc_sw128(sQ + qb * C::kQBytes + kb * (C::kQCols * 128));
 #pragma unroll
             for (int k = 0; k < 4; ++k) umma::mma<kKind>(tmem + b * C::kCols, ka + 2 * k, qa + 2 * k, id_s, kb + k > 0);
+            if constexpr (C::kSumTerms) {  // the second terms, rp rows on
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                umma::mma<kKind>(tmem + b * C::kCols, ka + 2 * k, qa + rp * 8 + 2 * k, id_s, 1);
+            }
             umma::commit(&B->empty[st]);
             if (kb == C::kBlk - 1) {
               umma::commit(&B->s_full[b]);
@@ -919,15 +929,14 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
           if (g < used) {
             uint32_t u[4][2], w[4][2];
             ld_tile8(ts + g * 8, ts + (16u << 16) + g * 8, u);
-            if constexpr (kE4m3) ld_tile8(ts + rp + g * 8, ts + (16u << 16) + rp + g * 8, w);
+            if constexpr (C::kOTerms == 2) ld_tile8(ts + rp + g * 8, ts + (16u << 16) + rp + g * 8, w);
             umma::wait_ld();
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               float2 v = make_float2(__uint_as_float(u[k][0]), __uint_as_float(u[k][1]));
-              if constexpr (kE4m3) {
+              if constexpr (C::kOTerms == 2)
                 v = __fadd2_rn(v, make_float2(__uint_as_float(w[k][0]), __uint_as_float(w[k][1])));
-                v = __fmul2_rn(v, make_float2(sk[k], sk[k]));
-              }
+              if constexpr (kE4m3) v = __fmul2_rn(v, make_float2(sk[k], sk[k]));
               x[g][k] = v;
             }
           } else {
@@ -937,7 +946,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         umma::fence_before_sync();
         __syncwarp();
         if (lane == 0) arrive(&B->s_empty[b]);
-        // the statistics of two tiles back have been read
+        // the output of two tiles back has been read: its statistics, its product and the weights are done with
         wait_warp(&B->o_empty[b], ph ^ 1, abort);
         if ((t + 1) * kTile > s.ctx) {  // drafted tokens, or tokens behind the last
 #pragma unroll
@@ -987,7 +996,6 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
           if ((tid & 127) == 0 && roff == 0) tile_s[b * (kRows + 4) + kRows] = most * (1.f / 256.f);
         }
         __syncwarp();
-        wait_warp(&B->p_empty[b], ph ^ 1, abort);
         const uint32_t prow = smem_u32(rest + C::oP + b * kBlock) + (32 * w4 + lane) * 128;
         uint32_t even[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
