@@ -990,9 +990,9 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         if constexpr (kE4m3) {
           const float* at = max_b + kRows + wg;
           const float most = fmaxf(fmaxf(at[0], at[kRows + 4]), fmaxf(at[2 * (kRows + 4)], at[3 * (kRows + 4)]));
-          const float r = __fdividef(256.f, most);
+          const float up = most < 1e-30f ? 0x1p64f : most > 1e30f ? 0x1p-64f : 1.f, r = __fdividef(256.f, most * up);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) f[k] = sv[k] == 0.f ? 0.f : most < 1e-30f ? 256.f * (sv[k] / most) : sv[k] * r;
+          for (int k = 0; k < 4; ++k) f[k] = sv[k] == 0.f ? 0.f : sv[k] * up * r;
           if ((tid & 127) == 0 && roff == 0) tile_s[b * (kRows + 4) + kRows] = most * (1.f / 256.f);
         }
         __syncwarp();
@@ -1105,22 +1105,22 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         wait_warp(&B->o_full[ob], (i / C::kOBuf) & 1, abort);
         umma::fence_after_sync();
         const uint32_t to = umma::taddr(tmem, 32 * (warp & 3), 2 * C::kCols + (ob * C::kHalves + half) * C::kOCols + roff * C::kOTerms);
-        // rows e .. e + 3 of eight, from g * kN on: their pairs' columns, see where P is stored
-        constexpr int kN = 8 * C::kOTerms;  // columns of eight rows
-        constexpr int kGo = C::kSumTerms ? 2 : 1;  // eights at a time
+        // kN columns at a time hold rows r .. r + 3 and, behind or between them (where P is stored says which), the next
+        // four, or with summed terms the same four of the next eight
+        constexpr int kN = C::kOTerms * 8, kOn = C::kSumTerms ? 8 : 4;
 #pragma unroll
-        for (int g = 0; g < kR / 8; g += kGo)
-          if (g < used) {
-            uint32_t u[kH][kGo * kN];
+        for (int g = 0; g < kR / 8; ++g)
+          if (C::kSumTerms ? g / 2 * 2 < used : g < used) {
+            uint32_t u[kH][kN];
 #pragma unroll
             for (int k = 0; k < kH; ++k) {
-              if constexpr (kE4m3) umma::ld16_nowait(to + k * C::kOCols + g * kN, u[k]);
+              if constexpr (kN == 16) umma::ld16_nowait(to + k * C::kOCols + g * kN, u[k]);
               else ld8_nowait(to + k * C::kOCols + g * kN, u[k]);
             }
             umma::wait_ld();
 #pragma unroll
-            for (int e = 0; e < 8 * kGo; e += 4) {
-              const int r = g * 8 + e;
+            for (int e = 0; e < 2; ++e) {
+              const int r = (C::kSumTerms ? g / 2 * 16 + g % 2 * 4 : g * 8) + e * kOn;
               const float4 w4 = *reinterpret_cast<const float4*>(w_s + roff + r);
               float4 k4 = make_float4(1.f, 1.f, 1.f, 1.f);
               if (moved) k4 = *reinterpret_cast<const float4*>(keep_s + roff + r);
@@ -1129,7 +1129,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
                 float2 o[2];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                  const int at = C::kSumTerms ? 2 * (e & 7) + 4 * y + 2 * (e >> 3) : kE4m3 ? 2 * e + 4 * y : e + 2 * y;
+                  const int at = C::kSumTerms ? 2 * e + 4 * y : kE4m3 ? 8 * e + 4 * y : 4 * e + 2 * y;
                   o[y] = make_float2(__uint_as_float(u[k][at]), __uint_as_float(u[k][at + 1]));
                   if constexpr (C::kOTerms == 2)
                     o[y] = __fadd2_rn(o[y], make_float2(__uint_as_float(u[k][at + 2]), __uint_as_float(u[k][at + 3])));
