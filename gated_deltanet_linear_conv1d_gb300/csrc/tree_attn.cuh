@@ -439,7 +439,7 @@ __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned 
       const int j = (r0 + r) / p.G;
       uint64_t m = 0;
       if (r < a.rows && j < p.P) m = p.mask ? __ldg(p.mask + (size_t)s.n * p.P + j) : j == 63 ? ~0ull : (2ull << j) - 1;
-      mask_s[r] = m;
+      mask_s[r] = m & ~0ull >> (64 - p.P);
     }
   // rows on their way at once: more hide their loads at the start of a short segment, fewer leave the instruction
   // cache to the loops (256 x 1k..8k tokens with 6 rows: 288 us with four, 294 with eight; 32 trees of 48 rows: 196 and 177)
@@ -949,18 +949,28 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         // the output of two tiles back has been read: its statistics, its product and the weights are done with
         wait_warp(&B->o_empty[b], ph ^ 1, abort);
         if ((t + 1) * kTile > s.ctx) {  // drafted tokens, or tokens behind the last
+          // of each row, bit 8 k: this thread's token k is seen (one of the context, or a node whose bit is set)
+          const int node0 = t * kTile + tt - s.ctx;
+          uint32_t before = 0;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int node = t * kTile + tt + 8 * k - s.ctx;
-            if (node < 0) continue;
+          for (int k = 0; k < 4; ++k) before |= node0 + 8 * k < 0 ? 1u << (8 * k) : 0u;
+          auto see = [&](uint64_t m) {
+            return before | (uint32_t)(node0 >= 64 || node0 <= -64 ? 0ull : node0 >= 0 ? m >> node0 : m << -node0);
+          };
 #pragma unroll
-            for (int g = 0; g < kC; ++g)
-              if (g < used) {
-                const bool in = node < p.P;
-                if (!in || !((mask_s[g * 8 + a4 * 2] >> (node & 63)) & 1)) x[g][k].x = -INFINITY;
-                if (!in || !((mask_s[g * 8 + a4 * 2 + 1] >> (node & 63)) & 1)) x[g][k].y = -INFINITY;
+          for (int g = 0; g < kC; ++g)
+            if (g < used) {
+              const uint32_t lo = see(mask_s[g * 8 + a4 * 2]), hi = see(mask_s[g * 8 + a4 * 2 + 1]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if (!((lo >> (8 * k)) & 1)) x[g][k].x = -INFINITY;
+                if (!((hi >> (8 * k)) & 1)) x[g][k].y = -INFINITY;
               }
-            if (kE4m3 && !(fabsf(sv[k]) < INFINITY)) sv[k] = 0.f;  // its values are zeros, see the check warp
+            }
+          if constexpr (kE4m3) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)  // the values of such a node are zeros, see the check warp
+              if (node0 + 8 * k >= 0 && !(fabsf(sv[k]) < INFINITY)) sv[k] = 0.f;
           }
         }
         // ---- the tile's maximum of each row: of the warp first, then of the four warps
