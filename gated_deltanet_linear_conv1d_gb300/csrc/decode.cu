@@ -139,7 +139,10 @@ __device__ int g_unit_counter[kSchedSlots * 2];
 // row's registers hold the last position's state; where the parent is another
 // one, the thread that holds the row loads it again, from the staged live state
 // or from the parent's checkpoint, which the same thread has written (one node
-// ahead: a trip to L2 next to the stream takes as long as a node).
+// ahead: a trip to L2 next to the stream takes as long as a node). Bound by HBM:
+// 64 requests of 8 nodes at 16/48 heads, random trees, 1.87 GB: 377 us, 73 % of
+// the copy bandwidth (the same kernel on chains 344 us, gdn_spec_verify's on
+// chains 324 us; with a parent loaded only when its node begins 386 us).
 template <bool kOne, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const StepArgs p, const int units, const int sched) {
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -731,6 +734,8 @@ __global__ void __launch_bounds__(1024) split_kernel(const StepArgs p, const int
 // node, or loads the parent's again (the live slot's, or a checkpoint that it has
 // written); the nodes' conv inputs stand in shared memory. The live slot is only
 // read, so no CTA waits for another before it writes.
+// One request of 5 nodes at 4/12 heads: 11.7 us, bound by its chain of loads, conv
+// and node updates (35.7 us with a persistent CTA per unit).
 // grid: units x nsplit CTAs, clusters of nsplit along x; blockDim >= 256 and >= 8 x G x (128 / nsplit)
 __global__ void __launch_bounds__(1024) split_tree_kernel(const StepArgs p, const int nsplit) {
   constexpr int kRowsMax = kHeadDim;                          // rows of a CTA: G x 128 / nsplit <= 128

@@ -88,6 +88,14 @@ enum { kNoCache = 0, kBf16Cache = 1, kE4m3Cache = 2 };
 
 enum { kPartial = 0, kWhole = 1, kInterleaved = 2 };  // up to D / 2 rotated dimensions, all D, neighbours as pairs
 
+// Batches of four rows per group on their way to shared memory, past the registers, next to the one that is worked on.
+constexpr int kAhead = 2, kBuffers = kAhead + 1, kRows = 4;
+constexpr int kBatchBytes = kThreads * kRows * 16;  // a lane has eight values of a row
+
+__device__ __forceinline__ void copy16(void* smem, const void* g) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(g) : "memory");
+}
+
 // The query rows (kQuery) or the key and value rows of a block's T tokens, H of them a token. D / 8 lanes hold a row:
 // lane l has four values from 4 l on, and four from D / 2 + 4 l on. A row group keeps its head over the tokens, so that
 // what goes by the head (addresses, gains) is found once. A batch is four rows, loaded before the first is worked on:
@@ -98,8 +106,10 @@ enum { kPartial = 0, kWhole = 1, kInterleaved = 2 };  // up to D / 2 rotated dim
 // the first lanes, and pairs half a rotation apart are in lanes l and l ^ (half / 4); with all D rotated they are a lane's
 // first and second four.
 template <int D, bool kNorm, int kCache, bool kQuery, bool kMany, int kRot>
-__device__ __forceinline__ void rows_pass(const RopeArgs& p, const KvArgs& c, const float2* turn, int t0, int T, int H) {
-  constexpr int kLanes = D / 8, kGroups = kThreads / kLanes, kRows = 4;
+__device__ __forceinline__ void rows_pass(const RopeArgs& p, const KvArgs& c, const float2* turn, unsigned char* stage,
+                                          int* place, int t0, int T, int H) {
+  constexpr int kLanes = D / 8, kGroups = kThreads / kLanes;
+  constexpr int kStep = kMany ? 1 : kRows;  // tokens of a batch
   const int tid = threadIdx.x, l = tid % kLanes, group = tid / kLanes;
   const int half = p.rotary / 2;
   const bool turns = kNorm && l * 4 < (kRot == kWhole ? D / 2 : p.rotary);
@@ -111,7 +121,7 @@ __device__ __forceinline__ void rows_pass(const RopeArgs& p, const KvArgs& c, co
     const int hh = value ? h - c.Hkv : h;
     const int64_t st = kQuery ? p.q_t : value ? p.v_t : p.k_t;
     // row i of a batch: i steps on from the first
-    const uint16_t* src = (kQuery ? p.q + hh * p.q_h : value ? p.v + hh * p.v_h : p.k + hh * p.k_h) + t0 * st + l * 4;
+    const uint16_t* src = (kQuery ? p.q + hh * p.q_h : value ? p.v + hh * p.v_h : p.k + hh * p.k_h) + t0 * st + l * 8;
     const int64_t step = kMany ? kGroups * p.q_h : st;
     uint16_t* dst = kQuery ? p.q_out : value ? nullptr : p.k_out;  // dense output, or none
     const int64_t out_t = (int64_t)(kQuery ? p.Hq : c.Hkv) * D, out_step = kMany ? kGroups * D : out_t;
@@ -129,24 +139,48 @@ __device__ __forceinline__ void rows_pass(const RopeArgs& p, const KvArgs& c, co
       other_gain[0] = make_float2(o.x, o.y);
       other_gain[1] = make_float2(o.z, o.w);
     }
-    for (int tl = 0; tl < T; tl += kMany ? 1 : kRows) {
-      uint2 raw[kRows][2];
+    unsigned char* rows = stage + group * (kRows * D * 2);  // of the group, in the first buffer
+    auto fetch = [&](int tl, int buf) {  // the batch from token tl on
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        raw[i][0] = raw[i][1] = make_uint2(0u, 0u);
-        if (kMany ? h + i * kGroups < H : live && tl + i < T) {
-          raw[i][0] = *reinterpret_cast<const uint2*>(src + i * step);
-          raw[i][1] = *reinterpret_cast<const uint2*>(src + i * step + D / 2);
+      for (int i = 0; i < kRows; ++i)
+        if (kMany ? tl < T && h + i * kGroups < H : live && tl + i < T)
+          copy16(rows + buf * kBatchBytes + i * (D * 2) + l * 16, src + tl * st + i * step);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    __syncwarp();  // the buffers have been read
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) fetch(k * kStep, k);
+    if constexpr (kCache != kNoCache && !kQuery) {
+      // where the tokens go: the row of the page's first head, -1: nowhere
+      if (h0 == 0) {
+        for (int t = tid; t < T; t += kThreads) {
+          const int to = __ldg(p.kv_slot + t0 + t), page = to / c.page;
+          if (to >= c.slots) report(p.dev_err, GDN_DEVERR_SLOT);
+          place[t] = to < 0 || to >= c.slots ? -1 : page * c.Hkv * c.page + (to - page * c.page);
         }
+        __syncthreads();
       }
-      src += kMany ? st : kRows * st;
+    }
+    int buf = 0;
+    for (int tl = 0; tl < T; tl += kStep) {
+      fetch(tl + kAhead * kStep, buf == 0 ? kAhead : buf - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+      __syncwarp();
+      const unsigned char* batch = rows + buf * kBatchBytes + l * 8;
+      auto load = [&](int i, uint2 (&raw)[2]) {
+        raw[0] = *reinterpret_cast<const uint2*>(batch + i * (D * 2));
+        raw[1] = *reinterpret_cast<const uint2*>(batch + i * (D * 2) + D);
+      };
+      if (++buf == kBuffers) buf = 0;
       float inv[kRows];
       if constexpr (kNorm) {
         // the sums of the rows' squares, each lane's part in `inv` first
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
           float2 x[4], ss = make_float2(0.f, 0.f);
-          unpack8(raw[i], x);
+          uint2 raw[2];
+          load(i, raw);
+          unpack8(raw, x);
 #pragma unroll
           for (int e = 0; e < 4; ++e) ss = __ffma2_rn(x[e], x[e], ss);
           inv[i] = ss.x + ss.y;
@@ -201,9 +235,11 @@ __device__ __forceinline__ void rows_pass(const RopeArgs& p, const KvArgs& c, co
         // nothing left for any group: the shuffles take whole warps
         if (ti >= T || hi - group >= H) break;
         float2 x[4];
-        unpack8(raw[i], x);
+        uint2 raw[2];
+        load(i, raw);
+        unpack8(raw, x);
         if constexpr (kNorm) {
-          uint2 o = raw[i][0];
+          uint2 o = raw[0];
           if (kRot == kPartial && half > 0) {
             const int from = (tid & 31) ^ (turns ? half / 4 : 0);
             o.x = __shfl_sync(0xffffffffu, o.x, from);
@@ -237,12 +273,10 @@ __device__ __forceinline__ void rows_pass(const RopeArgs& p, const KvArgs& c, co
           }
         }
         if constexpr (kCache != kNoCache && !kQuery) {
-          const int to = live ? __ldg(p.kv_slot + t0 + ti) : -1;
-          const bool store = to >= 0 && to < c.slots;
-          if (to >= c.slots && l == 0) report(p.dev_err, GDN_DEVERR_SLOT);
+          const int to = place[ti];
+          const bool store = live && to >= 0;
           if (!__any_sync(0xffffffffu, store)) continue;
-          const int page = store ? to / c.page : 0, row = store ? to - page * c.page : 0;
-          const size_t at = ((size_t)page * c.Hkv + hh) * c.page + row;
+          const size_t at = (size_t)to + (size_t)hh * c.page;
           if constexpr (kCache == kE4m3Cache) {
             // a / 448, rounded once, as in codes()
             constexpr float kInv = 1.f / kE4m3Max;
@@ -272,14 +306,20 @@ __device__ __forceinline__ void rows_pass(const RopeArgs& p, const KvArgs& c, co
 // The angles: a thread per (token, frequency) puts their cosine and sine into shared memory first. A position times a
 // frequency is taken in turns, in 64-bit fixed point (one turn = 2^64), where the whole turns fall away by themselves:
 // the error is the frequency's rounding to 2^-64 turns times the position, 2^-33 turns at the largest one.
-// What bounds it: the issue of instructions, close to HBM's bytes, at many tokens; the launch and the angles' chain at
-// few. 16,384 tokens of 24 + 4 heads of 256 into a bf16 cache, 571 MB: 116 us with 80 registers a thread (three blocks
-// an SM; 133 us with two and 124 us with four), 192 us when addresses and gains were found row by row, with the
-// compiler's division, 220 instructions a row. Holding a second batch in registers costs more blocks than it hides.
+// What bounds it: HBM at many tokens, the launch and the angles' chain at few. A batch is copied to shared memory while
+// the one before it is worked on: loads into registers left none in flight meanwhile, and a second batch of registers
+// spills at three blocks an SM. 16,384 tokens of 24 + 4 heads of 256 into a bf16 cache, 571 MB: 95 us, 6.0 TB/s (116 us
+// with loads into registers; 106 us with three blocks of 80 registers, which spill; 100 us one batch ahead instead of
+// two; 96 us with 28 tokens a block instead of 16). A token's place in the pool is found once per block: with the
+// page's division and the slot's load in every row, writing 16,384 tokens of 4 heads into an E4M3 cache, 101 MB, was
+// bound by instructions, 24 us; now 18 us. 256 tokens with their queries: 4.1 us with two tokens a block, one block
+// of each kind per SM; 5.4 us with one.
 template <int D, bool kNorm, int kCache, int kRot>
-__global__ void __launch_bounds__(kThreads, 3) rows_kernel(const RopeArgs p, const KvArgs c, int tokens_per_block) {
+__global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RopeArgs p, const KvArgs c, int tokens_per_block) {
   __shared__ uint64_t freq[kNorm ? D / 2 : 1];
-  extern __shared__ float2 turn[];  // [tokens][half]
+  __shared__ int place[kMaxTokens];
+  extern __shared__ __align__(16) unsigned char stage[];  // [kBuffers][groups][kRows][D] bf16
+  float2* turn = reinterpret_cast<float2*>(stage + kBuffers * kBatchBytes);  // [tokens][half]
   constexpr int kGroups = kThreads / (D / 8);
   const int t0 = blockIdx.x * tokens_per_block;
   const int T = min(tokens_per_block, p.T - t0);
@@ -302,12 +342,12 @@ __global__ void __launch_bounds__(kThreads, 3) rows_kernel(const RopeArgs p, con
       __syncthreads();
     }
     if (blockIdx.y == 1) {
-      if (p.Hq > kGroups) rows_pass<D, true, kNoCache, true, true, kRot>(p, c, turn, t0, T, p.Hq);
-      else rows_pass<D, true, kNoCache, true, false, kRot>(p, c, turn, t0, T, p.Hq);
+      if (p.Hq > kGroups) rows_pass<D, true, kNoCache, true, true, kRot>(p, c, turn, stage, place, t0, T, p.Hq);
+      else rows_pass<D, true, kNoCache, true, false, kRot>(p, c, turn, stage, place, t0, T, p.Hq);
       return;
     }
   }
-  rows_pass<D, kNorm, kCache, false, false, kRot>(p, c, turn, t0, T, c.Hkv + (p.v ? c.Hkv : 0));
+  rows_pass<D, kNorm, kCache, false, false, kRot>(p, c, turn, stage, place, t0, T, c.Hkv + (p.v ? c.Hkv : 0));
 }
 
 // Cached rows back to bf16: a block takes kReadTokens output tokens, a thread 16
@@ -383,37 +423,43 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadArgs p, const 
 
 namespace {
 
+template <int D, bool kNorm, int kCache, int kRot>
+cudaError_t run(const RopeArgs& a, const KvArgs& c, dim3 grid, int per, cudaStream_t stream) {
+  const int smem = kBuffers * kBatchBytes + (kNorm ? per * (a.rotary / 2) * (int)sizeof(float2) : 0);
+  const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(&rows_kernel<D, kNorm, kCache, kRot>),
+                                              kBuffers * kBatchBytes + kMaxTokens * D / 2 * (int)sizeof(float2));
+  if (err != cudaSuccess) return err;
+  rows_kernel<D, kNorm, kCache, kRot><<<grid, kThreads, smem, stream>>>(a, c, per);
+  return cudaGetLastError();
+}
+
 template <int D, int kRot>
-void run_norm(const RopeArgs& a, const KvArgs& c, dim3 grid, int per, cudaStream_t stream) {
-  const size_t smem = (size_t)per * (a.rotary / 2) * sizeof(float2);
-  if (!c.k) rows_kernel<D, true, kNoCache, kRot><<<grid, kThreads, smem, stream>>>(a, c, per);
-  else if (c.e4m3) rows_kernel<D, true, kE4m3Cache, kRot><<<grid, kThreads, smem, stream>>>(a, c, per);
-  else rows_kernel<D, true, kBf16Cache, kRot><<<grid, kThreads, smem, stream>>>(a, c, per);
+cudaError_t run_norm(const RopeArgs& a, const KvArgs& c, dim3 grid, int per, cudaStream_t stream) {
+  if (!c.k) return run<D, true, kNoCache, kRot>(a, c, grid, per, stream);
+  return c.e4m3 ? run<D, true, kE4m3Cache, kRot>(a, c, grid, per, stream)
+                : run<D, true, kBf16Cache, kRot>(a, c, grid, per, stream);
 }
 
 template <int D>
-void run_rows(const RopeArgs& a, const KvArgs& c, bool norm, dim3 grid, int per, cudaStream_t stream) {
+cudaError_t run_rows(const RopeArgs& a, const KvArgs& c, bool norm, dim3 grid, int per, cudaStream_t stream) {
   if (norm) {
-    if (a.interleaved) run_norm<D, kInterleaved>(a, c, grid, per, stream);
-    else if (a.rotary == D) run_norm<D, kWhole>(a, c, grid, per, stream);
-    else run_norm<D, kPartial>(a, c, grid, per, stream);
-  } else if (c.e4m3) {
-    rows_kernel<D, false, kE4m3Cache, kPartial><<<grid, kThreads, 0, stream>>>(a, c, per);
-  } else {
-    rows_kernel<D, false, kBf16Cache, kPartial><<<grid, kThreads, 0, stream>>>(a, c, per);
+    if (a.interleaved) return run_norm<D, kInterleaved>(a, c, grid, per, stream);
+    return a.rotary == D ? run_norm<D, kWhole>(a, c, grid, per, stream)
+                         : run_norm<D, kPartial>(a, c, grid, per, stream);
   }
+  return c.e4m3 ? run<D, false, kE4m3Cache, kPartial>(a, c, grid, per, stream)
+                : run<D, false, kBf16Cache, kPartial>(a, c, grid, per, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_rows(const RopeArgs& a, const KvArgs& c, bool norm, int D, cudaStream_t stream) {
-  // enough blocks for every SM before a block takes several tokens
-  int per = 1;
-  while (per < kMaxTokens && a.T / (2 * per) >= 4 * 152) per *= 2;
+  // as many blocks (of each kind) as SMs, or the fewest whole multiples that keep a block at kMaxTokens, in fours
+  const int most = 152 * kMaxTokens, waves = a.T / most + (a.T % most != 0), blocks = 152 * waves;
+  int per = a.T / blocks + (a.T % blocks != 0);
+  if (per > 4) per = (per + 3) / 4 * 4;
   const dim3 grid((unsigned)((a.T + per - 1) / per), norm && a.q ? 2 : 1, 1);
-  if (D == 256) run_rows<256>(a, c, norm, grid, per, stream);
-  else run_rows<128>(a, c, norm, grid, per, stream);
-  return cudaGetLastError();
+  return D == 256 ? run_rows<256>(a, c, norm, grid, per, stream) : run_rows<128>(a, c, norm, grid, per, stream);
 }
 
 cudaError_t launch_kv_read(const ReadArgs& a, const KvArgs& c, int D, cudaStream_t stream) {

@@ -10,12 +10,14 @@
 // row tile): the query rows of the Hq / Hkv heads of all P nodes, up to kRows of
 // them. The tiles of all requests stand in one line, cut into equal pieces, one
 // per CTA (one CTA per SM): every SM streams the same number of keys and values,
-// whatever the lengths, and a single long request uses the whole GPU. The lengths
-// are read on the device, so a captured graph takes new ones. A (request, head,
-// row tile) that lies in several CTAs' pieces leaves a partial result per CTA in
-// the workspace, and a second kernel adds them up in the order of the tiles. (With
-// the CTA that arrived last doing it, two tickets and a chain of trips to L2 took
-// up to 45 us for 64 rows.)
+// whatever the lengths, and a single long request uses the whole GPU. What a CTA
+// does once per unit (request, kv head, row tile) counts as kSegCost tiles: with
+// the tiles alone, CTAs with eight short units were 90 us behind the others. The
+// lengths are read on the device, so a captured graph takes new ones. A unit that
+// lies in several CTAs' pieces leaves a partial result per CTA in the workspace,
+// and a second kernel adds them up in the order of the tiles. (With the CTA that
+// arrived last doing it, two tickets and a chain of trips to L2 took up to 45 us
+// for 64 rows.)
 //
 // Both products take the cache as their first operand, so a tile costs the tensor
 // cores the same 128 lanes for few query rows as for many columns:
@@ -26,9 +28,10 @@
 // its rounding left: 4 + 4 significant bits, as many as bf16 has. For Q (bf16
 // values, scaled by a power of two per row) that is exact down to 2^-17 of the
 // row's largest value; a weight of P is off by at most 2^-8 of itself or 2^-18 of
-// its tile's largest. The two terms are neighbouring columns of one MMA, added up
-// as they are read. The scales stay outside: the key's multiplies the score, the
-// value's its weight (relative to the tile's largest scale).
+// its tile's largest. The two terms are columns of one MMA, added up as they are
+// read, or from 33 rows on two MMAs into the same columns. The scales stay
+// outside: the key's multiplies the score, the value's its weight (relative to
+// the tile's largest scale).
 //
 // Softmax without a chain between tiles: a tile's weights are taken relative to
 // its own maximum, and the accumulators of the output, in registers, take the
@@ -44,8 +47,16 @@
 // last token. Every wait is bounded: one that runs out sets
 // GDN_DEVERR_TIMEOUT and the CTA leaves.
 //
-// What bounds it: the cache's bytes from HBM while the rows of a tile are few, the
-// MMAs (their operand reads from shared memory, at N < 128) when they are many.
+// What bounds it, with 24 query and 4 kv heads of 256:
+//   one token per request: HBM. 256 requests of 1k..8k tokens, E4M3: 285 us, 6.5
+//   TB/s. One request of 509 tokens: 12 us, the launches and one tile's chain.
+//   48 rows (trees of 8 nodes), bf16, 32 requests of 129..16384 tokens: 109 us,
+//   4.1 TB/s. Per tile the copies take 7.2 k cycles where HBM's share is 5.6 k (the
+//   ring holds 160 KB, and V stays in it until its weights are there); a unit costs
+//   about five tiles' time.
+//   64 rows, E4M3, 131071 tokens: 306 us, the softmax: 8 warps at 0.57 instructions
+//   a cycle and scheduler in chains of exchanges, conversions and barriers, 3.7 k
+//   cycles a tile, of which the MMAs need 1.1 k.
 #pragma once
 
 #include "device.cuh"
@@ -109,6 +120,10 @@ struct Cfg {
   static constexpr int kAhead = kSplit ? 1 : 2;
   // query buffers: a tile's scores wait for no output that follows them, though every segment have one tile
   static constexpr int kQBuf = kAhead + 1;
+  // A unit's fixed work (its query rows, its result, the ends of its pipeline) in tiles, for the cut of the line. It
+  // takes as long as so many: 32 trees of 48 rows on 129..16384 tokens, bf16, with 0 / 2 / 4 / 5 / 6: 174 / 126 / 113 /
+  // 109 / 115 us, E4M3 with 0 / 5 / 9: 199 / 121 / 106 us. 128 single tokens on 129..8192: bf16 with 0 / 2 / 5 / 7:
+  // 168 / 161 / 166 / 169 us; 256 on 1k..8k, E4M3 with 0 / 4 / 6: 297 / 286 / 295 us.
   static constexpr int kSegCost = kRows == 16 ? (kE4m3 ? 4 : 2) : kE4m3 ? 9 : 5;
   static constexpr int kOutGroups = kRows == 16 ? 1 : 2;    // at few rows a group's fixed work outweighs the rows'
   static constexpr int kOutWarp = 8, kCopyWarp = kOutWarp + 4 * kOutGroups;  // first warps of the roles

@@ -6,6 +6,10 @@
     python -m gated_deltanet_linear_conv1d_gb300.profile_case commit  --requests 256 --launches 3
     python -m gated_deltanet_linear_conv1d_gb300.profile_case fp8     --requests 4096 --k 6144 --n 5120
     python -m gated_deltanet_linear_conv1d_gb300.profile_case gemm    --requests 256 --k 6144 --n 5120
+    python -m gated_deltanet_linear_conv1d_gb300.profile_case attn    --lengths 4096x64 --cache e4m3 --nodes 1
+    python -m gated_deltanet_linear_conv1d_gb300.profile_case rope    --requests 16384 --cache bf16
+    python -m gated_deltanet_linear_conv1d_gb300.profile_case kvread  --lengths 4096x64 --cache e4m3
+    python -m gated_deltanet_linear_conv1d_gb300.profile_case spectree --requests 64 --nodes 8
 
 Each launch is preceded by the same warm-up launches (--warmup) and followed
 by a device synchronisation; nothing else runs on the GPU besides the input
@@ -44,13 +48,40 @@ def _lengths(spec: str) -> list[int]:
     return out
 
 
+def _cache(gen, tokens, page, heads, fmt, dev):
+    """A filled key/value cache for requests of `tokens` tokens, and their block table (pages in random order)."""
+    from . import binding as b
+    need = [-(-t // page) for t in tokens]
+    pages = sum(need)
+    perm = torch.randperm(pages, generator=gen, device=dev).to(torch.int32)
+    table = torch.full((len(tokens), max(need)), -1, dtype=torch.int32, device=dev)
+    at = 0
+    for i, n in enumerate(need):
+        table[i, :n] = perm[at:at + n]
+        at += n
+    pool, scale = [], [None, None]
+    for i in range(2):
+        x = torch.randn((pages, heads, page, 256), generator=gen, device=dev)
+        if fmt == "e4m3":
+            scale[i] = x.abs().amax(-1) / 448
+            pool.append((x / scale[i][..., None]).to(torch.float8_e4m3fn).view(torch.uint8))
+        else:
+            pool.append(x.to(torch.bfloat16))
+    return b.make_kv_cache(pool[0], pool[1], *scale), table
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser()
-    ap.add_argument("case", choices=["decode", "prefill", "spec", "commit", "conv", "rmsnorm", "fp8", "gemm"])
+    ap.add_argument("case", choices=["decode", "prefill", "spec", "commit", "conv", "rmsnorm", "fp8", "gemm", "attn",
+                                     "rope", "kvread", "spectree"])
     ap.add_argument("--heads", choices=["full", "rank"], default="full")
     ap.add_argument("--requests", type=int, default=64)
     ap.add_argument("--slots", type=int, default=0)
-    ap.add_argument("--lengths", default="2048x8", help="prefill lengths, e.g. 2048x8 or 16,300,8192")
+    ap.add_argument("--lengths", default="2048x8",
+                    help="prefill lengths or cached contexts, e.g. 2048x8 or 16,300,8192")
+    ap.add_argument("--nodes", type=int, default=1, help="attn, spectree: drafted tokens per request")
+    ap.add_argument("--cache", choices=["bf16", "e4m3"], default="e4m3", help="attn, rope, kvread: the cache's format")
+    ap.add_argument("--page", type=int, default=64, help="attn, rope, kvread: tokens per page")
     ap.add_argument("--loguniform", type=int, default=0, help="prefill: N log-uniform lengths in [16, 8192]")
     ap.add_argument("--k", type=int, default=6144, help="fp8, gemm: input features")
     ap.add_argument("--n", type=int, default=5120, help="fp8, gemm: output features")
@@ -129,6 +160,54 @@ def main(argv=None):
 
         def run():
             b.gdn_out_proj(x, wt, out, residual=out, dev_err=err)
+    elif args.case in ("attn", "rope", "kvread"):
+        gen = torch.Generator(device=dev)
+        gen.manual_seed(8)
+        hq, hkv = (24, 4) if args.heads == "full" else (6, 1)
+        if args.case == "rope":
+            T = args.requests
+            cache, _ = _cache(gen, [T], args.page, hkv, args.cache, dev)
+            x = torch.randn((T, hq + 2 * hkv, 256), generator=gen, device=dev).to(torch.bfloat16)
+            gain = torch.ones(256, device=dev)
+            pos = torch.arange(T, dtype=torch.int32, device=dev)
+            freq = 1e7 ** (-torch.arange(0, 64, 2, dtype=torch.float64, device=dev) / 64)
+            out = torch.empty((T, hq, 256), dtype=torch.bfloat16, device=dev)
+
+            def run():
+                b.gdn_qk_norm_rope(x[:, :hq], x[:, hq:hq + hkv], gain, gain, 1e-6, pos, freq, out, v=x[:, hq + hkv:],
+                                   cache=cache, kv_slot=pos, dev_err=err)
+        else:
+            lengths, P = _lengths(args.lengths), args.nodes
+            cache, table = _cache(gen, [n + P for n in lengths], args.page, hkv, args.cache, dev)
+            N, T = len(lengths), sum(lengths) if args.case == "kvread" else len(lengths) * P
+            if args.case == "kvread":
+                start = torch.tensor([0] + lengths, device=dev).cumsum(0).to(torch.int32)
+                ko, vo = (torch.empty((T, hkv, 256), dtype=torch.bfloat16, device=dev) for _ in range(2))
+            else:
+                ctx = torch.tensor(lengths, dtype=torch.int32, device=dev)
+                q = torch.randn((T, hq, 256), generator=gen, device=dev).to(torch.bfloat16)
+                out = torch.empty_like(q)
+                ws = torch.empty(b.gdn_tree_attention_workspace_bytes(cache, N, P, hq), dtype=torch.uint8, device=dev)
+
+            def run():
+                if args.case == "kvread":
+                    b.gdn_kv_cache_read(cache, table, start, ko, vo, dev_err=err)
+                else:
+                    b.gdn_tree_attention(cache, q, table, ctx, 256 ** -0.5, out, P, workspace=ws, dev_err=err)
+    elif args.case == "spectree":
+        w = synth.spec_workload(geom, args.requests, num_pos=args.nodes, seed=4)
+        d = _dev(w, dev)
+        D = b.make_dims(geom, w["num_slots"])
+        rng = np.random.default_rng(9)
+        parent = torch.from_numpy(np.array([[rng.integers(-1, p) for p in range(args.nodes)]
+                                            for _ in range(args.requests)], dtype=np.int32)).to(dev)
+        T = args.requests * args.nodes
+        og = torch.empty((T, geom.num_v_heads * 128), dtype=torch.bfloat16, device=dev)
+
+        def run():
+            b.gdn_spec_verify_tree(D, d["qkv0"], d["conv_w"], d["conv_hist"], d["state"], d["slot_idx"],
+                                   d["spec_slot_idx"], parent, d["alpha"], d["beta"], d["z"], d["gamma"], w["eps"],
+                                   ogate=og, dev_err=err)
     else:
         rng = np.random.default_rng(5)
         T = args.requests
@@ -153,7 +232,7 @@ def main(argv=None):
     flag = b.gdn_read_device_error(err)
     tokens = {"decode": args.requests, "spec": args.requests * 4, "commit": args.requests,
               "fp8": args.requests, "gemm": args.requests}.get(args.case)
-    if args.case in ("prefill", "conv"):
+    if args.case in ("prefill", "conv", "attn", "rope", "kvread", "spectree"):
         tokens = T
     ms = sum(times) / max(1, len(times))
     rate = f", {tokens / (ms / 1e3):.4g} tokens/s" if tokens else ""
