@@ -308,12 +308,12 @@ __device__ __forceinline__ void rows_pass(const RopeArgs& p, const KvArgs& c, co
 // the error is the frequency's rounding to 2^-64 turns times the position, 2^-33 turns at the largest one.
 // What bounds it: HBM at many tokens, the launch and the angles' chain at few. A batch is copied to shared memory while
 // the one before it is worked on: loads into registers left none in flight meanwhile, and a second batch of registers
-// spills at three blocks an SM. 16,384 tokens of 24 + 4 heads of 256 into a bf16 cache, 571 MB: 95 us, 6.0 TB/s (116 us
-// with loads into registers; 106 us with three blocks of 80 registers, which spill; 100 us one batch ahead instead of
-// two; 96 us with 28 tokens a block instead of 16). A token's place in the pool is found once per block: with the
-// page's division and the slot's load in every row, writing 16,384 tokens of 4 heads into an E4M3 cache, 101 MB, was
-// bound by instructions, 24 us; now 18 us. 256 tokens with their queries: 4.1 us with two tokens a block, one block
-// of each kind per SM; 5.4 us with one.
+// spills at three blocks an SM. 16,384 tokens of 24 + 4 heads of 256, the keys dense and into a bf16 cache, 571 MB: 95
+// us, 6.0 TB/s (116 us with loads into registers; 106 us with three blocks of 80 registers, which spill; 100 us one
+// batch ahead instead of two; 96 us with 28 tokens a block instead of 16). A token's place in the pool is found once per
+// block: with the page's division and the slot's load in every row, writing 16,384 tokens of 4 heads into an E4M3 cache,
+// 101 MB, was bound by instructions, 24 us; now 18 us. 256 tokens with their queries: 4.1 us with two tokens a block,
+// one block of each kind per SM; 5.4 us with one.
 template <int D, bool kNorm, int kCache, int kRot>
 __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RopeArgs p, const KvArgs c, int tokens_per_block) {
   __shared__ uint64_t freq[kNorm ? D / 2 : 1];
@@ -335,9 +335,11 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RopeArgs p, con
         const int64_t pos = p.positions[t0 + i / half];
         // the upper 32 bits as a signed number: half turns in [-1, 1)
         const int32_t top = (int32_t)(((uint64_t)pos * freq[i % half]) >> 32);
+        // what the conversion to fp32 rounds off, up to 2^-25 half turns, turns sine and cosine on to first order
+        const float half_turns = (float)top, off = (float)(top - (int32_t)half_turns) * 1.4629180792671596e-09f;  // pi 2^-31
         float s, co;
-        sincospif((float)top * 4.656612873077393e-10f, &s, &co);
-        turn[i] = make_float2(co, s);
+        sincospif(half_turns * 4.656612873077393e-10f, &s, &co);
+        turn[i] = make_float2(fmaf(-s, off, co), fmaf(co, off, s));
       }
       __syncthreads();
     }
@@ -351,8 +353,10 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RopeArgs p, con
 }
 
 // Cached rows back to bf16: a block takes kReadTokens output tokens, a thread 16
-// values of one (token, k or v, head) row at a time. The request of the block's
-// first token is found by bisection, the others' by walking on from it.
+// values of one (token, k or v, head) row at a time. A thread per token finds its
+// request by bisection and its page in the table. Bound by HBM: 64 prefixes of up
+// to 8192 tokens, E4M3, 518 MB: 80 us, 6.5 TB/s; one of 2047 tokens 4.5 us, the
+// launch and the chain of two loads before the first row's.
 constexpr int kReadTokens = 8;
 
 template <int D>
