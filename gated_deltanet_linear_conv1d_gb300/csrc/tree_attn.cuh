@@ -48,14 +48,14 @@
 // GDN_DEVERR_TIMEOUT and the CTA leaves.
 //
 // What bounds it, with 24 query and 4 kv heads of 256:
-//   one token per request: HBM. 256 requests of 1k..8k tokens, E4M3: 285 us, 6.5
+//   one token per request: HBM. 256 requests of 1k..8k tokens, E4M3: 281 us, 6.5
 //   TB/s. One request of 509 tokens: 12 us, the launches and one tile's chain.
-//   48 rows (trees of 8 nodes), bf16, 32 requests of 129..16384 tokens: 109 us,
-//   4.1 TB/s. Per tile the copies take 7.2 k cycles where HBM's share is 5.6 k (the
-//   ring holds 160 KB, and V stays in it until its weights are there); a unit costs
+//   48 rows (trees of 8 nodes), bf16, 32 requests of 129..16384 tokens: 104 us,
+//   4.3 TB/s. The copies wait for room: a tile is 128 KB, the ring 128 KB (96 KB for
+//   64 rows: 109 us), and V stays in it until its weights are there; a unit costs
 //   about five tiles' time.
-//   64 rows, E4M3, 131071 tokens: 306 us, the softmax: 8 warps at 0.57 instructions
-//   a cycle and scheduler in chains of exchanges, conversions and barriers, 3.7 k
+//   64 rows, E4M3, 131071 tokens: 306 us, the softmax: 8 warps at 0.60 instructions
+//   a cycle and scheduler in chains of exchanges, conversions and barriers, 3.6 k
 //   cycles a tile, of which the MMAs need 1.1 k.
 #pragma once
 
@@ -75,6 +75,7 @@ constexpr int kScSlots = 4;              // tiles of scales in flight
 // A barrier's parity tells a phase from the next one only. So there are more of them than their writer can be
 // ahead of their reader: the ring (at most 11 blocks) holds K or V of fewer than 8 tiles.
 constexpr int kSlots = 8, kMarks = 16;
+constexpr int kBarBytes = 1216;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Args {
@@ -110,11 +111,9 @@ struct Cfg {
   // columns to read).
   static constexpr bool kSumTerms = kE4m3 && kRows == 64;
   static constexpr int kOTerms = kSumTerms ? 1 : kTerms;
-  static constexpr int kQCols = kTerms * kRows;               // rows of Q's operand
   static constexpr int kCols = kOTerms * kRows;               // of the scores
   static constexpr int kOCols = kOTerms * kRows;              // of the output
   static constexpr int kOBuf = 2;                            // outputs, as many as tiles of weights: see o_empty
-  static constexpr int kQBytes = kQCols * 128 * kBlk;
   static constexpr bool kSplit = kRows == 64;               // the softmax groups share each tile's rows
   // Tiles whose scores are ahead of the output: when a softmax group ends a tile, its next one's scores are there.
   static constexpr int kAhead = kSplit ? 1 : 2;
@@ -122,7 +121,7 @@ struct Cfg {
   static constexpr int kQBuf = kAhead + 1;
   // A unit's fixed work (its query rows, its result, the ends of its pipeline) in tiles, for the cut of the line. It
   // takes as long as so many: 32 trees of 48 rows on 129..16384 tokens, bf16, with 0 / 2 / 4 / 5 / 6: 174 / 126 / 113 /
-  // 109 / 115 us, E4M3 with 0 / 5 / 9: 199 / 121 / 106 us. 128 single tokens on 129..8192: bf16 with 0 / 2 / 5 / 7:
+  // 109 / 115 us, E4M3 with 0 / 5 / 9: 199 / 121 / 106 us (before later steps). 128 single tokens on 129..8192: bf16 with 0 / 2 / 5 / 7:
   // 168 / 161 / 166 / 169 us; 256 on 1k..8k, E4M3 with 0 / 4 / 6: 297 / 286 / 295 us.
   static constexpr int kSegCost = kRows == 16 ? (kE4m3 ? 4 : 2) : kE4m3 ? 9 : 5;
   static constexpr int kOutGroups = kRows == 16 ? 1 : 2;    // at few rows a group's fixed work outweighs the rows'
@@ -135,8 +134,7 @@ struct Cfg {
   static constexpr int kOutRows = kHalves >= kOutGroups ? kRows : kRows / 2;               // and its rows
   // shared memory behind the ring, by byte offsets from its end
   static constexpr int oP = 0;
-  static constexpr int oQ = oP + 2 * (int)kBlock;
-  static constexpr int oSc = oQ + kQBuf * kQBytes;                          // [kScSlots][2][128] fp32
+  static constexpr int oSc = oP + 2 * (int)kBlock;                          // [kScSlots][2][128] fp32
   static constexpr int oMax = oSc + (kE4m3 ? kScSlots * 2 * kTile * 4 : 0);  // [2][4 warps][kRows + 4]
   static constexpr int oSum = oMax + 2 * (kRows + 4) * 16;                  // [2][4 warps][kRows]
   static constexpr int oWarp = oSum + 2 * kRows * 16;                       // [8 warps][kSoftRows]
@@ -144,16 +142,24 @@ struct Cfg {
   static constexpr int oAb = oTile + 2 * (kRows + 4) * 4;                   // [2 groups][2][2][kRows]
   static constexpr int oMask = oAb + 8 * kRows * 4;                         // [kQBuf][kRows] uint64
   static constexpr int oQs = oMask + kQBuf * kRows * 8;                     // [kQBuf][kRows] fp32
-  static constexpr int oFin = oQs + kQBuf * kRows * 4;                      // [2 groups][2][kRows] fp32
-  static constexpr int kStageRows = kOutHalves == 2 ? 4 : 8;                // rows of a result on their way out at a time
-  static constexpr int oStage = oFin + 4 * kRows * 4;                       // [kOutGroups][kStageRows][kOutHalves * 128] fp32
+  static constexpr int oFin = oQs + kQBuf * kRows * 4;                      // [2 groups][kRows] fp32
+  static constexpr int kStageRows = kOutHalves == 2 ? 4 : 8;                             // rows of a result on their way out at a time
+  static constexpr int oStage = oFin + 2 * kRows * 4;                       // [kOutGroups][kStageRows][kOutHalves * 128] fp32
   static constexpr int oBars = oStage + kOutGroups * kStageRows * kOutHalves * 512;
-  static constexpr int kRest = oBars + 1408;
-  static constexpr int kFit = (kSmemLimit - kRest) / (int)kBlock;
-  // an even number of blocks keeps the two bf16 blocks of a 128-wide half of V side by side
-  static constexpr int kStages = kE4m3 ? kFit : kFit / 2 * 2;
-  static constexpr int kSmem = kStages * (int)kBlock + kRest;
-  static_assert(kStages >= kBlk + 2, "a tile's whole V stays until its weights are there");
+  // Q's buffers at the end, for the rows that there are: what they leave is the ring's. 48 rows of a bf16 cache of 256
+  // wide heads have eight blocks, two more than 64. (Not for summed terms: their loops are slower with sizes of the run,
+  // 311 us against 306 for 64 rows on 131071 tokens, 100 against 95 for 32 x 48 rows.)
+  static constexpr int oQ = (oBars + kBarBytes + 1023) / 1024 * 1024;
+  static __host__ __device__ constexpr int row_pad(int rows) { return kE4m3 ? (rows + 7) / 8 * 8 : (rows + 15) / 16 * 16; }
+  static __host__ __device__ constexpr int q_block(int rows) { return kTerms * (kSumTerms ? kRows : row_pad(rows)) * 128; }
+  static __host__ __device__ constexpr int q_bytes(int rows) { return q_block(rows) * kBlk; }
+  static __host__ __device__ constexpr int rest_bytes(int rows) { return oQ + kQBuf * q_bytes(rows); }  // behind the ring
+  static __host__ __device__ constexpr int stages(int rows) {
+    const int fit = (kSmemLimit - rest_bytes(rows)) / (int)kBlock, most = fit < 11 ? fit : 11;
+    // an even number of blocks keeps the two bf16 blocks of a 128-wide half of V side by side
+    return kE4m3 ? most : most / 2 * 2;
+  }
+  static_assert(stages(kRows) >= kBlk + 2, "a tile's whole V stays until its weights are there");
   static_assert(2 * kCols + kOBuf * kHalves * kOCols <= 512, "tensor memory");
 };
 
@@ -178,7 +184,7 @@ struct Bars {
   Plan plan;
   long long warp_total[20];
 };
-static_assert(sizeof(Bars) <= 1408, "barrier area");
+static_assert(sizeof(Bars) <= kBarBytes, "barrier area");
 
 // The piece's segments: runs of tiles of one (request n, unit u = head x row tiles + row tile).
 struct Seg {
@@ -441,12 +447,12 @@ __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned 
   using C = Cfg<D, kE4m3, kRows>;
   const TreeAttnArgs& p = a.p;
   const int lane = threadIdx.x & 31;
-  const int rp = kE4m3 ? (a.rows + 7) / 8 * 8 : (a.rows + 15) / 16 * 16;
+  const int rp = C::row_pad(a.rows), q_block = C::q_block(a.rows);
   // scores are maxima before they are scaled: a negative scale turns the query's sign, none leaves zeros
   const uint32_t sign = p.scale < 0.f ? 0x80008000u : 0u, mask_q = p.scale == 0.f ? 0u : ~0u;
   const float to_log2 = p.scale == 0.f ? 1.f : fabsf(p.scale) * kLog2e;
   const int h = s.u / a.row_tiles, r0 = (s.u % a.row_tiles) * a.rows;
-  unsigned char* q_s = rest + C::oQ + qb * C::kQBytes;
+  unsigned char* q_s = rest + C::oQ + qb * C::q_bytes(a.rows);
   float* qs_s = reinterpret_cast<float*>(rest + C::oQs) + qb * kRows;
   uint64_t* mask_s = reinterpret_cast<uint64_t*>(rest + C::oMask) + qb * kRows;
   if (share == 0)
@@ -476,7 +482,7 @@ __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned 
       if constexpr (!kE4m3) {
         // eight values are one 16-byte piece of block lane / 8
         if (lane < D / 8)
-          *reinterpret_cast<uint4*>(q_s + (lane >> 3) * (C::kQCols * 128) + swz(r, (lane & 7) * 16)) = raw[i];
+          *reinterpret_cast<uint4*>(q_s + (lane >> 3) * q_block + swz(r, (lane & 7) * 16)) = raw[i];
         if (lane == 0) qs_s[r] = fmaxf(to_log2, 1e-37f);
       } else {
         const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
@@ -498,7 +504,7 @@ __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned 
         uint2 first, second;
         two_terms(x, first, second);
         if (lane < D / 8) {
-          unsigned char* blk = q_s + (lane >> 4) * (C::kQCols * 128);
+          unsigned char* blk = q_s + (lane >> 4) * q_block;
           *reinterpret_cast<uint2*>(blk + swz(r, (lane & 15) * 8)) = first;
           *reinterpret_cast<uint2*>(blk + swz(rp + r, (lane & 15) * 8)) = second;
         }
@@ -515,7 +521,8 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
   using C = Cfg<D, kE4m3, kRows>;
   constexpr int kThreads = C::kThreads;
   extern __shared__ __align__(1024) unsigned char smem[];
-  unsigned char* rest = smem + C::kStages * kBlock;
+  const int stages = C::stages(a.rows);
+  unsigned char* rest = smem + stages * kBlock;
   Bars* B = reinterpret_cast<Bars*>(rest + C::oBars);
   const TreeAttnArgs& p = a.p;
   const KvArgs& c = a.c;
@@ -540,7 +547,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
     }
     if (lane == 31) B->warp_total[warp] = upto;
     if (tid == 0) {
-      for (int i = 0; i < C::kStages; ++i) mbar_init(&B->empty[i], 1);
+      for (int i = 0; i < stages; ++i) mbar_init(&B->empty[i], 1);
       for (int i = 0; i < kSlots; ++i) {
         mbar_init(&B->k_full[i], 1);
         mbar_init(&B->v_full[i], 1);
@@ -635,7 +642,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         ok = __all_sync(0xffffffffu, ok && wait(&B->empty[st], phase, abort));
         if (ok && lane < boxes)
           tma_load_2d(smem + st * kBlock + lane * a.box * 128, map, b * (kE4m3 ? 128 : 64), row, full);
-        if (++st == C::kStages) st = 0, phase ^= 1;
+        if (++st == stages) st = 0, phase ^= 1;
       }
     };
     Walk<C::kSegCost> walk(a, plan);
@@ -702,7 +709,8 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
     // ------------------------------------------------------------ MMAs
     // The whole warp walks and waits, one elected thread issues: with `if (lane == 0)` instead an MMA took
     // 73 cycles to issue on an idle SM, and about 200 next to the other warps; its work is 41 at 16 columns.
-    const int rp = kE4m3 ? (a.rows + 7) / 8 * 8 : (a.rows + 15) / 16 * 16;  // rows as columns of the MMAs
+    const int rp = C::row_pad(a.rows);  // rows as columns of the MMAs
+    const int q_block = C::q_block(a.rows), q_bytes = C::q_bytes(a.rows);
     // (an MMA of 128 lanes takes columns by sixteens)
     const int N = C::kSumTerms ? (rp + 15) / 16 * 16 : C::kTerms * rp;
     constexpr uint32_t kKind = kE4m3 ? umma::kKindF8 : umma::kKindF16, kType = kE4m3 ? umma::kE4M3 : umma::kBF16;
@@ -754,7 +762,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
           }
         }
         __syncwarp();
-        st = st2 + 1 == C::kStages ? 0 : st2 + 1;
+        st = st2 + 1 == stages ? 0 : st2 + 1;
       }
     };
     Walk<C::kSegCost> walk(a, plan);
@@ -771,7 +779,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
           umma::fence_after_sync();
           if (elect_one()) {
             const uint64_t ka = umma::smem_desc_sw128(ring + st * kBlock);
-            const uint64_t qa = umma::smem_desc_sw128(sQ + qb * C::kQBytes + kb * (C::kQCols * 128));
+            const uint64_t qa = umma::smem_desc_sw128(sQ + qb * q_bytes + kb * q_block);
 #pragma unroll
             for (int k = 0; k < 4; ++k) umma::mma<kKind>(tmem + b * C::kCols, ka + 2 * k, qa + 2 * k, id_s, kb + k > 0);
             if constexpr (C::kSumTerms) {  // the second terms, rp rows on
@@ -786,7 +794,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
             }
           }
           __syncwarp();
-          if (++st == C::kStages) st = 0;
+          if (++st == stages) st = 0;
         }
         if (ok && i >= C::kAhead) product_o(i - C::kAhead);
       }
@@ -859,7 +867,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         const int first = C::kBlk * min(i + 1 + C::kAhead, tiles) + C::kBlk * i;
         auto piece = [&](int k) {
           const int row = row0 + k / (8 * C::kBlk), x = k % (8 * C::kBlk);
-          return reinterpret_cast<uint4*>(smem + (first + (x >> 3)) % C::kStages * kBlock + row * 128) + (x & 7);
+          return reinterpret_cast<uint4*>(smem + (first + (x >> 3)) % stages * kBlock + row * 128) + (x & 7);
         };
         const int kept = (end - row0) * (8 * C::kBlk), all = (row1 - row0) * (8 * C::kBlk);
 #pragma unroll 1
@@ -902,7 +910,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
     // instruction for each row's maximum twice as long.)
     const int wg = warp >> 2, w4 = warp & 3, a4 = lane & 3;
     constexpr int kR = C::kSoftRows, kC = kR / 8;
-    const int rp = kE4m3 ? (a.rows + 7) / 8 * 8 : (a.rows + 15) / 16 * 16;
+    const int rp = C::row_pad(a.rows);
     const int roff = C::kSplit ? wg * kR : 0;                            // this group's first row
     const int used = min(kC, max(0, (a.rows - roff + 7) / 8));           // its groups of eight rows
     const int mine = reduced_column<kC>(lane);                           // the row whose statistics end in this lane
@@ -1090,7 +1098,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
     const float* sums = reinterpret_cast<const float*>(rest + C::oSum);
     const float* tile_s = reinterpret_cast<const float*>(rest + C::oTile);
     float* ab = reinterpret_cast<float*>(rest + C::oAb) + og * 4 * kRows;
-    float* fin = reinterpret_cast<float*>(rest + C::oFin) + og * 2 * kRows;
+    float* fin = reinterpret_cast<float*>(rest + C::oFin) + og * kRows;
     int marks = 0;
     Walk<C::kSegCost> walk(a, plan);
     Seg s;
@@ -1288,9 +1296,10 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
 template <int D, bool kE4m3, int kRows>
 cudaError_t launch_rows(const Args& a, const CUtensorMap& tmk, const CUtensorMap& tmv, int grid, cudaStream_t stream) {
   using C = Cfg<D, kE4m3, kRows>;
-  const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(&tree_attn_kernel<D, kE4m3, kRows>), C::kSmem);
+  const cudaError_t err =
+      ensure_dynamic_smem(reinterpret_cast<const void*>(&tree_attn_kernel<D, kE4m3, kRows>), kSmemLimit);
   if (err != cudaSuccess) return err;
-  tree_attn_kernel<D, kE4m3, kRows><<<grid, C::kThreads, C::kSmem, stream>>>(a, tmk, tmv);
+  tree_attn_kernel<D, kE4m3, kRows><<<grid, C::kThreads, C::stages(a.rows) * (int)kBlock + C::rest_bytes(a.rows), stream>>>(a, tmk, tmv);
   return cudaGetLastError();
 }
 
