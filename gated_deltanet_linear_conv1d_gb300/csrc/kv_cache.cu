@@ -462,12 +462,12 @@ cudaError_t launch_rows(const RopeArgs& a, const KvArgs& c, bool norm, int D, cu
   const int most = 152 * kMaxTokens, waves = a.T / most + (a.T % most != 0), blocks = 152 * waves;
   int per = a.T / blocks + (a.T % blocks != 0);
   if (per > 4) per = (per + 3) / 4 * 4;
-  const dim3 grid((unsigned)((a.T + per - 1) / per), norm && a.q ? 2 : 1, 1);
+  const dim3 grid((unsigned)(((long long)a.T + per - 1) / per), norm && a.q ? 2 : 1, 1);
   return D == 256 ? run_rows<256>(a, c, norm, grid, per, stream) : run_rows<128>(a, c, norm, grid, per, stream);
 }
 
 cudaError_t launch_kv_read(const ReadArgs& a, const KvArgs& c, int D, cudaStream_t stream) {
-  const unsigned grid = (unsigned)((a.T + kReadTokens - 1) / kReadTokens);
+  const unsigned grid = (unsigned)(((long long)a.T + kReadTokens - 1) / kReadTokens);
   if (D == 256) read_kernel<256><<<grid, kThreads, 0, stream>>>(a, c);
   else read_kernel<128><<<grid, kThreads, 0, stream>>>(a, c);
   return cudaGetLastError();

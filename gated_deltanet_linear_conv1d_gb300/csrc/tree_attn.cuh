@@ -120,10 +120,11 @@ struct Cfg {
   // query buffers: a tile's scores wait for no output that follows them, though every segment have one tile
   static constexpr int kQBuf = kAhead + 1;
   // A unit's fixed work (its query rows, its result, the ends of its pipeline) in tiles, for the cut of the line. It
-  // takes as long as so many: 32 trees of 48 rows on 129..16384 tokens, bf16, with 0 / 2 / 4 / 5 / 6: 174 / 126 / 113 /
-  // 109 / 115 us, E4M3 with 0 / 5 / 9: 199 / 121 / 106 us (before later steps). 128 single tokens on 129..8192: bf16 with 0 / 2 / 5 / 7:
-  // 168 / 161 / 166 / 169 us; 256 on 1k..8k, E4M3 with 0 / 4 / 6: 297 / 286 / 295 us.
-  static constexpr int kSegCost = kRows == 16 ? (kE4m3 ? 4 : 2) : kE4m3 ? 9 : 5;
+  // takes as long as so many. 32 trees of 48 rows on 129..16384 tokens, bf16, with 0 / 2 / 4 / 5 / 6: 174 / 126 / 113 /
+  // 109 / 115 us, E4M3 with 0 / 5 / 9: 199 / 121 / 106 us; 128 single tokens on 129..8192, bf16 with 0 / 2 / 5 / 7:
+  // 168 / 161 / 166 / 169 us; 256 on 1k..8k, E4M3 with 0 / 4 / 6: 297 / 286 / 295 us (all before later steps); heads of
+  // 128 have smaller tiles: 128 single tokens on 129..8192, E4M3 with 3 / 4 / 5 / 6: 140 / 144 / 138 / 131 us.
+  static constexpr int kSegCost = kRows > 16 ? (kE4m3 ? 9 : 5) : !kE4m3 ? 2 : D == 256 ? 4 : 6;
   static constexpr int kOutGroups = kRows == 16 ? 1 : 2;    // at few rows a group's fixed work outweighs the rows'
   static constexpr int kOutWarp = 8, kCopyWarp = kOutWarp + 4 * kOutGroups;  // first warps of the roles
   static constexpr int kMmaWarp = kCopyWarp + 1, kQueryWarp = kCopyWarp + 2, kCheckWarp = kCopyWarp + 3;
