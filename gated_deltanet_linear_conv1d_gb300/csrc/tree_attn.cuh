@@ -38,8 +38,9 @@
 // tile's product times e^(tile's maximum - running maximum). So the next tile's
 // scores never wait for the last one's.
 //
-// Roles: two groups of four warps for the softmax (a thread per token), which
-// take turns at the tiles, or, from 33 rows on, half of a tile's rows each; one
+// Roles: two groups of four warps for the softmax (a thread has four tokens and a
+// quarter of the rows), which take turns at the tiles, or, from 33 rows on, half
+// of a tile's rows each; one
 // group of four warps for the output (a thread per value of D, mod 128), from 17
 // rows on two with half of D each, or half of the rows at D = 128; a warp for the
 // copies (TMA, 16 KB blocks of 128 tokens x 128 bytes into a ring), one for the
@@ -113,7 +114,7 @@ struct Cfg {
   static constexpr int kOTerms = kSumTerms ? 1 : kTerms;
   static constexpr int kCols = kOTerms * kRows;               // of the scores
   static constexpr int kOCols = kOTerms * kRows;              // of the output
-  static constexpr int kOBuf = 2;                            // outputs, as many as tiles of weights: see o_empty
+  static constexpr int kOBuf = 2;                             // outputs, as many as tiles of weights: see o_empty
   static constexpr bool kSplit = kRows == 64;               // the softmax groups share each tile's rows
   // Tiles whose scores are ahead of the output: when a softmax group ends a tile, its next one's scores are there.
   static constexpr int kAhead = kSplit ? 1 : 2;
@@ -144,7 +145,7 @@ struct Cfg {
   static constexpr int oMask = oAb + 8 * kRows * 4;                         // [kQBuf][kRows] uint64
   static constexpr int oQs = oMask + kQBuf * kRows * 8;                     // [kQBuf][kRows] fp32
   static constexpr int oFin = oQs + kQBuf * kRows * 4;                      // [2 groups][kRows] fp32
-  static constexpr int kStageRows = kOutHalves == 2 ? 4 : 8;                             // rows of a result on their way out at a time
+  static constexpr int kStageRows = kOutHalves == 2 ? 4 : 8;                // rows of a result on their way out at a time
   static constexpr int oStage = oFin + 2 * kRows * 4;                       // [kOutGroups][kStageRows][kOutHalves * 128] fp32
   static constexpr int oBars = oStage + kOutGroups * kStageRows * kOutHalves * 512;
   // Q's buffers at the end, for the rows that there are: what they leave is the ring's. 48 rows of a bf16 cache of 256
@@ -1215,7 +1216,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
       const bool bad = *(volatile int*)&B->bad[seg % kMarks] != 0;
       if (lane == 0) arrive(&B->q_empty[qb]);
       ++seg;
-      // ---- the segment's result: whole, or a partial for the CTA that arrives last
+      // ---- the segment's result: whole, or a partial for the join
       if (any_in_group(bar, *(volatile int*)abort)) continue;
       if (bad && ot == 0) report(p.dev_err, GDN_DEVERR_SLOT);
       if (s.t0 == 0 && s.t1 == s.tiles) {
