@@ -23,6 +23,7 @@ int slot_floats(int rows, int D) { return (tree_attn::head_floats(rows) + rows *
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const tree_attn::Args a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
   const TreeAttnArgs& p = a.p;
   const tree_attn::Desc d = static_cast<const tree_attn::Desc*>(p.workspace)[blockIdx.x];
   if (!d.valid) return;
