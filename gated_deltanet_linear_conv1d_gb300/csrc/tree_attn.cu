@@ -20,6 +20,8 @@ int slot_floats(int rows, int D) { return (tree_attn::head_floats(rows) + rows *
 
 // The partial results of the units that several CTAs share, one after the other in the order of their tiles:
 // blockIdx.x is the CTA with a unit's first tile, blockIdx.y 1024 / D of its rows, a thread has four values.
+// Bound by its chain of trips to L2, the descriptor, the maxima and the rows: 9.5 us cold for the 11 MB of 64 nodes on
+// 131,071 tokens (2432 blocks), set up while the tiles' kernel runs.
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const tree_attn::Args a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
