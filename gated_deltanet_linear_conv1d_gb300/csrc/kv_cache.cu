@@ -163,6 +163,7 @@ __device__ __forceinline__ void rows_pass(const RopeArgs& p, const KvArgs& c, co
     }
     int buf = 0;
     for (int tl = 0; tl < T; tl += kStep) {
+      __syncwarp();  // the batch before has been read, by lanes other than those that copied it: its buffer is next
       fetch(tl + kAhead * kStep, buf == 0 ? kAhead : buf - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
       __syncwarp();
