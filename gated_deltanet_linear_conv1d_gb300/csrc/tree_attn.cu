@@ -40,6 +40,9 @@ __global__ void __launch_bounds__(256) join_kernel(const tree_attn::Args a) {
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   bool bad = false;
+  // E4M3: the maxima are those of the weights with the value scales, the sums are not. A sum may hold against a factor
+  // that is too small for a number: there a factor is the square of its root, which is 1 for bf16.
+  const float part = a.c.e4m3 ? 0.5f : 1.f;
   constexpr int kAtOnce = 4;
   for (int k0 = blockIdx.x; k0 <= d.last; k0 += kAtOnce) {
     float mk[kAtOnce], lk[kAtOnce];
@@ -57,13 +60,14 @@ __global__ void __launch_bounds__(256) join_kernel(const tree_attn::Args a) {
     float mn = m;
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) mn = fmaxf(mn, mk[i]);
-    const float keep = m == -INFINITY ? 0.f : tree_attn::ex2(m - mn);
-    l *= keep;
+    const float root = m == -INFINITY ? 0.f : tree_attn::ex2((m - mn) * part), again = a.c.e4m3 ? root : 1.f;
+    const float keep = root * again;
+    l = l * root * again;
     o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
-      const float w = mk[i] == -INFINITY ? 0.f : tree_attn::ex2(mk[i] - mn);
-      l += mk[i] == -INFINITY ? lk[i] : lk[i] * w;  // a NaN of a row without a maximum stays one
+      const float wr = mk[i] == -INFINITY ? 0.f : tree_attn::ex2((mk[i] - mn) * part), wa = a.c.e4m3 ? wr : 1.f, w = wr * wa;
+      l += mk[i] == -INFINITY ? lk[i] : lk[i] * wr * wa;  // a NaN of a row without a maximum stays one
       o = make_float4(fmaf(v[i].x, w, o.x), fmaf(v[i].y, w, o.y), fmaf(v[i].z, w, o.z), fmaf(v[i].w, w, o.w));
     }
     m = mn;

@@ -27,16 +27,27 @@
 // the other operand is written as the sum of two E4M3 terms, the value and what
 // its rounding left: 4 + 4 significant bits, as many as bf16 has. For Q (bf16
 // values, scaled by a power of two per row) that is exact down to 2^-17 of the
-// row's largest value; a weight of P is off by at most 2^-8 of itself or 2^-18 of
-// its tile's largest. The two terms are columns of one MMA, added up as they are
-// read, or from 33 rows on two MMAs into the same columns. The scales stay
-// outside: the key's multiplies the score, the value's its weight (relative to
-// the tile's largest scale).
+// row's largest value; a weight of P, which is one of the softmax times its value's
+// scale, is off by 2^-8 + 2^-11 of itself or 2^-17 of the row's largest in the tile.
+// The two terms are columns of one MMA, added up as they are read, or from 33 rows
+// on two MMAs into the same columns. The key's scale multiplies the score.
+// (A bf16 cache's weights go to bf16, 2^-8 of each; their sum is that of the fp32
+// weights either way.)
 //
 // Softmax without a chain between tiles: a tile's weights are taken relative to
 // its own maximum, and the accumulators of the output, in registers, take the
 // tile's product times e^(tile's maximum - running maximum). So the next tile's
 // scores never wait for the last one's.
+//
+// With an E4M3 cache the maximum is that of s_t log2(e) + e_t, 2^e_t the power of two
+// of the value's scale v_t: what E4M3 holds best are a row's largest weights with
+// their scales, not those of a token that it does not see or hardly weighs. (With
+// the weights alone relative to their maximum and the scales to the tile's largest,
+// a sibling node's scale of 2^14 times the others' put its neighbours' rows off by 14 %.)
+// The fp32 weight 2^(s_t log2(e) + e_t - maximum) goes to P times v_t / 2^e_t, to the
+// sum times 1 / 2^e_t. It costs a multiply-add for two scores and saves the scales'
+// maximum: 64 rows on 131071 tokens 303 us, 308 with the two maxima apart; with a test
+// of each tile's scales and a second pass where they are far apart, 323 .. 337.
 //
 // Roles: two groups of four warps for the softmax (a thread has four tokens and a
 // quarter of the rows), which take turns at the tiles, or, from 33 rows on, half
@@ -78,6 +89,14 @@ constexpr int kScSlots = 4;              // tiles of scales in flight
 constexpr int kSlots = 8, kMarks = 16;
 constexpr int kBarBytes = 1216;
 constexpr float kLog2e = 1.4426950408889634f;
+// E4M3: the largest of a row's fp32 weights in a tile is 2^kTopExp, so that one of 2^-190 of it, a value scale of the
+// smallest next to the largest, counts in the sum, and 128 of the most by 2 / 2^kMinScaleExp are no more than a number.
+// As E4M3 terms, before v_t / 2^e_t in [1, 2), that weight is kTermTop: 448 is the largest.
+constexpr int kTopExp = 64;
+constexpr float kTermTop = 224.f;
+// Exponents of the value scales: none below this. A write leaves -49 at least; of smaller scales a row that sees no other
+// holds its weights to 2^-17 of 2^-50.
+constexpr int kMinScaleExp = -50;
 
 struct Args {
   TreeAttnArgs p;
@@ -143,8 +162,8 @@ struct Cfg {
   static constexpr int oMax = oSc + (kE4m3 ? kScSlots * 2 * kTile * 4 : 0);  // [2][4 warps][kRows + 4]
   static constexpr int oSum = oMax + 2 * (kRows + 4) * 16;                  // [2][4 warps][kRows]
   static constexpr int oWarp = oSum + 2 * kRows * 16;                       // [8 warps][kSoftRows]
-  static constexpr int oTile = oWarp + 8 * kSoftRows * 4;                   // [2][kRows + 4]: maxima, the V scale
-  static constexpr int oAb = oTile + 2 * (kRows + 4) * 4;                   // [2 groups][2][2][kRows]
+  static constexpr int oTile = oWarp + 8 * kSoftRows * 4;                   // [2][kRows]: maxima
+  static constexpr int oAb = oTile + 2 * kRows * 4;                         // [2 groups][2][2][kRows]
   static constexpr int oMask = oAb + 8 * kRows * 4;                         // [kQBuf][kRows] uint64
   static constexpr int oQs = oMask + kQBuf * kRows * 8;                     // [kQBuf][kRows] fp32
   static constexpr int oFin = oQs + kQBuf * kRows * 4;                      // [2 groups][kRows] fp32
@@ -363,8 +382,16 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
       : "r"(h));
   return r;
 }
+// 2^e.
+constexpr float exp2_of(int e) { return e == 0 ? 1.f : e < 0 ? 0.5f * exp2_of(e + 1) : 2.f * exp2_of(e - 1); }
+// The exponent of a value scale, 128 of one that is no number, and 2 / 2^exponent, which is 0 then.
+__device__ __forceinline__ int scale_exp(float s) {
+  return max((int)(__float_as_uint(s) >> 23 & 255u) - 127, kMinScaleExp);
+}
+__device__ __forceinline__ float two_over_exp(float s) { return __uint_as_float((uint32_t)(128 - scale_exp(s)) << 23); }
+
 // Two values as E4M3 (lower half) and what their rounding left, again as E4M3 (upper half). By way of fp16, whose 11
-// bits hold the two terms' 4 + 4 and what is lost to it (2^-12) is far below what is lost to them.
+// bits hold the two terms' 4 + 4 and what is lost to it (2^-11) is below what is lost to them (2^-8).
 __device__ __forceinline__ uint32_t two_terms(float2 x) {
   uint32_t h, back;
   uint16_t first, rest;
@@ -942,7 +969,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
       for (int t = s.t0; t < s.t1; ++t, ++i) {
         const int b = i & 1, ph = (i >> 1) & 1;
         if (!C::kSplit && b != wg) continue;
-        float sk[4], sv[4];
+        float sk[4], sv[4], ev[4];  // the scales, and the exponents of the values'
         if constexpr (kE4m3) {
           const int slot = i % kScSlots;
           wait_warp(&B->sc_full[slot], (i / kScSlots) & 1, abort);
@@ -953,10 +980,18 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
           }
           __syncwarp();
           if (lane == 0) arrive(&B->sc_empty[slot]);
+          if ((t + 1) * kTile > s.ctx) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)  // the values of such a node are zeros, see the check warp
+              if (t * kTile + tt + 8 * k >= s.ctx && !(fabsf(sv[k]) < INFINITY)) sv[k] = 0.f;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ev[k] = (float)scale_exp(sv[k]);
         }
         wait_warp(&B->s_full[b], ph, abort);
         umma::fence_after_sync();
-        float2 x[kC][4];  // scores, not yet taken times the row's factor
+        // scores, not yet taken times the row's factor; E4M3: to base 2, with the exponent of the token's value scale
+        float2 x[kC][4];
         const uint32_t ts = umma::taddr(tmem, 32 * w4, b * C::kCols + roff);
 #pragma unroll
         for (int g = 0; g < kC; ++g)
@@ -964,13 +999,15 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
             uint32_t u[4][2], w[4][2];
             ld_tile8(ts + g * 8, ts + (16u << 16) + g * 8, u);
             if constexpr (C::kOTerms == 2) ld_tile8(ts + rp + g * 8, ts + (16u << 16) + rp + g * 8, w);
+            float2 q2;
+            if constexpr (kE4m3) q2 = *reinterpret_cast<const float2*>(qs_s + g * 8 + a4 * 2);
             umma::wait_ld();
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               float2 v = make_float2(__uint_as_float(u[k][0]), __uint_as_float(u[k][1]));
               if constexpr (C::kOTerms == 2)
                 v = __fadd2_rn(v, make_float2(__uint_as_float(w[k][0]), __uint_as_float(w[k][1])));
-              if constexpr (kE4m3) v = __fmul2_rn(v, make_float2(sk[k], sk[k]));
+              if constexpr (kE4m3) v = __ffma2_rn(__fmul2_rn(v, make_float2(sk[k], sk[k])), q2, make_float2(ev[k], ev[k]));
               x[g][k] = v;
             }
           } else {
@@ -1001,11 +1038,6 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
                 if (!((hi >> (8 * k)) & 1)) x[g][k].y = -INFINITY;
               }
             }
-          if constexpr (kE4m3) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)  // the values of such a node are zeros, see the check warp
-              if (node0 + 8 * k >= 0 && !(fabsf(sv[k]) < INFINITY)) sv[k] = 0.f;
-          }
         }
         // ---- the tile's maximum of each row: of the warp first, then of the four warps
         float* max_b = maxima + b * 4 * (kRows + 4);
@@ -1017,27 +1049,22 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
                                fmaxf(fmaxf(x[g][0].y, x[g][1].y), fmaxf(x[g][2].y, x[g][3].y)));
           max_b[w4 * (kRows + 4) + roff + mine] = reduce_pairs<kC>(m, lane, [](float u, float v) { return fmaxf(u, v); });
         }
-        if constexpr (kE4m3) {
-          float m = fmaxf(fmaxf(fabsf(sv[0]), fabsf(sv[1])), fmaxf(fabsf(sv[2]), fabsf(sv[3])));
-          m = warp_max(m);
-          if (lane == 0) max_b[w4 * (kRows + 4) + kRows + wg] = m;
-        }
         sync_group(1 + wg);
         if (lane < kR) {
           const float* at = max_b + roff + lane;
           const float m = fmaxf(fmaxf(at[0], at[kRows + 4]), fmaxf(at[2 * (kRows + 4)], at[3 * (kRows + 4)]));
-          const float scaled = m == -INFINITY ? m : m * qs_s[lane];
-          warp_s[lane] = m == -INFINITY ? 0.f : -scaled;
-          if (w4 == 0) tile_s[b * (kRows + 4) + roff + lane] = scaled;
+          const float scaled = kE4m3 || m == -INFINITY ? m : m * qs_s[lane];
+          warp_s[lane] = m == -INFINITY ? 0.f : kE4m3 ? kTopExp - scaled : -scaled;
+          if (w4 == 0) tile_s[b * kRows + roff + lane] = scaled;
         }
-        float f[4] = {1.f, 1.f, 1.f, 1.f};  // the weights' factors: the value's scale, the tile's largest at 256
+        // what makes of a weight with its value's power of two the one with its scale, as a term, and twice the plain one
+        float f[4], part[4];
         if constexpr (kE4m3) {
-          const float* at = max_b + kRows + wg;
-          const float most = fmaxf(fmaxf(at[0], at[kRows + 4]), fmaxf(at[2 * (kRows + 4)], at[3 * (kRows + 4)]));
-          const float up = most < 1e-30f ? 0x1p64f : most > 1e30f ? 0x1p-64f : 1.f, r = __fdividef(256.f, most * up);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) f[k] = sv[k] == 0.f ? 0.f : sv[k] * up * r;
-          if ((tid & 127) == 0 && roff == 0) tile_s[b * (kRows + 4) + kRows] = most * (1.f / 256.f);
+          for (int k = 0; k < 4; ++k) {
+            part[k] = two_over_exp(sv[k]);
+            f[k] = sv[k] * part[k] * (0.5f * kTermTop * exp2_of(-kTopExp));
+          }
         }
         __syncwarp();
         const uint32_t prow = smem_u32(rest + C::oP + b * kBlock) + (32 * w4 + lane) * 128;
@@ -1045,12 +1072,13 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
 #pragma unroll
         for (int g = 0; g < kC; ++g)
           if (g < used) {
-            const float2 q2 = *reinterpret_cast<const float2*>(qs_s + g * 8 + a4 * 2);
+            float2 q2;
+            if constexpr (!kE4m3) q2 = *reinterpret_cast<const float2*>(qs_s + g * 8 + a4 * 2);
             const float2 m2 = *reinterpret_cast<const float2*>(warp_s + g * 8 + a4 * 2);
             uint32_t r[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float2 v = __ffma2_rn(x[g][k], q2, m2);
+              const float2 v = kE4m3 ? __fadd2_rn(x[g][k], m2) : __ffma2_rn(x[g][k], q2, m2);
               x[g][k] = make_float2(ex2(v.x), ex2(v.y));
               if constexpr (kE4m3) {
                 r[k] = two_terms(__fmul2_rn(x[g][k], make_float2(f[k], f[k])));
@@ -1089,7 +1117,13 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
           float2 v[kC];
 #pragma unroll
           for (int g = 0; g < kC; ++g)
-            v[g] = __fadd2_rn(__fadd2_rn(x[g][0], x[g][1]), __fadd2_rn(x[g][2], x[g][3]));
+            if constexpr (kE4m3) {
+              v[g] = __fmul2_rn(x[g][0], make_float2(part[0], part[0]));
+#pragma unroll
+              for (int k = 1; k < 4; ++k) v[g] = __ffma2_rn(x[g][k], make_float2(part[k], part[k]), v[g]);
+            } else {
+              v[g] = __fadd2_rn(__fadd2_rn(x[g][0], x[g][1]), __fadd2_rn(x[g][2], x[g][3]));
+            }
           sums[(b * 4 + w4) * kRows + roff + mine] = reduce_pairs<kC>(v, lane, [](float u, float w) { return u + w; });
         }
         arrive(&B->st_full[b]);
@@ -1134,16 +1168,26 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
         float* w_s = keep_s + kRows;
         bool moved = false;  // a running maximum has changed
         if (ot < a.rows) {
-          const float mt = tile_s[b * (kRows + 4) + ot];
+          const float mt = tile_s[b * kRows + ot];
           const float* l4 = sums + b * 4 * kRows + ot;
-          const float lt = (l4[0] + l4[kRows]) + (l4[2 * kRows] + l4[3 * kRows]);
+          float lt = (l4[0] + l4[kRows]) + (l4[2 * kRows] + l4[3 * kRows]);
           const float mn = fmaxf(m_run, mt);
-          const float keep = m_run == -INFINITY ? 0.f : ex2(m_run - mn), w = mt == -INFINITY ? 0.f : ex2(mt - mn);
+          // E4M3: the maxima are those of the weights with the value scales, the sums are not. A sum may hold against a
+          // factor that is too small for a number, so it is taken times the factor's root twice.
+          constexpr float kPart = kE4m3 ? 0.5f : 1.f;
+          float keep = m_run == -INFINITY ? 0.f : ex2((m_run - mn) * kPart), w = mt == -INFINITY ? 0.f : ex2((mt - mn) * kPart);
+          if constexpr (kE4m3) {
+            lt *= exp2_of(-kTopExp - 1);
+            l_run = l_run * keep * keep + lt * w * w;
+            keep *= keep;
+            w *= w;
+          } else {
+            l_run = l_run * keep + lt * w;
+          }
           moved = keep != 1.f;
-          l_run = l_run * keep + lt * w;
           m_run = mn;
           keep_s[ot] = keep;
-          w_s[ot] = kE4m3 ? w * tile_s[b * (kRows + 4) + kRows] : w;
+          w_s[ot] = kE4m3 ? w * (1.f / kTermTop) : w;
         }
         moved = any_in_group(bar, moved);
         wait_warp(&B->o_full[ob], (i / C::kOBuf) & 1, abort);

@@ -541,7 +541,12 @@ gdn_status gdn_qk_norm_rope(const uint16_t *q, int64_t q_stride_t, int64_t q_str
  *   out = sum_t p_t v_t,  p = softmax over the seen t of scale * (q . k_t)
  * and with a gate out <- out (.) sigmoid(gate) before its one rounding. A node
  * that sees nothing gets zeros. A node that is not seen contributes nothing,
- * whatever its values. Softmax statistics and sums are fp32.
+ * whatever its values and scales. Softmax statistics and sums are fp32. For the
+ * products on the tensor cores each weight is held in fewer bits: with a bf16
+ * cache in bf16 (2^-8 of itself); with an E4M3 cache as two E4M3 terms, together
+ * with the value's scale (2^-8 + 2^-11 of itself, or 2^-17 of the largest that the
+ * row has within 128 tokens), and q as two E4M3 terms (2^-17 of the head row's
+ * largest value).
  *
  *   q         [N*P][Hq][D] bf16, request-major (row n*P + j); query head h reads
  *             kv head h / (Hq / Hkv)
