@@ -106,19 +106,39 @@ __device__ __forceinline__ void bulk_g2s_nohint(void* smem_dst, const void* gsrc
       : "memory");
 }
 
-// A tree's parents come before their children; -1 is the live slot.
-__device__ __forceinline__ bool unit_parents_ok(const StepArgs& p, int n) {
-  for (int q = 0; q < p.P; ++q) {
-    const int f = p.parent[n * p.P + q];
-    if (f < -1 || f >= q) return false;
+// What is wrong with a request's tree, 0 for nothing: slots out of the pool; parents that do not come before their
+// children (-1 is the live slot); a node whose state is loaded again, for a child that does not follow at once, when
+// another node between the two has its slot. All of the request's words are loaded before the first is looked at: one
+// after the other, the trips to L1 cost a unit of 8 nodes 1 us.
+__device__ __forceinline__ int tree_fault(const StepArgs& p, int n) {
+  const int live = p.slot_idx[n];
+  int slot[kMaxPos], parent[kMaxPos];
+#pragma unroll
+  for (int q = 0; q < kMaxPos; ++q) {
+    slot[q] = q < p.P ? p.spec_slot[n * p.P + q] : 0;
+    parent[q] = q < p.P ? p.parent[n * p.P + q] : -1;
   }
-  return true;
+  bool slots_ok = live >= 0 && live < p.Rs, parents_ok = true;
+  uint64_t same = 0;  // byte f, bit r: the later node r has node f's slot
+#pragma unroll
+  for (int q = 0; q < kMaxPos; ++q) {
+    slots_ok = slots_ok && slot[q] >= 0 && slot[q] < p.Rs;
+    parents_ok = parents_ok && parent[q] >= -1 && parent[q] < q;
+#pragma unroll
+    for (int r = q + 1; r < kMaxPos; ++r) same |= slot[r] == slot[q] ? 1ull << (8 * q + r) : 0ull;
+  }
+  bool kept = true;
+#pragma unroll
+  for (int q = 2; q < kMaxPos; ++q)
+    kept = kept && (parent[q] < 0 || ((uint32_t)(same >> (8 * (parent[q] & 7))) & ((1u << q) - 1)) == 0);
+  return !slots_ok ? GDN_DEVERR_SLOT : !parents_ok ? GDN_DEVERR_TREE : !kept ? GDN_DEVERR_SLOT : 0;
 }
 
 // Slot that receives the state after position p: the live slot (decode) or the
 // position's checkpoint slot (speculative verify). -1 when out of range.
 template <bool kTree>
 __device__ __forceinline__ bool unit_slots_ok(const StepArgs& p, int n) {
+  if constexpr (kTree) return tree_fault(p, n) == 0;
   const int slot = p.slot_idx[n];
   if (slot < 0 || slot >= p.Rs) return false;
   if (p.spec_slot)
@@ -126,7 +146,6 @@ __device__ __forceinline__ bool unit_slots_ok(const StepArgs& p, int n) {
       const int s = p.spec_slot[n * p.P + q];
       if (s < 0 || s >= p.Rs) return false;
     }
-  if constexpr (kTree) return unit_parents_ok(p, n);
   return true;
 }
 
@@ -327,9 +346,9 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const StepArgs p, c
     }
     if (skip) {  // a bad or padding slot: the producer handed over nothing
       if (ctid == 0 && slot >= 0) {
-        bool tree = false;  // the slots are fine, the parents are not
-        if constexpr (kTree) tree = unit_slots_ok<false>(p, n);
-        report(p.dev_err, tree ? GDN_DEVERR_TREE : GDN_DEVERR_SLOT);
+        int fault = GDN_DEVERR_SLOT;
+        if constexpr (kTree) fault = tree_fault(p, n);
+        report(p.dev_err, fault);
       }
       consumer_sync();
       if (ctid == 0) mbar_arrive(&in_empty[b]);
@@ -753,8 +772,8 @@ __global__ void __launch_bounds__(1024) split_tree_kernel(const StepArgs p, cons
   // the same for every CTA of the cluster: all of them leave here, or none
   const int slot = p.slot_idx[n];
   if (slot < 0) return;  // padding
-  if (!unit_slots_ok<true>(p, n)) {
-    if (part == 0 && tid == 0) report(p.dev_err, unit_slots_ok<false>(p, n) ? GDN_DEVERR_TREE : GDN_DEVERR_SLOT);
+  if (const int fault = tree_fault(p, n)) {
+    if (part == 0 && tid == 0) report(p.dev_err, fault);
     return;
   }
   const uint64_t wpol = l2_policy_evict_first();

@@ -429,6 +429,9 @@ gdn_status gdn_out_proj(const uint16_t *ogate, const uint16_t *w, const uint16_t
  *   arguments as gdn_spec_verify, plus
  *   parent  [N][P] int32, -1 <= parent[n][p] < p (parents before children).
  *           Anything else sets GDN_DEVERR_TREE and the request writes nothing.
+ *   spec_slot_idx: nodes of a request may share a slot (the last one's state
+ *           stays), but a node whose parent's slot another node has taken in
+ *           between sets GDN_DEVERR_SLOT and the request writes nothing.
  */
 gdn_status gdn_spec_verify_tree(const gdn_dims *dims, const uint16_t *qkv0, const float *conv_w,
                                 uint16_t *conv_hist, float *state, const int32_t *slot_idx,
