@@ -155,7 +155,8 @@ def _rows(t, name: str, shape):
     st, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name}'s head rows must be contiguous")
-    return t.data_ptr(), st, sh
+    # of a dimension with one entry a tensor may name any stride
+    return t.data_ptr(), st if shape[0] > 1 else 0, sh if shape[1] > 1 else 0
 
 
 _NO_ROWS = (None, 0, 0)

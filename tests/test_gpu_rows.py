@@ -51,3 +51,25 @@ def test_many_tokens_a_block_give_the_bits_of_few(b, fmt, hq, hkv, d, rotary, in
         runs.append([qo, ko] + [x for p in pools for x in (p.k, p.v, p.k_scale, p.v_scale) if x is not None])
     for x, y in zip(*runs):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+@pytest.mark.parametrize("T,heads", [(5, 1), (1, 3), (1, 1)])
+def test_strides_of_dimensions_with_one_entry_do_not_count(b, T, heads):
+    """One head or one token: whatever stride the tensor names for it, here one element, the rows are the same."""
+    d = 128
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(T, heads, d, generator=g, device="cuda").to(torch.bfloat16)
+    odd = x.as_strided(x.shape, (d * heads if T > 1 else 1, d if heads > 1 else 1, 1))
+    assert torch.equal(odd, x)
+    slots = torch.arange(T, device="cuda", dtype=torch.int32)
+    pos, f = slots.clone(), torch.ones(8, dtype=torch.float64, device="cuda")
+    gamma = torch.ones(d, device="cuda")
+    runs = []
+    for t in (x, odd):
+        pools = [R.Pool(1, heads, 16, d, "e4m3") for _ in range(2)]
+        out = torch.empty_like(x)
+        b.gdn_kv_cache_write(pools[0].handle(b), t, t, slots)
+        b.gdn_qk_norm_rope(t, t, gamma, gamma, 1e-6, pos, f, out, v=t, cache=pools[1].handle(b), kv_slot=slots)
+        runs.append([out] + [y for p in pools for y in (p.k, p.v, p.k_scale, p.v_scale)])
+    for a, c in zip(*runs):
+        assert torch.equal(a.view(torch.uint8), c.view(torch.uint8))
