@@ -139,11 +139,16 @@ struct Cfg {
   static constexpr int kAhead = kSplit ? 1 : 2;
   // query buffers: a tile's scores wait for no output that follows them, though every segment have one tile
   static constexpr int kQBuf = kAhead + 1;
-  // A unit's fixed work (its query rows, its result, the ends of its pipeline) in tiles, for the cut of the line. It
-  // takes as long as so many. 32 trees of 48 rows on 129..16384 tokens, bf16, with 0 / 2 / 4 / 5 / 6: 174 / 126 / 113 /
-  // 109 / 115 us, E4M3 with 0 / 5 / 9: 199 / 121 / 106 us; 128 single tokens on 129..8192, bf16 with 0 / 2 / 5 / 7:
-  // 168 / 161 / 166 / 169 us; 256 on 1k..8k, E4M3 with 0 / 4 / 6: 297 / 286 / 295 us (all before later steps); heads of
-  // 128 have smaller tiles: 128 single tokens on 129..8192, E4M3 with 3 / 4 / 5 / 6: 140 / 144 / 138 / 131 us.
+  // A unit's fixed work (its query rows, its result, the ends of its pipeline) in tiles, for the cut of the line. It takes
+  // as long as so many. Measured with 0 / 2 / 4 / 5 / 7 / 9 / 12:
+  //   32 trees of 48 rows on 129..16384 tokens, E4M3       185 / 144 / 129 / 116 / 104 / 108 / 110 us
+  //   the same with 32 query and 8 kv heads of 128         200 / 149 / 125 / 122 / 106 /  99 /  92
+  //   the same of 30 rows, heads of 256                    119 /  94 /  87 /  86 /  86 /  89 /  94
+  //   32 trees of 48 rows on 129..16384 tokens, bf16       164 / 124 / 111 / 110 / 111 / 115 / 122
+  //   the same of 30 rows                                  112 /  94 /  95 /  98 / 102 / 106 / 111
+  //   128 single tokens on 129..8192, bf16                 171 / 161 / 164 / 166 / 169 / 172 / 180
+  //   256 single tokens on 1k..8k, E4M3                    284 / 282 / 288 / 290 / 297 / 298 / 306
+  //   128 on 129..8192, E4M3, 32 / 8 heads of 128          167 / 129 / 128 / 131 / 140 / 143 / 155 (6: 134)
   static constexpr int kSegCost = kRows > 16 ? (kE4m3 ? 9 : 5) : !kE4m3 ? 2 : D == 256 ? 4 : 6;
   // The launch may begin before the kernel in front of it ends: one request of 509 tokens 11.9 -> 10.9 us, and 14.1 -> 11.1
   // us call after call. Not for more rows: 64 on 131071 tokens in E4M3 306 -> 319 us, 64 x 24 rows 85 -> 88 us.
@@ -185,6 +190,15 @@ struct Cfg {
   }
   static_assert(stages(kRows) >= kBlk + 2, "a tile's whole V stays until its weights are there");
   static_assert(2 * kCols + kOBuf * kHalves * kOCols <= 512, "tensor memory");
+  // Columns of the MMAs: an MMA of 128 lanes takes them by sixteens, up to 256.
+  static __host__ __device__ constexpr int mma_cols(int rows) {
+    return kSumTerms ? (row_pad(rows) + 15) / 16 * 16 : kTerms * row_pad(rows);
+  }
+  static constexpr bool cols_ok() {
+    for (int rows = 1; rows <= kRows; ++rows)
+      if (mma_cols(rows) % 16 != 0 || mma_cols(rows) < rows || mma_cols(rows) > kCols || kCols > 256) return false;
+    return true;
+  }
 };
 
 // One CTA's piece of the line. `t`: where it begins in the unit, whose first kSegCost places hold no tile.
@@ -749,8 +763,8 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
     // 73 cycles to issue on an idle SM, and about 200 next to the other warps; its work is 41 at 16 columns.
     const int rp = C::row_pad(a.rows);  // rows as columns of the MMAs
     const int q_block = C::q_block(a.rows), q_bytes = C::q_bytes(a.rows);
-    // (an MMA of 128 lanes takes columns by sixteens)
-    const int N = C::kSumTerms ? (rp + 15) / 16 * 16 : C::kTerms * rp;
+    static_assert(C::cols_ok(), "columns of the MMAs, for every number of rows");
+    const int N = C::mma_cols(a.rows);
     constexpr uint32_t kKind = kE4m3 ? umma::kKindF8 : umma::kKindF16, kType = kE4m3 ? umma::kE4M3 : umma::kBF16;
     const uint32_t id_s = umma::idesc(kType, false, false, kTile, N), id_o = umma::idesc(kType, true, true, kTile, N);
     const uint32_t sQ = smem_u32(rest + C::oQ), sP = smem_u32(rest + C::oP);
