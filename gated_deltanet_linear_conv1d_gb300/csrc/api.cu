@@ -497,7 +497,7 @@ gdn_status gdn_qk_norm_rope(const uint16_t* q, int64_t q_stride_t, int64_t q_str
   }
   if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0) return GDN_ERR_INVALID_ARG;
   if (head_dim != 128 && head_dim != 256) return GDN_ERR_UNSUPPORTED;
-  // the rows of the eight tokens that a block takes are counted in 32 bits
+  // the rows of the tokens that a block takes, up to sixteen, are counted in 32 bits
   if (num_q_heads > 65535 || num_kv_heads > 65535) return GDN_ERR_UNSUPPORTED;
   if (rotary_dim < 0 || rotary_dim > head_dim) return GDN_ERR_INVALID_ARG;
   if (rotary_dim % 16 != 0) return GDN_ERR_INVALID_ARG;

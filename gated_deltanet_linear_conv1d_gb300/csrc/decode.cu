@@ -160,8 +160,8 @@ __device__ int g_unit_counter[kSchedSlots * 2];
 // or from the parent's checkpoint, which the same thread has written (one node
 // ahead: a trip to L2 next to the stream takes as long as a node). Bound by HBM:
 // 64 requests of 8 nodes at 16/48 heads, random trees, 1.87 GB: 377 us, 73 % of
-// the copy bandwidth (the same kernel on chains 344 us, gdn_spec_verify's on
-// chains 324 us; with a parent loaded only when its node begins 386 us).
+// the copy bandwidth (the same kernel on chains 354 us, on stars 359, gdn_spec_verify's
+// on chains 340; with a parent loaded only when its node begins 9 us more).
 template <bool kOne, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const StepArgs p, const int units, const int sched) {
   extern __shared__ __align__(1024) unsigned char smem[];

@@ -305,8 +305,10 @@ __device__ __forceinline__ void rows_pass(const RopeArgs& p, const KvArgs& c, co
 // blockIdx.y 0: the key and value rows of the block's tokens, 1: their query rows.
 // kNorm: the head norm, the rotation and the dense outputs; without it the rows go to the cache as they are.
 // The angles: a thread per (token, frequency) puts their cosine and sine into shared memory first. A position times a
-// frequency is taken in turns, in 64-bit fixed point (one turn = 2^64), where the whole turns fall away by themselves:
-// the error is the frequency's rounding to 2^-64 turns times the position, 2^-33 turns at the largest one.
+// frequency is taken in turns, in 64-bit fixed point (one turn = 2^64), where the whole turns fall away by themselves.
+// The frequency in turns is an fp64 product with 1 / (2 pi), off by up to 2^-52 of itself, and so is the angle: 2^-24
+// turns at the largest position and a radian a position, about what the fp64 product of the two is off by. The fixed
+// point adds 2^-65 turns a position, the cut to the upper 32 bits up to 2^-32.
 // What bounds it: HBM at many tokens, the launch and the angles' chain at few. A batch is copied to shared memory while
 // the one before it is worked on: loads into registers left none in flight meanwhile, and a second batch of registers
 // spills at three blocks an SM. 16,384 tokens of 24 + 4 heads of 256, the keys dense and into a bf16 cache, 571 MB: 95

@@ -60,15 +60,18 @@
 // GDN_DEVERR_TIMEOUT and the CTA leaves.
 //
 // What bounds it, with 24 query and 4 kv heads of 256:
-//   one token per request: HBM. 256 requests of 1k..8k tokens, E4M3: 281 us, 6.5
+//   one token per request: HBM. 256 requests of 1k..8k tokens, E4M3: 284 us, 6.5
 //   TB/s. One request of 509 tokens: 11 us, the launches and one tile's chain.
-//   48 rows (trees of 8 nodes), bf16, 32 requests of 129..16384 tokens: 104 us,
-//   4.3 TB/s. The copies wait for room: a tile is 128 KB, the ring 128 KB (96 KB for
+//   Heads of 128, 32 over 8: 128 requests of 129..8192 tokens, E4M3: 134 us, 3.9
+//   TB/s, a unit's fixed work, about six of its small tiles' time, 1024 units.
+//   48 rows (trees of 8 nodes), bf16, 32 requests of 129..16384 tokens: 103 us,
+//   4.4 TB/s. The copies wait for room: a tile is 128 KB, the ring 128 KB (96 KB for
 //   64 rows: 109 us), and V stays in it until its weights are there; a unit costs
-//   about five tiles' time.
-//   64 rows, E4M3, 131071 tokens: 306 us, the softmax: 8 warps at 0.60 instructions
+//   about five tiles' time. E4M3: 107 us, 2.2 TB/s, a unit about nine tiles' time.
+//   64 rows, 131071 tokens, E4M3: 300 us, the softmax: 8 warps at 0.62 instructions
 //   a cycle and scheduler in chains of exchanges, conversions and barriers, 3.6 k
-//   cycles a tile, of which the MMAs need 1.1 k.
+//   cycles a tile, of which the MMAs need 1.1 k. bf16: 421 us, the ring as above, the
+//   six row tiles each reading the cache.
 #pragma once
 
 #include "device.cuh"
@@ -94,8 +97,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // As E4M3 terms, before v_t / 2^e_t in [1, 2), that weight is kTermTop: 448 is the largest.
 constexpr int kTopExp = 64;
 constexpr float kTermTop = 224.f;
-// Exponents of the value scales: none below this. A write leaves -49 at least; of smaller scales a row that sees no other
-// holds its weights to 2^-17 of 2^-50.
+// Exponents of the value scales: none below this. A write leaves -49 at least; a smaller scale, or none, counts as 2^-50
+// here, and beside a weight with such a value a row's others are held to 2^-17 of 2^-50 times that weight.
 constexpr int kMinScaleExp = -50;
 
 struct Args {

@@ -512,7 +512,8 @@ gdn_status gdn_kv_cache_read(const gdn_kv_cache *cache, const int32_t *block_tab
  * normalised. The pair of frequency i is (i, i + rotary_dim / 2), or with
  * interleaved != 0 (2i, 2i + 1): (a, b) -> (a cos - b sin, b cos + a sin), angle
  * position * inv_freq[i]. The angle is taken modulo a turn in 64-bit fixed
- * point, so its error does not grow with the position.
+ * point: it is off by up to 2^-52 of itself, about as a 64-bit floating-point product
+ * would be, and 2^-32 turns.
  *
  *   q, k       bf16 with strides as in gdn_kv_cache_write; q may be NULL (then
  *              q_out too): only the keys, e.g. to write accepted drafts again at
@@ -561,7 +562,9 @@ gdn_status gdn_qk_norm_rope(const uint16_t *q, int64_t q_stride_t, int64_t q_str
  *             j sees nodes 0 .. j
  *   gate      [N*P][Hq][D] bf16 or NULL
  *   out       [N*P][Hq][D] bf16; may be q or gate itself
- *   num_pos   1 <= P <= 64;  Hq / Hkv <= 64;  scale finite
+ *   num_pos   1 <= P <= 64;  Hq / Hkv <= 64;  num_seqs, Hq <= 65535;  scale finite.
+ *             (gdn_spec_verify_tree takes up to 8 nodes, so a tree that runs
+ *             through both kinds of layer has 8 at most.)
  *   workspace partial sums of requests that several CTAs share:
  *             gdn_tree_attention_workspace_bytes(...) bytes, 256-byte aligned.
  *             Contents need not be zeroed and are clobbered. Calls sharing one
