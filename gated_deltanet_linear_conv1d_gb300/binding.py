@@ -49,6 +49,28 @@ class GdnKvCache(ctypes.Structure):
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("format", ctypes.c_int32)]
 
 
+class GdnRopeAxes(ctypes.Structure):
+    """gdn_rope_axes: the position axis of each rotation frequency (make_rope_axes fills it)."""
+    _fields_ = [("num_axes", ctypes.c_int32), ("axis", ctypes.c_uint8 * 128)]
+
+
+def make_rope_axes(sections, mixed: bool = False) -> GdnRopeAxes:
+    """The axes of sum(sections) = rotary_dim / 2 frequencies, sections[a] of them axis a's: a run per axis in their
+    order, or, mixed, in turns: frequency i is axis i % len(sections)'s while that axis has some left by this rule, else
+    axis 0's."""
+    sections = [int(n) for n in sections]
+    axes, total = len(sections), sum(sections)
+    if not 1 <= axes <= 4 or min(sections) < 0 or total > 128:
+        raise ValueError("sections must be 1 to 4 counts, at most 128 frequencies in all")
+    if mixed:
+        axis = [i % axes if i < axes * sections[i % axes] else 0 for i in range(total)]
+        if [axis.count(a) for a in range(axes)] != sections:
+            raise ValueError("sections cannot take turns: axis 0 must have the most frequencies, or as many")
+    else:
+        axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    return GdnRopeAxes(axes, (ctypes.c_uint8 * 128)(*axis))
+
+
 def make_dims(geom, num_slots: int) -> GdnDims:
     """gdn_dims from any object with num_k_heads, num_v_heads, head_k_dim, head_v_dim, conv_kernel."""
     return GdnDims(geom.num_k_heads, geom.num_v_heads, geom.head_k_dim, geom.head_v_dim,
@@ -64,6 +86,7 @@ def _load() -> ctypes.CDLL:
     i32, i64, f32, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
     D = ctypes.POINTER(GdnDims)
     C = ctypes.POINTER(GdnKvCache)
+    A = ctypes.POINTER(GdnRopeAxes)
     sigs = {
         "gdn_conv_update": [D, P, P, P, P, P, P, i32, i32, P, P, P],
         "gdn_decode_step": [D, P, P, P, P, P, P, P, P, P, f32, P, P, i32, P, P],
@@ -77,7 +100,12 @@ def _load() -> ctypes.CDLL:
         "gdn_kv_cache_read": [C, P, i32, P, i32, i32, P, P, P, P],
         "gdn_qk_norm_rope": [P, i64, i64, P, i64, i64, P, P, f32, P, P, i32, i32, P, P, P, i64, i64, C, P, i32, i32,
                              i32, i32, P, P],
+        "gdn_qk_norm_mrope": [P, i64, i64, P, i64, i64, P, P, f32, P, P, i32, A, i32, P, P, P, i64, i64, C, P, i32, i32,
+                              i32, i32, P, P],
         "gdn_tree_attention": [C, P, P, i32, P, P, P, f32, P, i32, i32, i32, P, sz, P, P],
+        "gdn_tree_attention_lse": [C, P, P, i32, P, P, P, f32, P, P, i32, i32, i32, P, sz, P, P],
+        "gdn_kv_score": [C, P, P, P, i32, P, P, f32, f32, P, P, P, i32, i32, i32, i32, i32, P, P],
+        "gdn_kv_evict": [C, P, i32, P, P, i32, i32, P, i32, P, P, P, i32, i32, P, i32, P, i32, P, P],
         "gdn_spec_commit": [D, P, P, P, P, P, i32, i32, i32, P, P],
         "gdn_gated_rmsnorm": [P, P, P, f32, P, i32, i32, i32, P],
         "gdn_out_proj": [P, P, P, P, i32, i32, i32, P, P],
@@ -524,6 +552,25 @@ def gdn_qk_norm_rope(q, k, q_gamma, k_gamma, eps, positions, inv_freq, q_out, k_
                                  _arg(dev_err, "dev_err", _i32, (1,), True), _stream(stream)), "gdn_qk_norm_rope")
 
 
+def gdn_qk_norm_mrope(q, k, q_gamma, k_gamma, eps, positions, inv_freq, axes, q_out, k_out=None, v=None, cache=None,
+                      kv_slot=None, interleaved: bool = False, dev_err=None, stream=None):
+    """gdn_qk_norm_rope with a position per axis: positions [num_axes, T], axes from make_rope_axes."""
+    T, Hkv, D = kv = k.shape
+    Hq = Hkv if q is None else q.shape[1]
+    qs = (T, Hq, D)
+    rotary = 2 * inv_freq.numel()
+    _check(_lib.gdn_qk_norm_mrope(*(_NO_ROWS if q is None else _rows(q, "q", qs)), *_rows(k, "k", kv),
+                                  _arg(q_gamma, "q_gamma", _f32, (D,), q is None), _arg(k_gamma, "k_gamma", _f32, (D,)),
+                                  float(eps), _arg(positions, "positions", _i32, (axes.num_axes, T)),
+                                  _arg(inv_freq, "inv_freq", _f64, (rotary // 2,)), rotary, _byref(axes),
+                                  1 if interleaved else 0, _arg(q_out, "q_out", _bf16, qs, q is None),
+                                  _arg(k_out, "k_out", _bf16, kv, cache is not None),
+                                  *(_NO_ROWS if v is None else _rows(v, "v", kv)),
+                                  None if cache is None else _byref(cache),
+                                  _arg(kv_slot, "kv_slot", _i32, (T,), cache is None), T, Hq, Hkv, D,
+                                  _arg(dev_err, "dev_err", _i32, (1,), True), _stream(stream)), "gdn_qk_norm_mrope")
+
+
 def gdn_tree_attention_workspace_bytes(cache, num_seqs: int, num_pos: int, num_q_heads: int) -> int:
     return int(_lib.gdn_tree_attention_workspace_bytes(_byref(cache), int(num_seqs), int(num_pos), int(num_q_heads)))
 
@@ -544,6 +591,70 @@ def gdn_tree_attention(cache, q, block_table, ctx_len, scale, out, num_pos: int 
                                    N, int(num_pos), shape[1], _arg(workspace, "workspace", workspace.dtype),
                                    workspace.nbytes,
                                    _arg(dev_err, "dev_err", _i32, (1,), True), _stream(stream)), "gdn_tree_attention")
+
+
+def gdn_tree_attention_lse(cache, q, block_table, ctx_len, scale, out, lse, num_pos: int = 1, tree_mask=None, gate=None,
+                           workspace=None, dev_err=None, stream=None):
+    """gdn_tree_attention that also leaves each row's log-sum-exp in lse [N * num_pos, Hq] fp32."""
+    N, max_pages = block_table.shape
+    shape = (N * num_pos, q.shape[1], cache.head_dim)
+    if workspace is None:
+        need = gdn_tree_attention_workspace_bytes(cache, N, num_pos, shape[1])
+        workspace = _scratch(need, q.device, stream)
+    _check(_lib.gdn_tree_attention_lse(_byref(cache), _arg(q, "q", _bf16, shape),
+                                       _arg(block_table, "block_table", _i32), max_pages,
+                                       _arg(ctx_len, "ctx_len", _i32, (N,)),
+                                       _arg(tree_mask, "tree_mask", _i64, (N, num_pos), True),
+                                       _arg(gate, "gate", _bf16, shape, True), float(scale),
+                                       _arg(out, "out", _bf16, shape), _arg(lse, "lse", _f32, shape[:2]), N, int(num_pos),
+                                       shape[1], _arg(workspace, "workspace", workspace.dtype), workspace.nbytes,
+                                       _arg(dev_err, "dev_err", _i32, (1,), True), _stream(stream)),
+           "gdn_tree_attention_lse")
+
+
+def _flags(t, name: str, shape):
+    """The address of optional uint8 or bool flags."""
+    if t is None:
+        return None
+    _need(t, name, (torch.uint8, torch.bool), shape)
+    return t.data_ptr()
+
+
+def gdn_kv_score(cache, q, lse, block_table, ctx_len, scale, score, slot_idx, num_pos: int = 1, tree_mask=None,
+                 decay: float = 1.0, has_init=None, dev_err=None, stream=None):
+    """score [num_slots, Hkv, max_tokens] fp32 <- decay * score + the attention weight that each cached token receives
+    from rows q [N * num_pos, Hq, D] with log-sum-exps lse [N * num_pos, Hq], for requests in slots slot_idx [N]."""
+    N, max_pages = block_table.shape
+    shape = (N * num_pos, q.shape[1], cache.head_dim)
+    slots, heads, room = score.shape
+    _check(_lib.gdn_kv_score(_byref(cache), _arg(q, "q", _bf16, shape), _arg(lse, "lse", _f32, shape[:2]),
+                             _arg(block_table, "block_table", _i32), max_pages, _arg(ctx_len, "ctx_len", _i32, (N,)),
+                             _arg(tree_mask, "tree_mask", _i64, (N, num_pos), True), float(scale), float(decay),
+                             _arg(score, "score", _f32, (slots, cache.num_kv_heads, room)),
+                             _arg(slot_idx, "slot_idx", _i32, (N,)), _flags(has_init, "has_init", (N,)), slots, room, N,
+                             int(num_pos), shape[1], _arg(dev_err, "dev_err", _i32, (1,), True), _stream(stream)),
+           "gdn_kv_score")
+
+
+def gdn_kv_evict(cache, block_table, length, budget, score, slot_idx, kept, new_len, sink_tokens: int = 0,
+                 recent_tokens: int = 0, dst_table=None, dst_slot=None, dev_err=None, stream=None):
+    """Requests of length [N] tokens cut down to budget [N], by score [num_slots, Hkv, max_tokens]: in place, or into the
+    pages of dst_table. kept [N, Hkv, max_kept]: the kept tokens' old indices; new_len [N]."""
+    N, max_pages = block_table.shape
+    slots, heads, room = score.shape
+    most = kept.shape[-1]
+    if new_len is length:
+        raise ValueError("new_len must not be length itself")
+    _check(_lib.gdn_kv_evict(_byref(cache), _arg(block_table, "block_table", _i32), max_pages,
+                             _arg(length, "length", _i32, (N,)), _arg(budget, "budget", _i32, (N,)), int(sink_tokens),
+                             int(recent_tokens),
+                             None if dst_table is None else _arg(dst_table, "dst_table", _i32, (N, dst_table.shape[-1])),
+                             0 if dst_table is None else dst_table.shape[-1],
+                             _arg(score, "score", _f32, (slots, cache.num_kv_heads, room)),
+                             _arg(slot_idx, "slot_idx", _i32, (N,)), _arg(dst_slot, "dst_slot", _i32, (N,), True), slots,
+                             room, _arg(kept, "kept", _i32, (N, cache.num_kv_heads, most)), most,
+                             _arg(new_len, "new_len", _i32, (N,)), N, _arg(dev_err, "dev_err", _i32, (1,), True),
+                             _stream(stream)), "gdn_kv_evict")
 
 
 def gdn_spec_commit(dims, accepted, spec_slot_idx, slot_idx, state=None, conv_hist=None,

@@ -482,13 +482,15 @@ gdn_status gdn_kv_cache_read(const gdn_kv_cache* cache, const int32_t* block_tab
   return from_cuda(launch_kv_read(a, c, cache->head_dim, static_cast<cudaStream_t>(stream)));
 }
 
-gdn_status gdn_qk_norm_rope(const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h, const uint16_t* k,
-                            int64_t k_stride_t, int64_t k_stride_h, const float* q_gamma, const float* k_gamma,
-                            float eps, const int32_t* positions, const double* inv_freq, int32_t rotary_dim,
-                            int32_t interleaved, uint16_t* q_out, uint16_t* k_out, const uint16_t* v,
-                            int64_t v_stride_t, int64_t v_stride_h, const gdn_kv_cache* cache,
-                            const int32_t* kv_slot, int32_t num_tokens, int32_t num_q_heads,
-                            int32_t num_kv_heads, int32_t head_dim, int32_t* dev_err, void* stream) {
+namespace {
+
+// The head norms and the rotation, by one position a token (axes NULL) or one per axis.
+gdn_status norm_rope(const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h, const uint16_t* k, int64_t k_stride_t,
+                     int64_t k_stride_h, const float* q_gamma, const float* k_gamma, float eps, const int32_t* positions,
+                     const double* inv_freq, int32_t rotary_dim, const gdn_rope_axes* axes, int32_t interleaved,
+                     uint16_t* q_out, uint16_t* k_out, const uint16_t* v, int64_t v_stride_t, int64_t v_stride_h,
+                     const gdn_kv_cache* cache, const int32_t* kv_slot, int32_t num_tokens, int32_t num_q_heads,
+                     int32_t num_kv_heads, int32_t head_dim, int32_t* dev_err, void* stream) {
   KvArgs c{};
   if (cache) {
     gdn_status st = check_cache(cache, &c);
@@ -503,6 +505,11 @@ gdn_status gdn_qk_norm_rope(const uint16_t* q, int64_t q_stride_t, int64_t q_str
   if (rotary_dim % 16 != 0) return GDN_ERR_INVALID_ARG;
   if ((rotary_dim & (rotary_dim - 1)) != 0) return GDN_ERR_UNSUPPORTED;
   if (!eps_ok(eps)) return GDN_ERR_INVALID_ARG;
+  if (axes) {
+    if (axes->num_axes < 1 || axes->num_axes > 4) return GDN_ERR_INVALID_ARG;
+    for (int i = 0; i < rotary_dim / 2; ++i)
+      if (axes->axis[i] >= axes->num_axes) return GDN_ERR_INVALID_ARG;
+  }
   if (num_tokens == 0) return GDN_OK;
   if (!q != !q_out || (!cache && !k_out) || !cache != !v || !cache != !kv_slot) return GDN_ERR_INVALID_ARG;
   if (!rows_ok(k, k_stride_t, k_stride_h) || (q && !rows_ok(q, q_stride_t, q_stride_h)) ||
@@ -513,8 +520,36 @@ gdn_status gdn_qk_norm_rope(const uint16_t* q, int64_t q_stride_t, int64_t q_str
   if (!aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(inv_freq, 8)) return GDN_ERR_INVALID_ARG;
   c.Hkv = num_kv_heads;
   RopeArgs a{q, k, v, q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h, q_gamma, k_gamma, eps,
-             positions, inv_freq, rotary_dim, interleaved != 0, q_out, k_out, kv_slot, num_tokens, num_q_heads, dev_err};
+             positions, inv_freq, rotary_dim, interleaved != 0, q_out, k_out, kv_slot, num_tokens, num_q_heads, dev_err,
+             axes ? *axes : gdn_rope_axes{}};
   return from_cuda(launch_rows(a, c, true, head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+gdn_status gdn_qk_norm_rope(const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h, const uint16_t* k,
+                            int64_t k_stride_t, int64_t k_stride_h, const float* q_gamma, const float* k_gamma,
+                            float eps, const int32_t* positions, const double* inv_freq, int32_t rotary_dim,
+                            int32_t interleaved, uint16_t* q_out, uint16_t* k_out, const uint16_t* v,
+                            int64_t v_stride_t, int64_t v_stride_h, const gdn_kv_cache* cache,
+                            const int32_t* kv_slot, int32_t num_tokens, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t* dev_err, void* stream) {
+  return norm_rope(q, q_stride_t, q_stride_h, k, k_stride_t, k_stride_h, q_gamma, k_gamma, eps, positions, inv_freq,
+                   rotary_dim, nullptr, interleaved, q_out, k_out, v, v_stride_t, v_stride_h, cache, kv_slot, num_tokens,
+                   num_q_heads, num_kv_heads, head_dim, dev_err, stream);
+}
+
+gdn_status gdn_qk_norm_mrope(const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h, const uint16_t* k,
+                             int64_t k_stride_t, int64_t k_stride_h, const float* q_gamma, const float* k_gamma,
+                             float eps, const int32_t* positions, const double* inv_freq, int32_t rotary_dim,
+                             const gdn_rope_axes* axes, int32_t interleaved, uint16_t* q_out, uint16_t* k_out,
+                             const uint16_t* v, int64_t v_stride_t, int64_t v_stride_h, const gdn_kv_cache* cache,
+                             const int32_t* kv_slot, int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                             int32_t head_dim, int32_t* dev_err, void* stream) {
+  if (!axes) return GDN_ERR_INVALID_ARG;
+  return norm_rope(q, q_stride_t, q_stride_h, k, k_stride_t, k_stride_h, q_gamma, k_gamma, eps, positions, inv_freq,
+                   rotary_dim, axes, interleaved, q_out, k_out, v, v_stride_t, v_stride_h, cache, kv_slot, num_tokens,
+                   num_q_heads, num_kv_heads, head_dim, dev_err, stream);
 }
 
 namespace {
@@ -535,11 +570,12 @@ size_t gdn_tree_attention_workspace_bytes(const gdn_kv_cache* cache, int32_t num
   return tree_attn_workspace_bytes(num_pos, num_q_heads / c.Hkv, cache->head_dim);
 }
 
-gdn_status gdn_tree_attention(const gdn_kv_cache* cache, const uint16_t* q, const int32_t* block_table,
-                              int32_t max_pages, const int32_t* ctx_len, const uint64_t* tree_mask,
-                              const uint16_t* gate, float scale, uint16_t* out, int32_t num_seqs, int32_t num_pos,
-                              int32_t num_q_heads, void* workspace, size_t workspace_bytes, int32_t* dev_err,
-                              void* stream) {
+namespace {
+
+gdn_status tree_attention(const gdn_kv_cache* cache, const uint16_t* q, const int32_t* block_table, int32_t max_pages,
+                          const int32_t* ctx_len, const uint64_t* tree_mask, const uint16_t* gate, float scale,
+                          uint16_t* out, float* lse, int32_t num_seqs, int32_t num_pos, int32_t num_q_heads,
+                          void* workspace, size_t workspace_bytes, int32_t* dev_err, void* stream) {
   KvArgs c{};
   gdn_status st = check_cache(cache, &c);
   if (st != GDN_OK) return st;
@@ -552,8 +588,83 @@ gdn_status gdn_tree_attention(const gdn_kv_cache* cache, const uint16_t* q, cons
   const size_t need = tree_attn_workspace_bytes(num_pos, num_q_heads / c.Hkv, cache->head_dim);
   if (workspace_bytes < need || (need > 0 && (!workspace || !aligned(workspace, 256)))) return GDN_ERR_INVALID_ARG;
   TreeAttnArgs a{q, block_table, ctx_len, tree_mask, gate, out, scale, num_seqs, num_pos, num_q_heads,
-                 num_q_heads / c.Hkv, cache->head_dim, max_pages, workspace, dev_err};
+                 num_q_heads / c.Hkv, cache->head_dim, max_pages, workspace, dev_err, lse};
   return from_cuda(launch_tree_attn(a, c, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+gdn_status gdn_tree_attention(const gdn_kv_cache* cache, const uint16_t* q, const int32_t* block_table,
+                              int32_t max_pages, const int32_t* ctx_len, const uint64_t* tree_mask,
+                              const uint16_t* gate, float scale, uint16_t* out, int32_t num_seqs, int32_t num_pos,
+                              int32_t num_q_heads, void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                              void* stream) {
+  return tree_attention(cache, q, block_table, max_pages, ctx_len, tree_mask, gate, scale, out, nullptr, num_seqs, num_pos,
+                        num_q_heads, workspace, workspace_bytes, dev_err, stream);
+}
+
+gdn_status gdn_tree_attention_lse(const gdn_kv_cache* cache, const uint16_t* q, const int32_t* block_table,
+                                  int32_t max_pages, const int32_t* ctx_len, const uint64_t* tree_mask,
+                                  const uint16_t* gate, float scale, uint16_t* out, float* lse, int32_t num_seqs,
+                                  int32_t num_pos, int32_t num_q_heads, void* workspace, size_t workspace_bytes,
+                                  int32_t* dev_err, void* stream) {
+  if ((!lse && num_seqs != 0) || !aligned(lse, 4)) return GDN_ERR_INVALID_ARG;
+  return tree_attention(cache, q, block_table, max_pages, ctx_len, tree_mask, gate, scale, out, lse, num_seqs, num_pos,
+                        num_q_heads, workspace, workspace_bytes, dev_err, stream);
+}
+
+namespace {
+
+// The pool of scores that gdn_kv_score and gdn_kv_evict share.
+gdn_status check_score(const float* score, const int32_t* slot_idx, int32_t num_slots, int32_t max_tokens) {
+  if (num_slots <= 0 || max_tokens <= 0) return GDN_ERR_INVALID_ARG;
+  if (max_tokens > 1 << 30) return GDN_ERR_UNSUPPORTED;
+  return score && slot_idx && aligned(score, 4) ? GDN_OK : GDN_ERR_INVALID_ARG;
+}
+
+}  // namespace
+
+gdn_status gdn_kv_score(const gdn_kv_cache* cache, const uint16_t* q, const float* lse, const int32_t* block_table,
+                        int32_t max_pages, const int32_t* ctx_len, const uint64_t* tree_mask, float scale,
+                        float decay, float* score, const int32_t* slot_idx, const uint8_t* has_init,
+                        int32_t num_slots, int32_t max_tokens, int32_t num_seqs, int32_t num_pos,
+                        int32_t num_q_heads, int32_t* dev_err, void* stream) {
+  KvArgs c{};
+  gdn_status st = check_cache(cache, &c);
+  if (st != GDN_OK) return st;
+  st = check_tree_sizes(c, num_seqs, num_pos, num_q_heads);
+  if (st != GDN_OK) return st;
+  if (max_pages < 0 || !std::isfinite(scale) || !std::isfinite(decay)) return GDN_ERR_INVALID_ARG;
+  if (num_seqs == 0) return GDN_OK;
+  st = check_score(score, slot_idx, num_slots, max_tokens);
+  if (st != GDN_OK) return st;
+  if (!q || !lse || !block_table || !ctx_len || max_pages == 0) return GDN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(lse, 4) || !aligned(tree_mask, 8)) return GDN_ERR_INVALID_ARG;
+  ScoreArgs a{q, lse, block_table, ctx_len, tree_mask, scale, decay, score, slot_idx, has_init, num_slots, max_tokens,
+              num_seqs, num_pos, num_q_heads, num_q_heads / c.Hkv, cache->head_dim, max_pages, dev_err};
+  return from_cuda(launch_kv_score(a, c, static_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_kv_evict(const gdn_kv_cache* cache, const int32_t* block_table, int32_t max_pages,
+                        const int32_t* length, const int32_t* budget, int32_t sink_tokens, int32_t recent_tokens,
+                        const int32_t* dst_table, int32_t dst_max_pages, float* score, const int32_t* slot_idx,
+                        const int32_t* dst_slot, int32_t num_slots, int32_t max_tokens, int32_t* kept,
+                        int32_t max_kept, int32_t* new_len, int32_t num_seqs, int32_t* dev_err, void* stream) {
+  KvArgs c{};
+  gdn_status st = check_cache(cache, &c);
+  if (st != GDN_OK) return st;
+  if (num_seqs < 0 || max_pages < 0 || max_kept < 0 || sink_tokens < 0 || recent_tokens < 0) return GDN_ERR_INVALID_ARG;
+  if (dst_table ? dst_max_pages < 0 : dst_max_pages != 0) return GDN_ERR_INVALID_ARG;
+  if (num_seqs == 0) return GDN_OK;
+  if ((long long)num_seqs * c.Hkv > 1 << 28) return GDN_ERR_UNSUPPORTED;  // blocks are counted in 32 bits
+  st = check_score(score, slot_idx, num_slots, max_tokens);
+  if (st != GDN_OK) return st;
+  if (!block_table || max_pages == 0 || !length || !budget || !new_len || new_len == length || (!kept && max_kept > 0))
+    return GDN_ERR_INVALID_ARG;
+  EvictArgs a{block_table, dst_table ? dst_table : block_table, length, budget, score, slot_idx,
+              dst_slot ? dst_slot : slot_idx, kept, new_len, sink_tokens, recent_tokens, num_slots, max_tokens, max_pages,
+              dst_table ? dst_max_pages : max_pages, max_kept, num_seqs, cache->head_dim, dev_err};
+  return from_cuda(launch_kv_evict(a, c, static_cast<cudaStream_t>(stream)));
 }
 
 gdn_status gdn_fp8_quant_act(const uint16_t* x, uint8_t* x8, float* x_scale, int32_t num_tokens, int32_t k,

@@ -1,10 +1,12 @@
 // kv_cache.cu - the attention layers' query/key preparation and their paged
-// key/value cache: gdn_qk_norm_rope, gdn_kv_cache_write, gdn_kv_cache_read.
+// key/value cache: gdn_qk_norm_rope, gdn_qk_norm_mrope, gdn_kv_cache_write,
+// gdn_kv_cache_read.
 //
 // Math, per head row x of D values (page "Qwen3.8-27B: from model structure to
 // vLLM inference data flow", section 01, GQA rows; section 04, FP8 cache):
 //   y = x / sqrt(mean(x^2) + eps) * gamma
-//   (y_i, y_i') <- (y_i cos a_i - y_i' sin a_i, y_i' cos a_i + y_i sin a_i),  a_i = position * f_i
+//   (y_i, y_i') <- (y_i cos a_i - y_i' sin a_i, y_i' cos a_i + y_i sin a_i),  a_i = position * f_i,
+//   with several axes (time, height, width) the position along frequency i's axis
 //   E4M3 cache: s = max(amax |y|, 1e-12) / 448, code = E4M3(y / s)
 // Every byte is read once and written once, so HBM bounds all three at large
 // token counts and the launch at small ones.
@@ -308,7 +310,9 @@ __device__ __forceinline__ void rows_pass(const RopeArgs& p, const KvArgs& c, co
 // frequency is taken in turns, in 64-bit fixed point (one turn = 2^64), where the whole turns fall away by themselves.
 // The frequency in turns is an fp64 product with 1 / (2 pi), off by up to 2^-52 of itself, and so is the angle: 2^-24
 // turns at the largest position and a radian a position, about what the fp64 product of the two is off by. The fixed
-// point adds 2^-65 turns a position, the cut to the upper 32 bits up to 2^-32.
+// point adds 2^-65 turns a position, the cut to the upper 32 bits up to 2^-32. With several axes a frequency's row of
+// positions is found once per block, so that the angles cost what they cost with one: the positions of a block's tokens
+// are a few cache lines per axis.
 // What bounds it: HBM at many tokens, the launch and the angles' chain at few. A batch is copied to shared memory while
 // the one before it is worked on: loads into registers left none in flight meanwhile, and a second batch of registers
 // spills at three blocks an SM. 16,384 tokens of 24 + 4 heads of 256, the keys dense and into a bf16 cache, 571 MB: 95
@@ -320,6 +324,7 @@ __device__ __forceinline__ void rows_pass(const RopeArgs& p, const KvArgs& c, co
 template <int D, bool kNorm, int kCache, int kRot>
 __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RopeArgs p, const KvArgs c, int tokens_per_block) {
   __shared__ uint64_t freq[kNorm ? D / 2 : 1];
+  __shared__ int axis[kNorm ? D / 2 : 1];
   __shared__ int place[kMaxTokens];
   extern __shared__ __align__(16) unsigned char stage[];  // [kBuffers][groups][kRows][D] bf16
   float2* turn = reinterpret_cast<float2*>(stage + kBuffers * kBatchBytes);  // [tokens][half]
@@ -332,10 +337,11 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RopeArgs p, con
       for (int i = threadIdx.x; i < half; i += kThreads) {
         const double f = p.inv_freq[i] * 0.15915494309189535;  // 1 / (2 pi): turns per position
         freq[i] = __double2ull_rn((f - floor(f)) * 18446744073709551616.0);
+        axis[i] = p.axes.num_axes ? p.axes.axis[i] : 0;
       }
       __syncthreads();
       for (int i = threadIdx.x; i < T * half; i += kThreads) {
-        const int64_t pos = p.positions[t0 + i / half];
+        const int64_t pos = p.positions[(int64_t)axis[i % half] * p.T + t0 + i / half];
         // the upper 32 bits as a signed number: half turns in [-1, 1)
         const int32_t top = (int32_t)(((uint64_t)pos * freq[i % half]) >> 32);
         // what the conversion to fp32 rounds off, up to 2^-25 half turns, turns sine and cosine on to first order

@@ -8,6 +8,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "gdn.h"
+
 namespace gdn {
 
 struct StepArgs {
@@ -140,6 +142,7 @@ struct RopeArgs {
   const int32_t* kv_slot;  // [T] (with a cache)
   int T, Hq;
   int32_t* dev_err;
+  gdn_rope_axes axes;  // num_axes 0: one position a token; else positions [num_axes][T] and each frequency's axis
 };
 
 struct ReadArgs {
@@ -161,6 +164,38 @@ struct TreeAttnArgs {
   float scale;
   int N, P, Hq, G, D, max_pages;
   void* workspace;
+  int32_t* dev_err;
+  float* lse;              // [N*P][Hq] or nullptr
+};
+
+struct ScoreArgs {
+  const uint16_t* q;      // [N*P][Hq][D]
+  const float* lse;       // [N*P][Hq]
+  const int32_t* table;   // [N][max_pages]
+  const int32_t* ctx;     // [N]
+  const uint64_t* mask;   // [N][P] or nullptr (chain)
+  float scale, decay;
+  float* score;           // [Rs][Hkv][max_tokens]
+  const int32_t* slot;    // [N]
+  const uint8_t* init;    // [N] or nullptr (all have weights)
+  int Rs, max_tokens;
+  int N, P, Hq, G, D, max_pages;
+  int32_t* dev_err;
+};
+
+struct EvictArgs {
+  const int32_t* table;      // [N][max_pages]
+  const int32_t* dst_table;  // [N][dst_max_pages]; `table` where the tokens stay in their pages
+  const int32_t* len;        // [N]
+  const int32_t* budget;     // [N]
+  float* score;              // [Rs][Hkv][max_tokens]
+  const int32_t* slot;       // [N]
+  const int32_t* dst_slot;   // [N]
+  int32_t* kept;             // [N][Hkv][max_kept]
+  int32_t* new_len;          // [N]
+  int sinks, recent;
+  int Rs, max_tokens, max_pages, dst_max_pages, max_kept;
+  int N, D;
   int32_t* dev_err;
 };
 
@@ -264,6 +299,8 @@ cudaError_t launch_rows(const RopeArgs& a, const KvArgs& c, bool norm, int D, cu
 cudaError_t launch_kv_read(const ReadArgs& a, const KvArgs& c, int D, cudaStream_t stream);
 size_t tree_attn_workspace_bytes(int P, int G, int D);
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, const KvArgs& c, cudaStream_t stream);
+cudaError_t launch_kv_score(const ScoreArgs& a, const KvArgs& c, cudaStream_t stream);
+cudaError_t launch_kv_evict(const EvictArgs& a, const KvArgs& c, cudaStream_t stream);
 cudaError_t launch_quant_act(const QuantActArgs& a, cudaStream_t stream);
 cudaError_t launch_quant_weight(const QuantWeightArgs& a, cudaStream_t stream);
 // Workspace bytes for the split-K partial tiles of a [T][N] output with K inputs

@@ -73,12 +73,17 @@ __global__ void __launch_bounds__(256) join_kernel(const tree_attn::Args a) {
     m = mn;
   }
   if (bad) return;
+  if (p.lse && col == 0)
+    p.lse[((size_t)d.n * p.P + j) * p.Hq + d.u / a.row_tiles * p.G + r % p.G] = tree_attn::lse_of(m, l);
   const float f = l == 0.f ? 0.f : __fdividef(1.f, l);
   *reinterpret_cast<uint2*>(p.out + at) = tree_attn::to_out(make_float4(o.x * f, o.y * f, o.z * f, o.w * f), p.gate, gate);
 }
 
-// Rows of one token and kv head; a box is 128 bytes of `box` tokens, swizzled as the MMAs read it.
-bool encode(CUtensorMap* m, void* base, const KvArgs& c, int D, int box_rows) {
+}  // namespace
+
+namespace tree_attn {
+
+bool encode_rows(CUtensorMap* m, void* base, const KvArgs& c, int D, int box_rows) {
   const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return false;
   const int es = c.e4m3 ? 1 : 2;
@@ -91,7 +96,13 @@ bool encode(CUtensorMap* m, void* base, const KvArgs& c, int D, int box_rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-}  // namespace
+int box_tokens(int page) {
+  int box = 16;
+  while (box < kTile && page % (2 * box) == 0) box *= 2;
+  return box;
+}
+
+}  // namespace tree_attn
 
 size_t tree_attn_workspace_bytes(int P, int G, int D) {
   int rows, tiles;
@@ -109,10 +120,9 @@ cudaError_t launch_tree_attn(const TreeAttnArgs& p, const KvArgs& c, cudaStream_
   a.c = c;
   row_tiles(p.P, p.G, &a.rows, &a.row_tiles);
   a.slot_floats = slot_floats(a.rows, p.D);
-  a.box = 16;
-  while (a.box < tree_attn::kTile && c.page % (2 * a.box) == 0) a.box *= 2;
+  a.box = tree_attn::box_tokens(c.page);
   CUtensorMap tmk{}, tmv{};
-  if (!encode(&tmk, c.k, c, p.D, a.box) || !encode(&tmv, c.v, c, p.D, a.box)) return cudaErrorInvalidValue;
+  if (!tree_attn::encode_rows(&tmk, c.k, c, p.D, a.box) || !tree_attn::encode_rows(&tmv, c.v, c, p.D, a.box)) return cudaErrorInvalidValue;
   const int grid = sms < tree_attn::kMaxCtas ? sms : tree_attn::kMaxCtas;
   err = c.e4m3 ? tree_attn::launch_e4m3(a, tmk, tmv, grid, stream) : tree_attn::launch_bf16(a, tmk, tmv, grid, stream);
   if (err != cudaSuccess) return err;

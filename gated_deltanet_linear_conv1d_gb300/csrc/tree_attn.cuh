@@ -4,7 +4,7 @@
 //
 // Math, per query row (node j, query head h), over the tokens t that it sees:
 //   s_t = scale (q . k_t),  m = max s_t,  l = sum e^(s_t - m),  out = sum e^(s_t - m) v_t / l
-// and with a gate out <- out / (1 + e^-gate).
+// and with a gate out <- out / (1 + e^-gate). On request also lse = m + ln l, what the rows' weights are relative to.
 //
 // Work. The unit of work is a tile of 128 cached tokens for one (request, kv head,
 // row tile): the query rows of the Hq / Hkv heads of all P nodes, up to kRows of
@@ -483,6 +483,11 @@ __device__ __forceinline__ bool any_in_group(int id, bool x) {
       : "r"(id), "r"((uint32_t)x)
       : "memory");
   return r != 0;
+}
+
+// ln of a row's sum l of weights relative to 2^m.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 __device__ __forceinline__ int cta_of(long long tile, long long total, int grid) {
@@ -1291,7 +1296,12 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
       if (bad && ot == 0) report(p.dev_err, GDN_DEVERR_SLOT);
       if (s.t0 == 0 && s.t1 == s.tiles) {
         if (bad) continue;
-        if (ot < a.rows) fin[ot] = l_run == 0.f ? 0.f : __fdividef(1.f, l_run);
+        if (ot < a.rows) {
+          fin[ot] = l_run == 0.f ? 0.f : __fdividef(1.f, l_run);
+          const int rr = r0 - roff + ot, j = rr / p.G;
+          if (p.lse && og == 0 && j < p.P)
+            p.lse[((size_t)s.n * p.P + j) * p.Hq + h * p.G + rr % p.G] = lse_of(m_run, l_run);
+        }
         // A few rows at a time through shared memory, a thread then has neighbouring values of one or two rows. The
         // loop is not unrolled (the registers' choice is): code that runs once per segment costs its fetches.
         constexpr int kS = C::kStageRows, kY = kS / 4;
@@ -1395,6 +1405,12 @@ cudaError_t launch_format(const Args& a, const CUtensorMap& tmk, const CUtensorM
   if (a.rows <= 32) return launch_rows<128, kE4m3, 32>(a, tmk, tmv, grid, stream);
   return launch_rows<128, kE4m3, 64>(a, tmk, tmv, grid, stream);
 }
+
+// Tensor map of a cache's K or V: rows of one token and kv head; a box is 128 bytes of `box_rows` tokens, swizzled as the
+// MMAs read it.
+bool encode_rows(CUtensorMap* m, void* base, const KvArgs& c, int D, int box_rows);
+// Tokens per box: a power of two that divides the page, at most 128.
+int box_tokens(int page);
 
 cudaError_t launch_bf16(const Args& a, const CUtensorMap& tmk, const CUtensorMap& tmv, int grid, cudaStream_t stream);
 cudaError_t launch_e4m3(const Args& a, const CUtensorMap& tmk, const CUtensorMap& tmv, int grid, cudaStream_t stream);

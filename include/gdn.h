@@ -53,8 +53,8 @@
  * - Two requests of one call must not name the same slot (undefined result).
  * - Supported geometry: dk = dv = 128, K = 4, Hv a multiple of Hk with
  *   Hv / Hk <= 8. Anything else returns GDN_ERR_UNSUPPORTED.
- * - The attention layers' entry points (gdn_qk_norm_rope, gdn_kv_cache_*,
- *   gdn_tree_attention) have a geometry of their own, stated there.
+ * - The attention layers' entry points (gdn_qk_norm_rope, gdn_qk_norm_mrope,
+ *   gdn_kv_*, gdn_tree_attention*) have a geometry of their own, stated there.
  */
 #ifndef GDN_H
 #define GDN_H
@@ -537,6 +537,32 @@ gdn_status gdn_qk_norm_rope(const uint16_t *q, int64_t q_stride_t, int64_t q_str
                             int32_t num_kv_heads, int32_t head_dim, int32_t *dev_err, void *stream);
 
 /*
+ * gdn_qk_norm_mrope - gdn_qk_norm_rope with several position axes, for image and
+ * video prompts (page "Qwen3.8-27B: from model structure to vLLM inference data
+ * flow", section 07; the pages do not spell the axes out): a token has a position
+ * along each of them (time, height, width), and every frequency turns by the
+ * position of its own axis, angle = positions[axis[i]][t] * inv_freq[i]. With the
+ * same position on all axes the results are gdn_qk_norm_rope's, bit for bit.
+ *
+ *   axes       num_axes 1 .. 4, and axis[i] < num_axes of each of the rotary_dim / 2
+ *              frequencies (host memory, read by the call)
+ *   positions  [num_axes][T] int32
+ *   everything else as gdn_qk_norm_rope
+ */
+typedef struct gdn_rope_axes {
+    int32_t num_axes;
+    uint8_t axis[128];
+} gdn_rope_axes;
+
+gdn_status gdn_qk_norm_mrope(const uint16_t *q, int64_t q_stride_t, int64_t q_stride_h, const uint16_t *k,
+                             int64_t k_stride_t, int64_t k_stride_h, const float *q_gamma, const float *k_gamma,
+                             float eps, const int32_t *positions, const double *inv_freq, int32_t rotary_dim,
+                             const gdn_rope_axes *axes, int32_t interleaved, uint16_t *q_out, uint16_t *k_out,
+                             const uint16_t *v, int64_t v_stride_t, int64_t v_stride_h, const gdn_kv_cache *cache,
+                             const int32_t *kv_slot, int32_t num_tokens, int32_t num_q_heads,
+                             int32_t num_kv_heads, int32_t head_dim, int32_t *dev_err, void *stream);
+
+/*
  * gdn_tree_attention - attention of P = num_pos drafted tokens per request over
  * its cached context and over each other, in one forward (P = 1: a decode step).
  * Node j of request n is token ctx_len[n] + j of the request and its k and v are
@@ -581,6 +607,99 @@ gdn_status gdn_tree_attention(const gdn_kv_cache *cache, const uint16_t *q, cons
 /* Bytes of gdn_tree_attention's workspace for these sizes (whatever the lengths); 0 for invalid ones. */
 size_t gdn_tree_attention_workspace_bytes(const gdn_kv_cache *cache, int32_t num_seqs, int32_t num_pos,
                                           int32_t num_q_heads);
+
+/*
+ * gdn_tree_attention_lse - gdn_tree_attention that also leaves what each row's
+ * weights are relative to, lse = ln sum_t e^(scale (q . k_t)) over the tokens
+ * that the row sees: -inf for a row that sees nothing. Out and its bits are
+ * gdn_tree_attention's; the workspace too.
+ *
+ *   lse  [N*P][Hq] fp32 out, 4-byte aligned; a padding request's rows and those of a
+ *        request that writes nothing are left untouched
+ */
+gdn_status gdn_tree_attention_lse(const gdn_kv_cache *cache, const uint16_t *q, const int32_t *block_table,
+                                  int32_t max_pages, const int32_t *ctx_len, const uint64_t *tree_mask,
+                                  const uint16_t *gate, float scale, uint16_t *out, float *lse, int32_t num_seqs,
+                                  int32_t num_pos, int32_t num_q_heads, void *workspace, size_t workspace_bytes,
+                                  int32_t *dev_err, void *stream);
+
+/*
+ * gdn_kv_score - the attention weight that every cached token of a request
+ * receives from num_pos query rows a head, added to what earlier calls left:
+ *   score[t] <- decay score[t] + sum over the rows r that see t of e^(scale (q_r . k_t) - lse_r)
+ * with one score per (token, kv head), the sum over the kv head's Hq / Hkv query
+ * heads and the P positions. The rows are gdn_tree_attention_lse's (same q,
+ * block table, lengths, mask, scale), after a decode step or a verify, or the last
+ * rows of a prompt (its observation window; ctx_len is then the prompt's length
+ * less P). A token from ctx_len on is new: its score starts from zero, whatever is
+ * in its place. The scores are a state per request, in slots as the recurrent
+ * state is; tokens keep their order in the request, so gdn_kv_evict moves them
+ * along with the cache.
+ *
+ *   q, block_table, ctx_len, tree_mask, num_pos, num_q_heads: as gdn_tree_attention
+ *   lse       [N*P][Hq] fp32. A row whose lse is not a finite number adds nothing: a
+ *             caller leaves rows out (rejected drafts) with an infinity there
+ *   score     [num_slots][Hkv][max_tokens] fp32, in/out; 4-byte aligned; max_tokens at most 2^30
+ *   slot_idx  [N] int32: negative skips the request; >= num_slots sets
+ *             GDN_DEVERR_SLOT and skips it. Two requests of one call must not name
+ *             the same slot.
+ *   has_init  [N] uint8 or NULL (= all 1): 0 starts every score from zero without
+ *             reading the slot
+ *   decay     finite
+ * A negative ctx_len is a padding request. ctx_len + P tokens that the table or
+ * max_tokens cannot hold set GDN_DEVERR_OFFSETS and the request writes nothing; a
+ * page outside [0, num_pages) sets GDN_DEVERR_SLOT and its tokens' scores are
+ * left as they were. Scores from token ctx_len + P on are not touched. The sums are
+ * fp32, in a fixed order. An E4M3 cache's products take q as two E4M3 terms (2^-17
+ * of the head row's largest value). q 16-byte, tree_mask 8-byte aligned.
+ *   dev_err   GDN_DEVERR_TIMEOUT too, if a bounded wait inside the kernel ran out
+ */
+gdn_status gdn_kv_score(const gdn_kv_cache *cache, const uint16_t *q, const float *lse, const int32_t *block_table,
+                        int32_t max_pages, const int32_t *ctx_len, const uint64_t *tree_mask, float scale,
+                        float decay, float *score, const int32_t *slot_idx, const uint8_t *has_init,
+                        int32_t num_slots, int32_t max_tokens, int32_t num_seqs, int32_t num_pos,
+                        int32_t num_q_heads, int32_t *dev_err, void *stream);
+
+/*
+ * gdn_kv_evict - a request's cache cut down to min(length, budget) tokens, each
+ * kv head's own: first the first sink_tokens and the last recent_tokens of the
+ * request, then those of the largest score, equal ones by the lowest index (a NaN
+ * counts as the lowest score; where even the first and last ones are more than the
+ * budget, those of the lowest index stay). The kept tokens' keys, values, scales and scores go, in their order, to
+ * tokens 0, 1, .. of the request: of its own pages, or of other ones. Keys keep
+ * the rotation of their old position, so attention over what is left needs
+ * nothing else, and new tokens follow at new_len with the positions they would
+ * have had.
+ *
+ *   block_table [N][max_pages] int32;  length [N] int32: a negative length is a
+ *               padding request (skipped, new_len left untouched, as with a
+ *               negative slot)
+ *   budget      [N] int32 >= 0
+ *   dst_table   [N][dst_max_pages] int32: the pages that the kept tokens go to. An
+ *               entry is the request's own page in the same place of block_table,
+ *               or one that no request of the call has in its block_table and no other in its
+ *               dst_table (undefined values otherwise): a page that other
+ *               requests share stays whole that way. NULL: in place (dst_max_pages
+ *               is not used).
+ *   score       [num_slots][Hkv][max_tokens] fp32, in/out;  slot_idx [N]
+ *   dst_slot    [N] int32: the slots that the kept tokens' scores go to, the
+ *               request's own or one that no other request of the call names. NULL:
+ *               slot_idx
+ *   kept        [N][Hkv][max_kept] int32 out: the kept tokens' old indices,
+ *               ascending; entries from new_len on are not touched
+ *   new_len     [N] int32 out, not `length` itself: the request's tokens now, -1 if
+ *               the request breaks a limit
+ *   sink_tokens, recent_tokens >= 0;  max_tokens at most 2^30
+ * A request with a slot >= num_slots (or a negative dst_slot), or a page outside
+ * [0, num_pages) in either table, sets GDN_DEVERR_SLOT; one whose tokens the tables,
+ * max_tokens or max_kept cannot hold, or with a negative budget, sets
+ * GDN_DEVERR_OFFSETS; either way it writes nothing but its new_len.
+ */
+gdn_status gdn_kv_evict(const gdn_kv_cache *cache, const int32_t *block_table, int32_t max_pages,
+                        const int32_t *length, const int32_t *budget, int32_t sink_tokens, int32_t recent_tokens,
+                        const int32_t *dst_table, int32_t dst_max_pages, float *score, const int32_t *slot_idx,
+                        const int32_t *dst_slot, int32_t num_slots, int32_t max_tokens, int32_t *kept,
+                        int32_t max_kept, int32_t *new_len, int32_t num_seqs, int32_t *dev_err, void *stream);
 
 /* Bytes of one slot of the fp32 state pool: Hv*dv*dk*4 (3 MiB at 48x128x128,
  * the L00 table's "3 MiB per sequence per layer"). 0 for invalid dims. */
