@@ -18,6 +18,8 @@
 //
 // Roles: two groups of four warps that take the tiles in turn (a thread has one token), a warp for the copies (TMA, 16 KB
 // blocks of 128 tokens x 128 bytes into a ring), one for the MMAs, four for the query rows. Every wait is bounded.
+#include <type_traits>
+
 #include "tree_attn.cuh"
 
 namespace gdn {
@@ -72,11 +74,12 @@ struct Cfg {
   static constexpr int kCols = 2 * kRows < 32 ? 32 : 2 * kRows;  // of tensor memory: two tiles' scores
   static constexpr int kQBytes = kRows * D * 2;            // one buffer
   static constexpr int kBarBytes = (sizeof(Bars) + 15) / 16 * 16;
-  // behind the ring: Q, then by row what makes a score a base-2 logarithm of its weight (factor and -lse), then the masks
+  // behind the ring: Q, then by row what makes a score a base-2 logarithm of its weight (factor and -lse), then which
+  // tokens the row sees: bit i of words 0 and 1: node i, bit 0 of word 2: those of the context
   static constexpr int oFac = kQBuf * kQBytes;
   static constexpr int oLse = oFac + kQBuf * kRows * 4;
-  static constexpr int oMask = oLse + kQBuf * kRows * 4;
-  static constexpr int oBars = oMask + kQBuf * kRows * 8;
+  static constexpr int oSees = oLse + kQBuf * kRows * 4;
+  static constexpr int oBars = oSees + kQBuf * 3 * kRows * 4;
   static constexpr int kRest = oBars + kBarBytes;
   static constexpr int kFit = (kSmemLimit - kRest) / (int)kBlock;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
@@ -141,86 +144,97 @@ struct Walk {
   }
 };
 
-// The query rows of a segment into buffer qb, as rows of the MMAs' second operand, with their factors and masks.
+// The registers of a tensor-memory load, after the wait for it: nothing that uses them moves in front of the wait.
+template <int kN>
+__device__ __forceinline__ void loaded(uint32_t (&u)[kN]) {
+  umma::wait_ld();
+#pragma unroll
+  for (int i = 0; i < kN; ++i) asm volatile("" : "+r"(u[i]));
+}
+
+// The query rows of a segment into buffer qb, as rows of the MMAs' second operand, with their factors and what they see.
+// A warp has up to 32 rows in a row, a lane what goes by the row. The rows are copied past the registers, all of them on
+// their way at once. An E4M3 cache's are then taken apart into their two terms in place: a row's 2 D bytes are its own.
 template <int D, bool kE4m3, int kRows>
 __device__ __forceinline__ void load_queries(const Args& a, const Seg& s, unsigned char* rest, Bars* B, int qb, int share) {
   using C = Cfg<D, kE4m3, kRows>;
+  static_assert(kRows <= 32 * kQueryWarps, "a lane per row");
   const ScoreArgs& p = a.p;
-  const int lane = threadIdx.x & 31, rp = (a.rows + 15) / 16 * 16;
+  const int lane = threadIdx.x & 31, rp = (a.rows + 15) / 16 * 16, per = rp / kQueryWarps;
   const uint32_t q_block = rp * 128;
   const int r0 = s.c * a.rows, all = min(a.rows, p.P * p.G - r0);
   unsigned char* q_s = rest + qb * C::kQBytes;
   float* fac = reinterpret_cast<float*>(rest + C::oFac) + qb * kRows;
   float* lse = reinterpret_cast<float*>(rest + C::oLse) + qb * kRows;
-  uint64_t* mask = reinterpret_cast<uint64_t*>(rest + C::oMask) + qb * kRows;
-  bool dead = false;
-  constexpr int kBatch = 4;
-  for (int rb = share * kBatch; rb < rp; rb += kQueryWarps * kBatch) {
-    uint4 raw[kBatch];
-    float l[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r = rb + i, j = (r0 + r) / p.G, g = (r0 + r) % p.G;
-      raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      l[i] = INFINITY;
-      if (r < all) {
-        const size_t row = ((size_t)s.n * p.P + j) * p.Hq + s.h * p.G + g;
-        if (lane < D / 8) raw[i] = __ldg(reinterpret_cast<const uint4*>(p.q + row * D) + lane);
-        l[i] = __ldg(p.lse + row);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r = rb + i;
-      float f = p.scale * kLog2e;
-      if constexpr (!kE4m3) {
-        if (lane < D / 8) *reinterpret_cast<uint4*>(q_s + (lane >> 3) * q_block + swz(r, (lane & 7) * 16)) = raw[i];
-      } else {
-        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-        float x[8], most = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[2 * e] = __uint_as_float(w[e] << 16);
-          x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(x[e]));
-        most = tree_attn::warp_max(most);
-        // a power of two that takes the largest value below 256; a row with an infinity has no scores
-        const int ex = (int)(__float_as_uint(most) >> 23) - 127;
-        const int up = most == 0.f ? 0 : min(7 - ex, 120);
-        const float by = __uint_as_float((uint32_t)(up + 127) << 23);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= by;
-        uint2 first, second;
-        tree_attn::two_terms(x, first, second);
-        if (lane < D / 8) {
-          unsigned char* blk = q_s + (lane >> 4) * q_block;
-          *reinterpret_cast<uint2*>(blk + swz(r, (lane & 15) * 8)) = first;
-          *reinterpret_cast<uint2*>(blk + C::kBlk * q_block + swz(r, (lane & 15) * 8)) = second;
-        }
-        f = ex == 128 ? __uint_as_float(0x7fffffffu) : f * __uint_as_float((uint32_t)(127 - up) << 23);
-      }
-      const bool live = fabsf(l[i]) < INFINITY;  // a row without a finite sum adds nothing
-      dead |= r < all && !live;
-      if (lane == 0) {
-        const int j = (r0 + r) / p.G;
-        fac[r] = f;
-        lse[r] = live ? -l[i] * kLog2e : -INFINITY;
-        uint64_t m = 0;
-        if (r < all) m = p.mask ? __ldg(p.mask + (size_t)s.n * p.P + j) : j == 63 ? ~0ull : (2ull << j) - 1;
-        mask[r] = m & ~0ull >> (64 - p.P);
-      }
+  uint32_t* sees = reinterpret_cast<uint32_t*>(rest + C::oSees) + qb * 3 * kRows;
+  const int first = share * per, mine = first + lane;
+  const bool have = lane < per && mine < all;
+  const int j = (r0 + mine) / p.G;
+  const size_t row = ((size_t)s.n * p.P + j) * p.Hq + s.h * p.G + (r0 + mine) % p.G;
+  const size_t off = have ? row * D : 0;
+  // piece `lane` (16 bytes) of row r: where it lies, bf16 values
+  auto piece = [&](int r) { return q_s + (lane >> 3) * q_block + swz(r, (lane & 7) * 16); };
+  for (int i = 0; i < per; ++i) {
+    const size_t o = __shfl_sync(0xffffffffu, off, i);
+    const int r = first + i;
+    if (lane < D / 8) {
+      const uint32_t bytes = r < all ? 16u : 0u;  // zeros behind the last row
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(piece(r))), "l"(p.q + o + lane * 8), "r"(bytes)
+                   : "memory");
     }
   }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  const float l = have ? __ldg(p.lse + row) : INFINITY;
+  uint64_t m = 0;
+  if (have) m = p.mask ? __ldg(p.mask + (size_t)s.n * p.P + j) : j == 63 ? ~0ull : (2ull << j) - 1;
+  const bool live = fabsf(l) < INFINITY;  // a row without a finite sum adds nothing
+  m = live ? m & ~0ull >> (64 - p.P) : 0ull;
+  if (lane < per) {
+    lse[mine] = live ? -l * kLog2e : -INFINITY;
+    sees[mine] = (uint32_t)m;
+    sees[kRows + mine] = (uint32_t)(m >> 32);
+    sees[2 * kRows + mine] = live;
+  }
+  const bool dead = __any_sync(0xffffffffu, have && !live);
   if (lane == 0) B->dead[qb][share] = dead;
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if constexpr (kE4m3) {
+    const float f0 = p.scale * kLog2e;
+    __syncwarp();
+#pragma unroll 4
+    for (int i = 0; i < per; ++i) {
+      const int r = first + i;
+      uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+      if (lane < D / 8) raw = *reinterpret_cast<const uint4*>(piece(r));
+      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+      float x[8], most = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[2 * e] = __uint_as_float(w[e] << 16);
+        x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(x[e]));
+      most = tree_attn::warp_max(most);
+      // a power of two that takes the largest value below 256; a row with an infinity has no scores
+      const int ex = (int)(__float_as_uint(most) >> 23) - 127;
+      const int up = most == 0.f ? 0 : min(7 - ex, 120);
+      const float by = __uint_as_float((uint32_t)(up + 127) << 23);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] *= by;
+      uint2 one, two;
+      tree_attn::two_terms(x, one, two);
+      __syncwarp();
+      if (lane < D / 8) {
+        unsigned char* blk = q_s + (lane >> 4) * q_block + swz(r, (lane & 15) * 8);
+        *reinterpret_cast<uint2*>(blk) = one;
+        *reinterpret_cast<uint2*>(blk + C::kBlk * q_block) = two;
+      }
+      if (lane == 0)
+        fac[r] = ex == 128 ? __uint_as_float(0x7fffffffu) : f0 * __uint_as_float((uint32_t)(127 - up) << 23);
+    }
+  }
 }
-
-// What a thread knows of its token of a tile, loaded a tile ahead.
-struct Token {
-  float key_scale, before;
-  int state;  // 1: the token is the request's and its page is in the pool
-};
 
 template <int D, bool kE4m3, int kRows>
 __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const __grid_constant__ CUtensorMap tmk) {
@@ -406,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
     const int wg = warp >> 2, w4 = warp & 3, mine = 32 * w4 + lane;
     const float* fac_s = reinterpret_cast<const float*>(rest + C::oFac);
     const float* lse_s = reinterpret_cast<const float*>(rest + C::oLse);
-    const uint64_t* mask_s = reinterpret_cast<const uint64_t*>(rest + C::oMask);
+    const uint32_t* sees_s = reinterpret_cast<const uint32_t*>(rest + C::oSees);
     Walk walk(a, plan);
     Seg s;
     int seg = 0, used = 0;
@@ -416,79 +430,110 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
       const int32_t* table = p.table + (size_t)s.n * p.max_pages;
       const bool fresh = p.init && !p.init[s.n];
       float* out = p.score + ((size_t)__ldg(p.slot + s.n) * c.Hkv + s.h) * p.max_tokens;
-      auto fetch = [&](int t) {
-        Token k{1.f, 0.f, 0};
+      // A token's page, then its key's scale and its score so far, are loaded two tiles and one tile ahead of their use.
+      auto load_page = [&](int t) {
         const int tok = t * kTile + mine;
-        if (t >= s.t1 || tok >= s.len) return k;
-        const int page = __ldg(table + tok / c.page);
-        if (page < 0 || page >= c.pages) {
-          report(p.dev_err, GDN_DEVERR_SLOT);
-          return k;
-        }
-        k.state = 1;
-        if constexpr (kE4m3) k.key_scale = __ldg(c.k_scale + ((size_t)page * c.Hkv + s.h) * c.page + tok % c.page);
-        if (s.c > 0) k.before = out[tok];
-        else if (tok < s.ctx && !fresh) k.before = out[tok] * p.decay;
-        return k;
+        return t < s.t1 && tok < s.len ? __ldg(table + tok / c.page) : -1;
+      };
+      const bool again = s.c > 0, old = again || !fresh;
+      const float decay = again ? 1.f : p.decay;
+      float key_scale = 1.f, before = 0.f;
+      auto load_token = [&](int t, int page, float& ks, float& w) {
+        const int tok = t * kTile + mine;
+        ks = 1.f;
+        w = 0.f;
+        if (page < 0 || page >= c.pages) return;
+        if constexpr (kE4m3) ks = __ldg(c.k_scale + ((size_t)page * c.Hkv + s.h) * c.page + tok % c.page);
+        if (old && (again || tok < s.ctx)) w = out[tok];
       };
       int t = s.t0 + ((s.at & 1) == wg ? 0 : 1);
-      Token next = fetch(t);
+      int page = load_page(t), next_page = load_page(t + 2);
+      load_token(t, page, key_scale, before);
       wait_warp(&B->q_full[qb], (seg / kQBuf) & 1, abort);
       const volatile int* d4 = B->dead[qb];
       const bool dead = (d4[0] | d4[1] | d4[2] | d4[3]) != 0;
       const float* fac = fac_s + qb * kRows;
       const float* lse = lse_s + qb * kRows;
-      const uint64_t* mask = mask_s + qb * kRows;
+      const uint32_t* sees = sees_s + qb * 3 * kRows;
       const float f0 = p.scale * kLog2e;
       for (; t < s.t1; t += 2, ++used) {
-        const Token k = next;
-        next = fetch(t + 2);
+        const int this_page = page;
+        const float ks = key_scale, w = before;
+        page = next_page;
+        next_page = load_page(t + 4);
+        load_token(t + 2, page, key_scale, before);
         wait_warp(&B->s_full[wg], used & 1, abort);
         umma::fence_after_sync();
         const uint32_t ts = umma::taddr(tmem, 32 * w4, wg * kRows);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        const bool masked = dead || (t + 1) * kTile > s.ctx;
+        // The weights of eight rows' scores. kMasked: not of rows that are left out or behind the last, nor of nodes that
+        // a row does not see: by selection, whatever the score is.
         const int node = t * kTile + mine - s.ctx;
-        constexpr int kN = kRows < 32 ? 16 : 32;
-#pragma unroll 1
-        for (int r0 = 0; r0 < rows; r0 += kN) {
-          uint32_t u[kN];
-          if constexpr (kN == 32) umma::ld32_nowait(ts + r0, u);
-          else umma::ld16_nowait(ts + r0, u);
-          umma::wait_ld();
-          const bool whole = !masked && r0 + kN <= rows;
+        const uint32_t* sees_t = sees + (node < 0 ? 2 : node < 32 ? 0 : 1) * kRows;
+        const int bit = node < 0 ? 0 : node & 31;
+        auto weights = [&](const uint32_t* u, int r0, auto masked) {
 #pragma unroll
-          for (int i = 0; i < kN; i += 4) {
+          for (int i = 0; i < 8; i += 4) {
+            const int r = r0 + i;
             float4 f = make_float4(f0, f0, f0, f0);
-            if constexpr (kE4m3) f = *reinterpret_cast<const float4*>(fac + r0 + i);
-            const float4 l = *reinterpret_cast<const float4*>(lse + r0 + i);
+            if constexpr (kE4m3) f = *reinterpret_cast<const float4*>(fac + r);
+            const float4 l = *reinterpret_cast<const float4*>(lse + r);
             float2 x[2] = {make_float2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])),
                            make_float2(__uint_as_float(u[i + 2]), __uint_as_float(u[i + 3]))};
             if constexpr (kE4m3) {
-              x[0] = __fmul2_rn(x[0], make_float2(k.key_scale, k.key_scale));
-              x[1] = __fmul2_rn(x[1], make_float2(k.key_scale, k.key_scale));
+              x[0] = __fmul2_rn(x[0], make_float2(ks, ks));
+              x[1] = __fmul2_rn(x[1], make_float2(ks, ks));
             }
             x[0] = __ffma2_rn(x[0], make_float2(f.x, f.y), make_float2(l.x, l.y));
             x[1] = __ffma2_rn(x[1], make_float2(f.z, f.w), make_float2(l.z, l.w));
             float e[4] = {ex2(x[0].x), ex2(x[0].y), ex2(x[1].x), ex2(x[1].y)};
-            if (!whole) {
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const int r = r0 + i + y;
-                const bool seen = r < rows && lse[r] > -INFINITY &&
-                                  (node < 0 || (node < 64 && ((mask[r] >> node) & 1)));
-                e[y] = seen ? e[y] : 0.f;
-              }
+            if constexpr (decltype(masked)::value) {
+              const uint4 w = *reinterpret_cast<const uint4*>(sees_t + r);
+              e[0] = (w.x >> bit) & 1u ? e[0] : 0.f;
+              e[1] = (w.y >> bit) & 1u ? e[1] : 0.f;
+              e[2] = (w.z >> bit) & 1u ? e[2] : 0.f;
+              e[3] = (w.w >> bit) & 1u ? e[3] : 0.f;
             }
             sum[0] = __fadd2_rn(sum[0], make_float2(e[0], e[1]));
             sum[1] = __fadd2_rn(sum[1], make_float2(e[2], e[3]));
+          }
+        };
+        constexpr int kN = kRows < 32 ? 16 : 32;  // rows at a time
+        const bool masked = dead || (t + 1) * kTile > s.ctx;
+        auto load = [&](int r0, uint32_t (&u)[kN]) {
+          if constexpr (kN == 32) umma::ld32_nowait(ts + r0, u);
+          else umma::ld16_nowait(ts + r0, u);
+        };
+        auto compute = [&](int r0, const uint32_t (&u)[kN]) {
+          if (!masked && r0 + kN <= rows) {  // no branch inside: the chains of all rows run side by side
+#pragma unroll
+            for (int i = 0; i < kN; i += 8) weights(u + i, r0 + i, std::false_type());
+          } else {
+#pragma unroll
+            for (int i = 0; i < kN; i += 8)
+              if (r0 + i < rows) weights(u + i, r0 + i, std::true_type());
+          }
+        };
+        uint32_t u[kN], v[kN];  // one is on its way while the other is worked on
+        load(0, u);
+#pragma unroll 1
+        for (int r0 = 0; r0 < rows; r0 += 2 * kN) {
+          loaded(u);
+          if (kRows > kN && r0 + kN < rows) load(r0 + kN, v);
+          compute(r0, u);
+          if (kRows > kN && r0 + kN < rows) {
+            loaded(v);
+            if (r0 + 2 * kN < rows) load(r0 + 2 * kN, u);
+            compute(r0 + kN, v);
           }
         }
         umma::fence_before_sync();
         __syncwarp();
         if (lane == 0) arrive(&B->s_empty[wg]);
-        if (k.state && !*(volatile int*)abort)
-          out[t * kTile + mine] = k.before + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
+        if (t * kTile + mine < s.len && !*(volatile int*)abort) {
+          if (this_page < 0 || this_page >= c.pages) report(p.dev_err, GDN_DEVERR_SLOT);
+          else out[t * kTile + mine] = fmaf(w, decay, (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
+        }
       }
       __syncwarp();
       if (lane == 0) arrive(&B->q_empty[qb]);
