@@ -12,7 +12,7 @@
 // terms, exact down to 2^-17 of the row's largest value; the second term's MMAs add to the same columns.
 //
 // Work. The tiles of 128 tokens of all (request, kv head) units stand in one line, cut into equal pieces, one per CTA. Up
-// to 128 rows stay in shared memory for a unit's tiles. More are taken in chunks: the piece goes through kSub tiles with
+// to 128 rows stay in shared memory for a unit's tiles. More are taken in chunks: the piece goes through some tiles with
 // one chunk after the other, the keys coming from L2 from the second on, and a tile's later chunks add to the weights
 // that the same thread has stored.
 //
@@ -36,12 +36,12 @@ using tree_attn::swz;
 using tree_attn::wait;
 using tree_attn::wait_warp;
 
-constexpr int kMaxRows = 128;  // of a chunk
-constexpr int kSub = 8;        // tiles that the chunks of more rows go through in turn
-constexpr int kUnitCost = 1;   // what a unit takes beside its tiles, in tiles
-constexpr int kQBuf = 2;
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kQueryWarp = 10, kQueryWarps = 4;
-static_assert(kQueryWarps == 4, "see where their flags are read");
+constexpr int kMaxRows = 192;  // of a chunk
+// Bytes of keys that the chunks of more rows go through in turn, a CTA: what all CTAs have stays in L2.
+constexpr int kSubBytes = 640 * 1024;
+constexpr int kGroups = 2;     // of four warps for the weights
+constexpr int kCopyWarp = 4 * kGroups, kMmaWarp = kCopyWarp + 1, kQueryWarp = kCopyWarp + 2, kQueryWarps = 2;
+constexpr int kLoaders = 4 * kGroups + kQueryWarps;  // all but those of the copies and the MMAs
 constexpr int kThreads = 32 * (kQueryWarp + kQueryWarps);
 constexpr int kMaxStages = 12;
 
@@ -50,19 +50,23 @@ struct Args {
   KvArgs c;
   int rows, chunks;  // rows of a chunk (the last one may have fewer)
   int box;           // tokens per TMA box
+  int sub;           // tiles that the chunks go through in turn
+  int cost;          // what a unit takes beside its tiles, in tiles
 };
 
 struct Plan {
   long long lo;
-  int count, n, h, t;  // t: where the piece begins in the unit, whose first kUnitCost places hold no tile
+  int count, n, h, t;  // t: where the piece begins in the unit, whose first `cost` places hold no tile
 };
 
 struct Bars {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t s_full[2], s_empty[2], q_full[kQBuf], q_empty[kQBuf], drain;
+  uint64_t s_full[kGroups], s_empty[kGroups], q_full[2], q_empty[2], r_empty[2], drain;
   uint32_t tmem;
   int abort;
-  int dead[kQBuf][kQueryWarps];  // the buffer has a row that adds nothing
+  int rows[2];      // of the segment, without those that add nothing
+  float factor[2];  // what takes its scores to base 2
+  uint32_t most[kLoaders];
   Plan plan;
   long long warp_total[kThreads / 32];
 };
@@ -71,23 +75,26 @@ template <int D, bool kE4m3, int kRows>
 struct Cfg {
   static constexpr int kBlk = D * (kE4m3 ? 1 : 2) / 128;  // ring blocks of a tile
   static constexpr int kTerms = kE4m3 ? 2 : 1;
-  static constexpr int kCols = 2 * kRows < 32 ? 32 : 2 * kRows;  // of tensor memory: two tiles' scores
-  static constexpr int kQBytes = kRows * D * 2;            // one buffer
-  static constexpr int kBarBytes = (sizeof(Bars) + 15) / 16 * 16;
-  // behind the ring: Q, then by row what makes a score a base-2 logarithm of its weight (factor and -lse), then which
-  // tokens the row sees: bit i of words 0 and 1: node i, bit 0 of word 2: those of the context
-  static constexpr int oFac = kQBuf * kQBytes;
-  static constexpr int oLse = oFac + kQBuf * kRows * 4;
-  static constexpr int oSees = oLse + kQBuf * kRows * 4;
-  static constexpr int oBars = oSees + kQBuf * 3 * kRows * 4;
-  static constexpr int kRest = oBars + kBarBytes;
+  static constexpr int kBufs = kGroups;                    // tiles' scores in tensor memory
+  static constexpr int kCols = kRows == 16 ? 32 : kRows == 64 ? 128 : kRows == 128 ? 256 : 512;
+  static_assert(kBufs * kRows <= kCols, "tensor memory");
+  static constexpr int kQBytes = kRows * D * 2;            // query rows of a segment
+  // Two segments' query rows where the ring keeps six blocks beside them: the next segment's come while this one runs.
+  // What else goes by the row is there for two.
+  static constexpr int kRest1 = 3 * 2 * kRows * 4 + (sizeof(Bars) + 15) / 16 * 16;
+  static constexpr int kQBuf = kSmemLimit - kRest1 - 2 * kQBytes >= 6 * (int)kBlock ? 2 : 1;
+  // behind the ring: Q, then by row -lse to base 2, and the nodes that the row sees (in two words)
+  static constexpr int oLse = kQBuf * kQBytes;
+  static constexpr int oSees = oLse + 2 * kRows * 4;
+  static constexpr int oBars = oSees + 2 * 2 * kRows * 4;
+  static constexpr int kRest = kQBuf * kQBytes + kRest1;
   static constexpr int kFit = (kSmemLimit - kRest) / (int)kBlock;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static_assert(kStages >= 2, "a ring");
 };
 
 // What the roles go through: tiles t0 .. t1 - 1 of (request n, kv head h) with the rows of chunk c. `at`: the number of
-// tiles before t0 in the piece, each counted once; tile t's scores are in buffer (at + t - t0) % 2, whatever the chunk.
+// tiles before t0 in the piece, each counted once; tile t's scores are in buffer (at + t - t0) % kBufs, whatever the chunk.
 struct Seg {
   int n, h, c, t0, t1, len, ctx, at;
 };
@@ -119,11 +126,11 @@ struct Walk {
     }
     while (left > 0) {
       while (tiles == 0) tiles = tiles_of(a, ++n);  // the piece has places left, so a request with some follows
-      const int places = tiles + kUnitCost;
+      const int places = tiles + a.cost;
       int take = min(places - t, left);
-      if (a.chunks > 1) take = min(take, max(kUnitCost - t, 0) + kSub);
+      if (a.chunks > 1) take = min(take, max(a.cost - t, 0) + a.sub);
       const int ctx = __ldg(a.p.ctx + n);
-      cur = Seg{n, h, 0, max(t - kUnitCost, 0), t + take - kUnitCost, ctx + a.p.P, ctx, at};
+      cur = Seg{n, h, 0, max(t - a.cost, 0), t + take - a.cost, ctx + a.p.P, ctx, at};
       left -= take;
       t += take;
       if (t == places) {
@@ -152,86 +159,130 @@ __device__ __forceinline__ void loaded(uint32_t (&u)[kN]) {
   for (int i = 0; i < kN; ++i) asm volatile("" : "+r"(u[i]));
 }
 
-// The query rows of a segment into buffer qb, as rows of the MMAs' second operand, with their factors and what they see.
-// A warp has up to 32 rows in a row, a lane what goes by the row. The rows are copied past the registers, all of them on
-// their way at once. An E4M3 cache's are then taken apart into their two terms in place: a row's 2 D bytes are its own.
+// The query rows of a segment, number `seg` of the piece, as rows of the MMAs' second operand, with their constants. Rows
+// that add nothing (without a finite lse) are left out: the others move up. `shares` warps have an equal part of the rows
+// each, a lane what goes by the row. The rows are copied past the registers, all of them on their way at once. An E4M3
+// cache's are then taken apart into their two terms in place (a row's 2 D bytes are its own), by one power of two for all
+// of them: what a score is off by counts as such, whatever the row's size.
 template <int D, bool kE4m3, int kRows>
-__device__ __forceinline__ void load_queries(const Args& a, const Seg& s, unsigned char* rest, Bars* B, int qb, int share) {
+__device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned char* rest, Bars* B, int seg, int share,
+                                          int shares) {
   using C = Cfg<D, kE4m3, kRows>;
-  static_assert(kRows <= 32 * kQueryWarps, "a lane per row");
   const ScoreArgs& p = a.p;
-  const int lane = threadIdx.x & 31, rp = (a.rows + 15) / 16 * 16, per = rp / kQueryWarps;
-  const uint32_t q_block = rp * 128;
-  const int r0 = s.c * a.rows, all = min(a.rows, p.P * p.G - r0);
-  unsigned char* q_s = rest + qb * C::kQBytes;
-  float* fac = reinterpret_cast<float*>(rest + C::oFac) + qb * kRows;
-  float* lse = reinterpret_cast<float*>(rest + C::oLse) + qb * kRows;
-  uint32_t* sees = reinterpret_cast<uint32_t*>(rest + C::oSees) + qb * 3 * kRows;
-  const int first = share * per, mine = first + lane;
-  const bool have = lane < per && mine < all;
-  const int j = (r0 + mine) / p.G;
-  const size_t row = ((size_t)s.n * p.P + j) * p.Hq + s.h * p.G + (r0 + mine) % p.G;
-  const size_t off = have ? row * D : 0;
+  const int lane = threadIdx.x & 31, rp = (a.rows + 15) / 16 * 16;
+  const uint32_t q_block = rp * 128, lower = (1u << lane) - 1u;
+  const int r0 = s.c * a.rows, all = min(a.rows, p.P * p.G - r0), b = seg & 1;
+  const int per = (all + shares - 1) / shares;
+  unsigned char* q_s = rest + seg % C::kQBuf * C::kQBytes;
+  float* lse = reinterpret_cast<float*>(rest + C::oLse) + b * kRows;
+  uint32_t* sees = reinterpret_cast<uint32_t*>(rest + C::oSees) + b * 2 * kRows;
+  const int first = min(all, share * per), end = min(all, first + per);
+  const float* lse_g = p.lse + (size_t)s.n * p.P * p.Hq + s.h * p.G;
+  const uint16_t* q_g = p.q + ((size_t)s.n * p.P * p.Hq + s.h * p.G) * D;
+  auto row_of = [&](int r) {  // from the first position's first row of this kv head
+    const int j = (r0 + r) / p.G;
+    return j * p.Hq + (r0 + r - j * p.G);
+  };
+  // every 32 rows' lse up to this warp's last, at once: a lane has the rows g + lane
+  constexpr int kMost = (kRows + 31) / 32;
+  float l_all[kMost];
+#pragma unroll
+  for (int g = 0; g < kMost; ++g) {
+    const int r = 32 * g + lane;
+    l_all[g] = r < end ? __ldg(lse_g + row_of(r)) : INFINITY;
+  }
   // piece `lane` (16 bytes) of row r: where it lies, bf16 values
-  auto piece = [&](int r) { return q_s + (lane >> 3) * q_block + swz(r, (lane & 7) * 16); };
-  for (int i = 0; i < per; ++i) {
-    const size_t o = __shfl_sync(0xffffffffu, off, i);
-    const int r = first + i;
-    if (lane < D / 8) {
-      const uint32_t bytes = r < all ? 16u : 0u;  // zeros behind the last row
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(piece(r))), "l"(p.q + o + lane * 8), "r"(bytes)
+  const uint32_t q_a = smem_u32(q_s) + (lane >> 3) * q_block, piece_at = lane & 7;
+  auto piece = [&](int r) { return q_a + r * 128 + ((piece_at ^ (r & 7)) << 4); };
+  auto copy = [&](int r, int from) {
+    if (lane < D / 8)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(piece(r)), "l"(q_g + (size_t)from * D + lane * 8)
                    : "memory");
+  };
+  int at = 0;  // live rows so far
+  int begin = 0;  // of those before this warp's
+#pragma unroll
+  for (int g = 0; g < kMost; ++g) {
+    if (32 * g >= end) break;
+    const int r = 32 * g + lane;
+    const float l = l_all[g];
+    const uint32_t finite = __ballot_sync(0xffffffffu, fabsf(l) < INFINITY);
+    const uint32_t own = first <= 32 * g ? ~0u : first >= 32 * g + 32 ? 0u : ~0u << (first - 32 * g);
+    const uint32_t live = finite & own;
+    at += __popc(finite & ~own);
+    begin += __popc(finite & ~own);
+    const int from = row_of(r);
+    int to = at;
+#pragma unroll 4
+    for (uint32_t left = live; left; left &= left - 1) copy(to++, __shfl_sync(0xffffffffu, from, __ffs(left) - 1));
+    if (live >> lane & 1) {
+      const int mine = at + __popc(live & lower), j = (r0 + r) / p.G;
+      uint64_t m = p.mask ? __ldg(p.mask + (size_t)s.n * p.P + j) : j == 63 ? ~0ull : (2ull << j) - 1;
+      m &= ~0ull >> (64 - p.P);
+      lse[mine] = -l * kLog2e;
+      sees[mine] = (uint32_t)m;
+      sees[kRows + mine] = (uint32_t)(m >> 32);
     }
+    at += __popc(live);
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
-  const float l = have ? __ldg(p.lse + row) : INFINITY;
-  uint64_t m = 0;
-  if (have) m = p.mask ? __ldg(p.mask + (size_t)s.n * p.P + j) : j == 63 ? ~0ull : (2ull << j) - 1;
-  const bool live = fabsf(l) < INFINITY;  // a row without a finite sum adds nothing
-  m = live ? m & ~0ull >> (64 - p.P) : 0ull;
-  if (lane < per) {
-    lse[mine] = live ? -l * kLog2e : -INFINITY;
-    sees[mine] = (uint32_t)m;
-    sees[kRows + mine] = (uint32_t)(m >> 32);
-    sees[2 * kRows + mine] = live;
-  }
-  const bool dead = __any_sync(0xffffffffu, have && !live);
-  if (lane == 0) B->dead[qb][share] = dead;
+  if (share == shares - 1 && lane == 0) B->rows[b] = at;
   asm volatile("cp.async.wait_group 0;" ::: "memory");
-  if constexpr (kE4m3) {
-    const float f0 = p.scale * kLog2e;
+  const float f0 = p.scale * kLog2e;
+  if constexpr (!kE4m3) {
+    if (share == 0 && lane == 0) B->factor[b] = f0;
+  } else {
     __syncwarp();
-#pragma unroll 4
-    for (int i = 0; i < per; ++i) {
-      const int r = first + i;
+    auto values = [&](int r) {
       uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-      if (lane < D / 8) raw = *reinterpret_cast<const uint4*>(piece(r));
-      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-      float x[8], most = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[2 * e] = __uint_as_float(w[e] << 16);
-        x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      if (lane < D / 8)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(raw.x), "=r"(raw.y), "=r"(raw.z), "=r"(raw.w) : "r"(piece(r)));
+      return raw;
+    };
+    // the largest magnitude of all loaders' rows, as the bits of a bf16
+    auto largest = [](const uint4& w) {
+      const uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+      return max(m & 0xffffu, m >> 16);
+    };
+    constexpr uint32_t kInf = 0x7f80u;
+    uint32_t most = 0;
+#pragma unroll 4
+    for (int r = begin; r < at; ++r) most = max(most, largest(values(r)));
+    if (__any_sync(0xffffffffu, most >= kInf)) {  // rows with values that are no numbers have no scores, and no say in it
+      most = 0;
+      for (int r = begin; r < at; ++r) {
+        const uint32_t m = largest(values(r));
+        if (__any_sync(0xffffffffu, m >= kInf)) {
+          if (lane == 0) lse[r] = __uint_as_float(0x7fffffffu);
+        } else {
+          most = max(most, m);
+        }
       }
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) B->most[share] = most;
+    asm volatile("bar.sync 1, %0;" ::"r"(32 * shares) : "memory");
+    most = __reduce_max_sync(0xffffffffu, lane < shares ? B->most[lane] : 0u);
+    asm volatile("bar.sync 1, %0;" ::"r"(32 * shares) : "memory");  // before the next segment's
+    // a power of two that takes the largest value below 256
+    const int up = most == 0 ? 0 : min(134 - (int)(most >> 7), 120);
+    const float by = __uint_as_float((uint32_t)(up + 127) << 23);
+    if (share == 0 && lane == 0) B->factor[b] = f0 * __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll 2
+    for (int r = begin; r < at; ++r) {
+      const uint4 raw = values(r);
+      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+      uint32_t t[4];  // first terms of two values, then their second ones
 #pragma unroll
-      for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(x[e]));
-      most = tree_attn::warp_max(most);
-      // a power of two that takes the largest value below 256; a row with an infinity has no scores
-      const int ex = (int)(__float_as_uint(most) >> 23) - 127;
-      const int up = most == 0.f ? 0 : min(7 - ex, 120);
-      const float by = __uint_as_float((uint32_t)(up + 127) << 23);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= by;
-      uint2 one, two;
-      tree_attn::two_terms(x, one, two);
+      for (int e = 0; e < 4; ++e)
+        t[e] = tree_attn::two_terms(make_float2(__uint_as_float(w[e] << 16) * by, __uint_as_float(w[e] & 0xffff0000u) * by));
       __syncwarp();
       if (lane < D / 8) {
         unsigned char* blk = q_s + (lane >> 4) * q_block + swz(r, (lane & 15) * 8);
-        *reinterpret_cast<uint2*>(blk) = one;
-        *reinterpret_cast<uint2*>(blk + C::kBlk * q_block) = two;
+        *reinterpret_cast<uint2*>(blk) = make_uint2(__byte_perm(t[0], t[1], 0x5410), __byte_perm(t[2], t[3], 0x5410));
+        *reinterpret_cast<uint2*>(blk + C::kBlk * q_block) =
+            make_uint2(__byte_perm(t[0], t[1], 0x7632), __byte_perm(t[2], t[3], 0x7632));
       }
-      if (lane == 0)
-        fac[r] = ex == 128 ? __uint_as_float(0x7fffffffu) : f0 * __uint_as_float((uint32_t)(127 - up) << 23);
     }
   }
 }
@@ -251,13 +302,14 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
       mbar_init(&B->full[i], 1);
       mbar_init(&B->empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::kBufs; ++i) {
       mbar_init(&B->s_full[i], 1);
       mbar_init(&B->s_empty[i], 4);
     }
-    for (int i = 0; i < kQBuf; ++i) {
-      mbar_init(&B->q_full[i], kQueryWarps);
-      mbar_init(&B->q_empty[i], 1 + 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B->q_full[i], C::kQBuf == 1 ? kLoaders : kQueryWarps);
+      mbar_init(&B->q_empty[i], 1);
+      mbar_init(&B->r_empty[i], 4 * kGroups);
     }
     mbar_init(&B->drain, 1);
     B->abort = 0;
@@ -273,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
     int why = 0;
     for (int n = n0; n < n1; ++n) {
       const int tiles = tiles_of(a, n, &why);
-      mine += tiles + (tiles > 0 ? kUnitCost : 0);
+      mine += tiles + (tiles > 0 ? a.cost : 0);
     }
     if (why && blockIdx.x == 0) report(p.dev_err, why);
     long long upto = mine;
@@ -296,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
     if (blockIdx.x < ctas && before * c.Hkv <= lo && lo < (before + mine) * c.Hkv) {
       long long at = before * c.Hkv;
       for (int n = n0; n < n1; ++n) {
-        const int tiles = tiles_of(a, n), places = tiles + (tiles > 0 ? kUnitCost : 0);
+        const int tiles = tiles_of(a, n), places = tiles + (tiles > 0 ? a.cost : 0);
         const long long here = (long long)places * c.Hkv;
         if (lo < at + here) {
           B->plan = Plan{lo, (int)(hi - lo), n, (int)((lo - at) / places), (int)((lo - at) % places)};
@@ -313,36 +365,57 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
   const Plan plan = B->plan;
   const uint32_t tmem = B->tmem;
   int* abort = &B->abort;
+  // The first segment's query rows are loaded by all warps but the copies' and the MMAs', and so are all, where there is
+  // room for one segment's; else the later ones by the query warps, while the segment before is worked on. (By four warps
+  // of their own, 192 rows of an E4M3 cache took 12 us.)
+  auto load_segment = [&](const Seg& s, int seg, int share) {
+    const int qb = seg % C::kQBuf;
+    bool ok = wait(&B->q_empty[qb], ((seg / C::kQBuf) & 1) ^ 1, abort);
+    if (C::kQBuf == 2) ok = ok && wait(&B->r_empty[seg & 1], ((seg >> 1) & 1) ^ 1, abort);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    const bool together = C::kQBuf == 1 || seg == 0;
+    load_queries<D, kE4m3, kRows>(a, s, rest, B, seg, together ? share : share - 4 * kGroups, together ? kLoaders : kQueryWarps);
+    umma::fence_proxy_async_smem();
+    if (C::kQBuf == 2 && seg == 0) asm volatile("bar.sync 2, %0;" ::"n"(32 * kLoaders) : "memory");
+    else __syncwarp();
+    if ((C::kQBuf == 1 || share >= 4 * kGroups) && lane == 0) arrive(&B->q_full[seg & 1]);
+    return true;
+  };
 
   if (warp == kCopyWarp) {
     // ------------------------------------------------------------ copies
-    const int boxes = kTile / a.box, total_rows = c.slots * c.Hkv;
+    // The pages of `span` tiles are loaded at once, a lane per box, and the next tiles' before these are copied.
+    const int boxes = kTile / a.box, total_rows = c.slots * c.Hkv, span = 32 / boxes;
     int st = 0, phase = 1, issued = 0;
     bool ok = true;
     Walk walk(a, plan);
     Seg s;
-    while (ok && walk.next(a, s)) {
-      const int32_t* table = p.table + (size_t)s.n * p.max_pages;
-      auto row_of = [&](int t) {  // first row of this lane's box; behind the last token: rows that read as zeros
-        const int tok = t * kTile + lane * a.box;
-        if (lane >= boxes || tok >= s.len) return total_rows;
-        const int page = __ldg(table + tok / c.page);
-        if (page < 0 || page >= c.pages) return total_rows;
-        return (page * c.Hkv + s.h) * c.page + tok % c.page;
-      };
-      int row = row_of(s.t0);
-      for (int t = s.t0; t < s.t1 && ok; ++t) {
-        const int next = t + 1 < s.t1 ? row_of(t + 1) : 0;
-        for (int b = 0; b < C::kBlk; ++b) {
-          ok = __all_sync(0xffffffffu, ok && wait(&B->empty[st], phase, abort));
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&B->full[st], kBlock);
-          __syncwarp();
-          if (lane < boxes) tma_load_2d(smem + st * kBlock + lane * a.box * 128, &tmk, b * (kE4m3 ? 128 : 64), row, &B->full[st]);
-          ++issued;
-          if (++st == C::kStages) st = 0, phase ^= 1;
+    bool more = walk.next(a, s);
+    auto load_page = [&](const Seg& x, int t) {  // of box `lane` from tile t on; -1 behind the last token
+      const long long tok = (long long)t * kTile + lane * a.box;
+      return tok < x.len && t + lane / boxes < x.t1 ? __ldg(p.table + (size_t)x.n * p.max_pages + tok / c.page) : -1;
+    };
+    int page = more ? load_page(s, s.t0) : -1;
+    while (ok && more) {
+      const Seg cur = s;
+      more = walk.next(a, s);
+      for (int t0 = cur.t0; t0 < cur.t1 && ok; t0 += span) {
+        // the first row of this lane's box; a page out of the pool and behind the last token: rows that read as zeros
+        const int tok = t0 * kTile + lane * a.box;
+        const int row = page < 0 || page >= c.pages ? total_rows : (page * c.Hkv + cur.h) * c.page + tok % c.page;
+        page = t0 + span < cur.t1 ? load_page(cur, t0 + span) : more ? load_page(s, s.t0) : -1;
+        for (int t = t0; t < min(cur.t1, t0 + span) && ok; ++t) {
+          const int r = __shfl_sync(0xffffffffu, row, (t - t0) * boxes + lane % boxes);
+          for (int b = 0; b < C::kBlk; ++b) {
+            ok = __all_sync(0xffffffffu, ok && wait(&B->empty[st], phase, abort));
+            if (!ok) break;
+            if (elect_one()) mbar_arrive_expect_tx(&B->full[st], kBlock);
+            __syncwarp();
+            if (lane < boxes) tma_load_2d(smem + st * kBlock + lane * a.box * 128, &tmk, b * (kE4m3 ? 128 : 64), r, &B->full[st]);
+            ++issued;
+            if (++st == C::kStages) st = 0, phase ^= 1;
+          }
         }
-        row = next;
       }
     }
     // copies in flight land before the CTA may leave
@@ -354,9 +427,9 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
     const int rp = (a.rows + 15) / 16 * 16;
     const uint32_t q_block = rp * 128;
     constexpr uint32_t kKind = kE4m3 ? umma::kKindF8 : umma::kKindF16, kType = kE4m3 ? umma::kE4M3 : umma::kBF16;
-    const uint32_t id = umma::idesc(kType, false, false, kTile, rp);
     const uint32_t ring = smem_u32(smem), sQ = smem_u32(rest);
-    int st = 0, phase = 0, seg = 0, used[2] = {0, 0};
+    int st = 0, phase = 0, seg = 0;
+    uint32_t used = 0;  // bit b: parity of buffer b's uses
     bool ok = true;
     auto wait_all = [&](uint64_t* bar, uint32_t parity) {
       ok = ok && wait(bar, parity, abort);
@@ -366,12 +439,14 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
     Walk walk(a, plan);
     Seg s;
     while (ok && walk.next(a, s)) {
-      const int qb = seg % kQBuf;
-      if (!wait_all(&B->q_full[qb], (seg / kQBuf) & 1)) break;
+      const int qb = seg % C::kQBuf;
+      if (!wait_all(&B->q_full[seg & 1], (seg >> 1) & 1)) break;
+      const int cols = max(16, (*(volatile int*)&B->rows[seg & 1] + 15) / 16 * 16);
+      const uint32_t id = umma::idesc(kType, false, false, kTile, cols);
       for (int t = s.t0; t < s.t1 && ok; ++t) {
-        const int b = (s.at + t - s.t0) & 1;
-        const int use = b ? used[1]++ : used[0]++;
-        if (!wait_all(&B->s_empty[b], (use & 1) ^ 1)) break;
+        const int b = (s.at + t - s.t0) % C::kBufs;
+        if (!wait_all(&B->s_empty[b], (used >> b & 1) ^ 1)) break;
+        used ^= 1u << b;
         for (int kb = 0; kb < C::kBlk; ++kb) {
           if (!wait_all(&B->full[st], phase)) break;
           umma::fence_after_sync();
@@ -407,26 +482,19 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
     Seg s;
     int seg = 0;
     while (walk.next(a, s)) {
-      const int qb = seg % kQBuf;
-      if (!__all_sync(0xffffffffu, wait(&B->q_empty[qb], ((seg / kQBuf) & 1) ^ 1, abort))) break;
-      load_queries<D, kE4m3, kRows>(a, s, rest, B, qb, warp - kQueryWarp);
-      umma::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) arrive(&B->q_full[qb]);
+      if (!load_segment(s, seg, 4 * kGroups + warp - kQueryWarp)) break;
       ++seg;
     }
   } else {
     // ------------------------------------------------------------ weights: thread = token
     const int wg = warp >> 2, w4 = warp & 3, mine = 32 * w4 + lane;
-    const float* fac_s = reinterpret_cast<const float*>(rest + C::oFac);
     const float* lse_s = reinterpret_cast<const float*>(rest + C::oLse);
     const uint32_t* sees_s = reinterpret_cast<const uint32_t*>(rest + C::oSees);
     Walk walk(a, plan);
     Seg s;
     int seg = 0, used = 0;
     while (walk.next(a, s)) {
-      const int qb = seg % kQBuf;
-      const int rows = min(a.rows, p.P * p.G - s.c * a.rows);
+      const int rb = seg & 1;
       const int32_t* table = p.table + (size_t)s.n * p.max_pages;
       const bool fresh = p.init && !p.init[s.n];
       float* out = p.score + ((size_t)__ldg(p.slot + s.n) * c.Hkv + s.h) * p.max_tokens;
@@ -446,97 +514,114 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
         if constexpr (kE4m3) ks = __ldg(c.k_scale + ((size_t)page * c.Hkv + s.h) * c.page + tok % c.page);
         if (old && (again || tok < s.ctx)) w = out[tok];
       };
-      int t = s.t0 + ((s.at & 1) == wg ? 0 : 1);
-      int page = load_page(t), next_page = load_page(t + 2);
+      int t = s.t0 + (wg - s.at) % C::kBufs;
+      if (t < s.t0) t += C::kBufs;
+      int page = load_page(t), next_page = load_page(t + C::kBufs);
       load_token(t, page, key_scale, before);
-      wait_warp(&B->q_full[qb], (seg / kQBuf) & 1, abort);
-      const volatile int* d4 = B->dead[qb];
-      const bool dead = (d4[0] | d4[1] | d4[2] | d4[3]) != 0;
-      const float* fac = fac_s + qb * kRows;
-      const float* lse = lse_s + qb * kRows;
-      const uint32_t* sees = sees_s + qb * 3 * kRows;
-      const float f0 = p.scale * kLog2e;
-      for (; t < s.t1; t += 2, ++used) {
+      if (C::kQBuf == 1 || seg == 0)
+        if (!load_segment(s, seg, warp)) break;
+      wait_warp(&B->q_full[rb], (seg >> 1) & 1, abort);
+      const int rows = *(volatile int*)&B->rows[rb];
+      const float f0 = *(volatile float*)&B->factor[rb];
+      const float* lse = lse_s + rb * kRows;
+      const uint32_t* sees = sees_s + rb * 2 * kRows;
+      for (; t < s.t1; t += C::kBufs, ++used) {
         const int this_page = page;
         const float ks = key_scale, w = before;
         page = next_page;
-        next_page = load_page(t + 4);
-        load_token(t + 2, page, key_scale, before);
+        next_page = load_page(t + 2 * C::kBufs);
+        load_token(t + C::kBufs, page, key_scale, before);
         wait_warp(&B->s_full[wg], used & 1, abort);
         umma::fence_after_sync();
         const uint32_t ts = umma::taddr(tmem, 32 * w4, wg * kRows);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // The weights of eight rows' scores. kMasked: not of rows that are left out or behind the last, nor of nodes that
-        // a row does not see: by selection, whatever the score is.
+        const float f = kE4m3 ? f0 * ks : f0;
         const int node = t * kTile + mine - s.ctx;
-        const uint32_t* sees_t = sees + (node < 0 ? 2 : node < 32 ? 0 : 1) * kRows;
-        const int bit = node < 0 ? 0 : node & 31;
-        auto weights = [&](const uint32_t* u, int r0, auto masked) {
-#pragma unroll
-          for (int i = 0; i < 8; i += 4) {
-            const int r = r0 + i;
-            float4 f = make_float4(f0, f0, f0, f0);
-            if constexpr (kE4m3) f = *reinterpret_cast<const float4*>(fac + r);
-            const float4 l = *reinterpret_cast<const float4*>(lse + r);
-            float2 x[2] = {make_float2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])),
-                           make_float2(__uint_as_float(u[i + 2]), __uint_as_float(u[i + 3]))};
-            if constexpr (kE4m3) {
-              x[0] = __fmul2_rn(x[0], make_float2(ks, ks));
-              x[1] = __fmul2_rn(x[1], make_float2(ks, ks));
-            }
-            x[0] = __ffma2_rn(x[0], make_float2(f.x, f.y), make_float2(l.x, l.y));
-            x[1] = __ffma2_rn(x[1], make_float2(f.z, f.w), make_float2(l.z, l.w));
-            float e[4] = {ex2(x[0].x), ex2(x[0].y), ex2(x[1].x), ex2(x[1].y)};
-            if constexpr (decltype(masked)::value) {
-              const uint4 w = *reinterpret_cast<const uint4*>(sees_t + r);
-              e[0] = (w.x >> bit) & 1u ? e[0] : 0.f;
-              e[1] = (w.y >> bit) & 1u ? e[1] : 0.f;
-              e[2] = (w.z >> bit) & 1u ? e[2] : 0.f;
-              e[3] = (w.w >> bit) & 1u ? e[3] : 0.f;
-            }
-            sum[0] = __fadd2_rn(sum[0], make_float2(e[0], e[1]));
-            sum[1] = __fadd2_rn(sum[1], make_float2(e[2], e[3]));
-          }
-        };
+        const bool masked = (t + 1) * kTile > s.ctx;
         constexpr int kN = kRows < 32 ? 16 : 32;  // rows at a time
-        const bool masked = dead || (t + 1) * kTile > s.ctx;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
         auto load = [&](int r0, uint32_t (&u)[kN]) {
           if constexpr (kN == 32) umma::ld32_nowait(ts + r0, u);
           else umma::ld16_nowait(ts + r0, u);
         };
-        auto compute = [&](int r0, const uint32_t (&u)[kN]) {
+        auto constants = [&](int r0, float4 (&l)[kN / 4]) {
+#pragma unroll
+          for (int i = 0; i < kN / 4; ++i) l[i] = *reinterpret_cast<const float4*>(lse + r0 + 4 * i);
+        };
+        // The weights of four rows' scores. (Two at a time in packed operations, 32 rows took 443 cycles of a warp alone,
+        // 198 like this; the exponentials' pipe is busy for 128.)
+        auto weights = [&](const uint32_t* u, const float4& l, float (&e)[4]) {
+          e[0] = ex2(fmaf(__uint_as_float(u[0]), f, l.x));
+          e[1] = ex2(fmaf(__uint_as_float(u[1]), f, l.y));
+          e[2] = ex2(fmaf(__uint_as_float(u[2]), f, l.z));
+          e[3] = ex2(fmaf(__uint_as_float(u[3]), f, l.w));
+        };
+        auto add = [&](const float (&e)[4]) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) sum[y] += e[y];
+        };
+        auto compute = [&](int r0, const uint32_t (&u)[kN], const float4 (&l)[kN / 4]) {
           if (!masked && r0 + kN <= rows) {  // no branch inside: the chains of all rows run side by side
 #pragma unroll
-            for (int i = 0; i < kN; i += 8) weights(u + i, r0 + i, std::false_type());
+            for (int i = 0; i < kN; i += 4) {
+              float e[4];
+              weights(u + i, l[i / 4], e);
+              add(e);
+            }
           } else {
+            // rows behind the last and nodes that a row does not see: by selection, whatever the score is
 #pragma unroll
             for (int i = 0; i < kN; i += 8)
-              if (r0 + i < rows) weights(u + i, r0 + i, std::true_type());
+              if (r0 + i < rows) {
+#pragma unroll
+                for (int y0 = i; y0 < i + 8; y0 += 4) {
+                  float e[4];
+                  weights(u + y0, l[y0 / 4], e);
+                  const int r = r0 + y0;
+                  if (masked && node >= 0) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(sees + (node < 32 ? 0 : kRows) + r);
+                    const int bit = node & 31;
+                    e[0] = (w.x >> bit) & 1u ? e[0] : 0.f;
+                    e[1] = (w.y >> bit) & 1u ? e[1] : 0.f;
+                    e[2] = (w.z >> bit) & 1u ? e[2] : 0.f;
+                    e[3] = (w.w >> bit) & 1u ? e[3] : 0.f;
+                  }
+#pragma unroll
+                  for (int y = 0; y < 4; ++y) e[y] = r + y < rows ? e[y] : 0.f;
+                  add(e);
+                }
+              }
           }
         };
         uint32_t u[kN], v[kN];  // one is on its way while the other is worked on
+        float4 l[kN / 4];
         load(0, u);
+        constants(0, l);
 #pragma unroll 1
         for (int r0 = 0; r0 < rows; r0 += 2 * kN) {
+          const int r1 = r0 + kN, r2 = r0 + 2 * kN;
+          const bool more = kRows > kN && r1 < rows;
           loaded(u);
-          if (kRows > kN && r0 + kN < rows) load(r0 + kN, v);
-          compute(r0, u);
-          if (kRows > kN && r0 + kN < rows) {
+          if (more) load(r1, v);
+          compute(r0, u, l);
+          if (more) {
+            constants(r1, l);
             loaded(v);
-            if (r0 + 2 * kN < rows) load(r0 + 2 * kN, u);
-            compute(r0 + kN, v);
+            if (r2 < rows) load(r2, u);
+            compute(r1, v, l);
+            if (r2 < rows) constants(r2, l);
           }
         }
+        umma::wait_ld();  // of the first rows, where there are none
         umma::fence_before_sync();
         __syncwarp();
         if (lane == 0) arrive(&B->s_empty[wg]);
         if (t * kTile + mine < s.len && !*(volatile int*)abort) {
           if (this_page < 0 || this_page >= c.pages) report(p.dev_err, GDN_DEVERR_SLOT);
-          else out[t * kTile + mine] = fmaf(w, decay, (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
+          else out[t * kTile + mine] = fmaf(w, decay, (sum[0] + sum[1]) + (sum[2] + sum[3]));
         }
       }
       __syncwarp();
-      if (lane == 0) arrive(&B->q_empty[qb]);
+      if (lane == 0) arrive(&B->r_empty[rb]);
       ++seg;
     }
   }
@@ -570,7 +655,8 @@ template <int D, bool kE4m3>
 cudaError_t launch_dim(const Args& a, const CUtensorMap& tmk, int grid, cudaStream_t stream) {
   if (a.rows <= 16) return launch_rows<D, kE4m3, 16>(a, tmk, grid, stream);
   if (a.rows <= 64) return launch_rows<D, kE4m3, 64>(a, tmk, grid, stream);
-  return launch_rows<D, kE4m3, 128>(a, tmk, grid, stream);
+  if (a.rows <= 128) return launch_rows<D, kE4m3, 128>(a, tmk, grid, stream);
+  return launch_rows<D, kE4m3, 192>(a, tmk, grid, stream);
 }
 
 }  // namespace kv_score
@@ -588,6 +674,9 @@ cudaError_t launch_kv_score(const ScoreArgs& p, const KvArgs& c, cudaStream_t st
   a.rows = (all + a.chunks - 1) / a.chunks;
   a.chunks = (all + a.rows - 1) / a.rows;
   a.box = tree_attn::box_tokens(c.page);
+  // the wait for a unit's query rows: 8 x 32 rows on prompts of 1500 .. 32768 tokens 44 us with one tile, 41 with three
+  a.cost = all > 16 ? 3 : 1;
+  a.sub = kv_score::kSubBytes / (kv_score::kTile * p.D * (c.e4m3 ? 1 : 2));
   CUtensorMap tmk{};
   if (!tree_attn::encode_rows(&tmk, c.k, c, p.D, a.box)) return cudaErrorInvalidValue;
   if (p.D == 256) return c.e4m3 ? kv_score::launch_dim<256, true>(a, tmk, sms, stream)
