@@ -4,11 +4,10 @@
 // Two kernels, one after the other on the stream:
 //   select: per (request, kv head) the m-th largest weight by radix, 8 bits a pass from the top, and the indices of the
 //           kept tokens in ascending order. Weights that are equal at the border go to the lowest indices.
-//   move:   the kept tokens' keys, values, scales and weights to the front of the request's pages, or of other pages, in
-//           the order of the tokens. Kept token i has index kept[i] >= i, so in place a chunk of tokens is stored where
-//           only earlier chunks' tokens, or this one's, were read: a block takes its chunks in order and has read a
-//           chunk before it stores it. Blocks share no byte: a block has one head's keys, values or floats, or a slice of
-//           its rows.
+//   move:   the kept tokens' keys, values, scales and weights, in the order of the tokens, to other pages (copy_kernel) or
+//           to the front of the request's own (shift_kernel).
+#include <algorithm>
+
 #include "device.cuh"
 #include "launch.h"
 
@@ -18,9 +17,9 @@ namespace {
 
 // ---------------------------------------------------------------- select
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kCached = 16384;  // tokens of a CTA whose keys stay in shared memory
+constexpr int kFew = 256;  // weights at the border that are put in order all at once
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -60,13 +59,19 @@ __device__ __forceinline__ uint32_t key_of(float w) {
   return w != w ? 0u : u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-// kSplit CTAs, a cluster, have a (request, kv head), each an equal run of its tokens.
-template <int kSplit>
-__global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const EvictArgs p, const KvArgs c) {
-  extern __shared__ uint32_t keys[];                 // [kCached]
+// kSplit CTAs, a cluster, have a (request, kv head), each an equal run of its tokens; a thread has kHeld neighbours at a
+// time, and a CTA whose tokens are no more than its threads hold reads their weights once (else again, from L2, in each of
+// the passes). After two passes the weights with the border's upper 16 bits are a few, as a rule: those are put in order at
+// once, by counting for each the larger ones.
+// Bound by the chain of barriers and shared-memory atomics of the passes.
+template <int kSplit, int kHeld>
+__global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel(const EvictArgs p, const KvArgs c) {
+  constexpr int kBatch = kSelThreads * kHeld;
   __shared__ int hist[256 * 32];                     // [bin][lane]: no two lanes of a warp at one bank
-  __shared__ int bins[256], above_s[kSelWarps], scan_s[2][kSelWarps];
-  __shared__ int pick[2];                            // the bin of the m-th largest, and those above it
+  __shared__ int bins[256], above_s[8], scan_s[2][kSelWarps];
+  __shared__ int pick[3];                            // the bin of the m-th largest, those above it, and in it
+  __shared__ uint32_t few_s[kFew], own_few_s[kFew];
+  __shared__ int few, border_s[2];
   __shared__ int totals[2];                          // of this CTA: weights above the border, and equal to it
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
@@ -77,6 +82,39 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const EvictArgs 
   int why;
   const int m = kept_of(p, c, n, &why);
   const int len = __ldg(p.len + n);
+  // this CTA's run of tokens
+  const int per = ((max(len, 0) + kSplit - 1) / kSplit + kHeld - 1) / kHeld * kHeld;
+  const int lo = min(len, rank * per), count = min(len, lo + per) - lo;
+  const bool sift = m > 0 && m < len;
+  const float* w = p.score;
+  if (sift) w += ((size_t)__ldg(p.slot + n) * c.Hkv + h) * p.max_tokens + lo;
+  const int last = len - min(p.recent, max(len, 0));  // the first of the last tokens
+  const bool by_fours = (reinterpret_cast<uintptr_t>(w) & 15) == 0;
+  uint32_t key[kHeld];
+  int valid = 0;  // of this thread's tokens
+  auto load = [&](int base) {
+    const int i = base + tid * kHeld;
+    valid = max(0, min(kHeld, count - i));
+    float x[kHeld];
+    if (by_fours && valid == kHeld) {
+#pragma unroll
+      for (int j = 0; j < kHeld; j += 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(w + i + j));
+        x[j] = v.x;
+        x[j + 1] = v.y;
+        x[j + 2] = v.z;
+        x[j + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) x[j] = j < valid ? __ldg(w + i + j) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j)
+      key[j] = lo + i + j < p.sinks || lo + i + j >= last ? 0xffffffffu : key_of(x[j]);
+  };
+  const bool held = count <= kBatch;
+  if (sift && held) load(0);
   bool bad = false;
   if (m >= 0) {
     for (int i = tid; (long long)i * c.page < len; i += kSelThreads) {
@@ -96,31 +134,33 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const EvictArgs 
   }
   if (m <= 0 || why) return;  // the same in the whole cluster
   int* kept = p.kept + ((size_t)n * c.Hkv + h) * p.max_kept;
-  const int per = ((len + kSplit - 1) / kSplit + 31) / 32 * 32;
-  const int lo = min(len, rank * per), count = min(len, lo + per) - lo;
-  if (m == len) {
+  if (!sift) {
     for (int i = tid; i < count; i += kSelThreads) kept[lo + i] = lo + i;
     return;
   }
-  const float* w = p.score + ((size_t)__ldg(p.slot + n) * c.Hkv + h) * p.max_tokens + lo;
-  const int last = len - min(p.recent, len);  // the first of the last tokens
-  auto load_key = [&](int i) { return lo + i < p.sinks || lo + i >= last ? 0xffffffffu : key_of(__ldg(w + i)); };
-  const bool cached = count <= kCached;
-  if (cached) {
-#pragma unroll 4
-    for (int i = tid; i < count; i += kSelThreads) keys[i] = load_key(i);
-  }
-  auto key_at = [&](int i) { return cached ? keys[i] : load_key(i); };
+  auto batches = [&](auto work) {
+    if (held) {
+      work();
+    } else {
+      for (int base = 0; base < count; base += kBatch) {
+        load(base);
+        work();
+      }
+    }
+  };
 
   uint32_t border = 0;  // the key of the m-th largest, from the top
   int need = m;         // how many of those with its upper bits
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256 * 32; i += kSelThreads) hist[i] = 0;
+#pragma unroll
+    for (int i = 0; i < 256 * 32 / 4; i += kSelThreads) reinterpret_cast<int4*>(hist)[i + tid] = make_int4(0, 0, 0, 0);
     __syncthreads();
-    for (int i = tid; i < count; i += kSelThreads) {
-      const uint32_t k = key_at(i);
-      if (shift == 24 || (k >> (shift + 8)) == (border >> (shift + 8))) atomicAdd(&hist[(k >> shift & 255u) * 32 + lane], 1);
-    }
+    batches([&] {
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j)
+        if (j < valid && (shift == 24 || (key[j] >> (shift + 8)) == (border >> (shift + 8))))
+          atomicAdd(&hist[(key[j] >> shift & 255u) * 32 + lane], 1);
+    });
     __syncthreads();
     int mine = 0;
     if (tid < 256) {
@@ -150,32 +190,68 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const EvictArgs 
     if (tid < 256) {
       int above = upto - mine;
       for (int k = warp + 1; k < 8; ++k) above += above_s[k];
-      if (above < need && above + mine >= need) pick[0] = tid, pick[1] = above;
+      if (above < need && above + mine >= need) pick[0] = tid, pick[1] = above, pick[2] = mine;
     }
+    if (tid == 0) few = 0;
     if constexpr (kSplit > 1) cluster_sync();  // the bins have been read
     else __syncthreads();
     border |= (uint32_t)pick[0] << shift;
     need -= pick[1];
+    const int in_bin = pick[2];
+    if (shift > 0 && in_bin <= kFew) {
+      uint32_t* own = kSplit > 1 ? own_few_s : few_s;
+      batches([&] {
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j)
+          if (j < valid && key[j] >> shift == border >> shift) own[atomicAdd(&few, 1)] = key[j];
+      });
+      if constexpr (kSplit > 1) {  // every CTA's, one after the other
+        cluster_sync();
+        int at = 0;
+        for (int r = 0; r < kSplit; ++r) {
+          const int theirs = load_remote(&few, r);
+          if (tid < theirs) few_s[at + tid] = (uint32_t)load_remote(reinterpret_cast<const int*>(own_few_s) + tid, r);
+          at += theirs;
+        }
+      }
+      __syncthreads();
+      if (tid < in_bin) {
+        const uint32_t mine_key = few_s[tid];
+        int above = 0, same = 0;
+        for (int i = 0; i < in_bin; ++i) {
+          above += few_s[i] > mine_key;
+          same += few_s[i] == mine_key;
+        }
+        if (above < need && above + same >= need) border_s[0] = (int)mine_key, border_s[1] = need - above;
+      }
+      if constexpr (kSplit > 1) cluster_sync();  // the others' have been read
+      else __syncthreads();
+      border = (uint32_t)border_s[0];
+      need = border_s[1];
+      break;
+    }
     __syncthreads();  // `pick` and `above_s` have been read
   }
 
   // ---- the kept tokens' indices: those above the border, and the first `need` of those at it
-  int over = 0, equal = 0;
-  if (tid < 2) totals[tid] = 0;
-  __syncthreads();
-  for (int i = tid; i < count; i += kSelThreads) {
-    const uint32_t k = key_at(i);
-    over += k > border;
-    equal += k == border;
-  }
-  over = __reduce_add_sync(0xffffffffu, over);
-  equal = __reduce_add_sync(0xffffffffu, equal);
-  if (lane == 0) {
-    atomicAdd(&totals[0], over);
-    atomicAdd(&totals[1], equal);
-  }
   int over_before = 0, equal_before = 0;
-  if constexpr (kSplit > 1) {
+  if constexpr (kSplit > 1) {  // the numbers of both in the CTAs before this one
+    if (tid < 2) totals[tid] = 0;
+    __syncthreads();
+    int over = 0, equal = 0;
+    batches([&] {
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) {
+        over += j < valid && key[j] > border;
+        equal += j < valid && key[j] == border;
+      }
+    });
+    over = __reduce_add_sync(0xffffffffu, over);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    if (lane == 0) {
+      atomicAdd(&totals[0], over);
+      atomicAdd(&totals[1], equal);
+    }
     cluster_sync();
     for (int r = 0; r < rank; ++r) {
       over_before += load_remote(&totals[0], r);
@@ -183,28 +259,45 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const EvictArgs 
     }
     cluster_sync();  // no CTA leaves while another reads its shared memory
   }
-  for (int i0 = 0, buf = 0; i0 < count; i0 += kSelThreads, buf ^= 1) {
-    const int i = i0 + tid;
-    const uint32_t k = i < count ? key_at(i) : 0u;
-    const bool is_over = i < count && k > border, is_equal = i < count && k == border;
-    const uint32_t vo = __ballot_sync(0xffffffffu, is_over), ve = __ballot_sync(0xffffffffu, is_equal);
-    if (lane == 0) scan_s[buf][warp] = __popc(vo) | __popc(ve) << 16;
-    __syncthreads();
-    const int theirs = scan_s[buf][lane];  // of warp `lane`
-    int upto = theirs;
+  int buf = 0, base = 0;
+  batches([&] {
+    uint32_t is_over = 0, is_equal = 0;
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      is_over |= (j < valid && key[j] > border ? 1u : 0u) << j;
+      is_equal |= (j < valid && key[j] == border ? 1u : 0u) << j;
+    }
+    const int mine = __popc(is_over) | __popc(is_equal) << 16;  // no more than kBatch of each
+    int upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, upto, d);
       if (lane >= d) upto += o;
     }
-    const int before = __shfl_sync(0xffffffffu, upto - theirs, warp), all = __shfl_sync(0xffffffffu, upto, 31);
-    const uint32_t lower = (1u << lane) - 1u;
-    const int o = over_before + (before & 0xffff) + __popc(vo & lower);
-    const int e = equal_before + (before >> 16) + __popc(ve & lower);
-    if (is_over || (is_equal && e < need)) kept[o + min(e, need)] = lo + i;
+    if (lane == 31) scan_s[buf][warp] = upto;
+    __syncthreads();
+    const int theirs = lane < kSelWarps ? scan_s[buf][lane] : 0;
+    int sums = theirs;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, sums, d);
+      if (lane >= d) sums += o;
+    }
+    const int before = __shfl_sync(0xffffffffu, sums - theirs, warp) + upto - mine, all = __shfl_sync(0xffffffffu, sums, 31);
+    int o = over_before + (before & 0xffff), e = equal_before + (before >> 16);
+    const int i = lo + base + tid * kHeld;
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      const bool eq = is_equal >> j & 1, ov = is_over >> j & 1;
+      if (ov || (eq && e < need)) kept[o + min(e, need)] = i + j;
+      o += ov;
+      e += eq;
+    }
     over_before += all & 0xffff;
     equal_before += all >> 16;
-  }
+    base += kBatch;
+    buf ^= 1;
+  });
 }
 
 // ---------------------------------------------------------------- move
@@ -212,30 +305,194 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const EvictArgs 
 constexpr int kMoveThreads = 512;
 constexpr int kUnroll = 8;
 
-// Kept tokens [first, m) of one head: `lanes` threads a token, each with one T; chunks of kUnroll tokens a thread. `at`
-// gives the place of a token (page row or index) and thread, in units of T.
-template <typename T, typename From, typename To>
-__device__ __forceinline__ void move_rows(int first, int m, int lanes, const int* kept, From from, To to) {
+// Rows of the pool: of the page's first head and token, and of a token.
+struct Rows {
+  const int32_t* table;
+  int h, shift;  // shift: the page's tokens as a power of two, or -1
+  __device__ __forceinline__ int at(const KvArgs& c, int i) const {
+    const int k = shift >= 0 ? i >> shift : i / c.page;
+    return (__ldg(table + k) * c.Hkv + h) * c.page + (i - k * c.page);
+  }
+};
+
+// To other pages: nothing that is read is written, so the kept tokens of all (request, kv head) units stand in one line of
+// segments, cut into equal pieces, one per block. A segment is kUnroll pieces of 16 bytes a thread, of keys and values;
+// where its tokens come from and go to is found once per token, a segment ahead, in shared memory.
+// Bound by HBM: its reads and writes in turn, 64 KB on their way in each of two blocks an SM.
+template <int kRowBytes>
+__global__ void __launch_bounds__(kMoveThreads, 2) copy_kernel(const EvictArgs p, const KvArgs c, int shift) {
+  constexpr int kPieces = kRowBytes / 16, kTokens = kMoveThreads * kUnroll / (2 * kPieces);
+  static_assert(kTokens <= kMoveThreads, "a thread per token");
+  __shared__ int2 place[2][kTokens];  // rows of the pool: from, to
+  __shared__ long long warp_total[kMoveThreads / 32];
+  __shared__ struct {
+    long long left;
+    int n, h, s;
+  } plan;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto tokens_of = [&](int n) {
+    const int m = __ldg(p.len + n) < 0 || __ldg(p.slot + n) < 0 ? 0 : __ldg(p.new_len + n);
+    return max(m, 0);
+  };
+  auto segments_of = [&](int n) { return (tokens_of(n) + kTokens - 1) / kTokens; };
+  // ---- this block's piece: a scan over the requests' segments
+  {
+    if (tid == 0) plan.left = 0;
+    const int per = (p.N + kMoveThreads - 1) / kMoveThreads, n0 = min(p.N, tid * per), n1 = min(p.N, n0 + per);
+    long long mine = 0;
+    for (int n = n0; n < n1; ++n) mine += segments_of(n);
+    long long upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += o;
+    }
+    if (lane == 31) warp_total[warp] = upto;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int w = 0; w < kMoveThreads / 32; ++w) {
+      if (w < warp) before += warp_total[w];
+      total += warp_total[w];
+    }
+    before = (before + upto - mine) * c.Hkv;
+    total *= c.Hkv;
+    const long long lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+    if (hi > lo && before <= lo && lo < before + mine * c.Hkv) {
+      long long at = before;
+      for (int n = n0; n < n1; ++n) {
+        const long long segs = segments_of(n), here = segs * c.Hkv;
+        if (lo < at + here) {
+          plan.left = hi - lo;
+          plan.n = n;
+          plan.h = (int)((lo - at) / segs);
+          plan.s = (int)((lo - at) % segs);
+          break;
+        }
+        at += here;
+      }
+    }
+    __syncthreads();
+  }
+  long long left = plan.left;
+  if (left == 0) return;
+  // the segment whose places are looked up: request, head, first token, and the request's tokens
+  int n = plan.n, h = plan.h, s = plan.s, m = tokens_of(n);
+  struct Seg {
+    int n, h, first, count;
+  };
+  auto next = [&](Seg& x) {
+    if (left == 0) return false;
+    while (s * kTokens >= m) {  // the unit is through; the piece has segments left, so one follows
+      s = 0;
+      if (++h == c.Hkv) {
+        h = 0;
+        do m = tokens_of(++n);
+        while (m == 0);
+      }
+    }
+    x = Seg{n, h, s * kTokens, min(kTokens, m - s * kTokens)};
+    ++s;
+    --left;
+    return true;
+  };
+  auto index_of = [&](const Seg& x) {
+    return tid < x.count ? __ldg(p.kept + ((size_t)x.n * c.Hkv + x.h) * p.max_kept + x.first + tid) : -1;
+  };
+  auto look_up = [&](const Seg& x, int index) {
+    if (tid >= x.count) return make_int2(-1, -1);
+    const Rows from{p.table + (size_t)x.n * p.max_pages, x.h, shift}, to{p.dst_table + (size_t)x.n * p.dst_max_pages, x.h, shift};
+    return make_int2(from.at(c, index), to.at(c, x.first + tid));
+  };
+  Seg cur, after;
+  next(cur);
+  int index = index_of(cur);
+  int2 mine = look_up(cur, index);
+  if (tid < kTokens) place[0][tid] = mine;
+  bool more = next(after);
+  int next_index = more ? index_of(after) : -1;
+  const uint4* k = static_cast<const uint4*>(c.k);
+  const uint4* v = static_cast<const uint4*>(c.v);
+  for (int b = 0;; b ^= 1) {
+    __syncthreads();
+    // a warp's pieces are of one token's keys or values, or of several of the one
+    uint4 held[kUnroll];
+    const int piece = tid % kPieces, part = tid / kPieces;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int x = part + u * (kMoveThreads / kPieces), t = x >> 1;
+      if (t < cur.count) held[u] = __ldcs((x & 1 ? v : k) + (size_t)place[b][t].x * kPieces + piece);
+    }
+    float ks = 0.f, vs = 0.f, w = 0.f;
+    if (tid < cur.count) {
+      if (c.e4m3) {
+        ks = __ldcs(c.k_scale + mine.x);
+        vs = __ldcs(c.v_scale + mine.x);
+      }
+      w = __ldcs(p.score + ((size_t)__ldg(p.slot + cur.n) * c.Hkv + cur.h) * p.max_tokens + index);
+    }
+    // the next segment's places, and the one's after it indices
+    const Seg now = cur;
+    const int2 here = mine;
+    const bool go_on = more;
+    if (more) {
+      cur = after;
+      index = next_index;
+      mine = look_up(cur, index);
+      if (tid < kTokens) place[b ^ 1][tid] = mine;
+      more = next(after);
+      next_index = more ? index_of(after) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int x = part + u * (kMoveThreads / kPieces), t = x >> 1;
+      if (t < now.count)
+        __stcs(static_cast<uint4*>(x & 1 ? c.v : c.k) + (size_t)place[b][t].y * kPieces + piece, held[u]);
+    }
+    if (tid < now.count) {
+      if (c.e4m3) {
+        __stcs(c.k_scale + here.y, ks);
+        __stcs(c.v_scale + here.y, vs);
+      }
+      __stcs(p.score + ((size_t)__ldg(p.dst_slot + now.n) * c.Hkv + now.h) * p.max_tokens + now.first + tid, w);
+    }
+    if (!go_on) break;
+  }
+}
+
+// In place: kept token i has index kept[i] >= i, so a chunk of tokens is stored where only earlier chunks' tokens, or this
+// one's, were read: a block takes its chunks in order and has read a chunk before it stores it. Blocks share no byte: a
+// block has one head's keys or values, or a slice of their rows, or its floats.
+//
+// Tokens [first, m) of one head: `lanes` threads a token, each with one T; chunks of kUnroll tokens a thread. `row` finds
+// the place that a token comes from, `from` and `to` give its address and that of the place that it goes to. What a chunk
+// needs to be read comes a chunk ahead (its places) and two (its indices).
+template <typename T, typename Row, typename From, typename To>
+__device__ __forceinline__ void shift_rows(int first, int m, int lanes, const int* kept, Row row, From from, To to) {
   const int per = kMoveThreads / lanes, r = threadIdx.x / lanes, chunk = per * kUnroll;
   T held[kUnroll];
-  int src[kUnroll];
+  int place[kUnroll], index[kUnroll];
   auto indices = [&](int base) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int i = base + u * per + r;
-      src[u] = i < m ? __ldg(kept + i) : -1;
+      index[u] = i < m ? __ldg(kept + i) : -1;
     }
   };
-  auto load = [&] {
+  auto places = [&] {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (src[u] >= 0) held[u] = *from(src[u]);
+    for (int u = 0; u < kUnroll; ++u) place[u] = index[u] >= 0 ? row(index[u]) : -1;
   };
   indices(first);
+  places();
+  indices(first + chunk);
   for (int base = first; base < m; base += chunk) {
-    load();
-    indices(base + chunk);
-    __syncthreads();  // the whole chunk has been read, in place a part of it is where it goes
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (place[u] >= 0) held[u] = *from(place[u]);
+    places();
+    indices(base + 2 * chunk);
+    __syncthreads();  // the whole chunk has been read: a part of it is where it goes
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int i = base + u * per + r;
@@ -245,7 +502,7 @@ __device__ __forceinline__ void move_rows(int first, int m, int lanes, const int
 }
 
 // A unit's parts: its keys' slices, its values' slices, and its floats (scales and weights).
-__global__ void __launch_bounds__(kMoveThreads, 1) move_kernel(const EvictArgs p, const KvArgs c, int slices) {
+__global__ void __launch_bounds__(kMoveThreads, 2) shift_kernel(const EvictArgs p, const KvArgs c, int slices, int shift) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int parts = 2 * slices + 1;
   const long long unit = blockIdx.x / parts;
@@ -255,54 +512,38 @@ __global__ void __launch_bounds__(kMoveThreads, 1) move_kernel(const EvictArgs p
   const int m = kept_of(p, c, n, &why);
   if (m <= 0 || p.new_len[n] < 0) return;
   const int* kept = p.kept + ((size_t)n * c.Hkv + h) * p.max_kept;
-  const int32_t* table = p.table + (size_t)n * p.max_pages;
-  const int32_t* dst_table = p.dst_table + (size_t)n * p.dst_max_pages;
-  const int slot = __ldg(p.slot + n), dst_slot = __ldg(p.dst_slot + n);
-  // in place the tokens in front of the first that is gone stay where they are
-  auto first_moved = [&] {
-    int lo = 0, hi = m;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(kept + mid) == mid) lo = mid + 1;
-      else hi = mid;
-    }
-    return lo;
-  };
-  auto row = [&](const int32_t* t, int i) {
-    const int k = i / c.page;
-    return ((size_t)__ldg(t + k) * c.Hkv + h) * c.page + (i - k * c.page);
-  };
+  const Rows rows{p.table + (size_t)n * p.max_pages, h, shift};
+  // the tokens in front of the first that is gone stay where they are
+  int first = 0, hi = m;
+  while (first < hi) {
+    const int mid = (first + hi) >> 1;
+    if (__ldg(kept + mid) == mid) first = mid + 1;
+    else hi = mid;
+  }
+  auto row = [&](int i) { return rows.at(c, i); };
   if (part < 2 * slices) {
-    const int row_bytes = p.D * (c.e4m3 ? 1 : 2), lanes = row_bytes / 16 / slices;
+    const int pieces = p.D * (c.e4m3 ? 1 : 2) / 16, lanes = pieces / slices;
     uint4* pool = static_cast<uint4*>(part < slices ? c.k : c.v) + (part % slices) * lanes + threadIdx.x % lanes;
-    const int row_pieces = row_bytes / 16;
-    move_rows<uint4>(p.table == p.dst_table ? first_moved() : 0, m, lanes, kept,
-                     [&](int i) { return pool + row(table, i) * row_pieces; },
-                     [&](int i) { return pool + row(dst_table, i) * row_pieces; });
+    shift_rows<uint4>(first, m, lanes, kept, row, [&](int at) { return pool + (size_t)at * pieces; },
+                      [&](int i) { return pool + (size_t)row(i) * pieces; });
   } else {
     if (c.e4m3) {
-      const int first = p.table == p.dst_table ? first_moved() : 0;
-      move_rows<float>(first, m, 1, kept, [&](int i) { return c.k_scale + row(table, i); },
-                       [&](int i) { return c.k_scale + row(dst_table, i); });
-      move_rows<float>(first, m, 1, kept, [&](int i) { return c.v_scale + row(table, i); },
-                       [&](int i) { return c.v_scale + row(dst_table, i); });
+      shift_rows<float>(first, m, 1, kept, row, [&](int at) { return c.k_scale + at; },
+                        [&](int i) { return c.k_scale + row(i); });
+      shift_rows<float>(first, m, 1, kept, row, [&](int at) { return c.v_scale + at; },
+                        [&](int i) { return c.v_scale + row(i); });
     }
-    const float* w = p.score + ((size_t)slot * c.Hkv + h) * p.max_tokens;
-    float* to = p.score + ((size_t)dst_slot * c.Hkv + h) * p.max_tokens;
-    move_rows<float>(slot == dst_slot ? first_moved() : 0, m, 1, kept, [&](int i) { return w + i; },
-                     [&](int i) { return to + i; });
+    float* w = p.score + ((size_t)__ldg(p.slot + n) * c.Hkv + h) * p.max_tokens;
+    shift_rows<float>(first, m, 1, kept, [](int i) { return i; }, [&](int at) { return w + at; },
+                      [&](int i) { return w + i; });
   }
 }
 
-template <int kSplit>
+template <int kSplit, int kHeld>
 cudaError_t launch_select(const EvictArgs& a, const KvArgs& c, cudaStream_t stream) {
-  constexpr int kSmem = kCached * (int)sizeof(uint32_t);
-  const cudaError_t err = ensure_dynamic_smem(reinterpret_cast<const void*>(&select_kernel<kSplit>), kSmem);
-  if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((long long)a.N * c.Hkv * kSplit), 1, 1);
   cfg.blockDim = dim3(kSelThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -313,21 +554,27 @@ cudaError_t launch_select(const EvictArgs& a, const KvArgs& c, cudaStream_t stre
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, select_kernel<kSplit>, a, c);
+  return cudaLaunchKernelEx(&cfg, select_kernel<kSplit, kHeld>, a, c);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_evict(const EvictArgs& a, const KvArgs& c, cudaStream_t stream) {
   const long long units = (long long)a.N * c.Hkv;
-  cudaError_t err = units * 8 <= 152 ? launch_select<8>(a, c, stream) : launch_select<1>(a, c, stream);
+  // as many CTAs a head as hold the longest request that the tables allow in registers, up to 131072 tokens
+  const long long most = std::min<long long>((long long)a.max_pages * c.page, a.max_tokens);
+  const cudaError_t err = most <= 4 * kSelThreads    ? launch_select<1, 4>(a, c, stream)
+                          : most <= 16 * kSelThreads ? launch_select<1, 16>(a, c, stream)
+                          : most <= 32 * kSelThreads ? launch_select<2, 16>(a, c, stream)
+                          : most <= 64 * kSelThreads ? launch_select<4, 16>(a, c, stream)
+                          : most <= 128 * kSelThreads ? launch_select<8, 16>(a, c, stream)
+                                                      : launch_select<8, 32>(a, c, stream);
   if (err != cudaSuccess) return err;
-  // slices of the rows, down to 64 bytes, while there are too few blocks to keep HBM busy
   const int row_bytes = a.D * (c.e4m3 ? 1 : 2);
-  int slices = 1;
-  while (row_bytes / slices > 64 && units * 2 * slices < 4 * 152) slices *= 2;
+  int shift = -1;
+  if ((c.page & (c.page - 1)) == 0)
+    for (shift = 0; 1 << shift < c.page;) ++shift;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * (2 * slices + 1)), 1, 1);
   cfg.blockDim = dim3(kMoveThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
@@ -335,7 +582,17 @@ cudaError_t launch_kv_evict(const EvictArgs& a, const KvArgs& c, cudaStream_t st
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, move_kernel, a, c, slices);
+  if (a.dst_table != a.table) {
+    cfg.gridDim = dim3(2 * 152, 1, 1);
+    return row_bytes == 512   ? cudaLaunchKernelEx(&cfg, copy_kernel<512>, a, c, shift)
+           : row_bytes == 256 ? cudaLaunchKernelEx(&cfg, copy_kernel<256>, a, c, shift)
+                              : cudaLaunchKernelEx(&cfg, copy_kernel<128>, a, c, shift);
+  }
+  // slices of the rows, down to a sector, while there are too few blocks to keep HBM busy
+  int slices = 1;
+  while (row_bytes / slices > 32 && units * 2 * slices < 2 * 152) slices *= 2;
+  cfg.gridDim = dim3((unsigned)(units * (2 * slices + 1)), 1, 1);
+  return cudaLaunchKernelEx(&cfg, shift_kernel, a, c, slices, shift);
 }
 
 }  // namespace gdn

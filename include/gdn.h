@@ -675,16 +675,15 @@ gdn_status gdn_kv_score(const gdn_kv_cache *cache, const uint16_t *q, const floa
  *               padding request (skipped, new_len left untouched, as with a
  *               negative slot)
  *   budget      [N] int32 >= 0
- *   dst_table   [N][dst_max_pages] int32: the pages that the kept tokens go to. An
- *               entry is the request's own page in the same place of block_table,
- *               or one that no request of the call has in its block_table and no other in its
- *               dst_table (undefined values otherwise): a page that other
- *               requests share stays whole that way. NULL: in place (dst_max_pages
- *               is not used).
+ *   dst_table   [N][dst_max_pages] int32: the pages that the kept tokens go to, none
+ *               of them in any request's block_table or twice in the tables
+ *               (undefined values otherwise); pages that other requests share stay
+ *               whole that way. NULL: in place (dst_max_pages is 0); two requests of
+ *               the call must share no page then.
  *   score       [num_slots][Hkv][max_tokens] fp32, in/out;  slot_idx [N]
- *   dst_slot    [N] int32: the slots that the kept tokens' scores go to, the
- *               request's own or one that no other request of the call names. NULL:
- *               slot_idx
+ *   dst_slot    [N] int32: the slots that the kept tokens' scores go to, none of
+ *               them any request's slot_idx, or twice. NULL: in place. With a dst_table
+ *               there is a dst_slot, and without one there is none.
  *   kept        [N][Hkv][max_kept] int32 out: the kept tokens' old indices,
  *               ascending; entries from new_len on are not touched
  *   new_len     [N] int32 out, not `length` itself: the request's tokens now, -1 if

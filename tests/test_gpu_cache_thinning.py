@@ -351,20 +351,20 @@ EVICT = [  # kv heads, head_dim, page, lengths, budgets, sinks, recent
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
-@pytest.mark.parametrize("place", ["in place", "other pages", "other slots"])
+@pytest.mark.parametrize("place", ["in place", "other pages"])
 @pytest.mark.parametrize("heads,d,page,lens,budgets,sinks,recent", EVICT)
 def test_evict(b, err, fmt, place, heads, d, page, lens, budgets, sinks, recent):
     pool, table, w, fresh = evict_case(fmt, heads, d, page, lens, [min(x, y) for x, y in zip(lens, budgets)])
     N = len(lens)
     slots = torch.randperm(2 * N + 1, device="cuda").to(torch.int32)
     check_evict(b, err, pool, table, lens, budgets, w, slots[:N].contiguous(), sinks, recent,
-                fresh if place != "in place" else None, slots[N:2 * N].contiguous() if place == "other slots" else None)
+                *((fresh, slots[N:2 * N].contiguous()) if place != "in place" else ()))
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("seed", range(6))
 def test_evict_of_random_sizes(b, err, fmt, seed):
-    """Some of a request's pages its own and some fresh; weights of every kind."""
+    """Weights of every kind; requests that share pages, which stay whole."""
     rng = np.random.default_rng(seed)
     heads, d = int(rng.integers(1, 6)), int(rng.choice([128, 256]))
     page = int(rng.choice([16, 32, 48, 64, 128]))
@@ -375,9 +375,16 @@ def test_evict_of_random_sizes(b, err, fmt, seed):
     odd = torch.tensor([NAN, -NAN, INF, -INF, 0.0, -0.0, 1e-42, -3.0, 3e38], device="cuda")
     pick = torch.randint(0, 60, w.shape, device="cuda", generator=torch.Generator(device="cuda").manual_seed(seed))
     w = torch.where(pick < 9, odd[pick.clamp_max(8)], w)
-    mixed = torch.where(torch.rand(fresh.shape, device="cuda") < 0.5, fresh, table[:, :fresh.shape[1]])
-    slot = torch.randperm(len(lens), device="cuda").to(torch.int32)
-    check_evict(b, err, pool, table, lens, budgets, w, slot, int(rng.integers(0, 6)), int(rng.integers(0, 40)), mixed)
+    sinks, recent = int(rng.integers(0, 6)), int(rng.integers(0, 40))
+    slots = torch.randperm(2 * len(lens), device="cuda").to(torch.int32)
+    if seed % 2:
+        check_evict(b, err, pool, table, lens, budgets, w, slots[:len(lens)].contiguous(), sinks, recent)
+        return
+    for n in range(1, len(lens)):
+        shared = min(lens[0], lens[n]) // page
+        table[n, :shared] = table[0, :shared]
+    check_evict(b, err, pool, table, lens, budgets, w, slots[:len(lens)].contiguous(), sinks, recent, fresh,
+                slots[len(lens):].contiguous())
 
 
 @pytest.mark.parametrize("n,budget,place", [(140000, 70001, "in place"), (131072, 1000, "other pages"),
@@ -386,7 +393,8 @@ def test_evict_of_a_long_request(b, err, n, budget, place):
     """More tokens than the selection keeps in shared memory, one head, and all weights alike from some place on."""
     pool, table, w, fresh = evict_case("bf16", 1, 128, 16, [n], [budget], ties=False)
     w[0, 0, n // 2:] = 0.25
-    check_evict(b, err, pool, table, [n], [budget], w, ints([0]), 4, 100, fresh if place != "in place" else None)
+    check_evict(b, err, pool, table, [n], [budget], w, ints([0]), 4, 100,
+                *((fresh, ints([2])) if place != "in place" else ()))
 
 
 def test_evict_of_many_short_requests(b, err):
@@ -400,9 +408,9 @@ def test_evict_flags_what_breaks_the_limits(b, err):
     """Such a request writes nothing but a new length of -1, a padding request nothing at all; the others are whole."""
     lens, budgets = [40, 40, 40], [20, 20, 20]
 
-    def run(length=lens, budget=budgets, slot=(0, 1, 2), dst=None, bad_page=None, most=25, room=47):
+    def run(length=lens, budget=budgets, slot=(0, 1, 2), dst=None, dst_slot=(3, 4, 5), bad_page=None, most=25, room=47):
         pool, table, w, fresh = evict_case("bf16", 2, 128, 16, lens, budgets, ties=False)
-        w = w[:3, :, :room].contiguous()
+        w = w[:6, :, :room].contiguous()
         if bad_page:
             table[bad_page[0], bad_page[1]] = bad_page[2]
         if dst:
@@ -410,12 +418,12 @@ def test_evict_flags_what_breaks_the_limits(b, err):
         was, w_was = pool.k.clone(), w.clone()
         kept, new_len = torch.full((3, 2, most), -7, dtype=torch.int32, device="cuda"), ints([-9] * 3)
         b.gdn_kv_evict(pool.handle(b), table, ints(length), ints(budget), w, ints(slot), kept, new_len, 0, 0,
-                       fresh if dst else None, dev_err=err)
+                       fresh if dst else None, ints(dst_slot) if dst else None, dev_err=err)
         used = [fresh[n][:2] if dst else table[n][:3] for n in range(3)]
         moved = [bool((pool.k[u.clamp(0, pool.k.shape[0] - 1).long()] != was[u.clamp(0, pool.k.shape[0] - 1).long()]).any())
                  for u in used]
         kept_moved = [bool((kept[n] != -7).any()) for n in range(3)]
-        w_moved = [0 <= s < 3 and bool((w[s] != w_was[s]).any()) for s in slot]
+        w_moved = [0 <= s < 6 and bool((w[s] != w_was[s]).any()) for s in (dst_slot if dst else slot)]
         return b.gdn_read_device_error(err), new_len.tolist(), moved, kept_moved, w_moved
 
     whole = [True, True, True]
@@ -426,7 +434,8 @@ def test_evict_flags_what_breaks_the_limits(b, err):
     assert run(slot=(0, -1, 2)) == (0, [20, -9, 20], part, part, part)
     for kw, flag in ((dict(length=[40, 49, 40], room=49), OFFSETS), (dict(length=[40, 45, 40], room=44), OFFSETS),
                      (dict(length=[40, 2 ** 31 - 1, 40]), OFFSETS), (dict(budget=[20, -1, 20]), OFFSETS),
-                     (dict(budget=[20, 26, 20]), OFFSETS), (dict(slot=(0, 3, 2)), SLOT),
+                     (dict(budget=[20, 26, 20]), OFFSETS), (dict(slot=(0, 6, 2)), SLOT),
+                     (dict(dst=(1, 1, 9), dst_slot=(3, 6, 5)), SLOT), (dict(dst=(1, 1, 9), dst_slot=(3, -1, 5)), SLOT),
                      (dict(bad_page=(1, 2, -1)), SLOT), (dict(bad_page=(1, 0, 1000)), SLOT),
                      (dict(bad_page=(1, 1, 2 ** 31 - 1)), SLOT), (dict(dst=(1, 1, -1)), SLOT),
                      (dict(dst=(1, 0, 2 ** 31 - 1)), SLOT)):
