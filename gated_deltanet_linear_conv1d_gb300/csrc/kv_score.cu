@@ -8,56 +8,27 @@
 //
 // S^T [128 tokens x rows] = K Q^T on the tensor cores (tcgen05): the keys are the first operand, from shared memory as
 // they lie in the cache, so a token is a lane of tensor memory, and its sum over the rows is one thread's, in the order of
-// the rows. An E4M3 cache stays E4M3, and Q (bf16, scaled by a power of two per row) is written as the sum of two E4M3
-// terms, exact down to 2^-17 of the row's largest value; the second term's MMAs add to the same columns.
+// the rows. An E4M3 cache stays E4M3, and Q (bf16, scaled by a power of two) is written as the sum of two E4M3 terms, exact
+// down to 2^-17 of the largest value; the second term's MMAs add to the same columns.
 //
-// Work. The tiles of 128 tokens of all (request, kv head) units stand in one line, cut into equal pieces, one per CTA. Up
-// to 128 rows stay in shared memory for a unit's tiles. More are taken in chunks: the piece goes through some tiles with
-// one chunk after the other, the keys coming from L2 from the second on, and a tile's later chunks add to the weights
-// that the same thread has stored.
+// Work. The tiles of 128 tokens of all (request, kv head) units stand in one line, cut into equal pieces, one per CTA. A
+// unit's rows, up to 64, stay in shared memory for its tiles; more go to kv_score_pair.cu.
 //
 // Roles: two groups of four warps that take the tiles in turn (a thread has one token), a warp for the copies (TMA, 16 KB
-// blocks of 128 tokens x 128 bytes into a ring), one for the MMAs, four for the query rows. Every wait is bounded.
-#include <type_traits>
-
-#include "tree_attn.cuh"
+// blocks of 128 tokens x 128 bytes into a ring), one for the MMAs, two for the query rows. Every wait is bounded.
+#include "kv_score.cuh"
 
 namespace gdn {
 namespace kv_score {
 
-using tree_attn::arrive;
-using tree_attn::elect_one;
-using tree_attn::ex2;
-using tree_attn::kBlock;
-using tree_attn::kLog2e;
-using tree_attn::kSmemLimit;
-using tree_attn::kTile;
-using tree_attn::swz;
-using tree_attn::wait;
-using tree_attn::wait_warp;
+namespace {
 
-constexpr int kMaxRows = 192;  // of a chunk
-// Bytes of keys that the chunks of more rows go through in turn, a CTA: what all CTAs have stays in L2.
-constexpr int kSubBytes = 640 * 1024;
+constexpr int kMaxRows = 64;   // more go to pairs
 constexpr int kGroups = 2;     // of four warps for the weights
 constexpr int kCopyWarp = 4 * kGroups, kMmaWarp = kCopyWarp + 1, kQueryWarp = kCopyWarp + 2, kQueryWarps = 2;
 constexpr int kLoaders = 4 * kGroups + kQueryWarps;  // all but those of the copies and the MMAs
 constexpr int kThreads = 32 * (kQueryWarp + kQueryWarps);
 constexpr int kMaxStages = 12;
-
-struct Args {
-  ScoreArgs p;
-  KvArgs c;
-  int rows, chunks;  // rows of a chunk (the last one may have fewer)
-  int box;           // tokens per TMA box
-  int sub;           // tiles that the chunks go through in turn
-  int cost;          // what a unit takes beside its tiles, in tiles
-};
-
-struct Plan {
-  long long lo;
-  int count, n, h, t;  // t: where the piece begins in the unit, whose first `cost` places hold no tile
-};
 
 struct Bars {
   uint64_t full[kMaxStages], empty[kMaxStages];
@@ -76,88 +47,18 @@ struct Cfg {
   static constexpr int kBlk = D * (kE4m3 ? 1 : 2) / 128;  // ring blocks of a tile
   static constexpr int kTerms = kE4m3 ? 2 : 1;
   static constexpr int kBufs = kGroups;                    // tiles' scores in tensor memory
-  static constexpr int kCols = kRows == 16 ? 32 : kRows == 64 ? 128 : kRows == 128 ? 256 : 512;
+  static constexpr int kCols = 2 * kRows;
   static_assert(kBufs * kRows <= kCols, "tensor memory");
   static constexpr int kQBytes = kRows * D * 2;            // query rows of a segment
-  // Two segments' query rows where the ring keeps six blocks beside them: the next segment's come while this one runs.
-  // What else goes by the row is there for two.
-  static constexpr int kRest1 = 3 * 2 * kRows * 4 + (sizeof(Bars) + 15) / 16 * 16;
-  static constexpr int kQBuf = kSmemLimit - kRest1 - 2 * kQBytes >= 6 * (int)kBlock ? 2 : 1;
-  // behind the ring: Q, then by row -lse to base 2, and the nodes that the row sees (in two words)
-  static constexpr int oLse = kQBuf * kQBytes;
+  // behind the ring, for two segments each: Q, then by row -lse to base 2, and the nodes that the row sees (in two words)
+  static constexpr int oLse = 2 * kQBytes;
   static constexpr int oSees = oLse + 2 * kRows * 4;
   static constexpr int oBars = oSees + 2 * 2 * kRows * 4;
-  static constexpr int kRest = kQBuf * kQBytes + kRest1;
+  static constexpr int kRest = oBars + (sizeof(Bars) + 15) / 16 * 16;
   static constexpr int kFit = (kSmemLimit - kRest) / (int)kBlock;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static_assert(kStages >= 2, "a ring");
 };
-
-// What the roles go through: tiles t0 .. t1 - 1 of (request n, kv head h) with the rows of chunk c. `at`: the number of
-// tiles before t0 in the piece, each counted once; tile t's scores are in buffer (at + t - t0) % kBufs, whatever the chunk.
-struct Seg {
-  int n, h, c, t0, t1, len, ctx, at;
-};
-
-// The tiles of a request; none where it is a padding request or breaks the limits.
-__device__ __forceinline__ int tiles_of(const Args& a, int n, int* why = nullptr) {
-  const ScoreArgs& p = a.p;
-  const int ctx = __ldg(p.ctx + n), slot = __ldg(p.slot + n);
-  if (ctx < 0 || slot < 0) return 0;
-  const long long len = (long long)ctx + p.P;
-  int bad = slot >= p.Rs ? GDN_DEVERR_SLOT : 0;
-  if ((len + a.c.page - 1) / a.c.page > p.max_pages || len > p.max_tokens) bad |= GDN_DEVERR_OFFSETS;
-  if (why) *why |= bad;
-  return bad ? 0 : (int)((len + kTile - 1) / kTile);
-}
-
-struct Walk {
-  int n, h, t, left, tiles, at;
-  Seg cur;
-  __device__ __forceinline__ Walk(const Args& a, const Plan& p) : n(p.n), h(p.h), t(p.t), left(p.count), tiles(0), at(0) {
-    cur.c = a.chunks;  // none
-    if (left > 0) tiles = tiles_of(a, n);
-  }
-  __device__ __forceinline__ bool next(const Args& a, Seg& s) {
-    if (cur.c + 1 < a.chunks) {
-      ++cur.c;
-      s = cur;
-      return true;
-    }
-    while (left > 0) {
-      while (tiles == 0) tiles = tiles_of(a, ++n);  // the piece has places left, so a request with some follows
-      const int places = tiles + a.cost;
-      int take = min(places - t, left);
-      if (a.chunks > 1) take = min(take, max(a.cost - t, 0) + a.sub);
-      const int ctx = __ldg(a.p.ctx + n);
-      cur = Seg{n, h, 0, max(t - a.cost, 0), t + take - a.cost, ctx + a.p.P, ctx, at};
-      left -= take;
-      t += take;
-      if (t == places) {
-        t = 0;
-        if (++h == a.c.Hkv) {
-          h = 0;
-          tiles = 0;
-        }
-      }
-      if (cur.t1 > 0) {
-        at += cur.t1 - cur.t0;
-        s = cur;
-        return true;
-      }
-    }
-    cur.c = a.chunks;
-    return false;
-  }
-};
-
-// The registers of a tensor-memory load, after the wait for it: nothing that uses them moves in front of the wait.
-template <int kN>
-__device__ __forceinline__ void loaded(uint32_t (&u)[kN]) {
-  umma::wait_ld();
-#pragma unroll
-  for (int i = 0; i < kN; ++i) asm volatile("" : "+r"(u[i]));
-}
 
 // The query rows of a segment, number `seg` of the piece, as rows of the MMAs' second operand, with their constants. Rows
 // that add nothing (without a finite lse) are left out: the others move up. `shares` warps have an equal part of the rows
@@ -173,7 +74,7 @@ __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned 
   const uint32_t q_block = rp * 128, lower = (1u << lane) - 1u;
   const int r0 = s.c * a.rows, all = min(a.rows, p.P * p.G - r0), b = seg & 1;
   const int per = (all + shares - 1) / shares;
-  unsigned char* q_s = rest + seg % C::kQBuf * C::kQBytes;
+  unsigned char* q_s = rest + b * C::kQBytes;
   float* lse = reinterpret_cast<float*>(rest + C::oLse) + b * kRows;
   uint32_t* sees = reinterpret_cast<uint32_t*>(rest + C::oSees) + b * 2 * kRows;
   const int first = min(all, share * per), end = min(all, first + per);
@@ -307,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
       mbar_init(&B->s_empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&B->q_full[i], C::kQBuf == 1 ? kLoaders : kQueryWarps);
+      mbar_init(&B->q_full[i], kQueryWarps);
       mbar_init(&B->q_empty[i], 1);
       mbar_init(&B->r_empty[i], 4 * kGroups);
     }
@@ -318,68 +219,27 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // nothing of the kernel before is read or written earlier
   asm volatile("griddepcontrol.launch_dependents;");
-  // ---- this CTA's piece: a scan over the requests' tiles
-  {
-    const int per = (p.N + kThreads - 1) / kThreads, n0 = min(p.N, tid * per), n1 = min(p.N, n0 + per);
-    long long mine = 0;
-    int why = 0;
-    for (int n = n0; n < n1; ++n) {
-      const int tiles = tiles_of(a, n, &why);
-      mine += tiles + (tiles > 0 ? a.cost : 0);
-    }
-    if (why && blockIdx.x == 0) report(p.dev_err, why);
-    long long upto = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += o;
-    }
-    if (lane == 31) B->warp_total[warp] = upto;
-    __syncthreads();
-    long long before = 0, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += B->warp_total[w];
-      total += B->warp_total[w];
-    }
-    before += upto - mine;
-    total *= c.Hkv;
-    const long long ctas = min((long long)gridDim.x, total);  // with a piece: none of them empty
-    const long long lo = ctas ? total * blockIdx.x / ctas : 0, hi = ctas ? total * (blockIdx.x + 1) / ctas : 0;
-    if (blockIdx.x < ctas && before * c.Hkv <= lo && lo < (before + mine) * c.Hkv) {
-      long long at = before * c.Hkv;
-      for (int n = n0; n < n1; ++n) {
-        const int tiles = tiles_of(a, n), places = tiles + (tiles > 0 ? a.cost : 0);
-        const long long here = (long long)places * c.Hkv;
-        if (lo < at + here) {
-          B->plan = Plan{lo, (int)(hi - lo), n, (int)((lo - at) / places), (int)((lo - at) % places)};
-          break;
-        }
-        at += here;
-      }
-    }
-    if (warp == kMmaWarp) umma::tmem_alloc(&B->tmem, C::kCols);
-    umma::fence_before_sync();
-    __syncthreads();
-    umma::fence_after_sync();
-  }
+  make_plan<kTile, kThreads>(a, blockIdx.x, gridDim.x, B->warp_total, &B->plan);
+  if (warp == kMmaWarp) umma::tmem_alloc(&B->tmem, C::kCols);
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
   const Plan plan = B->plan;
   const uint32_t tmem = B->tmem;
   int* abort = &B->abort;
-  // The first segment's query rows are loaded by all warps but the copies' and the MMAs', and so are all, where there is
-  // room for one segment's; else the later ones by the query warps, while the segment before is worked on. (By four warps
-  // of their own, 192 rows of an E4M3 cache took 12 us.)
+  // The first segment's query rows are loaded by all warps but the copies' and the MMAs', the later ones by the query warps
+  // while the segment before is worked on. (Whoever gives up a wait goes on without effect: no warp is missing at a barrier
+  // of several.)
   auto load_segment = [&](const Seg& s, int seg, int share) {
-    const int qb = seg % C::kQBuf;
-    bool ok = wait(&B->q_empty[qb], ((seg / C::kQBuf) & 1) ^ 1, abort);
-    if (C::kQBuf == 2) ok = ok && wait(&B->r_empty[seg & 1], ((seg >> 1) & 1) ^ 1, abort);
-    if (!__all_sync(0xffffffffu, ok)) return false;
-    const bool together = C::kQBuf == 1 || seg == 0;
+    const int qb = seg & 1, parity = ((seg >> 1) & 1) ^ 1;
+    wait_warp(&B->q_empty[qb], parity, abort);
+    wait_warp(&B->r_empty[qb], parity, abort);
+    const bool together = seg == 0;
     load_queries<D, kE4m3, kRows>(a, s, rest, B, seg, together ? share : share - 4 * kGroups, together ? kLoaders : kQueryWarps);
     umma::fence_proxy_async_smem();
-    if (C::kQBuf == 2 && seg == 0) asm volatile("bar.sync 2, %0;" ::"n"(32 * kLoaders) : "memory");
+    if (together) asm volatile("bar.sync 2, %0;" ::"n"(32 * kLoaders) : "memory");
     else __syncwarp();
-    if ((C::kQBuf == 1 || share >= 4 * kGroups) && lane == 0) arrive(&B->q_full[seg & 1]);
-    return true;
+    if (share >= 4 * kGroups && lane == 0) arrive(&B->q_full[qb]);
   };
 
   if (warp == kCopyWarp) {
@@ -388,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
     const int boxes = kTile / a.box, total_rows = c.slots * c.Hkv, span = 32 / boxes;
     int st = 0, phase = 1, issued = 0;
     bool ok = true;
-    Walk walk(a, plan);
+    Walk<kTile> walk(a, plan);
     Seg s;
     bool more = walk.next(a, s);
     auto load_page = [&](const Seg& x, int t) {  // of box `lane` from tile t on; -1 behind the last token
@@ -436,10 +296,10 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
       ok = __all_sync(0xffffffffu, ok);
       return ok;
     };
-    Walk walk(a, plan);
+    Walk<kTile> walk(a, plan);
     Seg s;
     while (ok && walk.next(a, s)) {
-      const int qb = seg % C::kQBuf;
+      const int qb = seg & 1;
       if (!wait_all(&B->q_full[seg & 1], (seg >> 1) & 1)) break;
       const int cols = max(16, (*(volatile int*)&B->rows[seg & 1] + 15) / 16 * 16);
       const uint32_t id = umma::idesc(kType, false, false, kTile, cols);
@@ -478,11 +338,11 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
     __syncwarp();
   } else if (warp >= kQueryWarp) {
     // ------------------------------------------------------------ query rows
-    Walk walk(a, plan);
+    Walk<kTile> walk(a, plan);
     Seg s;
     int seg = 0;
     while (walk.next(a, s)) {
-      if (!load_segment(s, seg, 4 * kGroups + warp - kQueryWarp)) break;
+      load_segment(s, seg, 4 * kGroups + warp - kQueryWarp);
       ++seg;
     }
   } else {
@@ -490,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
     const int wg = warp >> 2, w4 = warp & 3, mine = 32 * w4 + lane;
     const float* lse_s = reinterpret_cast<const float*>(rest + C::oLse);
     const uint32_t* sees_s = reinterpret_cast<const uint32_t*>(rest + C::oSees);
-    Walk walk(a, plan);
+    Walk<kTile> walk(a, plan);
     Seg s;
     int seg = 0, used = 0;
     while (walk.next(a, s)) {
@@ -503,8 +363,6 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
         const int tok = t * kTile + mine;
         return t < s.t1 && tok < s.len ? __ldg(table + tok / c.page) : -1;
       };
-      const bool again = s.c > 0, old = again || !fresh;
-      const float decay = again ? 1.f : p.decay;
       float key_scale = 1.f, before = 0.f;
       auto load_token = [&](int t, int page, float& ks, float& w) {
         const int tok = t * kTile + mine;
@@ -512,14 +370,13 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
         w = 0.f;
         if (page < 0 || page >= c.pages) return;
         if constexpr (kE4m3) ks = __ldg(c.k_scale + ((size_t)page * c.Hkv + s.h) * c.page + tok % c.page);
-        if (old && (again || tok < s.ctx)) w = out[tok];
+        if (!fresh && tok < s.ctx) w = out[tok];
       };
       int t = s.t0 + (wg - s.at) % C::kBufs;
       if (t < s.t0) t += C::kBufs;
       int page = load_page(t), next_page = load_page(t + C::kBufs);
       load_token(t, page, key_scale, before);
-      if (C::kQBuf == 1 || seg == 0)
-        if (!load_segment(s, seg, warp)) break;
+      if (seg == 0) load_segment(s, seg, warp);
       wait_warp(&B->q_full[rb], (seg >> 1) & 1, abort);
       const int rows = *(volatile int*)&B->rows[rb];
       const float f0 = *(volatile float*)&B->factor[rb];
@@ -617,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
         if (lane == 0) arrive(&B->s_empty[wg]);
         if (t * kTile + mine < s.len && !*(volatile int*)abort) {
           if (this_page < 0 || this_page >= c.pages) report(p.dev_err, GDN_DEVERR_SLOT);
-          else out[t * kTile + mine] = fmaf(w, decay, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+          else out[t * kTile + mine] = fmaf(w, p.decay, (sum[0] + sum[1]) + (sum[2] + sum[3]));
         }
       }
       __syncwarp();
@@ -654,10 +511,10 @@ cudaError_t launch_rows(const Args& a, const CUtensorMap& tmk, int grid, cudaStr
 template <int D, bool kE4m3>
 cudaError_t launch_dim(const Args& a, const CUtensorMap& tmk, int grid, cudaStream_t stream) {
   if (a.rows <= 16) return launch_rows<D, kE4m3, 16>(a, tmk, grid, stream);
-  if (a.rows <= 64) return launch_rows<D, kE4m3, 64>(a, tmk, grid, stream);
-  if (a.rows <= 128) return launch_rows<D, kE4m3, 128>(a, tmk, grid, stream);
-  return launch_rows<D, kE4m3, 192>(a, tmk, grid, stream);
+  return launch_rows<D, kE4m3, 64>(a, tmk, grid, stream);
 }
+
+}  // namespace
 
 }  // namespace kv_score
 
@@ -669,16 +526,14 @@ cudaError_t launch_kv_score(const ScoreArgs& p, const KvArgs& c, cudaStream_t st
   kv_score::Args a{};
   a.p = p;
   a.c = c;
-  const int all = p.P * p.G;
-  a.chunks = (all + kv_score::kMaxRows - 1) / kv_score::kMaxRows;
-  a.rows = (all + a.chunks - 1) / a.chunks;
-  a.chunks = (all + a.rows - 1) / a.rows;
   a.box = tree_attn::box_tokens(c.page);
-  // the wait for a unit's query rows: 8 x 32 rows on prompts of 1500 .. 32768 tokens 44 us with one tile, 41 with three
-  a.cost = all > 16 ? 3 : 1;
-  a.sub = kv_score::kSubBytes / (kv_score::kTile * p.D * (c.e4m3 ? 1 : 2));
   CUtensorMap tmk{};
   if (!tree_attn::encode_rows(&tmk, c.k, c, p.D, a.box)) return cudaErrorInvalidValue;
+  if (p.P * p.G > kv_score::kMaxRows) return kv_score::launch_pairs(a, tmk, p.D, stream);
+  a.rows = p.P * p.G;
+  a.chunks = 1;
+  // the wait for a unit's query rows: trees of 48 rows on 129 .. 16384 tokens 38 us with one tile, 34 with three
+  a.cost = a.rows > 16 ? 3 : 1;
   if (p.D == 256) return c.e4m3 ? kv_score::launch_dim<256, true>(a, tmk, sms, stream)
                                 : kv_score::launch_dim<256, false>(a, tmk, sms, stream);
   return c.e4m3 ? kv_score::launch_dim<128, true>(a, tmk, sms, stream)
