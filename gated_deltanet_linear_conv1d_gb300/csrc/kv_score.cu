@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
       // A token's page, then its key's scale and its score so far, are loaded two tiles and one tile ahead of their use.
       auto load_page = [&](int t) {
         const int tok = t * kTile + mine;
-        return t < s.t1 && tok < s.len ? __ldg(table + tok / c.page) : -1;
+        return t < s.t1 && tok < s.len ? __ldg(table + page_of(a, tok)) : -1;
       };
       float key_scale = 1.f, before = 0.f;
       auto load_token = [&](int t, int page, float& ks, float& w) {
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
         ks = 1.f;
         w = 0.f;
         if (page < 0 || page >= c.pages) return;
-        if constexpr (kE4m3) ks = __ldg(c.k_scale + ((size_t)page * c.Hkv + s.h) * c.page + tok % c.page);
+        if constexpr (kE4m3) ks = __ldg(c.k_scale + ((size_t)page * c.Hkv + s.h) * c.page + tok - page_of(a, tok) * c.page);
         if (!fresh && tok < s.ctx) w = out[tok];
       };
       int t = s.t0 + (wg - s.at) % C::kBufs;
@@ -527,6 +527,9 @@ cudaError_t launch_kv_score(const ScoreArgs& p, const KvArgs& c, cudaStream_t st
   a.p = p;
   a.c = c;
   a.box = tree_attn::box_tokens(c.page);
+  a.shift = -1;
+  if ((c.page & (c.page - 1)) == 0)
+    for (a.shift = 0; 1 << a.shift < c.page;) ++a.shift;
   CUtensorMap tmk{};
   if (!tree_attn::encode_rows(&tmk, c.k, c, p.D, a.box)) return cudaErrorInvalidValue;
   if (p.P * p.G > kv_score::kMaxRows) return kv_score::launch_pairs(a, tmk, p.D, stream);

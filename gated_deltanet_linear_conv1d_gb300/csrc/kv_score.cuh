@@ -25,7 +25,11 @@ struct Args {
   int box;           // tokens per TMA box
   int sub;           // tiles that several chunks go through in turn
   int cost;          // what a unit takes beside its tiles, in tiles
+  int shift;         // the page's tokens as a power of two, or -1
 };
+
+// Page of a request's table that has token `tok`. (A division for every token of a tile takes a good part of its time.)
+__device__ __forceinline__ int page_of(const Args& a, int tok) { return a.shift >= 0 ? tok >> a.shift : tok / a.c.page; }
 
 struct Plan {
   long long lo;

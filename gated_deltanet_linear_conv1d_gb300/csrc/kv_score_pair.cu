@@ -24,9 +24,10 @@ namespace {
 constexpr int kPairTile = 2 * kTile;
 constexpr int kHalf = 192;       // rows of a chunk that a CTA keeps
 constexpr int kStepRows = 96;    // of those, at most, in one step
-constexpr int kLoaders = 8;      // warps of the two groups
-constexpr int kCopyWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 320;
+constexpr int kGroups = 4;       // of four warps for the weights
+constexpr int kLoaders = 4 * kGroups;
+constexpr int kCopyWarp = kLoaders, kMmaWarp = kLoaders + 1;
+constexpr int kThreads = 32 * (kLoaders + 2);
 constexpr int kMaxStages = 12;
 constexpr int kColsBuf = 256;    // columns of tensor memory from one buffer to the next
 constexpr int kSums = 4;         // tiles whose sums the groups may have under way: see where they meet
@@ -55,7 +56,7 @@ struct Cfg {
   static constexpr int oLse = kQBytes;
   static constexpr int oSees = oLse + 2 * 2 * kHalf * 4;
   static constexpr int oSum = oSees + 2 * 3 * 2 * kHalf * 4;
-  static constexpr int oBars = oSum + kSums * kTile * 4;
+  static constexpr int oBars = oSum + kSums * kGroups * kTile * 4;
   static constexpr int kRest = oBars + (sizeof(Bars) + 15) / 16 * 16;
   static constexpr int kFit = (kSmemLimit - kRest) / (int)kBlock;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
@@ -133,7 +134,8 @@ __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned 
   const ScoreArgs& p = a.p;
   const int lane = threadIdx.x & 31, b = seg & 1;
   const Rows rows(a.rows);
-  const int held = rows.steps * rows.hs, per = held / kLoaders, first = share * per;
+  const int held = rows.steps * rows.hs, most_rows = (held + kLoaders - 1) / kLoaders, first = min(held, share * most_rows);
+  const int per = min(most_rows, held - first);
   const uint32_t q_block = held * 128;
   const int r0 = s.c * a.rows, all = min(a.rows, p.P * p.G - r0);
   const float* lse_g = p.lse + (size_t)s.n * p.P * p.Hq + s.h * p.G;
@@ -145,7 +147,7 @@ __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned 
   // piece `lane` (16 bytes) of row q: where it lies, bf16 values
   const uint32_t q_a = smem_u32(rest) + (lane >> 3) * q_block, piece_at = lane & 7;
   auto piece = [&](int q) { return q_a + q * 128 + ((piece_at ^ (q & 7)) << 4); };
-  const int mine = rows.of(pr, first + min(lane, per - 1)), from = lane < per && mine < all ? row_of(mine) : -1;
+  const int mine = rows.of(pr, first + lane), from = lane < per && mine < all ? row_of(mine) : -1;
   const uint32_t there = __ballot_sync(0xffffffffu, from >= 0);
 #pragma unroll 8
   for (int i = 0; i < per; ++i) {
@@ -405,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const Args a, const _
     // ------------------------------------------------------------ weights: a group has half of the columns
     // A thread has four of its warp's tokens (lane / 4 + 8 k) with a quarter of the rows (2 (lane % 4) and the next of every
     // eight), so that what goes by the row is loaded for four tokens at once; at the end it has one token's sum.
-    const int g = warp >> 2, w4 = warp & 3, a4 = lane & 3, mine = 32 * w4 + (lane >> 2) + 8 * a4;
+    const int g = warp >> 3, part = warp >> 2 & 1, w4 = warp & 3, a4 = lane & 3, mine = 32 * w4 + (lane >> 2) + 8 * a4;
     float* sums = reinterpret_cast<float*>(rest + C::oSum);
     Walk<kPairTile> walk(a, plan);
     Seg s;
@@ -419,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const Args a, const _
       auto token_of = [&](int t) { return t * kPairTile + pr * kTile + mine; };
       auto load_page = [&](int t) {
         const int tok = token_of(t);
-        return t < s.t1 && tok < s.len ? __ldg(table + tok / c.page) : -1;
+        return t < s.t1 && tok < s.len ? __ldg(table + page_of(a, tok)) : -1;
       };
       const bool again = s.c > 0, old = again || !fresh;
       const float decay = again ? 1.f : p.decay;
@@ -429,8 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const Args a, const _
         key_scale = 1.f;
         before = 0.f;
         if (page < 0 || page >= c.pages) return;
-        if constexpr (kE4m3) key_scale = __ldg(c.k_scale + ((size_t)page * c.Hkv + s.h) * c.page + tok % c.page);
-        if (g == 0 && old && (again || tok < s.ctx)) before = out[tok];
+        if constexpr (kE4m3) key_scale = __ldg(c.k_scale + ((size_t)page * c.Hkv + s.h) * c.page + tok - page_of(a, tok) * c.page);
+        if (t % kGroups == warp >> 2 && old && (again || tok < s.ctx)) before = out[tok];
       };
       int page = load_page(s.t0), next_page = load_page(s.t0 + 1);
       load_token(s.t0, page);
@@ -443,8 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const Args a, const _
       if (lane == 0) arrive_both(&B->q_full[b2]);
       wait_cluster(&B->q_full[b2], (seg >> 1) & 1, abort);
       __syncwarp();
-      const volatile int* d8 = B->dead[b2];
-      const bool dead = (d8[0] | d8[1] | d8[2] | d8[3] | d8[4] | d8[5] | d8[6] | d8[7]) != 0;
+      const bool dead = __any_sync(0xffffffffu, lane < kLoaders && *(volatile int*)&B->dead[b2][lane % kLoaders] != 0);
       const float f0 = *(volatile float*)&B->factor[b2][g];
       const float* lse_h = reinterpret_cast<const float*>(rest + C::oLse) + (b2 * 2 + g) * kHalf + 2 * a4;
       const uint32_t* sees_h = reinterpret_cast<const uint32_t*>(rest + C::oSees) + b2 * 3 * 2 * kHalf + g * kHalf + 2 * a4;
@@ -467,7 +468,9 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const Args a, const _
         for (int sub = 0; sub < rows.steps; ++sub, ++step) {
           const int b = step & 1;
           const float* lse = lse_h + sub * rows.hs;
-          const int here = max(0, min(rows.hs, all - (2 * sub + g) * rows.hs));  // rows of this step's that there are
+          // rows of this step's that there are, and of those the group's
+          const int half = max(0, min(rows.hs, all - (2 * sub + g) * rows.hs)), mid = (half + 31) / 32 * 16;
+          const int from = part ? mid : 0, here = part ? half : min(mid, half);
           // Sixteen rows at a time, their scores and constants loaded while the sixteen before are worked on. (With 32, or
           // with all constants in registers, the compiler has too few left to let the chains of several rows run side by
           // side: 96 rows took 1.5 us.)
@@ -530,15 +533,15 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const Args a, const _
             else some(u, l, r0);
           };
           float2 lu[2], lv[2];
-          constants(0, lu);
-          constants(16, lv);
+          constants(from, lu);
+          constants(from + 16, lv);
           wait_warp(&B->s_full[b], (step >> 1) & 1, abort);
           umma::fence_after_sync();
           const uint32_t ts = umma::taddr(tmem, 32 * w4, b * kColsBuf + g * rows.hs);
           Scores u, v;
-          if (here > 0) u.load(ts);
+          if (from < here) u.load(ts + from);
 #pragma unroll 1
-          for (int r0 = 0; r0 < here; r0 += 32) {
+          for (int r0 = from; r0 < here; r0 += 32) {
             u.wait();
             if (r0 + 16 < here) v.load(ts + r0 + 16);
             work(u, lu, r0);
@@ -555,23 +558,25 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const Args a, const _
           if (lane == 0) arrive_cluster(cluster_addr(&B->s_empty[b], 0));
         }
         // the four lanes' parts of their four tokens: after two exchanges each lane has its own token's
-        float part[4];
+        float mix[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) part[k] = sum[k][0] + sum[k][1];
+        for (int k = 0; k < 4; ++k) mix[k] = sum[k][0] + sum[k][1];
         const bool up = a4 & 2, odd = a4 & 1;
-        const float even_part = (up ? part[2] : part[0]) + __shfl_xor_sync(0xffffffffu, up ? part[0] : part[2], 2);
-        const float odd_part = (up ? part[3] : part[1]) + __shfl_xor_sync(0xffffffffu, up ? part[1] : part[3], 2);
+        const float even_part = (up ? mix[2] : mix[0]) + __shfl_xor_sync(0xffffffffu, up ? mix[0] : mix[2], 2);
+        const float odd_part = (up ? mix[3] : mix[1]) + __shfl_xor_sync(0xffffffffu, up ? mix[1] : mix[3], 2);
         float total = (odd ? odd_part : even_part) + __shfl_xor_sync(0xffffffffu, odd ? even_part : odd_part, 1);
-        // The groups meet: the second one's sum by way of shared memory. It may be two steps ahead, since the first one has
-        // read a step's scores before the next but one's are made, so there are sums and barriers for the tiles of that.
-        float* other = sums + tile % kSums * kTile + mine;
-        if (g == 1) {
-          *other = total;
-          asm volatile("bar.arrive %0, 256;" ::"r"(2 + tile % kSums) : "memory");
+        // The groups meet: the others' sums by way of shared memory to the one whose turn it is (by the tile, whatever the
+        // chunk). They may be two steps ahead, since it has read a step's scores before the next but one's are made, so there
+        // are sums and barriers for the tiles of that.
+        float* all_sums = sums + tile % kSums * kGroups * kTile + mine;
+        if (t % kGroups != warp >> 2) {
+          all_sums[(warp >> 2) * kTile] = total;
+          asm volatile("bar.arrive %0, %1;" ::"r"(2 + tile % kSums), "n"(32 * kLoaders) : "memory");
           continue;
         }
-        asm volatile("bar.sync %0, 256;" ::"r"(2 + tile % kSums) : "memory");
-        total += *other;
+        asm volatile("bar.sync %0, %1;" ::"r"(2 + tile % kSums), "n"(32 * kLoaders) : "memory");
+#pragma unroll
+        for (int k = 1; k < kGroups; ++k) total += all_sums[((warp >> 2) + k) % kGroups * kTile];
         if (tok < s.len && !*(volatile int*)abort) {
           if (this_page < 0 || this_page >= c.pages) report(p.dev_err, GDN_DEVERR_SLOT);
           else out[tok] = fmaf(w, decay, total);
