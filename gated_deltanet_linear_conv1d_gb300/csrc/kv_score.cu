@@ -25,7 +25,8 @@ namespace {
 
 constexpr int kMaxRows = 64;   // more go to pairs
 constexpr int kGroups = 2;     // of four warps for the weights
-constexpr int kCopyWarp = 4 * kGroups, kMmaWarp = kCopyWarp + 1, kQueryWarp = kCopyWarp + 2, kQueryWarps = 2;
+constexpr int kCopyWarp = 4 * kGroups, kCopyWarps = 2, kMmaWarp = kCopyWarp + kCopyWarps, kQueryWarp = kMmaWarp + 1,
+              kQueryWarps = 4;
 constexpr int kLoaders = 4 * kGroups + kQueryWarps;  // all but those of the copies and the MMAs
 constexpr int kThreads = 32 * (kQueryWarp + kQueryWarps);
 constexpr int kMaxStages = 12;
@@ -242,10 +243,11 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
     if (share >= 4 * kGroups && lane == 0) arrive(&B->q_full[qb]);
   };
 
-  if (warp == kCopyWarp) {
+  if (warp >= kCopyWarp && warp < kMmaWarp) {
     // ------------------------------------------------------------ copies
+    // The warps take the blocks in turn: a box takes one about 100 cycles, and of pages of 16 tokens there are eight a block.
     // The pages of `span` tiles are loaded at once, a lane per box, and the next tiles' before these are copied.
-    const int boxes = kTile / a.box, total_rows = c.slots * c.Hkv, span = 32 / boxes;
+    const int boxes = kTile / a.box, total_rows = c.slots * c.Hkv, span = 32 / boxes, mine = warp - kCopyWarp;
     int st = 0, phase = 1, issued = 0;
     bool ok = true;
     Walk<kTile> walk(a, plan);
@@ -267,11 +269,14 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
         for (int t = t0; t < min(cur.t1, t0 + span) && ok; ++t) {
           const int r = __shfl_sync(0xffffffffu, row, (t - t0) * boxes + lane % boxes);
           for (int b = 0; b < C::kBlk; ++b) {
-            ok = __all_sync(0xffffffffu, ok && wait(&B->empty[st], phase, abort));
-            if (!ok) break;
-            if (elect_one()) mbar_arrive_expect_tx(&B->full[st], kBlock);
-            __syncwarp();
-            if (lane < boxes) tma_load_2d(smem + st * kBlock + lane * a.box * 128, &tmk, b * (kE4m3 ? 128 : 64), r, &B->full[st]);
+            if (issued % kCopyWarps == mine) {
+              ok = __all_sync(0xffffffffu, ok && wait(&B->empty[st], phase, abort));
+              if (!ok) break;
+              if (lane == 0) mbar_arrive_expect_tx(&B->full[st], kBlock);
+              __syncwarp();
+              if (lane < boxes)
+                tma_load_2d(smem + st * kBlock + lane * a.box * 128, &tmk, b * (kE4m3 ? 128 : 64), r, &B->full[st]);
+            }
             ++issued;
             if (++st == C::kStages) st = 0, phase ^= 1;
           }
@@ -281,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
     // copies in flight land before the CTA may leave
     if (!ok)
       for (int k = max(0, issued - C::kStages); k < issued; ++k)
-        if (!mbar_wait_bounded(&B->full[k % C::kStages], (k / C::kStages) & 1)) break;
+        if (k % kCopyWarps == mine && !mbar_wait_bounded(&B->full[k % C::kStages], (k / C::kStages) & 1)) break;
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMAs
     const int rp = (a.rows + 15) / 16 * 16;
@@ -394,11 +399,10 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
         const float f = kE4m3 ? f0 * ks : f0;
         const int node = t * kTile + mine - s.ctx;
         const bool masked = (t + 1) * kTile > s.ctx;
-        constexpr int kN = kRows < 32 ? 16 : 32;  // rows at a time
+        constexpr int kN = 16;  // rows at a time
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
         auto load = [&](int r0, uint32_t (&u)[kN]) {
-          if constexpr (kN == 32) umma::ld32_nowait(ts + r0, u);
-          else umma::ld16_nowait(ts + r0, u);
+          umma::ld16_nowait(ts + r0, u);
         };
         auto constants = [&](int r0, float4 (&l)[kN / 4]) {
 #pragma unroll
