@@ -9,7 +9,7 @@
 // S^T [128 tokens x rows] = K Q^T on the tensor cores (tcgen05): the keys are the first operand, from shared memory as
 // they lie in the cache, so a token is a lane of tensor memory, and its sum over the rows is one thread's, in the order of
 // the rows. An E4M3 cache stays E4M3, and Q (bf16, scaled by a power of two) is written as the sum of two E4M3 terms, exact
-// down to 2^-17 of the largest value; the second term's MMAs add to the same columns.
+// down to 2^-17 of the largest value; the two are columns of one MMA, added as they are read.
 //
 // Work. The tiles of 128 tokens of all (request, kv head) units stand in one line, cut into equal pieces, one per CTA. A
 // unit's rows, up to 64, stay in shared memory for its tiles; more go to kv_score_pair.cu.
@@ -48,8 +48,7 @@ struct Cfg {
   static constexpr int kBlk = D * (kE4m3 ? 1 : 2) / 128;  // ring blocks of a tile
   static constexpr int kTerms = kE4m3 ? 2 : 1;
   static constexpr int kBufs = kGroups;                    // tiles' scores in tensor memory
-  static constexpr int kCols = 2 * kRows;
-  static_assert(kBufs * kRows <= kCols, "tensor memory");
+  static constexpr int kCols = 2 * kTerms * kRows;
   static constexpr int kQBytes = kRows * D * 2;            // query rows of a segment
   // behind the ring, for two segments each: Q, then by row -lse to base 2, and the nodes that the row sees (in two words)
   static constexpr int oLse = 2 * kQBytes;
@@ -72,7 +71,7 @@ __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned 
   using C = Cfg<D, kE4m3, kRows>;
   const ScoreArgs& p = a.p;
   const int lane = threadIdx.x & 31, rp = (a.rows + 15) / 16 * 16;
-  const uint32_t q_block = rp * 128, lower = (1u << lane) - 1u;
+  const uint32_t q_block = C::kTerms * rp * 128, lower = (1u << lane) - 1u;
   const int r0 = s.c * a.rows, all = min(a.rows, p.P * p.G - r0), b = seg & 1;
   const int per = (all + shares - 1) / shares;
   unsigned char* q_s = rest + b * C::kQBytes;
@@ -94,7 +93,7 @@ __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned 
     l_all[g] = r < end ? __ldg(lse_g + row_of(r)) : INFINITY;
   }
   // piece `lane` (16 bytes) of row r: where it lies, bf16 values
-  const uint32_t q_a = smem_u32(q_s) + (lane >> 3) * q_block, piece_at = lane & 7;
+  const uint32_t q_a = smem_u32(q_s) + (lane >> 3) / C::kTerms * q_block + (lane >> 3) % C::kTerms * rp * 128, piece_at = lane & 7;
   auto piece = [&](int r) { return q_a + r * 128 + ((piece_at ^ (r & 7)) << 4); };
   auto copy = [&](int r, int from) {
     if (lane < D / 8)
@@ -182,7 +181,7 @@ __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned 
       if (lane < D / 8) {
         unsigned char* blk = q_s + (lane >> 4) * q_block + swz(r, (lane & 15) * 8);
         *reinterpret_cast<uint2*>(blk) = make_uint2(__byte_perm(t[0], t[1], 0x5410), __byte_perm(t[2], t[3], 0x5410));
-        *reinterpret_cast<uint2*>(blk + C::kBlk * q_block) =
+        *reinterpret_cast<uint2*>(blk + rp * 128) =
             make_uint2(__byte_perm(t[0], t[1], 0x7632), __byte_perm(t[2], t[3], 0x7632));
       }
     }
@@ -290,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMAs
     const int rp = (a.rows + 15) / 16 * 16;
-    const uint32_t q_block = rp * 128;
+    const uint32_t q_block = C::kTerms * rp * 128;
     constexpr uint32_t kKind = kE4m3 ? umma::kKindF8 : umma::kKindF16, kType = kE4m3 ? umma::kE4M3 : umma::kBF16;
     const uint32_t ring = smem_u32(smem), sQ = smem_u32(rest);
     int st = 0, phase = 0, seg = 0;
@@ -306,7 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
     while (ok && walk.next(a, s)) {
       const int qb = seg & 1;
       if (!wait_all(&B->q_full[seg & 1], (seg >> 1) & 1)) break;
-      const int cols = max(16, (*(volatile int*)&B->rows[seg & 1] + 15) / 16 * 16);
+      // bf16: the rows that there are; E4M3: the two terms of a row are rp columns apart
+      const int cols = kE4m3 ? 2 * rp : max(16, (*(volatile int*)&B->rows[seg & 1] + 15) / 16 * 16);
       const uint32_t id = umma::idesc(kType, false, false, kTile, cols);
       for (int t = s.t0; t < s.t1 && ok; ++t) {
         const int b = (s.at + t - s.t0) % C::kBufs;
@@ -317,13 +317,10 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
           umma::fence_after_sync();
           if (elect_one()) {
             const uint64_t ka = umma::smem_desc_sw128(ring + st * kBlock);
+            const uint64_t qa = umma::smem_desc_sw128(sQ + qb * C::kQBytes + kb * q_block);
 #pragma unroll
-            for (int term = 0; term < C::kTerms; ++term) {
-              const uint64_t qa = umma::smem_desc_sw128(sQ + qb * C::kQBytes + (term * C::kBlk + kb) * q_block);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                umma::mma<kKind>(tmem + b * kRows, ka + 2 * k, qa + 2 * k, id, kb + term + k > 0);
-            }
+            for (int k = 0; k < 4; ++k)
+              umma::mma<kKind>(tmem + b * C::kTerms * kRows, ka + 2 * k, qa + 2 * k, id, kb + k > 0);
             umma::commit(&B->empty[st]);
             if (kb == C::kBlk - 1) {
               umma::commit(&B->s_full[b]);
@@ -353,6 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
   } else {
     // ------------------------------------------------------------ weights: thread = token
     const int wg = warp >> 2, w4 = warp & 3, mine = 32 * w4 + lane;
+    const int rp = (a.rows + 15) / 16 * 16;
     const float* lse_s = reinterpret_cast<const float*>(rest + C::oLse);
     const uint32_t* sees_s = reinterpret_cast<const uint32_t*>(rest + C::oSees);
     Walk<kTile> walk(a, plan);
@@ -395,14 +393,26 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
         load_token(t + C::kBufs, page, key_scale, before);
         wait_warp(&B->s_full[wg], used & 1, abort);
         umma::fence_after_sync();
-        const uint32_t ts = umma::taddr(tmem, 32 * w4, wg * kRows);
+        const uint32_t ts = umma::taddr(tmem, 32 * w4, wg * C::kTerms * kRows);
         const float f = kE4m3 ? f0 * ks : f0;
         const int node = t * kTile + mine - s.ctx;
         const bool masked = (t + 1) * kTile > s.ctx;
         constexpr int kN = 16;  // rows at a time
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        auto load = [&](int r0, uint32_t (&u)[kN]) {
-          umma::ld16_nowait(ts + r0, u);
+        struct Scores {
+          uint32_t u[kN], v[kE4m3 ? kN : 1];  // v: the second terms'
+        };
+        auto load = [&](int r0, Scores& x) {
+          umma::ld16_nowait(ts + r0, x.u);
+          if constexpr (kE4m3) umma::ld16_nowait(ts + rp + r0, x.v);
+        };
+        auto arrived = [&](Scores& x) {
+          loaded(x.u);
+          if constexpr (kE4m3) {
+            loaded(x.v);
+#pragma unroll
+            for (int i = 0; i < kN; ++i) x.u[i] = __float_as_uint(__uint_as_float(x.u[i]) + __uint_as_float(x.v[i]));
+          }
         };
         auto constants = [&](int r0, float4 (&l)[kN / 4]) {
 #pragma unroll
@@ -453,22 +463,22 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
               }
           }
         };
-        uint32_t u[kN], v[kN];  // one is on its way while the other is worked on
+        Scores x, y;  // one is on its way while the other is worked on
         float4 l[kN / 4];
-        load(0, u);
+        load(0, x);
         constants(0, l);
 #pragma unroll 1
         for (int r0 = 0; r0 < rows; r0 += 2 * kN) {
           const int r1 = r0 + kN, r2 = r0 + 2 * kN;
           const bool more = kRows > kN && r1 < rows;
-          loaded(u);
-          if (more) load(r1, v);
-          compute(r0, u, l);
+          arrived(x);
+          if (more) load(r1, y);
+          compute(r0, x.u, l);
           if (more) {
             constants(r1, l);
-            loaded(v);
-            if (r2 < rows) load(r2, u);
-            compute(r1, v, l);
+            arrived(y);
+            if (r2 < rows) load(r2, x);
+            compute(r1, y.u, l);
             if (r2 < rows) constants(r2, l);
           }
         }
