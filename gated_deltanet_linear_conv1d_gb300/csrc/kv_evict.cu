@@ -19,7 +19,7 @@ namespace {
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kFew = 256;  // weights at the border that are put in order all at once
+constexpr int kFew = 64;  // weights at the border that are put in order all at once
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -42,10 +42,10 @@ __device__ __forceinline__ int load_remote(const int* mine, uint32_t rank) {
 // The limits of request n: how many tokens it keeps, -1 if none are to be touched (a padding request, *why 0, or one
 // that breaks a limit).
 __device__ __forceinline__ int kept_of(const EvictArgs& p, const KvArgs& c, int n, int* why) {
-  const int len = __ldg(p.len + n), slot = __ldg(p.slot + n);
+  const int len = __ldg(p.len + n), slot = __ldg(p.slot + n), dst = __ldg(p.dst_slot + n), budget = __ldg(p.budget + n);
+  const int m = min(len, budget);
   *why = 0;
   if (len < 0 || slot < 0) return -1;
-  const int dst = __ldg(p.dst_slot + n), budget = __ldg(p.budget + n), m = min(len, budget);
   if (slot >= p.Rs || dst < 0 || dst >= p.Rs) *why |= GDN_DEVERR_SLOT;
   if (budget < 0 || m > p.max_kept || len > p.max_tokens || (len - 1) / c.page >= p.max_pages ||
       (m > 0 && (m - 1) / c.page >= p.dst_max_pages))
@@ -67,10 +67,11 @@ __device__ __forceinline__ uint32_t key_of(float w) {
 template <int kSplit, int kHeld>
 __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel(const EvictArgs p, const KvArgs c) {
   constexpr int kBatch = kSelThreads * kHeld;
-  __shared__ int hist[256 * 32];                     // [bin][lane]: no two lanes of a warp at one bank
+  __shared__ __align__(16) int hist[256 * 32];       // [bin][lane]: no two lanes of a warp at one bank
   __shared__ int bins[256], above_s[8], scan_s[2][kSelWarps];
   __shared__ int pick[3];                            // the bin of the m-th largest, those above it, and in it
-  __shared__ uint32_t few_s[kFew], own_few_s[kFew];
+  __shared__ __align__(16) uint32_t few_s[kFew];
+  __shared__ uint32_t own_few_s[kFew];
   __shared__ int few, border_s[2];
   __shared__ int totals[2];                          // of this CTA: weights above the border, and equal to it
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -117,10 +118,12 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
   if (sift && held) load(0);
   bool bad = false;
   if (m >= 0) {
+#pragma unroll 4
     for (int i = tid; (long long)i * c.page < len; i += kSelThreads) {
       const int page = __ldg(p.table + (size_t)n * p.max_pages + i);
       bad |= page < 0 || page >= c.pages;
     }
+#pragma unroll 4
     for (int i = tid; (long long)i * c.page < m; i += kSelThreads) {
       const int page = __ldg(p.dst_table + (size_t)n * p.dst_max_pages + i);
       bad |= page < 0 || page >= c.pages;
@@ -201,28 +204,51 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
     if (shift > 0 && in_bin <= kFew) {
       uint32_t* own = kSplit > 1 ? own_few_s : few_s;
       batches([&] {
+        uint32_t in = 0;
 #pragma unroll
-        for (int j = 0; j < kHeld; ++j)
-          if (j < valid && key[j] >> shift == border >> shift) own[atomicAdd(&few, 1)] = key[j];
+        for (int j = 0; j < kHeld; ++j) in |= (j < valid && key[j] >> shift == border >> shift ? 1u : 0u) << j;
+        int upto = __popc(in);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, upto, d);
+          if (lane >= d) upto += o;
+        }
+        int at = 0;
+        if (lane == 31 && upto > 0) at = atomicAdd(&few, upto);
+        at = __shfl_sync(0xffffffffu, at, 31) + upto - __popc(in);
+        if (in) {
+#pragma unroll
+          for (int j = 0; j < kHeld; ++j)
+            if (in >> j & 1) own[at++] = key[j];
+        }
       });
       if constexpr (kSplit > 1) {  // every CTA's, one after the other
         cluster_sync();
-        int at = 0;
+        const int theirs = lane < kSplit ? load_remote(&few, lane) : 0;
+        int upto = theirs;
+#pragma unroll
+        for (int d = 1; d < kSplit; d <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, upto, d);
+          if (lane >= d) upto += o;
+        }
+#pragma unroll
         for (int r = 0; r < kSplit; ++r) {
-          const int theirs = load_remote(&few, r);
-          if (tid < theirs) few_s[at + tid] = (uint32_t)load_remote(reinterpret_cast<const int*>(own_few_s) + tid, r);
-          at += theirs;
+          const int n_r = __shfl_sync(0xffffffffu, theirs, r), at = __shfl_sync(0xffffffffu, upto, r) - n_r;
+          if (tid < n_r) few_s[at + tid] = (uint32_t)load_remote(reinterpret_cast<const int*>(own_few_s) + tid, r);
         }
       }
+      if (tid >= in_bin && tid < kFew) few_s[tid] = 0;  // below all that are in the bin, or counted as the least of them
       __syncthreads();
       if (tid < in_bin) {
         const uint32_t mine_key = few_s[tid];
-        int above = 0, same = 0;
-        for (int i = 0; i < in_bin; ++i) {
-          above += few_s[i] > mine_key;
-          same += few_s[i] == mine_key;
+        int above = 0, reach = 0;  // larger ones, and those as large too
+#pragma unroll 4
+        for (int i = 0; i < in_bin; i += 4) {
+          const uint4 x = *reinterpret_cast<const uint4*>(few_s + i);
+          above += (x.x > mine_key) + (x.y > mine_key) + (x.z > mine_key) + (x.w > mine_key);
+          reach += (x.x >= mine_key) + (x.y >= mine_key) + (x.z >= mine_key) + (x.w >= mine_key);
         }
-        if (above < need && above + same >= need) border_s[0] = (int)mine_key, border_s[1] = need - above;
+        if (above < need && reach >= need) border_s[0] = (int)mine_key, border_s[1] = need - above;
       }
       if constexpr (kSplit > 1) cluster_sync();  // the others' have been read
       else __syncthreads();
@@ -253,10 +279,12 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
       atomicAdd(&totals[1], equal);
     }
     cluster_sync();
-    for (int r = 0; r < rank; ++r) {
-      over_before += load_remote(&totals[0], r);
-      equal_before += load_remote(&totals[1], r);
+    if (lane < rank) {
+      over_before = load_remote(&totals[0], lane);
+      equal_before = load_remote(&totals[1], lane);
     }
+    over_before = __reduce_add_sync(0xffffffffu, over_before);
+    equal_before = __reduce_add_sync(0xffffffffu, equal_before);
     cluster_sync();  // no CTA leaves while another reads its shared memory
   }
   int buf = 0, base = 0;
@@ -264,9 +292,12 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
     uint32_t is_over = 0, is_equal = 0;
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
-      is_over |= (j < valid && key[j] > border ? 1u : 0u) << j;
-      is_equal |= (j < valid && key[j] == border ? 1u : 0u) << j;
+      is_over |= (key[j] > border ? 1u : 0u) << j;
+      is_equal |= (key[j] == border ? 1u : 0u) << j;
     }
+    const uint32_t real = valid == 32 ? ~0u : (1u << valid) - 1u;
+    is_over &= real;
+    is_equal &= real;
     const int mine = __popc(is_over) | __popc(is_equal) << 16;  // no more than kBatch of each
     int upto = mine;
 #pragma unroll
@@ -284,14 +315,22 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
       if (lane >= d) sums += o;
     }
     const int before = __shfl_sync(0xffffffffu, sums - theirs, warp) + upto - mine, all = __shfl_sync(0xffffffffu, sums, 31);
-    int o = over_before + (before & 0xffff), e = equal_before + (before >> 16);
+    // by way of shared memory, where the threads' runs of them join
+    const int from = over_before + min(equal_before, need);
+    const int until = over_before + (all & 0xffff) + min(equal_before + (all >> 16), need);
     const int i = lo + base + tid * kHeld;
-#pragma unroll
-    for (int j = 0; j < kHeld; ++j) {
-      const bool eq = is_equal >> j & 1, ov = is_over >> j & 1;
-      if (ov || (eq && e < need)) kept[o + min(e, need)] = i + j;
-      o += ov;
-      e += eq;
+    constexpr int kRoom = 256 * 32;
+    // this thread's: those above the border, and of those at it the ones that are needed
+    const int o = over_before + (before & 0xffff), e = equal_before + (before >> 16);
+    int spare = __popc(is_equal) - max(0, need - e);
+    for (; spare > 0 && is_equal; --spare) is_equal ^= 0x80000000u >> __clz(is_equal);
+    for (int at = from; at < until; at += kRoom) {
+      int to = o + min(e, need) - at;
+      for (uint32_t left = is_over | is_equal; left; left &= left - 1, ++to)
+        if (to >= 0 && to < kRoom) hist[to] = i + __ffs(left) - 1;
+      __syncthreads();
+      for (int k = tid; k < min(kRoom, until - at); k += kSelThreads) kept[at + k] = hist[k];
+      __syncthreads();
     }
     over_before += all & 0xffff;
     equal_before += all >> 16;
