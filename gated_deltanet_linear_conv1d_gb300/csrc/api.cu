@@ -661,7 +661,10 @@ gdn_status gdn_kv_evict(const gdn_kv_cache* cache, const int32_t* block_table, i
   if ((long long)num_seqs * c.Hkv > 1 << 28) return GDN_ERR_UNSUPPORTED;  // blocks are counted in 32 bits
   st = check_score(score, slot_idx, num_slots, max_tokens);
   if (st != GDN_OK) return st;
-  if (!block_table || max_pages == 0 || !length || !budget || !new_len || new_len == length || (!kept && max_kept > 0))
+  if (!block_table || max_pages == 0 || !length || !budget || !new_len || (!kept && max_kept > 0))
+    return GDN_ERR_INVALID_ARG;
+  if (new_len == length || new_len == budget || new_len == slot_idx || new_len == dst_slot || new_len == block_table ||
+      new_len == dst_table)
     return GDN_ERR_INVALID_ARG;
   EvictArgs a{block_table, dst_table ? dst_table : block_table, length, budget, score, slot_idx,
               dst_slot ? dst_slot : slot_idx, kept, new_len, sink_tokens, recent_tokens, num_slots, max_tokens, max_pages,

@@ -38,7 +38,8 @@ struct Bars {
   int abort;
   int rows[2];      // of the segment, without those that add nothing
   float factor[2];  // what takes its scores to base 2
-  uint32_t most[kLoaders];
+  uint32_t most[kLoaders], least[kLoaders];
+  int uneven[2];    // rows have factors of their own
   Plan plan;
   long long warp_total[kThreads / 32];
 };
@@ -53,7 +54,8 @@ struct Cfg {
   // behind the ring, for two segments each: Q, then by row -lse to base 2, and the nodes that the row sees (in two words)
   static constexpr int oLse = 2 * kQBytes;
   static constexpr int oSees = oLse + 2 * kRows * 4;
-  static constexpr int oBars = oSees + 2 * 2 * kRows * 4;
+  static constexpr int oOwn = oSees + 2 * 2 * kRows * 4;  // by row, its own factor (E4M3)
+  static constexpr int oBars = oOwn + (kE4m3 ? 2 * kRows * 4 : 0);
   static constexpr int kRest = oBars + (sizeof(Bars) + 15) / 16 * 16;
   static constexpr int kFit = (kSmemLimit - kRest) / (int)kBlock;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
@@ -63,8 +65,7 @@ struct Cfg {
 // The query rows of a segment, number `seg` of the piece, as rows of the MMAs' second operand, with their constants. Rows
 // that add nothing (without a finite lse) are left out: the others move up. `shares` warps have an equal part of the rows
 // each, a lane what goes by the row. The rows are copied past the registers, all of them on their way at once. An E4M3
-// cache's are then taken apart into their two terms in place (a row's 2 D bytes are its own), by one power of two for all
-// of them: what a score is off by counts as such, whatever the row's size.
+// cache's are then taken apart into their two terms in place (a row's 2 D bytes are its own).
 template <int D, bool kE4m3, int kRows>
 __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned char* rest, Bars* B, int seg, int share,
                                           int shares) {
@@ -146,31 +147,32 @@ __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned 
       return max(m & 0xffffu, m >> 16);
     };
     constexpr uint32_t kInf = 0x7f80u;
-    uint32_t most = 0;
+    uint32_t row_most = 0;  // of row begin + lane
 #pragma unroll 4
-    for (int r = begin; r < at; ++r) most = max(most, largest(values(r)));
-    if (__any_sync(0xffffffffu, most >= kInf)) {  // rows with values that are no numbers have no scores, and no say in it
-      most = 0;
-      for (int r = begin; r < at; ++r) {
-        const uint32_t m = largest(values(r));
-        if (__any_sync(0xffffffffu, m >= kInf)) {
-          if (lane == 0) lse[r] = __uint_as_float(0x7fffffffu);
-        } else {
-          most = max(most, m);
-        }
-      }
+    for (int r = begin; r < at; ++r) {
+      const uint32_t m = __reduce_max_sync(0xffffffffu, largest(values(r)));
+      if (lane == r - begin) row_most = m;
     }
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 0) B->most[share] = most;
+    if (row_most >= kInf) {  // a row with values that are no numbers has no scores, and no say in it
+      lse[begin + lane] = __uint_as_float(0x7fffffffu);
+      row_most = 0;
+    }
+    uint32_t most = __reduce_max_sync(0xffffffffu, row_most);
+    uint32_t least = __reduce_min_sync(0xffffffffu, row_most > 0 ? row_most : ~0u);
+    if (lane == 0) B->most[share] = most, B->least[share] = least;
     asm volatile("bar.sync 1, %0;" ::"r"(32 * shares) : "memory");
     most = __reduce_max_sync(0xffffffffu, lane < shares ? B->most[lane] : 0u);
+    least = __reduce_min_sync(0xffffffffu, lane < shares ? B->least[lane] : ~0u);
     asm volatile("bar.sync 1, %0;" ::"r"(32 * shares) : "memory");  // before the next segment's
-    // a power of two that takes the largest value below 256
-    const int up = most == 0 ? 0 : min(134 - (int)(most >> 7), 120);
-    const float by = __uint_as_float((uint32_t)(up + 127) << 23);
-    if (share == 0 && lane == 0) B->factor[b] = f0 * __uint_as_float((uint32_t)(127 - up) << 23);
+    const int up = power_of(most), own = power_of(row_most, most);
+    if (lane < at - begin) reinterpret_cast<float*>(rest + C::oOwn)[b * kRows + begin + lane] = two_to(up - own);
+    if (share == 0 && lane == 0) {
+      B->factor[b] = f0 * two_to(-up);
+      B->uneven[b] = smaller(least, most);
+    }
 #pragma unroll 2
     for (int r = begin; r < at; ++r) {
+      const float by = two_to(__shfl_sync(0xffffffffu, own, r - begin));
       const uint4 raw = values(r);
       const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
       uint32_t t[4];  // first terms of two values, then their second ones
@@ -385,6 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
       const float f0 = *(volatile float*)&B->factor[rb];
       const float* lse = lse_s + rb * kRows;
       const uint32_t* sees = sees_s + rb * 2 * kRows;
+      const float* own = reinterpret_cast<const float*>(rest + C::oOwn) + rb * kRows;
+      const bool uneven = kE4m3 && *(volatile int*)&B->uneven[rb] != 0;
       for (; t < s.t1; t += C::kBufs, ++used) {
         const int this_page = page;
         const float ks = key_scale, w = before;
@@ -420,22 +424,22 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
         };
         // The weights of four rows' scores. (Two at a time in packed operations, 32 rows took 443 cycles of a warp alone,
         // 198 like this; the exponentials' pipe is busy for 128.)
-        auto weights = [&](const uint32_t* u, const float4& l, float (&e)[4]) {
-          e[0] = ex2(fmaf(__uint_as_float(u[0]), f, l.x));
-          e[1] = ex2(fmaf(__uint_as_float(u[1]), f, l.y));
-          e[2] = ex2(fmaf(__uint_as_float(u[2]), f, l.z));
-          e[3] = ex2(fmaf(__uint_as_float(u[3]), f, l.w));
+        auto weights = [&](const uint32_t* u, const float4& l, float (&e)[4], const float4& f) {
+          e[0] = ex2(fmaf(__uint_as_float(u[0]), f.x, l.x));
+          e[1] = ex2(fmaf(__uint_as_float(u[1]), f.y, l.y));
+          e[2] = ex2(fmaf(__uint_as_float(u[2]), f.z, l.z));
+          e[3] = ex2(fmaf(__uint_as_float(u[3]), f.w, l.w));
         };
         auto add = [&](const float (&e)[4]) {
 #pragma unroll
           for (int y = 0; y < 4; ++y) sum[y] += e[y];
         };
         auto compute = [&](int r0, const uint32_t (&u)[kN], const float4 (&l)[kN / 4]) {
-          if (!masked && r0 + kN <= rows) {  // no branch inside: the chains of all rows run side by side
+          if (!masked && !uneven && r0 + kN <= rows) {  // no branch inside: the chains of all rows run side by side
 #pragma unroll
             for (int i = 0; i < kN; i += 4) {
               float e[4];
-              weights(u + i, l[i / 4], e);
+              weights(u + i, l[i / 4], e, make_float4(f, f, f, f));
               add(e);
             }
           } else {
@@ -446,8 +450,13 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
 #pragma unroll
                 for (int y0 = i; y0 < i + 8; y0 += 4) {
                   float e[4];
-                  weights(u + y0, l[y0 / 4], e);
                   const int r = r0 + y0;
+                  float4 fr = make_float4(f, f, f, f);
+                  if constexpr (kE4m3) {
+                    const float4 o = *reinterpret_cast<const float4*>(own + r);
+                    fr = make_float4(f * o.x, f * o.y, f * o.z, f * o.w);
+                  }
+                  weights(u + y0, l[y0 / 4], e, fr);
                   if (masked && node >= 0) {
                     const uint4 w = *reinterpret_cast<const uint4*>(sees + (node < 32 ? 0 : kRows) + r);
                     const int bit = node & 31;

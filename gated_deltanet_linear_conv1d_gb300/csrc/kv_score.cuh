@@ -104,6 +104,17 @@ __device__ __forceinline__ void loaded(uint32_t (&u)[kN]) {
   for (int i = 0; i < kN; ++i) asm volatile("" : "+r"(u[i]));
 }
 
+// An E4M3 cache's query rows are scaled by powers of two before they are taken apart into two terms: by one, `up`, that
+// takes the largest value of all (`most`, a bf16's bits) below 256, so that one factor does for all scores; but a row whose
+// own largest is more than two powers below has one of its own, and its scores a factor 2^(up - own) beside it.
+__device__ __forceinline__ int power_of(uint32_t most) { return most == 0 ? 0 : min(134 - (int)(most >> 7), 120); }
+__device__ __forceinline__ bool smaller(uint32_t row, uint32_t most) { return row > 0 && (row >> 7) + 2 < (most >> 7); }
+__device__ __forceinline__ int power_of(uint32_t row, uint32_t most) {
+  const int up = power_of(most);
+  return smaller(row, most) ? min(power_of(row), up + 126) : up;
+}
+__device__ __forceinline__ float two_to(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
 // Piece `index` of `pieces`: a scan over the requests' tiles by all threads of the block, `totals` a word a warp. The plan is
 // there after the next barrier.
 template <int kTokens, int kThreads>

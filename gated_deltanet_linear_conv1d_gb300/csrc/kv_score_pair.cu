@@ -11,8 +11,8 @@
 //
 // A pair tile is 256 tokens. Its rows are taken in up to two steps of up to 192 columns each, a buffer of tensor memory for
 // each of two steps; columns 0 .. hs - 1 of a step are rows of the even CTA, the next hs of the odd one. Roles in each CTA:
-// two groups of four warps that share a step's columns (the even CTA's rows for the one, the odd one's for the other), a warp for the copies, one for the MMAs (the even CTA's issues them). The groups
-// load the query rows too. Every wait is bounded.
+// four groups of four warps that share a step's columns (two the even CTA's rows, two the odd one's), a warp for the copies,
+// one for the MMAs (the even CTA's issues them). The groups load the query rows too. Every wait is bounded.
 #include "kv_score.cuh"
 #include "pair.cuh"
 
@@ -41,7 +41,8 @@ struct Bars {
   int abort;
   float factor[2][2];  // what takes the scores of each half's rows to base 2, by segment
   int dead[2][kLoaders];  // the segment has a row that adds nothing
-  uint32_t most[kLoaders];
+  uint32_t most[kLoaders], least[kLoaders];
+  int uneven[2][2];    // rows of the half have factors of their own
   Plan plan;
   long long warp_total[kThreads / 32];
 };
@@ -52,10 +53,11 @@ struct Cfg {
   static constexpr int kTerms = kE4m3 ? 2 : 1;
   static constexpr int kQBytes = kHalf * D * 2;
   // behind the ring: Q, then by segment, half and row -lse to base 2, and what the row sees: the nodes, in two words, and
-  // whether the context; then the second group's sums
+  // whether the context; its own factor (E4M3); then the groups' sums
   static constexpr int oLse = kQBytes;
   static constexpr int oSees = oLse + 2 * 2 * kHalf * 4;
-  static constexpr int oSum = oSees + 2 * 3 * 2 * kHalf * 4;
+  static constexpr int oOwn = oSees + 2 * 3 * 2 * kHalf * 4;
+  static constexpr int oSum = oOwn + (kE4m3 ? 2 * 2 * kHalf * 4 : 0);
   static constexpr int oBars = oSum + kSums * kGroups * kTile * 4;
   static constexpr int kRest = oBars + (sizeof(Bars) + 15) / 16 * 16;
   static constexpr int kFit = (kSmemLimit - kRest) / (int)kBlock;
@@ -126,8 +128,7 @@ struct Scores {
 
 // This CTA's rows of a segment, number `seg` of the piece, as rows of the MMAs' second operand, and the constants of both
 // CTAs' rows. The rows are copied past the registers, all of them on their way at once; an E4M3 cache's are then taken
-// apart into their two terms in place (a row's 2 D bytes are its own), by one power of two for the CTA's rows: what a score
-// is off by counts as such, whatever the row's size.
+// apart into their two terms in place (a row's 2 D bytes are its own).
 template <int D, bool kE4m3>
 __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned char* rest, Bars* B, int seg, int share, int pr) {
   using C = Cfg<D, kE4m3>;
@@ -148,6 +149,7 @@ __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned 
   const uint32_t q_a = smem_u32(rest) + (lane >> 3) * q_block, piece_at = lane & 7;
   auto piece = [&](int q) { return q_a + q * 128 + ((piece_at ^ (q & 7)) << 4); };
   const int mine = rows.of(pr, first + lane), from = lane < per && mine < all ? row_of(mine) : -1;
+  const float own_lse = kE4m3 && from >= 0 ? __ldg(lse_g + from) : INFINITY;
   const uint32_t there = __ballot_sync(0xffffffffu, from >= 0);
 #pragma unroll 8
   for (int i = 0; i < per; ++i) {
@@ -184,6 +186,7 @@ __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned 
   if (lane == 0) B->dead[b][share] = dead;
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   float factor = p.scale * kLog2e;
+  int uneven = 0;
   if constexpr (kE4m3) {
     __syncwarp();
     auto values = [&](int q) {
@@ -198,29 +201,33 @@ __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned 
       return max(m & 0xffffu, m >> 16);
     };
     constexpr uint32_t kInf = 0x7f80u;
-    uint32_t most = 0;
+    uint32_t row_most = 0;  // of row first + lane
 #pragma unroll 4
-    for (int i = 0; i < per; ++i)
-      if (there >> i & 1) most = max(most, largest(values(first + i)));
-    if (__any_sync(0xffffffffu, most >= kInf)) {  // rows with values that are no numbers have no say in it
-      most = 0;
-      for (int i = 0; i < per; ++i)
-        if (there >> i & 1) {
-          const uint32_t m = largest(values(first + i));
-          if (!__any_sync(0xffffffffu, m >= kInf)) most = max(most, m);
-        }
+    for (int i = 0; i < per; ++i) {
+      const uint32_t m = __reduce_max_sync(0xffffffffu, largest(values(first + i)));
+      if (lane == i) row_most = m;
     }
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 0) B->most[share] = most;
+    // one that is not there, adds nothing, or has values that are no numbers, has no say in it
+    if (row_most >= kInf || !(fabsf(own_lse) < INFINITY)) row_most = 0;
+    uint32_t most = __reduce_max_sync(0xffffffffu, row_most);
+    uint32_t least = __reduce_min_sync(0xffffffffu, row_most > 0 ? row_most : ~0u);
+    if (lane == 0) B->most[share] = most, B->least[share] = least;
     asm volatile("bar.sync 1, %0;" ::"n"(32 * kLoaders) : "memory");
     most = __reduce_max_sync(0xffffffffu, B->most[lane % kLoaders]);
+    least = __reduce_min_sync(0xffffffffu, B->least[lane % kLoaders]);
     asm volatile("bar.sync 1, %0;" ::"n"(32 * kLoaders) : "memory");  // before the next segment's
-    // a power of two that takes the largest value below 256
-    const int up = most == 0 ? 0 : min(134 - (int)(most >> 7), 120);
-    const float by = __uint_as_float((uint32_t)(up + 127) << 23);
-    factor *= __uint_as_float((uint32_t)(127 - up) << 23);
+    const int up = power_of(most), own = power_of(row_most, most);
+    uneven = smaller(least, most);
+    factor *= two_to(-up);
+    if (lane < per) {
+      float* at = reinterpret_cast<float*>(rest + C::oOwn) + (b * 2 + pr) * kHalf + first + lane;
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr(at, r)), "f"(two_to(up - own)) : "memory");
+    }
 #pragma unroll 2
     for (int i = 0; i < per; ++i) {
+      const float by = two_to(__shfl_sync(0xffffffffu, own, i));
       if (!(there >> i & 1)) continue;
       const int q = first + i;
       const uint4 raw = values(q);
@@ -252,8 +259,10 @@ __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned 
   }
   if (share == 0 && lane == 0) {  // for the groups of both CTAs that have this one's rows
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < 2; ++r) {
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr(&B->factor[b][pr], r)), "f"(factor) : "memory");
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(&B->uneven[b][pr], r)), "r"(uneven) : "memory");
+    }
   }
 }
 
@@ -404,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const Args a, const _
       __syncwarp();
     }
   } else {
-    // ------------------------------------------------------------ weights: a group has half of the columns
+    // ------------------------------------------------------------ weights: a group has a quarter of the columns
     // A thread has four of its warp's tokens (lane / 4 + 8 k) with a quarter of the rows (2 (lane % 4) and the next of every
     // eight), so that what goes by the row is loaded for four tokens at once; at the end it has one token's sum.
     const int g = warp >> 3, part = warp >> 2 & 1, w4 = warp & 3, a4 = lane & 3, mine = 32 * w4 + (lane >> 2) + 8 * a4;
@@ -445,9 +454,12 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const Args a, const _
       if (lane == 0) arrive_both(&B->q_full[b2]);
       wait_cluster(&B->q_full[b2], (seg >> 1) & 1, abort);
       __syncwarp();
-      const bool dead = __any_sync(0xffffffffu, lane < kLoaders && *(volatile int*)&B->dead[b2][lane % kLoaders] != 0);
+      // rows that add nothing or have factors of their own: the way of masked tiles for all of them
+      const bool dead = __any_sync(0xffffffffu, lane < kLoaders && *(volatile int*)&B->dead[b2][lane % kLoaders] != 0) ||
+                        *(volatile int*)&B->uneven[b2][g] != 0;
       const float f0 = *(volatile float*)&B->factor[b2][g];
       const float* lse_h = reinterpret_cast<const float*>(rest + C::oLse) + (b2 * 2 + g) * kHalf + 2 * a4;
+      const float* own_h = reinterpret_cast<const float*>(rest + C::oOwn) + (b2 * 2 + g) * kHalf + 2 * a4;
       const uint32_t* sees_h = reinterpret_cast<const uint32_t*>(rest + C::oSees) + b2 * 3 * 2 * kHalf + g * kHalf + 2 * a4;
       for (int t = s.t0; t < s.t1; ++t, ++tile) {
         const int this_page = page;
@@ -507,7 +519,9 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const Args a, const _
             for (int q = 0; q < 2; ++q) {
               const int r = r0 + 8 * q;
               uint32_t see[2] = {~0u, ~0u};
+              float2 own = make_float2(1.f, 1.f);
               if (masked) {
+                if constexpr (kE4m3) own = *reinterpret_cast<const float2*>(own_h + min(sub * rows.hs + r, kHalf - 8));
                 const uint32_t* at = sees_h + min(sub * rows.hs + r, kHalf - 8);
                 const uint2 w0 = *reinterpret_cast<const uint2*>(at), w1 = *reinterpret_cast<const uint2*>(at + 2 * kHalf),
                             live = *reinterpret_cast<const uint2*>(at + 4 * kHalf);
@@ -522,7 +536,8 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const Args a, const _
               if (r + 2 * a4 + 1 >= here) see[1] = 0u;
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                const float x = ex2(fmaf(u.at(q, k, 0), f[k], l[q].x)), y = ex2(fmaf(u.at(q, k, 1), f[k], l[q].y));
+                const float x = ex2(fmaf(u.at(q, k, 0), f[k] * own.x, l[q].x)),
+                            y = ex2(fmaf(u.at(q, k, 1), f[k] * own.y, l[q].y));
                 sum[k][0] += (see[0] >> (8 * k)) & 1u ? x : 0.f;
                 sum[k][1] += (see[1] >> (8 * k)) & 1u ? y : 0.f;
               }

@@ -650,8 +650,9 @@ gdn_status gdn_tree_attention_lse(const gdn_kv_cache *cache, const uint16_t *q, 
  * max_tokens cannot hold set GDN_DEVERR_OFFSETS and the request writes nothing; a
  * page outside [0, num_pages) sets GDN_DEVERR_SLOT and its tokens' scores are
  * left as they were. Scores from token ctx_len + P on are not touched. The sums are
- * fp32, in a fixed order. An E4M3 cache's products take q as two E4M3 terms (2^-17
- * of the head row's largest value). q 16-byte, tree_mask 8-byte aligned.
+ * fp32, in a fixed order. An E4M3 cache's products take q as two E4M3 terms (2^-15
+ * of the head row's largest value, and 2^-17 of the largest that the request's rows
+ * of the kv head have). q 16-byte, tree_mask 8-byte aligned.
  *   dev_err   GDN_DEVERR_TIMEOUT too, if a bounded wait inside the kernel ran out
  */
 gdn_status gdn_kv_score(const gdn_kv_cache *cache, const uint16_t *q, const float *lse, const int32_t *block_table,
@@ -686,8 +687,8 @@ gdn_status gdn_kv_score(const gdn_kv_cache *cache, const uint16_t *q, const floa
  *               there is a dst_slot, and without one there is none.
  *   kept        [N][Hkv][max_kept] int32 out: the kept tokens' old indices,
  *               ascending; entries from new_len on are not touched
- *   new_len     [N] int32 out, not `length` itself: the request's tokens now, -1 if
- *               the request breaks a limit
+ *   new_len     [N] int32 out, not `length` or another of the inputs: the request's
+ *               tokens now, -1 if the request breaks a limit
  *   sink_tokens, recent_tokens >= 0;  max_tokens at most 2^30
  * A request with a slot >= num_slots (or a negative dst_slot), or a page outside
  * [0, num_pages) in either table, sets GDN_DEVERR_SLOT; one whose tokens the tables,

@@ -114,7 +114,8 @@ def test_evict_arguments(b):
     for kw in (dict(table=None), dict(mp=0), dict(mp=-1), dict(length=None), dict(budget=None), dict(sinks=-1),
                dict(recent=-1), dict(dst=512, dmp=-1, dst_slot=512), dict(dmp=3), dict(dst=512, dmp=2), dict(dst_slot=512),
                dict(dst=P, dmp=2, dst_slot=512), dict(dst=512, dmp=2, dst_slot=P), dict(score=None), dict(score=258), dict(slot=None),
-               dict(slots=0), dict(room=0), dict(kept=None), dict(most=-1), dict(new_len=None), dict(new_len=P), dict(N=-1)):
+               dict(slots=0), dict(room=0), dict(kept=None), dict(most=-1), dict(new_len=None), dict(new_len=P), dict(N=-1),
+               dict(budget=P, new_len=P), dict(slot=512), dict(table=512), dict(dst=P + 64, dmp=2, dst_slot=512)):
         assert evict_call(b, c, **kw) == b.GDN_ERR_INVALID_ARG, kw
     assert evict_call(b, c, room=(1 << 30) + 1) == b.GDN_ERR_UNSUPPORTED
     assert evict_call(b, c, N=(1 << 26) + 1) == b.GDN_ERR_UNSUPPORTED  # 2^28 heads

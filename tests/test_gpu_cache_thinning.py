@@ -221,6 +221,48 @@ def test_score_of_random_sizes(b, err, fmt, seed):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,nodes,lens", [("24x4x256", 1, [300]), ("24x4x256", 10, [700, 130]), ("24x4x256", 64, [1000, 3]),
+                                              ("32x8x128", 20, [50, 900])])
+def test_score_of_rows_far_apart(b, err, fmt, heads, nodes, lens):
+    """Query rows from 2^-30 to 2^8 of each other, zeros among them, and rows left out that are large or no numbers: what a
+    row's weights are off by is counted by that row's own size."""
+    pool, table, ctx, q, scale = case(heads, fmt, 64, lens, nodes, seed=nodes)
+    g = torch.Generator(device="cuda").manual_seed(nodes)
+    power = torch.randint(-30, 9, q.shape[:2], generator=g, device="cuda").double()
+    power[torch.rand(power.shape, generator=g, device="cuda") < 0.3] = 0
+    q = (q.double() * 2 ** power[..., None]).to(torch.bfloat16)
+    q[0, 1] = 0
+    gone = torch.rand(q.shape[:2], generator=g, device="cuda") < 0.1
+    for i, value in enumerate((3e38, NAN, INF)):
+        q[..., 7 + i] = torch.where(gone & (torch.arange(q.shape[1], device="cuda") % 3 == i), value, q[..., 7 + i])
+    finite = torch.where(gone[..., None], 0, q)
+    lse = T.lse(pool, finite, table, ctx, scale, nodes)[0].float()
+    lse[gone] = INF
+    weights = randn(len(lens), pool.k.shape[1], max(lens) + nodes, seed=3)
+    slot = torch.arange(len(lens), dtype=torch.int32, device="cuda")
+    ref, bound = T.score(pool, finite, lse, table, ctx, scale, nodes, weights, slot)
+    b.gdn_kv_score(pool.handle(b), q, lse, table, ctx, scale, weights, slot, nodes, dev_err=err)
+    assert b.gdn_read_device_error(err) == 0
+    inside(weights, ref, bound, "score")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("nodes", [1, 48])
+def test_score_of_rows_that_are_no_numbers(b, err, fmt, nodes):
+    """A row with an infinity or a NaN and a finite lse: no score of a token that it sees is a number, other heads' are."""
+    pool, table, ctx, q, scale = case("24x4x256", fmt, 64, [300], nodes)
+    lse = T.lse(pool, q, table, ctx, scale, nodes)[0].float()
+    q[0, 2, 5] = NAN  # of kv head 0
+    q[0, 20, 5] = NAN  # of kv head 3
+    q[0, 20, 6] = INF
+    weights = torch.zeros(1, 4, 300 + nodes, device="cuda")
+    b.gdn_kv_score(pool.handle(b), q, lse, table, ctx, scale, weights, ints([0]), nodes, dev_err=err)
+    assert b.gdn_read_device_error(err) == 0
+    assert bool(weights[0, [0, 3], :301].isnan().all())
+    assert bool(weights[0, [0, 3], 301:].isfinite().all()) and bool(weights[0, 1:3].isfinite().all())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("nodes", [6, 48])
 def test_score_of_what_no_row_sees(b, err, fmt, nodes):
     """Keys that are no numbers, in nodes that no row sees, behind the last token and in unused pages, leave the others'

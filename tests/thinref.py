@@ -12,8 +12,9 @@ from tests import attnref as R
 F32 = 2.0 ** -23
 
 
-def logits(pool, q, table, n, ctx, scale, nodes, mask=None):
-    """Request n's scale (q . k) [P, Hkv, G, tokens], -inf where a row does not see the token, and their error bounds."""
+def logits(pool, q, table, n, ctx, scale, nodes, mask=None, together=False):
+    """Request n's scale (q . k) [P, Hkv, G, tokens], -inf where a row does not see the token, and their error bounds;
+    `together`: of rows that an E4M3 cache's products take by one power of two."""
     P, D, Hkv = nodes, q.shape[-1], pool.k.shape[1]
     G = q.shape[1] // Hkv
     pages = table[n, :-(-(ctx + P) // pool.page)].long()
@@ -26,8 +27,16 @@ def logits(pool, q, table, n, ctx, scale, nodes, mask=None):
     s = (torch.einsum("phgd,htd->phgt", x, k) * scale).masked_fill(~seen, -math.inf)
     # D products and additions, the key's scale, the factor and its rounding
     off = torch.einsum("phgd,htd->phgt", x.abs(), k.abs()) * abs(scale) * (D + 8) * F32
-    if pool.fmt == "e4m3":  # q as two E4M3 terms: 2^-17 of the head row's largest value each
-        off = off + 2.0 ** -17 * x.abs().amax(-1, keepdim=True) * k.abs().sum(-1)[None, :, None, :] * abs(scale)
+    if pool.fmt == "e4m3":
+        # q as two E4M3 terms. The largest value is taken into [128, 256). A bf16 value has 8 bits: the first term takes at
+        # least 4 of them, and the second holds the rest where the last of them counts 2^-9, E4M3's smallest step, or more;
+        # else it is off by half of that step, 2^-10: 2^-17 of the head row's largest value.
+        most = x.abs().nan_to_num(0, 0, 0).amax(-1, keepdim=True)
+        by = 2.0 ** -17 * most
+        if together:  # The largest of all the kv head's rows goes there, or a smaller one: 2^-17 of it. A row whose largest
+            # value is two powers below goes into [32, 64) at least, so that 2^-10 is 2^-15 of it; smaller ones have their own.
+            by = torch.minimum(2.0 ** -17 * most.amax((0, 2), keepdim=True), 4 * by)
+        off = off + by * k.abs().sum(-1)[None, :, None, :] * abs(scale)
     return s, torch.where(seen, off, 0)
 
 
@@ -58,7 +67,7 @@ def score(pool, q, lses, table, ctx, scale, nodes, weights, slot, mask=None, dec
         c, at = int(ctx[n]), int(slot[n])
         if c < 0 or at < 0 or at >= weights.shape[0]:
             continue
-        s, off = logits(pool, q, table, n, c, scale, P, mask)
+        s, off = logits(pool, q, table, n, c, scale, P, mask, together=True)
         z = lses[n * P:(n + 1) * P].double().reshape(P, Hkv, G, 1)
         live = z.isfinite()
         p = torch.where(live & (s > -math.inf), torch.exp(s - torch.where(live, z, 0)), 0)
