@@ -10,6 +10,9 @@
     python -m gated_deltanet_linear_conv1d_gb300.profile_case rope    --requests 16384 --cache bf16
     python -m gated_deltanet_linear_conv1d_gb300.profile_case kvread  --lengths 4096x64 --cache e4m3
     python -m gated_deltanet_linear_conv1d_gb300.profile_case spectree --requests 64 --nodes 8
+    python -m gated_deltanet_linear_conv1d_gb300.profile_case mrope   --requests 16384 --cache bf16
+    python -m gated_deltanet_linear_conv1d_gb300.profile_case score   --lengths 4096x64 --cache e4m3 --nodes 1
+    python -m gated_deltanet_linear_conv1d_gb300.profile_case evict   --lengths 8192x32 --cache e4m3
 
 Each launch is preceded by the same warm-up launches (--warmup) and followed
 by a device synchronisation; nothing else runs on the GPU besides the input
@@ -73,15 +76,16 @@ def _cache(gen, tokens, page, heads, fmt, dev):
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("case", choices=["decode", "prefill", "spec", "commit", "conv", "rmsnorm", "fp8", "gemm", "attn",
-                                     "rope", "kvread", "spectree"])
+                                     "rope", "kvread", "spectree", "mrope", "score", "evict"])
     ap.add_argument("--heads", choices=["full", "rank"], default="full")
     ap.add_argument("--requests", type=int, default=64)
     ap.add_argument("--slots", type=int, default=0)
     ap.add_argument("--lengths", default="2048x8",
                     help="prefill lengths or cached contexts, e.g. 2048x8 or 16,300,8192")
-    ap.add_argument("--nodes", type=int, default=1, help="attn, spectree: drafted tokens per request")
-    ap.add_argument("--cache", choices=["bf16", "e4m3"], default="e4m3", help="attn, rope, kvread: the cache's format")
-    ap.add_argument("--page", type=int, default=64, help="attn, rope, kvread: tokens per page")
+    ap.add_argument("--nodes", type=int, default=1, help="attn, score, spectree: new tokens per request")
+    ap.add_argument("--cache", choices=["bf16", "e4m3"], default="e4m3", help="attention side: the cache's format")
+    ap.add_argument("--page", type=int, default=64, help="attention side: tokens per page")
+    ap.add_argument("--in-place", action="store_true", help="evict: to the front of the request's own pages")
     ap.add_argument("--loguniform", type=int, default=0, help="prefill: N log-uniform lengths in [16, 8192]")
     ap.add_argument("--k", type=int, default=6144, help="fp8, gemm: input features")
     ap.add_argument("--n", type=int, default=5120, help="fp8, gemm: output features")
@@ -160,11 +164,11 @@ def main(argv=None):
 
         def run():
             b.gdn_out_proj(x, wt, out, residual=out, dev_err=err)
-    elif args.case in ("attn", "rope", "kvread"):
+    elif args.case in ("attn", "rope", "kvread", "mrope", "score", "evict"):
         gen = torch.Generator(device=dev)
         gen.manual_seed(8)
         hq, hkv = (24, 4) if args.heads == "full" else (6, 1)
-        if args.case == "rope":
+        if args.case in ("rope", "mrope"):
             T = args.requests
             cache, _ = _cache(gen, [T], args.page, hkv, args.cache, dev)
             x = torch.randn((T, hq + 2 * hkv, 256), generator=gen, device=dev).to(torch.bfloat16)
@@ -172,8 +176,13 @@ def main(argv=None):
             pos = torch.arange(T, dtype=torch.int32, device=dev)
             freq = 1e7 ** (-torch.arange(0, 64, 2, dtype=torch.float64, device=dev) / 64)
             out = torch.empty((T, hq, 256), dtype=torch.bfloat16, device=dev)
+            axes, three = b.make_rope_axes((12, 10, 10), mixed=True), pos.expand(3, T).contiguous()
 
             def run():
+                if args.case == "mrope":  # the 32 frequencies turn by three positions a token
+                    b.gdn_qk_norm_mrope(x[:, :hq], x[:, hq:hq + hkv], gain, gain, 1e-6, three, freq, axes, out,
+                                        v=x[:, hq + hkv:], cache=cache, kv_slot=pos, dev_err=err)
+                    return
                 b.gdn_qk_norm_rope(x[:, :hq], x[:, hq:hq + hkv], gain, gain, 1e-6, pos, freq, out, v=x[:, hq + hkv:],
                                    cache=cache, kv_slot=pos, dev_err=err)
         else:
@@ -183,15 +192,35 @@ def main(argv=None):
             if args.case == "kvread":
                 start = torch.tensor([0] + lengths, device=dev).cumsum(0).to(torch.int32)
                 ko, vo = (torch.empty((T, hkv, 256), dtype=torch.bfloat16, device=dev) for _ in range(2))
+            elif args.case == "evict":  # down to half of the tokens
+                ctx, budget = (torch.tensor([n // d for n in lengths], dtype=torch.int32, device=dev) for d in (1, 2))
+                score = torch.rand((2 * N, hkv, max(lengths)), generator=gen, device=dev)
+                slot = torch.arange(N, dtype=torch.int32, device=dev)
+                dst = {}
+                if not args.in_place:
+                    other, to = _cache(gen, lengths + lengths, args.page, hkv, args.cache, dev)
+                    cache, table, dst = other, to[:N].contiguous(), dict(dst_table=to[N:].contiguous(), dst_slot=slot + N)
+                kept = torch.empty((N, hkv, max(lengths)), dtype=torch.int32, device=dev)
+                new_len, T = torch.empty_like(ctx), sum(lengths)
             else:
                 ctx = torch.tensor(lengths, dtype=torch.int32, device=dev)
                 q = torch.randn((T, hq, 256), generator=gen, device=dev).to(torch.bfloat16)
                 out = torch.empty_like(q)
                 ws = torch.empty(b.gdn_tree_attention_workspace_bytes(cache, N, P, hq), dtype=torch.uint8, device=dev)
+                if args.case == "score":
+                    lse = torch.empty((T, hq), device=dev)
+                    b.gdn_tree_attention_lse(cache, q, table, ctx, 256 ** -0.5, out, lse, P, workspace=ws)
+                    score = torch.zeros((N, hkv, max(lengths) + P), device=dev)
+                    slot = torch.arange(N, dtype=torch.int32, device=dev)
 
             def run():
                 if args.case == "kvread":
                     b.gdn_kv_cache_read(cache, table, start, ko, vo, dev_err=err)
+                elif args.case == "score":
+                    b.gdn_kv_score(cache, q, lse, table, ctx, 256 ** -0.5, score, slot, P, dev_err=err)
+                elif args.case == "evict":
+                    b.gdn_kv_evict(cache, table, ctx, budget, score, slot, kept, new_len, sink_tokens=4, recent_tokens=64,
+                                   dev_err=err, **dst)
                 else:
                     b.gdn_tree_attention(cache, q, table, ctx, 256 ** -0.5, out, P, workspace=ws, dev_err=err)
     elif args.case == "spectree":
@@ -232,7 +261,7 @@ def main(argv=None):
     flag = b.gdn_read_device_error(err)
     tokens = {"decode": args.requests, "spec": args.requests * 4, "commit": args.requests,
               "fp8": args.requests, "gemm": args.requests}.get(args.case)
-    if args.case in ("prefill", "conv", "attn", "rope", "kvread", "spectree"):
+    if args.case in ("prefill", "conv", "attn", "rope", "kvread", "spectree", "mrope", "score", "evict"):
         tokens = T
     ms = sum(times) / max(1, len(times))
     rate = f", {tokens / (ms / 1e3):.4g} tokens/s" if tokens else ""
