@@ -2,7 +2,7 @@
 // accumulated weight (gdn_kv_score), the first and the last ones always among them.
 //
 // Two kernels, one after the other on the stream:
-//   select: per (request, kv head) the m-th largest weight by radix, 8 bits a pass from the top, and the indices of the
+//   select: per (request, kv head) the m-th largest weight by radix, 11 bits a pass from the top, and the indices of the
 //           kept tokens in ascending order. Weights that are equal at the border go to the lowest indices.
 //   move:   the kept tokens' keys, values, scales and weights, in the order of the tokens, to other pages (copy_kernel) or
 //           to the front of the request's own (shift_kernel).
@@ -19,16 +19,22 @@ namespace {
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kFew = 64;  // weights at the border that are put in order all at once
+constexpr int kBins = 2048;
+constexpr int kFew = 256;  // weights at the border that are put in order all at once
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive() {
   __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
 }
 // A 32-bit word of another CTA's shared memory, at the place of `mine` in this one's.
 __device__ __forceinline__ int load_remote(const int* mine, uint32_t rank) {
@@ -36,6 +42,14 @@ __device__ __forceinline__ int load_remote(const int* mine, uint32_t rank) {
   int v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(mine)), "r"(rank));
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ int4 load_remote4(const int* mine, uint32_t rank) {
+  uint32_t addr;
+  int4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(mine)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
 
@@ -61,19 +75,20 @@ __device__ __forceinline__ uint32_t key_of(float w) {
 
 // kSplit CTAs, a cluster, have a (request, kv head), each an equal run of its tokens; a thread has kHeld neighbours at a
 // time, and a CTA whose tokens are no more than its threads hold reads their weights once (else again, from L2, in each of
-// the passes). After two passes the weights with the border's upper 16 bits are a few, as a rule: those are put in order at
-// once, by counting for each the larger ones.
-// Bound by the chain of barriers and shared-memory atomics of the passes.
+// the passes). A pass counts the keys with the border's upper bits by their next 11. After two passes (after one of a short
+// request) few have all the bits so far, as a rule: those are put in order at once, by counting for each the larger ones.
+// Bound by the chain of loads, barriers and exchanges between the CTAs.
 template <int kSplit, int kHeld>
 __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel(const EvictArgs p, const KvArgs c) {
   constexpr int kBatch = kSelThreads * kHeld;
-  __shared__ __align__(16) int hist[256 * 32];       // [bin][lane]: no two lanes of a warp at one bank
-  __shared__ int bins[256], above_s[8], scan_s[2][kSelWarps];
-  __shared__ int pick[3];                            // the bin of the m-th largest, those above it, and in it
+  constexpr int kRoom = 2 * kBins;                       // kept indices on their way out
+  __shared__ __align__(16) int hist[2][kBins];           // of two passes in turn: the others' CTAs read the one before
+  __shared__ int above_s[kSelWarps], scan_s[2][kSelWarps];
+  __shared__ int pick[3];                                // the bin of the m-th largest, those above it, and in it
   __shared__ __align__(16) uint32_t few_s[kFew];
   __shared__ uint32_t own_few_s[kFew];
-  __shared__ int few, border_s[2];
-  __shared__ int totals[2];                          // of this CTA: weights above the border, and equal to it
+  __shared__ int few[2], border_s[2];                    // few: of this CTA, those in the bin and those above it
+  __shared__ int totals[2];                              // of this CTA: weights above the border, and equal to it
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -116,6 +131,9 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
   };
   const bool held = count <= kBatch;
   if (sift && held) load(0);
+#pragma unroll
+  for (int i = tid; i < 2 * kBins / 4; i += kSelThreads) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+  if (tid < 2) few[tid] = 0;
   bool bad = false;
   if (m >= 0) {
 #pragma unroll 4
@@ -154,50 +172,57 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
 
   uint32_t border = 0;  // the key of the m-th largest, from the top
   int need = m;         // how many of those with its upper bits
-  for (int shift = 24; shift >= 0; shift -= 8) {
-#pragma unroll
-    for (int i = 0; i < 256 * 32 / 4; i += kSelThreads) reinterpret_cast<int4*>(hist)[i + tid] = make_int4(0, 0, 0, 0);
-    __syncthreads();
+  int over_before = 0, equal_before = 0;  // keys above the border, and at it, in the CTAs before this one
+  bool counted = false;
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
+    int* bins = hist[pass & 1];
+    if (pass == 2) {
+      for (int i = tid; i < kBins / 4; i += kSelThreads) reinterpret_cast<int4*>(bins)[i] = make_int4(0, 0, 0, 0);
+      __syncthreads();
+    }
     batches([&] {
 #pragma unroll
       for (int j = 0; j < kHeld; ++j)
-        if (j < valid && (shift == 24 || (key[j] >> (shift + 8)) == (border >> (shift + 8))))
-          atomicAdd(&hist[(key[j] >> shift & 255u) * 32 + lane], 1);
+        if (j < valid && (pass == 0 || ((key[j] ^ border) >> (shift + width)) == 0))
+          atomicAdd(&bins[key[j] >> shift & ((1u << width) - 1)], 1);
     });
-    __syncthreads();
-    int mine = 0;
-    if (tid < 256) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) mine += hist[tid * 32 + (i + lane) % 32];
-      bins[tid] = mine;
-    }
-    if constexpr (kSplit > 1) {
-      cluster_sync();
-      if (tid < 256) {
-#pragma unroll
-        for (int r = 0; r < kSplit; ++r)
-          if (r != rank) mine += load_remote(&bins[tid], r);
-      }
-    }
-    // keys in higher bins: a scan from the top, thread t has bin t
-    int upto = mine;
-    if (tid < 256) {
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_down_sync(0xffffffffu, upto, d);
-        if (lane + d < 32) upto += o;
-      }
-      if (lane == 0) above_s[warp] = upto;
-    }
-    __syncthreads();
-    if (tid < 256) {
-      int above = upto - mine;
-      for (int k = warp + 1; k < 8; ++k) above += above_s[k];
-      if (above < need && above + mine >= need) pick[0] = tid, pick[1] = above, pick[2] = mine;
-    }
-    if (tid == 0) few = 0;
-    if constexpr (kSplit > 1) cluster_sync();  // the bins have been read
+    if constexpr (kSplit > 1) cluster_sync();
     else __syncthreads();
+    // this thread's four bins, and the keys in higher ones: a scan from the top
+    static_assert(kBins == 4 * kSelThreads, "four bins a thread");
+    int4 mine = reinterpret_cast<const int4*>(bins)[tid];
+    if constexpr (kSplit > 1) {
+      int4 theirs[kSplit - 1];
+#pragma unroll
+      for (int r = 1; r < kSplit; ++r) theirs[r - 1] = load_remote4(bins + 4 * tid, (rank + r) % kSplit);
+#pragma unroll
+      for (int r = 0; r < kSplit - 1; ++r) {
+        mine.x += theirs[r].x;
+        mine.y += theirs[r].y;
+        mine.z += theirs[r].z;
+        mine.w += theirs[r].w;
+      }
+    }
+    const int sum = mine.x + mine.y + mine.z + mine.w;
+    int upto = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_down_sync(0xffffffffu, upto, d);
+      if (lane + d < 32) upto += o;
+    }
+    if (lane == 0) above_s[warp] = upto;
+    __syncthreads();
+    int above = upto - sum + __reduce_add_sync(0xffffffffu, lane > warp && lane < kSelWarps ? above_s[lane] : 0);
+    if (above < need && above + sum >= need) {
+      const int in[4] = {mine.x, mine.y, mine.z, mine.w};
+#pragma unroll
+      for (int i = 3; i >= 0; --i) {
+        if (above < need && above + in[i] >= need) pick[0] = 4 * tid + i, pick[1] = above, pick[2] = in[i];
+        above += in[i];
+      }
+    }
+    __syncthreads();
     border |= (uint32_t)pick[0] << shift;
     need -= pick[1];
     const int in_bin = pick[2];
@@ -205,16 +230,22 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
       uint32_t* own = kSplit > 1 ? own_few_s : few_s;
       batches([&] {
         uint32_t in = 0;
+        int over = 0;
 #pragma unroll
-        for (int j = 0; j < kHeld; ++j) in |= (j < valid && key[j] >> shift == border >> shift ? 1u : 0u) << j;
+        for (int j = 0; j < kHeld; ++j) {
+          in |= (j < valid && key[j] >> shift == border >> shift ? 1u : 0u) << j;
+          if (kSplit > 1) over += j < valid && key[j] >> shift > border >> shift;
+        }
         int upto = __popc(in);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const int o = __shfl_up_sync(0xffffffffu, upto, d);
           if (lane >= d) upto += o;
         }
+        if (kSplit > 1) over = __reduce_add_sync(0xffffffffu, over);
         int at = 0;
-        if (lane == 31 && upto > 0) at = atomicAdd(&few, upto);
+        if (lane == 31 && upto > 0) at = atomicAdd(&few[0], upto);
+        if (kSplit > 1 && lane == 0 && over > 0) atomicAdd(&few[1], over);
         at = __shfl_sync(0xffffffffu, at, 31) + upto - __popc(in);
         if (in) {
 #pragma unroll
@@ -222,23 +253,31 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
             if (in >> j & 1) own[at++] = key[j];
         }
       });
+      int before = 0;  // keys of the CTAs before this one in few_s
       if constexpr (kSplit > 1) {  // every CTA's, one after the other
         cluster_sync();
-        const int theirs = lane < kSplit ? load_remote(&few, lane) : 0;
+        const int theirs = lane < kSplit ? load_remote(&few[0], lane) : 0;
+        over_before = lane < rank ? load_remote(&few[1], lane) : 0;
         int upto = theirs;
 #pragma unroll
         for (int d = 1; d < kSplit; d <<= 1) {
           const int o = __shfl_up_sync(0xffffffffu, upto, d);
           if (lane >= d) upto += o;
         }
+        int r = 0, first = 0;
 #pragma unroll
-        for (int r = 0; r < kSplit; ++r) {
-          const int n_r = __shfl_sync(0xffffffffu, theirs, r), at = __shfl_sync(0xffffffffu, upto, r) - n_r;
-          if (tid < n_r) few_s[at + tid] = (uint32_t)load_remote(reinterpret_cast<const int*>(own_few_s) + tid, r);
+        for (int x = 0; x < kSplit - 1; ++x) {
+          const int end = __shfl_sync(0xffffffffu, upto, x);
+          if (tid >= end) r = x + 1, first = end;
         }
+        static_assert(kFew <= kSelThreads, "a key a thread");
+        if (tid < in_bin) few_s[tid] = (uint32_t)load_remote(reinterpret_cast<const int*>(own_few_s) + tid - first, r);
+        before = __shfl_sync(0xffffffffu, upto - theirs, rank);
+        over_before = __reduce_add_sync(0xffffffffu, over_before);
       }
-      if (tid >= in_bin && tid < kFew) few_s[tid] = 0;  // below all that are in the bin, or counted as the least of them
+      if (tid >= in_bin && tid < (in_bin + 3) / 4 * 4) few_s[tid] = 0;  // counted as the least of them
       __syncthreads();
+      if constexpr (kSplit > 1) cluster_arrive();  // the others' have been read
       if (tid < in_bin) {
         const uint32_t mine_key = few_s[tid];
         int above = 0, reach = 0;  // larger ones, and those as large too
@@ -250,18 +289,25 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
         }
         if (above < need && reach >= need) border_s[0] = (int)mine_key, border_s[1] = need - above;
       }
-      if constexpr (kSplit > 1) cluster_sync();  // the others' have been read
-      else __syncthreads();
+      __syncthreads();
       border = (uint32_t)border_s[0];
       need = border_s[1];
+      if constexpr (kSplit > 1) {
+        int over = 0;
+        for (int i = lane; i < before; i += 32) {
+          over += few_s[i] > border;
+          equal_before += few_s[i] == border;
+        }
+        over_before += __reduce_add_sync(0xffffffffu, over);
+        equal_before = __reduce_add_sync(0xffffffffu, equal_before);
+        counted = true;
+      }
       break;
     }
-    __syncthreads();  // `pick` and `above_s` have been read
   }
 
   // ---- the kept tokens' indices: those above the border, and the first `need` of those at it
-  int over_before = 0, equal_before = 0;
-  if constexpr (kSplit > 1) {  // the numbers of both in the CTAs before this one
+  if (kSplit > 1 && !counted) {  // the numbers of both in the CTAs before this one
     if (tid < 2) totals[tid] = 0;
     __syncthreads();
     int over = 0, equal = 0;
@@ -285,7 +331,7 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
     }
     over_before = __reduce_add_sync(0xffffffffu, over_before);
     equal_before = __reduce_add_sync(0xffffffffu, equal_before);
-    cluster_sync();  // no CTA leaves while another reads its shared memory
+    cluster_arrive();
   }
   int buf = 0, base = 0;
   batches([&] {
@@ -319,7 +365,7 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
     const int from = over_before + min(equal_before, need);
     const int until = over_before + (all & 0xffff) + min(equal_before + (all >> 16), need);
     const int i = lo + base + tid * kHeld;
-    constexpr int kRoom = 256 * 32;
+    int* out = hist[0];  // (of a cluster: read by the others before they arrived)
     // this thread's: those above the border, and of those at it the ones that are needed
     const int o = over_before + (before & 0xffff), e = equal_before + (before >> 16);
     int spare = __popc(is_equal) - max(0, need - e);
@@ -327,9 +373,9 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
     for (int at = from; at < until; at += kRoom) {
       int to = o + min(e, need) - at;
       for (uint32_t left = is_over | is_equal; left; left &= left - 1, ++to)
-        if (to >= 0 && to < kRoom) hist[to] = i + __ffs(left) - 1;
+        if (to >= 0 && to < kRoom) out[to] = i + __ffs(left) - 1;
       __syncthreads();
-      for (int k = tid; k < min(kRoom, until - at); k += kSelThreads) kept[at + k] = hist[k];
+      for (int k = tid; k < min(kRoom, until - at); k += kSelThreads) kept[at + k] = out[k];
       __syncthreads();
     }
     over_before += all & 0xffff;
@@ -337,6 +383,7 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
     base += kBatch;
     buf ^= 1;
   });
+  if constexpr (kSplit > 1) cluster_wait();  // no CTA leaves while another reads its shared memory
 }
 
 // ---------------------------------------------------------------- move
