@@ -73,7 +73,7 @@ __device__ __forceinline__ uint32_t key_of(float w) {
   return w != w ? 0u : u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-// kSplit CTAs, a cluster, have a (request, kv head), each an equal run of its tokens; a thread has kHeld neighbours at a
+// kSplit CTAs, a cluster, have a (request, kv head), each an equal run of its tokens; a thread has kHeld of them at a
 // time, and a CTA whose tokens are no more than its threads hold reads their weights once (else again, from L2, in each of
 // the passes). A pass counts the keys with the border's upper bits by their next 11. After two passes (after one of a short
 // request) few have all the bits so far, as a rule: those are put in order at once, by counting for each the larger ones.
@@ -81,9 +81,9 @@ __device__ __forceinline__ uint32_t key_of(float w) {
 template <int kSplit, int kHeld>
 __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel(const EvictArgs p, const KvArgs c) {
   constexpr int kBatch = kSelThreads * kHeld;
-  constexpr int kRoom = 2 * kBins;                       // kept indices on their way out
   __shared__ __align__(16) int hist[2][kBins];           // of two passes in turn: the others' CTAs read the one before
-  __shared__ int above_s[kSelWarps], scan_s[2][kSelWarps];
+  __shared__ int above_s[kSelWarps];
+  __shared__ int2 scan_s[2][kSelWarps];
   __shared__ int pick[3];                                // the bin of the m-th largest, those above it, and in it
   __shared__ __align__(16) uint32_t few_s[kFew];
   __shared__ uint32_t own_few_s[kFew];
@@ -99,37 +99,29 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
   const int m = kept_of(p, c, n, &why);
   const int len = __ldg(p.len + n);
   // this CTA's run of tokens
-  const int per = ((max(len, 0) + kSplit - 1) / kSplit + kHeld - 1) / kHeld * kHeld;
+  const int per = ((max(len, 0) + kSplit - 1) / kSplit + 31) / 32 * 32;
   const int lo = min(len, rank * per), count = min(len, lo + per) - lo;
   const bool sift = m > 0 && m < len;
   const float* w = p.score;
   if (sift) w += ((size_t)__ldg(p.slot + n) * c.Hkv + h) * p.max_tokens + lo;
   const int last = len - min(p.recent, max(len, 0));  // the first of the last tokens
-  const bool by_fours = (reinterpret_cast<uintptr_t>(w) & 15) == 0;
+  // A warp has an equal run of these, or as many as it holds; a lane every 32nd of it.
+  const bool held = count <= kBatch;
+  const int run = held ? ((count + kSelWarps - 1) / kSelWarps + 31) / 32 * 32 : 32 * kHeld;
   uint32_t key[kHeld];
   int valid = 0;  // of this thread's tokens
   auto load = [&](int base) {
-    const int i = base + tid * kHeld;
-    valid = max(0, min(kHeld, count - i));
+    const int i = base + warp * run + lane;
+    valid = max(0, (min(count - base - warp * run, run) - lane + 31) >> 5);
     float x[kHeld];
-    if (by_fours && valid == kHeld) {
 #pragma unroll
-      for (int j = 0; j < kHeld; j += 4) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(w + i + j));
-        x[j] = v.x;
-        x[j + 1] = v.y;
-        x[j + 2] = v.z;
-        x[j + 3] = v.w;
-      }
-    } else {
+    for (int j = 0; j < kHeld; ++j) x[j] = j < valid ? __ldg(w + i + 32 * j) : 0.f;
 #pragma unroll
-      for (int j = 0; j < kHeld; ++j) x[j] = j < valid ? __ldg(w + i + j) : 0.f;
+    for (int j = 0; j < kHeld; ++j) {
+      const int t = lo + i + 32 * j;
+      key[j] = t < p.sinks || t >= last ? 0xffffffffu : key_of(x[j]);
     }
-#pragma unroll
-    for (int j = 0; j < kHeld; ++j)
-      key[j] = lo + i + j < p.sinks || lo + i + j >= last ? 0xffffffffu : key_of(x[j]);
   };
-  const bool held = count <= kBatch;
   if (sift && held) load(0);
 #pragma unroll
   for (int i = tid; i < 2 * kBins / 4; i += kSelThreads) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
@@ -334,52 +326,44 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
     cluster_arrive();
   }
   int buf = 0, base = 0;
+  const uint32_t lower = (1u << lane) - 1u;
   batches([&] {
-    uint32_t is_over = 0, is_equal = 0;
+    int over = 0, equal = 0;
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
-      is_over |= (key[j] > border ? 1u : 0u) << j;
-      is_equal |= (key[j] == border ? 1u : 0u) << j;
+      over += j < valid && key[j] > border;
+      equal += j < valid && key[j] == border;
     }
-    const uint32_t real = valid == 32 ? ~0u : (1u << valid) - 1u;
-    is_over &= real;
-    is_equal &= real;
-    const int mine = __popc(is_over) | __popc(is_equal) << 16;  // no more than kBatch of each
-    int upto = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += o;
-    }
-    if (lane == 31) scan_s[buf][warp] = upto;
+    over = __reduce_add_sync(0xffffffffu, over);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    if (lane == 0) scan_s[buf][warp] = make_int2(over, equal);
     __syncthreads();
-    const int theirs = lane < kSelWarps ? scan_s[buf][lane] : 0;
-    int sums = theirs;
+    const int2 theirs = lane < kSelWarps ? scan_s[buf][lane] : make_int2(0, 0);
+    int o = over_before + __reduce_add_sync(0xffffffffu, lane < warp ? theirs.x : 0);
+    int e = equal_before + __reduce_add_sync(0xffffffffu, lane < warp ? theirs.y : 0);
+    int* to = kept + min(e, need);
+    const int first = lo + base + warp * run + lane;
+    if (equal == 0) {  // as a rule
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, sums, d);
-      if (lane >= d) sums += o;
+      for (int j = 0; j < kHeld; ++j) {
+        const bool is_over = j < valid && key[j] > border;
+        const uint32_t overs = __ballot_sync(0xffffffffu, is_over);
+        if (is_over) to[o + __popc(overs & lower)] = first + 32 * j;
+        o += __popc(overs);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) {
+        const bool is_over = j < valid && key[j] > border, is_equal = j < valid && key[j] == border;
+        const uint32_t overs = __ballot_sync(0xffffffffu, is_over), equals = __ballot_sync(0xffffffffu, is_equal);
+        const int mine = e + __popc(equals & lower);
+        if (is_over || (is_equal && mine < need)) kept[o + __popc(overs & lower) + min(mine, need)] = first + 32 * j;
+        o += __popc(overs);
+        e += __popc(equals);
+      }
     }
-    const int before = __shfl_sync(0xffffffffu, sums - theirs, warp) + upto - mine, all = __shfl_sync(0xffffffffu, sums, 31);
-    // by way of shared memory, where the threads' runs of them join
-    const int from = over_before + min(equal_before, need);
-    const int until = over_before + (all & 0xffff) + min(equal_before + (all >> 16), need);
-    const int i = lo + base + tid * kHeld;
-    int* out = hist[0];  // (of a cluster: read by the others before they arrived)
-    // this thread's: those above the border, and of those at it the ones that are needed
-    const int o = over_before + (before & 0xffff), e = equal_before + (before >> 16);
-    int spare = __popc(is_equal) - max(0, need - e);
-    for (; spare > 0 && is_equal; --spare) is_equal ^= 0x80000000u >> __clz(is_equal);
-    for (int at = from; at < until; at += kRoom) {
-      int to = o + min(e, need) - at;
-      for (uint32_t left = is_over | is_equal; left; left &= left - 1, ++to)
-        if (to >= 0 && to < kRoom) out[to] = i + __ffs(left) - 1;
-      __syncthreads();
-      for (int k = tid; k < min(kRoom, until - at); k += kSelThreads) kept[at + k] = out[k];
-      __syncthreads();
-    }
-    over_before += all & 0xffff;
-    equal_before += all >> 16;
+    over_before += __reduce_add_sync(0xffffffffu, theirs.x);
+    equal_before += __reduce_add_sync(0xffffffffu, theirs.y);
     base += kBatch;
     buf ^= 1;
   });
