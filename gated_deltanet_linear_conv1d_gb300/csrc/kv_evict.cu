@@ -17,9 +17,6 @@ namespace {
 
 // ---------------------------------------------------------------- select
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;
 constexpr int kFew = 256;  // weights at the border that are put in order all at once
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -75,15 +72,19 @@ __device__ __forceinline__ uint32_t key_of(float w) {
 
 // kSplit CTAs, a cluster, have a (request, kv head), each an equal run of its tokens; a thread has kHeld of them at a
 // time, and a CTA whose tokens are no more than its threads hold reads their weights once (else again, from L2, in each of
-// the passes). A pass counts the keys with the border's upper bits by their next 11. After two passes (after one of a short
-// request) few have all the bits so far, as a rule: those are put in order at once, by counting for each the larger ones.
-// Bound by the chain of loads, barriers and exchanges between the CTAs.
-template <int kSplit, int kHeld>
-__global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel(const EvictArgs p, const KvArgs c) {
-  constexpr int kBatch = kSelThreads * kHeld;
+// the passes). A pass counts the keys with the border's upper bits by their next kBits. After two passes (after one of a
+// short request) few have all the bits so far, as a rule: those are put in order at once, by counting for each the larger
+// ones.
+// Bound by the chain of loads, barriers and exchanges between the CTAs: of the 17 us that a CTA of eight takes for its part
+// of 131071 tokens of four heads (floor, 2 MB: 0.3 us), 3.7 are the first loads, 3.3 and 3.5 the passes, 3 the few, 2.9 the
+// kept indices. (With 8 bits a pass in 32 histograms, a lane's own each, a pass took 4.5 us, and one more was needed.)
+template <int kSplit, int kHeld, int kThreads, int kPerSm>
+__global__ void __launch_bounds__(kThreads, kPerSm) select_kernel(const EvictArgs p, const KvArgs c) {
+  constexpr int kWarps = kThreads / 32, kBatch = kThreads * kHeld;
+  constexpr int kBits = kThreads == 512 ? 11 : 10, kBins = 1 << kBits;
   __shared__ __align__(16) int hist[2][kBins];           // of two passes in turn: the others' CTAs read the one before
-  __shared__ int above_s[kSelWarps];
-  __shared__ int2 scan_s[2][kSelWarps];
+  __shared__ int above_s[kWarps];
+  __shared__ int2 scan_s[2][kWarps];
   __shared__ int pick[3];                                // the bin of the m-th largest, those above it, and in it
   __shared__ __align__(16) uint32_t few_s[kFew];
   __shared__ uint32_t own_few_s[kFew];
@@ -107,7 +108,7 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
   const int last = len - min(p.recent, max(len, 0));  // the first of the last tokens
   // A warp has an equal run of these, or as many as it holds; a lane every 32nd of it.
   const bool held = count <= kBatch;
-  const int run = held ? ((count + kSelWarps - 1) / kSelWarps + 31) / 32 * 32 : 32 * kHeld;
+  const int run = held ? ((count + kWarps - 1) / kWarps + 31) / 32 * 32 : 32 * kHeld;
   uint32_t key[kHeld];
   int valid = 0;  // of this thread's tokens
   auto load = [&](int base) {
@@ -124,17 +125,17 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
   };
   if (sift && held) load(0);
 #pragma unroll
-  for (int i = tid; i < 2 * kBins / 4; i += kSelThreads) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+  for (int i = tid; i < 2 * kBins / 4; i += kThreads) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
   if (tid < 2) few[tid] = 0;
   bool bad = false;
   if (m >= 0) {
 #pragma unroll 4
-    for (int i = tid; (long long)i * c.page < len; i += kSelThreads) {
+    for (int i = tid; (long long)i * c.page < len; i += kThreads) {
       const int page = __ldg(p.table + (size_t)n * p.max_pages + i);
       bad |= page < 0 || page >= c.pages;
     }
 #pragma unroll 4
-    for (int i = tid; (long long)i * c.page < m; i += kSelThreads) {
+    for (int i = tid; (long long)i * c.page < m; i += kThreads) {
       const int page = __ldg(p.dst_table + (size_t)n * p.dst_max_pages + i);
       bad |= page < 0 || page >= c.pages;
     }
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
   if (m <= 0 || why) return;  // the same in the whole cluster
   int* kept = p.kept + ((size_t)n * c.Hkv + h) * p.max_kept;
   if (!sift) {
-    for (int i = tid; i < count; i += kSelThreads) kept[lo + i] = lo + i;
+    for (int i = tid; i < count; i += kThreads) kept[lo + i] = lo + i;
     return;
   }
   auto batches = [&](auto work) {
@@ -166,11 +167,12 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
   int need = m;         // how many of those with its upper bits
   int over_before = 0, equal_before = 0;  // keys above the border, and at it, in the CTAs before this one
   bool counted = false;
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
+  for (int pass = 0, top = 32; top > 0; ++pass) {
+    const int width = min(top, kBits), shift = top - width;
+    top = shift;
     int* bins = hist[pass & 1];
-    if (pass == 2) {
-      for (int i = tid; i < kBins / 4; i += kSelThreads) reinterpret_cast<int4*>(bins)[i] = make_int4(0, 0, 0, 0);
+    if (pass >= 2) {
+      for (int i = tid; i < kBins / 4; i += kThreads) reinterpret_cast<int4*>(bins)[i] = make_int4(0, 0, 0, 0);
       __syncthreads();
     }
     batches([&] {
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
     if constexpr (kSplit > 1) cluster_sync();
     else __syncthreads();
     // this thread's four bins, and the keys in higher ones: a scan from the top
-    static_assert(kBins == 4 * kSelThreads, "four bins a thread");
+    static_assert(kBins == 4 * kThreads, "four bins a thread");
     int4 mine = reinterpret_cast<const int4*>(bins)[tid];
     if constexpr (kSplit > 1) {
       int4 theirs[kSplit - 1];
@@ -205,7 +207,7 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
     }
     if (lane == 0) above_s[warp] = upto;
     __syncthreads();
-    int above = upto - sum + __reduce_add_sync(0xffffffffu, lane > warp && lane < kSelWarps ? above_s[lane] : 0);
+    int above = upto - sum + __reduce_add_sync(0xffffffffu, lane > warp && lane < kWarps ? above_s[lane] : 0);
     if (above < need && above + sum >= need) {
       const int in[4] = {mine.x, mine.y, mine.z, mine.w};
 #pragma unroll
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
           const int end = __shfl_sync(0xffffffffu, upto, x);
           if (tid >= end) r = x + 1, first = end;
         }
-        static_assert(kFew <= kSelThreads, "a key a thread");
+        static_assert(kFew <= kThreads, "a key a thread");
         if (tid < in_bin) few_s[tid] = (uint32_t)load_remote(reinterpret_cast<const int*>(own_few_s) + tid - first, r);
         before = __shfl_sync(0xffffffffu, upto - theirs, rank);
         over_before = __reduce_add_sync(0xffffffffu, over_before);
@@ -338,7 +340,7 @@ __global__ void __launch_bounds__(kSelThreads, kHeld > 16 ? 1 : 2) select_kernel
     equal = __reduce_add_sync(0xffffffffu, equal);
     if (lane == 0) scan_s[buf][warp] = make_int2(over, equal);
     __syncthreads();
-    const int2 theirs = lane < kSelWarps ? scan_s[buf][lane] : make_int2(0, 0);
+    const int2 theirs = lane < kWarps ? scan_s[buf][lane] : make_int2(0, 0);
     int o = over_before + __reduce_add_sync(0xffffffffu, lane < warp ? theirs.x : 0);
     int e = equal_before + __reduce_add_sync(0xffffffffu, lane < warp ? theirs.y : 0);
     int* to = kept + min(e, need);
@@ -609,11 +611,11 @@ __global__ void __launch_bounds__(kMoveThreads, 2) shift_kernel(const EvictArgs 
   }
 }
 
-template <int kSplit, int kHeld>
+template <int kSplit, int kHeld, int kThreads, int kPerSm>
 cudaError_t launch_select(const EvictArgs& a, const KvArgs& c, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((long long)a.N * c.Hkv * kSplit), 1, 1);
-  cfg.blockDim = dim3(kSelThreads, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -624,21 +626,24 @@ cudaError_t launch_select(const EvictArgs& a, const KvArgs& c, cudaStream_t stre
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, select_kernel<kSplit, kHeld>, a, c);
+  return cudaLaunchKernelEx(&cfg, select_kernel<kSplit, kHeld, kThreads, kPerSm>, a, c);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_evict(const EvictArgs& a, const KvArgs& c, cudaStream_t stream) {
   const long long units = (long long)a.N * c.Hkv;
-  // as many CTAs a head as hold the longest request that the tables allow in registers, up to 131072 tokens
   const long long most = std::min<long long>((long long)a.max_pages * c.page, a.max_tokens);
-  const cudaError_t err = most <= 4 * kSelThreads    ? launch_select<1, 4>(a, c, stream)
-                          : most <= 16 * kSelThreads ? launch_select<1, 16>(a, c, stream)
-                          : most <= 32 * kSelThreads ? launch_select<2, 16>(a, c, stream)
-                          : most <= 64 * kSelThreads ? launch_select<4, 16>(a, c, stream)
-                          : most <= 128 * kSelThreads ? launch_select<8, 16>(a, c, stream)
-                                                      : launch_select<8, 32>(a, c, stream);
+  // As many CTAs a head as hold the longest request that the tables allow in registers, up to 131072 tokens. What a CTA takes
+  // is a chain of steps, whatever its tokens, so of many heads the fewer CTAs the better, and four small ones an SM: with 4
+  // x 512 threads of 16 tokens, two an SM, 32 requests of 2k .. 32k took 150 us, selection and copy, with 4 x 256 of 32 143,
+  // with 8 x 256 of 16 158. (With 1 x 512 of 16, three an SM, 128 of 300 .. 8k took 193, with 1 x 256 of 32 195.)
+  const cudaError_t err = most <= 2048    ? launch_select<1, 4, 512, 2>(a, c, stream)
+                          : most <= 8192  ? launch_select<1, 16, 512, 3>(a, c, stream)
+                          : most <= 16384 ? launch_select<2, 32, 256, 4>(a, c, stream)
+                          : most <= 32768 ? launch_select<4, 32, 256, 4>(a, c, stream)
+                          : most <= 65536 ? launch_select<8, 32, 256, 4>(a, c, stream)
+                                          : launch_select<8, 32, 512, 1>(a, c, stream);
   if (err != cudaSuccess) return err;
   const int row_bytes = a.D * (c.e4m3 ? 1 : 2);
   int shift = -1;
