@@ -439,6 +439,23 @@ def test_evict_of_a_long_request(b, err, n, budget, place):
                 *((fresh, ints([2])) if place != "in place" else ()))
 
 
+@pytest.mark.parametrize("n", [2000, 8100, 16300, 32700, 65500, 131000, 139000])
+@pytest.mark.parametrize("kind", ["alike", "two values", "last bits", "steps", "few at the border"])
+def test_evict_of_weights_close_together(b, err, n, kind):
+    """Every number of blocks a head, with weights that differ late or not at all, beside requests of a part of the length."""
+    lens = [n, n // 3, 700, 33, 1]
+    budgets = [n // 2, n // 3 - 1, 699, 5, 1]
+    pool, table, w, fresh = evict_case("e4m3", 2, 128, 64, lens, budgets)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    pick = torch.randint(0, 1 << 20, w.shape, generator=g, device="cuda")
+    w = {"alike": torch.zeros_like(w), "two values": torch.where(pick % 2 == 0, 0.5, 0.5 + 2.0 ** -24),
+         "last bits": (0x3F000000 + pick % 1024).to(torch.int32).view(torch.float32),
+         "steps": 2.0 ** -(pick % 3).float() * (1 + (pick % 5).float() * 2.0 ** -12),
+         "few at the border": torch.where(pick % 4096 == 0, 1.0, torch.where(pick % 2 == 0, 2.0, 0.5))}[kind].contiguous()
+    slots = torch.randperm(11, device="cuda").to(torch.int32)
+    check_evict(b, err, pool, table, lens, budgets, w, slots[:5].contiguous(), 2, 9, fresh, slots[5:10].contiguous())
+
+
 def test_evict_of_many_short_requests(b, err):
     lens = [1 + i % 37 for i in range(300)]
     pool, table, w, _ = evict_case("bf16", 2, 128, 16, lens, [n // 2 for n in lens])
