@@ -444,7 +444,6 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const Args a, const _
         if (t % kGroups == warp >> 2 && old && (again || tok < s.ctx)) before = out[tok];
       };
       int page = load_page(s.t0), next_page = load_page(s.t0 + 1);
-      load_token(s.t0, page);
       // The segment's query rows, once the MMAs of the one before are through. (Whoever gives up a wait goes on without
       // effect: no warp is missing at a barrier of several.)
       wait_warp(&B->q_empty, (seg & 1) ^ 1, abort);
@@ -452,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const Args a, const _
       asm volatile("fence.proxy.async;" ::: "memory");
       __syncwarp();
       if (lane == 0) arrive_both(&B->q_full[b2]);
+      load_token(s.t0, page);
       wait_cluster(&B->q_full[b2], (seg >> 1) & 1, abort);
       __syncwarp();
       // rows that add nothing or have factors of their own: the way of masked tiles for all of them
