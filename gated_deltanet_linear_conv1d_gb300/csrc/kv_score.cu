@@ -9,13 +9,18 @@
 // S^T [128 tokens x rows] = K Q^T on the tensor cores (tcgen05): the keys are the first operand, from shared memory as
 // they lie in the cache, so a token is a lane of tensor memory, and its sum over the rows is one thread's, in the order of
 // the rows. An E4M3 cache stays E4M3, and Q (bf16, scaled by a power of two) is written as the sum of two E4M3 terms, exact
-// down to 2^-17 of the largest value; the two are columns of one MMA, added as they are read.
+// down to 2^-17 of the largest value, a rounding below the scores' own; the two are columns of one MMA, added as they are
+// read.
 //
 // Work. The tiles of 128 tokens of all (request, kv head) units stand in one line, cut into equal pieces, one per CTA. A
 // unit's rows, up to 64, stay in shared memory for its tiles; more go to kv_score_pair.cu.
 //
-// Roles: two groups of four warps that take the tiles in turn (a thread has one token), a warp for the copies (TMA, 16 KB
-// blocks of 128 tokens x 128 bytes into a ring), one for the MMAs, two for the query rows. Every wait is bounded.
+// Roles: two groups of four warps that take the tiles in turn (a thread has one token), two warps for the copies (TMA, 16 KB
+// blocks of 128 tokens x 128 bytes into a ring), one for the MMAs, four for the query rows. Every wait is bounded.
+//
+// Bound by HBM where there are few rows: 256 requests of 1k .. 8k tokens, 6 rows, E4M3, 152 us for 949 MB, 92 % of the
+// copy bandwidth. With more rows a unit's beginning (its pages, its query rows and their constants, its first keys, each a
+// trip to memory) is a good part: 32 trees of 8 nodes, 48 rows, on 129 .. 16384 tokens in pages of 16 32 us, for 118 MB.
 #include "kv_score.cuh"
 
 namespace gdn {
@@ -422,8 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1) score_kernel(const Args a, const 
 #pragma unroll
           for (int i = 0; i < kN / 4; ++i) l[i] = *reinterpret_cast<const float4*>(lse + r0 + 4 * i);
         };
-        // The weights of four rows' scores. (Two at a time in packed operations, 32 rows took 443 cycles of a warp alone,
-        // 198 like this; the exponentials' pipe is busy for 128.)
+        // The weights of four rows' scores. (32 rows of a warp alone: 443 cycles two at a time in packed operations, 198 like
+        // this; the exponentials' pipe is busy for 128.)
         auto weights = [&](const uint32_t* u, const float4& l, float (&e)[4], const float4& f) {
           e[0] = ex2(fmaf(__uint_as_float(u[0]), f.x, l.x));
           e[1] = ex2(fmaf(__uint_as_float(u[1]), f.y, l.y));
