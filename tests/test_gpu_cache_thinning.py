@@ -183,6 +183,73 @@ def test_lse_and_score(b, err, fmt, heads, page, lens, nodes, tree, strong):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,nodes", [("24x4x256", 1), ("24x4x256", 7), ("32x8x128", 64)])
+def test_lse_of_rows_that_see_nothing_and_of_requests_left_out(b, err, fmt, heads, nodes):
+    """-inf without a context and without a node; a padding request's, a bad page's and a too long request's rows stay."""
+    lens = [0, 700, -3, 0, 200, 90, 5000]
+    pool, table, ctx, q, scale = case(heads, fmt, 64, lens, nodes)
+    mask = torch.randint(-2 ** 63, 2 ** 63 - 1, (len(lens), nodes), device="cuda")
+    mask[0] = 0
+    mask[3, ::2] = 0
+    ref, bound = T.lse(pool, q, table, ctx, scale, nodes, mask)
+    gone = [2, 4, 5]
+    table[4, 1] = pool.k.shape[0]
+    ctx[5] = 64 * table.shape[1] - nodes + 1
+    _, lse = attend(b, pool, q, table, ctx, scale, nodes, mask, dev_err=err)
+    assert b.gdn_read_device_error(err) == b.GDN_DEVERR_SLOT | b.GDN_DEVERR_OFFSETS
+    rows = lambda n: slice(n * nodes, (n + 1) * nodes)  # noqa: E731
+    for n in gone:
+        assert bool(lse[rows(n)].isnan().all()), n
+    keep = torch.cat([torch.arange(len(lens) * nodes, device="cuda")[rows(n)] for n in range(len(lens)) if n not in gone])
+    inside(lse[keep], ref[keep], bound[keep], "lse")
+    assert bool((lse[rows(0)] == -INF).all()) and bool((lse[rows(3)][::2] == -INF).all())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("nodes", [2, 64])
+def test_captured_scores_and_evictions_replay_with_other_lengths(b, err, fmt, nodes):
+    """A step's scores and its eviction as one graph: replayed with other contexts, slots and budgets it takes them, as
+    eager calls do; two graphs of the same buffers in turn."""
+    pool, table, ctx, q, scale = case("24x4x256", fmt, 64, [900, 300, 40], nodes)
+    lse = T.lse(pool, q, table, ctx, scale, nodes)[0].float()
+    slot, weights = ints([0, 1, 2]), torch.zeros(6, 4, 1000, device="cuda")
+    length, budget, new_len = ints([0, 0, 0]), ints([500, 100, 60]), ints([0, 0, 0])
+    kept = torch.zeros(3, 4, 1000, dtype=torch.int32, device="cuda")
+
+    def step():
+        b.gdn_kv_score(pool.handle(b), q, lse, table, ctx, scale, weights, slot, nodes, dev_err=err)
+        torch.add(ctx, nodes, out=length)
+        b.gdn_kv_evict(pool.handle(b), table, length, budget, weights, slot, kept, new_len, 2, 8, dev_err=err)
+        torch.sub(new_len, nodes, out=ctx)
+
+    state = (pool.k, pool.v, weights, ctx, new_len, kept) + ((pool.k_scale, pool.v_scale) if fmt == "e4m3" else ())
+    start = [t.clone() for t in state]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g in graphs:
+        with torch.cuda.graph(g, stream=side):
+            step()
+    plans = [([500, 100, 60], [0, 1, 2]), ([400, 100, 66], [2, 0, 1]), ([333, -1, 0], [0, 1, 2]), ([nodes + 1] * 3, [3, 4, -1])]
+    results = []
+    for replayed in (False, True):
+        for t, was in zip(state, start):
+            t.copy_(was)
+        for i, (most, where) in enumerate(plans):
+            budget.copy_(ints(most))
+            slot.copy_(ints(where))
+            ctx.clamp_(min=0)
+            graphs[i % 2].replay() if replayed else step()
+        torch.cuda.synchronize()
+        results.append([t.clone() for t in state])
+        assert b.gdn_read_device_error(err) == b.GDN_DEVERR_OFFSETS  # the negative budget
+    for x, y in zip(*results):
+        assert torch.equal(bits(x), bits(y))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("seed", range(8))
 def test_score_of_random_sizes(b, err, fmt, seed):
     """Any mask, rows left out, padding requests and slots, shared pages; the scores of a new token start from zero whatever
