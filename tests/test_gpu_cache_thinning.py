@@ -523,6 +523,26 @@ def test_evict_of_weights_close_together(b, err, n, kind):
     check_evict(b, err, pool, table, lens, budgets, w, slots[:5].contiguous(), 2, 9, fresh, slots[5:10].contiguous())
 
 
+def test_scores_behind_32_bits(b, err):
+    """A pool of scores of more than 2^31 of them: the last slot's as a small pool's, scored, evicted to another slot and in
+    place."""
+    lens, nodes, room = [700, 90], 3, 1 << 26
+    pool, table, ctx, q, scale = case("24x4x256", "bf16", 64, lens, nodes)
+    lse = T.lse(pool, q, table, ctx, scale, nodes)[0].float()
+    far, near = torch.empty(9, 4, room, device="cuda"), torch.zeros(4, 4, 703, device="cuda")
+    far[[0, 8]], fresh = 0, torch.zeros(2, dtype=torch.bool, device="cuda")
+    kept = [torch.zeros(2, 4, 703, dtype=torch.int32, device="cuda") for _ in range(2)]
+    new_len, dst = ints([0, 0]), torch.arange(20, dtype=torch.int32, device="cuda").reshape(2, 10)
+    big = R.Pool(20 + pool.k.shape[0], 4, 64, 256, "bf16", seed=3)
+    for w, slot, to, k in ((far, ints([8, 7]), ints([6, 0]), kept[0]), (near, ints([3, 2]), ints([1, 0]), kept[1])):
+        b.gdn_kv_score(pool.handle(b), q, lse, table, ctx, scale, w, slot, nodes, has_init=fresh, dev_err=err)
+        b.gdn_kv_evict(big.handle(b), table + 20, ctx + nodes, ints([300, 50]), w, slot, k, new_len, 1, 2, dst, to, dev_err=err)
+    assert b.gdn_read_device_error(err) == 0 and new_len.tolist() == [300, 50]
+    assert torch.equal(kept[0], kept[1])
+    for x, y, n in ((8, 3, 703), (7, 2, 93), (6, 1, 300), (0, 0, 50)):
+        assert torch.equal(bits(far[x, :, :n]), bits(near[y, :, :n])), x
+
+
 def test_evict_of_many_short_requests(b, err):
     lens = [1 + i % 37 for i in range(300)]
     pool, table, w, _ = evict_case("bf16", 2, 128, 16, lens, [n // 2 for n in lens])
