@@ -17,7 +17,7 @@ namespace {
 
 // ---------------------------------------------------------------- select
 
-constexpr int kFew = 256;  // weights at the border that are put in order all at once
+constexpr int kFew = 128;  // weights at the border that are put in order all at once
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
