@@ -539,40 +539,52 @@ __global__ void __launch_bounds__(kMoveThreads, 2) copy_kernel(const EvictArgs p
 // Bound by the chunks of a block coming one after the other: 32 requests of 8192 tokens, E4M3, cut to half, 550 MB, 123 us
 // where copy_kernel takes 90.
 //
-// Tokens [first, m) of one head: `lanes` threads a token, each with one T; chunks of kUnroll tokens a thread. `row` finds
-// the place that a token comes from, `from` and `to` give its address and that of the place that it goes to. What a chunk
-// needs to be read comes a chunk ahead (its places) and two (its indices).
+// Tokens [first, m) of one head: `lanes` threads a token, each with one T; chunks of kShift tokens a thread. `row` finds
+// the place that a token comes from, `from` and `to` give its address and that of the place that it goes to. A chunk is
+// read while the one before it is stored: what it reads lies behind where that goes. Its places come a chunk ahead of
+// that, its indices two.
+constexpr int kShift = 4;
 template <typename T, typename Row, typename From, typename To>
 __device__ __forceinline__ void shift_rows(int first, int m, int lanes, const int* kept, Row row, From from, To to) {
-  const int per = kMoveThreads / lanes, r = threadIdx.x / lanes, chunk = per * kUnroll;
-  T held[kUnroll];
-  int place[kUnroll], index[kUnroll];
+  const int per = kMoveThreads / lanes, r = threadIdx.x / lanes, chunk = per * kShift;
+  T even[kShift], odd[kShift];
+  int place[kShift], index[kShift];
   auto indices = [&](int base) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < kShift; ++u) {
       const int i = base + u * per + r;
       index[u] = i < m ? __ldg(kept + i) : -1;
     }
   };
   auto places = [&] {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) place[u] = index[u] >= 0 ? row(index[u]) : -1;
+    for (int u = 0; u < kShift; ++u) place[u] = index[u] >= 0 ? row(index[u]) : -1;
+  };
+  auto read = [&](T (&held)[kShift]) {
+#pragma unroll
+    for (int u = 0; u < kShift; ++u)
+      if (place[u] >= 0) held[u] = *from(place[u]);
+  };
+  auto step = [&](int base, T (&now)[kShift], T (&next)[kShift]) {
+    read(next);
+    places();
+    indices(base + 3 * chunk);
+    __syncthreads();  // the whole chunk has been read: a part of it is where it goes
+#pragma unroll
+    for (int u = 0; u < kShift; ++u) {
+      const int i = base + u * per + r;
+      if (i < m) *to(i) = now[u];
+    }
   };
   indices(first);
   places();
   indices(first + chunk);
-  for (int base = first; base < m; base += chunk) {
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (place[u] >= 0) held[u] = *from(place[u]);
-    places();
-    indices(base + 2 * chunk);
-    __syncthreads();  // the whole chunk has been read: a part of it is where it goes
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = base + u * per + r;
-      if (i < m) *to(i) = held[u];
-    }
+  read(even);
+  places();
+  indices(first + 2 * chunk);
+  for (int base = first; base < m; base += 2 * chunk) {
+    step(base, even, odd);
+    if (base + chunk < m) step(base + chunk, odd, even);
   }
 }
 
