@@ -536,15 +536,14 @@ __global__ void __launch_bounds__(kMoveThreads, 2) copy_kernel(const EvictArgs p
 // In place: kept token i has index kept[i] >= i, so a chunk of tokens is stored where only earlier chunks' tokens, or this
 // one's, were read: a block takes its chunks in order and has read a chunk before it stores it. Blocks share no byte: a
 // block has one head's keys or values, or a slice of their rows, or its floats.
-// Bound by the chunks of a block coming one after the other: 32 requests of 8192 tokens, E4M3, cut to half, 550 MB, 123 us
-// where copy_kernel takes 90.
+// Bound by the chunks of a block coming one after the other: 32 requests of 8192 tokens, E4M3, cut to half, 550 MB, 110 us
+// where copy_kernel takes 88.
 //
 // Tokens [first, m) of one head: `lanes` threads a token, each with one T; chunks of kShift tokens a thread. `row` finds
 // the place that a token comes from, `from` and `to` give its address and that of the place that it goes to. A chunk is
 // read while the one before it is stored: what it reads lies behind where that goes. Its places come a chunk ahead of
 // that, its indices two.
-constexpr int kShift = 4;
-template <typename T, typename Row, typename From, typename To>
+template <typename T, int kShift, typename Row, typename From, typename To>
 __device__ __forceinline__ void shift_rows(int first, int m, int lanes, const int* kept, Row row, From from, To to) {
   const int per = kMoveThreads / lanes, r = threadIdx.x / lanes, chunk = per * kShift;
   T even[kShift], odd[kShift];
@@ -589,7 +588,8 @@ __device__ __forceinline__ void shift_rows(int first, int m, int lanes, const in
 }
 
 // A unit's parts: its keys' slices, its values' slices, and its floats (scales and weights).
-__global__ void __launch_bounds__(kMoveThreads, 2) shift_kernel(const EvictArgs p, const KvArgs c, int slices, int shift) {
+template <int kShift>
+__global__ void __launch_bounds__(kMoveThreads, kShift > 4 ? 1 : 2) shift_kernel(const EvictArgs p, const KvArgs c, int slices, int shift) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int parts = 2 * slices + 1;
   const long long unit = blockIdx.x / parts;
@@ -611,17 +611,17 @@ __global__ void __launch_bounds__(kMoveThreads, 2) shift_kernel(const EvictArgs 
   if (part < 2 * slices) {
     const int pieces = p.D * (c.e4m3 ? 1 : 2) / 16, lanes = pieces / slices;
     uint4* pool = static_cast<uint4*>(part < slices ? c.k : c.v) + (part % slices) * lanes + threadIdx.x % lanes;
-    shift_rows<uint4>(first, m, lanes, kept, row, [&](int at) { return pool + (size_t)at * pieces; },
+    shift_rows<uint4, kShift>(first, m, lanes, kept, row, [&](int at) { return pool + (size_t)at * pieces; },
                       [&](int i) { return pool + (size_t)row(i) * pieces; });
   } else {
     if (c.e4m3) {
-      shift_rows<float>(first, m, 1, kept, row, [&](int at) { return c.k_scale + at; },
+      shift_rows<float, kShift>(first, m, 1, kept, row, [&](int at) { return c.k_scale + at; },
                         [&](int i) { return c.k_scale + row(i); });
-      shift_rows<float>(first, m, 1, kept, row, [&](int at) { return c.v_scale + at; },
+      shift_rows<float, kShift>(first, m, 1, kept, row, [&](int at) { return c.v_scale + at; },
                         [&](int i) { return c.v_scale + row(i); });
     }
     float* w = p.score + ((size_t)__ldg(p.slot + n) * c.Hkv + h) * p.max_tokens;
-    shift_rows<float>(first, m, 1, kept, [](int i) { return i; }, [&](int at) { return w + at; },
+    shift_rows<float, kShift>(first, m, 1, kept, [](int i) { return i; }, [&](int at) { return w + at; },
                       [&](int i) { return w + i; });
   }
 }
@@ -681,8 +681,12 @@ cudaError_t launch_kv_evict(const EvictArgs& a, const KvArgs& c, cudaStream_t st
   // slices of the rows, down to a sector, while there are too few blocks to keep HBM busy
   int slices = 1;
   while (row_bytes / slices > 32 && units * 2 * slices < 2 * 152) slices *= 2;
-  cfg.gridDim = dim3((unsigned)(units * (2 * slices + 1)), 1, 1);
-  return cudaLaunchKernelEx(&cfg, shift_kernel, a, c, slices, shift);
+  const long long blocks = units * (2 * slices + 1);
+  cfg.gridDim = dim3((unsigned)blocks, 1, 1);
+  // A block that has an SM's registers for itself takes chunks twice as long: one request of 65536 tokens, bf16, to half,
+  // selection and shift, 123 us, with the short ones 148. (Where there are more blocks, 32 of 8192, E4M3, 161 and 131.)
+  return blocks <= 152 ? cudaLaunchKernelEx(&cfg, shift_kernel<8>, a, c, slices, shift)
+                       : cudaLaunchKernelEx(&cfg, shift_kernel<4>, a, c, slices, shift);
 }
 
 }  // namespace gdn
