@@ -311,7 +311,7 @@ __device__ __forceinline__ void rows_pass(const RopeArgs& p, const KvArgs& c, co
 // The frequency in turns is an fp64 product with 1 / (2 pi), off by up to 2^-52 of itself, and so is the angle: 2^-24
 // turns at the largest position and a radian a position, about what the fp64 product of the two is off by. The fixed
 // point adds 2^-65 turns a position, the cut to the upper 32 bits up to 2^-32. With several axes a frequency's row of
-// positions is found once per block, so that the angles cost what they cost with one: the positions of a block's tokens
+// positions is found once per thread, so that the angles cost what they cost with one: the positions of a block's tokens
 // are a few cache lines per axis.
 // What bounds it: HBM at many tokens, the launch and the angles' chain at few. A batch is copied to shared memory while
 // the one before it is worked on: loads into registers left none in flight meanwhile, and a second batch of registers
@@ -324,7 +324,6 @@ __device__ __forceinline__ void rows_pass(const RopeArgs& p, const KvArgs& c, co
 template <int D, bool kNorm, int kCache, int kRot>
 __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RopeArgs p, const KvArgs c, int tokens_per_block) {
   __shared__ uint64_t freq[kNorm ? D / 2 : 1];
-  __shared__ int axis[kNorm ? D / 2 : 1];
   __shared__ int place[kMaxTokens];
   extern __shared__ __align__(16) unsigned char stage[];  // [kBuffers][groups][kRows][D] bf16
   float2* turn = reinterpret_cast<float2*>(stage + kBuffers * kBatchBytes);  // [tokens][half]
@@ -334,14 +333,22 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const RopeArgs p, con
   if constexpr (kNorm) {
     const int half = p.rotary / 2;
     if (half > 0) {
+      // a power of two, so a thread has one frequency, and every (kThreads / half)th token; a token's position ahead
+      const int32_t* at = p.positions + t0 + threadIdx.x / half;
+      if (p.axes.num_axes) {  // (four axes a load: the lanes' loads of parameters go one address after the other)
+        const uint32_t f = threadIdx.x % half, four = reinterpret_cast<const uint32_t*>(p.axes.axis)[f / 4];
+        at += (int64_t)(four >> (8 * (f % 4)) & 255u) * p.T;
+      }
+      int32_t next = threadIdx.x < T * half ? *at : 0;
       for (int i = threadIdx.x; i < half; i += kThreads) {
         const double f = p.inv_freq[i] * 0.15915494309189535;  // 1 / (2 pi): turns per position
         freq[i] = __double2ull_rn((f - floor(f)) * 18446744073709551616.0);
-        axis[i] = p.axes.num_axes ? p.axes.axis[i] : 0;
       }
       __syncthreads();
       for (int i = threadIdx.x; i < T * half; i += kThreads) {
-        const int64_t pos = p.positions[(int64_t)axis[i % half] * p.T + t0 + i / half];
+        const int64_t pos = next;
+        at += kThreads / half;
+        if (i + kThreads < T * half) next = *at;
         // the upper 32 bits as a signed number: half turns in [-1, 1)
         const int32_t top = (int32_t)(((uint64_t)pos * freq[i % half]) >> 32);
         // what the conversion to fp32 rounds off, up to 2^-25 half turns, turns sine and cosine on to first order
