@@ -401,7 +401,8 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
 }
 // 2^e.
 constexpr float exp2_of(int e) { return e == 0 ? 1.f : e < 0 ? 0.5f * exp2_of(e + 1) : 2.f * exp2_of(e - 1); }
-// The exponent of a value scale, 128 of one that is no number, and 2 / 2^exponent, which is 0 then.
+// The exponent of a value scale, 128 of one that is no number, and 2 / 2^exponent, which is 0 then (so that a weight with
+// such a scale, a product with it, is a NaN).
 __device__ __forceinline__ int scale_exp(float s) {
   return max((int)(__float_as_uint(s) >> 23 & 255u) - 127, kMinScaleExp);
 }
@@ -1086,6 +1087,10 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
           for (int k = 0; k < 4; ++k) {
             part[k] = two_over_exp(sv[k]);
             f[k] = sv[k] * part[k] * (0.5f * kTermTop * exp2_of(-kTopExp));
+          }
+          if (p.lse) {  // what a token weighs does not go by its values: 2 / 2^128 of a scale that is no number
+#pragma unroll
+            for (int k = 0; k < 4; ++k) part[k] = __uint_as_float(max(__float_as_uint(part[k]), 0x00400000u));
           }
         }
         __syncwarp();

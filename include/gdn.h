@@ -611,8 +611,8 @@ size_t gdn_tree_attention_workspace_bytes(const gdn_kv_cache *cache, int32_t num
 /*
  * gdn_tree_attention_lse - gdn_tree_attention that also leaves what each row's
  * weights are relative to, lse = ln sum_t e^(scale (q . k_t)) over the tokens
- * that the row sees: -inf for a row that sees nothing. Out and its bits are
- * gdn_tree_attention's; the workspace too.
+ * that the row sees, whatever their values: -inf for a row that sees nothing. Out
+ * and its bits are gdn_tree_attention's; the workspace too.
  *
  *   lse  [N*P][Hq] fp32 out, 4-byte aligned; a padding request's rows and those of a
  *        request that writes nothing are left untouched

@@ -1,0 +1,131 @@
+"""Edges of what thins out a cache: values and pages that are no good, memory that the call in front has just written, long
+pieces of the line of tiles, calls on two streams, a captured step. Against the fp64 statements, whose tolerances count the
+roundings (attnref, thinref)."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from tests import attnref as R  # noqa: E402
+from tests import thinref as T  # noqa: E402
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module")
+def b():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from gated_deltanet_linear_conv1d_gb300 import build
+    build.build()
+    from gated_deltanet_linear_conv1d_gb300 import binding
+    return binding
+
+
+@pytest.fixture
+def err():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def randn(*shape, seed=0):
+    return torch.randn(shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def bits(t):
+    return t.contiguous().view(torch.uint8)
+
+
+def inside(got, ref, bound, what):
+    off = (got.double() - ref).abs()
+    bad = ~(off <= bound) & ~(got.isnan() & ref.isnan()) & ~(got.double() == ref)
+    assert not bool(bad.any()), f"{what}: {int(bad.sum())} of {bad.numel()} off, worst {float((off / bound)[bad].max())}" \
+                                f" times its bound at {torch.nonzero(bad)[0].tolist()}"
+
+
+def case(heads, fmt, page, lens, nodes, seed=0, strong=1.0):
+    hq, hkv, d = heads
+    held = [n + nodes for n in lens]
+    pages = sum(-(-n // page) for n in held) + 2
+    pool = R.Pool(pages, hkv, page, d, fmt, seed=seed)
+    table = R.tables(held, page, pages, seed=seed)
+    q = (randn(len(lens) * nodes, hq, d, seed=seed + 9) * strong).to(torch.bfloat16)
+    return pool, table, ints(lens), q, d ** -0.5
+
+
+def attend(b, pool, q, table, ctx, scale, nodes, was=NAN, **kw):
+    out, lse = torch.full_like(q, NAN), torch.full(q.shape[:2], was, device="cuda")
+    b.gdn_tree_attention_lse(pool.handle(b), q, table, ctx, scale, out, lse, nodes, **kw)
+    return out, lse
+
+
+def parts(pool):
+    return [x for x in ("k", "v", "k_scale", "v_scale") if getattr(pool, x) is not None]
+
+
+def copy_of(pool):
+    """A pool with the same contents."""
+    other = R.Pool(1, 1, pool.page, pool.k.shape[-1], pool.fmt)
+    for x in parts(pool):
+        setattr(other, x, getattr(pool, x).clone())
+    return other
+
+
+# ---------------------------------------------------------------- the log-sum-exp over an E4M3 cache
+
+# heads, nodes: a row tile of up to 16, of up to 32 and of up to 64 rows, and several of them
+ROWS = [((24, 4, 256), 1), ((24, 4, 256), 5), ((32, 8, 128), 7), ((24, 4, 256), 20)]
+
+
+def spread_bound(ref, bound):
+    """The attention's maxima are of scores with the exponents of the values' scales, of up to 128, in them: the score with
+    the exponent, that less the maximum, the maximum with the sum's logarithm (the sum is 2^-190 of the largest weight at
+    least) and its product with ln 2 are each rounded to fp32, 2^-24 of numbers of up to twice the log-sum-exp and 400."""
+    return bound + 4 * (2 * ref.abs().nan_to_num(0, 0, 0) + 400) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("odd", [NAN, INF, -INF])
+@pytest.mark.parametrize("heads,nodes", ROWS)
+def test_lse_of_values_that_are_no_numbers(b, err, heads, nodes, odd):
+    """The log-sum-exp is of queries and keys: a token whose values, or their scale, are no numbers counts in it like any
+    other, while the request's output shows it."""
+    lens = [300, 20000, 40]
+    pool, table, ctx, q, scale = case(heads, "e4m3", 64, lens, nodes)
+    ref, bound = T.lse(pool, q, table, ctx, scale, nodes)
+    weight = torch.exp(T.logits(pool, q, table, 2, lens[2], scale, nodes)[0][..., 7].reshape(nodes, -1) - ref[2 * nodes:])
+    assert float(weight.max()) > 1e-2  # what would be missing
+    for n, t in ((1, 0), (1, 19999), (2, 7)):
+        pool.v_scale[int(table[n, t // 64]), :, t % 64] = odd
+    pool.v[int(table[2, 0]), :, 9] = 0x7F
+    out, lse = attend(b, pool, q, table, ctx, scale, nodes, dev_err=err)
+    assert b.gdn_read_device_error(err) == 0
+    inside(lse, ref, spread_bound(ref, bound), "lse")
+    assert not bool(out[nodes:].isfinite().any()) and bool(out[:nodes].isfinite().all())
+
+
+@pytest.mark.parametrize("heads,nodes", ROWS)
+@pytest.mark.parametrize("strong", [0.0, 1.0, 12.0])
+@pytest.mark.parametrize("kind", ["0", "5", "60", "one large", "one small"])
+def test_lse_over_value_scales_far_apart(b, err, heads, nodes, strong, kind):
+    """Every token's values with a scale of their own, of either sign, or one token's at the other end of the format."""
+    lens = [777, 12, 127, 9000]
+    pool, table, ctx, q, scale = case(heads, "e4m3", 16, lens, nodes, seed=3, strong=strong)
+    if kind in ("one large", "one small"):
+        few, most = (2.0 ** 111, 1e-12 / 448) if kind == "one large" else (1e-12 / 448, 2.0 ** 111)
+        pool.v_scale.fill_(most)
+        for n, c in enumerate(lens):
+            pool.v_scale[int(table[n, c // 2 // 16]), :, c // 2 % 16] = few
+    else:
+        g = torch.Generator(device="cuda").manual_seed(7)
+        up = torch.randint(-int(kind), int(kind) + 1, pool.v_scale.shape, generator=g, device="cuda").float() / 2
+        sign = torch.randint(0, 2, pool.v_scale.shape, generator=g, device="cuda") * 2 - 1
+        pool.v_scale.mul_(torch.exp2(up) * sign)
+        if kind == "0":
+            pool.v_scale[:, :, ::3] = 0.0
+    _, lse = attend(b, pool, q, table, ctx, scale, nodes, dev_err=err)
+    assert b.gdn_read_device_error(err) == 0
+    ref, bound = T.lse(pool, q, table, ctx, scale, nodes)
+    inside(lse, ref, spread_bound(ref, bound), "lse")
