@@ -72,9 +72,9 @@ __global__ void __launch_bounds__(256) join_kernel(const tree_attn::Args a) {
     }
     m = mn;
   }
-  if (bad) return;
   if (p.lse && col == 0)
-    p.lse[((size_t)d.n * p.P + j) * p.Hq + d.u / a.row_tiles * p.G + r % p.G] = tree_attn::lse_of(m, l);
+    p.lse[((size_t)d.n * p.P + j) * p.Hq + d.u / a.row_tiles * p.G + r % p.G] = bad ? NAN : tree_attn::lse_of(m, l);
+  if (bad) return;
   const float f = l == 0.f ? 0.f : __fdividef(1.f, l);
   *reinterpret_cast<uint2*>(p.out + at) = tree_attn::to_out(make_float4(o.x * f, o.y * f, o.z * f, o.w * f), p.gate, gate);
 }

@@ -1300,13 +1300,11 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, kRows>::kThreads, 1) tree_attn_k
       if (any_in_group(bar, *(volatile int*)abort)) continue;
       if (bad && ot == 0) report(p.dev_err, GDN_DEVERR_SLOT);
       if (s.t0 == 0 && s.t1 == s.tiles) {
+        const int rr = r0 - roff + ot, j = rr / p.G;
+        if (p.lse && og == 0 && ot < a.rows && j < p.P)
+          p.lse[((size_t)s.n * p.P + j) * p.Hq + h * p.G + rr % p.G] = bad ? NAN : lse_of(m_run, l_run);
         if (bad) continue;
-        if (ot < a.rows) {
-          fin[ot] = l_run == 0.f ? 0.f : __fdividef(1.f, l_run);
-          const int rr = r0 - roff + ot, j = rr / p.G;
-          if (p.lse && og == 0 && j < p.P)
-            p.lse[((size_t)s.n * p.P + j) * p.Hq + h * p.G + rr % p.G] = lse_of(m_run, l_run);
-        }
+        if (ot < a.rows) fin[ot] = l_run == 0.f ? 0.f : __fdividef(1.f, l_run);
         // A few rows at a time through shared memory, a thread then has neighbouring values of one or two rows. The
         // loop is not unrolled (the registers' choice is): code that runs once per segment costs its fetches.
         constexpr int kS = C::kStageRows, kY = kS / 4;

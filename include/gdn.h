@@ -614,8 +614,10 @@ size_t gdn_tree_attention_workspace_bytes(const gdn_kv_cache *cache, int32_t num
  * that the row sees, whatever their values: -inf for a row that sees nothing. Out
  * and its bits are gdn_tree_attention's; the workspace too.
  *
- *   lse  [N*P][Hq] fp32 out, 4-byte aligned; a padding request's rows and those of a
- *        request that writes nothing are left untouched
+ *   lse  [N*P][Hq] fp32 out, 4-byte aligned. Rows of a padding request and of one that
+ *        the table cannot hold are left untouched; gdn_kv_score leaves both out too.
+ *        Those of a request with a page outside the pool are NaN: gdn_kv_score, which
+ *        skips that page's tokens alone, then adds nothing for them.
  */
 gdn_status gdn_tree_attention_lse(const gdn_kv_cache *cache, const uint16_t *q, const int32_t *block_table,
                                   int32_t max_pages, const int32_t *ctx_len, const uint64_t *tree_mask,

@@ -129,3 +129,34 @@ def test_lse_over_value_scales_far_apart(b, err, heads, nodes, strong, kind):
     assert b.gdn_read_device_error(err) == 0
     ref, bound = T.lse(pool, q, table, ctx, scale, nodes)
     inside(lse, ref, spread_bound(ref, bound), "lse")
+
+
+# ---------------------------------------------------------------- a page out of the pool
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,nodes", [((24, 4, 256), 1), ((24, 4, 256), 7), ((32, 8, 128), 30), ((24, 4, 256), 64)])
+def test_a_bad_page_leaves_no_weights_of_an_older_lse(b, err, fmt, heads, nodes):
+    """The attention leaves a request out that has a page outside the pool, and its log-sum-exp too: the buffer's older
+    contents, here the sums of much smaller scores, must not become weights. Scores of the other pages fade, new tokens' are
+    zero, the bad page's stay; the other requests are whole."""
+    lens = [300, 700, 20000, 20000, 90]
+    pool, table, ctx, q, scale = case(heads, fmt, 64, lens, nodes)
+    ref, bound = T.lse(pool, q, table, ctx, scale, nodes)
+    good = table.clone()
+    gone = {1: 3, 2: 0, 3: 20000 // 64}
+    for n, page in gone.items():
+        table[n, page] = pool.k.shape[0] if n % 2 else -1
+    _, lse = attend(b, pool, q, table, ctx, scale, nodes, was=-50.0, dev_err=err)
+    assert b.gdn_read_device_error(err) == b.GDN_DEVERR_SLOT
+    live = torch.tensor([n not in gone for n in range(5)], device="cuda").repeat_interleave(nodes)
+    assert bool(lse[~live].isnan().all())
+    inside(lse[live], ref[live], bound[live], "lse")
+    weights = randn(5, heads[1], 20100, seed=3).abs()
+    was, slot = weights.clone(), torch.arange(5, dtype=torch.int32, device="cuda")
+    want, lim = T.score(pool, q, lse, good, ctx, scale, nodes, weights, slot, None, 0.5)
+    b.gdn_kv_score(pool.handle(b), q, lse, table, ctx, scale, weights, slot, nodes, decay=0.5, dev_err=err)
+    assert b.gdn_read_device_error(err) == b.GDN_DEVERR_SLOT
+    for n, page in gone.items():
+        rows = slice(page * 64, page * 64 + 64)
+        want[n, :, rows], lim[n, :, rows] = was[n, :, rows].double(), 0
+    inside(weights, want, lim, "score")
