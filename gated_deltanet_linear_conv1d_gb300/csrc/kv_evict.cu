@@ -6,6 +6,8 @@
 //           kept tokens in ascending order. Weights that are equal at the border go to the lowest indices.
 //   move:   the kept tokens' keys, values, scales and weights, in the order of the tokens, to other pages (copy_kernel) or
 //           to the front of the request's own (shift_kernel).
+// Every kernel here may begin before the one in front of it ends, so what that one writes (the weights; the new lengths and
+// the kept indices) is read by plain loads: read-only ones are for memory that nobody writes while the kernel is there.
 #include <algorithm>
 
 #include "device.cuh"
@@ -116,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) select_kernel(const EvictArg
     valid = max(0, (min(count - base - warp * run, run) - lane + 31) >> 5);
     float x[kHeld];
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j) x[j] = j < valid ? __ldg(w + i + 32 * j) : 0.f;
+    for (int j = 0; j < kHeld; ++j) x[j] = j < valid ? w[i + 32 * j] : 0.f;
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
       const int t = lo + i + 32 * j;
@@ -405,7 +407,7 @@ __global__ void __launch_bounds__(kMoveThreads, 2) copy_kernel(const EvictArgs p
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto tokens_of = [&](int n) {
-    const int m = __ldg(p.len + n) < 0 || __ldg(p.slot + n) < 0 ? 0 : __ldg(p.new_len + n);
+    const int m = __ldg(p.len + n) < 0 || __ldg(p.slot + n) < 0 ? 0 : p.new_len[n];
     return max(m, 0);
   };
   auto segments_of = [&](int n) { return (tokens_of(n) + kTokens - 1) / kTokens; };
@@ -470,7 +472,7 @@ __global__ void __launch_bounds__(kMoveThreads, 2) copy_kernel(const EvictArgs p
     return true;
   };
   auto index_of = [&](const Seg& x) {
-    return tid < x.count ? __ldg(p.kept + ((size_t)x.n * c.Hkv + x.h) * p.max_kept + x.first + tid) : -1;
+    return tid < x.count ? p.kept[((size_t)x.n * c.Hkv + x.h) * p.max_kept + x.first + tid] : -1;
   };
   auto look_up = [&](const Seg& x, int index) {
     if (tid >= x.count) return make_int2(-1, -1);
@@ -552,7 +554,7 @@ __device__ __forceinline__ void shift_rows(int first, int m, int lanes, const in
 #pragma unroll
     for (int u = 0; u < kShift; ++u) {
       const int i = base + u * per + r;
-      index[u] = i < m ? __ldg(kept + i) : -1;
+      index[u] = i < m ? kept[i] : -1;
     }
   };
   auto places = [&] {
@@ -604,7 +606,7 @@ __global__ void __launch_bounds__(kMoveThreads, kShift > 4 ? 1 : 2) shift_kernel
   int first = 0, hi = m;
   while (first < hi) {
     const int mid = (first + hi) >> 1;
-    if (__ldg(kept + mid) == mid) first = mid + 1;
+    if (kept[mid] == mid) first = mid + 1;
     else hi = mid;
   }
   auto row = [&](int i) { return rows.at(c, i); };

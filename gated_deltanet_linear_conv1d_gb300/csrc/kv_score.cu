@@ -90,13 +90,14 @@ __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned 
     const int j = (r0 + r) / p.G;
     return j * p.Hq + (r0 + r - j * p.G);
   };
-  // every 32 rows' lse up to this warp's last, at once: a lane has the rows g + lane
+  // every 32 rows' lse up to this warp's last, at once: a lane has the rows g + lane (a plain load: the attention in front
+  // may have been writing them when this kernel began)
   constexpr int kMost = (kRows + 31) / 32;
   float l_all[kMost];
 #pragma unroll
   for (int g = 0; g < kMost; ++g) {
     const int r = 32 * g + lane;
-    l_all[g] = r < end ? __ldg(lse_g + row_of(r)) : INFINITY;
+    l_all[g] = r < end ? lse_g[row_of(r)] : INFINITY;
   }
   // piece `lane` (16 bytes) of row r: where it lies, bf16 values
   const uint32_t q_a = smem_u32(q_s) + (lane >> 3) / C::kTerms * q_block + (lane >> 3) % C::kTerms * rp * 128, piece_at = lane & 7;

@@ -154,7 +154,8 @@ __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned 
   const uint32_t q_a = smem_u32(rest) + (lane >> 3) * q_block, piece_at = lane & 7;
   auto piece = [&](int q) { return q_a + q * 128 + ((piece_at ^ (q & 7)) << 4); };
   const int mine = rows.of(pr, first + lane), from = lane < per && mine < all ? row_of(mine) : -1;
-  const float own_lse = kE4m3 && from >= 0 ? __ldg(lse_g + from) : INFINITY;
+  // (plain loads of lse: the attention in front may have been writing it when this kernel began)
+  const float own_lse = kE4m3 && from >= 0 ? lse_g[from] : INFINITY;
   const uint32_t there = __ballot_sync(0xffffffffu, from >= 0);
 #pragma unroll 8
   for (int i = 0; i < per; ++i) {
@@ -174,7 +175,7 @@ __device__ __noinline__ void load_queries(const Args& a, const Seg& s, unsigned 
     uint64_t m = 0;
     if (r < all) {
       const int j = (r0 + r) / p.G;
-      l = __ldg(lse_g + j * p.Hq + (r0 + r - j * p.G));
+      l = lse_g[j * p.Hq + (r0 + r - j * p.G)];
       m = p.mask ? __ldg(p.mask + (size_t)s.n * p.P + j) : j == 63 ? ~0ull : (2ull << j) - 1;
       m &= ~0ull >> (64 - p.P);
     }

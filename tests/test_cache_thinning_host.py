@@ -3,6 +3,8 @@
 compare with."""
 import ctypes
 import math
+import pathlib
+import re
 
 import pytest
 
@@ -134,6 +136,17 @@ def test_binding_checks(b):
                        i.clone())
     with pytest.raises(ValueError, match="new_len"):
         b.gdn_kv_evict(c, torch.zeros(2, 2, dtype=torch.int32), i, i, score, i, torch.zeros(2, 4, 9, dtype=torch.int32), i)
+
+
+def test_what_the_kernel_in_front_writes_is_read_by_plain_loads():
+    """These kernels may begin before the one in front of them ends. A read-only load (__ldg) is for memory that nobody writes
+    while a kernel is there: not for the weights, the log-sum-exps, the kept indices and the new lengths."""
+    csrc = pathlib.Path(gdn_build.CSRC)
+    for name in ("kv_evict.cu", "kv_score.cu", "kv_score.cuh", "kv_score_pair.cu"):
+        text = (csrc / name).read_text()
+        assert "griddepcontrol.wait" in text or name.endswith("h")
+        found = re.findall(r"__ldg\(\s*(?:w|kept|lse_g|p\.(?:score|lse|kept|new_len))\b[^;]*;", text)
+        assert not found, (name, found)
 
 
 # ---------------------------------------------------------------- pins of the fp64 statements

@@ -160,3 +160,72 @@ def test_a_bad_page_leaves_no_weights_of_an_older_lse(b, err, fmt, heads, nodes)
         rows = slice(page * 64, page * 64 + 64)
         want[n, :, rows], lim[n, :, rows] = was[n, :, rows].double(), 0
     inside(weights, want, lim, "score")
+
+
+# ---------------------------------------------------------------- memory that the call in front has written
+
+def test_evictions_read_what_their_selection_left(b, err):
+    """Calls one behind the other without a wait, with the lengths, the budgets, the new lengths and the kept indices in one
+    line of memory: the move takes this call's, whatever lay there."""
+    lens, rounds = [40, 25], 60
+    pool = R.Pool(40, 2, 16, 128, "bf16", seed=1)
+    table, fresh = R.tables([64, 64], 16, 10), R.tables([64, 64], 16, 10) + 20
+    weights = randn(4, 2, 64, seed=2)
+    line = torch.zeros(2 + 2 + 2 + 2 * 2 * 40, dtype=torch.int32, device="cuda")
+    new_len, length, budget, kept = line[:2], line[2:4], line[4:6], line[6:].reshape(2, 2, 40)
+    slot, dst = ints([0, 1]), ints([2, 3])
+    plans = [ints([1 + (7 * i) % x for x in lens]) for i in range(rounds)]
+    length.copy_(ints(lens))
+    got = []
+    c = pool.handle(b)
+    torch.cuda.synchronize()
+    for i in range(rounds):
+        pool.k[20:].zero_()
+        budget.copy_(plans[i])
+        b.gdn_kv_evict(c, table, length, budget, weights, slot, kept, new_len, 1, 2, fresh, dst, dev_err=err)
+        got.append((new_len.clone(), kept.clone(), pool.k.clone(), weights[2:].clone()))
+    assert b.gdn_read_device_error(err) == 0
+    for i, (n, k, keys, w) in enumerate(got):
+        m = plans[i].tolist()
+        assert n.tolist() == m
+        want = T.evict(pool, table, lens, m, weights, slot, 1, 2)[0]
+        for r in range(2):
+            dst_page, row = fresh[r, torch.arange(m[r], device="cuda") // 16].long(), torch.arange(m[r], device="cuda") % 16
+            for h in range(2):
+                assert k[r, h, :m[r]].tolist() == want[r][h], (i, r, h)
+                src = torch.tensor(want[r][h], device="cuda")
+                assert torch.equal(keys[dst_page, h, row], pool.k[table[r, src // 16].long(), h, src % 16]), (i, r, h)
+                assert torch.equal(w[r, h, :m[r]], weights[r, h, src]), (i, r, h)
+
+
+@pytest.mark.parametrize("nodes", [1, 20])
+def test_selections_read_what_the_scores_in_front_left(b, err, nodes):
+    """Attention, scores and eviction one behind the other without a wait, a head's scores beginning anywhere in a line of
+    memory: as with a wait between the calls."""
+    lens, room, rounds = [1500, 700, 90], 1531, 12
+    pool, table, ctx, q, scale = case((24, 4, 256), "bf16", 64, lens, nodes)
+    fresh = R.Pool(pool.k.shape[0] + 60, 4, 64, 256, "bf16", seed=4)
+    fresh.k[:pool.k.shape[0]], fresh.v[:pool.k.shape[0]] = pool.k, pool.v
+    dst = torch.arange(pool.k.shape[0], pool.k.shape[0] + 60, dtype=torch.int32, device="cuda").reshape(3, 20)
+    slot, to, length, budget = ints([0, 1, 2]), ints([3, 4, 5]), ctx + nodes, ints([600, 300, 40])
+    out, c = torch.empty_like(q), fresh.handle(b)
+    ws = torch.empty(b.gdn_tree_attention_workspace_bytes(c, 3, nodes, 24), dtype=torch.uint8, device="cuda")
+    results = []
+    for wait in (True, False):
+        weights, lse = torch.zeros(6, 4, room, device="cuda"), torch.full(q.shape[:2], NAN, device="cuda")
+        kept, new_len = torch.zeros(3, 4, 600, dtype=torch.int32, device="cuda"), ints([0, 0, 0])
+        scales = [scale * (1 + 0.1 * i) for i in range(rounds)]
+        here = []
+        for s in scales:
+            for call in (lambda: b.gdn_tree_attention_lse(c, q, table, ctx, s, out, lse, nodes, workspace=ws, dev_err=err),
+                         lambda: b.gdn_kv_score(c, q, lse, table, ctx, s, weights, slot, nodes, decay=0.5, dev_err=err),
+                         lambda: b.gdn_kv_evict(c, table, length, budget, weights, slot, kept, new_len, 0, 0, dst, to, dev_err=err)):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+            here.append([x.clone() for x in (lse, weights, kept, new_len, fresh.k[dst.flatten().long()])])
+        results.append(here)
+    assert b.gdn_read_device_error(err) == 0
+    for i, (x, y) in enumerate(zip(*results)):
+        for u, v in zip(x, y):
+            assert torch.equal(bits(u), bits(v)), i
