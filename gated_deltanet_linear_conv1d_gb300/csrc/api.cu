@@ -658,7 +658,7 @@ gdn_status gdn_kv_evict(const gdn_kv_cache* cache, const int32_t* block_table, i
   if (num_seqs > 0 && (!dst_table != !dst_slot || (dst_table && (dst_table == block_table || dst_slot == slot_idx))))
     return GDN_ERR_INVALID_ARG;
   if (num_seqs == 0) return GDN_OK;
-  if ((long long)num_seqs * c.Hkv > 1 << 28) return GDN_ERR_UNSUPPORTED;  // blocks are counted in 32 bits
+  if ((long long)num_seqs * c.Hkv >= 1 << 28) return GDN_ERR_UNSUPPORTED;  // eight blocks each: 2^31 are too many
   st = check_score(score, slot_idx, num_slots, max_tokens);
   if (st != GDN_OK) return st;
   if (!block_table || max_pages == 0 || !length || !budget || !new_len || (!kept && max_kept > 0))

@@ -124,6 +124,11 @@ def test_evict_arguments(b):
     assert evict_call(b, c, N=0) == b.GDN_OK
 
 
+def test_evict_of_more_heads_than_a_grid_has_blocks_is_refused(b):
+    """2^28 (request, head) pairs of eight blocks each are 2^31, one more than a grid may have."""
+    assert evict_call(b, cache(b), N=1 << 26) == b.GDN_ERR_UNSUPPORTED
+
+
 def test_binding_checks(b):
     c = cache(b)
     x = torch.zeros(2, 24, 256, dtype=torch.bfloat16)
