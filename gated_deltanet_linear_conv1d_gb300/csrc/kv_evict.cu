@@ -649,18 +649,22 @@ cudaError_t launch_select(const EvictArgs& a, const KvArgs& c, cudaStream_t stre
 }  // namespace
 
 cudaError_t launch_kv_evict(const EvictArgs& a, const KvArgs& c, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (err != cudaSuccess) return err;
   const long long units = (long long)a.N * c.Hkv;
   const long long most = std::min<long long>((long long)a.max_pages * c.page, a.max_tokens);
   // As many CTAs a head as hold the longest request that the tables allow in registers, up to 131072 tokens. What a CTA takes
   // is a chain of steps, whatever its tokens, so of many heads the fewer CTAs the better, and four small ones an SM: with 4
   // x 512 threads of 16 tokens, two an SM, 32 requests of 2k .. 32k took 150 us, selection and copy, with 4 x 256 of 32 143,
   // with 8 x 256 of 16 158. (With 1 x 512 of 16, three an SM, 128 of 300 .. 8k took 193, with 1 x 256 of 32 195.)
-  const cudaError_t err = most <= 2048    ? launch_select<1, 4, 512, 2>(a, c, stream)
-                          : most <= 8192  ? launch_select<1, 16, 512, 3>(a, c, stream)
-                          : most <= 16384 ? launch_select<2, 32, 256, 4>(a, c, stream)
-                          : most <= 32768 ? launch_select<4, 32, 256, 4>(a, c, stream)
-                          : most <= 65536 ? launch_select<8, 32, 256, 4>(a, c, stream)
-                                          : launch_select<8, 32, 512, 1>(a, c, stream);
+  err = most <= 2048    ? launch_select<1, 4, 512, 2>(a, c, stream)
+        : most <= 8192  ? launch_select<1, 16, 512, 3>(a, c, stream)
+        : most <= 16384 ? launch_select<2, 32, 256, 4>(a, c, stream)
+        : most <= 32768 ? launch_select<4, 32, 256, 4>(a, c, stream)
+        : most <= 65536 ? launch_select<8, 32, 256, 4>(a, c, stream)
+                        : launch_select<8, 32, 512, 1>(a, c, stream);
   if (err != cudaSuccess) return err;
   const int row_bytes = a.D * (c.e4m3 ? 1 : 2);
   int shift = -1;
@@ -675,19 +679,19 @@ cudaError_t launch_kv_evict(const EvictArgs& a, const KvArgs& c, cudaStream_t st
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   if (a.dst_table != a.table) {
-    cfg.gridDim = dim3(2 * 152, 1, 1);
+    cfg.gridDim = dim3((unsigned)(2 * sms), 1, 1);
     return row_bytes == 512   ? cudaLaunchKernelEx(&cfg, copy_kernel<512>, a, c, shift)
            : row_bytes == 256 ? cudaLaunchKernelEx(&cfg, copy_kernel<256>, a, c, shift)
                               : cudaLaunchKernelEx(&cfg, copy_kernel<128>, a, c, shift);
   }
   // slices of the rows, down to a sector, while there are too few blocks to keep HBM busy
   int slices = 1;
-  while (row_bytes / slices > 32 && units * 2 * slices < 2 * 152) slices *= 2;
+  while (row_bytes / slices > 32 && units * 2 * slices < 2 * sms) slices *= 2;
   const long long blocks = units * (2 * slices + 1);
   cfg.gridDim = dim3((unsigned)blocks, 1, 1);
   // A block that has an SM's registers for itself takes chunks twice as long: one request of 65536 tokens, bf16, to half,
   // selection and shift, 123 us, with the short ones 148. (Where there are more blocks, 32 of 8192, E4M3, 161 and 131.)
-  return blocks <= 152 ? cudaLaunchKernelEx(&cfg, shift_kernel<8>, a, c, slices, shift)
+  return blocks <= sms ? cudaLaunchKernelEx(&cfg, shift_kernel<8>, a, c, slices, shift)
                        : cudaLaunchKernelEx(&cfg, shift_kernel<4>, a, c, slices, shift);
 }
 
