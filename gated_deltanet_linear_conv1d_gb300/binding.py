@@ -68,7 +68,9 @@ def make_rope_axes(sections, mixed: bool = False) -> GdnRopeAxes:
             raise ValueError("sections cannot take turns: axis 0 must have the most frequencies, or as many")
     else:
         axis = [a for a, n in enumerate(sections) for _ in range(n)]
-    return GdnRopeAxes(axes, (ctypes.c_uint8 * 128)(*axis))
+    made = GdnRopeAxes(axes, (ctypes.c_uint8 * 128)(*axis))
+    made.frequencies = total  # what gdn_qk_norm_mrope holds against inv_freq
+    return made
 
 
 def make_dims(geom, num_slots: int) -> GdnDims:
@@ -554,11 +556,15 @@ def gdn_qk_norm_rope(q, k, q_gamma, k_gamma, eps, positions, inv_freq, q_out, k_
 
 def gdn_qk_norm_mrope(q, k, q_gamma, k_gamma, eps, positions, inv_freq, axes, q_out, k_out=None, v=None, cache=None,
                       kv_slot=None, interleaved: bool = False, dev_err=None, stream=None):
-    """gdn_qk_norm_rope with a position per axis: positions [num_axes, T], axes from make_rope_axes."""
+    """gdn_qk_norm_rope with a position per axis: positions [num_axes, T], axes from make_rope_axes, of as many frequencies
+    as inv_freq has."""
     T, Hkv, D = kv = k.shape
     Hq = Hkv if q is None else q.shape[1]
     qs = (T, Hq, D)
     rotary = 2 * inv_freq.numel()
+    made = getattr(axes, "frequencies", None)  # none: filled by hand
+    if made is not None and 2 * made != rotary:
+        raise ValueError(f"axes are of {made} frequencies, inv_freq has {rotary // 2}")
     _check(_lib.gdn_qk_norm_mrope(*(_NO_ROWS if q is None else _rows(q, "q", qs)), *_rows(k, "k", kv),
                                   _arg(q_gamma, "q_gamma", _f32, (D,), q is None), _arg(k_gamma, "k_gamma", _f32, (D,)),
                                   float(eps), _arg(positions, "positions", _i32, (axes.num_axes, T)),

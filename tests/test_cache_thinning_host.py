@@ -86,6 +86,15 @@ def test_axes_of_the_frequencies(b):
         b.make_rope_axes((1, 5, 5), mixed=True)
 
 
+@pytest.mark.parametrize("sections", [(6, 5, 5), (24, 20, 20), (32, 1)])
+def test_axes_of_more_or_fewer_frequencies_are_refused(b, sections):
+    """The frequencies without a section would all turn by axis 0."""
+    x, gamma = torch.zeros(2, 4, 256, dtype=torch.bfloat16), torch.ones(256)
+    pos, freq = torch.zeros(len(sections), 2, dtype=torch.int32), torch.ones(32, dtype=torch.float64)
+    with pytest.raises(ValueError, match="frequencies"):
+        b.gdn_qk_norm_mrope(x, x, gamma, gamma, 1e-6, pos, freq, b.make_rope_axes(sections), x.clone(), x.clone())
+
+
 def test_lse_arguments(b):
     c = cache(b)
     ref = ctypes.byref(c)
