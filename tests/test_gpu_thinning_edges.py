@@ -229,3 +229,42 @@ def test_selections_read_what_the_scores_in_front_left(b, err, nodes):
     for i, (x, y) in enumerate(zip(*results)):
         for u, v in zip(x, y):
             assert torch.equal(bits(u), bits(v)), i
+
+
+# ---------------------------------------------------------------- long pieces of the line of tiles
+
+LONG = [  # heads, context lengths, nodes, strength: tiles a CTA, or pair tiles a pair, with 152 SMs
+    ((24, 4, 256), [30000] * 8, 1, 1), ((32, 8, 128), [20000, 33, 47000, 9000], 6, 2),  # 49 and 31 tiles
+    ((24, 4, 256), [131000], 8, 1),                      # 27 tiles
+    ((24, 4, 256), [131071], 64, 1),                     # 27 pair tiles, two steps of 192 rows
+    ((24, 4, 256), [40000, 30000, 50, 20001, 9000], 32, 2),  # 21, one step, pieces over several requests and heads
+    ((6, 1, 256), [99999, 77777], 50, 1),                # 9, two steps of 160 rows
+    ((128, 8, 256), [60000], 64, 1),                     # 1024 rows in three chunks, 25 places a pair: several runs of tiles
+    ((64, 4, 128), [50001, 70000, 200], 40, 1),          # 640 rows in two chunks
+]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,lens,nodes,strong", LONG)
+def test_scores_of_long_pieces(b, err, fmt, heads, lens, nodes, strong):
+    """Many tiles a CTA, over several requests and heads, rings and buffers gone round many times; with more rows than a pair
+    keeps, several chunks in turn over runs of tiles. What was there fades once."""
+    pool, table, ctx, q, scale = case(heads, fmt, 64, lens, nodes, strong=strong)
+    _, lse = attend(b, pool, q, table, ctx, scale, nodes, dev_err=err)
+    room = max(lens) + nodes + 3
+    weights = randn(len(lens) + 1, heads[1], room, seed=3).abs()
+    weights *= 0.01
+    slot = torch.randperm(len(lens) + 1, device="cuda")[:len(lens)].to(torch.int32)
+    ref, bound = T.score(pool, q, lse, table, ctx, scale, nodes, weights, slot, None, 0.75)
+    again = weights.clone()
+    for w in (weights, again):
+        b.gdn_kv_score(pool.handle(b), q, lse, table, ctx, scale, w, slot, nodes, decay=0.75, dev_err=err)
+    assert b.gdn_read_device_error(err) == 0
+    inside(weights, ref, bound, "score")
+    assert torch.equal(bits(weights), bits(again))
+    for n, c in enumerate(lens):  # what a kv head's rows hand out is one each
+        total = weights[int(slot[n]), :, :c + nodes].double().sum(-1)
+        assert bool((total >= nodes * heads[0] / heads[1] * 0.999).all())
+    for n, c in enumerate(lens):
+        ref, bound = T.lse(pool, q[n * nodes:(n + 1) * nodes], table[n:n + 1], ctx[n:n + 1], scale, nodes)
+        inside(lse[n * nodes:(n + 1) * nodes], ref, bound, f"lse of request {n}")
