@@ -268,3 +268,132 @@ def test_scores_of_long_pieces(b, err, fmt, heads, lens, nodes, strong):
     for n, c in enumerate(lens):
         ref, bound = T.lse(pool, q[n * nodes:(n + 1) * nodes], table[n:n + 1], ctx[n:n + 1], scale, nodes)
         inside(lse[n * nodes:(n + 1) * nodes], ref, bound, f"lse of request {n}")
+
+
+# ---------------------------------------------------------------- two streams, a captured step
+
+def test_batches_on_two_streams_at_once(b, err):
+    """A batch on each of two streams, their calls enqueued in turn behind a pause and without a wait between them: rotation
+    of rows strided inside a packed projection, attention, scores of few rows and of many, evictions in place and to other
+    pages. Each batch's results are those of a run alone."""
+    hq, hkv, d, page, few, many = 24, 4, 256, 64, 4, 40
+    lens = [[2100, 70, 900], [1300, 3000]]
+    f = 1e7 ** (-torch.arange(32, dtype=torch.float64, device="cuda") / 32)
+    axes, g = b.make_rope_axes((12, 10, 10), True), randn(d, seed=2).abs() + 0.5
+
+    class Batch:
+        def __init__(self, i, stream):
+            N, fmt, self.stream = len(lens[i]), ("bf16", "e4m3")[i], stream
+            self.N, need = N, [n + many for n in lens[i]]
+            pages = sum(-(-n // page) for n in need)
+            self.pool = R.Pool(pages + 20 * N, hkv, page, d, fmt, seed=i)
+            self.c = self.pool.handle(b)
+            self.table = R.tables(need, page, pages, seed=i)
+            self.dst = torch.arange(pages, pages + 20 * N, dtype=torch.int32, device="cuda").reshape(N, 20)
+            self.ctx, self.length = ints(lens[i]), ints(need)
+            self.packed = randn(N * many, hq + 2 * hkv, d, seed=9 + i).to(torch.bfloat16)
+            self.pos = torch.randint(0, 9999, (3, N * many), generator=torch.Generator(device="cuda").manual_seed(i), device="cuda",
+                                     dtype=torch.int32)
+            t = torch.cat([torch.arange(n, n + many) for n in lens[i]]).cuda()
+            rows = torch.arange(N, device="cuda").repeat_interleave(many)
+            self.kv_slot = (self.table[rows, t // page] * page + t % page).to(torch.int32)
+            self.q = torch.zeros(N * many, hq, d, dtype=torch.bfloat16, device="cuda")
+            self.q_few = randn(N * few, hq, d, seed=20 + i).to(torch.bfloat16)
+            self.out, self.out_few = torch.zeros_like(self.q), torch.zeros_like(self.q_few)
+            self.lse, self.lse_few = (torch.zeros(x.shape[:2], device="cuda") for x in (self.q, self.q_few))
+            self.ws = [torch.empty(b.gdn_tree_attention_workspace_bytes(self.c, N, n, hq), dtype=torch.uint8, device="cuda")
+                       for n in (few, many)]
+            self.weights = torch.zeros(2 * N, hkv, 3100, device="cuda")
+            self.slot, self.to = ints(list(range(N))), ints(list(range(N, 2 * N)))
+            self.budget, self.half = ints([900] * N), ints([1100] * N)
+            self.kept = [torch.zeros(N, hkv, 1100, dtype=torch.int32, device="cuda") for _ in range(2)]
+            self.new_len = [torch.zeros(N, dtype=torch.int32, device="cuda") for _ in range(2)]
+
+        def calls(self):
+            kw = dict(dev_err=err, stream=self.stream)
+            p, s = self.packed, d ** -0.5
+            yield lambda: b.gdn_qk_norm_mrope(p[:, :hq], p[:, hq:hq + hkv], g, g, 1e-6, self.pos, f, axes, self.q,
+                                              v=p[:, hq + hkv:], cache=self.c, kv_slot=self.kv_slot, **kw)
+            yield lambda: b.gdn_tree_attention_lse(self.c, self.q, self.table, self.ctx, s, self.out, self.lse, many,
+                                                   workspace=self.ws[1], **kw)
+            yield lambda: b.gdn_tree_attention_lse(self.c, self.q_few, self.table, self.ctx, s, self.out_few, self.lse_few, few,
+                                                   workspace=self.ws[0], **kw)
+            yield lambda: b.gdn_kv_score(self.c, self.q, self.lse, self.table, self.ctx, s, self.weights, self.slot, many,
+                                         decay=0.9, **kw)
+            yield lambda: b.gdn_kv_score(self.c, self.q_few, self.lse_few, self.table, self.ctx, s, self.weights, self.slot, few,
+                                         decay=0.9, **kw)
+            yield lambda: b.gdn_kv_evict(self.c, self.table, self.length, self.budget, self.weights, self.slot, self.kept[0],
+                                         self.new_len[0], 2, 30, self.dst, self.to, **kw)
+            yield lambda: b.gdn_kv_evict(self.c, self.table, self.length, self.half, self.weights, self.slot, self.kept[1],
+                                         self.new_len[1], 2, 30, **kw)
+
+        def results(self):
+            return [getattr(self.pool, x) for x in parts(self.pool)] + [self.q, self.out, self.out_few, self.lse, self.lse_few,
+                                                                      self.weights, *self.kept, *self.new_len]
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    alone, both = ([Batch(i, streams[i]) for i in range(2)] for _ in range(2))
+    torch.cuda.synchronize()
+    for x in alone:
+        for _ in range(3):
+            for call in x.calls():
+                call()
+        torch.cuda.synchronize()
+    for s in streams:
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(4_000_000)  # some milliseconds: the calls below wait for each other on the host only
+    for _ in range(3):
+        for pair in zip(*(x.calls() for x in both)):
+            for call in pair:
+                call()
+    torch.cuda.synchronize()
+    assert b.gdn_read_device_error(err) == 0
+    for x, y in zip(alone, both):
+        for i, (u, v) in enumerate(zip(x.results(), y.results())):
+            assert torch.equal(bits(u), bits(v)), i
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("nodes", [2, 33, 64])
+def test_a_captured_step_against_the_statements(b, err, fmt, nodes):
+    """Scores and eviction in place captured on a stream that waits for what made its inputs; every replay, with contexts,
+    slots and budgets of its own, is the fp64 statements' step on the state in front of it."""
+    lens = [900, 300, 40]
+    pool, table, ctx, q, scale = case((24, 4, 256), fmt, 64, lens, nodes)
+    c = pool.handle(b)
+    lse = T.lse(pool, q, table, ctx, scale, nodes)[0].float()
+    slot, length, budget, new_len = ints([0, 1, 2]), ints([0, 0, 0]), ints([1, 1, 1]), ints([0, 0, 0])
+    weights, kept = randn(5, 4, 1000, seed=5).abs(), torch.zeros(3, 4, 1000, dtype=torch.int32, device="cuda")
+
+    def step(stream):
+        b.gdn_kv_score(c, q, lse, table, ctx, scale, weights, slot, nodes, decay=0.5, dev_err=err, stream=stream)
+        torch.add(ctx, nodes, out=length)
+        b.gdn_kv_evict(c, table, length, budget, weights, slot, kept, new_len, 2, 8, dev_err=err, stream=stream)
+
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    step(torch.cuda.current_stream())  # the first call outside the capture
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        step(side)
+    for held, most, where in ((lens, [500, 100, 60], [0, 1, 2]), ([500, 100, 20], [400, 90, 10], [2, 4, 1]),
+                              ([0, 300, 1], [1, 0, 2000], [3, 0, 4])):
+        ctx.copy_(ints(held))
+        budget.copy_(ints([min(m, 1000) for m in most]))
+        slot.copy_(ints(where))
+        before, w = copy_of(pool), weights.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert b.gdn_read_device_error(err) == 0
+        scored = w.clone()
+        b.gdn_kv_score(before.handle(b), q, lse, table, ctx, scale, scored, slot, nodes, decay=0.5)
+        ref, bound = T.score(before, q, lse, table, ctx, scale, nodes, w, slot, None, 0.5)
+        inside(scored, ref, bound, "score")
+        full = [n + nodes for n in held]
+        want, want_len, now, w_now = T.evict(before, table, full, most, scored, slot, 2, 8)
+        assert new_len.tolist() == want_len
+        for n in range(3):
+            for h in range(4):
+                assert kept[n, h, :want_len[n]].tolist() == want[n][h], (n, h)
+        for x, t in now.items():
+            assert torch.equal(bits(getattr(pool, x)), bits(t)), x
+        assert torch.equal(bits(weights), bits(w_now))
