@@ -397,3 +397,59 @@ def test_a_captured_step_against_the_statements(b, err, fmt, nodes):
         for x, t in now.items():
             assert torch.equal(bits(getattr(pool, x)), bits(t)), x
         assert torch.equal(bits(weights), bits(w_now))
+
+
+# ---------------------------------------------------------------- the rotation over several axes, into the cache
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,n,sections,mixed,inter,page", [
+    ((24, 4, 256), 256, (12, 10, 10), True, False, 64), ((24, 4, 256), 3001, (16, 8, 8), False, False, 48),
+    ((6, 1, 256), 41, (48, 40, 40), True, True, 16), ((32, 8, 128), 700, (2, 2, 2, 2), True, False, 128)])
+def test_rotation_by_other_positions_an_axis_into_the_cache(b, err, fmt, heads, n, sections, mixed, inter, page):
+    """Positions that differ between the axes: the cached keys against the statement, an axis at a time; the values' codes
+    and scales are the oracle's, bit by bit; nothing else moves."""
+    hq, hkv, d = heads
+    pool = R.Pool(-(-n // page) + 2, hkv, page, d, fmt, seed=n)
+    was = copy_of(pool)
+    packed = (randn(n, hq + 2 * hkv, d, seed=n) * 2).to(torch.bfloat16)
+    q, k, v = packed[:, :hq], packed[:, hq:hq + hkv], packed[:, hq + hkv:]
+    gain, half = randn(d, seed=2).abs() + 0.5, sum(sections)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    pos = torch.randint(0, 1 << 20, (len(sections), n), generator=g, device="cuda", dtype=torch.int32)
+    f = 1e7 ** (-torch.arange(half, dtype=torch.float64, device="cuda") / half)
+    axes = b.make_rope_axes(sections, mixed)
+    slots = torch.randperm(pool.k.shape[0] * page, generator=g, device="cuda")[:n].to(torch.int32)
+    slots[n // 2] = -1
+    qo = torch.empty(n, hq, d, dtype=torch.bfloat16, device="cuda")
+    b.gdn_qk_norm_mrope(q, k, gain, gain, 1e-6, pos, f, axes, qo, v=v, cache=pool.handle(b), kv_slot=slots, interleaved=inter,
+                        dev_err=err)
+    assert b.gdn_read_device_error(err) == 0
+    ref, mag = R.norm_rope(k, gain, 1e-6, pos[0], f * 0, inter)
+    for a in range(len(sections)):
+        i = torch.tensor([j for j in range(half) if axes.axis[j] == a], dtype=torch.long, device="cuda")
+        mine = torch.zeros(half, dtype=torch.float64, device="cuda")
+        mine[i] = 1
+        where = torch.cat((2 * i, 2 * i + 1) if inter else (i, i + half))
+        r, m = R.norm_rope(k, gain, 1e-6, pos[a], f * mine, inter)
+        ref[..., where], mag[..., where] = r[..., where], m[..., where]
+    kept = slots >= 0
+    pg, row = slots[kept].long() // page, slots[kept].long() % page
+    ref, mag = ref[kept], mag[kept]
+    if fmt == "bf16":
+        inside(pool.k[pg, :, row], ref, R.rope_bound(ref, mag), "keys")
+        assert torch.equal(bits(pool.v[pg, :, row]), bits(v[kept]))
+    else:
+        s, amax = pool.k_scale[pg, :, row].double(), ref.abs().amax(-1)
+        # the largest value: what rope_bound counts beside the rounding to bf16, of the largest pair; then a division
+        slack = (2.0 ** -16 + 2.0 ** -20) * mag
+        assert bool(((s - amax / 448).abs() <= slack.amax(-1) / 448 + 2.0 ** -23 * amax / 448).all())
+        val = R._TABLE.cuda()[pool.k[pg, :, row].long()] * s[..., None]
+        # half a step of the code, relative (2^-4) or E4M3's smallest (2^-10 of the scale), of a value that is off by slack
+        inside(val, ref, R.E4M3 * (ref.abs() + slack) * (1 + 2.0 ** -20) + 2.0 ** -10 * s[..., None] + slack, "keys")
+        codes, scale = R.quantise(v[kept].float())
+        assert torch.equal(pool.v[pg, :, row].cpu(), codes) and torch.equal(pool.v_scale[pg, :, row].cpu(), scale)
+    touched = torch.zeros(pool.k.shape[0], page, dtype=torch.bool, device="cuda")
+    touched[pg, row] = True
+    keep = ~touched[:, None].expand(-1, hkv, -1)
+    for x in parts(pool):
+        assert torch.equal(bits(getattr(pool, x)[keep]), bits(getattr(was, x)[keep])), x
