@@ -9,8 +9,8 @@
 // S^T [128 tokens x rows] = K Q^T on the tensor cores (tcgen05): the keys are the first operand, from shared memory as
 // they lie in the cache, so a token is a lane of tensor memory, and its sum over the rows is one thread's, in the order of
 // the rows. An E4M3 cache stays E4M3, and Q (bf16, scaled by a power of two) is written as the sum of two E4M3 terms, exact
-// down to 2^-17 of the largest value, a rounding below the scores' own; the two are columns of one MMA, added as they are
-// read.
+// down to 2^-17 of the largest value of the kv head's rows, or, where a row's own power of two is used, 2^-15 of the row's
+// largest; the two are columns of one MMA, added as they are read.
 //
 // Work. The tiles of 128 tokens of all (request, kv head) units stand in one line, cut into equal pieces, one per CTA. A
 // unit's rows, up to 64, stay in shared memory for its tiles; more go to kv_score_pair.cu.

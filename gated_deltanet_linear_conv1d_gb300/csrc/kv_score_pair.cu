@@ -14,10 +14,11 @@
 // four groups of four warps that share a step's columns (two the even CTA's rows, two the odd one's), a warp for the copies,
 // one for the MMAs (the even CTA's issues them). The groups load the query rows too. Every wait is bounded.
 //
-// 64 x 6 rows on 131071 tokens, bf16, 84 us (104 GFLOP, 66 % of the cuBLAS rate): 9 us to the first scores, then 1.2 us a
-// step of 192 rows, 1.0 of them the MMAs', with the weights' loop just behind them. 32 x 6 rows of 8 prompts of 1500 .. 32768
-// tokens 44 us, 9 of them to the first scores; 2 x 64 x 6 rows in one kv head on 40 .. 70 thousand tokens, E4M3, 35 us, 12
-// of them to the first scores, the rows' terms among them.
+// 64 x 6 rows on 131071 tokens, bf16, 84 us (104 GFLOP, 66 % of the cuBLAS rate): 9 us to the first scores, then 54 steps of
+// 192 rows at about 1.2 us each, 1.0 of them the MMAs', with the weights' loop just behind them; 10 us are in neither. 32 x 6
+// rows of 8 prompts of 1500 .. 32768 tokens 43 us, 9 of them to the first scores; 11 x 6 rows 39 us: what a unit takes beside
+// its tiles weighs most. 2 x 64 x 6 rows in one kv head on 40 .. 70 thousand tokens, E4M3, 33 us, 12 of them to the first
+// scores, the rows' terms among them, and 14 the steps.
 #include "kv_score.cuh"
 #include "pair.cuh"
 

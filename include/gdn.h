@@ -695,7 +695,11 @@ gdn_status gdn_kv_score(const gdn_kv_cache *cache, const uint16_t *q, const floa
  * A request with a slot >= num_slots (or a negative dst_slot), or a page outside
  * [0, num_pages) in either table, sets GDN_DEVERR_SLOT; one whose tokens the tables,
  * max_tokens or max_kept cannot hold, or with a negative budget, sets
- * GDN_DEVERR_OFFSETS; either way it writes nothing but its new_len.
+ * GDN_DEVERR_OFFSETS; either way it writes nothing but its new_len. The smaller of
+ * max_pages pages and max_tokens is the longest request that the call is laid out
+ * for: room far beyond the requests' lengths costs time (at 131,072 tokens of room
+ * 128 requests of up to 8192 take five times as long), so a caller with long tables
+ * gives narrower ones where the batch is short.
  */
 gdn_status gdn_kv_evict(const gdn_kv_cache *cache, const int32_t *block_table, int32_t max_pages,
                         const int32_t *length, const int32_t *budget, int32_t sink_tokens, int32_t recent_tokens,
